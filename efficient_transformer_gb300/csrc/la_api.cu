@@ -22,8 +22,8 @@ namespace la {
 __device__ int g_error_word;
 
 namespace {
-
 thread_local char t_last_cuda[256] = "";
+}
 
 la_status cuda_fail(cudaError_t e) {
     std::snprintf(t_last_cuda, sizeof t_last_cuda, "%s: %s", cudaGetErrorName(e), cudaGetErrorString(e));
@@ -48,6 +48,8 @@ cudaError_t error_word(int **out) {
     *out = cache[dev];
     return cudaSuccess;
 }
+
+namespace {
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 

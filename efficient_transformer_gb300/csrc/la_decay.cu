@@ -1,0 +1,209 @@
+// la_decay.cu -- C ABI of the decayed linear attention: argument checks, the work plan and
+// dispatch (see la_decay.cuh for the passes that the kernels run).
+#include <cmath>
+
+#include "la_decay.cuh"
+
+namespace la {
+namespace {
+
+bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+bool width_ok(int D) { return D == 32 || D == 64 || D == 128; }
+
+la_status check(int B, int Hq, int Hkv, int N, int D, int Dv, int dtype, float scale) {
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || N <= 0 || D <= 0 || Dv <= 0 || Hq % Hkv != 0) return LA_ERR_ARG;
+    if (dtype != LA_F32 && dtype != LA_BF16) return LA_ERR_ARG;
+    if (!std::isfinite(scale) || scale == 0.f) return LA_ERR_ARG;
+    // rows of a tensor are counted in 64 bits, heads and blocks in 31
+    if ((unsigned long long)B * Hq >= (1u << 26) || (((unsigned long long)B * Hq * N) >> 50)) return LA_ERR_ARG;
+    if (!width_ok(D) || !width_ok(Dv)) return LA_ERR_UNSUPPORTED;
+    return LA_OK;
+}
+
+struct DecayPlan {
+    la_path path;
+    int seg_len, nseg;
+    size_t state_bytes, ws_bytes;   // one array of segment states; all of them
+};
+
+// The segments of a sequence: the count whose schedule ends first, `units` blocks of work per segment
+// on `slots` places that run at once, a block costing its chunks plus about two for its
+// start; more than one segment costs the pass that sums them, about half a chunk each.
+DecayPlan make_plan(int B, int Hkv, int N, int D, int Dv, la_dtype dt, bool bwd) {
+    DecayPlan pl{};
+    pl.path = LA_PATH_SIMT;
+    (void)dt;
+    const int chunk = 32;
+    const long long units = (long long)B * Hkv * ((bwd ? (D > Dv ? D : Dv) : Dv) / kDecaySimtSlice);
+    const int slots = 3 * kPlanSms, nchunks = (N + chunk - 1) / chunk;
+    double best = -1.0;
+    int best_cps = nchunks;
+    for (int want = 1; want <= nchunks && want <= 64; ++want) {
+        const int cps = (nchunks + want - 1) / want, nseg = (nchunks + cps - 1) / cps;
+        const long long waves = (units * nseg + slots - 1) / slots;
+        const double cost = waves * (cps * (nseg > 1 ? 1.5 : 1.0) + 2.0 + (nseg > 1 ? 2.0 : 0.0));
+        if (best < 0 || cost < best) {
+            best = cost;
+            best_cps = cps;
+        }
+    }
+    pl.seg_len = best_cps * chunk;
+    pl.nseg = (N + pl.seg_len - 1) / pl.seg_len;
+    pl.state_bytes = pl.nseg > 1 ? ((size_t)B * Hkv * pl.nseg * D * Dv * 4 + 255) / 256 * 256 : 0;
+    pl.ws_bytes = pl.state_bytes * (bwd ? 2 : 1);
+    return pl;
+}
+
+// Strides of a [B, H, N, W] input (st NULL: contiguous); false for a negative one.  A dimension of one
+// has no step.
+bool input_strides(const la_strides *st, int B, int H, int N, int W, Strides *out) {
+    *out = contiguous_strides(H, N, W);
+    if (!st) return true;
+    if (st->b < 0 || st->h < 0 || st->n < 0) return false;
+    if (B > 1) out->b = st->b;
+    if (H > 1) out->h = st->h;
+    if (N > 1) out->n = st->n;
+    return true;
+}
+
+struct Given {
+    const void *q, *k, *v, *g;
+    const la_strides *sq, *sk, *sv, *sg;
+    void *out, *dq, *dk, *dv;
+    const float *log_decay, *s_in, *ds_in;
+    float *s_out, *ds_out;
+    const int *lengths;
+};
+
+la_status run(bool bwd, const Given &a, int B, int Hq, int Hkv, int N, int D, int Dv, la_dtype dt, float scale, void *ws,
+              size_t ws_bytes, void *stream) {
+    la_status st = check(B, Hq, Hkv, N, D, Dv, dt, scale);
+    if (st != LA_OK) return st;
+    if (!a.q || !a.k || !a.v || !a.log_decay) return LA_ERR_ARG;
+    if (bwd ? (!a.g || !a.dq || !a.dk || !a.dv) : !a.out) return LA_ERR_ARG;
+    const void *ptrs[] = {a.q, a.k, a.v, a.g, a.out, a.dq, a.dk, a.dv, a.s_in, a.ds_in, a.s_out, a.ds_out};
+    for (const void *p : ptrs)
+        if (p && !aligned(p, 16)) return LA_ERR_ALIGN;
+    if (!aligned(a.log_decay, 4) || (a.lengths && !aligned(a.lengths, 4))) return LA_ERR_ALIGN;
+    Strides sq, sk, sv, sg;
+    if (!input_strides(a.sq, B, Hq, N, D, &sq) || !input_strides(a.sk, B, Hkv, N, D, &sk) ||
+        !input_strides(a.sv, B, Hkv, N, Dv, &sv) || !input_strides(a.sg, B, Hq, N, Dv, &sg))
+        return LA_ERR_ARG;
+    const DecayPlan pl = make_plan(B, Hkv, N, D, Dv, dt, bwd);
+    if (pl.ws_bytes > 0) {
+        if (!ws || ws_bytes < pl.ws_bytes) return LA_ERR_WORKSPACE;
+        if (!aligned(ws, 256)) return LA_ERR_ALIGN;
+    }
+    DecayParams p{};
+    p.log_decay = a.log_decay;
+    p.lengths = a.lengths;
+    p.B = B; p.Hkv = Hkv; p.n_rep = Hq / Hkv; p.N = N; p.D = D; p.Dv = Dv;
+    p.scale = scale;
+    p.seg_len = pl.seg_len; p.nseg = pl.nseg;
+    float *slots0 = pl.nseg > 1 ? static_cast<float *>(ws) : nullptr;
+    float *slots1 = pl.nseg > 1 ? reinterpret_cast<float *>(static_cast<char *>(ws) + pl.state_bytes) : nullptr;
+    DecayStateParams sp{};
+    sp.log_decay = a.log_decay;
+    sp.lengths = a.lengths;
+    sp.B = B; sp.Hkv = Hkv; sp.N = N; sp.D = D; sp.Dv = Dv; sp.seg_len = pl.seg_len; sp.nseg = pl.nseg;
+    // S = sum k v^T (both directions of a training step start from it)
+    sp.y[0] = a.k; sp.z[0] = a.v; sp.sy[0] = sk; sp.sz[0] = sv; sp.init[0] = a.s_in; sp.init_mul[0] = 1.f;
+    sp.heads[0] = 1; sp.rev[0] = 0; sp.slots[0] = slots0;
+    sp.n = 1;
+    if (!bwd) {
+        DecayPass &f = p.pass[0];
+        f.x = a.q; f.y = a.k; f.z = a.v; f.sx = sq; f.sy = sk; f.sz = sv; f.out = a.out;
+        f.slots = slots0; f.init = a.s_in; f.fin = a.s_out; f.init_mul = f.fin_mul = 1.f;
+        p.npass = 1;
+    } else {
+        // A = sum q g^T from the last token back
+        sp.y[1] = a.q; sp.z[1] = a.g; sp.sy[1] = sq; sp.sz[1] = sg; sp.init[1] = a.ds_in; sp.init_mul[1] = 1.f / scale;
+        sp.heads[1] = p.n_rep; sp.rev[1] = 1; sp.slots[1] = slots1;
+        sp.n = 2;
+        DecayPass &q = p.pass[0], &k = p.pass[1], &v = p.pass[2];
+        q.x = a.g; q.y = a.v; q.z = a.k; q.sx = sg; q.sy = sv; q.sz = sk; q.out = a.dq;
+        q.slots = slots0; q.init = a.s_in; q.tr = 1; q.init_mul = q.fin_mul = 1.f;
+        k.x = a.v; k.y = a.g; k.z = a.q; k.sx = sv; k.sy = sg; k.sz = sq; k.out = a.dk;
+        k.slots = slots1; k.init = a.ds_in; k.tr = 1;
+        v.x = a.k; v.y = a.q; v.z = a.g; v.sx = sk; v.sy = sq; v.sz = sg; v.out = a.dv;
+        v.slots = slots1; v.init = a.ds_in; v.fin = a.ds_out;
+        for (DecayPass *ps : {&k, &v}) {
+            ps->many_yz = 1;
+            ps->rev = 1;
+            ps->first_off = 1;
+            ps->init_mul = 1.f / scale;
+            ps->fin_mul = scale;
+        }
+        p.npass = 3;
+    }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    if (pl.nseg > 1) e = decay_simt_states(sp, dt, s);
+    for (int i = 0; e == cudaSuccess && i < p.npass; ++i) e = decay_simt_pass(p, i, dt, s);
+    return e == cudaSuccess ? LA_OK : cuda_fail(e);
+}
+
+}  // namespace
+}  // namespace la
+
+using namespace la;
+
+extern "C" {
+
+size_t la_decay_workspace_size(int B, int Hq, int Hkv, int N, int D, int Dv, la_dtype dtype, int is_bwd) {
+    if (check(B, Hq, Hkv, N, D, Dv, dtype, 1.f) != LA_OK) return 0;
+    return make_plan(B, Hkv, N, D, Dv, dtype, is_bwd).ws_bytes;
+}
+
+la_path la_decay_kernel_path(int B, int Hq, int Hkv, int N, int D, int Dv, la_dtype dtype, int is_bwd) {
+    if (check(B, Hq, Hkv, N, D, Dv, dtype, 1.f) != LA_OK) return LA_PATH_SIMT;
+    return make_plan(B, Hkv, N, D, Dv, dtype, is_bwd).path;
+}
+
+la_status la_decay_fwd(const void *q, const void *k, const void *v, void *out, const float *log_decay,
+                       const float *initial_state, float *final_state, const int *lengths, int B, int Hq, int Hkv,
+                       int N, int D, int Dv, la_dtype dtype, float scale, const la_strides *q_strides,
+                       const la_strides *k_strides, const la_strides *v_strides, void *workspace, size_t ws_bytes,
+                       void *stream) {
+    Given a{};
+    a.q = q; a.k = k; a.v = v; a.out = out; a.log_decay = log_decay; a.s_in = initial_state; a.s_out = final_state;
+    a.lengths = lengths; a.sq = q_strides; a.sk = k_strides; a.sv = v_strides;
+    return run(false, a, B, Hq, Hkv, N, D, Dv, dtype, scale, workspace, ws_bytes, stream);
+}
+
+la_status la_decay_bwd(const void *q, const void *k, const void *v, const void *grad_out, void *dq, void *dk, void *dv,
+                       const float *log_decay, const float *initial_state, const float *grad_final_state,
+                       float *grad_initial_state, int B, int Hq, int Hkv, int N, int D, int Dv, la_dtype dtype,
+                       float scale, const la_strides *q_strides, const la_strides *k_strides,
+                       const la_strides *v_strides, const la_strides *g_strides, void *workspace, size_t ws_bytes,
+                       void *stream) {
+    Given a{};
+    a.q = q; a.k = k; a.v = v; a.g = grad_out; a.dq = dq; a.dk = dk; a.dv = dv; a.log_decay = log_decay;
+    a.s_in = initial_state; a.ds_in = grad_final_state; a.ds_out = grad_initial_state;
+    a.sq = q_strides; a.sk = k_strides; a.sv = v_strides; a.sg = g_strides;
+    return run(true, a, B, Hq, Hkv, N, D, Dv, dtype, scale, workspace, ws_bytes, stream);
+}
+
+la_status la_decay_step(const void *q, const void *k, const void *v, void *out, const float *state, float *state_out,
+                        const float *log_decay, const int *slots, int pool, int B, int Hq, int Hkv, int D, int Dv,
+                        la_dtype dtype, float scale, const la_strides *q_strides, const la_strides *k_strides,
+                        const la_strides *v_strides, void *stream) {
+    la_status st = check(B, Hq, Hkv, 1, D, Dv, dtype, scale);
+    if (st != LA_OK) return st;
+    if (!q || !k || !v || !out || !state || !state_out || !log_decay || pool <= 0) return LA_ERR_ARG;
+    if (!slots && pool < B) return LA_ERR_ARG;
+    const void *ptrs[] = {q, k, v, out, state, state_out};
+    for (const void *p : ptrs)
+        if (!aligned(p, 16)) return LA_ERR_ALIGN;
+    if (!aligned(log_decay, 4) || (slots && !aligned(slots, 4))) return LA_ERR_ALIGN;
+    DecayStepParams p{};
+    if (!input_strides(q_strides, B, Hq, 1, D, &p.sq) || !input_strides(k_strides, B, Hkv, 1, D, &p.sk) ||
+        !input_strides(v_strides, B, Hkv, 1, Dv, &p.sv))
+        return LA_ERR_ARG;
+    p.q = q; p.k = k; p.v = v; p.out = out; p.state = state; p.state_out = state_out; p.log_decay = log_decay;
+    p.slots = slots; p.pool = pool; p.B = B; p.Hkv = Hkv; p.n_rep = Hq / Hkv; p.D = D; p.Dv = Dv; p.scale = scale;
+    cudaError_t e = decay_step(p, dtype, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? LA_OK : cuda_fail(e);
+}
+
+}  // extern "C"

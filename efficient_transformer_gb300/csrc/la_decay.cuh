@@ -1,0 +1,97 @@
+// la_decay.cuh -- shared definitions of the decayed linear attention (la_decay_*).
+//
+// All the chunked products have one form, a pass F(X, Y, Z) over the tokens in order:
+//
+//   F_i = sum_{j <= i} gamma^(i-j) (x_i . y_j) z_j + gamma^(i+1) x_i^T S_0
+//
+// forward:  out = F(q, k, v), S = sum k v^T;
+// backward: dq = F(g, v, k) with S^T; and, with the tokens in reverse order and
+// A = sum q g^T in the place of S, dv = F(k, q, g) with A and dk = F(v, g, q) with A^T, summed over
+// the query heads of each group.  (A_i = sum_{j >= i} gamma^(j-i) q_j g_j^T is the gradient of S_i.)
+#pragma once
+
+#include "la_internal.cuh"
+
+namespace la {
+
+// A pass.  Tokens are counted along its direction (`rev`: from the last to the first).
+struct DecayPass {
+    const void *x, *y, *z;      // [B, Hx, N, DX], [B, Hyz, N, DX], [B, Hyz, N, DZ]
+    Strides sx, sy, sz;
+    void *out;                  // [B, Hx, N, DZ], contiguous
+    const float *slots;         // nseg > 1: workspace, [B Hkv][nseg] states [D][Dv]: slot 0 the starting
+                                // state, slot u > 0 the sum over segment u - 1 alone
+    const float *init;          // nseg = 1: starting state [B Hkv][D][Dv] or null
+    float *fin;                 // state after the last token, or null
+    int tr;                     // the pass's DX x DZ state is the transpose of the stored D x Dv one
+    int many_yz;                // Hyz = n_rep Hkv heads of y and z for each head of x (summed into one
+                                // out); else Hx = n_rep Hkv heads of x for each head of y and z
+    int rev;
+    // reverse order: the incoming gradient of the last state has not decayed when it meets the first
+    // token of the pass, so its powers of gamma are one lower (first_off = 1), and what
+    // leaves at the other end decays once more
+    int first_off;
+    float init_mul, fin_mul;    // the reverse states leave out `scale`, which comes in and goes out here
+};
+
+struct DecayParams {
+    const float *log_decay;     // [Hkv]
+    const int *lengths;         // [B] or null
+    int B, Hkv, n_rep, N, D, Dv;
+    float scale;
+    int seg_len, nseg;
+    int npass;
+    DecayPass pass[3];
+    int *err;
+};
+
+// The sums over single segments that later segments start from, natural orientation [D][Dv]:
+// slot u + 1 = sum over segment u of gamma^(tokens after j in the segment) y_j z_j^T (summed over the
+// heads of y, z), slot 0 = the starting state (times init_mul).
+struct DecayStateParams {
+    const float *log_decay;
+    const int *lengths;
+    const void *y[2], *z[2];
+    Strides sy[2], sz[2];
+    const float *init[2];
+    float init_mul[2];
+    int heads[2];               // heads of y and z per key/value head
+    int rev[2];
+    float *slots[2];
+    int n;                      // state arrays of this launch (1 or 2)
+    int B, Hkv, N, D, Dv, seg_len, nseg;
+    int *err;
+};
+
+// Tokens of sequence b.
+__device__ __forceinline__ int decay_tokens(const int *lengths, int b, int N) {
+    return lengths ? min(max(lengths[b], 0), N) : N;
+}
+
+// log2(gamma) of a head, with -inf (gamma = 0) kept finite so that gamma^0 = 2^(0 x) stays 1: 2^-1e30
+// and every power of it is 0.
+__device__ __forceinline__ float decay_log2(float log_decay) {
+    const float l2 = log_decay * 1.4426950408889634f;
+    return l2 < -1e30f ? -1e30f : l2;
+}
+
+// CUDA-core kernels (la_decay_simt.cu): every dtype, width and stride.
+constexpr int kDecaySimtSlice = 32;   // columns of out that a block owns
+cudaError_t decay_simt_states(const DecayStateParams &p, la_dtype dt, cudaStream_t s);
+cudaError_t decay_simt_pass(const DecayParams &p, int pass, la_dtype dt, cudaStream_t s);
+
+// One token (la_decay_step).
+struct DecayStepParams {
+    const void *q, *k, *v;
+    Strides sq, sk, sv;
+    void *out;
+    const float *state;
+    float *state_out;
+    const float *log_decay;
+    const int *slots;
+    int pool, B, Hkv, n_rep, D, Dv;
+    float scale;
+};
+cudaError_t decay_step(const DecayStepParams &p, la_dtype dt, cudaStream_t s);
+
+}  // namespace la

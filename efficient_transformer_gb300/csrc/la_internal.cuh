@@ -181,6 +181,11 @@ class TraceScope {
     cudaEvent_t start_ = nullptr;
 };
 
+// --- errors (defined in la_api.cu) ---------------------------------------------------------
+
+la_status cuda_fail(cudaError_t e);        // records e for la_last_cuda_error(): LA_ERR_CUDA
+cudaError_t error_word(int **out);         // device error word of the current device
+
 // --- launchers (defined in the kernel translation units) --------------------------------
 
 // Scan of per-segment states along the sequence (fixed order, per (batch, kv head)).

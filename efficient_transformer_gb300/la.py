@@ -38,6 +38,15 @@ class LaStrides(ctypes.Structure):
     _fields_ = [("b", ctypes.c_longlong), ("h", ctypes.c_longlong), ("n", ctypes.c_longlong)]
 
 
+class LaQkArgs(ctypes.Structure):
+    """la_qk_args: norm and rotation of la_qk_norm_rope_*."""
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("weight_dtype", ctypes.c_int),
+                ("eps", ctypes.c_float), ("normalize", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("rot", ctypes.c_int), ("axes", ctypes.c_int), ("sections", ctypes.POINTER(ctypes.c_int)),
+                ("positions", ctypes.c_void_p), ("pos_strides", ctypes.POINTER(ctypes.c_longlong)),
+                ("inv_freq", ctypes.c_void_p)]
+
+
 class LinearAttentionError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -96,6 +105,23 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.la_lowrank_bwd_t.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, sz, vp]
     lib.la_lowrank_bwd_t.restype = i
     lib.la_lowrank_bwd.restype = i
+    lib.la_decay_workspace_size.argtypes = [i] * 8
+    lib.la_decay_workspace_size.restype = sz
+    lib.la_decay_kernel_path.argtypes = [i] * 8
+    lib.la_decay_kernel_path.restype = i
+    lib.la_decay_fwd.argtypes = [vp] * 8 + [i] * 7 + [f, sp, sp, sp, vp, sz, vp]
+    lib.la_decay_fwd.restype = i
+    lib.la_decay_bwd.argtypes = [vp] * 11 + [i] * 7 + [f, sp, sp, sp, sp, vp, sz, vp]
+    lib.la_decay_bwd.restype = i
+    lib.la_decay_step.argtypes = [vp] * 8 + [i] * 7 + [f, sp, sp, sp, vp]
+    lib.la_decay_step.restype = i
+    qp = ctypes.POINTER(LaQkArgs)
+    lib.la_qk_norm_rope_fwd.argtypes = [vp] * 4 + [i] * 6 + [sp, sp, qp, vp]
+    lib.la_qk_norm_rope_fwd.restype = i
+    lib.la_qk_norm_rope_workspace_size.argtypes = [i] * 6
+    lib.la_qk_norm_rope_workspace_size.restype = sz
+    lib.la_qk_norm_rope_bwd.argtypes = [vp] * 8 + [i] * 6 + [sp, sp, sp, sp, qp, vp, sz, vp]
+    lib.la_qk_norm_rope_bwd.restype = i
     lib.la_trace_start.argtypes = []
     lib.la_trace_start.restype = i
     lib.la_trace_stop.argtypes = []
@@ -365,6 +391,240 @@ def lowrank_bwd(x: torch.Tensor, U: torch.Tensor, V: torch.Tensor, grad_out: tor
     if st != LA_OK:
         _raise(lib, st, call)
     return dx, dU, dV, db
+
+
+def decay_workspace_size(B, Hq, Hkv, N, D, dtype: torch.dtype, is_bwd: bool, Dv: int | None = None) -> int:
+    code = LA_F32 if dtype == torch.float32 else LA_BF16
+    return int(load().la_decay_workspace_size(B, Hq, Hkv, N, D, D if Dv is None else Dv, code, int(is_bwd)))
+
+
+def decay_kernel_path(B, Hq, Hkv, N, D, dtype: torch.dtype, is_bwd: bool, Dv: int | None = None) -> int:
+    code = LA_F32 if dtype == torch.float32 else LA_BF16
+    return int(load().la_decay_kernel_path(B, Hq, Hkv, N, D, D if Dv is None else Dv, code, int(is_bwd)))
+
+
+def _check_vector(name, t, n, dtype, device):
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or t.shape != (n,) \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} vector of {n} elements on q's device")
+
+
+def _check_state(name, t, shape, device):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.device != device or tuple(t.shape) != shape \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor {shape} on q's device")
+
+
+def _output(name, t, shape, like):
+    if t is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    if tuple(t.shape) != tuple(shape) or t.dtype != like.dtype or t.device != like.device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor of q's dtype on q's device")
+    return t
+
+
+def _nbytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def decay_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, *, scale: float = 1.0,
+              initial_state: torch.Tensor | None = None, final_state: torch.Tensor | None = None,
+              lengths: torch.Tensor | None = None, out: torch.Tensor | None = None,
+              workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Linear attention with a decay for each key/value head, for prompts and training
+    (``la_decay_fwd``): S_i = exp(log_decay) S_{i-1} + k_i v_i^T, out_i = scale q_i S_i.
+
+    ``initial_state`` (float32 [B, Hkv, D, Dv]) is S before the first token, ``final_state``
+    receives S after the last; they may be the same tensor.  ``lengths`` (int32 [B]): tokens of
+    each sequence; out rows past them are zeros and what the inputs hold there is not used.
+    Returns ``out`` [B, Hq, N, Dv]."""
+    lib = load()
+    B, Hq, Hkv, N, D, Dv = _check_inputs(q, k, v, None, None)
+    dev, dt = q.device, _dtype_code(q)
+    _check_vector("log_decay", log_decay, Hkv, torch.float32, dev)
+    if lengths is not None:
+        _check_vector("lengths", lengths, B, torch.int32, dev)
+    for name, t in (("initial_state", initial_state), ("final_state", final_state)):
+        if t is not None:
+            _check_state(name, t, (B, Hkv, D, Dv), dev)
+    out = _output("out", out, (B, Hq, N, Dv), q)
+    ws = _workspace(lib.la_decay_workspace_size(B, Hq, Hkv, N, D, Dv, dt, 0), dev, workspace)
+    st = lib.la_decay_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(log_decay), _ptr(initial_state),
+                          _ptr(final_state), _ptr(lengths), B, Hq, Hkv, N, D, Dv, dt, scale, _strides(q), _strides(k),
+                          _strides(v), _ptr(ws), _nbytes(ws), _stream_handle(stream))
+    if st != LA_OK:
+        _raise(lib, st, "la_decay_fwd")
+    return out
+
+
+def decay_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, grad_out: torch.Tensor, log_decay: torch.Tensor, *,
+              scale: float = 1.0, initial_state: torch.Tensor | None = None,
+              grad_final_state: torch.Tensor | None = None, grad_initial_state: torch.Tensor | None = None,
+              dq: torch.Tensor | None = None, dk: torch.Tensor | None = None, dv: torch.Tensor | None = None,
+              workspace: torch.Tensor | None = None, stream=None):
+    """Gradient of ``decay_fwd`` (``la_decay_bwd``): returns ``(dq, dk, dv)``, dk and dv summed
+    over each group's query heads.  ``grad_final_state`` is the gradient of the forward's
+    final state (None: zeros); ``grad_initial_state``, when given, receives the initial state's.
+    ``log_decay`` gets no gradient."""
+    lib = load()
+    B, Hq, Hkv, N, D, Dv = _check_inputs(q, k, v, None, None, (("grad_out", grad_out),))
+    if tuple(grad_out.shape) != (B, Hq, N, Dv):
+        raise ValueError("grad_out must have the shape of out ([B, Hq, N, Dv])")
+    dev, dt = q.device, _dtype_code(q)
+    _check_vector("log_decay", log_decay, Hkv, torch.float32, dev)
+    for name, t in (("initial_state", initial_state), ("grad_final_state", grad_final_state),
+                    ("grad_initial_state", grad_initial_state)):
+        if t is not None:
+            _check_state(name, t, (B, Hkv, D, Dv), dev)
+    dq, dk, dv = _output("dq", dq, q.shape, q), _output("dk", dk, k.shape, q), _output("dv", dv, v.shape, q)
+    ws = _workspace(lib.la_decay_workspace_size(B, Hq, Hkv, N, D, Dv, dt, 1), dev, workspace)
+    st = lib.la_decay_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(grad_out), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(log_decay),
+                          _ptr(initial_state), _ptr(grad_final_state), _ptr(grad_initial_state), B, Hq, Hkv, N, D, Dv,
+                          dt, scale, _strides(q), _strides(k), _strides(v), _strides(grad_out), _ptr(ws), _nbytes(ws),
+                          _stream_handle(stream))
+    if st != LA_OK:
+        _raise(lib, st, "la_decay_bwd")
+    return dq, dk, dv
+
+
+def decay_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, state: torch.Tensor, log_decay: torch.Tensor, *,
+               slots: torch.Tensor | None = None, scale: float = 1.0, state_out: torch.Tensor | None = None,
+               out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """One token of each sequence (``la_decay_step``): q [B, Hq, 1, D], k [B, Hkv, 1, D], v [B, Hkv,
+    1, Dv] on a pool of states ``state`` (float32 [pool, Hkv, D, Dv]); sequence b owns slot
+    ``slots[b]`` (int32 [B]; None: slot b), and a slot outside the pool marks a padding row (out
+    zeros, no state touched).  The new states go to ``state_out`` at the same slots (None: into
+    ``state``).  Returns ``out`` [B, Hq, 1, Dv]."""
+    lib = load()
+    B, Hq, Hkv, N, D, Dv = _check_inputs(q, k, v, None, None)
+    if N != 1:
+        raise ValueError(f"decay_step takes one token per sequence (N = 1), got N = {N}")
+    dev = q.device
+    _check_vector("log_decay", log_decay, Hkv, torch.float32, dev)
+    if slots is not None:
+        _check_vector("slots", slots, B, torch.int32, dev)
+    pool = state.shape[0] if state.dim() == 4 else 0
+    _check_state("state", state, (pool, Hkv, D, Dv), dev)
+    if state_out is not None:
+        _check_state("state_out", state_out, (pool, Hkv, D, Dv), dev)
+    out = _output("out", out, (B, Hq, 1, Dv), q)
+    st = lib.la_decay_step(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(state),
+                           _ptr(state if state_out is None else state_out), _ptr(log_decay), _ptr(slots), pool, B, Hq,
+                           Hkv, D, Dv, _dtype_code(q), scale, _strides(q), _strides(k), _strides(v),
+                           _stream_handle(stream))
+    if st != LA_OK:
+        _raise(lib, st, "la_decay_step")
+    return out
+
+
+def _check_qk(q, k, extra=()):
+    for name, t in (("q", q), ("k", k)) + tuple(extra):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1) or min(t.stride()) < 0:
+            raise ValueError(f"{name} must be a [B, H, N, D] tensor whose last dimension is contiguous")
+        if t.dtype != q.dtype or t.device != q.device:
+            raise TypeError(f"{name} must have q's dtype and device")
+    B, Hq, N, D = q.shape
+    if k.shape[0] != B or tuple(k.shape[2:]) != (N, D):
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}")
+    return B, Hq, k.shape[1], N, D
+
+
+def _qk_args(q, q_weight, k_weight, eps, positions, inv_freq, sections, interleaved, normalize):
+    """la_qk_args of a call (and the host arrays that it points to)."""
+    B, _, N, D = q.shape
+    a = LaQkArgs(eps=eps, normalize=int(normalize), interleaved=int(interleaved))
+    weights = [w for w in (q_weight, k_weight) if w is not None]
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            if w.dtype not in (torch.float32, q.dtype) or w.dtype != weights[0].dtype:
+                raise TypeError(f"{name} must be float32 or of q's dtype, the same for both")
+            _check_vector(name, w, D, w.dtype, q.device)
+    a.weight_dtype = _dtype_code(weights[0]) if weights else LA_F32
+    a.q_weight = q_weight.data_ptr() if q_weight is not None else None
+    a.k_weight = k_weight.data_ptr() if k_weight is not None else None
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("give both positions and inv_freq or neither")
+    if inv_freq is None:
+        if sections is not None:
+            raise ValueError("sections need positions and inv_freq")
+        return a
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be a vector")
+    _check_vector("inv_freq", inv_freq, inv_freq.numel(), torch.float64, q.device)
+    if positions.dim() == 2:
+        positions = positions.unsqueeze(0)
+    if positions.dtype != torch.int64 or positions.device != q.device or positions.dim() != 3 \
+            or tuple(positions.shape[1:]) != (B, N):
+        raise ValueError(f"positions must be an int64 tensor [axes, {B}, {N}] or [{B}, {N}] on q's device")
+    axes = positions.shape[0]
+    if sections is None:
+        if axes != 1:
+            raise ValueError("several position axes need sections (pairs of each axis)")
+        sections = (inv_freq.numel(),)
+    if len(sections) != axes or sum(sections) != inv_freq.numel():
+        raise ValueError(f"sections {tuple(sections)} must name {axes} axes and add up to {inv_freq.numel()} pairs")
+    a.rot, a.axes = 2 * inv_freq.numel(), axes
+    a.sections = (ctypes.c_int * axes)(*sections)
+    a.positions, a.inv_freq = positions.data_ptr(), inv_freq.data_ptr()
+    a.pos_strides = (ctypes.c_longlong * 3)(*positions.stride())
+    return a
+
+
+def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, *, q_weight: torch.Tensor | None = None,
+                     k_weight: torch.Tensor | None = None, eps: float = 1e-6, positions: torch.Tensor | None = None,
+                     inv_freq: torch.Tensor | None = None, sections=None, interleaved: bool = False,
+                     normalize: bool = True, q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                     stream=None):
+    """RMS norm of every head's query and key row, times its weight, then the rotation of
+    positions, in one pass (``la_qk_norm_rope_fwd``); returns ``(q_out, k_out)``, contiguous.
+
+    ``positions`` (int64 [B, N], or [axes, B, N] for up to four axes) times ``inv_freq`` (float64
+    [rot / 2]) are the angles of the pairs; ``sections`` gives the pairs of each axis in turn.
+    Pairs are (p, p + rot / 2), or (2p, 2p + 1) with ``interleaved``; elements past rot are not
+    turned.  Without positions: the norm alone; with ``normalize=False``: the rotation alone."""
+    lib = load()
+    B, Hq, Hkv, N, D = _check_qk(q, k)
+    a = _qk_args(q, q_weight, k_weight, eps, positions, inv_freq, sections, interleaved, normalize)
+    q_out, k_out = _output("q_out", q_out, q.shape, q), _output("k_out", k_out, k.shape, q)
+    st = lib.la_qk_norm_rope_fwd(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), B, Hq, Hkv, N, D, _dtype_code(q),
+                                 _strides(q), _strides(k), ctypes.byref(a), _stream_handle(stream))
+    if st != LA_OK:
+        _raise(lib, st, "la_qk_norm_rope_fwd")
+    return q_out, k_out
+
+
+def qk_norm_rope_workspace_size(B, Hq, Hkv, N, D, dtype: torch.dtype) -> int:
+    code = LA_F32 if dtype == torch.float32 else LA_BF16
+    return int(load().la_qk_norm_rope_workspace_size(B, Hq, Hkv, N, D, code))
+
+
+def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, grad_q: torch.Tensor, grad_k: torch.Tensor, *,
+                     q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                     positions: torch.Tensor | None = None, inv_freq: torch.Tensor | None = None, sections=None,
+                     interleaved: bool = False, normalize: bool = True, dq: torch.Tensor | None = None,
+                     dk: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Gradient of ``qk_norm_rope_fwd`` for its inputs q, k and the gradients of its outputs
+    (``la_qk_norm_rope_bwd``): returns ``(dq, dk, dq_weight, dk_weight)``, a weight's gradient None
+    without that weight."""
+    lib = load()
+    B, Hq, Hkv, N, D = _check_qk(q, k, (("grad_q", grad_q), ("grad_k", grad_k)))
+    if grad_q.shape != q.shape or grad_k.shape != k.shape:
+        raise ValueError("grad_q and grad_k must have the shapes of q and k")
+    a = _qk_args(q, q_weight, k_weight, eps, positions, inv_freq, sections, interleaved, normalize)
+    dq, dk = _output("dq", dq, q.shape, q), _output("dk", dk, k.shape, q)
+    dqw = torch.empty_like(q_weight) if q_weight is not None else None
+    dkw = torch.empty_like(k_weight) if k_weight is not None else None
+    dt, ws = _dtype_code(q), None
+    if dqw is not None or dkw is not None:
+        ws = _workspace(lib.la_qk_norm_rope_workspace_size(B, Hq, Hkv, N, D, dt), q.device, workspace)
+    st = lib.la_qk_norm_rope_bwd(_ptr(q), _ptr(k), _ptr(grad_q), _ptr(grad_k), _ptr(dq), _ptr(dk), _ptr(dqw),
+                                 _ptr(dkw), B, Hq, Hkv, N, D, dt, _strides(q), _strides(k), _strides(grad_q),
+                                 _strides(grad_k), ctypes.byref(a), _ptr(ws), _nbytes(ws), _stream_handle(stream))
+    if st != LA_OK:
+        _raise(lib, st, "la_qk_norm_rope_bwd")
+    return dq, dk, dqw, dkw
 
 
 def get_status(stream=None) -> None:

@@ -274,6 +274,114 @@ la_status la_lowrank_bwd_t(const void *x, const void *U, const void *V, const vo
                            int K_in, int r, int K_out, la_dtype dtype, void *workspace,
                            size_t ws_bytes, void *stream);
 
+/* ---- decayed linear attention -------------------------------------------------------------
+ *
+ * Linear attention whose state of each key/value head decays by gamma = exp(log_decay[head])
+ * with every token (a matrix-valued state S [D, Dv], float32):
+ *
+ *   S_i = gamma S_{i-1} + k_i v_i^T,      out_i = scale q_i^T S_i
+ *
+ * i.e. out_i = scale sum_{j <= i} gamma^(i-j) (q_i . k_j) v_j + scale gamma^(i+1) q_i^T S_0.  No
+ * feature map and no denominator: q and k are used as given (see la_qk_norm_rope_fwd).  The
+ * pages have no counterpart of these entry points; layouts, grouped heads, dtypes, ownership,
+ * streams and errors are la_fwd's: q, out [B, Hq, N, D | Dv], k, v [B, Hkv, N, D | Dv], D and Dv
+ * in {32, 64, 128}, query head h reads key/value head h / n_rep; inputs may be strided
+ * (la_strides, NULL: contiguous), outputs are contiguous.
+ *
+ * log_decay [Hkv] is a float32 device vector, expected <= 0 (a non-finite -inf is gamma = 0:
+ * each token sees itself alone); it gets no gradient.  Values above 0 grow the state by the
+ * same formula.  scale: finite and not 0.
+ *
+ * A NaN or infinity in a token's row reaches, besides the outputs that depend on it, at most
+ * the other rows of the same 128-token chunk. */
+
+/* Bytes of workspace of la_decay_fwd (is_bwd = 0) or la_decay_bwd (is_bwd = 1); 0 for arguments
+ * that they reject (and where none is needed).  Host-only. */
+size_t la_decay_workspace_size(int B, int Hq, int Hkv, int N, int D, int Dv, la_dtype dtype, int is_bwd);
+
+/* Kernel family of la_decay_fwd and la_decay_bwd: LA_PATH_TCGEN05 for bfloat16 with D and Dv in
+ * {64, 128}, any n_rep (every input stride must then be a multiple of 8 elements, else
+ * LA_ERR_ALIGN); LA_PATH_SIMT (float32 arithmetic, any strides) otherwise. */
+la_path la_decay_kernel_path(int B, int Hq, int Hkv, int N, int D, int Dv, la_dtype dtype, int is_bwd);
+
+/* Chunked form, for prompts and training.  initial_state [B, Hkv, D, Dv] float32 or NULL (zeros);
+ * final_state like it or NULL (not wanted), may be the same buffer.  lengths: NULL, or a device
+ * vector of B int32: sequence b has min(max(lengths[b], 0), N) tokens.  Rows past a sequence's
+ * length are never used, whatever they hold; their out rows are zeros and final_state is the
+ * state after the last token (the initial state when there is none). */
+la_status la_decay_fwd(const void *q, const void *k, const void *v, void *out, const float *log_decay,
+                       const float *initial_state, float *final_state, const int *lengths, int B, int Hq, int Hkv,
+                       int N, int D, int Dv, la_dtype dtype, float scale, const la_strides *q_strides,
+                       const la_strides *k_strides, const la_strides *v_strides, void *workspace, size_t ws_bytes,
+                       void *stream);
+
+/* Exact gradient of la_decay_fwd (without lengths): writes dq [B, Hq, N, D], dk [B, Hkv, N, D],
+ * dv [B, Hkv, N, Dv] (summed over each group's query heads) and, when given, grad_initial_state.
+ * grad_final_state: the gradient of final_state, or NULL (zeros); both [B, Hkv, D, Dv] float32,
+ * not overlapping.  Nothing of the forward is needed: the states are recomputed. */
+la_status la_decay_bwd(const void *q, const void *k, const void *v, const void *grad_out, void *dq, void *dk, void *dv,
+                       const float *log_decay, const float *initial_state, const float *grad_final_state,
+                       float *grad_initial_state, int B, int Hq, int Hkv, int N, int D, int Dv, la_dtype dtype,
+                       float scale, const la_strides *q_strides, const la_strides *k_strides,
+                       const la_strides *v_strides, const la_strides *g_strides, void *workspace, size_t ws_bytes,
+                       void *stream);
+
+/* Recurrent form, one token per sequence (q, out [B, Hq, 1, D | Dv], k, v [B, Hkv, 1, D | Dv]), on a
+ * pool of `pool` states [pool, Hkv, D, Dv] float32: sequence b owns slot slots[b] (device int32;
+ * NULL: slot b).  Its state becomes gamma S + k v^T, in state_out at the same slot (state_out may
+ * be `state`: in place; slots that no sequence names are not touched), and out = scale q^T S of the new
+ * state.  A sequence whose slot is outside [0, pool) is padding: its out rows are zeros and no
+ * state changes.  Two sequences of one call must not name the same slot.  Any strides (n is not used). */
+la_status la_decay_step(const void *q, const void *k, const void *v, void *out, const float *state, float *state_out,
+                        const float *log_decay, const int *slots, int pool, int B, int Hq, int Hkv, int D, int Dv,
+                        la_dtype dtype, float scale, const la_strides *q_strides, const la_strides *k_strides,
+                        const la_strides *v_strides, void *stream);
+
+/* ---- norm of queries and keys with the position rotation ------------------------------------
+ *
+ * One pass over q [B, Hq, N, D] and k [B, Hkv, N, D]: every head's row x becomes
+ *
+ *   y = Rot(x r w),   r = rsqrt(mean(x^2) + eps)
+ *
+ * normalize = 0 leaves out r and w (rotation alone).  q_weight, k_weight: NULL (ones) or D elements
+ * of weight_dtype (LA_F32, or the inputs' type).  Rot turns pair p of the row's first `rot` elements
+ * (rot a multiple of 16, <= D; 0: no rotation) by the angle positions[a][b][n] inv_freq[p], where a
+ * is the axis that pair p belongs to: the first sections[0] pairs to axis 0, the next sections[1]
+ * to axis 1 and so on (1 to 4 axes, e.g. time, height, width; sum of sections = rot / 2).  Pair p is
+ * elements (p, p + rot / 2), or (2p, 2p + 1) with interleaved = 1; elements past rot are not turned.
+ * positions: device int64 [axes, B, N] with element strides pos_strides[3] (0 broadcasts);
+ * inv_freq: rot / 2 device float64; sections and pos_strides are host arrays.  Angles are reduced
+ * in 64-bit integer turns, so they are exact to float32 for every position.
+ *
+ * Inputs may be strided (rows must start on 16-byte boundaries, else LA_ERR_ALIGN); outputs are
+ * contiguous and may not overlap the inputs.  Float32 arithmetic, D in {32, 64, 128}.  The pages have no
+ * counterpart of these entry points; errors and streams are la_fwd's. */
+typedef struct {
+    const void *q_weight, *k_weight;
+    la_dtype weight_dtype;
+    float eps;                       /* >= 0, finite */
+    int normalize, interleaved;
+    int rot, axes;
+    const int *sections;             /* host, `axes` entries (NULL: one axis) */
+    const long long *positions;      /* device */
+    const long long *pos_strides;    /* host, 3 entries */
+    const double *inv_freq;          /* device */
+} la_qk_args;
+
+la_status la_qk_norm_rope_fwd(const void *q, const void *k, void *q_out, void *k_out, int B, int Hq, int Hkv, int N,
+                              int D, la_dtype dtype, const la_strides *q_strides, const la_strides *k_strides,
+                              const la_qk_args *args, void *stream);
+
+/* Gradient: from grad_q, grad_k (of q_out, k_out) and the forward's inputs, dq [B, Hq, N, D], dk [B, Hkv, N,
+ * D] and, where not NULL, dq_weight and dk_weight (D elements of weight_dtype; they need normalize = 1).  The sums over rows
+ * are taken in a fixed order.  Workspace: la_qk_norm_rope_workspace_size (256-byte aligned). */
+size_t la_qk_norm_rope_workspace_size(int B, int Hq, int Hkv, int N, int D, la_dtype dtype);
+la_status la_qk_norm_rope_bwd(const void *q, const void *k, const void *grad_q, const void *grad_k, void *dq, void *dk,
+                              void *dq_weight, void *dk_weight, int B, int Hq, int Hkv, int N, int D, la_dtype dtype,
+                              const la_strides *q_strides, const la_strides *k_strides, const la_strides *gq_strides,
+                              const la_strides *gk_strides, const la_qk_args *args, void *workspace, size_t ws_bytes,
+                              void *stream);
+
 /* Forward for callers that cannot allocate device memory.
  *
  * Some callers have no way to obtain scratch memory on the GPU: a plugin host that hands
