@@ -26,22 +26,45 @@ struct DecayPlan {
     size_t state_bytes, ws_bytes;   // one array of segment states; all of them
 };
 
-// The segments of a sequence: the count whose schedule ends first, `units` blocks of work per segment
-// on `slots` places that run at once, a block costing its chunks plus about two for its
-// start; more than one segment costs the pass that sums them, about half a chunk each.
-DecayPlan make_plan(int B, int Hkv, int N, int D, int Dv, la_dtype dt, bool bwd) {
+bool tc_runs(int D, int Dv, la_dtype dt) { return dt == LA_BF16 && D != 32 && Dv != 32; }
+
+// The segments of a sequence: the count whose schedule ends first.  A schedule is waves of `places` blocks that
+// run at once, a block costing its chunks (`work` each) plus about two for its start; more than
+// one segment costs the kernel that sums them (state_units blocks of state_work a chunk).
+DecayPlan make_plan(int B, int Hq, int Hkv, int N, int D, int Dv, la_dtype dt, bool bwd) {
     DecayPlan pl{};
-    pl.path = LA_PATH_SIMT;
-    (void)dt;
-    const int chunk = 32;
-    const long long units = (long long)B * Hkv * ((bwd ? (D > Dv ? D : Dv) : Dv) / kDecaySimtSlice);
-    const int slots = 3 * kPlanSms, nchunks = (N + chunk - 1) / chunk;
+    const int reps = Hq / Hkv;
+    const long long heads = (long long)B * Hkv;
+    long long units, state_units;
+    int places, chunk, most;
+    double work, state_work;
+    if (tc_runs(D, Dv, dt)) {
+        // in units of one chunk's x, y, z and out tiles
+        pl.path = LA_PATH_TCGEN05;
+        chunk = kDecayTcChunk;
+        places = kPlanSms;
+        units = heads * (bwd ? 3 : 1);
+        work = (2.0 * reps + 2.0) / 4.0;
+        state_units = heads * (bwd ? 2 : 1);
+        state_work = bwd ? (2.0 * reps + 2.0) / 8.0 : 0.5;
+        most = 256;
+    } else {
+        pl.path = LA_PATH_SIMT;
+        chunk = 32;
+        places = 3 * kPlanSms;
+        units = heads * ((bwd ? (D > Dv ? D : Dv) : Dv) / kDecaySimtSlice);
+        work = 1.0;
+        state_units = heads * (Dv / kDecaySimtSlice) * (bwd ? 2 : 1);
+        state_work = 0.4;
+        most = 64;
+    }
+    const int nchunks = (N + chunk - 1) / chunk;
     double best = -1.0;
     int best_cps = nchunks;
-    for (int want = 1; want <= nchunks && want <= 64; ++want) {
+    for (int want = 1; want <= nchunks && want <= most; ++want) {
         const int cps = (nchunks + want - 1) / want, nseg = (nchunks + cps - 1) / cps;
-        const long long waves = (units * nseg + slots - 1) / slots;
-        const double cost = waves * (cps * (nseg > 1 ? 1.5 : 1.0) + 2.0 + (nseg > 1 ? 2.0 : 0.0));
+        double cost = (double)((units * nseg + places - 1) / places) * (cps * work + 2.0);
+        if (nseg > 1) cost += (double)((state_units * (nseg - 1) + places - 1) / places) * (cps * state_work + 2.0);
         if (best < 0 || cost < best) {
             best = cost;
             best_cps = cps;
@@ -49,7 +72,7 @@ DecayPlan make_plan(int B, int Hkv, int N, int D, int Dv, la_dtype dt, bool bwd)
     }
     pl.seg_len = best_cps * chunk;
     pl.nseg = (N + pl.seg_len - 1) / pl.seg_len;
-    pl.state_bytes = pl.nseg > 1 ? ((size_t)B * Hkv * pl.nseg * D * Dv * 4 + 255) / 256 * 256 : 0;
+    pl.state_bytes = pl.nseg > 1 ? ((size_t)heads * pl.nseg * D * Dv * 4 + 255) / 256 * 256 : 0;
     pl.ws_bytes = pl.state_bytes * (bwd ? 2 : 1);
     return pl;
 }
@@ -89,11 +112,15 @@ la_status run(bool bwd, const Given &a, int B, int Hq, int Hkv, int N, int D, in
     if (!input_strides(a.sq, B, Hq, N, D, &sq) || !input_strides(a.sk, B, Hkv, N, D, &sk) ||
         !input_strides(a.sv, B, Hkv, N, Dv, &sv) || !input_strides(a.sg, B, Hq, N, Dv, &sg))
         return LA_ERR_ARG;
-    const DecayPlan pl = make_plan(B, Hkv, N, D, Dv, dt, bwd);
+    const DecayPlan pl = make_plan(B, Hq, Hkv, N, D, Dv, dt, bwd);
     if (pl.ws_bytes > 0) {
         if (!ws || ws_bytes < pl.ws_bytes) return LA_ERR_WORKSPACE;
         if (!aligned(ws, 256)) return LA_ERR_ALIGN;
     }
+    const bool tc = pl.path == LA_PATH_TCGEN05;
+    if (tc)   // TMA: every stride a multiple of 16 bytes (8 bf16)
+        for (const Strides &x : {sq, sk, sv, sg})
+            if (x.b % 8 || x.h % 8 || x.n % 8) return LA_ERR_ALIGN;
     DecayParams p{};
     p.log_decay = a.log_decay;
     p.lengths = a.lengths;
@@ -138,6 +165,13 @@ la_status run(bool bwd, const Given &a, int B, int Hq, int Hkv, int N, int D, in
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
+    if (tc) {
+        e = error_word(&p.err);
+        sp.err = p.err;
+        if (e == cudaSuccess && pl.nseg > 1) e = decay_tc_states(sp, s);
+        if (e == cudaSuccess) e = decay_tc_passes(p, s);
+        return e == cudaSuccess ? LA_OK : cuda_fail(e);
+    }
     if (pl.nseg > 1) e = decay_simt_states(sp, dt, s);
     for (int i = 0; e == cudaSuccess && i < p.npass; ++i) e = decay_simt_pass(p, i, dt, s);
     return e == cudaSuccess ? LA_OK : cuda_fail(e);
@@ -152,12 +186,12 @@ extern "C" {
 
 size_t la_decay_workspace_size(int B, int Hq, int Hkv, int N, int D, int Dv, la_dtype dtype, int is_bwd) {
     if (check(B, Hq, Hkv, N, D, Dv, dtype, 1.f) != LA_OK) return 0;
-    return make_plan(B, Hkv, N, D, Dv, dtype, is_bwd).ws_bytes;
+    return make_plan(B, Hq, Hkv, N, D, Dv, dtype, is_bwd).ws_bytes;
 }
 
 la_path la_decay_kernel_path(int B, int Hq, int Hkv, int N, int D, int Dv, la_dtype dtype, int is_bwd) {
     if (check(B, Hq, Hkv, N, D, Dv, dtype, 1.f) != LA_OK) return LA_PATH_SIMT;
-    return make_plan(B, Hkv, N, D, Dv, dtype, is_bwd).path;
+    return make_plan(B, Hq, Hkv, N, D, Dv, dtype, is_bwd).path;
 }
 
 la_status la_decay_fwd(const void *q, const void *k, const void *v, void *out, const float *log_decay,

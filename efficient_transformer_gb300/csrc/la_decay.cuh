@@ -80,6 +80,12 @@ constexpr int kDecaySimtSlice = 32;   // columns of out that a block owns
 cudaError_t decay_simt_states(const DecayStateParams &p, la_dtype dt, cudaStream_t s);
 cudaError_t decay_simt_pass(const DecayParams &p, int pass, la_dtype dt, cudaStream_t s);
 
+// Tensor-core kernels (la_decay_tc.cu): bfloat16, widths 64 and 128.  Segments are cut in token
+// order, multiples of kDecayTcChunk tokens; every pass of a call in one launch where the widths allow.
+constexpr int kDecayTcChunk = 128;
+cudaError_t decay_tc_states(const DecayStateParams &p, cudaStream_t s);
+cudaError_t decay_tc_passes(const DecayParams &p, cudaStream_t s);
+
 // One token (la_decay_step).
 struct DecayStepParams {
     const void *q, *k, *v;
