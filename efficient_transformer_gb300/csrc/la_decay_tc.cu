@@ -17,7 +17,7 @@
 // Several heads of x share one chunk of y, z (grouped queries; S moves on after the last), or several heads
 // of y, z share one of x (their gradients; O and S sum over the heads).
 //
-// Warps: 0 TMA, 1 MMA, 4-7 P, 8-11 S -> S_bf and the decay of S, 12-15 O's row powers and the output,
+// Warps: 0 TMA, 1 MMA of scores and P Z, 2 MMA of X S_bf and the state, 4-7 P, 8-11 S -> S_bf and the decay of S, 12-15 O's row powers and the output,
 // 16-23 Y^T (and the zeros past a sequence's length).
 //
 // The reverse passes (gradients of k and v) take the same steps with j >= i and gamma^(j-i), chunks from the
@@ -63,28 +63,62 @@ __device__ __forceinline__ Part part_of(int n, int N, int u, int nseg, int seg_l
     return r;
 }
 
-// Y^T of one tile for the threads of lane quarter `wq`: lane d's 32 values j0 .. j0 + 31 times w[j] (times
-// `mul`), as two bf16 terms into 16 columns each at th and tl.  Values at j >= valid are taken as zeros.
-__device__ __forceinline__ void yt_block(const uint8_t *y, int d, int j0, const float *w, float mul, int valid,
-                                         uint32_t th, uint32_t tl) {
-    uint32_t hi[16], lo[16];
+// a b for two pairs of floats (one packed instruction).
+__device__ __forceinline__ void mul2(float &x, float &y, float a, float b) {
+    unsigned long long p, q;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(q) : "f"(a), "f"(b));
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(p) : "l"(q));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
+}
+
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t u) { return *reinterpret_cast<__nv_bfloat162 *>(&u); }
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 h) { return *reinterpret_cast<uint32_t *>(&h); }
+
+// The decays w of 64 tokens (8 groups of 8) of which a thread meets 2 in each group, as two bf16 terms.
+struct YtWeights {
+    uint32_t hi[8], lo[8];
+    __device__ __forceinline__ void set(const float *w, float mul) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        const int j = j0 + 2 * e;
-        uint32_t a = *reinterpret_cast<const uint16_t *>(y + swz_offset(C, j, d));
-        uint32_t b = *reinterpret_cast<const uint16_t *>(y + swz_offset(C, j + 1, d));
-        if (valid < C) {
-            a = j < valid ? a : 0u;
-            b = j + 1 < valid ? b : 0u;
+        for (int g = 0; g < 8; ++g) {
+            const float a = w[8 * g + 2 * (threadIdx.x % 4)] * mul, b = w[8 * g + 2 * (threadIdx.x % 4) + 1] * mul;
+            hi[g] = pack_bf16x2(a, b);
+            const float2 f = unpack_bf16x2(hi[g]);
+            lo[g] = pack_bf16x2(a - f.x, b - f.y);
         }
-        const float2 wj = *reinterpret_cast<const float2 *>(w + j);
-        const float fa = __uint_as_float(a << 16) * (wj.x * mul), fb = __uint_as_float(b << 16) * (wj.y * mul);
-        const uint32_t h = pack_bf16x2(fa, fb);
-        hi[e] = h;
-        lo[e] = pack_bf16x2(fa - __uint_as_float(h << 16), fb - __uint_as_float(h & 0xffff0000u));
     }
-    tmem_st16_raw(th, hi);
-    tmem_st16_raw(tl, lo);
+};
+
+// Decayed Y^T of one tile for the warp's 32 lanes d and the 64 tokens from j0: y w as two bf16 terms, into
+// 32 columns each at th and tl.  With w = wh + wl (bf16 each), hi = bf16(y wh), the remainder y wh - hi is exact in
+// bf16 (one fused multiply-add) and lo = bf16(remainder + y wl): three packed operations a pair, 2^-17 relative in
+// all.  The tile's 8 x 8 blocks come transposed out of shared memory in the layout of the store.
+// Tokens at or past `valid` count as zeros whatever they hold.
+__device__ __forceinline__ void yt_block(const uint8_t *y, int d0, int j0, const YtWeights &w, int valid, uint32_t th,
+                                         uint32_t tl) {
+    const int t = threadIdx.x % 32;
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {   // lanes d0 + 16 half ..
+        const uint32_t addr = smem_u32(y) + swz_chunk(C, j0 + 8 * (t / 16) + t % 8, (d0 + 16 * half) / 8 + ((t / 8) & 1));
+        uint32_t v[16], hi[16], lo[16];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) ldmatrix_x4_trans(addr + q * 16 * 128, v + 4 * q);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int g = i / 2;   // group of 8 tokens
+            uint32_t u = v[i];
+            if (valid < C) {
+                const int j = j0 + 8 * g + 2 * (t % 4);
+                u = j + 1 < valid ? u : j < valid ? u & 0xffffu : 0u;
+            }
+            const __nv_bfloat162 wh = as_bf162(w.hi[g]), h = __hmul2(as_bf162(u), wh);
+            const __nv_bfloat162 r = __hfma2(as_bf162(u), wh, __hneg2(h));
+            hi[i] = as_u32(h);
+            lo[i] = as_u32(__hfma2(as_bf162(u), as_bf162(w.lo[g]), r));
+        }
+        tmem_st_frag32(th + ((uint32_t)(16 * half) << 16), hi);
+        tmem_st_frag32(tl + ((uint32_t)(16 * half) << 16), lo);
+    }
 }
 
 // Zero rows [valid, C) of a C x W tile (what lies past a sequence's length must not meet the MMA, where 0
@@ -103,7 +137,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
     constexpr int NX = K::NX, NY = K::NY;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t x_full[NX], x_empty[NX], yz_full[NY], yz_empty[NY];
-    __shared__ uint64_t sc_full, p_ready, o_inter, o_scaled, o_full, o_free, s_full, s_conv, yt_ready, yt_done, fin;
+    __shared__ uint64_t sc_full, p_ready, o_inter, o_scaled, o_full, o_free, s_full, s_conv, yt_ready, yt_done, fin[2];
     __shared__ __align__(16) float pw[C + 4], wtab[2][C];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
@@ -134,7 +168,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         }
         for (int s = 0; s < NY; ++s) {
             mbar_init(&yz_full[s], 1);
-            mbar_init(&yz_empty[s], 1);
+            mbar_init(&yz_empty[s], 2);
         }
         mbar_init(&sc_full, 1);
         mbar_init(&p_ready, 128);
@@ -146,7 +180,8 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         mbar_init(&s_conv, 128);
         mbar_init(&yt_ready, kYtThreads);
         mbar_init(&yt_done, 1);
-        mbar_init(&fin, 1);
+        mbar_init(&fin[0], 1);
+        mbar_init(&fin[1], 1);
         fence_barrier_init();
     }
     for (int i = threadIdx.x; i <= C; i += kMainThreads) pw[i] = exp2f(l2 * i);
@@ -197,76 +232,107 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         for (int i = nx > NX ? nx - NX : 0; i < nx; ++i) warp_drain(&x_full[i % NX], (i / NX) & 1);
         for (int i = ny > NY ? ny - NY : 0; i < ny; ++i) warp_drain(&yz_full[i % NY], (i / NY) & 1);
     } else if (warp == 1) {
-        // ---------------- MMA issuer
+        // ---------------- scores and P Z
         constexpr uint32_t idA = idesc_bf16(128, C, false, false);
         constexpr uint32_t idO = idesc_bf16(128, DZ, false, true);
-        const uint32_t sb = smem_u32(sbf), tS = tm + K::T_S, tO = tm + K::T_O, tA = tm + K::T_A;
-        const uint32_t tYh = tm + K::T_YH, tYl = tm + K::T_YL;
-        int ix = 0, iy = 0, st = 0, ot = 0;   // x tile, y z tile, state update, output tile
-        bool ok = true;
-        for (int it = 0; ok && it < items; ++it) {
-            const int k = it / reps, r = it % reps;
+        const uint32_t tO = tm + K::T_O, tA = tm + K::T_A;
+        int ix = 0, iy = 0, ot = 0, k = 0, r = 0;   // x tile, y z tile, output tile, chunk, head
+        for (int it = 0; it < items; ++it) {
             const bool first = r == 0, last = r == reps - 1;
-            if (first || !many) {
-                if (it > 0) ++ix;
-                if (!warp_wait(&x_full[ix % NX], (ix / NX) & 1, &abort_flag)) break;
-            }
-            if (first || many) {
-                if (it > 0) ++iy;
-                if (!warp_wait(&yz_full[iy % NY], (iy / NY) & 1, &abort_flag)) break;
-            }
+            if ((first || !many) && !warp_wait(&x_full[ix % NX], (ix / NX) & 1, &abort_flag)) break;
+            if ((first || many) && !warp_wait(&yz_full[iy % NY], (iy / NY) & 1, &abort_flag)) break;
             const uint32_t x = smem_u32(xbuf + (ix % NX) * K::X_BYTES);
             const uint32_t y = smem_u32(yzbuf + (iy % NY) * K::YZ_BYTES), z = y + K::Y_BYTES;
             tc_fence_after();
-            // scores (P of the item before has been read: MMAs run in the order of their issue)
+            LA_TL(it, 0);
+            // (P of the item before has been read: this warp's MMAs run in the order of their issue)
+#pragma unroll
             for (int kk = 0; kk < DX / 16; ++kk) mma_bf16_w(tA, desc_kmajor(x, C, 0, kk), desc_kmajor(y, C, 0, kk), idA, kk > 0);
             mma_commit_w(&sc_full);
-            // X S_bf, once for each output tile
+            LA_TL(it, 1);
+            if ((first || !many) && !warp_wait(&o_scaled, ot & 1, &abort_flag)) break;
+            LA_TL(it, 5);
+            // rows past a sequence's length are zeroed by the Y^T warps before P Z may read them (o_scaled says
+            // that every earlier Y^T is over)
+            if (p.lengths && first && k == nchunk - 1 && vlast < C && !warp_wait(&yt_ready, k & 1, &abort_flag)) break;
+            if (!warp_wait(&p_ready, it & 1, &abort_flag)) break;
+            LA_TL(it, 4);
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < C / 16; ++kk) mma_bf16_ta_w(tO, tA + kk * 8, desc_mnmajor(z, C, 0, kk), idO, 1u);
+            if (last || !many) {
+                mma_commit_w(&o_full);
+                ++ot;
+                ++ix;
+            }
+            if (last || many) {
+                mma_commit_w(&yz_empty[iy % NY]);
+                ++iy;
+            }
+            LA_TL(it, 6);
+            if (++r == reps) {
+                r = 0;
+                ++k;
+            }
+        }
+        mma_commit_w(&fin[0]);
+        warp_drain(&fin[0], 0);
+    } else if (warp == 2) {
+        // ---------------- X S_bf, once for each output tile, and S += Y^T Z, once for each y z tile (grouped queries:
+        // after the chunk's last X S_bf)
+        constexpr uint32_t idO = idesc_bf16(128, DZ, false, true);
+        const uint32_t sb = smem_u32(sbf), tS = tm + K::T_S, tO = tm + K::T_O;
+        const uint32_t tYh = tm + K::T_YH, tYl = tm + K::T_YL;
+        int ix = 0, iy = 0, k = 0, r = 0;
+        for (int it = 0; it < items; ++it) {
+            const bool first = r == 0, last = r == reps - 1;
             if (first || !many) {
+                if (!warp_wait(&x_full[ix % NX], (ix / NX) & 1, &abort_flag)) break;
                 if (first && !warp_wait(&s_conv, k & 1, &abort_flag)) break;
-                if (ot > 0 && !warp_wait(&o_free, (ot - 1) & 1, &abort_flag)) break;
+                if (ix > 0 && !warp_wait(&o_free, (ix - 1) & 1, &abort_flag)) break;
+                LA_TL(it, 2);
                 tc_fence_after();
-                for (int kk = 0; kk < DX / 16; ++kk) mma_bf16_w(tO, desc_kmajor(x, C, 0, kk), desc_mnmajor(sb, DX, 0, kk), idO, kk > 0);
+                const uint32_t x = smem_u32(xbuf + (ix % NX) * K::X_BYTES);
+#pragma unroll
+                for (int kk = 0; kk < DX / 16; ++kk)
+                    mma_bf16_w(tO, desc_kmajor(x, C, 0, kk), desc_mnmajor(sb, DX, 0, kk), idO, kk > 0);
                 mma_commit_w(&o_inter);
+                ++ix;
             }
-            // S += Y^T Z, once for each y z tile (grouped queries: with the chunk's last head)
-            const bool upd = many || last;
-            // tiles with rows past the length are zeroed by the Y^T warps before P Z may read them (such
-            // a tile is the sequence's last, of grouped queries: its Y^T serves the last head's update too)
-            const bool zeroed = p.lengths && chunk0(k) + C > part.hi;
-            if (zeroed ? first : upd) {
-                if (!warp_wait(&yt_ready, st & 1, &abort_flag)) break;
+            if (last || many) {
+                if (!warp_wait(&yt_ready, iy & 1, &abort_flag)) break;
+                LA_TL(it, 3);
                 tc_fence_after();
-            }
-            if (upd) {
+                const uint32_t z = smem_u32(yzbuf + (iy % NY) * K::YZ_BYTES) + K::Y_BYTES;
+#pragma unroll
                 for (int kk = 0; kk < C / 16; ++kk) {
                     mma_bf16_ta_w(tS, tYh + kk * 8, desc_mnmajor(z, C, 0, kk), idO, 1u);
                     mma_bf16_ta_w(tS, tYl + kk * 8, desc_mnmajor(z, C, 0, kk), idO, 1u);
                 }
                 mma_commit_w(&yt_done);
                 if (last) mma_commit_w(&s_full);
-                ++st;
+                mma_commit_w(&yz_empty[iy % NY]);
+                ++iy;
             }
-            // O += P Z
-            if (!warp_wait(&p_ready, it & 1, &abort_flag)) break;
-            if ((first || !many) && !warp_wait(&o_scaled, ot & 1, &abort_flag)) break;
-            tc_fence_after();
-            for (int kk = 0; kk < C / 16; ++kk) mma_bf16_ta_w(tO, tA + kk * 8, desc_mnmajor(z, C, 0, kk), idO, 1u);
-            if (last || !many) {
-                mma_commit_w(&o_full);
-                ++ot;
+            if (++r == reps) {
+                r = 0;
+                ++k;
             }
-            if (upd) mma_commit_w(&yz_empty[iy % NY]);
         }
-        mma_commit_w(&fin);
-        warp_drain(&fin, 0);
+        mma_commit_w(&fin[1]);
+        warp_drain(&fin[1], 0);
     } else if (warp >= 4 && warp < 8) {
-        // ---------------- P = bf16(A o W), thread = row i
-        const int wq = warp % 4, lane = threadIdx.x % 32, i = wq * 32 + lane;
+        // ---------------- P = bf16(A o W), thread = row i, 16 columns at a time.  Away from the diagonal
+        // gamma^|i - j| = gamma^(distance to the block's near end) gamma^(distance in the block), the latter in registers
+        const int wq = warp % 4, i = wq * 32 + threadIdx.x % 32;
         const uint32_t ta = tm + K::T_A + ((uint32_t)(wq * 32) << 16);
+        float g[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) g[e] = pw[rev ? e : 15 - e];
         for (int it = 0; it < items; ++it) {
             if (!warp_wait(&sc_full, it & 1, &abort_flag)) break;
             tc_fence_after();
+            if (i == 127) LA_TL(it, 7);
 #pragma unroll 1
             for (int cb = 0; cb < C / 32; ++cb) {
                 uint32_t w[16];
@@ -276,27 +342,27 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                 } else {
                     float v[32];
                     tmem_ld32(ta + cb * 32, v);
-                    if (cb == wq) {
-                        // gamma^|i - j| of the tokens on this side of the diagonal
-                        const float *pd = pw;
-                        tmem_wait_regs<32>(v);
+                    tmem_wait_regs<32>(v);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const int ago = rev ? e - lane : lane - e;
-                            v[e] = ago >= 0 ? v[e] * pd[max(ago, 0)] : 0.f;
-                        }
-                    } else {
-                        // gamma^|i - j| = gamma^(distance to the block's near end) gamma^(distance in the block)
-                        const float base = pw[rev ? cb * 32 - i : i - cb * 32 - 31];
-                        const float4 *t4 = reinterpret_cast<const float4 *>(rev ? pw : &wtab[0][C - 32]);
-                        tmem_wait_regs<32>(v);
+                    for (int hb = 0; hb < 2; ++hb) {
+                        const int j0 = cb * 32 + hb * 16;
+                        if (cb == wq) {   // the diagonal: tokens on this side of it
+                            const float ago0 = (float)(rev ? j0 - i : i - j0);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const float4 t = t4[q];
-                            v[4 * q] *= base * t.x;
-                            v[4 * q + 1] *= base * t.y;
-                            v[4 * q + 2] *= base * t.z;
-                            v[4 * q + 3] *= base * t.w;
+                            for (int e = 0; e < 16; ++e) {
+                                const float ago = ago0 + (rev ? (float)e : -(float)e);
+                                float x;
+                                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(ago * l2));
+                                v[hb * 16 + e] = ago >= 0.f ? v[hb * 16 + e] * x : 0.f;
+                            }
+                        } else {
+                            const float base = pw[rev ? j0 - i : i - j0 - 15];
+#pragma unroll
+                            for (int e = 0; e < 16; e += 2) {
+                                float a = g[e], b = g[e + 1];
+                                mul2(a, b, base, base);
+                                mul2(v[hb * 16 + e], v[hb * 16 + e + 1], a, b);
+                            }
                         }
                     }
 #pragma unroll
@@ -307,6 +373,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             }
             tmem_st_wait();
             tc_fence_before();
+            if (i == 127) LA_TL(it, 8);
             mbar_arrive_warp(&p_ready);
         }
     } else if (warp >= 8 && warp < 12) {
@@ -343,25 +410,30 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                 if (!ok) break;
                 tc_fence_after();
             }
+            if (d == 0) LA_TL(k, 9);
             if (have) {
 #pragma unroll 1
-                for (int c16 = 0; c16 < DZ / 16; ++c16) {
-                    float v[16];
+                for (int c32 = 0; c32 < DZ / 32; ++c32) {
+                    float v[32];
                     if (k == 0) {
-                        start16(c16 * 16, v);
+                        start16(c32 * 32, v);
+                        start16(c32 * 32 + 16, v + 16);
                     } else {
-                        tmem_ld16(ts + c16 * 16, v);
-                        tmem_wait_regs<16>(v);
+                        tmem_ld32(ts + c32 * 32, v);
+                        tmem_wait_regs<32>(v);
                     }
-                    store_state_row<DX>(sbf, d, v, c16);
+                    store_state_row<DX>(sbf, d, v, 2 * c32);
+                    store_state_row<DX>(sbf, d, v + 16, 2 * c32 + 1);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) v[e] *= g;
-                    tmem_st16(ts + c16 * 16, v);
+                    for (int e = 0; e < 32; e += 2) mul2(v[e], v[e + 1], g, g);
+                    tmem_st16(ts + c32 * 32, v);
+                    tmem_st16(ts + c32 * 32 + 16, v + 16);
                 }
                 tmem_st_wait();
             }
             fence_proxy_async();
             tc_fence_before();
+            if (d == 0) LA_TL(k, 10);
             mbar_arrive_warp(&s_conv);
         }
         if (ok && ps.fin && u == p.nseg - 1) {
@@ -391,11 +463,13 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         const int wq = warp % 4, i = wq * 32 + threadIdx.x % 32;
         const uint32_t to = tm + K::T_O + ((uint32_t)(wq * 32) << 16);
         const int tiles = many ? nchunk : items;
+        int k = 0, r = 0;
         for (int t = 0; t < tiles; ++t) {
-            const int k = many ? t : t / reps, c0 = chunk0(k), valid = min(C, part.hi - c0);
-            const int hx = many ? h : h * reps + t % reps;
+            const int c0 = chunk0(k), valid = min(C, part.hi - c0);
+            const int hx = many ? h : h * reps + r;
             if (!warp_wait(&o_inter, t & 1, &abort_flag)) break;
             tc_fence_after();
+            if (i == 0) LA_TL(t, 11);
             const float g = pw[max((rev ? valid - i : i + 1) - (k == 0 ? off0 : 0), 0)];
 #pragma unroll 1
             for (int c32 = 0; c32 < DZ / 32; ++c32) {
@@ -403,29 +477,33 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                 tmem_ld32(to + c32 * 32, v);
                 tmem_wait_regs<32>(v);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] *= g;
+                for (int e = 0; e < 32; e += 2) mul2(v[e], v[e + 1], g, g);
                 tmem_st16(to + c32 * 32, v);
                 tmem_st16(to + c32 * 32 + 16, v + 16);
             }
             tmem_st_wait();
             tc_fence_before();
+            if (i == 0) LA_TL(t, 12);
             mbar_arrive_warp(&o_scaled);
             if (!warp_wait(&o_full, t & 1, &abort_flag)) break;
             tc_fence_after();
+            if (i == 0) LA_TL(t, 13);
             // staged in the x tile, which no MMA reads any more; rows past the length are zeros
             uint8_t *o = xbuf + (t % NX) * K::X_BYTES;
-            const float sc = i < valid ? p.scale : 0.f;
+            const uint32_t keep = i < valid ? ~0u : 0u;
 #pragma unroll 1
             for (int c32 = 0; c32 < DZ / 32; ++c32) {
                 float v[32];
                 tmem_ld32(to + c32 * 32, v);
                 tmem_wait_regs<32>(v);
 #pragma unroll
+                for (int e = 0; e < 32; e += 2) mul2(v[e], v[e + 1], p.scale, p.scale);
+#pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     uint32_t w[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        w[e] = i < valid ? pack_bf16x2(v[8 * q + 2 * e] * sc, v[8 * q + 2 * e + 1] * sc) : 0u;
+                        w[e] = pack_bf16x2(v[8 * q + 2 * e], v[8 * q + 2 * e + 1]) & keep;
                     *reinterpret_cast<uint4 *>(o + swz_chunk(C, i, c32 * 4 + q)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
@@ -439,13 +517,20 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             bulk_commit();
             bulk_wait_read();
             mbar_arrive_w(&x_empty[t % NX]);
+            if (i == 0) LA_TL(t, 14);
+            if (many || ++r == reps) {
+                r = 0;
+                ++k;
+            }
         }
         bulk_wait_all();
     } else if (warp >= 16) {
         // ---------------- Y^T of every y z tile; thread = (half of the tokens, lane d)
-        const int wq = warp % 4, half = (warp - 16) / 4, d = wq * 32 + threadIdx.x % 32;
+        const int wq = warp % 4, half = (warp - 16) / 4;
         const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
         const int tiles = many ? items : nchunk;
+        YtWeights w;
+        bool shorter = false;
         for (int t = 0; t < tiles; ++t) {
             const int k = many ? t / reps : t, c0 = chunk0(k), valid = min(C, part.hi - c0);
             if (!warp_wait(&yz_full[t % NY], (t / NY) & 1, &abort_flag)) break;
@@ -457,14 +542,15 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             if (t > 0 && !warp_wait(&yt_done, (t - 1) & 1, &abort_flag)) break;
             tc_fence_after();
             if (wq * 32 < DX) {
-#pragma unroll 1
-                for (int q = 0; q < 2; ++q) {
-                    const int j0 = half * 64 + q * 32;
-                    yt_block(y, d, j0, wtab[valid < C], 1.f, valid, tm + K::T_YH + lane_off + j0 / 2, tm + K::T_YL + lane_off + j0 / 2);
+                if (t == 0 || (valid < C) != shorter) {
+                    shorter = valid < C;
+                    w.set(&wtab[shorter][half * 64], 1.f);
                 }
+                yt_block(y, wq * 32, half * 64, w, valid, tm + K::T_YH + lane_off + half * 32, tm + K::T_YL + lane_off + half * 32);
                 tmem_st_wait();
             }
             tc_fence_before();
+            if (threadIdx.x == 512) LA_TL(t, 15);
             mbar_arrive_warp(&yt_ready);
         }
     }
@@ -598,13 +684,10 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
             tc_fence_after();
             if (wq * 32 < D) {
                 // what the chunk's last token has ahead of it in the segment
-                const float mul = exp2f(l2 * (rev ? c0 - part.lo : part.hi - c0 - valid));
-#pragma unroll 1
-                for (int x = 0; x < 2; ++x) {
-                    const int j0 = half * 64 + x * 32;
-                    yt_block(y, d, j0, wtab[valid < C], mul, valid, tm + T_Y + 128 * q + lane_off + j0 / 2,
-                             tm + T_Y + 128 * q + 64 + lane_off + j0 / 2);
-                }
+                YtWeights w;
+                w.set(&wtab[valid < C][half * 64], exp2f(l2 * (rev ? c0 - part.lo : part.hi - c0 - valid)));
+                yt_block(y, wq * 32, half * 64, w, valid, tm + T_Y + 128 * q + lane_off + half * 32,
+                         tm + T_Y + 128 * q + 64 + lane_off + half * 32);
                 tmem_st_wait();
             }
             tc_fence_before();
@@ -701,3 +784,9 @@ cudaError_t decay_tc_passes(const DecayParams &p, cudaStream_t s) {
 }
 
 }  // namespace la
+
+#ifdef LA_TIMELINE
+extern "C" int la_timeline_read_decay(long long *out) {
+    return cudaMemcpyFromSymbol(out, la::g_la_tl, sizeof(long long) * 64 * 16) == cudaSuccess ? 0 : 1;
+}
+#endif

@@ -474,6 +474,27 @@ __device__ __forceinline__ void tmem_st16_raw(uint32_t taddr, const uint32_t *w)
         : "memory");
 }
 
+// Warp-wide: 16 TMEM lanes (from the lane of taddr: the first or second half of the warp's 32) x 32
+// columns of raw words in the layout of 8 x 8 matrix fragments: thread t holds, of the four
+// columns 4 q .. 4 q + 3, column 4 q + t % 4 of lanes t / 4 (w[2 q]) and t / 4 + 8 (w[2 q + 1]).
+__device__ __forceinline__ void tmem_st_frag32(uint32_t taddr, const uint32_t *w) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(taddr),
+        "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
+        "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
+        : "memory");
+}
+
+// Four 8 x 8 matrices of 16-bit elements from shared memory, transposed: thread t gives the address of
+// row t % 8 of matrix t / 8 and gets, of matrix q, elements (2 (t % 4), t / 4) and (2 (t % 4) + 1, t / 4) in w[q].
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t *w) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
 // Zero two consecutive columns of this warp's 32 lanes.
 __device__ __forceinline__ void tmem_zero2(uint32_t taddr) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %1};" ::"r"(taddr), "r"(0u) : "memory");
