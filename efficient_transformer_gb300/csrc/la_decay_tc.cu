@@ -2,23 +2,25 @@
 //
 // One block walks one segment of one key/value head in chunks of C = 128 tokens.  Per chunk (X, Y, Z:
 // see la_decay.cuh; W_ij = gamma^(i-j) for j <= i, else 0):
-//   A   = X Y^T                                  [C x C]     scores
-//   P   = bf16(A o W), in TMEM                               (fp32 decay, one rounding)
-//   O   = X S_bf, then row i times gamma^(i+1), in TMEM
-//   O  += P Z                                    [C x DZ]
-//   S   = gamma^C S + (gamma^(C-1-j) y_j)^T Z    [DX x DZ]   fp32 in TMEM
+//   A  = X Y^T                                              [C x C]     scores
+//   P  = bf16(A o W)                                        (fp32 decay, one rounding)
+//   O  = P Z + bf16(gamma^(i+1) x_i) S_bf                   [C x DZ]
+//   S  = gamma^C S + (gamma^(C-1-j) y_j)^T Z                [DX x DZ]   fp32 in TMEM
 // Powers of gamma are only ever of whole distances >= 0, so no decay overflows.  The decayed Y^T is an
 // operand made from Y: it is split into two bf16 terms (hi + lo, 2^-17 relative) and both are multiplied,
 // because what it sums is a float32 output (the state); one rounding would leave 2^-9 there.
-// P and S_bf are rounded once: they only reach bf16 outputs.
+// P, S_bf and the decayed X are rounded once: they only reach bf16 outputs.
 //
-// Operands made by the CUDA cores go to TMEM (P over the scores it comes from, Y^T hi and lo), which
-// leaves the shared memory to two stages of every TMA tile.  TMEM columns: S, O, scores / P, Y^T hi | lo.
+// Operands made by the CUDA cores are read by the MMA from TMEM: P and the decayed X take the place of the
+// scores (P over columns that its thread has read, the decayed X over the rest when P is done),
+// Y^T has columns of its own.  That leaves the shared memory to the TMA tiles, the output tile and S_bf, and
+// halves the MMA's own shared-memory reads, which at 128 x 128 x 16 from shared memory would take all of its
+// bandwidth.  TMEM columns: S, O, scores / P / X, Y^T hi | lo.
 // Several heads of x share one chunk of y, z (grouped queries; S moves on after the last), or several heads
 // of y, z share one of x (their gradients; O and S sum over the heads).
 //
-// Warps: 0 TMA, 1 MMA of scores and P Z, 2 MMA of X S_bf and the state, 4-7 P, 8-11 S -> S_bf and the decay of S, 12-15 O's row powers and the output,
-// 16-23 Y^T (and the zeros past a sequence's length).
+// Warps: 0 TMA, 1 MMA of scores and O, 2 MMA of S, 4-7 P, 8-11 S -> S_bf and the decay of S, 12-15 the decayed X
+// and the output rows, 16-19 Y^T (and the zeros past a sequence's length).
 //
 // The reverse passes (gradients of k and v) take the same steps with j >= i and gamma^(j-i), chunks from the
 // last to the first.
@@ -29,7 +31,17 @@ namespace la {
 namespace {
 
 constexpr int C = kDecayTcChunk;
-constexpr int kMainThreads = 768, kYtThreads = 256;
+constexpr int kMainThreads = 640;
+
+// Bounded warp-uniform wait.  What follows a wait that does not end at once is out of line: the kernels have some
+// twenty waits, and their code has to stay in the instruction caches that all roles share.
+__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    return (*abort == 0) && mbar_wait(bar, parity, abort);
+}
+__device__ __forceinline__ bool await(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, wait_slow(bar, parity, abort));
+}
 
 struct PassMaps {
     CUtensorMap m[3][4];   // per pass: x, y, z, out
@@ -37,15 +49,13 @@ struct PassMaps {
 
 template <int DX, int DZ>
 struct MainCfg {
-    static constexpr int X_BYTES = C * (DX > DZ ? DX : DZ) * 2;   // also stages the output tile
-    static constexpr int Y_BYTES = C * DX * 2, Z_BYTES = C * DZ * 2, YZ_BYTES = Y_BYTES + Z_BYTES;
+    static constexpr int X_BYTES = C * DX * 2, Y_BYTES = C * DX * 2, Z_BYTES = C * DZ * 2, O_BYTES = C * DZ * 2;
     static constexpr int S_BYTES = DX * DZ * 2;
-    static constexpr int BUDGET = kSmemLimit - 1024 - 2048;   // alignment; barriers and tables
-    static constexpr int NX = (BUDGET - S_BYTES) / (2 * (X_BYTES + YZ_BYTES)) >= 2 ? 4 : 2;
-    static constexpr int NY_FIT = (BUDGET - S_BYTES - NX * X_BYTES) / YZ_BYTES;
-    static constexpr int NY = NY_FIT > 4 ? 4 : NY_FIT;
-    static constexpr int SMEM = NX * X_BYTES + NY * YZ_BYTES + S_BYTES + 1024;
-    static_assert(NY >= 2, "two stages");
+    // stages of each: y goes first (scores and Y^T have it read early in the chunk), z last
+    static constexpr int NX = DX == 64 ? 4 : 2, NY = DX == 64 || DZ == 64 ? 2 : 1, NZ = DZ == 64 ? 4 : 2;
+    static constexpr int NO = DX == 64 && DZ == 64 ? 2 : 1;
+    static constexpr int SMEM = NX * X_BYTES + NY * Y_BYTES + NZ * Z_BYTES + NO * O_BYTES + S_BYTES + 1024;
+    static_assert(SMEM + 2048 <= kSmemLimit, "tiles, barriers and tables");
     static constexpr int T_S = 0, T_O = 128, T_A = 256, T_YH = 384, T_YL = 448;
 };
 
@@ -72,15 +82,25 @@ __device__ __forceinline__ void mul2(float &x, float &y, float a, float b) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
 }
 
+__device__ __forceinline__ void fma2(float &x, float &y, float a, float b, float c) {   // x = a c + x, y = b c + y
+    unsigned long long p, q, r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(q) : "f"(a), "f"(b));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(c));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(p) : "l"(q), "l"(r));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
+}
+
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t u) { return *reinterpret_cast<__nv_bfloat162 *>(&u); }
 __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 h) { return *reinterpret_cast<uint32_t *>(&h); }
 
-// The decays w of 64 tokens (8 groups of 8) of which a thread meets 2 in each group, as two bf16 terms.
+// The decays w of a chunk's tokens, 16 groups of 8 of which a thread meets 2 in each group, as two bf16
+// terms.
 struct YtWeights {
-    uint32_t hi[8], lo[8];
+    uint32_t hi[16], lo[16];
     __device__ __forceinline__ void set(const float *w, float mul) {
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
+        for (int g = 0; g < 16; ++g) {
             const float a = w[8 * g + 2 * (threadIdx.x % 4)] * mul, b = w[8 * g + 2 * (threadIdx.x % 4) + 1] * mul;
             hi[g] = pack_bf16x2(a, b);
             const float2 f = unpack_bf16x2(hi[g]);
@@ -89,40 +109,35 @@ struct YtWeights {
     }
 };
 
-// Decayed Y^T of one tile for the warp's 32 lanes d and the 64 tokens from j0: y w as two bf16 terms, into
-// 32 columns each at th and tl.  With w = wh + wl (bf16 each), hi = bf16(y wh), the remainder y wh - hi is exact in
+// Decayed Y^T of one tile for the warp's 32 lanes d from d0: y w as two bf16 terms, into 64 columns each at
+// th and tl.  With w = wh + wl (bf16 each), hi = bf16(y wh), the remainder y wh - hi is exact in
 // bf16 (one fused multiply-add) and lo = bf16(remainder + y wl): three packed operations a pair, 2^-17 relative in
 // all.  The tile's 8 x 8 blocks come transposed out of shared memory in the layout of the store.
-// Tokens at or past `valid` count as zeros whatever they hold.
-__device__ __forceinline__ void yt_block(const uint8_t *y, int d0, int j0, const YtWeights &w, int valid, uint32_t th,
-                                         uint32_t tl) {
+__device__ __forceinline__ void yt_tile(const uint8_t *y, int d0, const YtWeights &w, uint32_t th, uint32_t tl) {
     const int t = threadIdx.x % 32;
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {   // lanes d0 + 16 half ..
-        const uint32_t addr = smem_u32(y) + swz_chunk(C, j0 + 8 * (t / 16) + t % 8, (d0 + 16 * half) / 8 + ((t / 8) & 1));
-        uint32_t v[16], hi[16], lo[16];
+        const uint32_t addr = smem_u32(y) + swz_chunk(C, 8 * (t / 16) + t % 8, (d0 + 16 * half) / 8 + ((t / 8) & 1));
 #pragma unroll
-        for (int q = 0; q < 4; ++q) ldmatrix_x4_trans(addr + q * 16 * 128, v + 4 * q);
+        for (int jh = 0; jh < 2; ++jh) {     // tokens 64 jh ..
+            uint32_t v[16], hi[16], lo[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int g = i / 2;   // group of 8 tokens
-            uint32_t u = v[i];
-            if (valid < C) {
-                const int j = j0 + 8 * g + 2 * (t % 4);
-                u = j + 1 < valid ? u : j < valid ? u & 0xffffu : 0u;
+            for (int q = 0; q < 4; ++q) ldmatrix_x4_trans(addr + (jh * 64 + q * 16) * 128, v + 4 * q);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int g = jh * 8 + i / 2;   // group of 8 tokens
+                const __nv_bfloat162 u = as_bf162(v[i]), wh = as_bf162(w.hi[g]), h = __hmul2(u, wh);
+                hi[i] = as_u32(h);
+                lo[i] = as_u32(__hfma2(u, as_bf162(w.lo[g]), __hfma2(u, wh, __hneg2(h))));
             }
-            const __nv_bfloat162 wh = as_bf162(w.hi[g]), h = __hmul2(as_bf162(u), wh);
-            const __nv_bfloat162 r = __hfma2(as_bf162(u), wh, __hneg2(h));
-            hi[i] = as_u32(h);
-            lo[i] = as_u32(__hfma2(as_bf162(u), as_bf162(w.lo[g]), r));
+            tmem_st_frag32(th + ((uint32_t)(16 * half) << 16) + jh * 32, hi);
+            tmem_st_frag32(tl + ((uint32_t)(16 * half) << 16) + jh * 32, lo);
         }
-        tmem_st_frag32(th + ((uint32_t)(16 * half) << 16), hi);
-        tmem_st_frag32(tl + ((uint32_t)(16 * half) << 16), lo);
     }
 }
 
-// Zero rows [valid, C) of a C x W tile (what lies past a sequence's length must not meet the MMA, where 0
-// times a non-finite value is not 0); nth threads, this one being i.
+// Zero rows [valid, C) of a C x W tile (what lies past a sequence's length must not meet an MMA or a weight of
+// 0, where 0 times a non-finite value is not 0); nth threads, this one being i.
 template <int W>
 __device__ __forceinline__ void zero_rows(uint8_t *tile, int valid, int i, int nth) {
     for (int idx = i; idx < (C - valid) * (W / 8); idx += nth)
@@ -134,22 +149,23 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                                                               const __grid_constant__ DecayParams p, int pass0,
                                                               int npass) {
     using K = MainCfg<DX, DZ>;
-    constexpr int NX = K::NX, NY = K::NY;
+    constexpr int NX = K::NX, NY = K::NY, NZ = K::NZ;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t x_full[NX], x_empty[NX], yz_full[NY], yz_empty[NY];
-    __shared__ uint64_t sc_full, p_ready, o_inter, o_scaled, o_full, o_free, s_full, s_conv, yt_ready, yt_done, fin[2];
+    __shared__ uint64_t x_full[NX], x_empty[NX], y_full[NY], y_empty[NY], z_full[NZ], z_empty[NZ];
+    __shared__ uint64_t sc_full, p_ready, p_first, xd_ready, o_full, o_free, s_full, s_conv, yt_ready, yt_done, zeroed, fin[2];
     __shared__ __align__(16) float pw[C + 4], wtab[2][C];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
     uint8_t *xbuf = align1024(smem_raw);
-    uint8_t *yzbuf = xbuf + NX * K::X_BYTES;
-    uint8_t *sbf = yzbuf + NY * K::YZ_BYTES;
+    uint8_t *ybuf = xbuf + NX * K::X_BYTES;
+    uint8_t *zbuf = ybuf + NY * K::Y_BYTES;
+    uint8_t *obuf = zbuf + NZ * K::Z_BYTES;
+    uint8_t *sbf = obuf + K::NO * K::O_BYTES;
 
     pdl_wait();
     const int warp = threadIdx.x / 32;
     const int pi = pass0 + blockIdx.x % npass, rest = blockIdx.x / npass;
     const DecayPass &ps = p.pass[pi];
-    const CUtensorMap *mx = &maps.m[pi][0], *my = &maps.m[pi][1], *mz = &maps.m[pi][2], *mo = &maps.m[pi][3];
     const int u = rest % p.nseg, bg = rest / p.nseg, b = bg / p.Hkv, h = bg % p.Hkv;
     const int n = decay_tokens(p.lengths, b, p.N), rev = ps.rev, many = ps.many_yz, reps = p.n_rep;
     const Part part = part_of(n, p.N, u, p.nseg, p.seg_len, rev);
@@ -164,22 +180,27 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         abort_flag = 0;
         for (int s = 0; s < NX; ++s) {
             mbar_init(&x_full[s], 1);
-            mbar_init(&x_empty[s], 4);
+            mbar_init(&x_empty[s], 1 + 4);
         }
         for (int s = 0; s < NY; ++s) {
-            mbar_init(&yz_full[s], 1);
-            mbar_init(&yz_empty[s], 2);
+            mbar_init(&y_full[s], 1);
+            mbar_init(&y_empty[s], 1 + 4);
+        }
+        for (int s = 0; s < NZ; ++s) {
+            mbar_init(&z_full[s], 1);
+            mbar_init(&z_empty[s], 2);
         }
         mbar_init(&sc_full, 1);
         mbar_init(&p_ready, 128);
-        mbar_init(&o_inter, 1);
-        mbar_init(&o_scaled, 128);
+        mbar_init(&p_first, 128);
+        mbar_init(&xd_ready, 128);
         mbar_init(&o_full, 1);
         mbar_init(&o_free, 128);
-        mbar_init(&s_full, 1);
+        mbar_init(&s_full, 2);
         mbar_init(&s_conv, 128);
-        mbar_init(&yt_ready, kYtThreads);
+        mbar_init(&yt_ready, 128);
         mbar_init(&yt_done, 1);
+        mbar_init(&zeroed, 128);
         mbar_init(&fin[0], 1);
         mbar_init(&fin[1], 1);
         fence_barrier_init();
@@ -200,137 +221,165 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
     const uint32_t tm = tmem_base;
     const int items = nchunk * reps;
 
-    if (warp == 0) {
-        // ---------------- TMA producer: x tiles and y, z tiles in the order of their first use
-        int nx = 0, ny = 0;
-        bool ok = true;
-        for (int k = 0; ok && k < nchunk; ++k) {
-            const int c0 = chunk0(k);
-            for (int r = 0; ok && r < reps; ++r) {
-                const int hq = h * reps + r;
-                if (r == 0 || many) {
-                    const int s = ny % NY;
-                    if (ny >= NY && !warp_wait(&yz_empty[s], (ny / NY - 1) & 1, &abort_flag)) { ok = false; break; }
-                    uint8_t *y = yzbuf + s * K::YZ_BYTES, *z = y + K::Y_BYTES;
-                    const int hyz = many ? hq : h;
-                    mbar_arrive_expect_tx_w(&yz_full[s], K::YZ_BYTES);
-                    for (int blk = 0; blk < DX / 64; ++blk) tma_load_4d_w(y + blk * C * 128, my, &yz_full[s], blk * 64, c0, hyz, b);
-                    for (int blk = 0; blk < DZ / 64; ++blk) tma_load_4d_w(z + blk * C * 128, mz, &yz_full[s], blk * 64, c0, hyz, b);
-                    ++ny;
-                }
-                if (r == 0 || !many) {
-                    const int s = nx % NX;
-                    if (nx >= NX && !warp_wait(&x_empty[s], (nx / NX - 1) & 1, &abort_flag)) { ok = false; break; }
-                    uint8_t *x = xbuf + s * K::X_BYTES;
-                    mbar_arrive_expect_tx_w(&x_full[s], C * DX * 2);
-                    for (int blk = 0; blk < DX / 64; ++blk)
-                        tma_load_4d_w(x + blk * C * 128, mx, &x_full[s], blk * 64, c0, many ? h : hq, b);
-                    ++nx;
-                }
-            }
-        }
-        for (int i = nx > NX ? nx - NX : 0; i < nx; ++i) warp_drain(&x_full[i % NX], (i / NX) & 1);
-        for (int i = ny > NY ? ny - NY : 0; i < ny; ++i) warp_drain(&yz_full[i % NY], (i / NY) & 1);
-    } else if (warp == 1) {
-        // ---------------- scores and P Z
-        constexpr uint32_t idA = idesc_bf16(128, C, false, false);
-        constexpr uint32_t idO = idesc_bf16(128, DZ, false, true);
-        const uint32_t tO = tm + K::T_O, tA = tm + K::T_A;
-        int ix = 0, iy = 0, ot = 0, k = 0, r = 0;   // x tile, y z tile, output tile, chunk, head
-        for (int it = 0; it < items; ++it) {
-            const bool first = r == 0, last = r == reps - 1;
-            if ((first || !many) && !warp_wait(&x_full[ix % NX], (ix / NX) & 1, &abort_flag)) break;
-            if ((first || many) && !warp_wait(&yz_full[iy % NY], (iy / NY) & 1, &abort_flag)) break;
-            const uint32_t x = smem_u32(xbuf + (ix % NX) * K::X_BYTES);
-            const uint32_t y = smem_u32(yzbuf + (iy % NY) * K::YZ_BYTES), z = y + K::Y_BYTES;
-            tc_fence_after();
-            LA_TL(it, 0);
-            // (P of the item before has been read: this warp's MMAs run in the order of their issue)
+    if (warp < 4) {
+        if (warp == 0) {
+            // ---------------- TMA producer.  y waits for the scores before it where it has one stage, so x and z go first
+            const CUtensorMap *mx = &maps.m[pi][0], *my = &maps.m[pi][1], *mz = &maps.m[pi][2];
+            int nx = 0, nyz = 0, nz = 0;   // issued (z is one ahead of y when a wait for y gives up)
+            bool ok = true;
+            for (int k = 0; ok && k < nchunk; ++k) {
+                const int c0 = chunk0(k);
+                for (int r = 0; ok && r < reps; ++r) {
+                    const int hq = h * reps + r;
+                    if (r == 0 || !many) {
+                        const int s = nx % NX;
+                        if (nx >= NX && !await(&x_empty[s], (nx / NX - 1) & 1, &abort_flag)) { ok = false; break; }
+                        uint8_t *x = xbuf + s * K::X_BYTES;
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(&x_full[s], K::X_BYTES);
 #pragma unroll
-            for (int kk = 0; kk < DX / 16; ++kk) mma_bf16_w(tA, desc_kmajor(x, C, 0, kk), desc_kmajor(y, C, 0, kk), idA, kk > 0);
-            mma_commit_w(&sc_full);
-            LA_TL(it, 1);
-            if ((first || !many) && !warp_wait(&o_scaled, ot & 1, &abort_flag)) break;
-            LA_TL(it, 5);
-            // rows past a sequence's length are zeroed by the Y^T warps before P Z may read them (o_scaled says
-            // that every earlier Y^T is over)
-            if (p.lengths && first && k == nchunk - 1 && vlast < C && !warp_wait(&yt_ready, k & 1, &abort_flag)) break;
-            if (!warp_wait(&p_ready, it & 1, &abort_flag)) break;
-            LA_TL(it, 4);
-            tc_fence_after();
+                            for (int blk = 0; blk < DX / 64; ++blk)
+                                tma_load_4d(x + blk * C * 128, mx, &x_full[s], blk * 64, c0, many ? h : hq, b);
+                        }
+                        __syncwarp();
+                        ++nx;
+                    }
+                    if (r == 0 || many) {
+                        const int hyz = many ? hq : h, sz = nyz % NZ, sy = nyz % NY;
+                        if (nyz >= NZ && !await(&z_empty[sz], (nyz / NZ - 1) & 1, &abort_flag)) { ok = false; break; }
+                        uint8_t *z = zbuf + sz * K::Z_BYTES, *y = ybuf + sy * K::Y_BYTES;
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(&z_full[sz], K::Z_BYTES);
 #pragma unroll
-            for (int kk = 0; kk < C / 16; ++kk) mma_bf16_ta_w(tO, tA + kk * 8, desc_mnmajor(z, C, 0, kk), idO, 1u);
-            if (last || !many) {
-                mma_commit_w(&o_full);
-                ++ot;
-                ++ix;
+                            for (int blk = 0; blk < DZ / 64; ++blk) tma_load_4d(z + blk * C * 128, mz, &z_full[sz], blk * 64, c0, hyz, b);
+                        }
+                        __syncwarp();
+                        ++nz;
+                        if (nyz >= NY && !await(&y_empty[sy], (nyz / NY - 1) & 1, &abort_flag)) { ok = false; break; }
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(&y_full[sy], K::Y_BYTES);
+#pragma unroll
+                            for (int blk = 0; blk < DX / 64; ++blk) tma_load_4d(y + blk * C * 128, my, &y_full[sy], blk * 64, c0, hyz, b);
+                        }
+                        __syncwarp();
+                        ++nyz;
+                    }
+                }
             }
-            if (last || many) {
-                mma_commit_w(&yz_empty[iy % NY]);
-                ++iy;
-            }
-            LA_TL(it, 6);
-            if (++r == reps) {
-                r = 0;
-                ++k;
-            }
-        }
-        mma_commit_w(&fin[0]);
-        warp_drain(&fin[0], 0);
-    } else if (warp == 2) {
-        // ---------------- X S_bf, once for each output tile, and S += Y^T Z, once for each y z tile (grouped queries:
-        // after the chunk's last X S_bf)
-        constexpr uint32_t idO = idesc_bf16(128, DZ, false, true);
-        const uint32_t sb = smem_u32(sbf), tS = tm + K::T_S, tO = tm + K::T_O;
-        const uint32_t tYh = tm + K::T_YH, tYl = tm + K::T_YL;
-        int ix = 0, iy = 0, k = 0, r = 0;
-        for (int it = 0; it < items; ++it) {
-            const bool first = r == 0, last = r == reps - 1;
-            if (first || !many) {
-                if (!warp_wait(&x_full[ix % NX], (ix / NX) & 1, &abort_flag)) break;
-                if (first && !warp_wait(&s_conv, k & 1, &abort_flag)) break;
-                if (ix > 0 && !warp_wait(&o_free, (ix - 1) & 1, &abort_flag)) break;
-                LA_TL(it, 2);
-                tc_fence_after();
+            for (int i = nx > NX ? nx - NX : 0; i < nx; ++i) warp_drain(&x_full[i % NX], (i / NX) & 1);
+            for (int i = nyz > NY ? nyz - NY : 0; i < nyz; ++i) warp_drain(&y_full[i % NY], (i / NY) & 1);
+            for (int i = nz > NZ ? nz - NZ : 0; i < nz; ++i) warp_drain(&z_full[i % NZ], (i / NZ) & 1);
+        } else if (warp == 1) {
+            // ---------------- scores, then O = P Z (+ the decayed X times S_bf, once for each output tile).  This warp's
+            // MMAs run in the order of their issue, so the next scores cannot overtake P and X
+            constexpr uint32_t idA = idesc_bf16(128, C, false, false);
+            constexpr uint32_t idO = idesc_bf16(128, DZ, false, true);
+            const uint32_t tO = tm + K::T_O, tA = tm + K::T_A, sb = smem_u32(sbf);
+            int ix = 0, iy = 0, ot = 0, k = 0, r = 0;   // x tile, y z tile, output tile, chunk, head
+            for (int it = 0; it < items; ++it) {
+                const bool first = r == 0, last = r == reps - 1;
+                const bool opens = first || !many, ends = last || !many;   // an output tile
+                if (opens && !await(&x_full[ix % NX], (ix / NX) & 1, &abort_flag)) break;
+                if ((first || many) && !await(&y_full[iy % NY], (iy / NY) & 1, &abort_flag)) break;
                 const uint32_t x = smem_u32(xbuf + (ix % NX) * K::X_BYTES);
-#pragma unroll
-                for (int kk = 0; kk < DX / 16; ++kk)
-                    mma_bf16_w(tO, desc_kmajor(x, C, 0, kk), desc_mnmajor(sb, DX, 0, kk), idO, kk > 0);
-                mma_commit_w(&o_inter);
-                ++ix;
-            }
-            if (last || many) {
-                if (!warp_wait(&yt_ready, iy & 1, &abort_flag)) break;
-                LA_TL(it, 3);
+                const uint32_t y = smem_u32(ybuf + (iy % NY) * K::Y_BYTES), z = smem_u32(zbuf + (iy % NZ) * K::Z_BYTES);
+                // a tile with rows past the sequence's length (its last): those are zeroed first
+                if (p.lengths && first && k == nchunk - 1 && vlast < C && !await(&zeroed, 0, &abort_flag)) break;
                 tc_fence_after();
-                const uint32_t z = smem_u32(yzbuf + (iy % NY) * K::YZ_BYTES) + K::Y_BYTES;
-#pragma unroll
-                for (int kk = 0; kk < C / 16; ++kk) {
-                    mma_bf16_ta_w(tS, tYh + kk * 8, desc_mnmajor(z, C, 0, kk), idO, 1u);
-                    mma_bf16_ta_w(tS, tYl + kk * 8, desc_mnmajor(z, C, 0, kk), idO, 1u);
+                LA_TL(it, 0);
+                if (elect_one()) {
+                    mma_ss_kk<DX / 16>(tA, desc_kmajor(x, C, 0, 0), desc_kmajor(y, C, 0, 0), idA);
+                    mma_commit(&sc_full);
+                    if (ends) mma_commit(&x_empty[ix % NX]);
+                    if (last || many) mma_commit(&y_empty[iy % NY]);
                 }
-                mma_commit_w(&yt_done);
-                if (last) mma_commit_w(&s_full);
-                mma_commit_w(&yz_empty[iy % NY]);
-                ++iy;
+                __syncwarp();
+                LA_TL(it, 1);
+                if (opens && ot > 0 && !await(&o_free, (ot - 1) & 1, &abort_flag)) break;
+                LA_TL(it, 2);
+                if ((first || many) && !await(&z_full[iy % NZ], (iy / NZ) & 1, &abort_flag)) break;
+                if (!await(&p_ready, it & 1, &abort_flag)) break;
+                LA_TL(it, 4);
+                tc_fence_after();
+                if (elect_one()) mma_ts_mn<C / 16>(tO, tA, desc_mnmajor(z, C, 0, 0), idO, opens ? 0u : 1u);
+                __syncwarp();
+                if (opens) {
+                    if (!await(&xd_ready, ot & 1, &abort_flag)) break;
+                    if (first && !await(&s_conv, k & 1, &abort_flag)) break;
+                    LA_TL(it, 5);
+                    tc_fence_after();
+                    if (elect_one()) mma_ts_mn<DX / 16>(tO, tA + 64, desc_mnmajor(sb, DX, 0, 0), idO, 1u);
+                    __syncwarp();
+                }
+                if (elect_one()) {
+                    if (ends) mma_commit(&o_full);
+                    if (many ? first : last) mma_commit(&s_full);   // the chunk's last reader of S_bf
+                    if (last || many) mma_commit(&z_empty[iy % NZ]);
+                }
+                __syncwarp();
+                if (ends) {
+                    ++ot;
+                    ++ix;
+                }
+                if (last || many) ++iy;
+                LA_TL(it, 6);
+                if (++r == reps) {
+                    r = 0;
+                    ++k;
+                }
             }
-            if (++r == reps) {
-                r = 0;
-                ++k;
+            if (elect_one()) mma_commit(&fin[0]);
+            __syncwarp();
+            warp_drain(&fin[0], 0);
+        } else if (warp == 2) {
+            // ---------------- S += Y^T Z, once for each y z tile
+            constexpr uint32_t idS = idesc_bf16(128, DZ, false, true);
+            const uint32_t tS = tm + K::T_S, tYh = tm + K::T_YH, tYl = tm + K::T_YL;
+            const int tiles = many ? items : nchunk, per = many ? reps : 1;
+            int k = 0, r = 0;
+            for (int t = 0; t < tiles; ++t) {
+                if (r == 0 && !await(&s_conv, k & 1, &abort_flag)) break;
+                if (!await(&z_full[t % NZ], (t / NZ) & 1, &abort_flag)) break;
+                if (!await(&yt_ready, t & 1, &abort_flag)) break;
+                LA_TL(t, 3);
+                tc_fence_after();
+                const uint32_t z = smem_u32(zbuf + (t % NZ) * K::Z_BYTES);
+                const bool ends = ++r == per;
+                if (elect_one()) {
+                    mma_ts_mn<C / 16>(tS, tYh, desc_mnmajor(z, C, 0, 0), idS, 1u);
+                    mma_ts_mn<C / 16>(tS, tYl, desc_mnmajor(z, C, 0, 0), idS, 1u);
+                    mma_commit(&yt_done);
+                    mma_commit(&z_empty[t % NZ]);
+                    if (ends) mma_commit(&s_full);
+                }
+                __syncwarp();
+                if (ends) {
+                    r = 0;
+                    ++k;
+                }
             }
+            if (elect_one()) mma_commit(&fin[1]);
+            __syncwarp();
+            warp_drain(&fin[1], 0);
         }
-        mma_commit_w(&fin[1]);
-        warp_drain(&fin[1], 0);
-    } else if (warp >= 4 && warp < 8) {
-        // ---------------- P = bf16(A o W), thread = row i, 16 columns at a time.  Away from the diagonal
-        // gamma^|i - j| = gamma^(distance to the block's near end) gamma^(distance in the block), the latter in registers
-        const int wq = warp % 4, i = wq * 32 + threadIdx.x % 32;
+    } else if (warp < 8) {
+        // ---------------- P = bf16(scale A o W), thread = row i, 32 columns at a time.  Away from the diagonal
+        // gamma^|i - j| = gamma^(distance to the near end of a block of 16) gamma^(distance in the block); on it the blocks
+        // of 16 have the lower (reverse: upper) triangle of one pattern, or are such a full block, or nothing.  Both
+        // patterns stay in registers, with `scale`
+        const int wq = warp % 4, lane = threadIdx.x % 32, i = wq * 32 + lane;
         const uint32_t ta = tm + K::T_A + ((uint32_t)(wq * 32) << 16);
-        float g[16];
+        float g[16], tri[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) g[e] = pw[rev ? e : 15 - e];
+        for (int e = 0; e < 16; ++e) {
+            const int ago = rev ? e - lane % 16 : lane % 16 - e;
+            g[e] = p.scale * pw[rev ? e : 15 - e];
+            tri[e] = ago >= 0 ? p.scale * pw[max(ago, 0)] : 0.f;
+        }
+        const bool low = lane < 16;
+        int r = 0;
         for (int it = 0; it < items; ++it) {
-            if (!warp_wait(&sc_full, it & 1, &abort_flag)) break;
+            if (!await(&sc_full, it & 1, &abort_flag)) break;
             tc_fence_after();
             if (i == 127) LA_TL(it, 7);
 #pragma unroll 1
@@ -346,17 +395,19 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
 #pragma unroll
                     for (int hb = 0; hb < 2; ++hb) {
                         const int j0 = cb * 32 + hb * 16;
-                        if (cb == wq) {   // the diagonal: tokens on this side of it
-                            const float ago0 = (float)(rev ? j0 - i : i - j0);
+                        const int near = rev ? j0 - i : i - j0 - 15;   // distance to the block's near end
+                        if (cb == wq) {
+                            const float full = (rev ? hb == 1 && low : hb == 0 && !low) ? pw[max(near, 0)] : 0.f;
+                            const float half = low == (hb == 0) ? 1.f : 0.f;
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const float ago = ago0 + (rev ? (float)e : -(float)e);
-                                float x;
-                                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(ago * l2));
-                                v[hb * 16 + e] = ago >= 0.f ? v[hb * 16 + e] * x : 0.f;
+                            for (int e = 0; e < 16; e += 2) {
+                                float a = g[e], b = g[e + 1];
+                                mul2(a, b, full, full);
+                                fma2(a, b, tri[e], tri[e + 1], half);
+                                mul2(v[hb * 16 + e], v[hb * 16 + e + 1], a, b);
                             }
                         } else {
-                            const float base = pw[rev ? j0 - i : i - j0 - 15];
+                            const float base = pw[near];
 #pragma unroll
                             for (int e = 0; e < 16; e += 2) {
                                 float a = g[e], b = g[e + 1];
@@ -368,15 +419,17 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
 #pragma unroll
                     for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
                 }
-                // over the scores of this row that have been read (columns 16 cb .. 16 cb + 15 <= 32 cb + 31)
+                // over columns that this thread has read (16 cb .. 16 cb + 15 <= 32 cb + 31)
                 tmem_st16_raw(ta + cb * 16, w);
             }
             tmem_st_wait();
             tc_fence_before();
             if (i == 127) LA_TL(it, 8);
             mbar_arrive_warp(&p_ready);
+            if (r == 0 || !many) mbar_arrive_warp(&p_first);
+            if (++r == reps) r = 0;
         }
-    } else if (warp >= 8 && warp < 12) {
+    } else if (warp < 12) {
         // ---------------- S: the operand S_bf of the state before the chunk, and its decay; thread = row d
         const int wq = warp % 4, d = wq * 32 + threadIdx.x % 32;
         const uint32_t ts = tm + K::T_S + ((uint32_t)(wq * 32) << 16);
@@ -401,35 +454,44 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                 for (int e = 0; e < 16; ++e) v[e] = fmaf(fw[e * se], g, v[e]);
             }
         };
+        // the powers of gamma that S takes before each chunk's Y^T Z; first the chunk that starts from memory
         bool ok = true;
+        const float g0 = nchunk > 0 ? pw[min(C, part.hi - chunk0(0)) - off0] : 1.f;
+        const float g = pw[C], gl = pw[rev ? C : vlast];
+        if (have) {
+#pragma unroll 1
+            for (int c16 = 0; c16 < DZ / 16; ++c16) {
+                float v[16];
+                start16(c16 * 16, v);
+                store_state_row<DX>(sbf, d, v, c16);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] *= g0;
+                tmem_st16(ts + c16 * 16, v);
+            }
+            tmem_st_wait();
+        }
         for (int k = 0; k < nchunk; ++k) {
-            const int valid = min(C, part.hi - chunk0(k));
-            const float g = pw[valid - (k == 0 ? off0 : 0)];
             if (k > 0) {
-                ok = warp_wait(&s_full, (k - 1) & 1, &abort_flag);
+                ok = await(&s_full, (k - 1) & 1, &abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-            }
-            if (d == 0) LA_TL(k, 9);
-            if (have) {
+                if (d == 0) LA_TL(k, 9);
+                const float gk = k == nchunk - 1 ? gl : g;
+                if (have) {
 #pragma unroll 1
-                for (int c32 = 0; c32 < DZ / 32; ++c32) {
-                    float v[32];
-                    if (k == 0) {
-                        start16(c32 * 32, v);
-                        start16(c32 * 32 + 16, v + 16);
-                    } else {
+                    for (int c32 = 0; c32 < DZ / 32; ++c32) {
+                        float v[32];
                         tmem_ld32(ts + c32 * 32, v);
                         tmem_wait_regs<32>(v);
-                    }
-                    store_state_row<DX>(sbf, d, v, 2 * c32);
-                    store_state_row<DX>(sbf, d, v + 16, 2 * c32 + 1);
+                        store_state_row<DX>(sbf, d, v, 2 * c32);
+                        store_state_row<DX>(sbf, d, v + 16, 2 * c32 + 1);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) mul2(v[e], v[e + 1], g, g);
-                    tmem_st16(ts + c32 * 32, v);
-                    tmem_st16(ts + c32 * 32 + 16, v + 16);
+                        for (int e = 0; e < 32; e += 2) mul2(v[e], v[e + 1], gk, gk);
+                        tmem_st16(ts + c32 * 32, v);
+                        tmem_st16(ts + c32 * 32 + 16, v + 16);
+                    }
+                    tmem_st_wait();
                 }
-                tmem_st_wait();
             }
             fence_proxy_async();
             tc_fence_before();
@@ -440,7 +502,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             // what leaves a reverse pass decays once more; with no token at all it is what came in
             const float mul = ps.fin_mul * (ps.first_off && n > 0 ? exp2f(l2 * ps.first_off) : 1.f);
             if (nchunk > 0) {
-                ok = warp_wait(&s_full, (nchunk - 1) & 1, &abort_flag);
+                ok = await(&s_full, (nchunk - 1) & 1, &abort_flag);
                 tc_fence_after();
             }
             float *f = ps.fin + (size_t)bg * E + d * sd;
@@ -448,110 +510,132 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
 #pragma unroll 1
                 for (int c16 = 0; c16 < DZ / 16; ++c16) {
                     float v[16];
-                    if (nchunk > 0) {
-                        tmem_ld16(ts + c16 * 16, v);
-                        tmem_wait_regs<16>(v);
-                    } else {
-                        start16(c16 * 16, v);
-                    }
+                    tmem_ld16(ts + c16 * 16, v);
+                    tmem_wait_regs<16>(v);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) f[(size_t)(c16 * 16 + e) * se] = v[e] * mul;
                 }
         }
-    } else if (warp >= 12 && warp < 16) {
-        // ---------------- O: row i of X S_bf times gamma^(i + 1), then the finished tile to memory; thread = row i
+    } else if (warp < 16) {
+        // ---------------- rows of x and of the output; thread = row i.  The decayed x is made in registers while P is
+        // under way and stored where the scores have been read
         const int wq = warp % 4, i = wq * 32 + threadIdx.x % 32;
-        const uint32_t to = tm + K::T_O + ((uint32_t)(wq * 32) << 16);
+        const uint32_t lane_off = (uint32_t)(wq * 32) << 16, to = tm + K::T_O + lane_off, tx = tm + K::T_A + 64 + lane_off;
         const int tiles = many ? nchunk : items;
+        const CUtensorMap *mo = &maps.m[pi][3];
         int k = 0, r = 0;
         for (int t = 0; t < tiles; ++t) {
             const int c0 = chunk0(k), valid = min(C, part.hi - c0);
-            const int hx = many ? h : h * reps + r;
-            if (!warp_wait(&o_inter, t & 1, &abort_flag)) break;
-            tc_fence_after();
-            if (i == 0) LA_TL(t, 11);
-            const float g = pw[max((rev ? valid - i : i + 1) - (k == 0 ? off0 : 0), 0)];
-#pragma unroll 1
-            for (int c32 = 0; c32 < DZ / 32; ++c32) {
-                float v[32];
-                tmem_ld32(to + c32 * 32, v);
-                tmem_wait_regs<32>(v);
+            if (!await(&x_full[t % NX], (t / NX) & 1, &abort_flag)) break;
+            {
+                // scale x gamma^(i + 1) with the factor as two bf16 terms: one rounding, that of the result
+                const float g = p.scale * pw[max((rev ? valid - i : i + 1) - (k == 0 ? off0 : 0), 0)];
+                const __nv_bfloat162 gh = as_bf162(pack_bf16x2(g, g));
+                const float gr = g - unpack_bf16x2(as_u32(gh)).x;
+                const __nv_bfloat162 gl = as_bf162(pack_bf16x2(gr, gr));
+                const uint8_t *x = xbuf + (t % NX) * K::X_BYTES;
+                uint32_t w[DX / 2];
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) mul2(v[e], v[e + 1], g, g);
-                tmem_st16(to + c32 * 32, v);
-                tmem_st16(to + c32 * 32 + 16, v + 16);
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            if (i == 0) LA_TL(t, 12);
-            mbar_arrive_warp(&o_scaled);
-            if (!warp_wait(&o_full, t & 1, &abort_flag)) break;
-            tc_fence_after();
-            if (i == 0) LA_TL(t, 13);
-            // staged in the x tile, which no MMA reads any more; rows past the length are zeros
-            uint8_t *o = xbuf + (t % NX) * K::X_BYTES;
-            const uint32_t keep = i < valid ? ~0u : 0u;
-#pragma unroll 1
-            for (int c32 = 0; c32 < DZ / 32; ++c32) {
-                float v[32];
-                tmem_ld32(to + c32 * 32, v);
-                tmem_wait_regs<32>(v);
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) mul2(v[e], v[e + 1], p.scale, p.scale);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t w[4];
+                for (int c = 0; c < DX / 8; ++c) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(x + swz_chunk(C, i, c));
+                    const uint32_t a[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        w[e] = pack_bf16x2(v[8 * q + 2 * e], v[8 * q + 2 * e + 1]) & keep;
-                    *reinterpret_cast<uint4 *>(o + swz_chunk(C, i, c32 * 4 + q)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        w[4 * c + e] = as_u32(__hfma2(as_bf162(a[e]), gh, __hmul2(as_bf162(a[e]), gl)));
                 }
+                mbar_arrive_w(&x_empty[t % NX]);
+                if (!await(&p_first, t & 1, &abort_flag)) break;
+                tc_fence_after();
+                if (i == 0) LA_TL(t, 11);
+#pragma unroll
+                for (int q = 0; q < DX / 32; ++q) tmem_st16_raw(tx + q * 16, w + 16 * q);
+                tmem_st_wait();
+            }
+            tc_fence_before();
+            if (i == 0) LA_TL(t, 12);
+            mbar_arrive_warp(&xd_ready);
+            if (!await(&o_full, t & 1, &abort_flag)) break;
+            tc_fence_after();
+            if (i == 0) LA_TL(t, 13);
+            // each warp stages and stores its own 32 rows; those past the length are zeros
+            uint8_t *o = obuf + (t % K::NO) * K::O_BYTES;
+            bulk_wait_read_but<K::NO - 1>();   // (of the elected lane)
+            __syncwarp();
+#pragma unroll 1
+            for (int c32 = 0; c32 < DZ / 32; ++c32) {
+                float v[32];
+                tmem_ld32(to + c32 * 32, v);
+                tmem_wait_regs<32>(v);
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+                if (i >= valid) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) w[e] = 0u;
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<uint4 *>(o + swz_chunk(C, i, c32 * 4 + q)) =
+                        make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
             }
             tc_fence_before();
             mbar_arrive_warp(&o_free);
+            if (i == 0) LA_TL(t, 14);
             fence_proxy_async();
             __syncwarp();
-            if (c0 + wq * 32 < p.N)
-                for (int blk = 0; blk < DZ / 64; ++blk)
-                    tma_store_4d_w(mo, o + blk * C * 128 + wq * 32 * 128, blk * 64, c0 + wq * 32, hx, b);
-            bulk_commit();
-            bulk_wait_read();
-            mbar_arrive_w(&x_empty[t % NX]);
-            if (i == 0) LA_TL(t, 14);
+            if (elect_one()) {
+                if (c0 + wq * 32 < p.N)
+#pragma unroll
+                    for (int blk = 0; blk < DZ / 64; ++blk)
+                        tma_store_4d(mo, o + blk * C * 128 + wq * 32 * 128, blk * 64, c0 + wq * 32, many ? h : h * reps + r, b);
+                bulk_commit();
+            }
+            __syncwarp();
             if (many || ++r == reps) {
                 r = 0;
                 ++k;
             }
         }
         bulk_wait_all();
-    } else if (warp >= 16) {
-        // ---------------- Y^T of every y z tile; thread = (half of the tokens, lane d)
-        const int wq = warp % 4, half = (warp - 16) / 4;
+    } else {
+        // ---------------- Y^T of every y z tile
+        const int wq = warp % 4;
         const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
         const int tiles = many ? items : nchunk;
         YtWeights w;
         bool shorter = false;
+        int k = 0, r = 0;
         for (int t = 0; t < tiles; ++t) {
-            const int k = many ? t / reps : t, c0 = chunk0(k), valid = min(C, part.hi - c0);
-            if (!warp_wait(&yz_full[t % NY], (t / NY) & 1, &abort_flag)) break;
-            uint8_t *y = yzbuf + (t % NY) * K::YZ_BYTES;
+            const int c0 = chunk0(k), valid = min(C, part.hi - c0);
+            if (!await(&y_full[t % NY], (t / NY) & 1, &abort_flag)) break;
+            uint8_t *y = ybuf + (t % NY) * K::Y_BYTES;
             if (p.lengths && valid < C) {
-                zero_rows<DZ>(y + K::Y_BYTES, valid, threadIdx.x - 512, kYtThreads);
+                if (!await(&z_full[t % NZ], (t / NZ) & 1, &abort_flag)) break;
+                zero_rows<DX>(y, valid, threadIdx.x - 512, 128);
+                zero_rows<DZ>(zbuf + (t % NZ) * K::Z_BYTES, valid, threadIdx.x - 512, 128);
                 fence_proxy_async();
+                mbar_arrive_warp(&zeroed);
+                // (the warps read one another's zeros)
+                if (!await(&zeroed, 0, &abort_flag)) break;
             }
-            if (t > 0 && !warp_wait(&yt_done, (t - 1) & 1, &abort_flag)) break;
+            if (t > 0 && !await(&yt_done, (t - 1) & 1, &abort_flag)) break;
             tc_fence_after();
             if (wq * 32 < DX) {
                 if (t == 0 || (valid < C) != shorter) {
                     shorter = valid < C;
-                    w.set(&wtab[shorter][half * 64], 1.f);
+                    w.set(wtab[shorter], 1.f);
                 }
-                yt_block(y, wq * 32, half * 64, w, valid, tm + K::T_YH + lane_off + half * 32, tm + K::T_YL + lane_off + half * 32);
+                yt_tile(y, wq * 32, w, tm + K::T_YH + lane_off, tm + K::T_YL + lane_off);
                 tmem_st_wait();
             }
+            mbar_arrive_w(&y_empty[t % NY]);
             tc_fence_before();
             if (threadIdx.x == 512) LA_TL(t, 15);
             mbar_arrive_warp(&yt_ready);
+            if (!many || ++r == reps) {
+                r = 0;
+                ++k;
+            }
         }
     }
     // rows of whole chunks past the sequence's length: zeros
@@ -574,8 +658,8 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
 // ---------------------------------------------------------------------------------------
 // The sums over single segments (see DecayStateParams).  Y^T is decayed to the segment's end at once, so S in
 // TMEM only ever accumulates; Y^T is double-buffered and made by two groups of warps in turn.
-// Warps: 0 TMA, 1 MMA, 4-11 and 12-19 Y^T of even and odd tiles (4-7 then write S).
-constexpr int kStateThreads = 640;
+// Warps: 0 TMA, 1 MMA, 4-7 and 8-11 Y^T of even and odd tiles (4-7 then write S).
+constexpr int kStateThreads = 384;
 
 struct StateMaps {
     CUtensorMap m[2][2];   // per array: y, z
@@ -594,7 +678,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
     using K = StateCfg<D, DV>;
     constexpr int NS = K::NS;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[NS], empty[NS], yt_ready[2], yt_done[2], fin;
+    __shared__ uint64_t full[NS], empty[NS], yt_ready[2], yt_done[2], zeroed[2], fin;
     __shared__ __align__(16) float wtab[2][C];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
@@ -618,8 +702,9 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
             mbar_init(&empty[s], 1);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&yt_ready[s], kYtThreads);
+            mbar_init(&yt_ready[s], 128);
             mbar_init(&yt_done[s], 1);
+            mbar_init(&zeroed[s], 128);
         }
         mbar_init(&fin, 1);
         fence_barrier_init();
@@ -642,11 +727,16 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
         int issued = 0;
         for (int it = 0; it < items; ++it) {
             const int s = it % NS, c0 = part.lo + C * (it / heads), hh = h * heads + it % heads;
-            if (it >= NS && !warp_wait(&empty[s], (it / NS - 1) & 1, &abort_flag)) break;
+            if (it >= NS && !await(&empty[s], (it / NS - 1) & 1, &abort_flag)) break;
             uint8_t *y = stage + s * K::STAGE, *z = y + K::Y_BYTES;
-            mbar_arrive_expect_tx_w(&full[s], K::STAGE);
-            for (int blk = 0; blk < D / 64; ++blk) tma_load_4d_w(y + blk * C * 128, &maps.m[a][0], &full[s], blk * 64, c0, hh, b);
-            for (int blk = 0; blk < DV / 64; ++blk) tma_load_4d_w(z + blk * C * 128, &maps.m[a][1], &full[s], blk * 64, c0, hh, b);
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&full[s], K::STAGE);
+#pragma unroll
+                for (int blk = 0; blk < D / 64; ++blk) tma_load_4d(y + blk * C * 128, &maps.m[a][0], &full[s], blk * 64, c0, hh, b);
+#pragma unroll
+                for (int blk = 0; blk < DV / 64; ++blk) tma_load_4d(z + blk * C * 128, &maps.m[a][1], &full[s], blk * 64, c0, hh, b);
+            }
+            __syncwarp();
             issued = it + 1;
         }
         for (int i = issued > NS ? issued - NS : 0; i < issued; ++i) warp_drain(&full[i % NS], (i / NS) & 1);
@@ -654,47 +744,51 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
         constexpr uint32_t id = idesc_bf16(128, DV, false, true);
         for (int it = 0; it < items; ++it) {
             const int s = it % NS, q = it % 2;
-            if (!warp_wait(&yt_ready[q], (it / 2) & 1, &abort_flag)) break;
+            if (!await(&yt_ready[q], (it / 2) & 1, &abort_flag)) break;
             tc_fence_after();
             const uint32_t z = smem_u32(stage + s * K::STAGE + K::Y_BYTES), ty = tm + T_Y + 128 * q;
-            for (int kk = 0; kk < C / 16; ++kk) {
-                mma_bf16_ta_w(tm + T_S, ty + kk * 8, desc_mnmajor(z, C, 0, kk), id, it > 0 || kk > 0);
-                mma_bf16_ta_w(tm + T_S, ty + 64 + kk * 8, desc_mnmajor(z, C, 0, kk), id, 1u);
+            if (elect_one()) {
+                mma_ts_mn<C / 16>(tm + T_S, ty, desc_mnmajor(z, C, 0, 0), id, it > 0 ? 1u : 0u);
+                mma_ts_mn<C / 16>(tm + T_S, ty + 64, desc_mnmajor(z, C, 0, 0), id, 1u);
+                mma_commit(&yt_done[q]);
+                mma_commit(&empty[s]);
             }
-            mma_commit_w(&yt_done[q]);
-            mma_commit_w(&empty[s]);
+            __syncwarp();
         }
-        mma_commit_w(&fin);
+        if (elect_one()) mma_commit(&fin);
+        __syncwarp();
         warp_drain(&fin, 0);
     } else if (warp >= 4) {
-        const int grp = (warp - 4) / 8, wq = warp % 4, half = ((warp - 4) / 4) % 2, d = wq * 32 + threadIdx.x % 32;
+        const int grp = (warp - 4) / 4, wq = warp % 4, d = wq * 32 + threadIdx.x % 32;
         const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
         bool ok = true;
         for (int it = grp; it < items; it += 2) {
             const int s = it % NS, c0 = part.lo + C * (it / heads), valid = min(C, part.hi - c0), q = it % 2;
             // the buffer's last tile first: then every earlier use of this stage is over too (a group sees
             // only every other tile, and a parity tells only neighbouring phases apart)
-            if (it >= 2 && !(ok = warp_wait(&yt_done[q], (it / 2 - 1) & 1, &abort_flag))) break;
-            if (!(ok = warp_wait(&full[s], (it / NS) & 1, &abort_flag))) break;
+            if (it >= 2 && !(ok = await(&yt_done[q], (it / 2 - 1) & 1, &abort_flag))) break;
+            if (!(ok = await(&full[s], (it / NS) & 1, &abort_flag))) break;
             uint8_t *y = stage + s * K::STAGE;
             if (p.lengths && valid < C) {
-                zero_rows<DV>(y + K::Y_BYTES, valid, (threadIdx.x - 128) % kYtThreads, kYtThreads);
+                zero_rows<D>(y, valid, threadIdx.x % 128, 128);
+                zero_rows<DV>(y + K::Y_BYTES, valid, threadIdx.x % 128, 128);
                 fence_proxy_async();
+                mbar_arrive_warp(&zeroed[grp]);
+                if (!(ok = await(&zeroed[grp], 0, &abort_flag))) break;
             }
             tc_fence_after();
             if (wq * 32 < D) {
                 // what the chunk's last token has ahead of it in the segment
                 YtWeights w;
-                w.set(&wtab[valid < C][half * 64], exp2f(l2 * (rev ? c0 - part.lo : part.hi - c0 - valid)));
-                yt_block(y, wq * 32, half * 64, w, valid, tm + T_Y + 128 * q + lane_off + half * 32,
-                         tm + T_Y + 128 * q + 64 + lane_off + half * 32);
+                w.set(wtab[valid < C], exp2f(l2 * (rev ? c0 - part.lo : part.hi - c0 - valid)));
+                yt_tile(y, wq * 32, w, tm + T_Y + 128 * q + lane_off, tm + T_Y + 128 * q + 64 + lane_off);
                 tmem_st_wait();
             }
             tc_fence_before();
             mbar_arrive_warp(&yt_ready[q]);
         }
         if (warp < 8 && wq * 32 < D) {
-            if (ok && items > 0) ok = warp_wait(&fin, 0, &abort_flag);
+            if (ok && items > 0) ok = await(&fin, 0, &abort_flag);
             tc_fence_after();
             if (ok)
 #pragma unroll 1
@@ -711,9 +805,9 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
 #pragma unroll
                     for (int e = 0; e < 4; ++e) f[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                 }
-        } else if (warp >= 12 && u == 0) {   // slot 0: the starting state
+        } else if (warp >= 8 && u == 0) {   // slot 0: the starting state
             const float *f = p.init[a] ? p.init[a] + (size_t)bg * E : nullptr;
-            for (int i = threadIdx.x - 384; i < (int)E; i += 256) slots[i] = f ? f[i] * p.init_mul[a] : 0.f;
+            for (int i = threadIdx.x - 256; i < (int)E; i += 128) slots[i] = f ? f[i] * p.init_mul[a] : 0.f;
         }
     }
     tc_fence_before();
@@ -724,8 +818,6 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
 
 // ---- launches ---------------------------------------------------------------------------
 
-Strides out_strides(int H, int N, int W) { return contiguous_strides(H, N, W); }
-
 template <int DX, int DZ>
 cudaError_t passes_d(const DecayParams &p, int pass0, int npass, cudaStream_t s) {
     PassMaps maps;
@@ -735,7 +827,7 @@ cudaError_t passes_d(const DecayParams &p, int pass0, int npass, cudaStream_t s)
         cudaError_t e = make_map_in(&maps.m[i][0], ps.x, p.B, Hx, p.N, DX, ps.sx, C);
         if (e == cudaSuccess) e = make_map_in(&maps.m[i][1], ps.y, p.B, Hyz, p.N, DX, ps.sy, C);
         if (e == cudaSuccess) e = make_map_in(&maps.m[i][2], ps.z, p.B, Hyz, p.N, DZ, ps.sz, C);
-        if (e == cudaSuccess) e = make_map_in(&maps.m[i][3], ps.out, p.B, Hx, p.N, DZ, out_strides(Hx, p.N, DZ), 32);
+        if (e == cudaSuccess) e = make_map_in(&maps.m[i][3], ps.out, p.B, Hx, p.N, DZ, contiguous_strides(Hx, p.N, DZ), 32);
         if (e != cudaSuccess) return e;
     }
     auto kern = k_decay_tc<DX, DZ>;

@@ -278,18 +278,92 @@ __device__ __forceinline__ void mma_bf16_lastuse_w(uint32_t d_tmem, uint64_t a_d
 }
 #undef LA_LANE0_MMA
 
-// The MMA with its A operand (M rows x 16 of K, bf16) in tensor memory: row m in lane m, two
-// consecutive K elements in each 32-bit column, 8 columns a K step.
-__device__ __forceinline__ void mma_bf16_ta_w(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                              uint32_t accumulate) {
+// ---- one elected thread -------------------------------------------------------------------
+// elect.sync leaves the compiler a uniform predicate: a branch on it keeps descriptors and addresses in
+// uniform registers (code size of 16 MMAs in a loop: 1.8 KB, against 4.6 KB with the lane-0 predicate of the *_w
+// forms, whose code is more than a third of a kernel's issue slots next to busy warps).  The
+// elected lane is the same each time, so a commit covers its MMAs.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z, int w) {
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\t.reg .u32 l;\n\t"
-        "mov.u32 l, %%laneid;\n\tsetp.eq.u32 e, l, 0;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+        "[%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
         : "memory");
 }
+
+// Store one box from shared memory (bulk-group completion).
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, const void *src, int x, int y, int z, int w) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
+// Wait until at most N committed bulk groups of this thread are still reading shared memory.
+template <int N> __device__ __forceinline__ void bulk_wait_read_but() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
+// Whole products by one thread: KSTEPS MMAs of 16 of K each, descriptors stepped by constants (units of 16 bytes).
+// K-major tile of 128 rows: 2 a K step, 1024 from one 64-column block to the next (4 K steps); MN-major
+// tile (rows = K): 128 a K step, whatever its height.
+
+// A in tensor memory: row m in lane m, two consecutive K elements in each 32-bit column, 8 columns a K step.
+#define LA_TS_STEP(i, pred)                                                      \
+    "add.u32 ta, %1, (" #i " * 8);\n\tadd.s64 db, %2, (" #i " * 128);\n\t"            \
+    "tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %3, " pred ";\n\t"
+// D (+)= A B, A in TMEM at a_tmem (KSTEPS x 8 columns), B an MN-major tile.
+template <int KSTEPS>
+__device__ __forceinline__ void mma_ts_mn(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    static_assert(KSTEPS == 4 || KSTEPS == 8, "K steps");
+    if constexpr (KSTEPS == 8)
+        asm volatile(
+            "{\n\t.reg .pred p, t;\n\t.reg .b32 ta;\n\t.reg .b64 db;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t"
+            LA_TS_STEP(0, "p") LA_TS_STEP(1, "t") LA_TS_STEP(2, "t") LA_TS_STEP(3, "t") LA_TS_STEP(4, "t")
+            LA_TS_STEP(5, "t") LA_TS_STEP(6, "t") LA_TS_STEP(7, "t") "}" ::"r"(d_tmem),
+            "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, t;\n\t.reg .b32 ta;\n\t.reg .b64 db;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t"
+            LA_TS_STEP(0, "p") LA_TS_STEP(1, "t") LA_TS_STEP(2, "t") LA_TS_STEP(3, "t") "}" ::"r"(d_tmem),
+            "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+#undef LA_TS_STEP
+
+// D = A B^T of two K-major tiles of 128 rows.
+#define LA_SS_STEP(off, pred)                                                    \
+    "add.s64 da, %1, " #off ";\n\tadd.s64 db, %2, " #off ";\n\t"                   \
+    "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, " pred ";\n\t"
+template <int KSTEPS>
+__device__ __forceinline__ void mma_ss_kk(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
+    static_assert(KSTEPS == 4 || KSTEPS == 8, "K steps");
+    if constexpr (KSTEPS == 8)
+        asm volatile(
+            "{\n\t.reg .pred f, t;\n\t.reg .b64 da, db;\n\t"
+            "setp.ne.u32 f, 0, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t"
+            LA_SS_STEP(0, "f") LA_SS_STEP(2, "t") LA_SS_STEP(4, "t") LA_SS_STEP(6, "t") LA_SS_STEP(1024, "t")
+            LA_SS_STEP(1026, "t") LA_SS_STEP(1028, "t") LA_SS_STEP(1030, "t") "}" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred f, t;\n\t.reg .b64 da, db;\n\t"
+            "setp.ne.u32 f, 0, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t"
+            LA_SS_STEP(0, "f") LA_SS_STEP(2, "t") LA_SS_STEP(4, "t") LA_SS_STEP(6, "t") "}" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc)
+            : "memory");
+}
+#undef LA_SS_STEP
 
 // Arrive once on *bar when every tcgen05 operation issued so far by the issuing lane is done.
 __device__ __forceinline__ void mma_commit_w(uint64_t *bar) {
@@ -354,15 +428,6 @@ __device__ __forceinline__ void tma_store_3d_w(const CUtensorMap *map, const voi
         "@e cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];\n\t}" ::"l"(
             reinterpret_cast<uint64_t>(map)),
         "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
-        : "memory");
-}
-
-__device__ __forceinline__ void tma_store_4d_w(const CUtensorMap *map, const void *src, int x, int y, int z, int w) {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t.reg .u32 l;\n\tmov.u32 l, %%laneid;\n\tsetp.eq.u32 e, l, 0;\n\t"
-        "@e cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];\n\t}" ::"l"(
-            reinterpret_cast<uint64_t>(map)),
-        "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z), "r"(w)
         : "memory");
 }
 
