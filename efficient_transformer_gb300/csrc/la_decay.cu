@@ -23,7 +23,8 @@ la_status check(int B, int Hq, int Hkv, int N, int D, int Dv, int dtype, float s
 struct DecayPlan {
     la_path path;
     int seg_len, nseg;
-    size_t state_bytes, ws_bytes;   // one array of segment states; all of them
+    int nsub, sub_len;                          // tensor cores: parts of a segment that the state kernel sums
+    size_t state_bytes, part_bytes, ws_bytes;   // one array of segment states, one of their parts; all of them
 };
 
 bool tc_runs(int D, int Dv, la_dtype dt) { return dt == LA_BF16 && D != 32 && Dv != 32; }
@@ -72,8 +73,22 @@ DecayPlan make_plan(int B, int Hq, int Hkv, int N, int D, int Dv, la_dtype dt, b
     }
     pl.seg_len = best_cps * chunk;
     pl.nseg = (N + pl.seg_len - 1) / pl.seg_len;
-    pl.state_bytes = pl.nseg > 1 ? ((size_t)heads * pl.nseg * D * Dv * 4 + 255) / 256 * 256 : 0;
-    pl.ws_bytes = pl.state_bytes * (bwd ? 2 : 1);
+    if (pl.nseg == 1) return pl;
+    pl.state_bytes = ((size_t)heads * pl.nseg * D * Dv * 4 + 255) / 256 * 256;
+    if (pl.path == LA_PATH_SIMT) {
+        pl.ws_bytes = pl.state_bytes * (bwd ? 2 : 1);
+        return pl;
+    }
+    // as many parts as one wave of the state kernel takes
+    const long long sums = state_units * (pl.nseg - 1);
+    int nsub = (int)(places / (sums < places ? sums : places));
+    if (nsub > best_cps) nsub = best_cps;
+    const int spc = (best_cps + nsub - 1) / nsub;
+    pl.nsub = (best_cps + spc - 1) / spc;
+    pl.sub_len = spc * chunk;
+    pl.part_bytes = ((size_t)heads * (pl.nseg - 1) * pl.nsub * D * Dv * 4 + 255) / 256 * 256;
+    // forward: S; backward: S^T, A and A^T
+    pl.ws_bytes = pl.state_bytes * (bwd ? 3 : 1) + pl.part_bytes * (bwd ? 2 : 1);
     return pl;
 }
 
@@ -127,17 +142,21 @@ la_status run(bool bwd, const Given &a, int B, int Hq, int Hkv, int N, int D, in
     p.B = B; p.Hkv = Hkv; p.n_rep = Hq / Hkv; p.N = N; p.D = D; p.Dv = Dv;
     p.scale = scale;
     p.seg_len = pl.seg_len; p.nseg = pl.nseg;
-    float *slots0 = pl.nseg > 1 ? static_cast<float *>(ws) : nullptr;
-    float *slots1 = pl.nseg > 1 ? reinterpret_cast<float *>(static_cast<char *>(ws) + pl.state_bytes) : nullptr;
+    auto at = [&](size_t off) { return pl.nseg > 1 ? reinterpret_cast<float *>(static_cast<char *>(ws) + off) : nullptr; };
+    float *slots0 = at(0), *slots1 = at(pl.state_bytes), *slots2 = tc ? at(2 * pl.state_bytes) : slots1;
     DecayStateParams sp{};
     sp.log_decay = a.log_decay;
     sp.lengths = a.lengths;
     sp.B = B; sp.Hkv = Hkv; sp.N = N; sp.D = D; sp.Dv = Dv; sp.seg_len = pl.seg_len; sp.nseg = pl.nseg;
     // S = sum k v^T (both directions of a training step start from it)
     sp.y[0] = a.k; sp.z[0] = a.v; sp.sy[0] = sk; sp.sz[0] = sv; sp.init[0] = a.s_in; sp.init_mul[0] = 1.f;
-    sp.heads[0] = 1; sp.rev[0] = 0; sp.slots[0] = slots0;
+    sp.heads[0] = 1; sp.rev[0] = 0; sp.slots[0] = slots0; sp.exact[0] = a.s_out != nullptr;
     sp.n = 1;
+    sp.nsub = pl.nsub; sp.sub_len = pl.sub_len;
+    sp.part[0] = at(pl.state_bytes * (bwd ? 3 : 1));
+    sp.part[1] = at(pl.state_bytes * 3 + pl.part_bytes);
     if (!bwd) {
+        sp.start[0] = slots0;
         DecayPass &f = p.pass[0];
         f.x = a.q; f.y = a.k; f.z = a.v; f.sx = sq; f.sy = sk; f.sz = sv; f.out = a.out;
         f.slots = slots0; f.init = a.s_in; f.fin = a.s_out; f.init_mul = f.fin_mul = 1.f;
@@ -145,13 +164,15 @@ la_status run(bool bwd, const Given &a, int B, int Hq, int Hkv, int N, int D, in
     } else {
         // A = sum q g^T from the last token back
         sp.y[1] = a.q; sp.z[1] = a.g; sp.sy[1] = sq; sp.sz[1] = sg; sp.init[1] = a.ds_in; sp.init_mul[1] = 1.f / scale;
-        sp.heads[1] = p.n_rep; sp.rev[1] = 1; sp.slots[1] = slots1;
+        sp.heads[1] = p.n_rep; sp.rev[1] = 1; sp.slots[1] = slots1; sp.exact[1] = a.ds_out != nullptr;
         sp.n = 2;
+        sp.first_off[1] = 1;
+        sp.start_tr[0] = slots0; sp.start[1] = slots1; sp.start_tr[1] = slots2;
         DecayPass &q = p.pass[0], &k = p.pass[1], &v = p.pass[2];
         q.x = a.g; q.y = a.v; q.z = a.k; q.sx = sg; q.sy = sv; q.sz = sk; q.out = a.dq;
         q.slots = slots0; q.init = a.s_in; q.tr = 1; q.init_mul = q.fin_mul = 1.f;
         k.x = a.v; k.y = a.g; k.z = a.q; k.sx = sv; k.sy = sg; k.sz = sq; k.out = a.dk;
-        k.slots = slots1; k.init = a.ds_in; k.tr = 1;
+        k.slots = slots2; k.init = a.ds_in; k.tr = 1;
         v.x = a.k; v.y = a.q; v.z = a.g; v.sx = sk; v.sy = sq; v.sz = sg; v.out = a.dv;
         v.slots = slots1; v.init = a.ds_in; v.fin = a.ds_out;
         for (DecayPass *ps : {&k, &v}) {
@@ -169,6 +190,7 @@ la_status run(bool bwd, const Given &a, int B, int Hq, int Hkv, int N, int D, in
         e = error_word(&p.err);
         sp.err = p.err;
         if (e == cudaSuccess && pl.nseg > 1) e = decay_tc_states(sp, s);
+        if (e == cudaSuccess && pl.nseg > 1) e = decay_tc_join(sp, s);
         if (e == cudaSuccess) e = decay_tc_passes(p, s);
         return e == cudaSuccess ? LA_OK : cuda_fail(e);
     }

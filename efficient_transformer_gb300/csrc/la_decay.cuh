@@ -19,8 +19,10 @@ struct DecayPass {
     const void *x, *y, *z;      // [B, Hx, N, DX], [B, Hyz, N, DX], [B, Hyz, N, DZ]
     Strides sx, sy, sz;
     void *out;                  // [B, Hx, N, DZ], contiguous
-    const float *slots;         // nseg > 1: workspace, [B Hkv][nseg] states [D][Dv]: slot 0 the starting
-                                // state, slot u > 0 the sum over segment u - 1 alone
+    const float *slots;         // nseg > 1: workspace.  CUDA cores: [B Hkv][nseg] states [D][Dv], slot 0 the
+                                // starting state, slot u > 0 the sum over segment u - 1 alone.  Tensor cores:
+                                // [B Hkv][nseg] starting states of the segments, lane-blocked (decay_blocked) in the
+                                // pass's own orientation
     const float *init;          // nseg = 1: starting state [B Hkv][D][Dv] or null
     float *fin;                 // state after the last token, or null
     int tr;                     // the pass's DX x DZ state is the transpose of the stored D x Dv one
@@ -45,9 +47,11 @@ struct DecayParams {
     int *err;
 };
 
-// The sums over single segments that later segments start from, natural orientation [D][Dv]:
-// slot u + 1 = sum over segment u of gamma^(tokens after j in the segment) y_j z_j^T (summed over the
-// heads of y, z), slot 0 = the starting state (times init_mul).
+// The sums over single segments that later segments start from: for segment u, the sum of
+// gamma^(tokens after j in the segment) y_j z_j^T (over the heads of y, z), a state D x Dv.
+// CUDA cores: in slot u + 1, [D][Dv], with the starting state (times init_mul) in slot 0.
+// Tensor cores: each segment but the last in nsub parts (more blocks than segments: the kernel is short), in
+// part[(nseg - 1) nsub], lane-blocked; decay_tc_join() then makes the segments' starting states of them.
 struct DecayStateParams {
     const float *log_decay;
     const int *lengths;
@@ -58,10 +62,19 @@ struct DecayStateParams {
     int heads[2];               // heads of y and z per key/value head
     int rev[2];
     float *slots[2];
+    int exact[2];               // a float32 state that the caller gets depends on these sums (tensor cores)
     int n;                      // state arrays of this launch (1 or 2)
     int B, Hkv, N, D, Dv, seg_len, nseg;
+    int nsub, sub_len;          // tensor cores: parts of a segment
+    float *part[2];
+    float *start[2], *start_tr[2];   // ... and where the starting states go: as S, and as its transpose (or null)
+    int first_off[2];
     int *err;
 };
+
+// Lane-blocked states: element (row d, column e) of R rows at ((e / 4) R + d) 4 + e % 4, so that a warp whose
+// threads hold rows moves 16 bytes of each in one run.
+__host__ __device__ constexpr size_t decay_blocked(int R, int d, int e) { return ((size_t)(e / 4) * R + d) * 4 + e % 4; }
 
 // Tokens of sequence b.
 __device__ __forceinline__ int decay_tokens(const int *lengths, int b, int N) {
@@ -84,6 +97,7 @@ cudaError_t decay_simt_pass(const DecayParams &p, int pass, la_dtype dt, cudaStr
 // order, multiples of kDecayTcChunk tokens; every pass of a call in one launch where the widths allow.
 constexpr int kDecayTcChunk = 128;
 cudaError_t decay_tc_states(const DecayStateParams &p, cudaStream_t s);
+cudaError_t decay_tc_join(const DecayStateParams &p, cudaStream_t s);
 cudaError_t decay_tc_passes(const DecayParams &p, cudaStream_t s);
 
 // One token (la_decay_step).

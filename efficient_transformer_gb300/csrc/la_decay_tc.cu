@@ -7,20 +7,20 @@
 //   O  = P Z + bf16(gamma^(i+1) x_i) S_bf                   [C x DZ]
 //   S  = gamma^C S + (gamma^(C-1-j) y_j)^T Z                [DX x DZ]   fp32 in TMEM
 // Powers of gamma are only ever of whole distances >= 0, so no decay overflows.  The decayed Y^T is an
-// operand made from Y: it is split into two bf16 terms (hi + lo, 2^-17 relative) and both are multiplied,
-// because what it sums is a float32 output (the state); one rounding would leave 2^-9 there.
-// P, S_bf and the decayed X are rounded once: they only reach bf16 outputs.
+// operand made from Y.  Where the state is an output (float32) it is split into two bf16 terms (hi + lo, 2^-17
+// relative) and both are multiplied; one rounding would leave 2^-9 there.  Where the state only reaches bf16
+// outputs it is rounded once, as P, S_bf and the decayed X are.
 //
 // Operands made by the CUDA cores are read by the MMA from TMEM: P and the decayed X take the place of the
-// scores (P over columns that its thread has read, the decayed X over the rest when P is done),
+// scores (each warp of P puts its half over columns that its thread has read, the decayed X fills the rest),
 // Y^T has columns of its own.  That leaves the shared memory to the TMA tiles, the output tile and S_bf, and
 // halves the MMA's own shared-memory reads, which at 128 x 128 x 16 from shared memory would take all of its
 // bandwidth.  TMEM columns: S, O, scores / P / X, Y^T hi | lo.
 // Several heads of x share one chunk of y, z (grouped queries; S moves on after the last), or several heads
 // of y, z share one of x (their gradients; O and S sum over the heads).
 //
-// Warps: 0 TMA, 1 MMA of scores and O, 2 MMA of S, 4-7 P, 8-11 S -> S_bf and the decay of S, 12-15 the decayed X
-// and the output rows, 16-19 Y^T (and the zeros past a sequence's length).
+// Warps: 0 TMA, 1 MMA of scores and O, 2 MMA of S, 4-11 P (columns in two halves), 12-15 S -> S_bf and the decay of S,
+// 16-19 the decayed X and the output rows, 20-23 Y^T (and the zeros past a sequence's length).
 //
 // The reverse passes (gradients of k and v) take the same steps with j >= i and gamma^(j-i), chunks from the
 // last to the first.
@@ -31,7 +31,7 @@ namespace la {
 namespace {
 
 constexpr int C = kDecayTcChunk;
-constexpr int kMainThreads = 640;
+constexpr int kMainThreads = 768;
 
 // Bounded warp-uniform wait.  What follows a wait that does not end at once is out of line: the kernels have some
 // twenty waits, and their code has to stay in the instruction caches that all roles share.
@@ -73,6 +73,17 @@ __device__ __forceinline__ Part part_of(int n, int N, int u, int nseg, int seg_l
     return r;
 }
 
+// Part `sub` (in the pass's order) of segment u.
+__device__ __forceinline__ Part sub_part_of(int n, int N, int u, int nseg, int seg_len, int sub, int nsub, int sub_len,
+                                            int rev) {
+    const int s = rev ? nseg - 1 - u : u, q = rev ? nsub - 1 - sub : sub;
+    Part r;
+    r.lo = min(n, s * seg_len + min(seg_len, q * sub_len));
+    r.hi = min(n, s * seg_len + min(seg_len, (q + 1) * sub_len));
+    r.before = rev ? n - r.hi : r.lo;
+    return r;
+}
+
 // a b for two pairs of floats (one packed instruction).
 __device__ __forceinline__ void mul2(float &x, float &y, float a, float b) {
     unsigned long long p, q;
@@ -109,29 +120,40 @@ struct YtWeights {
     }
 };
 
-// Decayed Y^T of one tile for the warp's 32 lanes d from d0: y w as two bf16 terms, into 64 columns each at
-// th and tl.  With w = wh + wl (bf16 each), hi = bf16(y wh), the remainder y wh - hi is exact in
-// bf16 (one fused multiply-add) and lo = bf16(remainder + y wl): three packed operations a pair, 2^-17 relative in
-// all.  The tile's 8 x 8 blocks come transposed out of shared memory in the layout of the store.
-__device__ __forceinline__ void yt_tile(const uint8_t *y, int d0, const YtWeights &w, uint32_t th, uint32_t tl) {
+// Decayed Y^T of one tile for the warp's 32 lanes d from d0: y w in bf16 into 64 columns at th and, with
+// `lo`, what that rounding left, into 64 at tl.  With w = wh + wl (bf16 each), hi = bf16(y wh), the remainder
+// y wh - hi is exact in bf16 (one fused multiply-add) and lo = bf16(remainder + y wl): three packed operations
+// a pair, 2^-17 relative in all.  (Alone, hi = bf16(y wh + bf16(y wl)).)  The tile's 8 x 8 blocks come
+// transposed out of shared memory in the layout of the store.
+__device__ __forceinline__ void yt_tile(const uint8_t *y, int d0, const YtWeights &w, bool lo, uint32_t th, uint32_t tl) {
     const int t = threadIdx.x % 32;
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {   // lanes d0 + 16 half ..
         const uint32_t addr = smem_u32(y) + swz_chunk(C, 8 * (t / 16) + t % 8, (d0 + 16 * half) / 8 + ((t / 8) & 1));
+        const uint32_t lane = (uint32_t)(16 * half) << 16;
 #pragma unroll
-        for (int jh = 0; jh < 2; ++jh) {     // tokens 64 jh ..
-            uint32_t v[16], hi[16], lo[16];
+        for (int jq = 0; jq < 4; ++jq) {     // tokens 32 jq ..
+            uint32_t v[8], h[8];
+            ldmatrix_x4_trans(addr + jq * 32 * 128, v);
+            ldmatrix_x4_trans(addr + (jq * 32 + 16) * 128, v + 4);
+            if (lo) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) ldmatrix_x4_trans(addr + (jh * 64 + q * 16) * 128, v + 4 * q);
+                for (int i = 0; i < 8; ++i) {
+                    const int g = jq * 4 + i / 2;   // group of 8 tokens
+                    const __nv_bfloat162 u = as_bf162(v[i]), wh = as_bf162(w.hi[g]), p = __hmul2(u, wh);
+                    h[i] = as_u32(p);
+                    v[i] = as_u32(__hfma2(u, as_bf162(w.lo[g]), __hfma2(u, wh, __hneg2(p))));
+                }
+                tmem_st_frag16(tl + lane + jq * 16, v);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int g = jh * 8 + i / 2;   // group of 8 tokens
-                const __nv_bfloat162 u = as_bf162(v[i]), wh = as_bf162(w.hi[g]), h = __hmul2(u, wh);
-                hi[i] = as_u32(h);
-                lo[i] = as_u32(__hfma2(u, as_bf162(w.lo[g]), __hfma2(u, wh, __hneg2(h))));
+                for (int i = 0; i < 8; ++i) {
+                    const int g = jq * 4 + i / 2;
+                    const __nv_bfloat162 u = as_bf162(v[i]);
+                    h[i] = as_u32(__hfma2(u, as_bf162(w.hi[g]), __hmul2(u, as_bf162(w.lo[g]))));
+                }
             }
-            tmem_st_frag32(th + ((uint32_t)(16 * half) << 16) + jh * 32, hi);
-            tmem_st_frag32(tl + ((uint32_t)(16 * half) << 16) + jh * 32, lo);
+            tmem_st_frag16(th + lane + jq * 16, h);
         }
     }
 }
@@ -180,19 +202,19 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         abort_flag = 0;
         for (int s = 0; s < NX; ++s) {
             mbar_init(&x_full[s], 1);
-            mbar_init(&x_empty[s], 1 + 4);
+            mbar_init(&x_empty[s], 8 + 4);   // warps of P (the scores are over), of the decayed X
         }
         for (int s = 0; s < NY; ++s) {
             mbar_init(&y_full[s], 1);
-            mbar_init(&y_empty[s], 1 + 4);
+            mbar_init(&y_empty[s], 8 + 4);   // warps of P, of Y^T
         }
         for (int s = 0; s < NZ; ++s) {
             mbar_init(&z_full[s], 1);
             mbar_init(&z_empty[s], 2);
         }
         mbar_init(&sc_full, 1);
-        mbar_init(&p_ready, 128);
-        mbar_init(&p_first, 128);
+        mbar_init(&p_ready, 256);
+        mbar_init(&p_first, 256);
         mbar_init(&xd_ready, 128);
         mbar_init(&o_full, 1);
         mbar_init(&o_free, 128);
@@ -220,6 +242,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
     tc_fence_after();
     const uint32_t tm = tmem_base;
     const int items = nchunk * reps;
+    const bool exact = ps.fin != nullptr;   // the state is an output
 
     if (warp < 4) {
         if (warp == 0) {
@@ -290,8 +313,6 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                 if (elect_one()) {
                     mma_ss_kk<DX / 16>(tA, desc_kmajor(x, C, 0, 0), desc_kmajor(y, C, 0, 0), idA);
                     mma_commit(&sc_full);
-                    if (ends) mma_commit(&x_empty[ix % NX]);
-                    if (last || many) mma_commit(&y_empty[iy % NY]);
                 }
                 __syncwarp();
                 LA_TL(it, 1);
@@ -301,14 +322,14 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                 if (!await(&p_ready, it & 1, &abort_flag)) break;
                 LA_TL(it, 4);
                 tc_fence_after();
-                if (elect_one()) mma_ts_mn<C / 16>(tO, tA, desc_mnmajor(z, C, 0, 0), idO, opens ? 0u : 1u);
+                if (elect_one()) mma_ts_mn<C / 16, 4>(tO, tA, desc_mnmajor(z, C, 0, 0), idO, opens ? 0u : 1u);
                 __syncwarp();
                 if (opens) {
                     if (!await(&xd_ready, ot & 1, &abort_flag)) break;
                     if (first && !await(&s_conv, k & 1, &abort_flag)) break;
                     LA_TL(it, 5);
                     tc_fence_after();
-                    if (elect_one()) mma_ts_mn<DX / 16>(tO, tA + 64, desc_mnmajor(sb, DX, 0, 0), idO, 1u);
+                    if (elect_one()) mma_ts_mn<DX / 16, 4>(tO, tA + 32, desc_mnmajor(sb, DX, 0, 0), idO, 1u);
                     __syncwarp();
                 }
                 if (elect_one()) {
@@ -347,7 +368,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                 const bool ends = ++r == per;
                 if (elect_one()) {
                     mma_ts_mn<C / 16>(tS, tYh, desc_mnmajor(z, C, 0, 0), idS, 1u);
-                    mma_ts_mn<C / 16>(tS, tYl, desc_mnmajor(z, C, 0, 0), idS, 1u);
+                    if (exact) mma_ts_mn<C / 16>(tS, tYl, desc_mnmajor(z, C, 0, 0), idS, 1u);
                     mma_commit(&yt_done);
                     mma_commit(&z_empty[t % NZ]);
                     if (ends) mma_commit(&s_full);
@@ -362,13 +383,13 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             __syncwarp();
             warp_drain(&fin[1], 0);
         }
-    } else if (warp < 8) {
-        // ---------------- P = bf16(scale A o W), thread = row i, 32 columns at a time.  Away from the diagonal
-        // gamma^|i - j| = gamma^(distance to the near end of a block of 16) gamma^(distance in the block); on it the blocks
-        // of 16 have the lower (reverse: upper) triangle of one pattern, or are such a full block, or nothing.  Both
-        // patterns stay in registers, with `scale`
-        const int wq = warp % 4, lane = threadIdx.x % 32, i = wq * 32 + lane;
-        const uint32_t ta = tm + K::T_A + ((uint32_t)(wq * 32) << 16);
+    } else if (warp < 12) {
+        // ---------------- P = bf16(scale A o W), thread = (row i, half of the columns), 32 columns at a time.  Away from
+        // the diagonal gamma^|i - j| = gamma^(distance to the near end of a block of 16) gamma^(distance in the block); on
+        // it the blocks of 16 have the lower (reverse: upper) triangle of one pattern, or are such a full block, or
+        // nothing.  Both patterns stay in registers, with `scale`
+        const int wq = warp % 4, lane = threadIdx.x % 32, i = wq * 32 + lane, hc = (warp - 4) / 4;
+        const uint32_t ta = tm + K::T_A + hc * 64 + ((uint32_t)(wq * 32) << 16);
         float g[16], tri[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
@@ -377,20 +398,24 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             tri[e] = ago >= 0 ? p.scale * pw[max(ago, 0)] : 0.f;
         }
         const bool low = lane < 16;
-        int r = 0;
+        int r = 0, nx = 0, ny = 0;
         for (int it = 0; it < items; ++it) {
             if (!await(&sc_full, it & 1, &abort_flag)) break;
             tc_fence_after();
-            if (i == 127) LA_TL(it, 7);
+            if (threadIdx.x == 383) LA_TL(it, 7);
+            const bool last = ++r == reps;
+            if (last || !many) mbar_arrive_w(&x_empty[nx++ % NX]);
+            if (last || many) mbar_arrive_w(&y_empty[ny++ % NY]);
 #pragma unroll 1
-            for (int cb = 0; cb < C / 32; ++cb) {
+            for (int c = 0; c < 2; ++c) {
+                const int cb = hc * 2 + c;   // 32 columns
                 uint32_t w[16];
                 if (rev ? cb < wq : cb > wq) {   // the warp's rows have no such token
 #pragma unroll
                     for (int e = 0; e < 16; ++e) w[e] = 0u;
                 } else {
                     float v[32];
-                    tmem_ld32(ta + cb * 32, v);
+                    tmem_ld32(ta + c * 32, v);
                     tmem_wait_regs<32>(v);
 #pragma unroll
                     for (int hb = 0; hb < 2; ++hb) {
@@ -419,39 +444,56 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
 #pragma unroll
                     for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
                 }
-                // over columns that this thread has read (16 cb .. 16 cb + 15 <= 32 cb + 31)
-                tmem_st16_raw(ta + cb * 16, w);
+                // over columns of this half that this thread has read (16 c .. 16 c + 15 <= 32 c + 31)
+                tmem_st16_raw(ta + c * 16, w);
             }
             tmem_st_wait();
             tc_fence_before();
-            if (i == 127) LA_TL(it, 8);
+            if (threadIdx.x == 383) LA_TL(it, 8);
             mbar_arrive_warp(&p_ready);
-            if (r == 0 || !many) mbar_arrive_warp(&p_first);
-            if (++r == reps) r = 0;
+            if (r == 1 || !many) mbar_arrive_warp(&p_first);
+            if (last) r = 0;
         }
-    } else if (warp < 12) {
+    } else if (warp < 16) {
         // ---------------- S: the operand S_bf of the state before the chunk, and its decay; thread = row d
         const int wq = warp % 4, d = wq * 32 + threadIdx.x % 32;
         const uint32_t ts = tm + K::T_S + ((uint32_t)(wq * 32) << 16);
         const bool have = wq * 32 < DX;
         const size_t E = (size_t)p.D * p.Dv;
-        // the segment's starting state (element [d][e] of the pass's state is at d sd + e se of a stored one)
+        // element [d][e] of the pass's state is at d sd + e se of a state that the caller keeps
         const size_t sd = ps.tr ? 1 : p.Dv, se = ps.tr ? p.Dv : 1;
-        const float *from = p.nseg > 1 ? ps.slots + (size_t)bg * p.nseg * E : ps.init ? ps.init + (size_t)bg * E : nullptr;
-        const float m0 = p.nseg > 1 ? (u > 0 ? exp2f(l2 * (part.before - ps.first_off)) : 1.f) : ps.init_mul;
-        auto start16 = [&](int e0, float *v) {
+        // 32 columns of the segment's starting state
+        auto start32 = [&](int e0, float *v) {
+            if (p.nseg > 1) {
+                const float4 *f = reinterpret_cast<const float4 *>(ps.slots + ((size_t)bg * p.nseg + u) * E + decay_blocked(DX, d, e0));
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = 0.f;
-            if (!from) return;
-            const float *f = from + d * sd + e0 * se;
+                for (int q = 0; q < 8; ++q) {
+                    const float4 x = f[q * DX];
+                    v[4 * q] = x.x;
+                    v[4 * q + 1] = x.y;
+                    v[4 * q + 2] = x.z;
+                    v[4 * q + 3] = x.w;
+                }
+            } else if (ps.init) {
+                const float *f = ps.init + (size_t)bg * E + d * sd + e0 * se;
+                if (ps.tr) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = f[e * se] * m0;
-            for (int w = 1; w <= u; ++w) {
-                const float g = exp2f(l2 * (part.before - (part_of(n, p.N, w, p.nseg, p.seg_len, rev).before)));
-                if (g == 0.f) continue;   // decayed to nothing
-                const float *fw = f + (size_t)w * E;
+                    for (int e = 0; e < 32; ++e) v[e] = f[e * se];
+                } else {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = fmaf(fw[e * se], g, v[e]);
+                    for (int q = 0; q < 8; ++q) {
+                        const float4 x = reinterpret_cast<const float4 *>(f)[q];
+                        v[4 * q] = x.x;
+                        v[4 * q + 1] = x.y;
+                        v[4 * q + 2] = x.z;
+                        v[4 * q + 3] = x.w;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] *= ps.init_mul;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = 0.f;
             }
         };
         // the powers of gamma that S takes before each chunk's Y^T Z; first the chunk that starts from memory
@@ -460,13 +502,15 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         const float g = pw[C], gl = pw[rev ? C : vlast];
         if (have) {
 #pragma unroll 1
-            for (int c16 = 0; c16 < DZ / 16; ++c16) {
-                float v[16];
-                start16(c16 * 16, v);
-                store_state_row<DX>(sbf, d, v, c16);
+            for (int c32 = 0; c32 < DZ / 32; ++c32) {
+                float v[32];
+                start32(c32 * 32, v);
+                store_state_row<DX>(sbf, d, v, 2 * c32);
+                store_state_row<DX>(sbf, d, v + 16, 2 * c32 + 1);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] *= g0;
-                tmem_st16(ts + c16 * 16, v);
+                for (int e = 0; e < 32; ++e) v[e] *= g0;
+                tmem_st16(ts + c32 * 32, v);
+                tmem_st16(ts + c32 * 32 + 16, v + 16);
             }
             tmem_st_wait();
         }
@@ -516,11 +560,11 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                     for (int e = 0; e < 16; ++e) f[(size_t)(c16 * 16 + e) * se] = v[e] * mul;
                 }
         }
-    } else if (warp < 16) {
+    } else if (warp < 20) {
         // ---------------- rows of x and of the output; thread = row i.  The decayed x is made in registers while P is
         // under way and stored where the scores have been read
         const int wq = warp % 4, i = wq * 32 + threadIdx.x % 32;
-        const uint32_t lane_off = (uint32_t)(wq * 32) << 16, to = tm + K::T_O + lane_off, tx = tm + K::T_A + 64 + lane_off;
+        const uint32_t lane_off = (uint32_t)(wq * 32) << 16, to = tm + K::T_O + lane_off, tx = tm + K::T_A + 32 + lane_off;
         const int tiles = many ? nchunk : items;
         const CUtensorMap *mo = &maps.m[pi][3];
         int k = 0, r = 0;
@@ -548,7 +592,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                 tc_fence_after();
                 if (i == 0) LA_TL(t, 11);
 #pragma unroll
-                for (int q = 0; q < DX / 32; ++q) tmem_st16_raw(tx + q * 16, w + 16 * q);
+                for (int q = 0; q < DX / 32; ++q) tmem_st16_raw(tx + (q / 2) * 64 + (q % 2) * 16, w + 16 * q);
                 tmem_st_wait();
             }
             tc_fence_before();
@@ -611,8 +655,8 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             uint8_t *y = ybuf + (t % NY) * K::Y_BYTES;
             if (p.lengths && valid < C) {
                 if (!await(&z_full[t % NZ], (t / NZ) & 1, &abort_flag)) break;
-                zero_rows<DX>(y, valid, threadIdx.x - 512, 128);
-                zero_rows<DZ>(zbuf + (t % NZ) * K::Z_BYTES, valid, threadIdx.x - 512, 128);
+                zero_rows<DX>(y, valid, threadIdx.x - 640, 128);
+                zero_rows<DZ>(zbuf + (t % NZ) * K::Z_BYTES, valid, threadIdx.x - 640, 128);
                 fence_proxy_async();
                 mbar_arrive_warp(&zeroed);
                 // (the warps read one another's zeros)
@@ -625,12 +669,12 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                     shorter = valid < C;
                     w.set(wtab[shorter], 1.f);
                 }
-                yt_tile(y, wq * 32, w, tm + K::T_YH + lane_off, tm + K::T_YL + lane_off);
+                yt_tile(y, wq * 32, w, exact, tm + K::T_YH + lane_off, tm + K::T_YL + lane_off);
                 tmem_st_wait();
             }
             mbar_arrive_w(&y_empty[t % NY]);
             tc_fence_before();
-            if (threadIdx.x == 512) LA_TL(t, 15);
+            if (threadIdx.x == 640) LA_TL(t, 15);
             mbar_arrive_warp(&yt_ready);
             if (!many || ++r == reps) {
                 r = 0;
@@ -685,15 +729,14 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
     uint8_t *stage = align1024(smem_raw);
     pdl_wait();
     const int warp = threadIdx.x / 32;
-    const int u = blockIdx.x % (p.nseg - 1), ah = blockIdx.x / (p.nseg - 1);
+    const int nparts = (p.nseg - 1) * p.nsub, pidx = blockIdx.x % nparts, ah = blockIdx.x / nparts;
     const int a = ah / (p.B * p.Hkv), bg = ah % (p.B * p.Hkv), b = bg / p.Hkv, h = bg % p.Hkv;
     const int n = decay_tokens(p.lengths, b, p.N), rev = p.rev[a], heads = p.heads[a];
-    const Part part = part_of(n, p.N, u, p.nseg, p.seg_len, rev);
+    const Part part = sub_part_of(n, p.N, pidx / p.nsub, p.nseg, p.seg_len, pidx % p.nsub, p.nsub, p.sub_len, rev);
     const int nchunk = (part.hi - part.lo + C - 1) / C, items = nchunk * heads;
     const float l2 = decay_log2(p.log_decay[h]);
     const int vlast = part.hi - part.lo - C * (nchunk - 1);
-    const size_t E = (size_t)D * DV;
-    float *slots = p.slots[a] + (size_t)bg * p.nseg * E;
+    float *dst = p.part[a] + ((size_t)bg * nparts + pidx) * D * DV;
 
     if (threadIdx.x == 0) {
         abort_flag = 0;
@@ -749,7 +792,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
             const uint32_t z = smem_u32(stage + s * K::STAGE + K::Y_BYTES), ty = tm + T_Y + 128 * q;
             if (elect_one()) {
                 mma_ts_mn<C / 16>(tm + T_S, ty, desc_mnmajor(z, C, 0, 0), id, it > 0 ? 1u : 0u);
-                mma_ts_mn<C / 16>(tm + T_S, ty + 64, desc_mnmajor(z, C, 0, 0), id, 1u);
+                if (p.exact[a]) mma_ts_mn<C / 16>(tm + T_S, ty + 64, desc_mnmajor(z, C, 0, 0), id, 1u);
                 mma_commit(&yt_done[q]);
                 mma_commit(&empty[s]);
             }
@@ -781,7 +824,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
                 // what the chunk's last token has ahead of it in the segment
                 YtWeights w;
                 w.set(wtab[valid < C], exp2f(l2 * (rev ? c0 - part.lo : part.hi - c0 - valid)));
-                yt_tile(y, wq * 32, w, tm + T_Y + 128 * q + lane_off, tm + T_Y + 128 * q + 64 + lane_off);
+                yt_tile(y, wq * 32, w, p.exact[a], tm + T_Y + 128 * q + lane_off, tm + T_Y + 128 * q + 64 + lane_off);
                 tmem_st_wait();
             }
             tc_fence_before();
@@ -801,19 +844,83 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
 #pragma unroll
                         for (int e = 0; e < 16; ++e) v[e] = 0.f;
                     }
-                    float4 *f = reinterpret_cast<float4 *>(slots + (size_t)(u + 1) * E + (size_t)d * DV + c16 * 16);
+                    float4 *f = reinterpret_cast<float4 *>(dst + decay_blocked(D, d, c16 * 16));
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) f[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                    for (int e = 0; e < 4; ++e) f[e * D] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                 }
-        } else if (warp >= 8 && u == 0) {   // slot 0: the starting state
-            const float *f = p.init[a] ? p.init[a] + (size_t)bg * E : nullptr;
-            for (int i = threadIdx.x - 256; i < (int)E; i += 128) slots[i] = f ? f[i] * p.init_mul[a] : 0.f;
         }
     }
     tc_fence_before();
     __syncthreads();
     if (warp == 1) tmem_dealloc(tm, 512);
     if (threadIdx.x == 0 && abort_flag) atomicExch(p.err, kErrTimeout);
+}
+
+// ---------------------------------------------------------------------------------------
+// Starting states of the segments: T = the given state, then for each segment T = gamma^tokens T + its sum, a
+// thread carrying 4 x 4 elements; all states lane-blocked but the caller's.
+constexpr int kJoinThreads = 64;
+
+template <int D, int DV>
+__global__ void __launch_bounds__(kJoinThreads) k_decay_join(const __grid_constant__ DecayStateParams p) {
+    pdl_wait();
+    constexpr int kBlocks = D * DV / 16 / kJoinThreads;   // of one state
+    const int ah = blockIdx.x / kBlocks, a = ah / (p.B * p.Hkv), bg = ah % (p.B * p.Hkv), b = bg / p.Hkv, h = bg % p.Hkv;
+    const int idx = blockIdx.x % kBlocks * kJoinThreads + threadIdx.x, d = idx % (D / 4) * 4, e = idx / (D / 4) * 4;
+    constexpr size_t E = (size_t)D * DV;
+    const int n = decay_tokens(p.lengths, b, p.N), nparts = (p.nseg - 1) * p.nsub;
+    const float l2 = decay_log2(p.log_decay[h]);
+    float4 t[4];   // rows d .. d + 3, columns e .. e + 3
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        t[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p.init[a]) {
+            const float4 x = *reinterpret_cast<const float4 *>(p.init[a] + bg * E + (size_t)(d + i) * DV + e);
+            const float m = p.init_mul[a];
+            t[i] = make_float4(x.x * m, x.y * m, x.z * m, x.w * m);
+        }
+    }
+    const float4 *src = reinterpret_cast<const float4 *>(p.part[a] + (size_t)bg * nparts * E + decay_blocked(D, d, e));
+    auto store = [&](int u) {
+        if (p.start[a]) {
+            float4 *o = reinterpret_cast<float4 *>(p.start[a] + ((size_t)bg * p.nseg + u) * E + decay_blocked(D, d, e));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = t[i];
+        }
+        if (p.start_tr[a]) {
+            float4 *o = reinterpret_cast<float4 *>(p.start_tr[a] + ((size_t)bg * p.nseg + u) * E + decay_blocked(DV, e, d));
+            o[0] = make_float4(t[0].x, t[1].x, t[2].x, t[3].x);
+            o[1] = make_float4(t[0].y, t[1].y, t[2].y, t[3].y);
+            o[2] = make_float4(t[0].z, t[1].z, t[2].z, t[3].z);
+            o[3] = make_float4(t[0].w, t[1].w, t[2].w, t[3].w);
+        }
+    };
+    store(0);
+    int off = p.first_off[a];
+    // kAhead parts' sums are on their way at a time: one after the other costs a memory latency each
+    constexpr int kAhead = 4;
+    for (int i0 = 0; i0 < nparts; i0 += kAhead) {
+        float4 x[kAhead][4];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x[j][i] = i0 + j < nparts ? src[(size_t)(i0 + j) * (E / 4) + i] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (i0 + j >= nparts) break;
+            const int u = (i0 + j) / p.nsub, s = (i0 + j) % p.nsub;
+            const Part part = sub_part_of(n, p.N, u, p.nseg, p.seg_len, s, p.nsub, p.sub_len, p.rev[a]);
+            const int len = part.hi - part.lo;
+            const float g = exp2f(l2 * max(len - off, 0));
+            if (len > 0) off = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                t[i] = make_float4(fmaf(g, t[i].x, x[j][i].x), fmaf(g, t[i].y, x[j][i].y), fmaf(g, t[i].z, x[j][i].z),
+                                   fmaf(g, t[i].w, x[j][i].w));
+            if (s == p.nsub - 1) store(u + 1);
+        }
+    }
 }
 
 // ---- launches ---------------------------------------------------------------------------
@@ -857,7 +964,7 @@ cudaError_t states_d(const DecayStateParams &p, cudaStream_t s) {
     cudaError_t e = prepare(kern, StateCfg<D, DV>::SMEM);
     if (e != cudaSuccess) return e;
     TraceScope tr("decay_tc_state", s);
-    return launch_pdl(kern, dim3((unsigned)p.n * (p.nseg - 1) * p.B * p.Hkv), dim3(kStateThreads), StateCfg<D, DV>::SMEM, s,
+    return launch_pdl(kern, dim3((unsigned)p.n * (p.nseg - 1) * p.nsub * p.B * p.Hkv), dim3(kStateThreads), StateCfg<D, DV>::SMEM, s,
                       maps, p);
 }
 
@@ -866,6 +973,13 @@ cudaError_t states_d(const DecayStateParams &p, cudaStream_t s) {
 cudaError_t decay_tc_states(const DecayStateParams &p, cudaStream_t s) {
     if (p.D == 64) return p.Dv == 64 ? states_d<64, 64>(p, s) : states_d<64, 128>(p, s);
     return p.Dv == 64 ? states_d<128, 64>(p, s) : states_d<128, 128>(p, s);
+}
+
+cudaError_t decay_tc_join(const DecayStateParams &p, cudaStream_t s) {
+    auto kern = p.D == 64 ? (p.Dv == 64 ? k_decay_join<64, 64> : k_decay_join<64, 128>)
+                          : (p.Dv == 64 ? k_decay_join<128, 64> : k_decay_join<128, 128>);
+    TraceScope tr("decay_join", s);
+    return launch_pdl(kern, dim3(p.D * p.Dv / 16 / kJoinThreads * (unsigned)(p.n * p.B * p.Hkv)), dim3(kJoinThreads), 0, s, p);
 }
 
 cudaError_t decay_tc_passes(const DecayParams &p, cudaStream_t s) {
