@@ -6,8 +6,10 @@
 //
 // Bound by memory: each row is read once and written once (the backward reads x and g).  A row of D
 // elements lies in D / V neighbouring lanes, V = 16 bytes' worth each; such a group of lanes
-// owns one token and walks its heads, so the token's cos and sin stay in registers.  kBatch heads' rows are
-// loaded before the first is used.
+// owns a token at a time and walks its heads, so that the token's cos and sin, with the weights in them
+// (y[e] = r (x[e] w[e] c[e] + x[e'] w[e'] s[e]), e' the pair's other element), stay in registers; the
+// partner's elements come by shuffles of the packed row.  kBatch heads' rows are loaded before the
+// first is used.
 //
 // Angles.  positions are 64-bit integers and inv_freq doubles, so an angle in float32, or even its
 // reduction mod 2 pi there, would lose far positions.  inv_freq / 2 pi becomes a 64-bit binary fraction of a
@@ -20,7 +22,7 @@
 namespace la {
 namespace {
 
-constexpr int kThreads = 256, kBatch = 4;
+constexpr int kThreads = 256, kBatch = 4, kBatchBwd = 4;
 
 struct QkParams {
     const void *x[2], *g[2];     // q and k rows; their output gradients (backward)
@@ -36,7 +38,8 @@ struct QkParams {
     long long ps[3];
     const double *inv_freq;
     int heads_per_block;         // forward: heads of the joined list q, k that a block walks
-    float *part;                 // backward: [blocks][2][D] sums for the weights' gradients, or null
+    int y_blocks[2];             // backward: shares of q's and of k's heads (gridDim.y in all)
+    float *part;                 // backward: [gridDim.y][gridDim.x][D] sums for the weights' gradients, or null
 };
 
 // inv_freq / 2 pi as a fraction of 2^64, wrapping: the double's 53-bit significand times
@@ -94,49 +97,132 @@ template <> struct Row<__nv_bfloat16> {
     }
 };
 
-// One lane's part of a token: its cos and (signed) sin, so that element e of the turned row is
-// x[e] c[e] + partner[e] s[e].
+__device__ __forceinline__ unsigned long long pack2(float a, float b) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(unsigned long long p) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// A lane's 16 bytes of a row as V / 2 packed pairs of floats.
+template <typename T>
+__device__ __forceinline__ void unpack_row(const uint4 &u, unsigned long long *v) {
+    float f[Row<T>::V];
+    Row<T>::unpack(u, f);
+#pragma unroll
+    for (int i = 0; i < Row<T>::V / 2; ++i) v[i] = pack2(f[2 * i], f[2 * i + 1]);
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack_row(const unsigned long long *v) {
+    float f[Row<T>::V];
+#pragma unroll
+    for (int i = 0; i < Row<T>::V / 2; ++i) {
+        const float2 x = unpack2(v[i]);
+        f[2 * i] = x.x;
+        f[2 * i + 1] = x.y;
+    }
+    return Row<T>::pack(f);
+}
+
+// One lane's angles: the turned row is x[e] c[e] + partner[e] s[e].
 template <typename T, int D, bool INTER>
 struct Turn {
-    static constexpr int V = Row<T>::V;   // elements a lane
-    float c[V], s[V];
-    bool on;
-    int src;   // lane of the partner's elements (split halves)
+    static constexpr int V = Row<T>::V;                  // elements a lane
+    static constexpr int PAIRS = V / 2;                  // pairs that it finds the angles of
+    unsigned long long freq[PAIRS];                      // turns of them
+    const long long *pos[PAIRS];                         // positions of their axes
+    bool on, first;
+    int src;                                             // lane of the partner's elements (split halves)
 
-    __device__ __forceinline__ void set(const QkParams &p, int b, int n, int lane, bool back) {
+    __device__ __forceinline__ void init(const QkParams &p, int lane) {
         const int col = lane * V, half = p.rot / 2;
         on = col < p.rot;
-        src = threadIdx.x % 32;
-        if (!on) return;
-        const bool first = col < half;
-        if (!INTER) src += first ? half / V : -(half / V);
+        first = col < half;
+        src = threadIdx.x % 32 + (INTER || !on ? 0 : first ? half / V : -(half / V));
 #pragma unroll
-        for (int e = 0; e < V; e += INTER ? 2 : 1) {
-            const int pair = INTER ? (col + e) / 2 : (first ? col : col - half) + e;
+        for (int i = 0; i < PAIRS; ++i) {
+            // split halves: both lanes of a pair of lanes need all V angles, each finds half of them
+            const int pair = INTER ? col / 2 + i : (first ? col : col - half + PAIRS) + i;
             int a = 0;
-            while (a + 1 < p.axes && pair >= p.first_pair[a + 1]) ++a;
-            const unsigned long long pos = (unsigned long long)p.pos[a * p.ps[0] + b * p.ps[1] + n * p.ps[2]];
-            const int t = (int)((pos * turns_of(p.inv_freq[pair])) >> 32);   // turns in 2^-32, [-1/2, 1/2)
-            float sn, cs;
-            sincospif((float)t * 4.656612873077393e-10f, &sn, &cs);   // 2^-31: half turns
-            if (back) sn = -sn;
+            while (on && a + 1 < p.axes && pair >= p.first_pair[a + 1]) ++a;
+            pos[i] = p.pos + a * p.ps[0];
+            freq[i] = on ? turns_of(p.inv_freq[pair]) : 0ull;
+        }
+    }
+    // cos and sin of a token: c[e], s[e] (signed; the other way with `back`)
+    __device__ __forceinline__ void at(const QkParams &p, int b, int n, bool back, float *c, float *s) const {
+        float cs[PAIRS], sn[PAIRS];
+        const long long off = b * p.ps[1] + n * p.ps[2];
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) {
+            const unsigned long long at = on ? (unsigned long long)pos[i][off] : 0ull;
+            const int t = (int)((at * freq[i]) >> 32);   // turns in 2^-32, [-1/2, 1/2)
+            sincospif((float)t * 4.656612873077393e-10f, &sn[i], &cs[i]);   // 2^-31: half turns
+            if (back) sn[i] = -sn[i];
+        }
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) {
             if (INTER) {
-                c[e] = c[e + 1] = cs;
-                s[e] = -sn;
-                s[e + 1] = sn;
+                c[2 * i] = c[2 * i + 1] = cs[i];
+                s[2 * i] = -sn[i];
+                s[2 * i + 1] = sn[i];
             } else {
-                c[e] = cs;
-                s[e] = first ? -sn : sn;
+                const float co = __shfl_sync(0xffffffffu, cs[i], src), so = __shfl_sync(0xffffffffu, sn[i], src);
+                c[i] = first ? cs[i] : co;
+                c[PAIRS + i] = first ? co : cs[i];
+                s[i] = first ? -sn[i] : so;
+                s[PAIRS + i] = first ? -so : sn[i];
+            }
+        }
+        if (!on) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                c[e] = 1.f;
+                s[e] = 0.f;
             }
         }
     }
-    __device__ __forceinline__ void apply(float *v) const {
-        float o[V];
+    // The partner's elements of a packed row; a lane that is not turned gets zeros (0 times whatever lies there).
+    __device__ __forceinline__ uint4 partner(const uint4 &u) const {
+        if (INTER) return u;
+        uint4 r;
+        r.x = __shfl_sync(0xffffffffu, u.x, src);
+        r.y = __shfl_sync(0xffffffffu, u.y, src);
+        r.z = __shfl_sync(0xffffffffu, u.z, src);
+        r.w = __shfl_sync(0xffffffffu, u.w, src);
+        return r;
+    }
+    // x c + partner s, packed pairs
+    __device__ __forceinline__ void apply(const unsigned long long *x, const uint4 &raw, const unsigned long long *c,
+                                          const unsigned long long *s, unsigned long long *y) const {
+        unsigned long long o[V / 2];
+        if (INTER) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = INTER ? v[e ^ 1] : __shfl_sync(0xffffffffu, v[e], src);
-        if (on) {
+            for (int i = 0; i < V / 2; ++i) {
+                const float2 f = unpack2(x[i]);
+                o[i] = pack2(f.y, f.x);
+            }
+        } else {
+            unpack_row<T>(partner(raw), o);
+        }
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[e] = fmaf(v[e], c[e], o[e] * s[e]);
+        for (int i = 0; i < V / 2; ++i) {
+            y[i] = mul2(x[i], c[i]);
+            if (on) y[i] = fma2(o[i], s[i], y[i]);
         }
     }
 };
@@ -157,147 +243,178 @@ __device__ __forceinline__ void load_weights(const QkParams &p, int which, int c
                            : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.w[which])[col + e]);
 }
 
-// blockIdx.x: kThreads / L tokens, blockIdx.y: heads_per_block heads.
+// Blocks walk the tokens in strides of gridDim.x, kThreads / L at a time; blockIdx.y: heads_per_block heads.
 template <typename T, int D, bool INTER>
-__global__ void __launch_bounds__(kThreads) k_qk_fwd(QkParams p) {
-    using R = Row<T>;
-    constexpr int V = R::V, L = D / V;
+__global__ void __launch_bounds__(kThreads, 3) k_qk_fwd(QkParams p) {
+    constexpr int V = Row<T>::V, L = D / V, kTok = kThreads / L;
     pdl_wait();
     const int lane = threadIdx.x % L;
-    const long long tok = (long long)blockIdx.x * (kThreads / L) + threadIdx.x / L;
-    const bool live = tok < (long long)p.B * p.N;
-    const int b = live ? (int)(tok / p.N) : 0, n = live ? (int)(tok % p.N) : 0;
-    Turn<T, D, INTER> turn;
-    turn.set(p, b, n, lane, false);
+    const unsigned ntok = (unsigned)p.B * p.N;   // below 2^31
     const int h0 = blockIdx.y * p.heads_per_block, h1 = min(h0 + p.heads_per_block, p.H[0] + p.H[1]);
+    Turn<T, D, INTER> turn;
+    turn.init(p, lane);
+    for (unsigned t0 = blockIdx.x * kTok; t0 < ntok; t0 += gridDim.x * kTok) {
+        const unsigned tok = t0 + threadIdx.x / L;
+        const bool live = tok < ntok;
+        const int b = live ? (int)(tok / (unsigned)p.N) : 0, n = live ? (int)(tok - (unsigned)b * p.N) : 0;
+        float ct[V], st[V];
+        turn.at(p, b, n, false, ct, st);
 #pragma unroll 1
-    for (int which = 0; which < 2; ++which) {
-        const int base = which ? p.H[0] : 0;
-        const int lo = max(h0 - base, 0), hi = min(h1 - base, p.H[which]);
-        if (lo >= hi) continue;
-        float w[V];
-        load_weights<V>(p, which, lane * V, w);
-        const T *x = static_cast<const T *>(p.x[which]) + b * p.sx[which].b + n * p.sx[which].n + lane * V;
-        T *y = static_cast<T *>(p.y[which]) + ((size_t)b * p.H[which] * p.N + n) * D + lane * V;
-#pragma unroll 1
-        for (int h = lo; h < hi; h += kBatch) {
-            uint4 raw[kBatch];
+        for (int which = 0; which < 2; ++which) {
+            const int base = which ? p.H[0] : 0;
+            const int lo = max(h0 - base, 0), hi = min(h1 - base, p.H[which]);
+            if (lo >= hi) continue;
+            unsigned long long c[V / 2], s[V / 2];
+            {
+                float w[V], wo[V];
+                load_weights<V>(p, which, lane * V, w);
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                raw[i] = live && h + i < hi ? *reinterpret_cast<const uint4 *>(x + (h + i) * p.sx[which].h)
-                                            : make_uint4(0u, 0u, 0u, 0u);
+                for (int e = 0; e < V; ++e) wo[e] = INTER ? w[e ^ 1] : __shfl_sync(0xffffffffu, w[e], turn.src);
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                float v[V];
-                R::unpack(raw[i], v);
-                if (p.normalize) {
-                    float ss = 0.f;
-#pragma unroll
-                    for (int e = 0; e < V; ++e) ss = fmaf(v[e], v[e], ss);
-                    const float r = rsqrtf(row_sum<L>(ss) * (1.f / D) + p.eps);
-#pragma unroll
-                    for (int e = 0; e < V; ++e) v[e] = v[e] * r * w[e];
+                for (int i = 0; i < V / 2; ++i) {
+                    c[i] = pack2(ct[2 * i] * w[2 * i], ct[2 * i + 1] * w[2 * i + 1]);
+                    s[i] = pack2(st[2 * i] * wo[2 * i], st[2 * i + 1] * wo[2 * i + 1]);
                 }
-                turn.apply(v);
-                if (live && h + i < hi) *reinterpret_cast<uint4 *>(y + (size_t)(h + i) * p.N * D) = R::pack(v);
+            }
+            const T *x = static_cast<const T *>(p.x[which]) + b * p.sx[which].b + n * p.sx[which].n + lane * V;
+            T *y = static_cast<T *>(p.y[which]) + ((size_t)b * p.H[which] * p.N + n) * D + lane * V;
+#pragma unroll 1
+            for (int h = lo; h < hi; h += kBatch) {
+                uint4 raw[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i)
+                    raw[i] = live && h + i < hi ? *reinterpret_cast<const uint4 *>(x + (h + i) * p.sx[which].h)
+                                                : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    unsigned long long v[V / 2], o[V / 2];
+                    unpack_row<T>(raw[i], v);
+                    turn.apply(v, raw[i], c, s, o);
+                    if (p.normalize) {
+                        unsigned long long q = 0ull;
+#pragma unroll
+                        for (int e = 0; e < V / 2; ++e) q = fma2(v[e], v[e], q);
+                        const float2 ss = unpack2(q);
+                        const float r = rsqrtf(row_sum<L>(ss.x + ss.y) * (1.f / D) + p.eps);
+#pragma unroll
+                        for (int e = 0; e < V / 2; ++e) o[e] = mul2(o[e], pack2(r, r));
+                    }
+                    if (live && h + i < hi) *reinterpret_cast<uint4 *>(y + (size_t)(h + i) * p.N * D) = pack_row<T>(o);
+                }
             }
         }
     }
 }
 
-// Blocks walk the tokens in strides of the grid and keep their part of the weights' gradients.
+// Blocks walk the tokens in strides of gridDim.x and keep their part of a weight's gradient; blockIdx.y: a share
+// of q's heads (the first y_blocks[0] of them) or of k's.
 template <typename T, int D, bool INTER>
-__global__ void __launch_bounds__(kThreads) k_qk_bwd(QkParams p) {
-    using R = Row<T>;
-    constexpr int V = R::V, L = D / V, kTok = kThreads / L;
+__global__ void __launch_bounds__(kThreads, 2) k_qk_bwd(QkParams p) {
+    constexpr int V = Row<T>::V, L = D / V, kTok = kThreads / L;
     __shared__ float red[kThreads / 32][D];
     pdl_wait();
-    const int lane = threadIdx.x % L;
-    const long long ntok = (long long)p.B * p.N;
-    float dw[2][V];
+    const int lane = threadIdx.x % L, which = (int)blockIdx.y >= p.y_blocks[0];
+    const int h0 = (blockIdx.y - (which ? p.y_blocks[0] : 0)) * p.heads_per_block, h1 = min(h0 + p.heads_per_block, p.H[which]);
+    const unsigned ntok = (unsigned)p.B * p.N;   // below 2^31
+    unsigned long long dw[V / 2], w[V / 2];
+    {
+        float wf[V];
+        load_weights<V>(p, which, lane * V, wf);
 #pragma unroll
-    for (int e = 0; e < V; ++e) dw[0][e] = dw[1][e] = 0.f;
-    for (long long t0 = (long long)blockIdx.x * kTok; t0 < ntok; t0 += (long long)gridDim.x * kTok) {
-        const long long tok = t0 + threadIdx.x / L;
+        for (int i = 0; i < V / 2; ++i) {
+            w[i] = pack2(wf[2 * i], wf[2 * i + 1]);
+            dw[i] = 0ull;
+        }
+    }
+    Turn<T, D, INTER> turn;
+    turn.init(p, lane);
+    const Strides sx = which ? p.sx[1] : p.sx[0], sg = which ? p.sg[1] : p.sg[0];
+    for (unsigned t0 = blockIdx.x * kTok; t0 < ntok; t0 += gridDim.x * kTok) {
+        const unsigned tok = t0 + threadIdx.x / L;
         const bool live = tok < ntok;
-        const int b = live ? (int)(tok / p.N) : 0, n = live ? (int)(tok % p.N) : 0;
-        Turn<T, D, INTER> turn;
-        turn.set(p, b, n, lane, true);
+        const int b = live ? (int)(tok / (unsigned)p.N) : 0, n = live ? (int)(tok - (unsigned)b * p.N) : 0;
+        unsigned long long c[V / 2], s[V / 2];
+        {
+            float ct[V], st[V];
+            turn.at(p, b, n, true, ct, st);
 #pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            float w[V];
-            load_weights<V>(p, which, lane * V, w);
-            const T *x = static_cast<const T *>(p.x[which]) + b * p.sx[which].b + n * p.sx[which].n + lane * V;
-            const T *g = static_cast<const T *>(p.g[which]) + b * p.sg[which].b + n * p.sg[which].n + lane * V;
-            T *y = static_cast<T *>(p.y[which]) + ((size_t)b * p.H[which] * p.N + n) * D + lane * V;
+            for (int i = 0; i < V / 2; ++i) {
+                c[i] = pack2(ct[2 * i], ct[2 * i + 1]);
+                s[i] = pack2(st[2 * i], st[2 * i + 1]);
+            }
+        }
+        const T *x = static_cast<const T *>(which ? p.x[1] : p.x[0]) + b * sx.b + n * sx.n + lane * V;
+        const T *g = static_cast<const T *>(which ? p.g[1] : p.g[0]) + b * sg.b + n * sg.n + lane * V;
+        T *y = static_cast<T *>(which ? p.y[1] : p.y[0]) + ((size_t)b * p.H[which] * p.N + n) * D + lane * V;
 #pragma unroll 1
-            for (int h = 0; h < p.H[which]; h += kBatch) {
-                uint4 rx[kBatch], rg[kBatch];
+        for (int h = h0; h < h1; h += kBatchBwd) {
+            uint4 rx[kBatchBwd], rg[kBatchBwd];
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const bool there = live && h + i < p.H[which];
-                    rg[i] = there ? *reinterpret_cast<const uint4 *>(g + (h + i) * p.sg[which].h) : make_uint4(0u, 0u, 0u, 0u);
-                    rx[i] = there && p.normalize ? *reinterpret_cast<const uint4 *>(x + (h + i) * p.sx[which].h)
-                                                 : make_uint4(0u, 0u, 0u, 0u);
-                }
+            for (int i = 0; i < kBatchBwd; ++i) {
+                const bool there = live && h + i < h1;
+                rg[i] = there ? *reinterpret_cast<const uint4 *>(g + (h + i) * sg.h) : make_uint4(0u, 0u, 0u, 0u);
+                rx[i] = there && p.normalize ? *reinterpret_cast<const uint4 *>(x + (h + i) * sx.h) : make_uint4(0u, 0u, 0u, 0u);
+            }
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    float u[V];
-                    R::unpack(rg[i], u);
-                    turn.apply(u);
-                    if (p.normalize) {
-                        float v[V], ss = 0.f;
-                        R::unpack(rx[i], v);
+            for (int i = 0; i < kBatchBwd; ++i) {
+                const bool there = live && h + i < h1;
+                unsigned long long u[V / 2], gv[V / 2];
+                unpack_row<T>(rg[i], gv);
+                turn.apply(gv, rg[i], c, s, u);
+                if (p.normalize) {
+                    unsigned long long v[V / 2], q = 0ull, m2 = 0ull;
+                    unpack_row<T>(rx[i], v);
 #pragma unroll
-                        for (int e = 0; e < V; ++e) ss = fmaf(v[e], v[e], ss);
-                        const float r = rsqrtf(row_sum<L>(ss) * (1.f / D) + p.eps);
-                        float m = 0.f;
+                    for (int e = 0; e < V / 2; ++e) q = fma2(v[e], v[e], q);
+                    const float2 ss = unpack2(q);
+                    // (rows that are not there are zeros and add nothing)
+                    const float sum = row_sum<L>(ss.x + ss.y), r = there ? rsqrtf(sum * (1.f / D) + p.eps) : 0.f;
+                    const unsigned long long r2 = pack2(r, r);
 #pragma unroll
-                        for (int e = 0; e < V; ++e) {
-                            v[e] *= r;                                  // x r
-                            if (live && h + i < p.H[which]) dw[which][e] = fmaf(u[e], v[e], dw[which][e]);
-                            u[e] *= w[e];
-                            m = fmaf(u[e], v[e], m);
-                        }
-                        m = row_sum<L>(m) * (1.f / D);
-#pragma unroll
-                        for (int e = 0; e < V; ++e) u[e] = r * fmaf(-m, v[e], u[e]);
+                    for (int e = 0; e < V / 2; ++e) {
+                        v[e] = mul2(v[e], r2);                              // x r
+                        dw[e] = fma2(u[e], v[e], dw[e]);
+                        u[e] = mul2(u[e], w[e]);
+                        m2 = fma2(u[e], v[e], m2);
                     }
-                    if (live && h + i < p.H[which]) *reinterpret_cast<uint4 *>(y + (size_t)(h + i) * p.N * D) = R::pack(u);
+                    const float2 mm = unpack2(m2);
+                    const float m = row_sum<L>(mm.x + mm.y) * (-1.f / D);
+                    const unsigned long long mneg = pack2(m, m);
+#pragma unroll
+                    for (int e = 0; e < V / 2; ++e) u[e] = mul2(r2, fma2(mneg, v[e], u[e]));
                 }
+                if (there) *reinterpret_cast<uint4 *>(y + (size_t)(h + i) * p.N * D) = pack_row<T>(u);
             }
         }
     }
     if (!p.part) return;
-    // the block's sums: rows of the warp by shuffles, warps through shared memory
+    // the block's sum: rows of the warp by shuffles, warps through shared memory
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
+    for (int e = 0; e < V; ++e) {
+        const float2 t2 = unpack2(dw[e / 2]);
+        float t = e % 2 ? t2.y : t2.x;
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            float t = dw[which][e];
+        for (int d = L; d < 32; d *= 2) t += __shfl_xor_sync(0xffffffffu, t, d);
+        if (threadIdx.x % 32 < L) red[threadIdx.x / 32][lane * V + e] = t;
+    }
+    __syncthreads();
+    if (threadIdx.x < D) {
+        float t = 0.f;
 #pragma unroll
-            for (int d = L; d < 32; d *= 2) t += __shfl_xor_sync(0xffffffffu, t, d);
-            if (threadIdx.x % 32 < L) red[threadIdx.x / 32][lane * V + e] = t;
-        }
-        __syncthreads();
-        if (threadIdx.x < D) {
-            float t = 0.f;
-#pragma unroll
-            for (int wp = 0; wp < kThreads / 32; ++wp) t += red[wp][threadIdx.x];
-            p.part[((size_t)blockIdx.x * 2 + which) * D + threadIdx.x] = t;
-        }
-        __syncthreads();
+        for (int wp = 0; wp < kThreads / 32; ++wp) t += red[wp][threadIdx.x];
+        p.part[((size_t)blockIdx.y * gridDim.x + blockIdx.x) * D + threadIdx.x] = t;
     }
 }
 
 // dw[which] = sum over the blocks' parts, in a fixed order; blockIdx.x = (which, 32 columns).
 template <typename T>
-__global__ void __launch_bounds__(1024) k_qk_dw(const float *part, int blocks, int D, void *dq_w, void *dk_w, int w_f32) {
+__global__ void __launch_bounds__(1024) k_qk_dw(const float *part, int q_parts, int parts, int D, void *dq_w, void *dk_w,
+                                                int w_f32) {
     __shared__ float red[32][33];
     pdl_wait();
     const int which = blockIdx.x / (D / 32), col = blockIdx.x % (D / 32) * 32 + threadIdx.x % 32, row = threadIdx.x / 32;
     float t = 0.f;
-    for (int i = row; i < blocks; i += 32) t += part[((size_t)i * 2 + which) * D + col];
+    for (int i = (which ? q_parts : 0) + row; i < (which ? parts : q_parts); i += 32) t += part[(size_t)i * D + col];
     red[row][threadIdx.x % 32] = t;
     __syncthreads();
     t = red[threadIdx.x % 32][row];   // a warp per column
@@ -313,12 +430,23 @@ __global__ void __launch_bounds__(1024) k_qk_dw(const float *part, int blocks, i
     }
 }
 
-constexpr int kBwdBlocks = 4 * kPlanSms;   // blocks of the backward at most (about four an SM run at once)
+constexpr int kFwdBlocks = 6 * kPlanSms;   // blocks of the forward at most: two waves, each block with several tokens
+constexpr int kBwdBlocks = 4 * kPlanSms;   // ... and of the backward (two an SM run at once)
 
-int bwd_blocks(int B, int N, int D, la_dtype dt) {
+// The backward's grid: heads in shares of at most 16, tokens over as many blocks as kBwdBlocks leaves.
+struct BwdGrid {
+    int heads, y[2], x;
+};
+BwdGrid bwd_grid(int B, int Hq, int Hkv, int N, int D, la_dtype dt) {
+    BwdGrid g;
+    g.heads = Hq < 16 ? Hq : 16;
+    g.y[0] = (Hq + g.heads - 1) / g.heads;
+    g.y[1] = (Hkv + g.heads - 1) / g.heads;
     const int tok = kThreads / (D / (dt == LA_BF16 ? 8 : 4));
     const long long groups = ((long long)B * N + tok - 1) / tok;
-    return groups < kBwdBlocks ? (int)groups : kBwdBlocks;
+    const int most = kBwdBlocks / (g.y[0] + g.y[1]) > 1 ? kBwdBlocks / (g.y[0] + g.y[1]) : 1;
+    g.x = groups < most ? (int)groups : most;
+    return g;
 }
 
 template <typename T, int D, bool INTER>
@@ -330,22 +458,26 @@ cudaError_t fwd_launch(QkParams &p, cudaStream_t s) {
     int hpb = H;
     while (hpb > kBatch && (long long)groups * ((H + hpb - 1) / hpb) < 2 * kPlanSms) hpb = (hpb + 1) / 2;
     p.heads_per_block = hpb;
+    const unsigned blocks = groups < kFwdBlocks ? groups : kFwdBlocks;
     TraceScope tr("qk_norm_rope_fwd", s);
-    return launch_pdl(k_qk_fwd<T, D, INTER>, dim3(groups, (H + hpb - 1) / hpb), dim3(kThreads), 0, s, p);
+    return launch_pdl(k_qk_fwd<T, D, INTER>, dim3(blocks, (H + hpb - 1) / hpb), dim3(kThreads), 0, s, p);
 }
 
 template <typename T, int D, bool INTER>
 cudaError_t bwd_launch(QkParams &p, void *dqw, void *dkw, cudaStream_t s) {
-    const int blocks = bwd_blocks(p.B, p.N, D, sizeof(T) == 2 ? LA_BF16 : LA_F32);
+    const BwdGrid g = bwd_grid(p.B, p.H[0], p.H[1], p.N, D, sizeof(T) == 2 ? LA_BF16 : LA_F32);
+    p.heads_per_block = g.heads;
+    p.y_blocks[0] = g.y[0];
+    p.y_blocks[1] = g.y[1];
     cudaError_t e;
     {
         TraceScope tr("qk_norm_rope_bwd", s);
-        e = launch_pdl(k_qk_bwd<T, D, INTER>, dim3(blocks), dim3(kThreads), 0, s, p);
+        e = launch_pdl(k_qk_bwd<T, D, INTER>, dim3(g.x, g.y[0] + g.y[1]), dim3(kThreads), 0, s, p);
     }
     if (e != cudaSuccess || !p.part) return e;
     TraceScope tr("qk_norm_rope_dw", s);
-    return launch_pdl(k_qk_dw<T>, dim3(2 * (D / 32)), dim3(1024), 0, s, static_cast<const float *>(p.part), blocks, D, dqw,
-                      dkw, p.w_f32);
+    return launch_pdl(k_qk_dw<T>, dim3(2 * (D / 32)), dim3(1024), 0, s, static_cast<const float *>(p.part), g.x * g.y[0],
+                      g.x * (g.y[0] + g.y[1]), D, dqw, dkw, p.w_f32);
 }
 
 template <typename T, int D>
@@ -454,7 +586,8 @@ extern "C" {
 
 size_t la_qk_norm_rope_workspace_size(int B, int Hq, int Hkv, int N, int D, la_dtype dtype) {
     if (check_sizes(B, Hq, Hkv, N, D, dtype) != LA_OK) return 0;
-    return (size_t)bwd_blocks(B, N, D, dtype) * 2 * D * sizeof(float);
+    const BwdGrid g = bwd_grid(B, Hq, Hkv, N, D, dtype);
+    return (size_t)g.x * (g.y[0] + g.y[1]) * D * sizeof(float);
 }
 
 la_status la_qk_norm_rope_fwd(const void *q, const void *k, void *q_out, void *k_out, int B, int Hq, int Hkv, int N,

@@ -17,6 +17,7 @@ fails, an exception says why.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -403,8 +404,67 @@ def decay_kernel_path(B, Hq, Hkv, N, D, dtype: torch.dtype, is_bwd: bool, Dv: in
     return int(load().la_decay_kernel_path(B, Hq, Hkv, N, D, D if Dv is None else Dv, code, int(is_bwd)))
 
 
+# The calls below can be as short as a few microseconds on the GPU, so their marshalling is kept small: addresses
+# go as plain ints, sizes and strides that were asked for before come from caches (pure functions of their
+# arguments), and the checks are one expression that names the culprit only when it fails.
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream):
+    return _current_stream() if stream is None else stream.cuda_stream
+
+
+# torch's current stream as an integer, without a Stream object (2.8 of a call's 15 us) where torch has that
+_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _current_stream():
+    return torch.cuda.current_stream().cuda_stream if _raw is None else _raw(torch.cuda.current_device())
+
+
+@functools.lru_cache(maxsize=256)
+def _strides_of(b, h, n):
+    return ctypes.pointer(LaStrides(b, h, n))
+
+
+def _stride_arg(t):
+    return None if t.is_contiguous() else _strides_of(*t.stride()[:3])
+
+
+@functools.lru_cache(maxsize=256)
+def _decay_need(B, Hq, Hkv, N, D, Dv, dt, is_bwd):
+    return int(load().la_decay_workspace_size(B, Hq, Hkv, N, D, Dv, dt, is_bwd))
+
+
+@functools.lru_cache(maxsize=256)
+def _qk_need(B, Hq, Hkv, N, D, dt):
+    return int(load().la_qk_norm_rope_workspace_size(B, Hq, Hkv, N, D, dt))
+
+
+def _rows_ok(t, dtype):
+    """A [B, H, N, D] CUDA tensor of this dtype with D contiguous."""
+    return t.is_cuda and t.dtype == dtype and t.dim() == 4 and (t.stride(3) == 1 or t.shape[3] == 1)
+
+
+def _check_qkv(q, k, v, *extra):
+    """(B, Hq, Hkv, N, D, Dv), as _check_inputs (which raises when something is wrong)."""
+    try:
+        dt = q.dtype
+        ok = _rows_ok(q, dt) and _rows_ok(k, dt) and _rows_ok(v, dt) and all(_rows_ok(t, dt) for t in extra)
+        if ok:
+            B, Hq, N, D = q.shape
+            _, Hkv, Nk, Dk = k.shape
+            Dv = v.shape[3]
+            if Nk == N and Dk == D and k.shape[0] == B and v.shape[:3] == k.shape[:3]:
+                return B, Hq, Hkv, N, D, Dv
+    except AttributeError:
+        pass
+    return _check_inputs(q, k, v, None, None, tuple(("grad_out", t) for t in extra))
+
+
 def _check_vector(name, t, n, dtype, device):
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or t.shape != (n,) \
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or t.dim() != 1 or t.shape[0] != n \
             or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} vector of {n} elements on q's device")
 
@@ -417,7 +477,7 @@ def _check_state(name, t, shape, device):
 
 def _output(name, t, shape, like):
     if t is None:
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
+        return like.new_empty(shape)
     if tuple(t.shape) != tuple(shape) or t.dtype != like.dtype or t.device != like.device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor of q's dtype on q's device")
     return t
@@ -439,7 +499,7 @@ def decay_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torc
     each sequence; out rows past them are zeros and what the inputs hold there is not used.
     Returns ``out`` [B, Hq, N, Dv]."""
     lib = load()
-    B, Hq, Hkv, N, D, Dv = _check_inputs(q, k, v, None, None)
+    B, Hq, Hkv, N, D, Dv = _check_qkv(q, k, v)
     dev, dt = q.device, _dtype_code(q)
     _check_vector("log_decay", log_decay, Hkv, torch.float32, dev)
     if lengths is not None:
@@ -448,10 +508,10 @@ def decay_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torc
         if t is not None:
             _check_state(name, t, (B, Hkv, D, Dv), dev)
     out = _output("out", out, (B, Hq, N, Dv), q)
-    ws = _workspace(lib.la_decay_workspace_size(B, Hq, Hkv, N, D, Dv, dt, 0), dev, workspace)
-    st = lib.la_decay_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(log_decay), _ptr(initial_state),
-                          _ptr(final_state), _ptr(lengths), B, Hq, Hkv, N, D, Dv, dt, scale, _strides(q), _strides(k),
-                          _strides(v), _ptr(ws), _nbytes(ws), _stream_handle(stream))
+    ws = _workspace(_decay_need(B, Hq, Hkv, N, D, Dv, dt, 0), dev, workspace)
+    st = lib.la_decay_fwd(_addr(q), _addr(k), _addr(v), _addr(out), _addr(log_decay), _addr(initial_state),
+                          _addr(final_state), _addr(lengths), B, Hq, Hkv, N, D, Dv, dt, scale, _stride_arg(q), _stride_arg(k),
+                          _stride_arg(v), _addr(ws), _nbytes(ws), _raw_stream(stream))
     if st != LA_OK:
         _raise(lib, st, "la_decay_fwd")
     return out
@@ -467,7 +527,7 @@ def decay_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, grad_out: torch
     final state (None: zeros); ``grad_initial_state``, when given, receives the initial state's.
     ``log_decay`` gets no gradient."""
     lib = load()
-    B, Hq, Hkv, N, D, Dv = _check_inputs(q, k, v, None, None, (("grad_out", grad_out),))
+    B, Hq, Hkv, N, D, Dv = _check_qkv(q, k, v, grad_out)
     if tuple(grad_out.shape) != (B, Hq, N, Dv):
         raise ValueError("grad_out must have the shape of out ([B, Hq, N, Dv])")
     dev, dt = q.device, _dtype_code(q)
@@ -477,11 +537,11 @@ def decay_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, grad_out: torch
         if t is not None:
             _check_state(name, t, (B, Hkv, D, Dv), dev)
     dq, dk, dv = _output("dq", dq, q.shape, q), _output("dk", dk, k.shape, q), _output("dv", dv, v.shape, q)
-    ws = _workspace(lib.la_decay_workspace_size(B, Hq, Hkv, N, D, Dv, dt, 1), dev, workspace)
-    st = lib.la_decay_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(grad_out), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(log_decay),
-                          _ptr(initial_state), _ptr(grad_final_state), _ptr(grad_initial_state), B, Hq, Hkv, N, D, Dv,
-                          dt, scale, _strides(q), _strides(k), _strides(v), _strides(grad_out), _ptr(ws), _nbytes(ws),
-                          _stream_handle(stream))
+    ws = _workspace(_decay_need(B, Hq, Hkv, N, D, Dv, dt, 1), dev, workspace)
+    st = lib.la_decay_bwd(_addr(q), _addr(k), _addr(v), _addr(grad_out), _addr(dq), _addr(dk), _addr(dv), _addr(log_decay),
+                          _addr(initial_state), _addr(grad_final_state), _addr(grad_initial_state), B, Hq, Hkv, N, D, Dv,
+                          dt, scale, _stride_arg(q), _stride_arg(k), _stride_arg(v), _stride_arg(grad_out), _addr(ws), _nbytes(ws),
+                          _raw_stream(stream))
     if st != LA_OK:
         _raise(lib, st, "la_decay_bwd")
     return dq, dk, dv
@@ -496,7 +556,7 @@ def decay_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, state: torch.T
     zeros, no state touched).  The new states go to ``state_out`` at the same slots (None: into
     ``state``).  Returns ``out`` [B, Hq, 1, Dv]."""
     lib = load()
-    B, Hq, Hkv, N, D, Dv = _check_inputs(q, k, v, None, None)
+    B, Hq, Hkv, N, D, Dv = _check_qkv(q, k, v)
     if N != 1:
         raise ValueError(f"decay_step takes one token per sequence (N = 1), got N = {N}")
     dev = q.device
@@ -508,16 +568,24 @@ def decay_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, state: torch.T
     if state_out is not None:
         _check_state("state_out", state_out, (pool, Hkv, D, Dv), dev)
     out = _output("out", out, (B, Hq, 1, Dv), q)
-    st = lib.la_decay_step(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(state),
-                           _ptr(state if state_out is None else state_out), _ptr(log_decay), _ptr(slots), pool, B, Hq,
-                           Hkv, D, Dv, _dtype_code(q), scale, _strides(q), _strides(k), _strides(v),
-                           _stream_handle(stream))
+    st = lib.la_decay_step(_addr(q), _addr(k), _addr(v), _addr(out), _addr(state),
+                           _addr(state if state_out is None else state_out), _addr(log_decay), _addr(slots), pool, B, Hq,
+                           Hkv, D, Dv, _dtype_code(q), scale, _stride_arg(q), _stride_arg(k), _stride_arg(v),
+                           _raw_stream(stream))
     if st != LA_OK:
         _raise(lib, st, "la_decay_step")
     return out
 
 
 def _check_qk(q, k, extra=()):
+    try:
+        dt = q.dtype
+        if _rows_ok(q, dt) and _rows_ok(k, dt) and all(_rows_ok(t, dt) for _, t in extra):
+            B, Hq, N, D = q.shape
+            if k.shape[0] == B and k.shape[2] == N and k.shape[3] == D:
+                return B, Hq, k.shape[1], N, D
+    except AttributeError:
+        pass
     for name, t in (("q", q), ("k", k)) + tuple(extra):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
@@ -588,8 +656,8 @@ def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, *, q_weight: torch.Tensor
     B, Hq, Hkv, N, D = _check_qk(q, k)
     a = _qk_args(q, q_weight, k_weight, eps, positions, inv_freq, sections, interleaved, normalize)
     q_out, k_out = _output("q_out", q_out, q.shape, q), _output("k_out", k_out, k.shape, q)
-    st = lib.la_qk_norm_rope_fwd(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), B, Hq, Hkv, N, D, _dtype_code(q),
-                                 _strides(q), _strides(k), ctypes.byref(a), _stream_handle(stream))
+    st = lib.la_qk_norm_rope_fwd(_addr(q), _addr(k), _addr(q_out), _addr(k_out), B, Hq, Hkv, N, D, _dtype_code(q),
+                                 _stride_arg(q), _stride_arg(k), ctypes.byref(a), _raw_stream(stream))
     if st != LA_OK:
         _raise(lib, st, "la_qk_norm_rope_fwd")
     return q_out, k_out
@@ -618,10 +686,10 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, grad_q: torch.Tensor, gra
     dkw = torch.empty_like(k_weight) if k_weight is not None else None
     dt, ws = _dtype_code(q), None
     if dqw is not None or dkw is not None:
-        ws = _workspace(lib.la_qk_norm_rope_workspace_size(B, Hq, Hkv, N, D, dt), q.device, workspace)
-    st = lib.la_qk_norm_rope_bwd(_ptr(q), _ptr(k), _ptr(grad_q), _ptr(grad_k), _ptr(dq), _ptr(dk), _ptr(dqw),
-                                 _ptr(dkw), B, Hq, Hkv, N, D, dt, _strides(q), _strides(k), _strides(grad_q),
-                                 _strides(grad_k), ctypes.byref(a), _ptr(ws), _nbytes(ws), _stream_handle(stream))
+        ws = _workspace(_qk_need(B, Hq, Hkv, N, D, dt), q.device, workspace)
+    st = lib.la_qk_norm_rope_bwd(_addr(q), _addr(k), _addr(grad_q), _addr(grad_k), _addr(dq), _addr(dk), _addr(dqw),
+                                 _addr(dkw), B, Hq, Hkv, N, D, dt, _stride_arg(q), _stride_arg(k), _stride_arg(grad_q),
+                                 _stride_arg(grad_k), ctypes.byref(a), _addr(ws), _nbytes(ws), _raw_stream(stream))
     if st != LA_OK:
         _raise(lib, st, "la_qk_norm_rope_bwd")
     return dq, dk, dqw, dkw
