@@ -11,16 +11,17 @@
 // relative) and both are multiplied; one rounding would leave 2^-9 there.  Where the state only reaches bf16
 // outputs it is rounded once, as P, S_bf and the decayed X are.
 //
-// Operands made by the CUDA cores are read by the MMA from TMEM: P and the decayed X take the place of the
-// scores (each warp of P puts its half over columns that its thread has read, the decayed X fills the rest),
-// Y^T has columns of its own.  That leaves the shared memory to the TMA tiles, the output tile and S_bf, and
-// halves the MMA's own shared-memory reads, which at 128 x 128 x 16 from shared memory would take all of its
-// bandwidth.  TMEM columns: S, O, scores / P / X, Y^T hi | lo.
+// Operands made by the CUDA cores are read by the MMA from TMEM where it has room: P and the decayed X take the place
+// of the scores (P over columns that its thread has read, the decayed X over the rest when P is done), Y^T has columns
+// of its own.  That halves the MMA's shared-memory reads, which at 128 x 128 x 16 from shared memory would
+// take all of its bandwidth, and leaves the shared memory to the TMA tiles.  The scores have two buffers, so that the
+// next item's scores and P run beside this one's O; where S and O are 128 columns wide that takes Y^T's place, and y is
+// decayed in its tile instead (in one term: with a state as output, in two, the scores have one buffer).
 // Several heads of x share one chunk of y, z (grouped queries; S moves on after the last), or several heads
 // of y, z share one of x (their gradients; O and S sum over the heads).
 //
-// Warps: 0 TMA, 1 MMA of scores and O, 2 MMA of S, 4-11 P (columns in two halves), 12-15 S -> S_bf and the decay of S,
-// 16-19 the decayed X and the output rows, 20-23 Y^T (and the zeros past a sequence's length).
+// Warps: 0 TMA, 1 MMA of scores and O, 2 MMA of S, 4-7 P, 8-11 S -> S_bf and the decay of S, 12-15 the decayed X,
+// 16-19 the output rows, 20-23 the decayed y (and the zeros past a sequence's length).
 //
 // The reverse passes (gradients of k and v) take the same steps with j >= i and gamma^(j-i), chunks from the
 // last to the first.
@@ -36,7 +37,22 @@ constexpr int kMainThreads = 768;
 // Bounded warp-uniform wait.  What follows a wait that does not end at once is out of line: the kernels have some
 // twenty waits, and their code has to stay in the instruction caches that all roles share.
 __device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    return (*abort == 0) && mbar_wait(bar, parity, abort);
+    uint64_t t0 = 0;
+    for (;;) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)   // (each may suspend the warp)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
+        const uint64_t t = globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > kWaitNs) {
+            *abort = 1;
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool is_over(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_test(bar, parity));
 }
 __device__ __forceinline__ bool await(uint64_t *bar, uint32_t parity, volatile int *abort) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
@@ -47,16 +63,24 @@ struct PassMaps {
     CUtensorMap m[3][4];   // per pass: x, y, z, out
 };
 
-template <int DX, int DZ>
+// YSM: y is decayed in place in shared memory (else Y^T is made in TMEM, one or two terms).
+template <int DX, int DZ, bool YSM>
 struct MainCfg {
-    static constexpr int X_BYTES = C * DX * 2, Y_BYTES = C * DX * 2, Z_BYTES = C * DZ * 2, O_BYTES = C * DZ * 2;
-    static constexpr int S_BYTES = DX * DZ * 2;
-    // stages of each: y goes first (scores and Y^T have it read early in the chunk), z last
-    static constexpr int NX = DX == 64 ? 4 : 2, NY = DX == 64 || DZ == 64 ? 2 : 1, NZ = DZ == 64 ? 4 : 2;
-    static constexpr int NO = DX == 64 && DZ == 64 ? 2 : 1;
+    static constexpr int X_BYTES = C * DX * 2, Y_BYTES = C * DX * 2, Z_BYTES = C * DZ * 2, S_BYTES = DX * DZ * 2;
+    static constexpr int O_BYTES = C * DZ * 2;
+    static constexpr int NX = DX == 64 ? 4 : 2;
+    static constexpr int NY = YSM ? (DX == 64 ? 3 : 2) : DZ == 64 ? (DX == 64 ? 3 : 2) : (DX == 64 ? 2 : 1);
+    static constexpr int NZ = DZ == 64 ? 4 : YSM && DX == 64 ? 3 : 2;
+    // output tiles: of their own; with YSM in the z tile that is used up or, where several heads share it, in place of
+    // y's other stages (which such a block needs less: a y tile serves all of them)
+    static constexpr int NO = YSM ? 0 : DX == 64 && DZ == 64 ? 2 : 1;
     static constexpr int SMEM = NX * X_BYTES + NY * Y_BYTES + NZ * Z_BYTES + NO * O_BYTES + S_BYTES + 1024;
     static_assert(SMEM + 2048 <= kSmemLimit, "tiles, barriers and tables");
-    static constexpr int T_S = 0, T_O = 128, T_A = 256, T_YH = 384, T_YL = 448;
+    static_assert(!YSM || (NY - 1) * Y_BYTES >= O_BYTES, "an output tile in y's other stages");
+    // TMEM: S, O, one or two buffers of scores, Y^T hi | lo
+    static constexpr int NSC = DZ == 64 || YSM ? 2 : 1;
+    static constexpr int T_S = 0, T_O = DZ, T_A = 2 * DZ, T_YH = T_A + 128 * NSC, T_YL = T_YH + 64;
+    static_assert((YSM ? T_YH : T_YL + 64) <= 512, "TMEM columns");
 };
 
 // A block's part of the sequence: tokens [lo, hi), `before` tokens of the sequence precede it in the pass's
@@ -166,23 +190,26 @@ __device__ __forceinline__ void zero_rows(uint8_t *tile, int valid, int i, int n
         *reinterpret_cast<uint4 *>(tile + swz_chunk(C, valid + idx / (W / 8), idx % (W / 8))) = make_uint4(0u, 0u, 0u, 0u);
 }
 
-template <int DX, int DZ>
+template <int DX, int DZ, bool YSM>
 __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_constant__ PassMaps maps,
                                                               const __grid_constant__ DecayParams p, int pass0,
                                                               int npass) {
-    using K = MainCfg<DX, DZ>;
-    constexpr int NX = K::NX, NY = K::NY, NZ = K::NZ;
+    using K = MainCfg<DX, DZ, YSM>;
+    constexpr int NX = K::NX, NYS = K::NY, NZ = K::NZ, NSC = K::NSC, NO = K::NO;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t x_full[NX], x_empty[NX], y_full[NY], y_empty[NY], z_full[NZ], z_empty[NZ];
-    __shared__ uint64_t sc_full, p_ready, p_first, xd_ready, o_full, o_free, s_full, s_conv, yt_ready, yt_done, zeroed, fin[2];
+    __shared__ uint64_t x_full[NX], x_empty[NX], y_full[NYS], y_empty[NYS], z_full[NZ], z_empty[NZ];
+    // of one buffer of the scores: in, P made; by output tile: P of its first scores made, decayed X made
+    __shared__ uint64_t sc_full[NSC], p_ready[NSC], p_first[2], xd_ready[2];
+    __shared__ uint64_t y_scored[NYS], yt_ready[NYS];   // of a stage of y: its scores done, its decayed form made
+    __shared__ uint64_t o_full, o_free, s_full, s_conv, yt_done, z_used[2], zeroed, fin[2];
     __shared__ __align__(16) float pw[C + 4], wtab[2][C];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
     uint8_t *xbuf = align1024(smem_raw);
     uint8_t *ybuf = xbuf + NX * K::X_BYTES;
-    uint8_t *zbuf = ybuf + NY * K::Y_BYTES;
-    uint8_t *obuf = zbuf + NZ * K::Z_BYTES;
-    uint8_t *sbf = obuf + K::NO * K::O_BYTES;
+    uint8_t *zbuf = ybuf + NYS * K::Y_BYTES;
+    uint8_t *sbf = zbuf + NZ * K::Z_BYTES;
+    uint8_t *obuf = YSM ? ybuf + K::Y_BYTES : sbf + K::S_BYTES;
 
     pdl_wait();
     const int warp = threadIdx.x / 32;
@@ -190,6 +217,8 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
     const DecayPass &ps = p.pass[pi];
     const int u = rest % p.nseg, bg = rest / p.nseg, b = bg / p.Hkv, h = bg % p.Hkv;
     const int n = decay_tokens(p.lengths, b, p.N), rev = ps.rev, many = ps.many_yz, reps = p.n_rep;
+    const int NY = YSM && !many && reps > 1 ? 1 : NYS;        // stages of y in use
+    const bool o_in_z = YSM && (many || reps == 1);           // output tiles are staged in z's
     const Part part = part_of(n, p.N, u, p.nseg, p.seg_len, rev);
     const int nchunk = (part.hi - part.lo + C - 1) / C;
     const int off0 = u == 0 ? ps.first_off : 0;   // of the first chunk
@@ -202,26 +231,33 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         abort_flag = 0;
         for (int s = 0; s < NX; ++s) {
             mbar_init(&x_full[s], 1);
-            mbar_init(&x_empty[s], 8 + 4);   // warps of P (the scores are over), of the decayed X
+            mbar_init(&x_empty[s], 4 + 4);             // warps of P (the scores are over), of the decayed X
         }
-        for (int s = 0; s < NY; ++s) {
+        for (int s = 0; s < NYS; ++s) {
             mbar_init(&y_full[s], 1);
-            mbar_init(&y_empty[s], 8 + 4);   // warps of P, of Y^T
+            mbar_init(&y_empty[s], YSM ? 1 : 4 + 4);   // S's MMA, or warps of P, of Y^T
+            mbar_init(&y_scored[s], 1);
+            mbar_init(&yt_ready[s], 128);
         }
         for (int s = 0; s < NZ; ++s) {
             mbar_init(&z_full[s], 1);
-            mbar_init(&z_empty[s], 2);
+            mbar_init(&z_empty[s], YSM ? 2 + 4 : 2);   // both MMA warps (and the warps that store the output)
         }
-        mbar_init(&sc_full, 1);
-        mbar_init(&p_ready, 256);
-        mbar_init(&p_first, 256);
-        mbar_init(&xd_ready, 128);
+        for (int s = 0; s < NSC; ++s) {
+            mbar_init(&sc_full[s], 1);
+            mbar_init(&p_ready[s], 128);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&p_first[s], 128);
+            mbar_init(&xd_ready[s], 128);
+        }
         mbar_init(&o_full, 1);
         mbar_init(&o_free, 128);
         mbar_init(&s_full, 2);
         mbar_init(&s_conv, 128);
-        mbar_init(&yt_ready, 128);
         mbar_init(&yt_done, 1);
+        mbar_init(&z_used[0], 1);
+        mbar_init(&z_used[1], 1);
         mbar_init(&zeroed, 128);
         mbar_init(&fin[0], 1);
         mbar_init(&fin[1], 1);
@@ -242,154 +278,184 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
     tc_fence_after();
     const uint32_t tm = tmem_base;
     const int items = nchunk * reps;
-    const bool exact = ps.fin != nullptr;   // the state is an output
+    const bool exact = !YSM && ps.fin != nullptr;   // the state is an output
 
-    if (warp < 4) {
-        if (warp == 0) {
-            // ---------------- TMA producer.  y waits for the scores before it where it has one stage, so x and z go first
-            const CUtensorMap *mx = &maps.m[pi][0], *my = &maps.m[pi][1], *mz = &maps.m[pi][2];
-            int nx = 0, nyz = 0, nz = 0;   // issued (z is one ahead of y when a wait for y gives up)
-            bool ok = true;
-            for (int k = 0; ok && k < nchunk; ++k) {
-                const int c0 = chunk0(k);
-                for (int r = 0; ok && r < reps; ++r) {
-                    const int hq = h * reps + r;
-                    if (r == 0 || !many) {
-                        const int s = nx % NX;
-                        if (nx >= NX && !await(&x_empty[s], (nx / NX - 1) & 1, &abort_flag)) { ok = false; break; }
-                        uint8_t *x = xbuf + s * K::X_BYTES;
-                        if (elect_one()) {
-                            mbar_arrive_expect_tx(&x_full[s], K::X_BYTES);
+    if (warp == 0) {
+        // ---------------- TMA producer
+        const CUtensorMap *mx = &maps.m[pi][0], *my = &maps.m[pi][1], *mz = &maps.m[pi][2];
+        int nx = 0, ny = 0, nz = 0;
+        bool ok = true;
+        for (int k = 0; ok && k < nchunk; ++k) {
+            const int c0 = chunk0(k);
+            for (int r = 0; ok && r < reps; ++r) {
+                const int hq = h * reps + r, hyz = many ? hq : h;
+                if (r == 0 || !many) {
+                    const int s = nx % NX;
+                    if (nx >= NX && !await(&x_empty[s], (nx / NX - 1) & 1, &abort_flag)) { ok = false; break; }
+                    uint8_t *x = xbuf + s * K::X_BYTES;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&x_full[s], K::X_BYTES);
 #pragma unroll
-                            for (int blk = 0; blk < DX / 64; ++blk)
-                                tma_load_4d(x + blk * C * 128, mx, &x_full[s], blk * 64, c0, many ? h : hq, b);
-                        }
-                        __syncwarp();
-                        ++nx;
+                        for (int blk = 0; blk < DX / 64; ++blk)
+                            tma_load_4d(x + blk * C * 128, mx, &x_full[s], blk * 64, c0, many ? h : hq, b);
                     }
-                    if (r == 0 || many) {
-                        const int hyz = many ? hq : h, sz = nyz % NZ, sy = nyz % NY;
-                        if (nyz >= NZ && !await(&z_empty[sz], (nyz / NZ - 1) & 1, &abort_flag)) { ok = false; break; }
-                        uint8_t *z = zbuf + sz * K::Z_BYTES, *y = ybuf + sy * K::Y_BYTES;
-                        if (elect_one()) {
-                            mbar_arrive_expect_tx(&z_full[sz], K::Z_BYTES);
-#pragma unroll
-                            for (int blk = 0; blk < DZ / 64; ++blk) tma_load_4d(z + blk * C * 128, mz, &z_full[sz], blk * 64, c0, hyz, b);
-                        }
-                        __syncwarp();
-                        ++nz;
-                        if (nyz >= NY && !await(&y_empty[sy], (nyz / NY - 1) & 1, &abort_flag)) { ok = false; break; }
-                        if (elect_one()) {
-                            mbar_arrive_expect_tx(&y_full[sy], K::Y_BYTES);
-#pragma unroll
-                            for (int blk = 0; blk < DX / 64; ++blk) tma_load_4d(y + blk * C * 128, my, &y_full[sy], blk * 64, c0, hyz, b);
-                        }
-                        __syncwarp();
-                        ++nyz;
-                    }
-                }
-            }
-            for (int i = nx > NX ? nx - NX : 0; i < nx; ++i) warp_drain(&x_full[i % NX], (i / NX) & 1);
-            for (int i = nyz > NY ? nyz - NY : 0; i < nyz; ++i) warp_drain(&y_full[i % NY], (i / NY) & 1);
-            for (int i = nz > NZ ? nz - NZ : 0; i < nz; ++i) warp_drain(&z_full[i % NZ], (i / NZ) & 1);
-        } else if (warp == 1) {
-            // ---------------- scores, then O = P Z (+ the decayed X times S_bf, once for each output tile).  This warp's
-            // MMAs run in the order of their issue, so the next scores cannot overtake P and X
-            constexpr uint32_t idA = idesc_bf16(128, C, false, false);
-            constexpr uint32_t idO = idesc_bf16(128, DZ, false, true);
-            const uint32_t tO = tm + K::T_O, tA = tm + K::T_A, sb = smem_u32(sbf);
-            int ix = 0, iy = 0, ot = 0, k = 0, r = 0;   // x tile, y z tile, output tile, chunk, head
-            for (int it = 0; it < items; ++it) {
-                const bool first = r == 0, last = r == reps - 1;
-                const bool opens = first || !many, ends = last || !many;   // an output tile
-                if (opens && !await(&x_full[ix % NX], (ix / NX) & 1, &abort_flag)) break;
-                if ((first || many) && !await(&y_full[iy % NY], (iy / NY) & 1, &abort_flag)) break;
-                const uint32_t x = smem_u32(xbuf + (ix % NX) * K::X_BYTES);
-                const uint32_t y = smem_u32(ybuf + (iy % NY) * K::Y_BYTES), z = smem_u32(zbuf + (iy % NZ) * K::Z_BYTES);
-                // a tile with rows past the sequence's length (its last): those are zeroed first
-                if (p.lengths && first && k == nchunk - 1 && vlast < C && !await(&zeroed, 0, &abort_flag)) break;
-                tc_fence_after();
-                LA_TL(it, 0);
-                if (elect_one()) {
-                    mma_ss_kk<DX / 16>(tA, desc_kmajor(x, C, 0, 0), desc_kmajor(y, C, 0, 0), idA);
-                    mma_commit(&sc_full);
-                }
-                __syncwarp();
-                LA_TL(it, 1);
-                if (opens && ot > 0 && !await(&o_free, (ot - 1) & 1, &abort_flag)) break;
-                LA_TL(it, 2);
-                if ((first || many) && !await(&z_full[iy % NZ], (iy / NZ) & 1, &abort_flag)) break;
-                if (!await(&p_ready, it & 1, &abort_flag)) break;
-                LA_TL(it, 4);
-                tc_fence_after();
-                if (elect_one()) mma_ts_mn<C / 16, 4>(tO, tA, desc_mnmajor(z, C, 0, 0), idO, opens ? 0u : 1u);
-                __syncwarp();
-                if (opens) {
-                    if (!await(&xd_ready, ot & 1, &abort_flag)) break;
-                    if (first && !await(&s_conv, k & 1, &abort_flag)) break;
-                    LA_TL(it, 5);
-                    tc_fence_after();
-                    if (elect_one()) mma_ts_mn<DX / 16, 4>(tO, tA + 32, desc_mnmajor(sb, DX, 0, 0), idO, 1u);
                     __syncwarp();
+                    ++nx;
                 }
-                if (elect_one()) {
-                    if (ends) mma_commit(&o_full);
-                    if (many ? first : last) mma_commit(&s_full);   // the chunk's last reader of S_bf
-                    if (last || many) mma_commit(&z_empty[iy % NZ]);
-                }
-                __syncwarp();
-                if (ends) {
-                    ++ot;
-                    ++ix;
-                }
-                if (last || many) ++iy;
-                LA_TL(it, 6);
-                if (++r == reps) {
-                    r = 0;
-                    ++k;
-                }
-            }
-            if (elect_one()) mma_commit(&fin[0]);
-            __syncwarp();
-            warp_drain(&fin[0], 0);
-        } else if (warp == 2) {
-            // ---------------- S += Y^T Z, once for each y z tile
-            constexpr uint32_t idS = idesc_bf16(128, DZ, false, true);
-            const uint32_t tS = tm + K::T_S, tYh = tm + K::T_YH, tYl = tm + K::T_YL;
-            const int tiles = many ? items : nchunk, per = many ? reps : 1;
-            int k = 0, r = 0;
-            for (int t = 0; t < tiles; ++t) {
-                if (r == 0 && !await(&s_conv, k & 1, &abort_flag)) break;
-                if (!await(&z_full[t % NZ], (t / NZ) & 1, &abort_flag)) break;
-                if (!await(&yt_ready, t & 1, &abort_flag)) break;
-                LA_TL(t, 3);
-                tc_fence_after();
-                const uint32_t z = smem_u32(zbuf + (t % NZ) * K::Z_BYTES);
-                const bool ends = ++r == per;
-                if (elect_one()) {
-                    mma_ts_mn<C / 16>(tS, tYh, desc_mnmajor(z, C, 0, 0), idS, 1u);
-                    if (exact) mma_ts_mn<C / 16>(tS, tYl, desc_mnmajor(z, C, 0, 0), idS, 1u);
-                    mma_commit(&yt_done);
-                    mma_commit(&z_empty[t % NZ]);
-                    if (ends) mma_commit(&s_full);
-                }
-                __syncwarp();
-                if (ends) {
-                    r = 0;
-                    ++k;
+                if (r == 0 || many) {
+                    const int s = ny % NY;
+                    if (ny >= NY && !await(&y_empty[s], (ny / NY - 1) & 1, &abort_flag)) { ok = false; break; }
+                    uint8_t *y = ybuf + s * K::Y_BYTES;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&y_full[s], K::Y_BYTES);
+#pragma unroll
+                        for (int blk = 0; blk < DX / 64; ++blk) tma_load_4d(y + blk * C * 128, my, &y_full[s], blk * 64, c0, hyz, b);
+                    }
+                    __syncwarp();
+                    ++ny;
+                    const int sz = nz % NZ;
+                    if (nz >= NZ && !await(&z_empty[sz], (nz / NZ - 1) & 1, &abort_flag)) { ok = false; break; }
+                    uint8_t *z = zbuf + sz * K::Z_BYTES;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&z_full[sz], K::Z_BYTES);
+#pragma unroll
+                        for (int blk = 0; blk < DZ / 64; ++blk) tma_load_4d(z + blk * C * 128, mz, &z_full[sz], blk * 64, c0, hyz, b);
+                    }
+                    __syncwarp();
+                    ++nz;
                 }
             }
-            if (elect_one()) mma_commit(&fin[1]);
-            __syncwarp();
-            warp_drain(&fin[1], 0);
         }
-    } else if (warp < 12) {
-        // ---------------- P = bf16(scale A o W), thread = (row i, half of the columns), 32 columns at a time.  Away from
-        // the diagonal gamma^|i - j| = gamma^(distance to the near end of a block of 16) gamma^(distance in the block); on
-        // it the blocks of 16 have the lower (reverse: upper) triangle of one pattern, or are such a full block, or
-        // nothing.  Both patterns stay in registers, with `scale`
-        const int wq = warp % 4, lane = threadIdx.x % 32, i = wq * 32 + lane, hc = (warp - 4) / 4;
-        const uint32_t ta = tm + K::T_A + hc * 64 + ((uint32_t)(wq * 32) << 16);
+        for (int i = nx > NX ? nx - NX : 0; i < nx; ++i) warp_drain(&x_full[i % NX], (i / NX) & 1);
+        for (int i = ny > NY ? ny - NY : 0; i < ny; ++i) warp_drain(&y_full[i % NY], (i / NY) & 1);
+        for (int i = nz > NZ ? nz - NZ : 0; i < nz; ++i) warp_drain(&z_full[i % NZ], (i / NZ) & 1);
+    } else if (warp == 1) {
+        // ---------------- scores, and O = P Z (+ the decayed X times S_bf, once for each output tile).  With two
+        // buffers the scores of the next item go ahead of this one's O where their tiles are in.  This warp's MMAs
+        // run in the order of their issue, so scores cannot overtake the P and X that they replace
+        constexpr uint32_t idA = idesc_bf16(128, C, false, false);
+        constexpr uint32_t idO = idesc_bf16(128, DZ, false, true);
+        const uint32_t tO = tm + K::T_O, sb = smem_u32(sbf);
+        int sx = 0, sy = 0, sk = 0, sr = 0, si = 0;   // of the next scores: x tile, y tile, chunk, head, item
+        auto scores_in = [&]() {
+            return is_over(&x_full[sx % NX], (sx / NX) & 1) && is_over(&y_full[sy % NY], (sy / NY) & 1);
+        };
+        auto scores = [&]() -> bool {
+            const bool first = sr == 0, last = sr == reps - 1;
+            if ((first || !many) && !await(&x_full[sx % NX], (sx / NX) & 1, &abort_flag)) return false;
+            if ((first || many) && !await(&y_full[sy % NY], (sy / NY) & 1, &abort_flag)) return false;
+            // a tile with rows past the sequence's length (its last): those are zeroed first
+            if (p.lengths && first && sk == nchunk - 1 && vlast < C && !await(&zeroed, 0, &abort_flag)) return false;
+            const uint32_t x = smem_u32(xbuf + (sx % NX) * K::X_BYTES), y = smem_u32(ybuf + (sy % NY) * K::Y_BYTES);
+            tc_fence_after();
+            LA_TL(si, 0);
+            if (elect_one()) {
+                mma_ss_kk<DX / 16>(tm + K::T_A + (si % NSC) * 128, desc_kmajor(x, C, 0, 0), desc_kmajor(y, C, 0, 0), idA);
+                mma_commit(&sc_full[si % NSC]);
+                if (YSM && (last || many)) mma_commit(&y_scored[sy % NY]);
+            }
+            __syncwarp();
+            LA_TL(si, 1);
+            if (last || !many) ++sx;
+            if (last || many) ++sy;
+            ++si;
+            if (++sr == reps) {
+                sr = 0;
+                ++sk;
+            }
+            return true;
+        };
+        int iz = 0, ot = 0, k = 0, r = 0;   // of the current item: z tile, output tile, chunk, head
+        bool ok = items == 0 || scores();
+        for (int it = 0; ok && it < items; ++it) {
+            const bool first = r == 0, last = r == reps - 1;
+            const bool opens = first || !many, ends = last || !many;   // an output tile
+            const bool more = it + 1 < items, early = NSC == 2 && more && scores_in();
+            if (early && !scores()) break;
+            const uint32_t tA = tm + K::T_A + (it % NSC) * 128;
+            if ((first || many) && !await(&z_full[iz % NZ], (iz / NZ) & 1, &abort_flag)) break;
+            if (opens && ot > 0 && !await(&o_free, (ot - 1) & 1, &abort_flag)) break;
+            LA_TL(it, 2);
+            if (!await(&p_ready[it % NSC], (it / NSC) & 1, &abort_flag)) break;
+            LA_TL(it, 4);
+            const uint32_t z = smem_u32(zbuf + (iz % NZ) * K::Z_BYTES);
+            tc_fence_after();
+            if (elect_one()) mma_ts_mn<C / 16>(tO, tA, desc_mnmajor(z, C, 0, 0), idO, opens ? 0u : 1u);
+            __syncwarp();
+            if (opens) {
+                if (!await(&xd_ready[ot % 2], (ot / 2) & 1, &abort_flag)) break;
+                if (first && !await(&s_conv, k & 1, &abort_flag)) break;
+                LA_TL(it, 5);
+                tc_fence_after();
+                if (elect_one()) mma_ts_mn<DX / 16>(tO, tA + 64, desc_mnmajor(sb, DX, 0, 0), idO, 1u);
+                __syncwarp();
+            }
+            if (elect_one()) {
+                if (ends) mma_commit(&o_full);
+                if (many ? first : last) mma_commit(&s_full);   // the chunk's last reader of S_bf
+                if (last || many) mma_commit(&z_empty[iz % NZ]);
+            }
+            __syncwarp();
+            LA_TL(it, 6);
+            if (ends) ++ot;
+            if (last || many) ++iz;
+            if (++r == reps) {
+                r = 0;
+                ++k;
+            }
+            if (more && !early && !scores()) break;
+        }
+        if (elect_one()) mma_commit(&fin[0]);
+        __syncwarp();
+        warp_drain(&fin[0], 0);
+    } else if (warp == 2) {
+        // ---------------- S += Y^T Z, once for each y z tile
+        constexpr uint32_t idS = idesc_bf16(128, DZ, YSM, true);
+        const uint32_t tS = tm + K::T_S;
+        const int tiles = many ? items : nchunk, per = many ? reps : 1;
+        int k = 0, r = 0;
+        for (int t = 0; t < tiles; ++t) {
+            if (r == 0 && !await(&s_conv, k & 1, &abort_flag)) break;
+            if (!await(&z_full[t % NZ], (t / NZ) & 1, &abort_flag)) break;
+            if (!await(&yt_ready[t % NY], (t / NY) & 1, &abort_flag)) break;
+            LA_TL(t, 3);
+            tc_fence_after();
+            const uint32_t y = smem_u32(ybuf + (t % NY) * K::Y_BYTES), z = smem_u32(zbuf + (t % NZ) * K::Z_BYTES);
+            const bool ends = ++r == per;
+            if (elect_one()) {
+                if constexpr (YSM) {
+                    // (M = 128 rows d of which DX count: with 64 the others read what lies behind the tile)
+                    mma_ss_mn8(tS, desc_mnmajor(y, C, 0, 0), desc_mnmajor(z, C, 0, 0), idS);
+                    mma_commit(&y_empty[t % NY]);
+                } else {
+                    mma_ts_mn<C / 16>(tS, tm + K::T_YH, desc_mnmajor(z, C, 0, 0), idS, 1u);
+                    if (exact) mma_ts_mn<C / 16>(tS, tm + K::T_YL, desc_mnmajor(z, C, 0, 0), idS, 1u);
+                    mma_commit(&yt_done);
+                }
+                mma_commit(&z_empty[t % NZ]);
+                if (ends) mma_commit(&s_full);
+                if constexpr (YSM) {   // the output goes where this z was, or not
+                    if (o_in_z && ends)
+                        mma_commit(&z_used[k % 2]);
+                    else
+                        mbar_arrive_cnt(&z_empty[t % NZ], 4);
+                }
+            }
+            __syncwarp();
+            if (ends) {
+                r = 0;
+                ++k;
+            }
+        }
+        if (elect_one()) mma_commit(&fin[1]);
+        __syncwarp();
+        warp_drain(&fin[1], 0);
+    } else if (warp >= 4 && warp < 8) {
+        // ---------------- P = bf16(scale A o W), thread = row i, 32 columns at a time.  Away from the diagonal
+        // gamma^|i - j| = gamma^(distance to the near end of a block of 16) gamma^(distance in the block); on it the blocks
+        // of 16 have the lower (reverse: upper) triangle of one pattern, or are such a full block, or nothing.  Both
+        // patterns stay in registers, with `scale`
+        const int wq = warp % 4, lane = threadIdx.x % 32, i = wq * 32 + lane;
         float g[16], tri[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
@@ -398,24 +464,24 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             tri[e] = ago >= 0 ? p.scale * pw[max(ago, 0)] : 0.f;
         }
         const bool low = lane < 16;
-        int r = 0, nx = 0, ny = 0;
+        int r = 0, nx = 0, ny = 0, ot = 0;
         for (int it = 0; it < items; ++it) {
-            if (!await(&sc_full, it & 1, &abort_flag)) break;
+            if (!await(&sc_full[it % NSC], (it / NSC) & 1, &abort_flag)) break;
             tc_fence_after();
-            if (threadIdx.x == 383) LA_TL(it, 7);
-            const bool last = ++r == reps;
+            if (i == 127) LA_TL(it, 7);
+            const uint32_t ta = tm + K::T_A + (it % NSC) * 128 + ((uint32_t)(wq * 32) << 16);
+            const bool first = r == 0, last = ++r == reps;
             if (last || !many) mbar_arrive_w(&x_empty[nx++ % NX]);
-            if (last || many) mbar_arrive_w(&y_empty[ny++ % NY]);
+            if (!YSM && (last || many)) mbar_arrive_w(&y_empty[ny++ % NY]);
 #pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
-                const int cb = hc * 2 + c;   // 32 columns
+            for (int cb = 0; cb < C / 32; ++cb) {
                 uint32_t w[16];
                 if (rev ? cb < wq : cb > wq) {   // the warp's rows have no such token
 #pragma unroll
                     for (int e = 0; e < 16; ++e) w[e] = 0u;
                 } else {
                     float v[32];
-                    tmem_ld32(ta + c * 32, v);
+                    tmem_ld32(ta + cb * 32, v);
                     tmem_wait_regs<32>(v);
 #pragma unroll
                     for (int hb = 0; hb < 2; ++hb) {
@@ -444,17 +510,17 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
 #pragma unroll
                     for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
                 }
-                // over columns of this half that this thread has read (16 c .. 16 c + 15 <= 32 c + 31)
-                tmem_st16_raw(ta + c * 16, w);
+                // over columns that this thread has read (16 cb .. 16 cb + 15 <= 32 cb + 31)
+                tmem_st16_raw(ta + cb * 16, w);
             }
             tmem_st_wait();
             tc_fence_before();
-            if (threadIdx.x == 383) LA_TL(it, 8);
-            mbar_arrive_warp(&p_ready);
-            if (r == 1 || !many) mbar_arrive_warp(&p_first);
+            if (i == 127) LA_TL(it, 8);
+            mbar_arrive_warp(&p_ready[it % NSC]);
+            if (first || !many) mbar_arrive_warp(&p_first[ot++ % 2]);
             if (last) r = 0;
         }
-    } else if (warp < 16) {
+    } else if (warp >= 8 && warp < 12) {
         // ---------------- S: the operand S_bf of the state before the chunk, and its decay; thread = row d
         const int wq = warp % 4, d = wq * 32 + threadIdx.x % 32;
         const uint32_t ts = tm + K::T_S + ((uint32_t)(wq * 32) << 16);
@@ -560,50 +626,61 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                     for (int e = 0; e < 16; ++e) f[(size_t)(c16 * 16 + e) * se] = v[e] * mul;
                 }
         }
-    } else if (warp < 20) {
-        // ---------------- rows of x and of the output; thread = row i.  The decayed x is made in registers while P is
-        // under way and stored where the scores have been read
+    } else if (warp >= 12 && warp < 16) {
+        // ---------------- the decayed X, thread = row i: made in registers while P is under way, stored where the
+        // scores have been read.  scale x gamma^(i + 1) with the factor as two bf16 terms: one rounding
         const int wq = warp % 4, i = wq * 32 + threadIdx.x % 32;
-        const uint32_t lane_off = (uint32_t)(wq * 32) << 16, to = tm + K::T_O + lane_off, tx = tm + K::T_A + 32 + lane_off;
+        const int tiles = many ? nchunk : items, step = many ? reps : 1;   // output tiles; items of each
+        int k = 0, r = 0;
+        for (int t = 0; t < tiles; ++t) {
+            const int valid = min(C, part.hi - chunk0(k));
+            if (!await(&x_full[t % NX], (t / NX) & 1, &abort_flag)) break;
+            if (i == 0) LA_TL(t, 11);
+            const float g = p.scale * pw[max((rev ? valid - i : i + 1) - (k == 0 ? off0 : 0), 0)];
+            const __nv_bfloat162 gh = as_bf162(pack_bf16x2(g, g));
+            const float gr = g - unpack_bf16x2(as_u32(gh)).x;
+            const __nv_bfloat162 gl = as_bf162(pack_bf16x2(gr, gr));
+            const uint8_t *x = xbuf + (t % NX) * K::X_BYTES;
+            uint32_t w[DX / 2];
+#pragma unroll
+            for (int c = 0; c < DX / 8; ++c) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(x + swz_chunk(C, i, c));
+                const uint32_t a[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[4 * c + e] = as_u32(__hfma2(as_bf162(a[e]), gh, __hmul2(as_bf162(a[e]), gl)));
+            }
+            mbar_arrive_w(&x_empty[t % NX]);
+            if (!await(&p_first[t % 2], (t / 2) & 1, &abort_flag)) break;
+            tc_fence_after();
+            const uint32_t tx = tm + K::T_A + ((t * step) % NSC) * 128 + 64 + ((uint32_t)(wq * 32) << 16);
+#pragma unroll
+            for (int q = 0; q < DX / 32; ++q) tmem_st16_raw(tx + q * 16, w + 16 * q);
+            tmem_st_wait();
+            tc_fence_before();
+            if (i == 0) LA_TL(t, 12);
+            mbar_arrive_warp(&xd_ready[t % 2]);
+            if (many || ++r == reps) {
+                r = 0;
+                ++k;
+            }
+        }
+    } else if (warp >= 16 && warp < 20) {
+        // ---------------- the output rows, thread = row i; each warp stages and stores its own 32
+        // (written from registers the rows, 32 bytes at a time, took a third of the chunk's time)
+        const int wq = warp % 4, i = wq * 32 + threadIdx.x % 32;
+        const uint32_t to = tm + K::T_O + ((uint32_t)(wq * 32) << 16);
         const int tiles = many ? nchunk : items;
         const CUtensorMap *mo = &maps.m[pi][3];
         int k = 0, r = 0;
         for (int t = 0; t < tiles; ++t) {
-            const int c0 = chunk0(k), valid = min(C, part.hi - c0);
-            if (!await(&x_full[t % NX], (t / NX) & 1, &abort_flag)) break;
-            {
-                // scale x gamma^(i + 1) with the factor as two bf16 terms: one rounding, that of the result
-                const float g = p.scale * pw[max((rev ? valid - i : i + 1) - (k == 0 ? off0 : 0), 0)];
-                const __nv_bfloat162 gh = as_bf162(pack_bf16x2(g, g));
-                const float gr = g - unpack_bf16x2(as_u32(gh)).x;
-                const __nv_bfloat162 gl = as_bf162(pack_bf16x2(gr, gr));
-                const uint8_t *x = xbuf + (t % NX) * K::X_BYTES;
-                uint32_t w[DX / 2];
-#pragma unroll
-                for (int c = 0; c < DX / 8; ++c) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(x + swz_chunk(C, i, c));
-                    const uint32_t a[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        w[4 * c + e] = as_u32(__hfma2(as_bf162(a[e]), gh, __hmul2(as_bf162(a[e]), gl)));
-                }
-                mbar_arrive_w(&x_empty[t % NX]);
-                if (!await(&p_first, t & 1, &abort_flag)) break;
-                tc_fence_after();
-                if (i == 0) LA_TL(t, 11);
-#pragma unroll
-                for (int q = 0; q < DX / 32; ++q) tmem_st16_raw(tx + (q / 2) * 64 + (q % 2) * 16, w + 16 * q);
-                tmem_st_wait();
-            }
-            tc_fence_before();
-            if (i == 0) LA_TL(t, 12);
-            mbar_arrive_warp(&xd_ready);
+            const int c0 = chunk0(k), valid = min(C, part.hi - c0), zi = (many ? (t + 1) * reps - 1 : t) % NZ;
+            uint8_t *o = o_in_z ? zbuf + zi * K::Z_BYTES : obuf + (NO > 1 ? t % NO : 0) * K::O_BYTES;
             if (!await(&o_full, t & 1, &abort_flag)) break;
+            if (o_in_z && !await(&z_used[t % 2], (t / 2) & 1, &abort_flag)) break;
             tc_fence_after();
             if (i == 0) LA_TL(t, 13);
-            // each warp stages and stores its own 32 rows; those past the length are zeros
-            uint8_t *o = obuf + (t % K::NO) * K::O_BYTES;
-            bulk_wait_read_but<K::NO - 1>();   // (of the elected lane)
+            bulk_wait_read_but<(NO > 1 ? NO - 1 : 0)>();   // (of the elected lane)
             __syncwarp();
 #pragma unroll 1
             for (int c32 = 0; c32 < DZ / 32; ++c32) {
@@ -613,7 +690,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                 uint32_t w[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
-                if (i >= valid) {
+                if (i >= valid) {   // past the length: zeros
 #pragma unroll
                     for (int e = 0; e < 16; ++e) w[e] = 0u;
                 }
@@ -635,47 +712,76 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                 bulk_commit();
             }
             __syncwarp();
+            if (o_in_z) {
+                bulk_wait_read_but<0>();
+                mbar_arrive_w(&z_empty[zi]);
+            }
             if (many || ++r == reps) {
                 r = 0;
                 ++k;
             }
         }
         bulk_wait_all();
-    } else {
-        // ---------------- Y^T of every y z tile
-        const int wq = warp % 4;
+    } else if (warp >= 20) {
+        // ---------------- the decayed y of every y z tile
+        const int wq = warp % 4, j = threadIdx.x - 640;
         const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
         const int tiles = many ? items : nchunk;
         YtWeights w;
+        __nv_bfloat162 gh, gl;
         bool shorter = false;
         int k = 0, r = 0;
         for (int t = 0; t < tiles; ++t) {
             const int c0 = chunk0(k), valid = min(C, part.hi - c0);
-            if (!await(&y_full[t % NY], (t / NY) & 1, &abort_flag)) break;
             uint8_t *y = ybuf + (t % NY) * K::Y_BYTES;
-            if (p.lengths && valid < C) {
+            if (!YSM || p.lengths)
+                if (!await(&y_full[t % NY], (t / NY) & 1, &abort_flag)) break;
+            if (p.lengths) {
                 if (!await(&z_full[t % NZ], (t / NZ) & 1, &abort_flag)) break;
-                zero_rows<DX>(y, valid, threadIdx.x - 640, 128);
-                zero_rows<DZ>(zbuf + (t % NZ) * K::Z_BYTES, valid, threadIdx.x - 640, 128);
-                fence_proxy_async();
-                mbar_arrive_warp(&zeroed);
-                // (the warps read one another's zeros)
-                if (!await(&zeroed, 0, &abort_flag)) break;
-            }
-            if (t > 0 && !await(&yt_done, (t - 1) & 1, &abort_flag)) break;
-            tc_fence_after();
-            if (wq * 32 < DX) {
-                if (t == 0 || (valid < C) != shorter) {
-                    shorter = valid < C;
-                    w.set(wtab[shorter], 1.f);
+                if (valid < C) {
+                    zero_rows<DX>(y, valid, j, 128);
+                    zero_rows<DZ>(zbuf + (t % NZ) * K::Z_BYTES, valid, j, 128);
+                    fence_proxy_async();
+                    mbar_arrive_warp(&zeroed);
+                    // (the warps read one another's zeros)
+                    if (!await(&zeroed, 0, &abort_flag)) break;
                 }
-                yt_tile(y, wq * 32, w, exact, tm + K::T_YH + lane_off, tm + K::T_YL + lane_off);
-                tmem_st_wait();
             }
-            mbar_arrive_w(&y_empty[t % NY]);
-            tc_fence_before();
+            const bool fresh = t == 0 || (valid < C) != shorter;
+            shorter = valid < C;
+            if constexpr (YSM) {
+                // in place, thread = row (token) j, once the scores have read the tile
+                if (fresh) {
+                    const float g = wtab[shorter][j];
+                    gh = as_bf162(pack_bf16x2(g, g));
+                    const float gr = g - unpack_bf16x2(as_u32(gh)).x;
+                    gl = as_bf162(pack_bf16x2(gr, gr));
+                }
+                if (!await(&y_scored[t % NY], (t / NY) & 1, &abort_flag)) break;
+#pragma unroll
+                for (int c = 0; c < DX / 8; ++c) {
+                    uint4 *q = reinterpret_cast<uint4 *>(y + swz_chunk(C, j, c));
+                    uint4 v = *q;
+                    v.x = as_u32(__hfma2(as_bf162(v.x), gh, __hmul2(as_bf162(v.x), gl)));
+                    v.y = as_u32(__hfma2(as_bf162(v.y), gh, __hmul2(as_bf162(v.y), gl)));
+                    v.z = as_u32(__hfma2(as_bf162(v.z), gh, __hmul2(as_bf162(v.z), gl)));
+                    v.w = as_u32(__hfma2(as_bf162(v.w), gh, __hmul2(as_bf162(v.w), gl)));
+                    *q = v;
+                }
+                fence_proxy_async();
+            } else {
+                if (fresh && wq * 32 < DX) w.set(wtab[shorter], 1.f);
+                if (t > 0 && !await(&yt_done, (t - 1) & 1, &abort_flag)) break;
+                tc_fence_after();
+                if (wq * 32 < DX) {
+                    yt_tile(y, wq * 32, w, exact, tm + K::T_YH + lane_off, tm + K::T_YL + lane_off);
+                    tmem_st_wait();
+                }
+                mbar_arrive_w(&y_empty[t % NY]);
+                tc_fence_before();
+            }
             if (threadIdx.x == 640) LA_TL(t, 15);
-            mbar_arrive_warp(&yt_ready);
+            mbar_arrive_warp(&yt_ready[t % NY]);
             if (!many || ++r == reps) {
                 r = 0;
                 ++k;
@@ -925,7 +1031,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_decay_join(const __grid_consta
 
 // ---- launches ---------------------------------------------------------------------------
 
-template <int DX, int DZ>
+template <int DX, int DZ, bool YSM>
 cudaError_t passes_d(const DecayParams &p, int pass0, int npass, cudaStream_t s) {
     PassMaps maps;
     for (int i = pass0; i < pass0 + npass; ++i) {
@@ -937,19 +1043,24 @@ cudaError_t passes_d(const DecayParams &p, int pass0, int npass, cudaStream_t s)
         if (e == cudaSuccess) e = make_map_in(&maps.m[i][3], ps.out, p.B, Hx, p.N, DZ, contiguous_strides(Hx, p.N, DZ), 32);
         if (e != cudaSuccess) return e;
     }
-    auto kern = k_decay_tc<DX, DZ>;
-    cudaError_t e = prepare(kern, MainCfg<DX, DZ>::SMEM);
+    auto kern = k_decay_tc<DX, DZ, YSM>;
+    constexpr int smem = MainCfg<DX, DZ, YSM>::SMEM;
+    cudaError_t e = prepare(kern, smem);
     if (e != cudaSuccess) return e;
     TraceScope tr("decay_tc", s);
-    return launch_pdl(kern, dim3((unsigned)npass * p.nseg * p.B * p.Hkv), dim3(kMainThreads), MainCfg<DX, DZ>::SMEM, s, maps,
-                      p, pass0, npass);
+    return launch_pdl(kern, dim3((unsigned)npass * p.nseg * p.B * p.Hkv), dim3(kMainThreads), smem, s, maps, p, pass0, npass);
 }
 
 cudaError_t passes(const DecayParams &p, int pass0, int npass, cudaStream_t s) {
     const bool tr = p.pass[pass0].tr;
     const int DX = tr ? p.Dv : p.D, DZ = tr ? p.D : p.Dv;
-    if (DX == 64) return DZ == 64 ? passes_d<64, 64>(p, pass0, npass, s) : passes_d<64, 128>(p, pass0, npass, s);
-    return DZ == 64 ? passes_d<128, 64>(p, pass0, npass, s) : passes_d<128, 128>(p, pass0, npass, s);
+    if (DZ == 64) return DX == 64 ? passes_d<64, 64, false>(p, pass0, npass, s) : passes_d<128, 64, false>(p, pass0, npass, s);
+    // 128 columns of S and O leave no room in TMEM for two buffers of scores and Y^T; where the state is not an
+    // output y is decayed in shared memory instead, once rounded
+    bool exact = false;
+    for (int i = pass0; i < pass0 + npass; ++i) exact = exact || p.pass[i].fin;
+    if (exact) return DX == 64 ? passes_d<64, 128, false>(p, pass0, npass, s) : passes_d<128, 128, false>(p, pass0, npass, s);
+    return DX == 64 ? passes_d<64, 128, true>(p, pass0, npass, s) : passes_d<128, 128, true>(p, pass0, npass, s);
 }
 
 template <int D, int DV>
