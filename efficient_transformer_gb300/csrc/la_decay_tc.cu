@@ -34,29 +34,34 @@ namespace {
 constexpr int C = kDecayTcChunk;
 constexpr int kMainThreads = 768;
 
-// Bounded warp-uniform wait.  What follows a wait that does not end at once is out of line: the kernels have some
-// twenty waits, and their code has to stay in the instruction caches that all roles share.
-__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    uint64_t t0 = 0;
-    for (;;) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)   // (each may suspend the warp)
-            if (mbar_try_wait(bar, parity)) return true;
-        if (*abort) return false;
-        const uint64_t t = globaltimer_ns();
-        if (t0 == 0) t0 = t;
-        if (t - t0 > kWaitNs) {
-            *abort = 1;
-            return false;
-        }
-    }
+// Bounded warp-uniform wait.  A try suspends the thread for 2 us at most, so that kTries of them are a few seconds
+// at most and tens of milliseconds at least; no wait of a block that runs takes one of them.
+//
+// Code size is what this and the loops below are shaped by.  Each role's loop body runs once a chunk, so the roles'
+// code passes through the instruction caches in turn; at 38 KB in all it was fetched anew for each chunk (300
+// misses of 128 bytes a chunk and SM, warps at one instruction in six cycles).  So a wait is a dozen instructions,
+// loops stay rolled where that costs a few instructions, and there is one copy of each product.
+#ifdef LA_TEST_HOOKS
+constexpr uint32_t kTries = 1u << 13;
+#else
+constexpr uint32_t kTries = 1u << 21;
+#endif
+__device__ __forceinline__ bool await(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 n;\n\tmov.b32 n, %3;\n"
+        "AGAIN:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 2000;\n\t"
+        "@p bra OVER;\n\tsub.u32 n, n, 1;\n\tsetp.ne.u32 q, n, 0;\n\t@q bra AGAIN;\n"
+        "OVER:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity), "n"(kTries)
+        : "memory");
+    if (__all_sync(0xffffffffu, done)) return true;
+    *abort = 1;
+    return false;
 }
 __device__ __forceinline__ bool is_over(uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_test(bar, parity));
-}
-__device__ __forceinline__ bool await(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    return __all_sync(0xffffffffu, wait_slow(bar, parity, abort));
 }
 
 struct PassMaps {
@@ -77,6 +82,8 @@ struct MainCfg {
     static constexpr int SMEM = NX * X_BYTES + NY * Y_BYTES + NZ * Z_BYTES + NO * O_BYTES + S_BYTES + 1024;
     static_assert(SMEM + 2048 <= kSmemLimit, "tiles, barriers and tables");
     static_assert(!YSM || (NY - 1) * Y_BYTES >= O_BYTES, "an output tile in y's other stages");
+    // (S's MMA reads 128 columns from a y tile's start: with DX = 64 the next y stage or the first z tile)
+    static_assert(DX == 128 || Z_BYTES >= C * 64 * 2, "128 columns from a y tile's start");
     // TMEM: S, O, one or two buffers of scores, Y^T hi | lo
     static constexpr int NSC = DZ == 64 || YSM ? 2 : 1;
     static constexpr int T_S = 0, T_O = DZ, T_A = 2 * DZ, T_YH = T_A + 128 * NSC, T_YL = T_YH + 64;
@@ -263,6 +270,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         mbar_init(&fin[1], 1);
         fence_barrier_init();
     }
+    if (threadIdx.x >= 96 && threadIdx.x < 100) tma_prefetch_map(&maps.m[pi][threadIdx.x - 96]);
     for (int i = threadIdx.x; i <= C; i += kMainThreads) pw[i] = exp2f(l2 * i);
     // powers that the tokens of a chunk have ahead of them: full chunks, and the short one
     for (int i = threadIdx.x; i < 2 * C; i += kMainThreads) {
@@ -340,38 +348,40 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         auto scores_in = [&]() {
             return is_over(&x_full[sx % NX], (sx / NX) & 1) && is_over(&y_full[sy % NY], (sy / NY) & 1);
         };
-        auto scores = [&]() -> bool {
-            const bool first = sr == 0, last = sr == reps - 1;
-            if ((first || !many) && !await(&x_full[sx % NX], (sx / NX) & 1, &abort_flag)) return false;
-            if ((first || many) && !await(&y_full[sy % NY], (sy / NY) & 1, &abort_flag)) return false;
-            // a tile with rows past the sequence's length (its last): those are zeroed first
-            if (p.lengths && first && sk == nchunk - 1 && vlast < C && !await(&zeroed, 0, &abort_flag)) return false;
-            const uint32_t x = smem_u32(xbuf + (sx % NX) * K::X_BYTES), y = smem_u32(ybuf + (sy % NY) * K::Y_BYTES);
-            tc_fence_after();
-            LA_TL(si, 0);
-            if (elect_one()) {
-                mma_ss_kk<DX / 16>(tm + K::T_A + (si % NSC) * 128, desc_kmajor(x, C, 0, 0), desc_kmajor(y, C, 0, 0), idA);
-                mma_commit(&sc_full[si % NSC]);
-                if (YSM && (last || many)) mma_commit(&y_scored[sy % NY]);
-            }
-            __syncwarp();
-            LA_TL(si, 1);
-            if (last || !many) ++sx;
-            if (last || many) ++sy;
-            ++si;
-            if (++sr == reps) {
-                sr = 0;
-                ++sk;
-            }
-            return true;
-        };
         int iz = 0, ot = 0, k = 0, r = 0;   // of the current item: z tile, output tile, chunk, head
-        bool ok = items == 0 || scores();
-        for (int it = 0; ok && it < items; ++it) {
+        bool ok = true;
+#pragma unroll 1
+        for (int it = 0; it < items; ++it) {
+            // this item's scores if they are not out yet, and the next one's if its tiles are in
+#pragma unroll 1
+            while (ok && (si <= it || (NSC == 2 && si == it + 1 && si < items && scores_in()))) {
+                const bool first = sr == 0, last = sr == reps - 1;
+                ok = (!(first || !many) || await(&x_full[sx % NX], (sx / NX) & 1, &abort_flag)) &&
+                     (!(first || many) || await(&y_full[sy % NY], (sy / NY) & 1, &abort_flag)) &&
+                     // a tile with rows past the sequence's length (its last): those are zeroed first
+                     (!(p.lengths && first && sk == nchunk - 1 && vlast < C) || await(&zeroed, 0, &abort_flag));
+                if (!ok) break;
+                const uint32_t x = smem_u32(xbuf + (sx % NX) * K::X_BYTES), y = smem_u32(ybuf + (sy % NY) * K::Y_BYTES);
+                tc_fence_after();
+                LA_TL(si, 0);
+                if (elect_one()) {
+                    mma_ss_kk<DX / 16>(tm + K::T_A + (si % NSC) * 128, desc_kmajor(x, C, 0, 0), desc_kmajor(y, C, 0, 0), idA);
+                    mma_commit(&sc_full[si % NSC]);
+                    if (YSM && (last || many)) mma_commit(&y_scored[sy % NY]);
+                }
+                __syncwarp();
+                LA_TL(si, 1);
+                if (last || !many) ++sx;
+                if (last || many) ++sy;
+                ++si;
+                if (++sr == reps) {
+                    sr = 0;
+                    ++sk;
+                }
+            }
+            if (!ok) break;
             const bool first = r == 0, last = r == reps - 1;
             const bool opens = first || !many, ends = last || !many;   // an output tile
-            const bool more = it + 1 < items, early = NSC == 2 && more && scores_in();
-            if (early && !scores()) break;
             const uint32_t tA = tm + K::T_A + (it % NSC) * 128;
             if ((first || many) && !await(&z_full[iz % NZ], (iz / NZ) & 1, &abort_flag)) break;
             if (opens && ot > 0 && !await(&o_free, (ot - 1) & 1, &abort_flag)) break;
@@ -403,7 +413,6 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                 r = 0;
                 ++k;
             }
-            if (more && !early && !scores()) break;
         }
         if (elect_one()) mma_commit(&fin[0]);
         __syncwarp();
@@ -414,6 +423,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         const uint32_t tS = tm + K::T_S;
         const int tiles = many ? items : nchunk, per = many ? reps : 1;
         int k = 0, r = 0;
+#pragma unroll 1
         for (int t = 0; t < tiles; ++t) {
             if (r == 0 && !await(&s_conv, k & 1, &abort_flag)) break;
             if (!await(&z_full[t % NZ], (t / NZ) & 1, &abort_flag)) break;
@@ -465,6 +475,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         }
         const bool low = lane < 16;
         int r = 0, nx = 0, ny = 0, ot = 0;
+#pragma unroll 1
         for (int it = 0; it < items; ++it) {
             if (!await(&sc_full[it % NSC], (it / NSC) & 1, &abort_flag)) break;
             tc_fence_after();
@@ -487,24 +498,15 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                     for (int hb = 0; hb < 2; ++hb) {
                         const int j0 = cb * 32 + hb * 16;
                         const int near = rev ? j0 - i : i - j0 - 15;   // distance to the block's near end
-                        if (cb == wq) {
-                            const float full = (rev ? hb == 1 && low : hb == 0 && !low) ? pw[max(near, 0)] : 0.f;
-                            const float half = low == (hb == 0) ? 1.f : 0.f;
+                        const bool diag = cb == wq;
+                        const float full = !diag || (rev ? hb == 1 && low : hb == 0 && !low) ? pw[max(near, 0)] : 0.f;
+                        const float half = diag && low == (hb == 0) ? 1.f : 0.f;
 #pragma unroll
-                            for (int e = 0; e < 16; e += 2) {
-                                float a = g[e], b = g[e + 1];
-                                mul2(a, b, full, full);
-                                fma2(a, b, tri[e], tri[e + 1], half);
-                                mul2(v[hb * 16 + e], v[hb * 16 + e + 1], a, b);
-                            }
-                        } else {
-                            const float base = pw[near];
-#pragma unroll
-                            for (int e = 0; e < 16; e += 2) {
-                                float a = g[e], b = g[e + 1];
-                                mul2(a, b, base, base);
-                                mul2(v[hb * 16 + e], v[hb * 16 + e + 1], a, b);
-                            }
+                        for (int e = 0; e < 16; e += 2) {
+                            float a = g[e], b = g[e + 1];
+                            mul2(a, b, full, full);
+                            fma2(a, b, tri[e], tri[e + 1], half);
+                            mul2(v[hb * 16 + e], v[hb * 16 + e + 1], a, b);
                         }
                     }
 #pragma unroll
@@ -580,6 +582,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             }
             tmem_st_wait();
         }
+#pragma unroll 1
         for (int k = 0; k < nchunk; ++k) {
             if (k > 0) {
                 ok = await(&s_full, (k - 1) & 1, &abort_flag);
@@ -588,17 +591,22 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                 if (d == 0) LA_TL(k, 9);
                 const float gk = k == nchunk - 1 ? gl : g;
                 if (have) {
+                    float va[16], vb[16];
+                    auto part16 = [&](float *v, int c16) {
+                        store_state_row<DX>(sbf, d, v, c16);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) mul2(v[e], v[e + 1], gk, gk);
+                        tmem_st16(ts + c16 * 16, v);
+                    };
+                    tmem_ld16(ts, va);
 #pragma unroll 1
                     for (int c32 = 0; c32 < DZ / 32; ++c32) {
-                        float v[32];
-                        tmem_ld32(ts + c32 * 32, v);
-                        tmem_wait_regs<32>(v);
-                        store_state_row<DX>(sbf, d, v, 2 * c32);
-                        store_state_row<DX>(sbf, d, v + 16, 2 * c32 + 1);
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) mul2(v[e], v[e + 1], gk, gk);
-                        tmem_st16(ts + c32 * 32, v);
-                        tmem_st16(ts + c32 * 32 + 16, v + 16);
+                        tmem_wait_regs<16>(va);
+                        tmem_ld16(ts + c32 * 32 + 16, vb);
+                        part16(va, 2 * c32);
+                        tmem_wait_regs<16>(vb);
+                        if (c32 + 1 < DZ / 32) tmem_ld16(ts + c32 * 32 + 32, va);
+                        part16(vb, 2 * c32 + 1);
                     }
                     tmem_st_wait();
                 }
@@ -627,11 +635,12 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                 }
         }
     } else if (warp >= 12 && warp < 16) {
-        // ---------------- the decayed X, thread = row i: made in registers while P is under way, stored where the
-        // scores have been read.  scale x gamma^(i + 1) with the factor as two bf16 terms: one rounding
+        // ---------------- the decayed X, thread = row i, where the scores have been read (beside P Z): scale x
+        // gamma^(i + 1) with the factor as two bf16 terms, rounded once
         const int wq = warp % 4, i = wq * 32 + threadIdx.x % 32;
         const int tiles = many ? nchunk : items, step = many ? reps : 1;   // output tiles; items of each
         int k = 0, r = 0;
+#pragma unroll 1
         for (int t = 0; t < tiles; ++t) {
             const int valid = min(C, part.hi - chunk0(k));
             if (!await(&x_full[t % NX], (t / NX) & 1, &abort_flag)) break;
@@ -641,21 +650,23 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             const float gr = g - unpack_bf16x2(as_u32(gh)).x;
             const __nv_bfloat162 gl = as_bf162(pack_bf16x2(gr, gr));
             const uint8_t *x = xbuf + (t % NX) * K::X_BYTES;
-            uint32_t w[DX / 2];
-#pragma unroll
-            for (int c = 0; c < DX / 8; ++c) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(x + swz_chunk(C, i, c));
-                const uint32_t a[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    w[4 * c + e] = as_u32(__hfma2(as_bf162(a[e]), gh, __hmul2(as_bf162(a[e]), gl)));
-            }
-            mbar_arrive_w(&x_empty[t % NX]);
             if (!await(&p_first[t % 2], (t / 2) & 1, &abort_flag)) break;
             tc_fence_after();
             const uint32_t tx = tm + K::T_A + ((t * step) % NSC) * 128 + 64 + ((uint32_t)(wq * 32) << 16);
+#pragma unroll 1
+            for (int q = 0; q < DX / 32; ++q) {
+                uint32_t w[16];
 #pragma unroll
-            for (int q = 0; q < DX / 32; ++q) tmem_st16_raw(tx + q * 16, w + 16 * q);
+                for (int c = 0; c < 4; ++c) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(x + swz_chunk(C, i, 4 * q + c));
+                    const uint32_t a[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[4 * c + e] = as_u32(__hfma2(as_bf162(a[e]), gh, __hmul2(as_bf162(a[e]), gl)));
+                }
+                tmem_st16_raw(tx + q * 16, w);
+            }
+            mbar_arrive_w(&x_empty[t % NX]);
             tmem_st_wait();
             tc_fence_before();
             if (i == 0) LA_TL(t, 12);
@@ -673,13 +684,14 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         const int tiles = many ? nchunk : items;
         const CUtensorMap *mo = &maps.m[pi][3];
         int k = 0, r = 0;
+#pragma unroll 1
         for (int t = 0; t < tiles; ++t) {
             const int c0 = chunk0(k), valid = min(C, part.hi - c0), zi = (many ? (t + 1) * reps - 1 : t) % NZ;
             uint8_t *o = o_in_z ? zbuf + zi * K::Z_BYTES : obuf + (NO > 1 ? t % NO : 0) * K::O_BYTES;
             if (!await(&o_full, t & 1, &abort_flag)) break;
-            if (o_in_z && !await(&z_used[t % 2], (t / 2) & 1, &abort_flag)) break;
             tc_fence_after();
             if (i == 0) LA_TL(t, 13);
+            if (o_in_z && !await(&z_used[t % 2], (t / 2) & 1, &abort_flag)) break;
             bulk_wait_read_but<(NO > 1 ? NO - 1 : 0)>();   // (of the elected lane)
             __syncwarp();
 #pragma unroll 1
@@ -687,6 +699,11 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                 float v[32];
                 tmem_ld32(to + c32 * 32, v);
                 tmem_wait_regs<32>(v);
+                if (c32 == DZ / 32 - 1) {   // O is free for the next item's products
+                    tc_fence_before();
+                    mbar_arrive_warp(&o_free);
+                    if (i == 0) LA_TL(t, 14);
+                }
                 uint32_t w[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
@@ -699,9 +716,6 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                     *reinterpret_cast<uint4 *>(o + swz_chunk(C, i, c32 * 4 + q)) =
                         make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
             }
-            tc_fence_before();
-            mbar_arrive_warp(&o_free);
-            if (i == 0) LA_TL(t, 14);
             fence_proxy_async();
             __syncwarp();
             if (elect_one()) {
@@ -731,6 +745,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         __nv_bfloat162 gh, gl;
         bool shorter = false;
         int k = 0, r = 0;
+#pragma unroll 1
         for (int t = 0; t < tiles; ++t) {
             const int c0 = chunk0(k), valid = min(C, part.hi - c0);
             uint8_t *y = ybuf + (t % NY) * K::Y_BYTES;
@@ -758,7 +773,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                     gl = as_bf162(pack_bf16x2(gr, gr));
                 }
                 if (!await(&y_scored[t % NY], (t / NY) & 1, &abort_flag)) break;
-#pragma unroll
+#pragma unroll 4
                 for (int c = 0; c < DX / 8; ++c) {
                     uint4 *q = reinterpret_cast<uint4 *>(y + swz_chunk(C, j, c));
                     uint4 v = *q;
@@ -806,10 +821,10 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
 }
 
 // ---------------------------------------------------------------------------------------
-// The sums over single segments (see DecayStateParams).  Y^T is decayed to the segment's end at once, so S in
-// TMEM only ever accumulates; Y^T is double-buffered and made by two groups of warps in turn.
-// Warps: 0 TMA, 1 MMA, 4-7 and 8-11 Y^T of even and odd tiles (4-7 then write S).
-constexpr int kStateThreads = 384;
+// The sums over parts of segments (see DecayStateParams).  y is decayed to the part's end at once, so S in
+// TMEM only ever accumulates; in place in its tile, and where the state is exact with the rounding's remainder
+// in a tile of its own.  Warps: 0 TMA, 1 MMA, 4-11 y (two threads a token; 4-7 then write S).
+constexpr int kStateThreads = 384, kStateY = 256;
 
 struct StateMaps {
     CUtensorMap m[2][2];   // per array: y, z
@@ -818,8 +833,13 @@ struct StateMaps {
 template <int D, int DV>
 struct StateCfg {
     static constexpr int Y_BYTES = C * D * 2, STAGE = Y_BYTES + C * DV * 2;
-    static constexpr int NS = (kSmemLimit - 1024 - 2048) / STAGE > 4 ? 4 : (kSmemLimit - 1024 - 2048) / STAGE;
-    static constexpr int SMEM = NS * STAGE + 1024;
+    // the MMA's M is 128 whatever D: what lies behind a y tile is its z tile; the remainder's tile, the last, has
+    // room for 128 columns of its own
+    static constexpr int LO_BYTES = C * 128 * 2;
+    static constexpr int FIT = (kSmemLimit - 1024 - 2048 - LO_BYTES) / STAGE, NS = FIT > 4 ? 4 : FIT;
+    static constexpr int SMEM = NS * STAGE + LO_BYTES + 1024;
+    static_assert(D == 128 || STAGE - Y_BYTES >= C * 64 * 2, "128 columns from a y tile's start");
+    static_assert(NS >= 2, "two stages");
 };
 
 template <int D, int DV>
@@ -828,20 +848,19 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
     using K = StateCfg<D, DV>;
     constexpr int NS = K::NS;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[NS], empty[NS], yt_ready[2], yt_done[2], zeroed[2], fin;
-    __shared__ __align__(16) float wtab[2][C];
+    __shared__ uint64_t full[NS], empty[NS], y_ready[NS], lo_free, zeroed, fin;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
-    uint8_t *stage = align1024(smem_raw);
+    uint8_t *stage = align1024(smem_raw), *lo_tile = stage + NS * K::STAGE;
     pdl_wait();
     const int warp = threadIdx.x / 32;
     const int nparts = (p.nseg - 1) * p.nsub, pidx = blockIdx.x % nparts, ah = blockIdx.x / nparts;
     const int a = ah / (p.B * p.Hkv), bg = ah % (p.B * p.Hkv), b = bg / p.Hkv, h = bg % p.Hkv;
     const int n = decay_tokens(p.lengths, b, p.N), rev = p.rev[a], heads = p.heads[a];
+    const bool exact = p.exact[a];
     const Part part = sub_part_of(n, p.N, pidx / p.nsub, p.nseg, p.seg_len, pidx % p.nsub, p.nsub, p.sub_len, rev);
     const int nchunk = (part.hi - part.lo + C - 1) / C, items = nchunk * heads;
     const float l2 = decay_log2(p.log_decay[h]);
-    const int vlast = part.hi - part.lo - C * (nchunk - 1);
     float *dst = p.part[a] + ((size_t)bg * nparts + pidx) * D * DV;
 
     if (threadIdx.x == 0) {
@@ -849,28 +868,22 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
         for (int s = 0; s < NS; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
+            mbar_init(&y_ready[s], kStateY);
         }
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(&yt_ready[s], 128);
-            mbar_init(&yt_done[s], 1);
-            mbar_init(&zeroed[s], 128);
-        }
+        mbar_init(&lo_free, 1);
+        mbar_init(&zeroed, kStateY);
         mbar_init(&fin, 1);
         fence_barrier_init();
     }
-    for (int i = threadIdx.x; i < 2 * C; i += kStateThreads) {
-        const int j = i % C, v = i < C ? C : vlast;
-        wtab[i / C][j] = j < v ? exp2f(l2 * (rev ? j : v - 1 - j)) : 0.f;
-    }
+    if (threadIdx.x >= 96 && threadIdx.x < 98) tma_prefetch_map(&maps.m[a][threadIdx.x - 96]);
     if (warp == 1) {
-        tmem_alloc(&tmem_base, 512);
+        tmem_alloc(&tmem_base, 128);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = tmem_base;
-    constexpr int T_S = 0, T_Y = 128;   // buffer i: hi at T_Y + 128 i, lo 64 further
 
     if (warp == 0) {
         int issued = 0;
@@ -890,16 +903,20 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
         }
         for (int i = issued > NS ? issued - NS : 0; i < issued; ++i) warp_drain(&full[i % NS], (i / NS) & 1);
     } else if (warp == 1) {
-        constexpr uint32_t id = idesc_bf16(128, DV, false, true);
+        constexpr uint32_t id = idesc_bf16(128, DV, true, true);
+        // (M = 128 rows d of which D count: with 64 the others read what lies behind the tile; the accumulator
+        // starts at zero)
         for (int it = 0; it < items; ++it) {
-            const int s = it % NS, q = it % 2;
-            if (!await(&yt_ready[q], (it / 2) & 1, &abort_flag)) break;
+            const int s = it % NS;
+            if (!await(&y_ready[s], (it / NS) & 1, &abort_flag)) break;
             tc_fence_after();
-            const uint32_t z = smem_u32(stage + s * K::STAGE + K::Y_BYTES), ty = tm + T_Y + 128 * q;
+            const uint32_t y = smem_u32(stage + s * K::STAGE), z = y + K::Y_BYTES;
             if (elect_one()) {
-                mma_ts_mn<C / 16>(tm + T_S, ty, desc_mnmajor(z, C, 0, 0), id, it > 0 ? 1u : 0u);
-                if (p.exact[a]) mma_ts_mn<C / 16>(tm + T_S, ty + 64, desc_mnmajor(z, C, 0, 0), id, 1u);
-                mma_commit(&yt_done[q]);
+                mma_ss_mn8(tm, desc_mnmajor(y, C, 0, 0), desc_mnmajor(z, C, 0, 0), id);
+                if (exact) {
+                    mma_ss_mn8(tm, desc_mnmajor(smem_u32(lo_tile), C, 0, 0), desc_mnmajor(z, C, 0, 0), id);
+                    mma_commit(&lo_free);
+                }
                 mma_commit(&empty[s]);
             }
             __syncwarp();
@@ -908,33 +925,54 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
         __syncwarp();
         warp_drain(&fin, 0);
     } else if (warp >= 4) {
-        const int grp = (warp - 4) / 4, wq = warp % 4, d = wq * 32 + threadIdx.x % 32;
+        const int i = threadIdx.x - 128, j = i % C, half = i / C, wq = warp % 4, d = wq * 32 + threadIdx.x % 32;
         const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+        if (warp < 8) {   // S = 0
+            const float z16[16] = {};
+#pragma unroll
+            for (int c16 = 0; c16 < DV / 16; ++c16) tmem_st16(tm + lane_off + c16 * 16, z16);
+            tmem_st_wait();
+            tc_fence_before();
+        }
         bool ok = true;
-        for (int it = grp; it < items; it += 2) {
-            const int s = it % NS, c0 = part.lo + C * (it / heads), valid = min(C, part.hi - c0), q = it % 2;
-            // the buffer's last tile first: then every earlier use of this stage is over too (a group sees
-            // only every other tile, and a parity tells only neighbouring phases apart)
-            if (it >= 2 && !(ok = await(&yt_done[q], (it / 2 - 1) & 1, &abort_flag))) break;
+        for (int it = 0; it < items; ++it) {
+            const int s = it % NS, c0 = part.lo + C * (it / heads), valid = min(C, part.hi - c0);
             if (!(ok = await(&full[s], (it / NS) & 1, &abort_flag))) break;
             uint8_t *y = stage + s * K::STAGE;
             if (p.lengths && valid < C) {
-                zero_rows<D>(y, valid, threadIdx.x % 128, 128);
-                zero_rows<DV>(y + K::Y_BYTES, valid, threadIdx.x % 128, 128);
-                fence_proxy_async();
-                mbar_arrive_warp(&zeroed[grp]);
-                if (!(ok = await(&zeroed[grp], 0, &abort_flag))) break;
+                zero_rows<D>(y, valid, i, kStateY);
+                zero_rows<DV>(y + K::Y_BYTES, valid, i, kStateY);
+                mbar_arrive_warp(&zeroed);
+                if (!(ok = await(&zeroed, 0, &abort_flag))) break;
             }
-            tc_fence_after();
-            if (wq * 32 < D) {
-                // what the chunk's last token has ahead of it in the segment
-                YtWeights w;
-                w.set(wtab[valid < C], exp2f(l2 * (rev ? c0 - part.lo : part.hi - c0 - valid)));
-                yt_tile(y, wq * 32, w, p.exact[a], tm + T_Y + 128 * q + lane_off, tm + T_Y + 128 * q + 64 + lane_off);
-                tmem_st_wait();
+            // what token j has ahead of it in the part, as two bf16 terms
+            const float g = exp2f(l2 * max(rev ? c0 + j - part.lo : part.hi - 1 - c0 - j, 0));
+            const __nv_bfloat162 gh = as_bf162(pack_bf16x2(g, g));
+            const float gr = g - unpack_bf16x2(as_u32(gh)).x;
+            const __nv_bfloat162 gl = as_bf162(pack_bf16x2(gr, gr));
+            if (exact && it > 0 && !(ok = await(&lo_free, (it - 1) & 1, &abort_flag))) break;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+                const uint32_t at = swz_chunk(C, j, half * (D / 16) + c);
+                uint4 v = *reinterpret_cast<uint4 *>(y + at);
+                uint32_t x[4] = {v.x, v.y, v.z, v.w}, r[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const __nv_bfloat162 q = as_bf162(x[e]);
+                    if (exact) {
+                        // hi = bf16(y gh), the remainder y gh - hi exact in one multiply-add, lo = bf16(remainder + y gl)
+                        const __nv_bfloat162 hi = __hmul2(q, gh);
+                        r[e] = as_u32(__hfma2(q, gl, __hfma2(q, gh, __hneg2(hi))));
+                        x[e] = as_u32(hi);
+                    } else {
+                        x[e] = as_u32(__hfma2(q, gh, __hmul2(q, gl)));
+                    }
+                }
+                *reinterpret_cast<uint4 *>(y + at) = make_uint4(x[0], x[1], x[2], x[3]);
+                if (exact) *reinterpret_cast<uint4 *>(lo_tile + at) = make_uint4(r[0], r[1], r[2], r[3]);
             }
-            tc_fence_before();
-            mbar_arrive_warp(&yt_ready[q]);
+            fence_proxy_async();
+            mbar_arrive_warp(&y_ready[s]);
         }
         if (warp < 8 && wq * 32 < D) {
             if (ok && items > 0) ok = await(&fin, 0, &abort_flag);
@@ -943,13 +981,8 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
 #pragma unroll 1
                 for (int c16 = 0; c16 < DV / 16; ++c16) {
                     float v[16];
-                    if (items > 0) {
-                        tmem_ld16(tm + T_S + lane_off + c16 * 16, v);
-                        tmem_wait_regs<16>(v);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] = 0.f;
-                    }
+                    tmem_ld16(tm + lane_off + c16 * 16, v);
+                    tmem_wait_regs<16>(v);
                     float4 *f = reinterpret_cast<float4 *>(dst + decay_blocked(D, d, c16 * 16));
 #pragma unroll
                     for (int e = 0; e < 4; ++e) f[e * D] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
@@ -958,7 +991,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) tmem_dealloc(tm, 512);
+    if (warp == 1) tmem_dealloc(tm, 128);
     if (threadIdx.x == 0 && abort_flag) atomicExch(p.err, kErrTimeout);
 }
 
