@@ -64,6 +64,18 @@ __device__ __forceinline__ bool is_over(uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_test(bar, parity));
 }
 
+// A place in a ring of stages and the parity of its current use.
+struct Ring {
+    int s = 0;
+    uint32_t p = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++s == n) {
+            s = 0;
+            p ^= 1u;
+        }
+    }
+};
+
 struct PassMaps {
     CUtensorMap m[3][4];   // per pass: x, y, z, out
 };
@@ -192,7 +204,7 @@ __device__ __forceinline__ void yt_tile(const uint8_t *y, int d0, const YtWeight
 // Zero rows [valid, C) of a C x W tile (what lies past a sequence's length must not meet an MMA or a weight of
 // 0, where 0 times a non-finite value is not 0); nth threads, this one being i.
 template <int W>
-__device__ __forceinline__ void zero_rows(uint8_t *tile, int valid, int i, int nth) {
+__device__ __noinline__ void zero_rows(uint8_t *tile, int valid, int i, int nth) {
     for (int idx = i; idx < (C - valid) * (W / 8); idx += nth)
         *reinterpret_cast<uint4 *>(tile + swz_chunk(C, valid + idx / (W / 8), idx % (W / 8))) = make_uint4(0u, 0u, 0u, 0u);
 }
@@ -291,47 +303,54 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
     if (warp == 0) {
         // ---------------- TMA producer
         const CUtensorMap *mx = &maps.m[pi][0], *my = &maps.m[pi][1], *mz = &maps.m[pi][2];
-        int nx = 0, ny = 0, nz = 0;
+        Ring rx, ry, rz;
+        int nx = 0, ny = 0, nz = 0;   // issued
         bool ok = true;
-        for (int k = 0; ok && k < nchunk; ++k) {
-            const int c0 = chunk0(k);
-            for (int r = 0; ok && r < reps; ++r) {
-                const int hq = h * reps + r, hyz = many ? hq : h;
-                if (r == 0 || !many) {
-                    const int s = nx % NX;
-                    if (nx >= NX && !await(&x_empty[s], (nx / NX - 1) & 1, &abort_flag)) { ok = false; break; }
-                    uint8_t *x = xbuf + s * K::X_BYTES;
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(&x_full[s], K::X_BYTES);
+        int k = 0, r = 0;
+#pragma unroll 1
+        for (int it = 0; it < items; ++it) {
+            const int c0 = chunk0(k), hq = h * reps + r, hyz = many ? hq : h;
+            if (r == 0 || !many) {
+                // (the first use of a stage: the phase before the first counts as over)
+                if (!(ok = await(&x_empty[rx.s], rx.p ^ 1u, &abort_flag))) break;
+                if (elect_one()) {
+                    uint8_t *x = xbuf + rx.s * K::X_BYTES;
+                    mbar_arrive_expect_tx(&x_full[rx.s], K::X_BYTES);
 #pragma unroll
-                        for (int blk = 0; blk < DX / 64; ++blk)
-                            tma_load_4d(x + blk * C * 128, mx, &x_full[s], blk * 64, c0, many ? h : hq, b);
-                    }
-                    __syncwarp();
-                    ++nx;
+                    for (int blk = 0; blk < DX / 64; ++blk)
+                        tma_load_4d(x + blk * C * 128, mx, &x_full[rx.s], blk * 64, c0, many ? h : hq, b);
                 }
-                if (r == 0 || many) {
-                    const int s = ny % NY;
-                    if (ny >= NY && !await(&y_empty[s], (ny / NY - 1) & 1, &abort_flag)) { ok = false; break; }
-                    uint8_t *y = ybuf + s * K::Y_BYTES;
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(&y_full[s], K::Y_BYTES);
+                __syncwarp();
+                rx.next(NX);
+                ++nx;
+            }
+            if (r == 0 || many) {
+                if (!(ok = await(&y_empty[ry.s], ry.p ^ 1u, &abort_flag))) break;
+                if (elect_one()) {
+                    uint8_t *y = ybuf + ry.s * K::Y_BYTES;
+                    mbar_arrive_expect_tx(&y_full[ry.s], K::Y_BYTES);
 #pragma unroll
-                        for (int blk = 0; blk < DX / 64; ++blk) tma_load_4d(y + blk * C * 128, my, &y_full[s], blk * 64, c0, hyz, b);
-                    }
-                    __syncwarp();
-                    ++ny;
-                    const int sz = nz % NZ;
-                    if (nz >= NZ && !await(&z_empty[sz], (nz / NZ - 1) & 1, &abort_flag)) { ok = false; break; }
-                    uint8_t *z = zbuf + sz * K::Z_BYTES;
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(&z_full[sz], K::Z_BYTES);
-#pragma unroll
-                        for (int blk = 0; blk < DZ / 64; ++blk) tma_load_4d(z + blk * C * 128, mz, &z_full[sz], blk * 64, c0, hyz, b);
-                    }
-                    __syncwarp();
-                    ++nz;
+                    for (int blk = 0; blk < DX / 64; ++blk)
+                        tma_load_4d(y + blk * C * 128, my, &y_full[ry.s], blk * 64, c0, hyz, b);
                 }
+                __syncwarp();
+                ry.next(NY);
+                ++ny;
+                if (!(ok = await(&z_empty[rz.s], rz.p ^ 1u, &abort_flag))) break;
+                if (elect_one()) {
+                    uint8_t *z = zbuf + rz.s * K::Z_BYTES;
+                    mbar_arrive_expect_tx(&z_full[rz.s], K::Z_BYTES);
+#pragma unroll
+                    for (int blk = 0; blk < DZ / 64; ++blk)
+                        tma_load_4d(z + blk * C * 128, mz, &z_full[rz.s], blk * 64, c0, hyz, b);
+                }
+                __syncwarp();
+                rz.next(NZ);
+                ++nz;
+            }
+            if (++r == reps) {
+                r = 0;
+                ++k;
             }
         }
         for (int i = nx > NX ? nx - NX : 0; i < nx; ++i) warp_drain(&x_full[i % NX], (i / NX) & 1);
@@ -344,56 +363,63 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         constexpr uint32_t idA = idesc_bf16(128, C, false, false);
         constexpr uint32_t idO = idesc_bf16(128, DZ, false, true);
         const uint32_t tO = tm + K::T_O, sb = smem_u32(sbf);
-        int sx = 0, sy = 0, sk = 0, sr = 0, si = 0;   // of the next scores: x tile, y tile, chunk, head, item
-        auto scores_in = [&]() {
-            return is_over(&x_full[sx % NX], (sx / NX) & 1) && is_over(&y_full[sy % NY], (sy / NY) & 1);
-        };
-        int iz = 0, ot = 0, k = 0, r = 0;   // of the current item: z tile, output tile, chunk, head
-        bool ok = true;
+        // of the next scores: x and y tile, buffer, item, chunk, head
+        Ring sx, sy, sc;
+        int si = 0, sk = 0, sr = 0;
+        // of the item whose O is next: z tile, buffer, output tile (two barriers in turn, and one)
+        Ring iz, ic, it2;
+        uint32_t op = 1;
+        int it = 0, k = 0, r = 0;
+        // what can go next goes: the next item's scores when its tiles are in and a buffer is free, this item's O when
+        // its P is made
+        uint32_t idle = 0;
 #pragma unroll 1
-        for (int it = 0; it < items; ++it) {
-            // this item's scores if they are not out yet, and the next one's if its tiles are in
-#pragma unroll 1
-            while (ok && (si <= it || (NSC == 2 && si == it + 1 && si < items && scores_in()))) {
+        while (it < items) {
+            if (si < items && si < it + NSC && is_over(&x_full[sx.s], sx.p) && is_over(&y_full[sy.s], sy.p)) {
                 const bool first = sr == 0, last = sr == reps - 1;
-                ok = (!(first || !many) || await(&x_full[sx % NX], (sx / NX) & 1, &abort_flag)) &&
-                     (!(first || many) || await(&y_full[sy % NY], (sy / NY) & 1, &abort_flag)) &&
-                     // a tile with rows past the sequence's length (its last): those are zeroed first
-                     (!(p.lengths && first && sk == nchunk - 1 && vlast < C) || await(&zeroed, 0, &abort_flag));
-                if (!ok) break;
-                const uint32_t x = smem_u32(xbuf + (sx % NX) * K::X_BYTES), y = smem_u32(ybuf + (sy % NY) * K::Y_BYTES);
+                // a tile with rows past the sequence's length (its last): those are zeroed first
+                if (p.lengths && first && sk == nchunk - 1 && vlast < C && !await(&zeroed, 0, &abort_flag)) break;
+                const uint32_t x = smem_u32(xbuf + sx.s * K::X_BYTES), y = smem_u32(ybuf + sy.s * K::Y_BYTES);
                 tc_fence_after();
                 LA_TL(si, 0);
                 if (elect_one()) {
-                    mma_ss_kk<DX / 16>(tm + K::T_A + (si % NSC) * 128, desc_kmajor(x, C, 0, 0), desc_kmajor(y, C, 0, 0), idA);
-                    mma_commit(&sc_full[si % NSC]);
-                    if (YSM && (last || many)) mma_commit(&y_scored[sy % NY]);
+                    mma_ss_kk<DX / 16>(tm + K::T_A + sc.s * 128, desc_kmajor(x, C, 0, 0), desc_kmajor(y, C, 0, 0), idA);
+                    mma_commit(&sc_full[sc.s]);
+                    if (YSM && (last || many)) mma_commit(&y_scored[sy.s]);
                 }
                 __syncwarp();
                 LA_TL(si, 1);
-                if (last || !many) ++sx;
-                if (last || many) ++sy;
+                if (last || !many) sx.next(NX);
+                if (last || many) sy.next(NY);
+                sc.next(NSC);
                 ++si;
                 if (++sr == reps) {
                     sr = 0;
                     ++sk;
                 }
+                idle = 0;
+                continue;
             }
-            if (!ok) break;
+            if (si == it || !is_over(&p_ready[ic.s], ic.p)) {
+                if (++idle > kTries) {
+                    abort_flag = 1;
+                    break;
+                }
+                continue;
+            }
+            idle = 0;
             const bool first = r == 0, last = r == reps - 1;
             const bool opens = first || !many, ends = last || !many;   // an output tile
-            const uint32_t tA = tm + K::T_A + (it % NSC) * 128;
-            if ((first || many) && !await(&z_full[iz % NZ], (iz / NZ) & 1, &abort_flag)) break;
-            if (opens && ot > 0 && !await(&o_free, (ot - 1) & 1, &abort_flag)) break;
-            LA_TL(it, 2);
-            if (!await(&p_ready[it % NSC], (it / NSC) & 1, &abort_flag)) break;
             LA_TL(it, 4);
-            const uint32_t z = smem_u32(zbuf + (iz % NZ) * K::Z_BYTES);
+            if (!await(&z_full[iz.s], iz.p, &abort_flag)) break;
+            if (opens && !await(&o_free, op, &abort_flag)) break;   // (the first: the phase before it counts as over)
+            LA_TL(it, 2);
+            const uint32_t z = smem_u32(zbuf + iz.s * K::Z_BYTES), tA = tm + K::T_A + ic.s * 128;
             tc_fence_after();
             if (elect_one()) mma_ts_mn<C / 16>(tO, tA, desc_mnmajor(z, C, 0, 0), idO, opens ? 0u : 1u);
             __syncwarp();
             if (opens) {
-                if (!await(&xd_ready[ot % 2], (ot / 2) & 1, &abort_flag)) break;
+                if (!await(&xd_ready[it2.s], it2.p, &abort_flag)) break;
                 if (first && !await(&s_conv, k & 1, &abort_flag)) break;
                 LA_TL(it, 5);
                 tc_fence_after();
@@ -403,12 +429,17 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             if (elect_one()) {
                 if (ends) mma_commit(&o_full);
                 if (many ? first : last) mma_commit(&s_full);   // the chunk's last reader of S_bf
-                if (last || many) mma_commit(&z_empty[iz % NZ]);
+                if (last || many) mma_commit(&z_empty[iz.s]);
             }
             __syncwarp();
             LA_TL(it, 6);
-            if (ends) ++ot;
-            if (last || many) ++iz;
+            if (ends) {
+                it2.next(2);
+                op ^= 1u;
+            }
+            if (last || many) iz.next(NZ);
+            ic.next(NSC);
+            ++it;
             if (++r == reps) {
                 r = 0;
                 ++k;
@@ -422,36 +453,39 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         constexpr uint32_t idS = idesc_bf16(128, DZ, YSM, true);
         const uint32_t tS = tm + K::T_S;
         const int tiles = many ? items : nchunk, per = many ? reps : 1;
+        Ring ry, rz;
         int k = 0, r = 0;
 #pragma unroll 1
         for (int t = 0; t < tiles; ++t) {
             if (r == 0 && !await(&s_conv, k & 1, &abort_flag)) break;
-            if (!await(&z_full[t % NZ], (t / NZ) & 1, &abort_flag)) break;
-            if (!await(&yt_ready[t % NY], (t / NY) & 1, &abort_flag)) break;
+            if (!await(&z_full[rz.s], rz.p, &abort_flag)) break;
+            if (!await(&yt_ready[ry.s], ry.p, &abort_flag)) break;
             LA_TL(t, 3);
             tc_fence_after();
-            const uint32_t y = smem_u32(ybuf + (t % NY) * K::Y_BYTES), z = smem_u32(zbuf + (t % NZ) * K::Z_BYTES);
+            const uint32_t y = smem_u32(ybuf + ry.s * K::Y_BYTES), z = smem_u32(zbuf + rz.s * K::Z_BYTES);
             const bool ends = ++r == per;
             if (elect_one()) {
                 if constexpr (YSM) {
                     // (M = 128 rows d of which DX count: with 64 the others read what lies behind the tile)
                     mma_ss_mn8(tS, desc_mnmajor(y, C, 0, 0), desc_mnmajor(z, C, 0, 0), idS);
-                    mma_commit(&y_empty[t % NY]);
+                    mma_commit(&y_empty[ry.s]);
                 } else {
                     mma_ts_mn<C / 16>(tS, tm + K::T_YH, desc_mnmajor(z, C, 0, 0), idS, 1u);
                     if (exact) mma_ts_mn<C / 16>(tS, tm + K::T_YL, desc_mnmajor(z, C, 0, 0), idS, 1u);
                     mma_commit(&yt_done);
                 }
-                mma_commit(&z_empty[t % NZ]);
+                mma_commit(&z_empty[rz.s]);
                 if (ends) mma_commit(&s_full);
                 if constexpr (YSM) {   // the output goes where this z was, or not
                     if (o_in_z && ends)
                         mma_commit(&z_used[k % 2]);
                     else
-                        mbar_arrive_cnt(&z_empty[t % NZ], 4);
+                        mbar_arrive_cnt(&z_empty[rz.s], 4);
                 }
             }
             __syncwarp();
+            ry.next(NY);
+            rz.next(NZ);
             if (ends) {
                 r = 0;
                 ++k;
@@ -474,16 +508,23 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             tri[e] = ago >= 0 ? p.scale * pw[max(ago, 0)] : 0.f;
         }
         const bool low = lane < 16;
-        int r = 0, nx = 0, ny = 0, ot = 0;
+        Ring sc, rx, ry;
+        int r = 0, ot = 0;
 #pragma unroll 1
         for (int it = 0; it < items; ++it) {
-            if (!await(&sc_full[it % NSC], (it / NSC) & 1, &abort_flag)) break;
+            if (!await(&sc_full[sc.s], sc.p, &abort_flag)) break;
             tc_fence_after();
             if (i == 127) LA_TL(it, 7);
-            const uint32_t ta = tm + K::T_A + (it % NSC) * 128 + ((uint32_t)(wq * 32) << 16);
+            const uint32_t ta = tm + K::T_A + sc.s * 128 + ((uint32_t)(wq * 32) << 16);
             const bool first = r == 0, last = ++r == reps;
-            if (last || !many) mbar_arrive_w(&x_empty[nx++ % NX]);
-            if (!YSM && (last || many)) mbar_arrive_w(&y_empty[ny++ % NY]);
+            if (last || !many) {
+                mbar_arrive_w(&x_empty[rx.s]);
+                rx.next(NX);
+            }
+            if (!YSM && (last || many)) {
+                mbar_arrive_w(&y_empty[ry.s]);
+                ry.next(NY);
+            }
 #pragma unroll 1
             for (int cb = 0; cb < C / 32; ++cb) {
                 uint32_t w[16];
@@ -518,8 +559,9 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             tmem_st_wait();
             tc_fence_before();
             if (i == 127) LA_TL(it, 8);
-            mbar_arrive_warp(&p_ready[it % NSC]);
-            if (first || !many) mbar_arrive_warp(&p_first[ot++ % 2]);
+            mbar_arrive_warp(&p_ready[sc.s]);
+            sc.next(NSC);
+            if (first || !many) mbar_arrive_warp(&p_first[ot++ & 1]);
             if (last) r = 0;
         }
     } else if (warp >= 8 && warp < 12) {
@@ -639,38 +681,43 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         // gamma^(i + 1) with the factor as two bf16 terms, rounded once
         const int wq = warp % 4, i = wq * 32 + threadIdx.x % 32;
         const int tiles = many ? nchunk : items, step = many ? reps : 1;   // output tiles; items of each
+        Ring rx;
         int k = 0, r = 0;
 #pragma unroll 1
         for (int t = 0; t < tiles; ++t) {
             const int valid = min(C, part.hi - chunk0(k));
-            if (!await(&x_full[t % NX], (t / NX) & 1, &abort_flag)) break;
+            if (!await(&x_full[rx.s], rx.p, &abort_flag)) break;
             if (i == 0) LA_TL(t, 11);
+            const uint8_t *x = xbuf + rx.s * K::X_BYTES;
+            uint4 v[DX / 8];   // the row: its tile is free for the next load
+#pragma unroll
+            for (int c = 0; c < DX / 8; ++c) v[c] = *reinterpret_cast<const uint4 *>(x + swz_chunk(C, i, c));
+            mbar_arrive_w(&x_empty[rx.s]);
+            rx.next(NX);
             const float g = p.scale * pw[max((rev ? valid - i : i + 1) - (k == 0 ? off0 : 0), 0)];
             const __nv_bfloat162 gh = as_bf162(pack_bf16x2(g, g));
             const float gr = g - unpack_bf16x2(as_u32(gh)).x;
             const __nv_bfloat162 gl = as_bf162(pack_bf16x2(gr, gr));
-            const uint8_t *x = xbuf + (t % NX) * K::X_BYTES;
-            if (!await(&p_first[t % 2], (t / 2) & 1, &abort_flag)) break;
+            if (!await(&p_first[t & 1], (t >> 1) & 1, &abort_flag)) break;
             tc_fence_after();
             const uint32_t tx = tm + K::T_A + ((t * step) % NSC) * 128 + 64 + ((uint32_t)(wq * 32) << 16);
-#pragma unroll 1
+#pragma unroll
             for (int q = 0; q < DX / 32; ++q) {
                 uint32_t w[16];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(x + swz_chunk(C, i, 4 * q + c));
-                    const uint32_t a[4] = {v.x, v.y, v.z, v.w};
+                    const uint4 u4 = v[4 * q + c];
+                    const uint32_t a[4] = {u4.x, u4.y, u4.z, u4.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         w[4 * c + e] = as_u32(__hfma2(as_bf162(a[e]), gh, __hmul2(as_bf162(a[e]), gl)));
                 }
                 tmem_st16_raw(tx + q * 16, w);
             }
-            mbar_arrive_w(&x_empty[t % NX]);
             tmem_st_wait();
             tc_fence_before();
             if (i == 0) LA_TL(t, 12);
-            mbar_arrive_warp(&xd_ready[t % 2]);
+            mbar_arrive_warp(&xd_ready[t & 1]);
             if (many || ++r == reps) {
                 r = 0;
                 ++k;
@@ -686,12 +733,12 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         int k = 0, r = 0;
 #pragma unroll 1
         for (int t = 0; t < tiles; ++t) {
-            const int c0 = chunk0(k), valid = min(C, part.hi - c0), zi = (many ? (t + 1) * reps - 1 : t) % NZ;
+            const int c0 = chunk0(k), valid = min(C, part.hi - c0), zi = o_in_z ? (many ? (t + 1) * reps - 1 : t) % NZ : 0;
             uint8_t *o = o_in_z ? zbuf + zi * K::Z_BYTES : obuf + (NO > 1 ? t % NO : 0) * K::O_BYTES;
             if (!await(&o_full, t & 1, &abort_flag)) break;
             tc_fence_after();
             if (i == 0) LA_TL(t, 13);
-            if (o_in_z && !await(&z_used[t % 2], (t / 2) & 1, &abort_flag)) break;
+            if (o_in_z && !await(&z_used[t & 1], (t >> 1) & 1, &abort_flag)) break;
             bulk_wait_read_but<(NO > 1 ? NO - 1 : 0)>();   // (of the elected lane)
             __syncwarp();
 #pragma unroll 1
@@ -744,18 +791,19 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         YtWeights w;
         __nv_bfloat162 gh, gl;
         bool shorter = false;
+        Ring ry, rz;
         int k = 0, r = 0;
 #pragma unroll 1
         for (int t = 0; t < tiles; ++t) {
             const int c0 = chunk0(k), valid = min(C, part.hi - c0);
-            uint8_t *y = ybuf + (t % NY) * K::Y_BYTES;
+            uint8_t *y = ybuf + ry.s * K::Y_BYTES;
             if (!YSM || p.lengths)
-                if (!await(&y_full[t % NY], (t / NY) & 1, &abort_flag)) break;
+                if (!await(&y_full[ry.s], ry.p, &abort_flag)) break;
             if (p.lengths) {
-                if (!await(&z_full[t % NZ], (t / NZ) & 1, &abort_flag)) break;
+                if (!await(&z_full[rz.s], rz.p, &abort_flag)) break;
                 if (valid < C) {
                     zero_rows<DX>(y, valid, j, 128);
-                    zero_rows<DZ>(zbuf + (t % NZ) * K::Z_BYTES, valid, j, 128);
+                    zero_rows<DZ>(zbuf + rz.s * K::Z_BYTES, valid, j, 128);
                     fence_proxy_async();
                     mbar_arrive_warp(&zeroed);
                     // (the warps read one another's zeros)
@@ -772,7 +820,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                     const float gr = g - unpack_bf16x2(as_u32(gh)).x;
                     gl = as_bf162(pack_bf16x2(gr, gr));
                 }
-                if (!await(&y_scored[t % NY], (t / NY) & 1, &abort_flag)) break;
+                if (!await(&y_scored[ry.s], ry.p, &abort_flag)) break;
 #pragma unroll 4
                 for (int c = 0; c < DX / 8; ++c) {
                     uint4 *q = reinterpret_cast<uint4 *>(y + swz_chunk(C, j, c));
@@ -792,11 +840,13 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                     yt_tile(y, wq * 32, w, exact, tm + K::T_YH + lane_off, tm + K::T_YL + lane_off);
                     tmem_st_wait();
                 }
-                mbar_arrive_w(&y_empty[t % NY]);
+                mbar_arrive_w(&y_empty[ry.s]);
                 tc_fence_before();
             }
             if (threadIdx.x == 640) LA_TL(t, 15);
-            mbar_arrive_warp(&yt_ready[t % NY]);
+            mbar_arrive_warp(&yt_ready[ry.s]);
+            ry.next(NY);
+            rz.next(NZ);
             if (!many || ++r == reps) {
                 r = 0;
                 ++k;
