@@ -23,49 +23,86 @@ la_status check(int B, int Hq, int Hkv, int N, int D, int Dv, int dtype, float s
 struct DecayPlan {
     la_path path;
     int seg_len, nseg;
-    int nsub, sub_len;                          // tensor cores: parts of a segment that the state kernel sums
+    long long state_units;                      // sequences that the state kernel sums
     size_t state_bytes, part_bytes, ws_bytes;   // one array of segment states, one of their parts; all of them
 };
 
 bool tc_runs(int D, int Dv, la_dtype dt) { return dt == LA_BF16 && D != 32 && Dv != 32; }
 
-// The segments of a sequence: the count whose schedule ends first.  A schedule is waves of `places` blocks that
-// run at once, a block costing its chunks (`work` each) plus about two for its start; more than
-// one segment costs the kernel that sums them (state_units blocks of state_work a chunk).
+// The parts of a segment that the state kernel sums in blocks of their own: as many as one wave takes.
+struct Parts {
+    int n, len;
+};
+Parts sum_parts(long long units, int nsum, int chunks) {
+    const long long fit = kPlanSms / (units * nsum);
+    const int want = fit < 1 ? 1 : fit < chunks ? (int)fit : chunks;
+    const int per = (chunks + want - 1) / want;
+    return Parts{(chunks + per - 1) / per, per * kDecayTcChunk};
+}
+
+// The segments of a sequence: the count whose schedule ends first.  A schedule is waves of blocks that run at once,
+// a block costing its start and its chunks (a chunk more where two blocks share an SM), and at least what the memory
+// traffic takes; more than one segment costs the kernels that sum and join them.  Times in microseconds, fitted to
+// GB300: on the tensor cores (one block an SM) 64 chunks of 128 x 128 take 157 us, 32 of 64 x 64 67 us, sums of 8
+// chunks 128 x 128 20 us; on the CUDA cores 64 chunks of 64 x 64 362 us with one block an SM and 610 us with two.
+struct Cost {
+    int per_sm;                      // blocks an SM holds
+    double start, chunk, pair;       // of a block: its start, a chunk, a chunk's factor beside another block
+    double waves(long long blocks, int chunks) const {
+        const long long full = blocks / (per_sm * kPlanSms), rest = blocks % (per_sm * kPlanSms);
+        return full * (start + chunks * chunk * pair) + (rest ? start + chunks * chunk * (rest > kPlanSms ? pair : 1.0) : 0.0);
+    }
+};
+
 DecayPlan make_plan(int B, int Hq, int Hkv, int N, int D, int Dv, la_dtype dt, bool bwd) {
     DecayPlan pl{};
     const int reps = Hq / Hkv;
     const long long heads = (long long)B * Hkv;
-    long long units, state_units;
-    int places, chunk, most;
-    double work, state_work;
+    long long units, state_units;                  // blocks of a segment: of the passes, of the sums
+    int chunk;
+    Cost pass, sum;
+    double bytes = 0.0, s_bytes = 0.0;             // of a chunk over all blocks
+    double join, join_seg;                         // the sums' join, and of it each segment
+    const double rate = 5.8e6;                     // bytes a microsecond
     if (tc_runs(D, Dv, dt)) {
-        // in units of one chunk's x, y, z and out tiles
         pl.path = LA_PATH_TCGEN05;
         chunk = kDecayTcChunk;
-        places = kPlanSms;
         units = heads * (bwd ? 3 : 1);
-        work = (2.0 * reps + 2.0) / 4.0;
+        pass = Cost{1, 6.0, reps * (D + Dv == 256 ? 2.4 : D + Dv == 192 ? 2.2 : 2.0), 1.0};
+        // q, k, v and out; the gradients: three passes of as much (their common inputs from L2 in part)
+        bytes = chunk * 2.0 * heads * ((reps + 1.0) * (D + Dv)) * (bwd ? 2.5 : 1.0);
         state_units = heads * (bwd ? 2 : 1);
-        state_work = bwd ? (2.0 * reps + 2.0) / 8.0 : 0.5;
-        most = 256;
+        sum = Cost{1, 7.0, (bwd ? (reps + 1.0) / 2.0 : 1.0) * (D + Dv == 256 ? 1.4 : D + Dv == 192 ? 1.1 : 0.8), 1.0};
+        s_bytes = chunk * 2.0 * heads * (D + Dv) * (bwd ? reps + 1.0 : 1.0);
+        join = 5.0;
+        join_seg = 0.2;
     } else {
         pl.path = LA_PATH_SIMT;
         chunk = 32;
-        places = 3 * kPlanSms;
-        units = heads * ((bwd ? (D > Dv ? D : Dv) : Dv) / kDecaySimtSlice);
-        work = 1.0;
-        state_units = heads * (Dv / kDecaySimtSlice) * (bwd ? 2 : 1);
-        state_work = 0.4;
-        most = 64;
+        const int wide = D > Dv ? D : Dv, DZ = bwd ? wide : Dv;
+        units = heads * (DZ / decay_simt_slice(DZ)) * (bwd ? 3 : 1);
+        pass = Cost{2, 3.0, reps * (0.5 + 0.085 * wide), 1.7};
+        state_units = heads * (Dv / decay_simt_slice(Dv)) * (bwd ? 2 : 1);
+        sum = Cost{2, 4.0, (bwd ? reps : 1) * (0.4 + 0.026 * D), 1.7};
+        join = 0.0;
+        join_seg = 0.5;   // (each block of a pass sums the segments before its own)
     }
     const int nchunks = (N + chunk - 1) / chunk;
     double best = -1.0;
     int best_cps = nchunks;
+    // (past a few waves more segments only cost)
+    const long long most = 4 * pass.per_sm * kPlanSms / units + 2;
     for (int want = 1; want <= nchunks && want <= most; ++want) {
         const int cps = (nchunks + want - 1) / want, nseg = (nchunks + cps - 1) / cps;
-        double cost = (double)((units * nseg + places - 1) / places) * (cps * work + 2.0);
-        if (nseg > 1) cost += (double)((state_units * (nseg - 1) + places - 1) / places) * (cps * state_work + 2.0);
+        const double mem = nchunks * bytes / rate;
+        double cost = pass.waves(units * nseg, cps);
+        if (cost < mem) cost = mem;
+        if (nseg > 1) {
+            const Parts parts = pl.path == LA_PATH_SIMT ? Parts{1, 0} : sum_parts(state_units, nseg - 1, cps);
+            const double smem = nchunks * s_bytes / rate;
+            const double sc = sum.waves(state_units * (nseg - 1) * parts.n, (cps + parts.n - 1) / parts.n);
+            cost += (sc < smem ? smem : sc) + join + join_seg * nseg;
+        }
         if (best < 0 || cost < best) {
             best = cost;
             best_cps = cps;
@@ -79,14 +116,11 @@ DecayPlan make_plan(int B, int Hq, int Hkv, int N, int D, int Dv, la_dtype dt, b
         pl.ws_bytes = pl.state_bytes * (bwd ? 2 : 1);
         return pl;
     }
-    // as many parts as one wave of the state kernel takes
-    const long long sums = state_units * (pl.nseg - 1);
-    int nsub = (int)(places / (sums < places ? sums : places));
-    if (nsub > best_cps) nsub = best_cps;
-    const int spc = (best_cps + nsub - 1) / nsub;
-    pl.nsub = (best_cps + spc - 1) / spc;
-    pl.sub_len = spc * chunk;
-    pl.part_bytes = ((size_t)heads * (pl.nseg - 1) * pl.nsub * D * Dv * 4 + 255) / 256 * 256;
+    // room for the parts of all segments (with a final state) and of all but the last
+    pl.state_units = state_units;
+    const int n0 = (pl.nseg - 1) * sum_parts(state_units, pl.nseg - 1, best_cps).n,
+              n1 = pl.nseg * sum_parts(state_units, pl.nseg, best_cps).n;
+    pl.part_bytes = ((size_t)heads * (n0 > n1 ? n0 : n1) * D * Dv * 4 + 255) / 256 * 256;
     // forward: S; backward: S^T, A and A^T
     pl.ws_bytes = pl.state_bytes * (bwd ? 3 : 1) + pl.part_bytes * (bwd ? 2 : 1);
     return pl;
@@ -152,14 +186,22 @@ la_status run(bool bwd, const Given &a, int B, int Hq, int Hkv, int N, int D, in
     sp.y[0] = a.k; sp.z[0] = a.v; sp.sy[0] = sk; sp.sz[0] = sv; sp.init[0] = a.s_in; sp.init_mul[0] = 1.f;
     sp.heads[0] = 1; sp.rev[0] = 0; sp.slots[0] = slots0; sp.exact[0] = a.s_out != nullptr;
     sp.n = 1;
-    sp.nsub = pl.nsub; sp.sub_len = pl.sub_len;
+    // on the tensor cores a cut sequence's last state comes with the segments' sums, else with the pass itself
+    const bool main_fin = !tc || pl.nseg == 1;
+    sp.fin[0] = a.s_out; sp.fin[1] = a.ds_out; sp.fin_mul[0] = 1.f; sp.fin_mul[1] = scale;
+    sp.nsum = a.s_out || a.ds_out ? pl.nseg : pl.nseg - 1;
+    if (tc && pl.nseg > 1) {
+        const Parts parts = sum_parts(pl.state_units, sp.nsum, pl.seg_len / kDecayTcChunk);
+        sp.nsub = parts.n;
+        sp.sub_len = parts.len;
+    }
     sp.part[0] = at(pl.state_bytes * (bwd ? 3 : 1));
     sp.part[1] = at(pl.state_bytes * 3 + pl.part_bytes);
     if (!bwd) {
         sp.start[0] = slots0;
         DecayPass &f = p.pass[0];
         f.x = a.q; f.y = a.k; f.z = a.v; f.sx = sq; f.sy = sk; f.sz = sv; f.out = a.out;
-        f.slots = slots0; f.init = a.s_in; f.fin = a.s_out; f.init_mul = f.fin_mul = 1.f;
+        f.slots = slots0; f.init = a.s_in; f.fin = main_fin ? a.s_out : nullptr; f.init_mul = f.fin_mul = 1.f;
         p.npass = 1;
     } else {
         // A = sum q g^T from the last token back
@@ -174,7 +216,7 @@ la_status run(bool bwd, const Given &a, int B, int Hq, int Hkv, int N, int D, in
         k.x = a.v; k.y = a.g; k.z = a.q; k.sx = sv; k.sy = sg; k.sz = sq; k.out = a.dk;
         k.slots = slots2; k.init = a.ds_in; k.tr = 1;
         v.x = a.k; v.y = a.q; v.z = a.g; v.sx = sk; v.sy = sq; v.sz = sg; v.out = a.dv;
-        v.slots = slots1; v.init = a.ds_in; v.fin = a.ds_out;
+        v.slots = slots1; v.init = a.ds_in; v.fin = main_fin ? a.ds_out : nullptr;
         for (DecayPass *ps : {&k, &v}) {
             ps->many_yz = 1;
             ps->rev = 1;
@@ -195,7 +237,13 @@ la_status run(bool bwd, const Given &a, int B, int Hq, int Hkv, int N, int D, in
         return e == cudaSuccess ? LA_OK : cuda_fail(e);
     }
     if (pl.nseg > 1) e = decay_simt_states(sp, dt, s);
-    for (int i = 0; e == cudaSuccess && i < p.npass; ++i) e = decay_simt_pass(p, i, dt, s);
+    // (the gradients' passes have two shapes of state, D x Dv and its transpose)
+    if (e == cudaSuccess && (p.npass == 1 || D == Dv)) {
+        e = decay_simt_passes(p, 0, p.npass, dt, s);
+    } else if (e == cudaSuccess) {
+        e = decay_simt_passes(p, 0, 2, dt, s);
+        if (e == cudaSuccess) e = decay_simt_passes(p, 2, 1, dt, s);
+    }
     return e == cudaSuccess ? LA_OK : cuda_fail(e);
 }
 
@@ -208,7 +256,11 @@ extern "C" {
 
 size_t la_decay_workspace_size(int B, int Hq, int Hkv, int N, int D, int Dv, la_dtype dtype, int is_bwd) {
     if (check(B, Hq, Hkv, N, D, Dv, dtype, 1.f) != LA_OK) return 0;
-    return make_plan(B, Hq, Hkv, N, D, Dv, dtype, is_bwd).ws_bytes;
+    // (a training step's one workspace serves its forward too, which may be cut into more segments)
+    const size_t fwd = make_plan(B, Hq, Hkv, N, D, Dv, dtype, false).ws_bytes;
+    if (!is_bwd) return fwd;
+    const size_t bwd = make_plan(B, Hq, Hkv, N, D, Dv, dtype, true).ws_bytes;
+    return fwd > bwd ? fwd : bwd;
 }
 
 la_path la_decay_kernel_path(int B, int Hq, int Hkv, int N, int D, int Dv, la_dtype dtype, int is_bwd) {

@@ -50,8 +50,8 @@ struct DecayParams {
 // The sums over single segments that later segments start from: for segment u, the sum of
 // gamma^(tokens after j in the segment) y_j z_j^T (over the heads of y, z), a state D x Dv.
 // CUDA cores: in slot u + 1, [D][Dv], with the starting state (times init_mul) in slot 0.
-// Tensor cores: each segment but the last in nsub parts (more blocks than segments: the kernel is short), in
-// part[(nseg - 1) nsub], lane-blocked; decay_tc_join() then makes the segments' starting states of them.
+// Tensor cores: the first nsum segments in nsub parts each (more blocks than segments: the kernel is short), in
+// part[nsum nsub], lane-blocked; decay_tc_join() then makes the segments' starting states of them.
 struct DecayStateParams {
     const float *log_decay;
     const int *lengths;
@@ -63,6 +63,9 @@ struct DecayStateParams {
     int rev[2];
     float *slots[2];
     int exact[2];               // a float32 state that the caller gets depends on these sums (tensor cores)
+    float *fin[2];              // tensor cores: the state after the last segment, or null (its sum is taken
+    float fin_mul[2];           // too then: nsum = nseg segments)
+    int nsum;
     int n;                      // state arrays of this launch (1 or 2)
     int B, Hkv, N, D, Dv, seg_len, nseg;
     int nsub, sub_len;          // tensor cores: parts of a segment
@@ -89,9 +92,9 @@ __device__ __forceinline__ float decay_log2(float log_decay) {
 }
 
 // CUDA-core kernels (la_decay_simt.cu): every dtype, width and stride.
-constexpr int kDecaySimtSlice = 32;   // columns of out that a block owns
+inline int decay_simt_slice(int DZ) { return DZ < 64 ? DZ : 64; }   // columns of out that a block owns
 cudaError_t decay_simt_states(const DecayStateParams &p, la_dtype dt, cudaStream_t s);
-cudaError_t decay_simt_pass(const DecayParams &p, int pass, la_dtype dt, cudaStream_t s);
+cudaError_t decay_simt_passes(const DecayParams &p, int pass0, int npass, la_dtype dt, cudaStream_t s);
 
 // Tensor-core kernels (la_decay_tc.cu): bfloat16, widths 64 and 128.  Segments are cut in token
 // order, multiples of kDecayTcChunk tokens; every pass of a call in one launch where the widths allow.

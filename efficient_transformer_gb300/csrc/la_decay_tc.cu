@@ -233,19 +233,6 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
     pdl_wait();
     const int warp = threadIdx.x / 32;
     const int pi = pass0 + blockIdx.x % npass, rest = blockIdx.x / npass;
-    const DecayPass &ps = p.pass[pi];
-    const int u = rest % p.nseg, bg = rest / p.nseg, b = bg / p.Hkv, h = bg % p.Hkv;
-    const int n = decay_tokens(p.lengths, b, p.N), rev = ps.rev, many = ps.many_yz, reps = p.n_rep;
-    const int NY = YSM && !many && reps > 1 ? 1 : NYS;        // stages of y in use
-    const bool o_in_z = YSM && (many || reps == 1);           // output tiles are staged in z's
-    const Part part = part_of(n, p.N, u, p.nseg, p.seg_len, rev);
-    const int nchunk = (part.hi - part.lo + C - 1) / C;
-    const int off0 = u == 0 ? ps.first_off : 0;   // of the first chunk
-    const float l2 = decay_log2(p.log_decay[h]);
-    auto chunk0 = [&](int k) { return part.lo + C * (rev ? nchunk - 1 - k : k); };
-    // tokens of the short chunk (the last in token order)
-    const int vlast = part.hi - part.lo - C * (nchunk - 1);
-
     if (threadIdx.x == 0) {
         abort_flag = 0;
         for (int s = 0; s < NX; ++s) {
@@ -283,15 +270,28 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         fence_barrier_init();
     }
     if (threadIdx.x >= 96 && threadIdx.x < 100) tma_prefetch_map(&maps.m[pi][threadIdx.x - 96]);
+    if (warp == 1) {
+        tmem_alloc(&tmem_base, 512);
+        tmem_relinquish();
+    }
+    const DecayPass &ps = p.pass[pi];
+    const int u = rest % p.nseg, bg = rest / p.nseg, b = bg / p.Hkv, h = bg % p.Hkv;
+    const int n = decay_tokens(p.lengths, b, p.N), rev = ps.rev, many = ps.many_yz, reps = p.n_rep;
+    const int NY = YSM && !many && reps > 1 ? 1 : NYS;        // stages of y in use
+    const bool o_in_z = YSM && (many || reps == 1);           // output tiles are staged in z's
+    const Part part = part_of(n, p.N, u, p.nseg, p.seg_len, rev);
+    const int nchunk = (part.hi - part.lo + C - 1) / C;
+    const int off0 = u == 0 ? ps.first_off : 0;   // of the first chunk
+    const float l2 = decay_log2(p.log_decay[h]);
+    auto chunk0 = [&](int k) { return part.lo + C * (rev ? nchunk - 1 - k : k); };
+    // tokens of the short chunk (the last in token order)
+    const int vlast = part.hi - part.lo - C * (nchunk - 1);
+
     for (int i = threadIdx.x; i <= C; i += kMainThreads) pw[i] = exp2f(l2 * i);
     // powers that the tokens of a chunk have ahead of them: full chunks, and the short one
     for (int i = threadIdx.x; i < 2 * C; i += kMainThreads) {
         const int j = i % C, v = i < C ? C : vlast;
         wtab[i / C][j] = j < v ? exp2f(l2 * (rev ? j : v - 1 - j)) : 0.f;
-    }
-    if (warp == 1) {
-        tmem_alloc(&tmem_base, 512);
-        tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
@@ -677,8 +677,8 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                 }
         }
     } else if (warp >= 12 && warp < 16) {
-        // ---------------- the decayed X, thread = row i, where the scores have been read (beside P Z): scale x
-        // gamma^(i + 1) with the factor as two bf16 terms, rounded once
+        // ---------------- the decayed X, thread = row i: made in registers while P is under way, stored where the
+        // scores have been read.  scale x gamma^(i + 1) with the factor as two bf16 terms: one rounding
         const int wq = warp % 4, i = wq * 32 + threadIdx.x % 32;
         const int tiles = many ? nchunk : items, step = many ? reps : 1;   // output tiles; items of each
         Ring rx;
@@ -689,31 +689,26 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             if (!await(&x_full[rx.s], rx.p, &abort_flag)) break;
             if (i == 0) LA_TL(t, 11);
             const uint8_t *x = xbuf + rx.s * K::X_BYTES;
-            uint4 v[DX / 8];   // the row: its tile is free for the next load
-#pragma unroll
-            for (int c = 0; c < DX / 8; ++c) v[c] = *reinterpret_cast<const uint4 *>(x + swz_chunk(C, i, c));
-            mbar_arrive_w(&x_empty[rx.s]);
-            rx.next(NX);
             const float g = p.scale * pw[max((rev ? valid - i : i + 1) - (k == 0 ? off0 : 0), 0)];
             const __nv_bfloat162 gh = as_bf162(pack_bf16x2(g, g));
             const float gr = g - unpack_bf16x2(as_u32(gh)).x;
             const __nv_bfloat162 gl = as_bf162(pack_bf16x2(gr, gr));
+            uint32_t w[DX / 2];
+#pragma unroll
+            for (int c = 0; c < DX / 8; ++c) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(x + swz_chunk(C, i, c));
+                const uint32_t a[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[4 * c + e] = as_u32(__hfma2(as_bf162(a[e]), gh, __hmul2(as_bf162(a[e]), gl)));
+            }
+            mbar_arrive_w(&x_empty[rx.s]);   // the tile is free for the next load
+            rx.next(NX);
             if (!await(&p_first[t & 1], (t >> 1) & 1, &abort_flag)) break;
             tc_fence_after();
             const uint32_t tx = tm + K::T_A + ((t * step) % NSC) * 128 + 64 + ((uint32_t)(wq * 32) << 16);
 #pragma unroll
-            for (int q = 0; q < DX / 32; ++q) {
-                uint32_t w[16];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint4 u4 = v[4 * q + c];
-                    const uint32_t a[4] = {u4.x, u4.y, u4.z, u4.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        w[4 * c + e] = as_u32(__hfma2(as_bf162(a[e]), gh, __hmul2(as_bf162(a[e]), gl)));
-                }
-                tmem_st16_raw(tx + q * 16, w);
-            }
+            for (int q = 0; q < DX / 32; ++q) tmem_st16_raw(tx + q * 16, w + 16 * q);
             tmem_st_wait();
             tc_fence_before();
             if (i == 0) LA_TL(t, 12);
@@ -904,7 +899,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
     uint8_t *stage = align1024(smem_raw), *lo_tile = stage + NS * K::STAGE;
     pdl_wait();
     const int warp = threadIdx.x / 32;
-    const int nparts = (p.nseg - 1) * p.nsub, pidx = blockIdx.x % nparts, ah = blockIdx.x / nparts;
+    const int nparts = p.nsum * p.nsub, pidx = blockIdx.x % nparts, ah = blockIdx.x / nparts;
     const int a = ah / (p.B * p.Hkv), bg = ah % (p.B * p.Hkv), b = bg / p.Hkv, h = bg % p.Hkv;
     const int n = decay_tokens(p.lengths, b, p.N), rev = p.rev[a], heads = p.heads[a];
     const bool exact = p.exact[a];
@@ -1046,7 +1041,8 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
 }
 
 // ---------------------------------------------------------------------------------------
-// Starting states of the segments: T = the given state, then for each segment T = gamma^tokens T + its sum, a
+// Starting states of the segments, and the last state where it is an output: T = the given state, then for each segment T =
+// gamma^tokens T + its sum, a
 // thread carrying 4 x 4 elements; all states lane-blocked but the caller's.
 constexpr int kJoinThreads = 64;
 
@@ -1057,7 +1053,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_decay_join(const __grid_consta
     const int ah = blockIdx.x / kBlocks, a = ah / (p.B * p.Hkv), bg = ah % (p.B * p.Hkv), b = bg / p.Hkv, h = bg % p.Hkv;
     const int idx = blockIdx.x % kBlocks * kJoinThreads + threadIdx.x, d = idx % (D / 4) * 4, e = idx / (D / 4) * 4;
     constexpr size_t E = (size_t)D * DV;
-    const int n = decay_tokens(p.lengths, b, p.N), nparts = (p.nseg - 1) * p.nsub;
+    const int n = decay_tokens(p.lengths, b, p.N), nparts = p.nsum * p.nsub;
     const float l2 = decay_log2(p.log_decay[h]);
     float4 t[4];   // rows d .. d + 3, columns e .. e + 3
 #pragma unroll
@@ -1107,8 +1103,16 @@ __global__ void __launch_bounds__(kJoinThreads) k_decay_join(const __grid_consta
             for (int i = 0; i < 4; ++i)
                 t[i] = make_float4(fmaf(g, t[i].x, x[j][i].x), fmaf(g, t[i].y, x[j][i].y), fmaf(g, t[i].z, x[j][i].z),
                                    fmaf(g, t[i].w, x[j][i].w));
-            if (s == p.nsub - 1) store(u + 1);
+            if (s == p.nsub - 1 && u + 1 < p.nseg) store(u + 1);
         }
+    }
+    if (p.fin[a]) {
+        // all segments summed: the state after the last token (what leaves a reverse pass decays once more)
+        const float m = p.fin_mul[a] * (p.first_off[a] && n > 0 ? exp2f(l2 * p.first_off[a]) : 1.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4 *>(p.fin[a] + bg * E + (size_t)(d + i) * DV + e) =
+                make_float4(t[i].x * m, t[i].y * m, t[i].z * m, t[i].w * m);
     }
 }
 
@@ -1138,8 +1142,8 @@ cudaError_t passes(const DecayParams &p, int pass0, int npass, cudaStream_t s) {
     const bool tr = p.pass[pass0].tr;
     const int DX = tr ? p.Dv : p.D, DZ = tr ? p.D : p.Dv;
     if (DZ == 64) return DX == 64 ? passes_d<64, 64, false>(p, pass0, npass, s) : passes_d<128, 64, false>(p, pass0, npass, s);
-    // 128 columns of S and O leave no room in TMEM for two buffers of scores and Y^T; where the state is not an
-    // output y is decayed in shared memory instead, once rounded
+    // 128 columns of S and O leave no room in TMEM for two buffers of scores and Y^T; where this kernel's state is not
+    // an output (it is in one segment only) y is decayed in shared memory instead, once rounded
     bool exact = false;
     for (int i = pass0; i < pass0 + npass; ++i) exact = exact || p.pass[i].fin;
     if (exact) return DX == 64 ? passes_d<64, 128, false>(p, pass0, npass, s) : passes_d<128, 128, false>(p, pass0, npass, s);
@@ -1158,7 +1162,7 @@ cudaError_t states_d(const DecayStateParams &p, cudaStream_t s) {
     cudaError_t e = prepare(kern, StateCfg<D, DV>::SMEM);
     if (e != cudaSuccess) return e;
     TraceScope tr("decay_tc_state", s);
-    return launch_pdl(kern, dim3((unsigned)p.n * (p.nseg - 1) * p.nsub * p.B * p.Hkv), dim3(kStateThreads), StateCfg<D, DV>::SMEM, s,
+    return launch_pdl(kern, dim3((unsigned)p.n * p.nsum * p.nsub * p.B * p.Hkv), dim3(kStateThreads), StateCfg<D, DV>::SMEM, s,
                       maps, p);
 }
 
