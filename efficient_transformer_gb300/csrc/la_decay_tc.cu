@@ -102,17 +102,15 @@ struct MainCfg {
     static_assert((YSM ? T_YH : T_YL + 64) <= 512, "TMEM columns");
 };
 
-// A block's part of the sequence: tokens [lo, hi), `before` tokens of the sequence precede it in the pass's
-// order.
+// A block's part of the sequence: tokens [lo, hi).
 struct Part {
-    int lo, hi, before;
+    int lo, hi;
 };
 __device__ __forceinline__ Part part_of(int n, int N, int u, int nseg, int seg_len, int rev) {
     const int s = rev ? nseg - 1 - u : u;
     Part r;
     r.lo = min(n, s * seg_len);
     r.hi = min(n, r.lo + seg_len);
-    r.before = rev ? n - r.hi : r.lo;
     return r;
 }
 
@@ -123,7 +121,6 @@ __device__ __forceinline__ Part sub_part_of(int n, int N, int u, int nseg, int s
     Part r;
     r.lo = min(n, s * seg_len + min(seg_len, q * sub_len));
     r.hi = min(n, s * seg_len + min(seg_len, (q + 1) * sub_len));
-    r.before = rev ? n - r.hi : r.lo;
     return r;
 }
 

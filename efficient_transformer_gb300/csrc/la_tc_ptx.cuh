@@ -317,8 +317,7 @@ template <int N> __device__ __forceinline__ void bulk_wait_read_but() {
 // K-major tile of 128 rows: 2 a K step, 1024 from one 64-column block to the next (4 K steps); MN-major
 // tile (rows = K): 128 a K step, whatever its height.
 
-// A in tensor memory: row m in lane m, two consecutive K elements in each 32-bit column, 8 columns a K step; with
-// RUN = 4 every four K steps are 64 columns apart.
+// A in tensor memory: row m in lane m, two consecutive K elements in each 32-bit column, 8 columns a K step.
 #define LA_TS_STEP(i, col, pred)                                                 \
     "add.u32 ta, %1, " #col ";\n\tadd.s64 db, %2, (" #i " * 128);\n\t"            \
     "tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %3, " pred ";\n\t"
@@ -328,18 +327,15 @@ template <int N> __device__ __forceinline__ void bulk_wait_read_but() {
                  ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) \
                  : "memory")
 // D (+)= A B, A in TMEM at a_tmem, B an MN-major tile.
-template <int KSTEPS, int RUN = 8>
+template <int KSTEPS>
 __device__ __forceinline__ void mma_ts_mn(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                           uint32_t accumulate) {
     static_assert(KSTEPS == 4 || KSTEPS == 8, "K steps");
     if constexpr (KSTEPS == 4)
         LA_TS_MMA(LA_TS_STEP(0, 0, "p") LA_TS_STEP(1, 8, "t") LA_TS_STEP(2, 16, "t") LA_TS_STEP(3, 24, "t"));
-    else if constexpr (RUN == 8)
-        LA_TS_MMA(LA_TS_STEP(0, 0, "p") LA_TS_STEP(1, 8, "t") LA_TS_STEP(2, 16, "t") LA_TS_STEP(3, 24, "t")
-                  LA_TS_STEP(4, 32, "t") LA_TS_STEP(5, 40, "t") LA_TS_STEP(6, 48, "t") LA_TS_STEP(7, 56, "t"));
     else
         LA_TS_MMA(LA_TS_STEP(0, 0, "p") LA_TS_STEP(1, 8, "t") LA_TS_STEP(2, 16, "t") LA_TS_STEP(3, 24, "t")
-                  LA_TS_STEP(4, 64, "t") LA_TS_STEP(5, 72, "t") LA_TS_STEP(6, 80, "t") LA_TS_STEP(7, 88, "t"));
+                  LA_TS_STEP(4, 32, "t") LA_TS_STEP(5, 40, "t") LA_TS_STEP(6, 48, "t") LA_TS_STEP(7, 56, "t"));
 }
 #undef LA_TS_MMA
 #undef LA_TS_STEP
@@ -553,13 +549,6 @@ __device__ __forceinline__ void tmem_st16_raw(uint32_t taddr, const uint32_t *w)
         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
         "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
         : "memory");
-}
-
-// Warp-wide: thread t writes TMEM lane (lane of taddr) + t, 8 consecutive columns of raw words.
-__device__ __forceinline__ void tmem_st8_raw(uint32_t taddr, const uint32_t *w) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(w[0]),
-                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
 }
 
 // Warp-wide: 16 TMEM lanes (from the lane of taddr: the first or second half of the warp's 32) x 16

@@ -4,9 +4,11 @@ Tolerances.  Let A be the same sum with every input replaced by its absolute val
 errors are relative to).  float32: each of the D products of a score, the terms of a chunk and the
 chunks' carries rounds once, and gamma^n errs by n |log gamma| 2^-24 (below 104 2^-24 wherever the power is
 not 0): (D + 128 + 3 chunks + 104) 2^-24 A with chunks of 32 at least.  bfloat16 adds half a step (2^-8)
-of the result, and on the tensor cores half a step of A for the operands rounded once (the
-masked scores, the state read by the queries).  What the states add up is rounded to two bfloat16 terms there:
-2^-16 A."""
+of the result, and on the tensor cores half a step of A for the operands rounded once: what comes from the
+chunk has one such factor (the masked scores), what comes through the state has x, S and, where the state itself is no
+output, y as well.  At worst those are three half steps; as they are sums of 64 products or more whose roundings are
+independent, one half step holds them wherever the state is an output (three are allowed where not).  A state that is
+an output adds up two bfloat16 terms of each y: 2^-16 A."""
 import numpy as np
 import pytest
 import torch
@@ -29,12 +31,12 @@ def f32_part(N, D):
     return (D + 128 + 3 * (N / 32) + 104) * 2.0 ** -24
 
 
-def check(got, want, A, N, D, tc, name):
+def check(got, want, A, N, D, tc, name, factors=1):
     got = got.detach().double().cpu().numpy()
     half = 2.0 ** -8 if name in ("out", "dq", "dk", "dv") and check.dtype == torch.bfloat16 else 2.0 ** -24
     tol = half * np.abs(want) + f32_part(N, D) * A + 1e-37
     if tc:
-        tol = tol + (2.0 ** -8 if half > 1e-3 else 0) * A + 2.0 ** -16 * A
+        tol = tol + (factors * 2.0 ** -8 if half > 1e-3 else 0) * A + 2.0 ** -16 * A
     assert np.isfinite(got).all(), name
     bad = np.abs(got - want) / tol
     assert bad.max() <= 1.0, (name, float(bad.max()), np.unravel_index(bad.argmax(), bad.shape))
@@ -112,6 +114,64 @@ def test_long_sequence_in_segments(dtype):
     assert la.decay_workspace_size(*shape[:5], dtype, True) > 0
     run(shape, dtype)
     run((1, 2, 1, 2560, 128, 128), dtype, state=False, seed=2)
+
+
+@pytest.mark.parametrize("D,Dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("reps,N", [(1, 1), (1, 257), (3, 130), (2, 640), (1, 1400), (5, 1300)])
+def test_no_state_goes_out(reps, N, D, Dv):
+    """Without final_state and grad_initial_state: the kernels that round y once.  Given and absent initial states,
+    lengths, views of one projection."""
+    check.dtype = BF
+    Hkv = 2
+    q, k, v, go, ld, S0, dS1 = draw(2, reps * Hkv, Hkv, N, D, Dv, BF, seed=N + reps)
+    views = [t.transpose(1, 2).contiguous().cuda().transpose(1, 2) for t in (q, k, v, go)]
+    n = torch.tensor([N, N // 2], dtype=torch.int32)
+    for lengths, state in ((None, S0), (n, None)):
+        out = la.decay_fwd(*views[:3], ld.cuda(), scale=0.25, initial_state=None if state is None else state.cuda(),
+                           lengths=None if lengths is None else lengths.cuda())
+        want, A = od.fwd(q, k, v, ld, 0.25, state, lengths)[0], \
+            od.fwd(q.abs(), k.abs(), v.abs(), ld, 0.25, None if state is None else state.abs(), lengths)[0]
+        check(out, want, A, N, D, True, "out", factors=3)
+    for state, dstate in ((S0, None), (None, dS1)):
+        got = la.decay_bwd(*views, ld.cuda(), scale=0.25, initial_state=None if state is None else state.cuda(),
+                           grad_final_state=None if dstate is None else dstate.cuda())
+        want = od.bwd(q, k, v, go, ld, 0.25, state, dstate)
+        A = od.bwd(q.abs(), k.abs(), v.abs(), go.abs(), ld, 0.25, None if state is None else state.abs(),
+                   None if dstate is None else dstate.abs())
+        for name, a, b, c in zip(("dq", "dk", "dv"), got, want, A):
+            check(a, b, c, N, max(D, Dv) * reps, True, name, factors=3)
+    la.get_status()
+
+
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^31 elements, and a slot whose state lies past 2^31 floats."""
+    B, H, N, D = 2, 16, 530000, 128
+    assert B * H * N * D > 2 ** 31
+    part = torch.randn(4, 4001, D, generator=torch.Generator().manual_seed(5)).bfloat16().cuda()
+    x = torch.empty(B, H, N, D, dtype=BF, device="cuda")
+    q, k, v = x.fill_(1.0), torch.zeros_like(x), torch.zeros_like(x)
+    q[-1, -1, -4001:], k[-1, -1, -4001:], v[-1, -1, -4001:] = part[0], part[1], part[2]
+    ld = torch.full((H,), -0.02, device="cuda")
+    got = [t[-1:, -1:, -4001:].clone() for t in (la.decay_fwd(q, k, v, ld),)]
+    g = torch.zeros_like(x)
+    g[-1, -1, -4001:] = part[3]
+    got += [t[-1:, -1:, -4001:].clone() for t in la.decay_bwd(q, k, v, g, ld)]
+    la.get_status()
+    small = [p[None, None].contiguous() for p in part]
+    want = (la.decay_fwd(*small[:3], ld[-1:]),) + la.decay_bwd(*small, ld[-1:])
+    for a, b in zip(got, want):
+        # both are within four half steps of the exact rows, which random signs make of a like size
+        assert float((a.float() - b.float()).norm() / b.float().norm()) < 8 * 2.0 ** -8
+    del x, q, k, v, g
+    pool, Hkv = 16500, 8
+    assert (pool - 1) * Hkv * D * D > 2 ** 31
+    state = torch.zeros(pool, Hkv, D, D, device="cuda")
+    state[-1] = torch.randn(Hkv, D, D, generator=torch.Generator().manual_seed(6)).cuda()
+    mine = state[-1:].clone()
+    t = [torch.randn(1, Hkv, 1, D, device="cuda") for _ in range(3)]
+    out = la.decay_step(*t, state, ld[:Hkv], slots=torch.tensor([pool - 1], dtype=torch.int32, device="cuda"))
+    assert torch.equal(out, la.decay_step(*t, mine, ld[:Hkv])) and torch.equal(state[-1:], mine)
+    assert not state[:-1].any()
 
 
 @pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
