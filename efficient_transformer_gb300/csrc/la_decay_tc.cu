@@ -272,8 +272,10 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         tmem_relinquish();
     }
     const DecayPass &ps = p.pass[pi];
-    const int u = rest % p.nseg, bg = rest / p.nseg, b = bg / p.Hkv, h = bg % p.Hkv;
+    const int heads = p.B * p.Hkv, bg = rest % heads, b = bg / p.Hkv, h = bg % p.Hkv;
     const int n = decay_tokens(p.lengths, b, p.N), rev = ps.rev, many = ps.many_yz, reps = p.n_rep;
+    // (the last segment in token order may be a short one: those blocks come last)
+    const int u = rev ? p.nseg - 1 - rest / heads : rest / heads;
     const int NY = YSM && !many && reps > 1 ? 1 : NYS;        // stages of y in use
     const bool o_in_z = YSM && (many || reps == 1);           // output tiles are staged in z's
     const Part part = part_of(n, p.N, u, p.nseg, p.seg_len, rev);
