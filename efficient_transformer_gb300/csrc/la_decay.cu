@@ -176,6 +176,8 @@ la_status run(bool bwd, const Given &a, int B, int Hq, int Hkv, int N, int D, in
     if (st != LA_OK) return st;
     if (!a.q || !a.k || !a.v || !a.log_decay) return LA_ERR_ARG;
     if (bwd ? (!a.g || !a.dq || !a.dk || !a.dv) : !a.out) return LA_ERR_ARG;
+    // (the passes of the gradients read both states while one of them writes grad_initial_state)
+    if (a.ds_out && (a.ds_out == a.s_in || a.ds_out == a.ds_in)) return LA_ERR_ARG;
     const void *ptrs[] = {a.q, a.k, a.v, a.g, a.out, a.dq, a.dk, a.dv, a.s_in, a.ds_in, a.s_out, a.ds_out};
     for (const void *p : ptrs)
         if (p && !aligned(p, 16)) return LA_ERR_ALIGN;

@@ -7,7 +7,10 @@
 //   P   = (X Y^T) o gamma^(i-j), j <= i          [C x C]
 //   out = P Z + gamma^(i+1) X S                  [C x SZ]
 //   S   = gamma^C S + (gamma^(C-1-j) Y)^T Z      [DX x SZ]
-// The slices of one head repeat P (a third of the work at DX = 128) for two to four times the blocks.
+// SZ = 64 (32 where z is no wider): slices of one head repeat P, a third of the work at DX = 128; slices of 32 gave
+// twice the blocks and were slower (gradients of 2 x 6/2 heads, N 777, D 64 float32: 68 us, with 64 columns 59).  Bound
+// by the shared memory: 6 loads of 8 to 16 bytes for 16 FMA a thread with slices of 32, 76 % of its bandwidth where
+// every SM had blocks, for 32 FMA with 64.  Two blocks an SM, as the registers hold the next chunk's rows.
 #include "la_decay.cuh"
 
 namespace la {

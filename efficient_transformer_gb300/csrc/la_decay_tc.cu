@@ -25,6 +25,13 @@
 //
 // The reverse passes (gradients of k and v) take the same steps with j >= i and gamma^(j-i), chunks from the
 // last to the first.
+//
+// What bounds it: with grouped queries the memory (32 query on 8 key/value heads, N 65536, D 128: 251 us for 1.34 GB,
+// 5.3 TB/s; 314 us with the segments' sums, which read k and v once more); with one head of x to one of y and z the
+// instructions of the roles, 2.4 us a chunk of 128 x 128 and 2.0 us of 64 x 64 on an SM (8 x 19 heads, N 1024, D 128:
+// 33 us; gradients of 2 x 16 heads, N 8192, D 128: 161 us).  There the tensor pipe is busy for 15 to 30 % of the time
+// and an SM's warps issue 1.3 to 1.7 instructions a cycle.  With one buffer of scores (and y in two
+// terms) the grouped queries took 366 us.
 #include "la_decay.cuh"
 #include "la_tc_common.cuh"
 
@@ -867,7 +874,9 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
 // ---------------------------------------------------------------------------------------
 // The sums over parts of segments (see DecayStateParams).  y is decayed to the part's end at once, so S in
 // TMEM only ever accumulates; in place in its tile, and where the state is exact with the rounding's remainder
-// in a tile of its own.  Warps: 0 TMA, 1 MMA, 4-11 y (two threads a token; 4-7 then write S).
+// in a tile of its own.  Warps: 0 TMA, 1 MMA, 4-11 y (two threads a token; 4-7 then write S).  Bound by memory where
+// the parts are long (8 heads, N 65536, 128 x 128: 57 us for 268 MB, 4.7 TB/s), else by its first chunk's latency (64
+// heads, N 4096, 64 x 64, parts of 8 chunks: 14 us).
 constexpr int kStateThreads = 384, kStateY = 256;
 
 struct StateMaps {
@@ -1040,9 +1049,10 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
 }
 
 // ---------------------------------------------------------------------------------------
-// Starting states of the segments, and the last state where it is an output: T = the given state, then for each segment T =
-// gamma^tokens T + its sum, a
-// thread carrying 4 x 4 elements; all states lane-blocked but the caller's.
+// Starting states of the segments, and the last state where it is an output: T = the given state, then for each
+// segment T = gamma^tokens T + its sum, a thread carrying 4 x 4 elements; all states lane-blocked but the caller's.
+// A few microseconds of latency (4 to 9; eight parts loaded ahead instead of four do not shorten them).  Lane-blocked,
+// as a thread of the passes reads a whole row: from plain [D][Dv] states that took up to 50 us.
 constexpr int kJoinThreads = 64;
 
 template <int D, int DV>

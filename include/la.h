@@ -318,7 +318,8 @@ la_status la_decay_fwd(const void *q, const void *k, const void *v, void *out, c
 /* Exact gradient of la_decay_fwd (without lengths): writes dq [B, Hq, N, D], dk [B, Hkv, N, D],
  * dv [B, Hkv, N, Dv] (summed over each group's query heads) and, when given, grad_initial_state.
  * grad_final_state: the gradient of final_state, or NULL (zeros); both [B, Hkv, D, Dv] float32,
- * not overlapping.  Nothing of the forward is needed: the states are recomputed. */
+ * contiguous; grad_initial_state may overlap no input (LA_ERR_ARG where it is initial_state or
+ * grad_final_state).  Nothing of the forward is needed: the states are recomputed. */
 la_status la_decay_bwd(const void *q, const void *k, const void *v, const void *grad_out, void *dq, void *dk, void *dv,
                        const float *log_decay, const float *initial_state, const float *grad_final_state,
                        float *grad_initial_state, int B, int Hq, int Hkv, int N, int D, int Dv, la_dtype dtype,

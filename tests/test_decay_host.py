@@ -52,6 +52,17 @@ def test_bwd_rejects(lib):
     assert lib.la_decay_bwd(*a) == la.LA_ERR_WORKSPACE
     for i in (4, 5, 6, 8, 9, 10):
         assert lib.la_decay_bwd(*(a[:i] + [ODD] + a[i + 1:])) == la.LA_ERR_ALIGN
+    for i in (8, 9):     # the initial state's gradient in place of a state that is read
+        b = list(a)
+        b[i] = b[10] = FAKE
+        assert lib.la_decay_bwd(*b) == la.LA_ERR_ARG
+
+
+def test_a_gradients_workspace_serves_the_forward(lib):
+    for B, Hq, Hkv, N, D, Dv in ((1, 2, 2, 256, 32, 32), (2, 4, 2, 1111, 64, 64), (2, 16, 16, 8192, 128, 128), (1, 32, 8, 65536, 128, 64)):
+        for dt in (torch.float32, torch.bfloat16):
+            f, b = (la.decay_workspace_size(B, Hq, Hkv, N, D, dt, x, Dv=Dv) for x in (False, True))
+            assert b >= f >= 0
 
 
 def step(lib, **over):
