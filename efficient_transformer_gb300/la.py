@@ -442,17 +442,17 @@ def _qk_need(B, Hq, Hkv, N, D, dt):
     return int(load().la_qk_norm_rope_workspace_size(B, Hq, Hkv, N, D, dt))
 
 
-def _rows_ok(t, dtype):
-    """A [B, H, N, D] CUDA tensor of this dtype with D contiguous."""
-    return t.is_cuda and t.dtype == dtype and t.dim() == 4 and (t.stride(3) == 1 or t.shape[3] == 1)
+def _rows_ok(t, dtype, device):
+    """A [B, H, N, D] tensor of this dtype on CUDA device number `device`, D contiguous."""
+    return t.dtype is dtype and t.get_device() == device >= 0 and t.dim() == 4 and (t.stride(3) == 1 or t.shape[3] == 1)
 
 
 def _check_qkv(q, k, v, *extra):
     """(B, Hq, Hkv, N, D, Dv), as _check_inputs (which raises when something is wrong)."""
     try:
-        dt = q.dtype
-        ok = _rows_ok(q, dt) and _rows_ok(k, dt) and _rows_ok(v, dt) and all(_rows_ok(t, dt) for t in extra)
-        if ok:
+        dt, dev = q.dtype, q.get_device()
+        if _rows_ok(q, dt, dev) and _rows_ok(k, dt, dev) and _rows_ok(v, dt, dev) and \
+                (not extra or _rows_ok(extra[0], dt, dev)):
             B, Hq, N, D = q.shape
             _, Hkv, Nk, Dk = k.shape
             Dv = v.shape[3]
@@ -463,21 +463,21 @@ def _check_qkv(q, k, v, *extra):
     return _check_inputs(q, k, v, None, None, tuple(("grad_out", t) for t in extra))
 
 
-def _check_vector(name, t, n, dtype, device):
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or t.dim() != 1 or t.shape[0] != n \
-            or not t.is_contiguous():
+def _check_vector(name, t, n, dtype, like):
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != like.get_device() or t.dim() != 1 \
+            or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} vector of {n} elements on q's device")
 
 
-def _check_state(name, t, shape, device):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.device != device or tuple(t.shape) != shape \
-            or not t.is_contiguous():
+def _check_state(name, t, shape, like):
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.get_device() != like.get_device() \
+            or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor {shape} on q's device")
 
 
 def _output(name, t, shape, like):
-    if t is None:
-        return like.new_empty(shape)
+    if t is None:   # (empty_like is the quicker of the two by 1 to 2 us)
+        return torch.empty_like(like) if like.shape == shape and like.is_contiguous() else like.new_empty(shape)
     if tuple(t.shape) != tuple(shape) or t.dtype != like.dtype or t.device != like.device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor of q's dtype on q's device")
     return t
@@ -500,18 +500,18 @@ def decay_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torc
     Returns ``out`` [B, Hq, N, Dv]."""
     lib = load()
     B, Hq, Hkv, N, D, Dv = _check_qkv(q, k, v)
-    dev, dt = q.device, _dtype_code(q)
-    _check_vector("log_decay", log_decay, Hkv, torch.float32, dev)
+    dt = _dtype_code(q)
+    _check_vector("log_decay", log_decay, Hkv, torch.float32, q)
     if lengths is not None:
-        _check_vector("lengths", lengths, B, torch.int32, dev)
+        _check_vector("lengths", lengths, B, torch.int32, q)
     for name, t in (("initial_state", initial_state), ("final_state", final_state)):
         if t is not None:
-            _check_state(name, t, (B, Hkv, D, Dv), dev)
+            _check_state(name, t, (B, Hkv, D, Dv), q)
     out = _output("out", out, (B, Hq, N, Dv), q)
-    ws = _workspace(_decay_need(B, Hq, Hkv, N, D, Dv, dt, 0), dev, workspace)
-    st = lib.la_decay_fwd(_addr(q), _addr(k), _addr(v), _addr(out), _addr(log_decay), _addr(initial_state),
-                          _addr(final_state), _addr(lengths), B, Hq, Hkv, N, D, Dv, dt, scale, _stride_arg(q), _stride_arg(k),
-                          _stride_arg(v), _addr(ws), _nbytes(ws), _raw_stream(stream))
+    ws = _workspace(_decay_need(B, Hq, Hkv, N, D, Dv, dt, 0), q.device, workspace)
+    st = lib.la_decay_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), log_decay.data_ptr(),
+                          _addr(initial_state), _addr(final_state), _addr(lengths), B, Hq, Hkv, N, D, Dv, dt, scale,
+                          _stride_arg(q), _stride_arg(k), _stride_arg(v), _addr(ws), _nbytes(ws), _raw_stream(stream))
     if st != LA_OK:
         _raise(lib, st, "la_decay_fwd")
     return out
@@ -530,18 +530,18 @@ def decay_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, grad_out: torch
     B, Hq, Hkv, N, D, Dv = _check_qkv(q, k, v, grad_out)
     if tuple(grad_out.shape) != (B, Hq, N, Dv):
         raise ValueError("grad_out must have the shape of out ([B, Hq, N, Dv])")
-    dev, dt = q.device, _dtype_code(q)
-    _check_vector("log_decay", log_decay, Hkv, torch.float32, dev)
+    dt = _dtype_code(q)
+    _check_vector("log_decay", log_decay, Hkv, torch.float32, q)
     for name, t in (("initial_state", initial_state), ("grad_final_state", grad_final_state),
                     ("grad_initial_state", grad_initial_state)):
         if t is not None:
-            _check_state(name, t, (B, Hkv, D, Dv), dev)
-    dq, dk, dv = _output("dq", dq, q.shape, q), _output("dk", dk, k.shape, q), _output("dv", dv, v.shape, q)
-    ws = _workspace(_decay_need(B, Hq, Hkv, N, D, Dv, dt, 1), dev, workspace)
-    st = lib.la_decay_bwd(_addr(q), _addr(k), _addr(v), _addr(grad_out), _addr(dq), _addr(dk), _addr(dv), _addr(log_decay),
-                          _addr(initial_state), _addr(grad_final_state), _addr(grad_initial_state), B, Hq, Hkv, N, D, Dv,
-                          dt, scale, _stride_arg(q), _stride_arg(k), _stride_arg(v), _stride_arg(grad_out), _addr(ws), _nbytes(ws),
-                          _raw_stream(stream))
+            _check_state(name, t, (B, Hkv, D, Dv), q)
+    dq, dk, dv = _output("dq", dq, q.shape, q), _output("dk", dk, k.shape, k), _output("dv", dv, v.shape, v)
+    ws = _workspace(_decay_need(B, Hq, Hkv, N, D, Dv, dt, 1), q.device, workspace)
+    st = lib.la_decay_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), grad_out.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                          dv.data_ptr(), log_decay.data_ptr(), _addr(initial_state), _addr(grad_final_state),
+                          _addr(grad_initial_state), B, Hq, Hkv, N, D, Dv, dt, scale, _stride_arg(q), _stride_arg(k),
+                          _stride_arg(v), _stride_arg(grad_out), _addr(ws), _nbytes(ws), _raw_stream(stream))
     if st != LA_OK:
         _raise(lib, st, "la_decay_bwd")
     return dq, dk, dv
@@ -559,19 +559,18 @@ def decay_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, state: torch.T
     B, Hq, Hkv, N, D, Dv = _check_qkv(q, k, v)
     if N != 1:
         raise ValueError(f"decay_step takes one token per sequence (N = 1), got N = {N}")
-    dev = q.device
-    _check_vector("log_decay", log_decay, Hkv, torch.float32, dev)
+    _check_vector("log_decay", log_decay, Hkv, torch.float32, q)
     if slots is not None:
-        _check_vector("slots", slots, B, torch.int32, dev)
+        _check_vector("slots", slots, B, torch.int32, q)
     pool = state.shape[0] if state.dim() == 4 else 0
-    _check_state("state", state, (pool, Hkv, D, Dv), dev)
+    _check_state("state", state, (pool, Hkv, D, Dv), q)
     if state_out is not None:
-        _check_state("state_out", state_out, (pool, Hkv, D, Dv), dev)
+        _check_state("state_out", state_out, (pool, Hkv, D, Dv), q)
     out = _output("out", out, (B, Hq, 1, Dv), q)
-    st = lib.la_decay_step(_addr(q), _addr(k), _addr(v), _addr(out), _addr(state),
-                           _addr(state if state_out is None else state_out), _addr(log_decay), _addr(slots), pool, B, Hq,
-                           Hkv, D, Dv, _dtype_code(q), scale, _stride_arg(q), _stride_arg(k), _stride_arg(v),
-                           _raw_stream(stream))
+    st = lib.la_decay_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), state.data_ptr(),
+                           (state if state_out is None else state_out).data_ptr(), log_decay.data_ptr(), _addr(slots),
+                           pool, B, Hq, Hkv, D, Dv, _dtype_code(q), scale, _stride_arg(q), _stride_arg(k),
+                           _stride_arg(v), _raw_stream(stream))
     if st != LA_OK:
         _raise(lib, st, "la_decay_step")
     return out
@@ -579,11 +578,13 @@ def decay_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, state: torch.T
 
 def _check_qk(q, k, extra=()):
     try:
-        dt = q.dtype
-        if _rows_ok(q, dt) and _rows_ok(k, dt) and all(_rows_ok(t, dt) for _, t in extra):
+        dt, dev = q.dtype, q.get_device()
+        if _rows_ok(q, dt, dev) and _rows_ok(k, dt, dev) and \
+                (not extra or (_rows_ok(extra[0][1], dt, dev) and _rows_ok(extra[1][1], dt, dev))):
             B, Hq, N, D = q.shape
-            if k.shape[0] == B and k.shape[2] == N and k.shape[3] == D:
-                return B, Hq, k.shape[1], N, D
+            Bk, Hkv, Nk, Dk = k.shape
+            if Bk == B and Nk == N and Dk == D:
+                return B, Hq, Hkv, N, D
     except AttributeError:
         pass
     for name, t in (("q", q), ("k", k)) + tuple(extra):
@@ -599,44 +600,58 @@ def _check_qk(q, k, extra=()):
     return B, Hq, k.shape[1], N, D
 
 
+@functools.lru_cache(maxsize=256)
+def _sections_of(sections, pairs):
+    """The host array of the axes' pairs; None where they do not add up."""
+    return (ctypes.c_int * len(sections))(*sections) if sum(sections) == pairs else None
+
+
+@functools.lru_cache(maxsize=256)
+def _pos_strides_of(strides):
+    return (ctypes.c_longlong * 3)(*strides)
+
+
 def _qk_args(q, q_weight, k_weight, eps, positions, inv_freq, sections, interleaved, normalize):
     """la_qk_args of a call (and the host arrays that it points to)."""
     B, _, N, D = q.shape
-    a = LaQkArgs(eps=eps, normalize=int(normalize), interleaved=int(interleaved))
-    weights = [w for w in (q_weight, k_weight) if w is not None]
+    a = LaQkArgs(None, None, LA_F32, eps, normalize, interleaved)
+    wt = None
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None:
-            if w.dtype not in (torch.float32, q.dtype) or w.dtype != weights[0].dtype:
+            t = w.dtype
+            if (t is not torch.float32 and t is not q.dtype) or (wt is not None and t is not wt):
                 raise TypeError(f"{name} must be float32 or of q's dtype, the same for both")
-            _check_vector(name, w, D, w.dtype, q.device)
-    a.weight_dtype = _dtype_code(weights[0]) if weights else LA_F32
-    a.q_weight = q_weight.data_ptr() if q_weight is not None else None
-    a.k_weight = k_weight.data_ptr() if k_weight is not None else None
-    if (positions is None) != (inv_freq is None):
-        raise ValueError("give both positions and inv_freq or neither")
+            wt = t
+            _check_vector(name, w, D, t, q)
+            setattr(a, name, w.data_ptr())
+    if wt is torch.bfloat16:
+        a.weight_dtype = LA_BF16
     if inv_freq is None:
+        if positions is not None:
+            raise ValueError("give both positions and inv_freq or neither")
         if sections is not None:
             raise ValueError("sections need positions and inv_freq")
         return a
-    if inv_freq.dim() != 1:
-        raise ValueError("inv_freq must be a vector")
-    _check_vector("inv_freq", inv_freq, inv_freq.numel(), torch.float64, q.device)
-    if positions.dim() == 2:
-        positions = positions.unsqueeze(0)
-    if positions.dtype != torch.int64 or positions.device != q.device or positions.dim() != 3 \
-            or tuple(positions.shape[1:]) != (B, N):
+    if positions is None:
+        raise ValueError("give both positions and inv_freq or neither")
+    pairs = inv_freq.numel()
+    _check_vector("inv_freq", inv_freq, pairs, torch.float64, q)
+    shape, strides = positions.shape, positions.stride()
+    if len(shape) == 2:
+        shape, strides = (1, *shape), (0, *strides)
+    if positions.dtype is not torch.int64 or positions.get_device() != q.get_device() or len(shape) != 3 \
+            or shape[1] != B or shape[2] != N:
         raise ValueError(f"positions must be an int64 tensor [axes, {B}, {N}] or [{B}, {N}] on q's device")
-    axes = positions.shape[0]
+    axes = shape[0]
     if sections is None:
         if axes != 1:
             raise ValueError("several position axes need sections (pairs of each axis)")
-        sections = (inv_freq.numel(),)
-    if len(sections) != axes or sum(sections) != inv_freq.numel():
-        raise ValueError(f"sections {tuple(sections)} must name {axes} axes and add up to {inv_freq.numel()} pairs")
-    a.rot, a.axes = 2 * inv_freq.numel(), axes
-    a.sections = (ctypes.c_int * axes)(*sections)
-    a.positions, a.inv_freq = positions.data_ptr(), inv_freq.data_ptr()
-    a.pos_strides = (ctypes.c_longlong * 3)(*positions.stride())
+        sections = (pairs,)
+    host = _sections_of(tuple(sections), pairs) if len(sections) == axes else None
+    if host is None:
+        raise ValueError(f"sections {tuple(sections)} must name {axes} axes and add up to {pairs} pairs")
+    a.rot, a.axes, a.sections = 2 * pairs, axes, host
+    a.positions, a.inv_freq, a.pos_strides = positions.data_ptr(), inv_freq.data_ptr(), _pos_strides_of(strides)
     return a
 
 
@@ -655,9 +670,9 @@ def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, *, q_weight: torch.Tensor
     lib = load()
     B, Hq, Hkv, N, D = _check_qk(q, k)
     a = _qk_args(q, q_weight, k_weight, eps, positions, inv_freq, sections, interleaved, normalize)
-    q_out, k_out = _output("q_out", q_out, q.shape, q), _output("k_out", k_out, k.shape, q)
-    st = lib.la_qk_norm_rope_fwd(_addr(q), _addr(k), _addr(q_out), _addr(k_out), B, Hq, Hkv, N, D, _dtype_code(q),
-                                 _stride_arg(q), _stride_arg(k), ctypes.byref(a), _raw_stream(stream))
+    q_out, k_out = _output("q_out", q_out, q.shape, q), _output("k_out", k_out, k.shape, k)
+    st = lib.la_qk_norm_rope_fwd(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), B, Hq, Hkv, N, D,
+                                 _dtype_code(q), _stride_arg(q), _stride_arg(k), ctypes.byref(a), _raw_stream(stream))
     if st != LA_OK:
         _raise(lib, st, "la_qk_norm_rope_fwd")
     return q_out, k_out
@@ -681,15 +696,16 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, grad_q: torch.Tensor, gra
     if grad_q.shape != q.shape or grad_k.shape != k.shape:
         raise ValueError("grad_q and grad_k must have the shapes of q and k")
     a = _qk_args(q, q_weight, k_weight, eps, positions, inv_freq, sections, interleaved, normalize)
-    dq, dk = _output("dq", dq, q.shape, q), _output("dk", dk, k.shape, q)
+    dq, dk = _output("dq", dq, q.shape, q), _output("dk", dk, k.shape, k)
     dqw = torch.empty_like(q_weight) if q_weight is not None else None
     dkw = torch.empty_like(k_weight) if k_weight is not None else None
     dt, ws = _dtype_code(q), None
     if dqw is not None or dkw is not None:
         ws = _workspace(_qk_need(B, Hq, Hkv, N, D, dt), q.device, workspace)
-    st = lib.la_qk_norm_rope_bwd(_addr(q), _addr(k), _addr(grad_q), _addr(grad_k), _addr(dq), _addr(dk), _addr(dqw),
-                                 _addr(dkw), B, Hq, Hkv, N, D, dt, _stride_arg(q), _stride_arg(k), _stride_arg(grad_q),
-                                 _stride_arg(grad_k), ctypes.byref(a), _addr(ws), _nbytes(ws), _raw_stream(stream))
+    st = lib.la_qk_norm_rope_bwd(q.data_ptr(), k.data_ptr(), grad_q.data_ptr(), grad_k.data_ptr(), dq.data_ptr(),
+                                 dk.data_ptr(), _addr(dqw), _addr(dkw), B, Hq, Hkv, N, D, dt, _stride_arg(q),
+                                 _stride_arg(k), _stride_arg(grad_q), _stride_arg(grad_k), ctypes.byref(a), _addr(ws),
+                                 _nbytes(ws), _raw_stream(stream))
     if st != LA_OK:
         _raise(lib, st, "la_qk_norm_rope_bwd")
     return dq, dk, dqw, dkw
