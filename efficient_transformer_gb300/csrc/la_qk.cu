@@ -10,8 +10,9 @@
 // (y[e] = r (x[e] w[e] c[e] + x[e'] w[e'] s[e]), e' the pair's other element), stay in registers; the
 // partner's elements come by shuffles of the packed row.  kBatch heads' rows are loaded before the
 // first is used, in the backward before the batch ahead of them is: its two sums a row are chains of
-// shuffles that the loads run beside (2 x 32/8 heads, N 8192, D 128 bf16: 112 us without that, 99 us with it,
-// 5.1 TB/s; 4 x 16/16 heads, N 4096, D 64: 51.5 and 46 us).  The forward on 32/8 heads, N 65536, D 128:
+// shuffles that the loads run beside (2 x 32/8 heads, N 8192, D 128 bf16: 112 us without that, 95 us with it
+// and a token's first rows loaded before its angles are found, 5.3 TB/s; 4 x 16/16 heads, N 4096, D 64: 51 and 44 us; in
+// the forward the same costs registers, 222 -> 229 us).  The forward on 32/8 heads, N 65536, D 128:
 // 222 us, 6.0 TB/s.
 //
 // Angles.  positions are 64-bit integers and inv_freq doubles, so an angle in float32, or even its
@@ -336,16 +337,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_bwd(QkParams p) {
         const unsigned tok = t0 + threadIdx.x / L;
         const bool live = tok < ntok;
         const int b = live ? (int)(tok / (unsigned)p.N) : 0, n = live ? (int)(tok - (unsigned)b * p.N) : 0;
-        unsigned long long c[V / 2], s[V / 2];
-        {
-            float ct[V], st[V];
-            turn.at(p, b, n, true, ct, st);
-#pragma unroll
-            for (int i = 0; i < V / 2; ++i) {
-                c[i] = pack2(ct[2 * i], ct[2 * i + 1]);
-                s[i] = pack2(st[2 * i], st[2 * i + 1]);
-            }
-        }
         const T *x = static_cast<const T *>(which ? p.x[1] : p.x[0]) + b * sx.b + n * sx.n + lane * V;
         const T *g = static_cast<const T *>(which ? p.g[1] : p.g[0]) + b * sg.b + n * sg.n + lane * V;
         T *y = static_cast<T *>(which ? p.y[1] : p.y[0]) + ((size_t)b * p.H[which] * p.N + n) * D + lane * V;
@@ -358,7 +349,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_bwd(QkParams p) {
                 nx[i] = there && p.normalize ? *reinterpret_cast<const uint4 *>(x + (h + i) * sx.h) : make_uint4(0u, 0u, 0u, 0u);
             }
         };
-        fetch(h0);
+        fetch(h0);   // (the rows come while the angles are found)
+        unsigned long long c[V / 2], s[V / 2];
+        {
+            float ct[V], st[V];
+            turn.at(p, b, n, true, ct, st);
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                c[i] = pack2(ct[2 * i], ct[2 * i + 1]);
+                s[i] = pack2(st[2 * i], st[2 * i + 1]);
+            }
+        }
 #pragma unroll 1
         for (int h = h0; h < h1; h += kBatchBwd) {
             uint4 rx[kBatchBwd], rg[kBatchBwd];
