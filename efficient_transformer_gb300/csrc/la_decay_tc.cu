@@ -914,6 +914,9 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
     const Part part = sub_part_of(n, p.N, pidx / p.nsub, p.nseg, p.seg_len, pidx % p.nsub, p.nsub, p.sub_len, rev);
     const int nchunk = (part.hi - part.lo + C - 1) / C, items = nchunk * heads;
     const float l2 = decay_log2(p.log_decay[h]);
+    // chunks in the pass's order, the smallest powers first: the MMA's sums are cut, not rounded, to float32 at each
+    // step, and large terms at the start would have every later step cut at their size
+    auto chunk0 = [&](int it) { return part.lo + C * (rev ? nchunk - 1 - it / heads : it / heads); };
     float *dst = p.part[a] + ((size_t)bg * nparts + pidx) * D * DV;
 
     if (threadIdx.x == 0) {
@@ -941,7 +944,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
     if (warp == 0) {
         int issued = 0;
         for (int it = 0; it < items; ++it) {
-            const int s = it % NS, c0 = part.lo + C * (it / heads), hh = h * heads + it % heads;
+            const int s = it % NS, c0 = chunk0(it), hh = h * heads + it % heads;
             if (it >= NS && !await(&empty[s], (it / NS - 1) & 1, &abort_flag)) break;
             uint8_t *y = stage + s * K::STAGE, *z = y + K::Y_BYTES;
             if (elect_one()) {
@@ -989,7 +992,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
         }
         bool ok = true;
         for (int it = 0; it < items; ++it) {
-            const int s = it % NS, c0 = part.lo + C * (it / heads), valid = min(C, part.hi - c0);
+            const int s = it % NS, c0 = chunk0(it), valid = min(C, part.hi - c0);
             if (!(ok = await(&full[s], (it / NS) & 1, &abort_flag))) break;
             uint8_t *y = stage + s * K::STAGE;
             if (p.lengths && valid < C) {
