@@ -893,6 +893,7 @@ struct StateCfg {
     static constexpr int SMEM = NS * STAGE + LO_BYTES + 1024;
     static_assert(D == 128 || STAGE - Y_BYTES >= C * 64 * 2, "128 columns from a y tile's start");
     static_assert(NS >= 2, "two stages");
+    static constexpr int NA = 512 / DV;   // accumulators
 };
 
 template <int D, int DV>
@@ -914,8 +915,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
     const Part part = sub_part_of(n, p.N, pidx / p.nsub, p.nseg, p.seg_len, pidx % p.nsub, p.nsub, p.sub_len, rev);
     const int nchunk = (part.hi - part.lo + C - 1) / C, items = nchunk * heads;
     const float l2 = decay_log2(p.log_decay[h]);
-    // chunks in the pass's order, the smallest powers first: the MMA's sums are cut, not rounded, to float32 at each
-    // step, and large terms at the start would have every later step cut at their size
+    // chunks in the pass's order, the smallest powers first (small terms after large ones would be cut at their size)
     auto chunk0 = [&](int it) { return part.lo + C * (rev ? nchunk - 1 - it / heads : it / heads); };
     float *dst = p.part[a] + ((size_t)bg * nparts + pidx) * D * DV;
 
@@ -933,13 +933,16 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
     }
     if (threadIdx.x >= 96 && threadIdx.x < 98) tma_prefetch_map(&maps.m[a][threadIdx.x - 96]);
     if (warp == 1) {
-        tmem_alloc(&tmem_base, 128);
+        tmem_alloc(&tmem_base, 512);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = tmem_base;
+    // The MMA's sums are cut, not rounded, to float32 at each of their steps, so that a long chain of them drifts: a sum
+    // that is an output is made in several accumulators in turn, which meet at the end.
+    const int na = exact ? K::NA : 1;
 
     if (warp == 0) {
         int issued = 0;
@@ -967,10 +970,11 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
             if (!await(&y_ready[s], (it / NS) & 1, &abort_flag)) break;
             tc_fence_after();
             const uint32_t y = smem_u32(stage + s * K::STAGE), z = y + K::Y_BYTES;
+            const uint32_t acc = tm + (exact ? it % K::NA : 0) * DV;
             if (elect_one()) {
-                mma_ss_mn8(tm, desc_mnmajor(y, C, 0, 0), desc_mnmajor(z, C, 0, 0), id);
+                mma_ss_mn8(acc, desc_mnmajor(y, C, 0, 0), desc_mnmajor(z, C, 0, 0), id);
                 if (exact) {
-                    mma_ss_mn8(tm, desc_mnmajor(smem_u32(lo_tile), C, 0, 0), desc_mnmajor(z, C, 0, 0), id);
+                    mma_ss_mn8(acc, desc_mnmajor(smem_u32(lo_tile), C, 0, 0), desc_mnmajor(z, C, 0, 0), id);
                     mma_commit(&lo_free);
                 }
                 mma_commit(&empty[s]);
@@ -985,8 +989,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
         const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
         if (warp < 8) {   // S = 0
             const float z16[16] = {};
-#pragma unroll
-            for (int c16 = 0; c16 < DV / 16; ++c16) tmem_st16(tm + lane_off + c16 * 16, z16);
+            for (int c16 = 0; c16 < na * DV / 16; ++c16) tmem_st16(tm + lane_off + c16 * 16, z16);
             tmem_st_wait();
             tc_fence_before();
         }
@@ -1039,6 +1042,14 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
                     float v[16];
                     tmem_ld16(tm + lane_off + c16 * 16, v);
                     tmem_wait_regs<16>(v);
+#pragma unroll 1
+                    for (int k = 1; k < na; ++k) {
+                        float x[16];
+                        tmem_ld16(tm + lane_off + k * DV + c16 * 16, x);
+                        tmem_wait_regs<16>(x);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[e] += x[e];
+                    }
                     float4 *f = reinterpret_cast<float4 *>(dst + decay_blocked(D, d, c16 * 16));
 #pragma unroll
                     for (int e = 0; e < 4; ++e) f[e * D] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
@@ -1047,7 +1058,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) tmem_dealloc(tm, 128);
+    if (warp == 1) tmem_dealloc(tm, 512);
     if (threadIdx.x == 0 && abort_flag) atomicExch(p.err, kErrTimeout);
 }
 

@@ -143,6 +143,30 @@ def test_no_state_goes_out(reps, N, D, Dv):
     la.get_status()
 
 
+@pytest.mark.parametrize("shape", [(6, 12, 4, 3699, 64, 64), (2, 16, 16, 4000, 128, 128), (2, 32, 4, 8192, 128, 128)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_states_of_long_memories(shape):
+    """Sums over long memories in cut sequences.  y's two terms leave 2^-17 of each product; the matrix units cut their
+    sums at each step of 16 tokens (2^-24 of the sum so far), which the steps within the memory, two a token's head, add
+    up over the 512 / Dv accumulators that take turns."""
+    B, Hq, Hkv, N, D, Dv = shape
+    r, memory = Hq // Hkv, 1000
+    assert la.decay_workspace_size(B, Hq, Hkv, N, D, BF, False, Dv=Dv) > 0
+    q, k, v, go = (t.cuda() for t in draw(*shape, BF, 13)[:4])
+    ld = torch.full((Hkv,), -1.0 / memory, device="cuda")
+    S1, dS0 = torch.empty(B, Hkv, D, Dv, device="cuda"), torch.empty(B, Hkv, D, Dv, device="cuda")
+    la.decay_fwd(q, k, v, ld, final_state=S1)
+    la.decay_bwd(q, k, v, go, ld, grad_initial_state=dS0)
+    la.get_status()
+    j = torch.arange(N, device="cuda", dtype=torch.float64)
+    l = float(ld[0])
+    S = (k.double() * torch.exp(l * (N - 1 - j))[:, None]).transpose(2, 3) @ v.double()
+    w = (q.double() * torch.exp(l * (j + 1))[:, None]).transpose(2, 3) @ go.double()
+    for name, got, want, heads in (("S", S1, S, 1), ("dS", dS0, w.view(B, Hkv, r, D, Dv).sum(2), r)):
+        bound = 2.0 ** -17 + 2.0 ** -24 * memory * heads * 2 / 16 / (512 // Dv)
+        assert float((got - want).norm() / want.norm()) < bound, name
+
+
 def test_offsets_past_32_bits():
     """Tensors of more than 2^31 elements, and a slot whose state lies past 2^31 floats."""
     B, H, N, D = 2, 16, 530000, 128
