@@ -13,9 +13,14 @@ come back with the key/value shape, summed over each group.  Inputs may be strid
 PyTorch supplies device memory and the current stream; every arithmetic step runs in
 the library's CUDA kernels.  There is no fallback: if libla.so is missing or a call
 fails, an exception says why.
+
+``stream=`` enqueues a call on another stream than torch's current one.  The caller orders
+that stream after whatever makes the inputs and lets whatever uses the results wait for it;
+memory is safe either way: see ``_memory_on`` and ``_keep``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -210,6 +215,32 @@ def kernel_path(B, Hq, Hkv, N, D, dtype: torch.dtype, is_causal: bool, has_weigh
                                        int(has_weights), int(is_bwd)))
 
 
+_NO_SWITCH = contextlib.nullcontext()
+
+
+def _memory_on(stream):
+    """Context of a call's own allocations: memory of the stream that its kernels run on.  torch reuses a block in the
+    order of the stream that it was allocated on, so scratch of the current stream could go to the next operation there
+    while the kernels still use it, or come from an earlier one that has not finished."""
+    return _NO_SWITCH if stream is None else torch.cuda.stream(stream)
+
+
+def _keep(stream, made, given):
+    """Tensors that a call on ``stream`` shares with the current stream (``made`` by the call, or ``given`` to it): freed,
+    their memory is not reused before both streams are done with it."""
+    if stream is None:
+        return
+    here = torch.cuda.current_stream()
+    if here == stream:
+        return
+    for t in made:
+        if t is not None:
+            t.record_stream(here)
+    for t in given:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def _workspace(nbytes: int, device, given):
     if nbytes == 0:
         return None
@@ -230,13 +261,15 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, is_causal: bool = Fal
     lib = load()
     B, Hq, Hkv, N, D, Dv = _check_inputs(q, k, v, cos_weight, sin_weight)
     oshape = (B, Hq, N, Dv)
-    if out is None:
-        out = torch.empty(oshape, dtype=q.dtype, device=q.device)
-    elif tuple(out.shape) != oshape or out.dtype != q.dtype or not out.is_contiguous():
+    given = [q, k, v, cos_weight, sin_weight, out, workspace]
+    if out is not None and (tuple(out.shape) != oshape or out.dtype != q.dtype or not out.is_contiguous()):
         raise ValueError(f"out must be a contiguous {oshape} tensor of q's dtype")
     dt = _dtype_code(q)
-    ws = _workspace(lib.la_workspace_size_v(B, Hq, Hkv, N, D, Dv, dt, int(is_causal),
-                                            int(cos_weight is not None), 0), q.device, workspace)
+    with _memory_on(stream):
+        out = torch.empty(oshape, dtype=q.dtype, device=q.device) if out is None else out
+        ws = _workspace(lib.la_workspace_size_v(B, Hq, Hkv, N, D, Dv, dt, int(is_causal),
+                                                int(cos_weight is not None), 0), q.device, workspace)
+    _keep(stream, (out,), given)
     nws = 0 if ws is None else ws.numel() * ws.element_size()
     strides = [_strides(t) for t in (q, k, v)]
     if Dv != D:
@@ -276,18 +309,22 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, grad_out: torch.Tenso
     B, Hq, Hkv, N, D, Dv = _check_inputs(q, k, v, cos_weight, sin_weight, (("grad_out", grad_out),))
     if tuple(grad_out.shape) != (B, Hq, N, Dv):
         raise ValueError("grad_out must have the shape of out ([B, Hq, N, Dv])")
-    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
-    dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
-    dv = torch.empty(v.shape, dtype=v.dtype, device=v.device) if dv is None else dv
+    given = [q, k, v, grad_out, cos_weight, sin_weight, dq, dk, dv, workspace, fwd_workspace]
+    with _memory_on(stream):
+        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
+        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
+        dv = torch.empty(v.shape, dtype=v.dtype, device=v.device) if dv is None else dv
     for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
         if t.shape != like.shape or t.dtype != like.dtype or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous tensor like its input")
     dt = _dtype_code(q)
-    ws = _workspace(lib.la_workspace_size_v(B, Hq, Hkv, N, D, Dv, dt, int(is_causal),
-                                            int(cos_weight is not None), 1), q.device, workspace)
+    with _memory_on(stream):
+        ws = _workspace(lib.la_workspace_size_v(B, Hq, Hkv, N, D, Dv, dt, int(is_causal),
+                                                int(cos_weight is not None), 1), q.device, workspace)
     nws = 0 if ws is None else ws.numel() * ws.element_size()
     if fwd_workspace is not None and fwd_workspace.device != q.device:
         raise ValueError("fwd_workspace must be on q's device")
+    _keep(stream, (dq, dk, dv), given)
     strides = [_strides(t) for t in (q, k, v, grad_out)]
     if Dv != D:
         if any(x is not None for x in strides):
@@ -344,10 +381,13 @@ def lowrank_fwd(x: torch.Tensor, U: torch.Tensor, V: torch.Tensor, bias: torch.T
     t = x V^T for ``lowrank_bwd(..., t=t_out)`` (``la_lowrank_fwd_t``)."""
     lib = load()
     M, K_in, r, K_out = _check_lowrank(x, U, V, bias)
+    given = [x, U, V, bias, out, t_out]
     if out is None:
-        out = torch.empty(x.shape[:-1] + (K_out,), dtype=x.dtype, device=x.device)
+        with _memory_on(stream):
+            out = torch.empty(x.shape[:-1] + (K_out,), dtype=x.dtype, device=x.device)
     elif out.shape != x.shape[:-1] + (K_out,) or out.dtype != x.dtype or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor [..., K_out] of x's dtype")
+    _keep(stream, (out,), given)
     if t_out is None:
         st = lib.la_lowrank_fwd(_ptr(x), _ptr(U), _ptr(V), _ptr(bias), _ptr(out), M, K_in, r, K_out,
                                 _dtype_code(x), _stream_handle(stream))
@@ -375,9 +415,11 @@ def lowrank_bwd(x: torch.Tensor, U: torch.Tensor, V: torch.Tensor, grad_out: tor
     if grad_out.shape != x.shape[:-1] + (K_out,) or grad_out.dtype != x.dtype or not grad_out.is_contiguous():
         raise ValueError("grad_out must be a contiguous tensor [..., K_out] of x's dtype")
     dt = _dtype_code(x)
-    dx, dU, dV = torch.empty_like(x), torch.empty_like(U), torch.empty_like(V)
-    db = torch.empty_like(bias) if bias is not None else None
-    ws = _workspace(lib.la_lowrank_workspace_size(M, K_in, r, K_out, dt, 1), x.device, workspace)
+    with _memory_on(stream):
+        dx, dU, dV = torch.empty_like(x), torch.empty_like(U), torch.empty_like(V)
+        db = torch.empty_like(bias) if bias is not None else None
+        ws = _workspace(lib.la_lowrank_workspace_size(M, K_in, r, K_out, dt, 1), x.device, workspace)
+    _keep(stream, (dx, dU, dV, db), (x, U, V, grad_out, bias, workspace, t))
     nws = 0 if ws is None else ws.numel() * ws.element_size()
     if t is None:
         st = lib.la_lowrank_bwd(_ptr(x), _ptr(U), _ptr(V), _ptr(grad_out), _ptr(dx), _ptr(dU), _ptr(dV), _ptr(db),
@@ -507,8 +549,11 @@ def decay_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torc
     for name, t in (("initial_state", initial_state), ("final_state", final_state)):
         if t is not None:
             _check_state(name, t, (B, Hkv, D, Dv), q)
-    out = _output("out", out, (B, Hq, N, Dv), q)
-    ws = _workspace(_decay_need(B, Hq, Hkv, N, D, Dv, dt, 0), q.device, workspace)
+    given = (q, k, v, log_decay, initial_state, final_state, lengths, out, workspace)
+    with _memory_on(stream):
+        out = _output("out", out, (B, Hq, N, Dv), q)
+        ws = _workspace(_decay_need(B, Hq, Hkv, N, D, Dv, dt, 0), q.device, workspace)
+    _keep(stream, (out,), given)
     st = lib.la_decay_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), log_decay.data_ptr(),
                           _addr(initial_state), _addr(final_state), _addr(lengths), B, Hq, Hkv, N, D, Dv, dt, scale,
                           _stride_arg(q), _stride_arg(k), _stride_arg(v), _addr(ws), _nbytes(ws), _raw_stream(stream))
@@ -536,8 +581,11 @@ def decay_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, grad_out: torch
                     ("grad_initial_state", grad_initial_state)):
         if t is not None:
             _check_state(name, t, (B, Hkv, D, Dv), q)
-    dq, dk, dv = _output("dq", dq, q.shape, q), _output("dk", dk, k.shape, k), _output("dv", dv, v.shape, v)
-    ws = _workspace(_decay_need(B, Hq, Hkv, N, D, Dv, dt, 1), q.device, workspace)
+    given = (q, k, v, grad_out, log_decay, initial_state, grad_final_state, grad_initial_state, dq, dk, dv, workspace)
+    with _memory_on(stream):
+        dq, dk, dv = _output("dq", dq, q.shape, q), _output("dk", dk, k.shape, k), _output("dv", dv, v.shape, v)
+        ws = _workspace(_decay_need(B, Hq, Hkv, N, D, Dv, dt, 1), q.device, workspace)
+    _keep(stream, (dq, dk, dv), given)
     st = lib.la_decay_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), grad_out.data_ptr(), dq.data_ptr(), dk.data_ptr(),
                           dv.data_ptr(), log_decay.data_ptr(), _addr(initial_state), _addr(grad_final_state),
                           _addr(grad_initial_state), B, Hq, Hkv, N, D, Dv, dt, scale, _stride_arg(q), _stride_arg(k),
@@ -566,7 +614,10 @@ def decay_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, state: torch.T
     _check_state("state", state, (pool, Hkv, D, Dv), q)
     if state_out is not None:
         _check_state("state_out", state_out, (pool, Hkv, D, Dv), q)
-    out = _output("out", out, (B, Hq, 1, Dv), q)
+    given = (q, k, v, state, log_decay, slots, state_out, out)
+    with _memory_on(stream):
+        out = _output("out", out, (B, Hq, 1, Dv), q)
+    _keep(stream, (out,), given)
     st = lib.la_decay_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), state.data_ptr(),
                            (state if state_out is None else state_out).data_ptr(), log_decay.data_ptr(), _addr(slots),
                            pool, B, Hq, Hkv, D, Dv, _dtype_code(q), scale, _stride_arg(q), _stride_arg(k),
@@ -670,7 +721,10 @@ def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, *, q_weight: torch.Tensor
     lib = load()
     B, Hq, Hkv, N, D = _check_qk(q, k)
     a = _qk_args(q, q_weight, k_weight, eps, positions, inv_freq, sections, interleaved, normalize)
-    q_out, k_out = _output("q_out", q_out, q.shape, q), _output("k_out", k_out, k.shape, k)
+    given = (q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out)
+    with _memory_on(stream):
+        q_out, k_out = _output("q_out", q_out, q.shape, q), _output("k_out", k_out, k.shape, k)
+    _keep(stream, (q_out, k_out), given)
     st = lib.la_qk_norm_rope_fwd(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), B, Hq, Hkv, N, D,
                                  _dtype_code(q), _stride_arg(q), _stride_arg(k), ctypes.byref(a), _raw_stream(stream))
     if st != LA_OK:
@@ -696,12 +750,15 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, grad_q: torch.Tensor, gra
     if grad_q.shape != q.shape or grad_k.shape != k.shape:
         raise ValueError("grad_q and grad_k must have the shapes of q and k")
     a = _qk_args(q, q_weight, k_weight, eps, positions, inv_freq, sections, interleaved, normalize)
-    dq, dk = _output("dq", dq, q.shape, q), _output("dk", dk, k.shape, k)
-    dqw = torch.empty_like(q_weight) if q_weight is not None else None
-    dkw = torch.empty_like(k_weight) if k_weight is not None else None
+    given = (q, k, grad_q, grad_k, q_weight, k_weight, positions, inv_freq, dq, dk, workspace)
     dt, ws = _dtype_code(q), None
-    if dqw is not None or dkw is not None:
-        ws = _workspace(_qk_need(B, Hq, Hkv, N, D, dt), q.device, workspace)
+    with _memory_on(stream):
+        dq, dk = _output("dq", dq, q.shape, q), _output("dk", dk, k.shape, k)
+        dqw = torch.empty_like(q_weight) if q_weight is not None else None
+        dkw = torch.empty_like(k_weight) if k_weight is not None else None
+        if dqw is not None or dkw is not None:
+            ws = _workspace(_qk_need(B, Hq, Hkv, N, D, dt), q.device, workspace)
+    _keep(stream, (dq, dk, dqw, dkw), given)
     st = lib.la_qk_norm_rope_bwd(q.data_ptr(), k.data_ptr(), grad_q.data_ptr(), grad_k.data_ptr(), dq.data_ptr(),
                                  dk.data_ptr(), _addr(dqw), _addr(dkw), B, Hq, Hkv, N, D, dt, _stride_arg(q),
                                  _stride_arg(k), _stride_arg(grad_q), _stride_arg(grad_k), ctypes.byref(a), _addr(ws),
