@@ -177,15 +177,17 @@ def _check_inputs(q, k, v, cos_weight, sin_weight, extra=()):
             raise ValueError(f"{name} must be a [B, H, N, D] tensor whose last dimension is contiguous")
         if t.dtype != q.dtype:
             raise TypeError(f"{name} has dtype {t.dtype}, q has {q.dtype}")
+        if t.device != q.device:
+            raise ValueError(f"{name} is on {t.device}, q on {q.device}")
     B, Hq, N, D = q.shape
     if k.shape[0] != B or k.shape[2:] != (N, D) or v.shape[:3] != k.shape[:3]:
         raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
     if (cos_weight is None) != (sin_weight is None):
         raise ValueError("give both cos_weight and sin_weight or neither")
     for name, w in (("cos_weight", cos_weight), ("sin_weight", sin_weight)):
-        if w is not None and (w.dtype != torch.float32 or not w.is_cuda or w.shape != (N,)
+        if w is not None and (w.dtype != torch.float32 or w.device != q.device or w.shape != (N,)
                               or not w.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous float32 CUDA vector of length N={N}")
+            raise ValueError(f"{name} must be a contiguous float32 CUDA vector of length N={N} on q's device")
     return B, Hq, k.shape[1], N, D, v.shape[3]
 
 
@@ -199,6 +201,17 @@ def _strides(t):
 def _stream_handle(stream) -> ctypes.c_void_p:
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _check_device(like, stream):
+    """The library launches on the current device; the call's tensors, which lie on ``like``'s, and its stream must be of
+    that one."""
+    at, here = like.get_device(), torch.cuda.current_device()
+    if at != here:
+        raise ValueError(f"the tensors are on cuda:{at}, the current device is cuda:{here}: "
+                         f"call under torch.cuda.device({at})")
+    if stream is not None and stream.device.index != at:
+        raise ValueError(f"the tensors are on cuda:{at}, the stream is one of {stream.device}")
 
 
 def workspace_size(B, Hq, Hkv, N, D, dtype: torch.dtype, is_causal: bool, has_weights: bool,
@@ -248,6 +261,8 @@ def _workspace(nbytes: int, device, given):
         if given.numel() * given.element_size() < nbytes:
             raise ValueError(f"workspace holds {given.numel() * given.element_size()} bytes, "
                              f"{nbytes} needed")
+        if given.device != device or not given.is_contiguous():
+            raise ValueError("workspace must be contiguous and on the inputs' device")
         return given
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
@@ -260,10 +275,12 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, is_causal: bool = Fal
     v's last dimension; with Dv != D the inputs must be contiguous)."""
     lib = load()
     B, Hq, Hkv, N, D, Dv = _check_inputs(q, k, v, cos_weight, sin_weight)
+    _check_device(q, stream)
     oshape = (B, Hq, N, Dv)
     given = [q, k, v, cos_weight, sin_weight, out, workspace]
-    if out is not None and (tuple(out.shape) != oshape or out.dtype != q.dtype or not out.is_contiguous()):
-        raise ValueError(f"out must be a contiguous {oshape} tensor of q's dtype")
+    if out is not None and (tuple(out.shape) != oshape or out.dtype != q.dtype or out.device != q.device
+                            or not out.is_contiguous()):
+        raise ValueError(f"out must be a contiguous {oshape} tensor of q's dtype on q's device")
     dt = _dtype_code(q)
     with _memory_on(stream):
         out = torch.empty(oshape, dtype=q.dtype, device=q.device) if out is None else out
@@ -307,6 +324,7 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, grad_out: torch.Tenso
     (``la_bwd_from_fwd``).  The results are the same either way."""
     lib = load()
     B, Hq, Hkv, N, D, Dv = _check_inputs(q, k, v, cos_weight, sin_weight, (("grad_out", grad_out),))
+    _check_device(q, stream)
     if tuple(grad_out.shape) != (B, Hq, N, Dv):
         raise ValueError("grad_out must have the shape of out ([B, Hq, N, Dv])")
     given = [q, k, v, grad_out, cos_weight, sin_weight, dq, dk, dv, workspace, fwd_workspace]
@@ -315,7 +333,7 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, grad_out: torch.Tenso
         dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
         dv = torch.empty(v.shape, dtype=v.dtype, device=v.device) if dv is None else dv
     for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        if t.shape != like.shape or t.dtype != like.dtype or not t.is_contiguous():
+        if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous tensor like its input")
     dt = _dtype_code(q)
     with _memory_on(stream):
@@ -365,6 +383,8 @@ def _check_lowrank(x, U, V, bias):
             raise ValueError(f"{name} must be a contiguous CUDA tensor")
         if t.dtype != x.dtype:
             raise TypeError(f"{name} has dtype {t.dtype}, x has {x.dtype}")
+        if t.device != x.device:
+            raise ValueError(f"{name} is on {t.device}, x on {x.device}")
     if U.dim() != 2 or V.dim() != 2 or x.shape[-1] != V.shape[1] or U.shape[1] != V.shape[0]:
         raise ValueError(f"shapes disagree: x {tuple(x.shape)}, U {tuple(U.shape)}, V {tuple(V.shape)}")
     if bias is not None and bias.shape != (U.shape[0],):
@@ -381,20 +401,22 @@ def lowrank_fwd(x: torch.Tensor, U: torch.Tensor, V: torch.Tensor, bias: torch.T
     t = x V^T for ``lowrank_bwd(..., t=t_out)`` (``la_lowrank_fwd_t``)."""
     lib = load()
     M, K_in, r, K_out = _check_lowrank(x, U, V, bias)
+    _check_device(x, stream)
     given = [x, U, V, bias, out, t_out]
     if out is None:
         with _memory_on(stream):
             out = torch.empty(x.shape[:-1] + (K_out,), dtype=x.dtype, device=x.device)
-    elif out.shape != x.shape[:-1] + (K_out,) or out.dtype != x.dtype or not out.is_contiguous():
-        raise ValueError("out must be a contiguous tensor [..., K_out] of x's dtype")
+    elif out.shape != x.shape[:-1] + (K_out,) or out.dtype != x.dtype or out.device != x.device \
+            or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor [..., K_out] of x's dtype on x's device")
     _keep(stream, (out,), given)
     if t_out is None:
         st = lib.la_lowrank_fwd(_ptr(x), _ptr(U), _ptr(V), _ptr(bias), _ptr(out), M, K_in, r, K_out,
                                 _dtype_code(x), _stream_handle(stream))
         call = "la_lowrank_fwd"
     else:
-        if t_out.shape != (M, r) or t_out.dtype != x.dtype or not t_out.is_contiguous() or not t_out.is_cuda:
-            raise ValueError(f"t_out must be a contiguous CUDA tensor [{M}, {r}] of x's dtype")
+        if t_out.shape != (M, r) or t_out.dtype != x.dtype or not t_out.is_contiguous() or t_out.device != x.device:
+            raise ValueError(f"t_out must be a contiguous CUDA tensor [{M}, {r}] of x's dtype on x's device")
         st = lib.la_lowrank_fwd_t(_ptr(x), _ptr(U), _ptr(V), _ptr(bias), _ptr(out), _ptr(t_out), M, K_in, r,
                                   K_out, _dtype_code(x), _stream_handle(stream))
         call = "la_lowrank_fwd_t"
@@ -412,8 +434,10 @@ def lowrank_bwd(x: torch.Tensor, U: torch.Tensor, V: torch.Tensor, grad_out: tor
     one pass over x fewer)."""
     lib = load()
     M, K_in, r, K_out = _check_lowrank(x, U, V, bias)
-    if grad_out.shape != x.shape[:-1] + (K_out,) or grad_out.dtype != x.dtype or not grad_out.is_contiguous():
-        raise ValueError("grad_out must be a contiguous tensor [..., K_out] of x's dtype")
+    _check_device(x, stream)
+    if grad_out.shape != x.shape[:-1] + (K_out,) or grad_out.dtype != x.dtype or grad_out.device != x.device \
+            or not grad_out.is_contiguous():
+        raise ValueError("grad_out must be a contiguous tensor [..., K_out] of x's dtype on x's device")
     dt = _dtype_code(x)
     with _memory_on(stream):
         dx, dU, dV = torch.empty_like(x), torch.empty_like(U), torch.empty_like(V)
@@ -426,8 +450,8 @@ def lowrank_bwd(x: torch.Tensor, U: torch.Tensor, V: torch.Tensor, grad_out: tor
                                 M, K_in, r, K_out, dt, _ptr(ws), nws, _stream_handle(stream))
         call = "la_lowrank_bwd"
     else:
-        if t.shape != (M, r) or t.dtype != x.dtype or not t.is_contiguous() or not t.is_cuda:
-            raise ValueError(f"t must be a contiguous CUDA tensor [{M}, {r}] of x's dtype")
+        if t.shape != (M, r) or t.dtype != x.dtype or not t.is_contiguous() or t.device != x.device:
+            raise ValueError(f"t must be a contiguous CUDA tensor [{M}, {r}] of x's dtype on x's device")
         st = lib.la_lowrank_bwd_t(_ptr(x), _ptr(U), _ptr(V), _ptr(t), _ptr(grad_out), _ptr(dx), _ptr(dU), _ptr(dV),
                                   _ptr(db), M, K_in, r, K_out, dt, _ptr(ws), nws, _stream_handle(stream))
         call = "la_lowrank_bwd_t"
@@ -542,6 +566,7 @@ def decay_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torc
     Returns ``out`` [B, Hq, N, Dv]."""
     lib = load()
     B, Hq, Hkv, N, D, Dv = _check_qkv(q, k, v)
+    _check_device(q, stream)
     dt = _dtype_code(q)
     _check_vector("log_decay", log_decay, Hkv, torch.float32, q)
     if lengths is not None:
@@ -573,6 +598,7 @@ def decay_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, grad_out: torch
     ``log_decay`` gets no gradient."""
     lib = load()
     B, Hq, Hkv, N, D, Dv = _check_qkv(q, k, v, grad_out)
+    _check_device(q, stream)
     if tuple(grad_out.shape) != (B, Hq, N, Dv):
         raise ValueError("grad_out must have the shape of out ([B, Hq, N, Dv])")
     dt = _dtype_code(q)
@@ -605,6 +631,7 @@ def decay_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, state: torch.T
     ``state``).  Returns ``out`` [B, Hq, 1, Dv]."""
     lib = load()
     B, Hq, Hkv, N, D, Dv = _check_qkv(q, k, v)
+    _check_device(q, stream)
     if N != 1:
         raise ValueError(f"decay_step takes one token per sequence (N = 1), got N = {N}")
     _check_vector("log_decay", log_decay, Hkv, torch.float32, q)
@@ -720,6 +747,7 @@ def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, *, q_weight: torch.Tensor
     turned.  Without positions: the norm alone; with ``normalize=False``: the rotation alone."""
     lib = load()
     B, Hq, Hkv, N, D = _check_qk(q, k)
+    _check_device(q, stream)
     a = _qk_args(q, q_weight, k_weight, eps, positions, inv_freq, sections, interleaved, normalize)
     given = (q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out)
     with _memory_on(stream):
@@ -747,6 +775,7 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, grad_q: torch.Tensor, gra
     without that weight."""
     lib = load()
     B, Hq, Hkv, N, D = _check_qk(q, k, (("grad_q", grad_q), ("grad_k", grad_k)))
+    _check_device(q, stream)
     if grad_q.shape != q.shape or grad_k.shape != k.shape:
         raise ValueError("grad_q and grad_k must have the shapes of q and k")
     a = _qk_args(q, q_weight, k_weight, eps, positions, inv_freq, sections, interleaved, normalize)
