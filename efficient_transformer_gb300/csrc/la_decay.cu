@@ -24,6 +24,7 @@ struct DecayPlan {
     la_path path;
     int seg_len, nseg;
     long long state_units;                      // sequences that the state kernel sums
+    bool sums_fin;                              // a state that goes out comes from the state kernel, not from the passes
     size_t state_bytes, part_bytes, ws_bytes;   // one array of segment states, one of their parts; all of them
 };
 
@@ -33,11 +34,29 @@ bool tc_runs(int D, int Dv, la_dtype dt) { return dt == LA_BF16 && D != 32 && Dv
 struct Parts {
     int n, len;
 };
+Parts parts_of(int chunks, int per) { return Parts{(chunks + per - 1) / per, per * kDecayTcChunk}; }
 Parts sum_parts(long long units, int nsum, int chunks) {
     const long long fit = kPlanSms / (units * nsum);
     const int want = fit < 1 ? 1 : fit < chunks ? (int)fit : chunks;
-    const int per = (chunks + want - 1) / want;
-    return Parts{(chunks + per - 1) / per, per * kDecayTcChunk};
+    return parts_of(chunks, (chunks + want - 1) / want);
+}
+// The same where the sum over `heads` is an output: at most kDecayChain products in an accumulator, and where there
+// are more blocks than SMs the length whose waves end first, a block's start costing five products (10 x 16 heads, N 8192,
+// D 128, with the join: 222 us in whole sequences, 159 us in four parts each).
+Parts exact_parts(long long units, int nsum, int chunks, int heads, int Dv) {
+    const int chain = kDecayChain * decay_accumulators(Dv) / heads, most = chain < 1 ? 1 : chain < chunks ? chain : chunks;
+    Parts best = sum_parts(units, nsum, chunks);
+    if (best.n > 1 && best.len <= most * kDecayTcChunk) return best;
+    long long cost = -1;
+    for (int per = most; per >= 1 && per >= most / 16; --per) {
+        const Parts p = parts_of(chunks, per);
+        const long long c = (units * nsum * p.n + kPlanSms - 1) / kPlanSms * (5 + (long long)per * heads);
+        if (cost < 0 || c < cost) {
+            cost = c;
+            best = p;
+        }
+    }
+    return best;
 }
 
 // The segments of a sequence: the count whose schedule ends first.  A schedule is waves of blocks that run at once,
@@ -133,7 +152,16 @@ DecayPlan make_plan(int B, int Hq, int Hkv, int N, int D, int Dv, la_dtype dt, b
     }
     pl.seg_len = best_cps * chunk;
     pl.nseg = (N + pl.seg_len - 1) / pl.seg_len;
-    if (pl.nseg == 1) return pl;
+    const int out_heads = bwd ? reps : 1;
+    if (pl.nseg == 1) {
+        // one array is summed, where a state goes out
+        pl.sums_fin = pl.path == LA_PATH_TCGEN05 && (Dv == 128 || (long long)nchunks * out_heads > kDecayChain);
+        pl.state_units = heads;
+        if (pl.sums_fin)
+            pl.ws_bytes = pl.part_bytes = (size_t)heads * exact_parts(heads, 1, nchunks, out_heads, Dv).n * D * Dv * 4;
+        return pl;
+    }
+    pl.sums_fin = pl.path == LA_PATH_TCGEN05;
     pl.state_bytes = ((size_t)heads * pl.nseg * D * Dv * 4 + 255) / 256 * 256;
     if (pl.path == LA_PATH_SIMT) {
         pl.ws_bytes = pl.state_bytes * (bwd ? 2 : 1);
@@ -142,7 +170,7 @@ DecayPlan make_plan(int B, int Hq, int Hkv, int N, int D, int Dv, la_dtype dt, b
     // room for the parts of all segments (with a final state) and of all but the last
     pl.state_units = state_units;
     const int n0 = (pl.nseg - 1) * sum_parts(state_units, pl.nseg - 1, best_cps).n,
-              n1 = pl.nseg * sum_parts(state_units, pl.nseg, best_cps).n;
+              n1 = pl.nseg * exact_parts(state_units, pl.nseg, best_cps, out_heads, Dv).n;
     pl.part_bytes = ((size_t)heads * (n0 > n1 ? n0 : n1) * D * Dv * 4 + 255) / 256 * 256;
     // forward: S; backward: S^T, A and A^T
     pl.ws_bytes = pl.state_bytes * (bwd ? 3 : 1) + pl.part_bytes * (bwd ? 2 : 1);
@@ -187,11 +215,12 @@ la_status run(bool bwd, const Given &a, int B, int Hq, int Hkv, int N, int D, in
         !input_strides(a.sv, B, Hkv, N, Dv, &sv) || !input_strides(a.sg, B, Hq, N, Dv, &sg))
         return LA_ERR_ARG;
     const DecayPlan pl = make_plan(B, Hq, Hkv, N, D, Dv, dt, bwd);
-    if (pl.ws_bytes > 0) {
+    const bool tc = pl.path == LA_PATH_TCGEN05, state_out = a.s_out || a.ds_out;
+    const bool sums = tc && (pl.nseg > 1 || (pl.sums_fin && state_out));   // the state kernel runs
+    if (tc ? sums : pl.ws_bytes > 0) {
         if (!ws || ws_bytes < pl.ws_bytes) return LA_ERR_WORKSPACE;
         if (!aligned(ws, 256)) return LA_ERR_ALIGN;
     }
-    const bool tc = pl.path == LA_PATH_TCGEN05;
     if (tc)   // TMA: every stride a multiple of 16 bytes (8 bf16)
         for (const Strides &x : {sq, sk, sv, sg})
             if (x.b % 8 || x.h % 8 || x.n % 8) return LA_ERR_ALIGN;
@@ -201,7 +230,8 @@ la_status run(bool bwd, const Given &a, int B, int Hq, int Hkv, int N, int D, in
     p.B = B; p.Hkv = Hkv; p.n_rep = Hq / Hkv; p.N = N; p.D = D; p.Dv = Dv;
     p.scale = scale;
     p.seg_len = pl.seg_len; p.nseg = pl.nseg;
-    auto at = [&](size_t off) { return pl.nseg > 1 ? reinterpret_cast<float *>(static_cast<char *>(ws) + off) : nullptr; };
+    auto mem = [&](size_t off) { return reinterpret_cast<float *>(static_cast<char *>(ws) + off); };
+    auto at = [&](size_t off) { return pl.nseg > 1 ? mem(off) : nullptr; };
     float *slots0 = at(0), *slots1 = at(pl.state_bytes), *slots2 = tc ? at(2 * pl.state_bytes) : slots1;
     DecayStateParams sp{};
     sp.log_decay = a.log_decay;
@@ -211,12 +241,15 @@ la_status run(bool bwd, const Given &a, int B, int Hq, int Hkv, int N, int D, in
     sp.y[0] = a.k; sp.z[0] = a.v; sp.sy[0] = sk; sp.sz[0] = sv; sp.init[0] = a.s_in; sp.init_mul[0] = 1.f;
     sp.heads[0] = 1; sp.rev[0] = 0; sp.slots[0] = slots0; sp.exact[0] = a.s_out != nullptr;
     sp.n = 1;
-    // on the tensor cores a cut sequence's last state comes with the segments' sums, else with the pass itself
-    const bool main_fin = !tc || pl.nseg == 1;
+    // on the tensor cores a cut sequence's last state comes with the segments' sums, and so does one whose chain of
+    // products is long (kDecayChain); else with the pass itself
+    const bool main_fin = !pl.sums_fin;
     sp.fin[0] = a.s_out; sp.fin[1] = a.ds_out; sp.fin_mul[0] = 1.f; sp.fin_mul[1] = scale;
-    sp.nsum = a.s_out || a.ds_out ? pl.nseg : pl.nseg - 1;
-    if (tc && pl.nseg > 1) {
-        const Parts parts = sum_parts(pl.state_units, sp.nsum, pl.seg_len / kDecayTcChunk);
+    sp.nsum = state_out ? pl.nseg : pl.nseg - 1;
+    if (sums) {
+        const int chunks = pl.seg_len / kDecayTcChunk;
+        const Parts parts = state_out ? exact_parts(pl.state_units, sp.nsum, chunks, bwd ? p.n_rep : 1, Dv)
+                                      : sum_parts(pl.state_units, sp.nsum, chunks);
         sp.nsub = parts.n;
         sp.sub_len = parts.len;
     }
@@ -259,6 +292,15 @@ la_status run(bool bwd, const Given &a, int B, int Hq, int Hkv, int N, int D, in
         if (e == cudaSuccess && pl.nseg > 1) e = decay_tc_states(sp, s);
         if (e == cudaSuccess && pl.nseg > 1) e = decay_tc_join(sp, s);
         if (e == cudaSuccess) e = decay_tc_passes(p, s);
+        if (sums && pl.nseg == 1) {
+            // the sum of the array that goes out; after the pass, which reads the starting state that this may replace
+            sp.start[0] = sp.start[1] = sp.start_tr[0] = sp.start_tr[1] = nullptr;
+            sp.part[0] = sp.part[1] = mem(0);
+            sp.first = bwd;
+            sp.n = 1;
+            if (e == cudaSuccess) e = decay_tc_states(sp, s);
+            if (e == cudaSuccess) e = decay_tc_join(sp, s);
+        }
         return e == cudaSuccess ? LA_OK : cuda_fail(e);
     }
     if (pl.nseg > 1) e = decay_simt_states(sp, dt, s);

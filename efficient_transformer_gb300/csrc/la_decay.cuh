@@ -66,7 +66,7 @@ struct DecayStateParams {
     float *fin[2];              // tensor cores: the state after the last segment, or null (its sum is taken
     float fin_mul[2];           // too then: nsum = nseg segments)
     int nsum;
-    int n;                      // state arrays of this launch (1 or 2)
+    int first, n;               // state arrays of this launch: [first, first + n)
     int B, Hkv, N, D, Dv, seg_len, nseg;
     int nsub, sub_len;          // tensor cores: parts of a segment
     float *part[2];
@@ -99,6 +99,11 @@ cudaError_t decay_simt_passes(const DecayParams &p, int pass0, int npass, la_dty
 // Tensor-core kernels (la_decay_tc.cu): bfloat16, widths 64 and 128.  Segments are cut in token
 // order, multiples of kDecayTcChunk tokens; every pass of a call in one launch where the widths allow.
 constexpr int kDecayTcChunk = 128;
+// The MMA's sums are cut, not rounded, to float32 at each of their steps, so that a long chain of them drifts towards
+// zero: with two terms of y, 2.4e-7 of the sum a chunk and head.  Beside the 4e-6 that y's two terms leave, a
+// state that is an output has kDecayChain of them at most in an accumulator: 9e-6 in all, whatever the batch.
+constexpr int kDecayChain = 32;
+__host__ __device__ constexpr int decay_accumulators(int Dv) { return 512 / Dv; }   // of the state kernel
 cudaError_t decay_tc_states(const DecayStateParams &p, cudaStream_t s);
 cudaError_t decay_tc_join(const DecayStateParams &p, cudaStream_t s);
 cudaError_t decay_tc_passes(const DecayParams &p, cudaStream_t s);

@@ -16,7 +16,7 @@
 // of its own.  That halves the MMA's shared-memory reads, which at 128 x 128 x 16 from shared memory would
 // take all of its bandwidth, and leaves the shared memory to the TMA tiles.  The scores have two buffers, so that the
 // next item's scores and P run beside this one's O; where S and O are 128 columns wide that takes Y^T's place, and y is
-// decayed in its tile instead (in one term: with a state as output, in two, the scores have one buffer).
+// decayed in its tile instead, in one term: there a state that is an output comes from the state kernel.
 // Several heads of x share one chunk of y, z (grouped queries; S moves on after the last), or several heads
 // of y, z share one of x (their gradients; O and S sum over the heads).
 //
@@ -30,8 +30,7 @@
 // 5.3 TB/s; 314 us with the segments' sums, which read k and v once more); with one head of x to one of y and z the
 // instructions of the roles, 2.4 us a chunk of 128 x 128 and 2.0 us of 64 x 64 on an SM (8 x 19 heads, N 1024, D 128:
 // 33 us; gradients of 2 x 16 heads, N 8192, D 128: 161 us).  There the tensor pipe is busy for 15 to 30 % of the time
-// and an SM's warps issue 1.3 to 1.7 instructions a cycle.  With one buffer of scores (and y in two
-// terms) the grouped queries took 366 us.
+// and an SM's warps issue 1.3 to 1.7 instructions a cycle.
 #include "la_decay.cuh"
 #include "la_tc_common.cuh"
 
@@ -88,23 +87,24 @@ struct PassMaps {
 };
 
 // YSM: y is decayed in place in shared memory (else Y^T is made in TMEM, one or two terms).
-template <int DX, int DZ, bool YSM>
+template <int DX, int DZ>
 struct MainCfg {
+    static constexpr bool YSM = DZ == 128;
     static constexpr int X_BYTES = C * DX * 2, Y_BYTES = C * DX * 2, Z_BYTES = C * DZ * 2, S_BYTES = DX * DZ * 2;
     static constexpr int O_BYTES = C * DZ * 2;
     static constexpr int NX = DX == 64 ? 4 : 2;
-    static constexpr int NY = YSM ? (DX == 64 ? 3 : 2) : DZ == 64 ? (DX == 64 ? 3 : 2) : (DX == 64 ? 2 : 1);
-    static constexpr int NZ = DZ == 64 ? 4 : YSM && DX == 64 ? 3 : 2;
+    static constexpr int NY = DX == 64 ? 3 : 2;
+    static constexpr int NZ = DZ == 64 ? 4 : DX == 64 ? 3 : 2;
     // output tiles: of their own; with YSM in the z tile that is used up or, where several heads share it, in place of
     // y's other stages (which such a block needs less: a y tile serves all of them)
-    static constexpr int NO = YSM ? 0 : DX == 64 && DZ == 64 ? 2 : 1;
+    static constexpr int NO = YSM ? 0 : DX == 64 ? 2 : 1;
     static constexpr int SMEM = NX * X_BYTES + NY * Y_BYTES + NZ * Z_BYTES + NO * O_BYTES + S_BYTES + 1024;
     static_assert(SMEM + 2048 <= kSmemLimit, "tiles, barriers and tables");
     static_assert(!YSM || (NY - 1) * Y_BYTES >= O_BYTES, "an output tile in y's other stages");
     // (S's MMA reads 128 columns from a y tile's start: with DX = 64 the next y stage or the first z tile)
     static_assert(DX == 128 || Z_BYTES >= C * 64 * 2, "128 columns from a y tile's start");
-    // TMEM: S, O, one or two buffers of scores, Y^T hi | lo
-    static constexpr int NSC = DZ == 64 || YSM ? 2 : 1;
+    // TMEM: S, O, two buffers of scores, Y^T hi | lo
+    static constexpr int NSC = 2;
     static constexpr int T_S = 0, T_O = DZ, T_A = 2 * DZ, T_YH = T_A + 128 * NSC, T_YL = T_YH + 64;
     static_assert((YSM ? T_YH : T_YL + 64) <= 512, "TMEM columns");
 };
@@ -213,11 +213,12 @@ __device__ __noinline__ void zero_rows(uint8_t *tile, int valid, int i, int nth)
         *reinterpret_cast<uint4 *>(tile + swz_chunk(C, valid + idx / (W / 8), idx % (W / 8))) = make_uint4(0u, 0u, 0u, 0u);
 }
 
-template <int DX, int DZ, bool YSM>
+template <int DX, int DZ>
 __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_constant__ PassMaps maps,
                                                               const __grid_constant__ DecayParams p, int pass0,
                                                               int npass) {
-    using K = MainCfg<DX, DZ, YSM>;
+    using K = MainCfg<DX, DZ>;
+    constexpr bool YSM = K::YSM;
     constexpr int NX = K::NX, NYS = K::NY, NZ = K::NZ, NSC = K::NSC, NO = K::NO;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t x_full[NX], x_empty[NX], y_full[NYS], y_empty[NYS], z_full[NZ], z_empty[NZ];
@@ -664,7 +665,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             if (d == 0) LA_TL(k, 10);
             mbar_arrive_warp(&s_conv);
         }
-        if (ok && ps.fin && u == p.nseg - 1) {
+        if (!YSM && ok && ps.fin && u == p.nseg - 1) {
             // what leaves a reverse pass decays once more; with no token at all it is what came in
             const float mul = ps.fin_mul * (ps.first_off && n > 0 ? exp2f(l2 * ps.first_off) : 1.f);
             if (nchunk > 0) {
@@ -893,7 +894,7 @@ struct StateCfg {
     static constexpr int SMEM = NS * STAGE + LO_BYTES + 1024;
     static_assert(D == 128 || STAGE - Y_BYTES >= C * 64 * 2, "128 columns from a y tile's start");
     static_assert(NS >= 2, "two stages");
-    static constexpr int NA = 512 / DV;   // accumulators
+    static constexpr int NA = decay_accumulators(DV);
 };
 
 template <int D, int DV>
@@ -909,7 +910,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
     pdl_wait();
     const int warp = threadIdx.x / 32;
     const int nparts = p.nsum * p.nsub, pidx = blockIdx.x % nparts, ah = blockIdx.x / nparts;
-    const int a = ah / (p.B * p.Hkv), bg = ah % (p.B * p.Hkv), b = bg / p.Hkv, h = bg % p.Hkv;
+    const int a = p.first + ah / (p.B * p.Hkv), bg = ah % (p.B * p.Hkv), b = bg / p.Hkv, h = bg % p.Hkv;
     const int n = decay_tokens(p.lengths, b, p.N), rev = p.rev[a], heads = p.heads[a];
     const bool exact = p.exact[a];
     const Part part = sub_part_of(n, p.N, pidx / p.nsub, p.nseg, p.seg_len, pidx % p.nsub, p.nsub, p.sub_len, rev);
@@ -940,8 +941,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = tmem_base;
-    // The MMA's sums are cut, not rounded, to float32 at each of their steps, so that a long chain of them drifts: a sum
-    // that is an output is made in several accumulators in turn, which meet at the end.
+    // a sum that is an output is made in several accumulators in turn, which meet at the end (kDecayChain)
     const int na = exact ? K::NA : 1;
 
     if (warp == 0) {
@@ -1073,7 +1073,7 @@ template <int D, int DV>
 __global__ void __launch_bounds__(kJoinThreads) k_decay_join(const __grid_constant__ DecayStateParams p) {
     pdl_wait();
     constexpr int kBlocks = D * DV / 16 / kJoinThreads;   // of one state
-    const int ah = blockIdx.x / kBlocks, a = ah / (p.B * p.Hkv), bg = ah % (p.B * p.Hkv), b = bg / p.Hkv, h = bg % p.Hkv;
+    const int ah = blockIdx.x / kBlocks, a = p.first + ah / (p.B * p.Hkv), bg = ah % (p.B * p.Hkv), b = bg / p.Hkv, h = bg % p.Hkv;
     const int idx = blockIdx.x % kBlocks * kJoinThreads + threadIdx.x, d = idx % (D / 4) * 4, e = idx / (D / 4) * 4;
     constexpr size_t E = (size_t)D * DV;
     const int n = decay_tokens(p.lengths, b, p.N), nparts = p.nsum * p.nsub;
@@ -1141,7 +1141,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_decay_join(const __grid_consta
 
 // ---- launches ---------------------------------------------------------------------------
 
-template <int DX, int DZ, bool YSM>
+template <int DX, int DZ>
 cudaError_t passes_d(const DecayParams &p, int pass0, int npass, cudaStream_t s) {
     PassMaps maps;
     for (int i = pass0; i < pass0 + npass; ++i) {
@@ -1153,8 +1153,8 @@ cudaError_t passes_d(const DecayParams &p, int pass0, int npass, cudaStream_t s)
         if (e == cudaSuccess) e = make_map_in(&maps.m[i][3], ps.out, p.B, Hx, p.N, DZ, contiguous_strides(Hx, p.N, DZ), 32);
         if (e != cudaSuccess) return e;
     }
-    auto kern = k_decay_tc<DX, DZ, YSM>;
-    constexpr int smem = MainCfg<DX, DZ, YSM>::SMEM;
+    auto kern = k_decay_tc<DX, DZ>;
+    constexpr int smem = MainCfg<DX, DZ>::SMEM;
     cudaError_t e = prepare(kern, smem);
     if (e != cudaSuccess) return e;
     TraceScope tr("decay_tc", s);
@@ -1164,19 +1164,14 @@ cudaError_t passes_d(const DecayParams &p, int pass0, int npass, cudaStream_t s)
 cudaError_t passes(const DecayParams &p, int pass0, int npass, cudaStream_t s) {
     const bool tr = p.pass[pass0].tr;
     const int DX = tr ? p.Dv : p.D, DZ = tr ? p.D : p.Dv;
-    if (DZ == 64) return DX == 64 ? passes_d<64, 64, false>(p, pass0, npass, s) : passes_d<128, 64, false>(p, pass0, npass, s);
-    // 128 columns of S and O leave no room in TMEM for two buffers of scores and Y^T; where this kernel's state is not
-    // an output (it is in one segment only) y is decayed in shared memory instead, once rounded
-    bool exact = false;
-    for (int i = pass0; i < pass0 + npass; ++i) exact = exact || p.pass[i].fin;
-    if (exact) return DX == 64 ? passes_d<64, 128, false>(p, pass0, npass, s) : passes_d<128, 128, false>(p, pass0, npass, s);
-    return DX == 64 ? passes_d<64, 128, true>(p, pass0, npass, s) : passes_d<128, 128, true>(p, pass0, npass, s);
+    if (DZ == 64) return DX == 64 ? passes_d<64, 64>(p, pass0, npass, s) : passes_d<128, 64>(p, pass0, npass, s);
+    return DX == 64 ? passes_d<64, 128>(p, pass0, npass, s) : passes_d<128, 128>(p, pass0, npass, s);
 }
 
 template <int D, int DV>
 cudaError_t states_d(const DecayStateParams &p, cudaStream_t s) {
     StateMaps maps;
-    for (int a = 0; a < p.n; ++a) {
+    for (int a = p.first; a < p.first + p.n; ++a) {
         cudaError_t e = make_map_in(&maps.m[a][0], p.y[a], p.B, p.Hkv * p.heads[a], p.N, D, p.sy[a], C);
         if (e == cudaSuccess) e = make_map_in(&maps.m[a][1], p.z[a], p.B, p.Hkv * p.heads[a], p.N, DV, p.sz[a], C);
         if (e != cudaSuccess) return e;

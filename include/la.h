@@ -296,7 +296,8 @@ la_status la_lowrank_bwd_t(const void *x, const void *U, const void *V, const vo
  * the other rows of the same 128-token chunk. */
 
 /* Bytes of workspace of la_decay_fwd (is_bwd = 0) or la_decay_bwd (is_bwd = 1, enough for the
- * forward too); 0 for arguments that they reject (and where none is needed).  Host-only. */
+ * forward too), with or without a state that goes out; 0 for arguments that they reject (and where
+ * none is needed).  Host-only. */
 size_t la_decay_workspace_size(int B, int Hq, int Hkv, int N, int D, int Dv, la_dtype dtype, int is_bwd);
 
 /* Kernel family of la_decay_fwd and la_decay_bwd: LA_PATH_TCGEN05 for bfloat16 with D and Dv in
