@@ -203,6 +203,8 @@ la_status run(bool bwd, const Given &a, int B, int Hq, int Hkv, int N, int D, in
     la_status st = check(B, Hq, Hkv, N, D, Dv, dt, scale);
     if (st != LA_OK) return st;
     if (!a.q || !a.k || !a.v || !a.log_decay) return LA_ERR_ARG;
+    // (the reverse states are carried without `scale`: the incoming gradient is divided by it)
+    if (bwd && !std::isfinite(1.f / scale)) return LA_ERR_ARG;
     if (bwd ? (!a.g || !a.dq || !a.dk || !a.dv) : !a.out) return LA_ERR_ARG;
     // (the passes of the gradients read both states while one of them writes grad_initial_state)
     if (a.ds_out && (a.ds_out == a.s_in || a.ds_out == a.ds_in)) return LA_ERR_ARG;

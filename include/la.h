@@ -290,7 +290,8 @@ la_status la_lowrank_bwd_t(const void *x, const void *U, const void *V, const vo
  *
  * log_decay [Hkv] is a float32 device vector, expected <= 0 (a non-finite -inf is gamma = 0:
  * each token sees itself alone); it gets no gradient.  Values above 0 grow the state by the
- * same formula.  scale: finite and not 0.
+ * same formula.  scale: finite and not 0; for the gradient with a finite reciprocal too, and
+ * grad_final_state / scale has to be within float32.
  *
  * A NaN or infinity in a token's row reaches, besides the outputs that depend on it, at most
  * the other rows of the same 128-token chunk. */

@@ -1,0 +1,21 @@
+"""More refusals of the decayed attention, on the host before any CUDA call."""
+import pytest
+
+from efficient_transformer_gb300 import build as la_build
+from efficient_transformer_gb300 import la
+from test_decay_host import FAKE, fwd
+
+
+@pytest.fixture(scope="module")
+def lib():
+    la_build.build()
+    return la.load()
+
+
+@pytest.mark.parametrize("scale,want", [(1e-39, la.LA_ERR_ARG), (-1e-40, la.LA_ERR_ARG), (float("inf"), la.LA_ERR_ARG),
+                                        (2e-38, la.LA_ERR_WORKSPACE), (-3e38, la.LA_ERR_WORKSPACE)])
+def test_gradients_divide_by_the_scale(lib, scale, want):
+    """The incoming state gradient is divided by `scale`: one without a finite reciprocal made NaN of zeros."""
+    a = [FAKE] * 8 + [None, None, None, 1, 4, 2, 4096, 64, 64, la.LA_BF16, scale, None, None, None, None, None, 0, None]
+    assert lib.la_decay_bwd(*a) == want
+    assert fwd(lib, scale=scale) == (la.LA_ERR_WORKSPACE if scale < 1e38 else la.LA_ERR_ARG)   # (the forward does not)
