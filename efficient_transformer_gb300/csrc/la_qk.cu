@@ -17,8 +17,9 @@
 //
 // Angles.  positions are 64-bit integers and inv_freq doubles, so an angle in float32, or even its
 // reduction mod 2 pi there, would lose far positions.  inv_freq / 2 pi becomes a 64-bit binary fraction of a
-// turn, and the integer product with the position wraps mod 2^64, i.e. mod one turn, exactly: the
-// remaining error is pos 2^-65 turns, before sincospif in float32.
+// turn, rounded to nearest, and the integer product with the position wraps mod 2^64, i.e. mod one turn, exactly: the
+// remaining error is |pos| 2^-65 turns (1.01 times that with inv_freq up to 1), before sincospif in float32, whose
+// argument has 2^-26: so far positions are as good as near ones up to 2^39.
 #include <cmath>
 
 #include "la_internal.cuh"
@@ -47,21 +48,24 @@ struct QkParams {
 };
 
 // inv_freq / 2 pi as a fraction of 2^64, wrapping: the double's 53-bit significand times
-// round(2^66 / 2 pi), shifted to its place (integer arithmetic: float64 units are few).
+// round(2^66 / 2 pi) = 2^66 / 2 pi + 0.015, shifted to its place with one rounding (integer arithmetic: float64 units
+// are few).
 __device__ __forceinline__ unsigned long long turns_of(double f) {
     const unsigned long long bits = (unsigned long long)__double_as_longlong(f);
     const int e = (int)((bits >> 52) & 0x7ff);
     const unsigned long long m = (bits & 0xfffffffffffffull) | (e ? 1ull << 52 : 0ull);
-    const unsigned long long k = 0xa2f9836e4e441529ull;   // 2^66 / (2 pi), rounded down
+    const unsigned long long k = 0xa2f9836e4e44152aull;
     const unsigned long long lo = m * k, hi = __umul64hi(m, k);
     const int sh = 54 - ((e ? e : 1) - 1023);   // m 2^(E - 52) / (2 pi) 2^64 = (m k) 2^(E - 54)
     unsigned long long r;
-    if (sh >= 128)
+    if (sh >= 128)   // (the product has 117 bits)
         r = 0;
-    else if (sh >= 64)
-        r = hi >> (sh - 64);
+    else if (sh > 64)
+        r = (hi >> (sh - 64)) + ((hi >> (sh - 65)) & 1);
+    else if (sh == 64)
+        r = hi + (lo >> 63);
     else if (sh > 0)
-        r = (hi << (64 - sh)) | (lo >> sh);
+        r = ((hi << (64 - sh)) | (lo >> sh)) + ((lo >> (sh - 1)) & 1);
     else
         r = sh > -64 ? lo << -sh : 0;
     return (bits >> 63) ? 0ull - r : r;

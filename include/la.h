@@ -354,7 +354,8 @@ la_status la_decay_step(const void *q, const void *k, const void *v, void *out, 
  * elements (p, p + rot / 2), or (2p, 2p + 1) with interleaved = 1; elements past rot are not turned.
  * positions: device int64 [axes, B, N] with element strides pos_strides[3] (0 broadcasts);
  * inv_freq: rot / 2 device float64; sections and pos_strides are host arrays.  Angles are reduced
- * in 64-bit integer turns, so they are exact to float32 for every position.
+ * in 64-bit integer turns: the reduction errs by |position| 2^-65 turns (inv_freq up to 1), which is
+ * below float32's own error for positions up to 2^39, and 2^-15 turns at 2^50.
  *
  * Inputs may be strided (rows must start on 16-byte boundaries, else LA_ERR_ALIGN); outputs are
  * contiguous and may not overlap the inputs.  Float32 arithmetic, D in {32, 64, 128}.  The pages have no
