@@ -41,7 +41,10 @@ constexpr int C = kDecayTcChunk;
 constexpr int kMainThreads = 768;
 
 // Bounded warp-uniform wait.  A try suspends the thread for 2 us at most, so that kTries of them are a few seconds
-// at most and tens of milliseconds at least; no wait of a block that runs takes one of them.
+// at most and tens of milliseconds at least; no wait of a block that runs takes one of them.  (The MMA warp of the scores
+// polls two barriers in turn without a suspension, kTries times at most: tens of milliseconds.)  A role whose wait ran out
+// leaves its loop, the others' waits then run out too, and the block ends as always: copies and MMAs in flight
+// drained, TMEM freed, the error latched.
 //
 // Code size is what this and the loops below are shaped by.  Each role's loop body runs once a chunk, so the roles'
 // code passes through the instruction caches in turn; at 38 KB in all it was fetched anew for each chunk (300
@@ -49,6 +52,7 @@ constexpr int kMainThreads = 768;
 // loops stay rolled where that costs a few instructions, and there is one copy of each product.
 #ifdef LA_TEST_HOOKS
 constexpr uint32_t kTries = 1u << 13;
+__device__ int g_la_test_skip_decay;   // withhold the first arrival of warp 4 of block 0: 1 passes, 2 sums (see there)
 #else
 constexpr uint32_t kTries = 1u << 21;
 #endif
@@ -566,7 +570,10 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             tmem_st_wait();
             tc_fence_before();
             if (i == 127) LA_TL(it, 8);
-            mbar_arrive_warp(&p_ready[sc.s]);
+#ifdef LA_TEST_HOOKS
+            if (!(g_la_test_skip_decay == 1 && blockIdx.x == 0 && it == 0 && warp == 4))
+#endif
+                mbar_arrive_warp(&p_ready[sc.s]);
             sc.next(NSC);
             if (first || !many) mbar_arrive_warp(&p_first[ot++ & 1]);
             if (last) r = 0;
@@ -1031,7 +1038,10 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
                 if (exact) *reinterpret_cast<uint4 *>(lo_tile + at) = make_uint4(r[0], r[1], r[2], r[3]);
             }
             fence_proxy_async();
-            mbar_arrive_warp(&y_ready[s]);
+#ifdef LA_TEST_HOOKS
+            if (!(g_la_test_skip_decay == 2 && blockIdx.x == 0 && it == 0 && warp == 4))
+#endif
+                mbar_arrive_warp(&y_ready[s]);
         }
         if (warp < 8 && wq * 32 < D) {
             if (ok && items > 0) ok = await(&fin, 0, &abort_flag);
@@ -1206,6 +1216,13 @@ cudaError_t decay_tc_passes(const DecayParams &p, cudaStream_t s) {
 }
 
 }  // namespace la
+
+#ifdef LA_TEST_HOOKS
+// Test builds only: arm the withheld arrival of the passes (1) or of the sums (2), or disarm it (0).
+extern "C" int la_test_withhold_decay(int which) {
+    return cudaMemcpyToSymbol(la::g_la_test_skip_decay, &which, sizeof(int)) == cudaSuccess ? 0 : 1;
+}
+#endif
 
 #ifdef LA_TIMELINE
 extern "C" int la_timeline_read_decay(long long *out) {
