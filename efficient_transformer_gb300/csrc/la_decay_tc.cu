@@ -26,11 +26,13 @@
 // The reverse passes (gradients of k and v) take the same steps with j >= i and gamma^(j-i), chunks from the
 // last to the first.
 //
-// What bounds it: with grouped queries the memory (32 query on 8 key/value heads, N 65536, D 128: 251 us for 1.34 GB,
-// 5.3 TB/s; 314 us with the segments' sums, which read k and v once more); with one head of x to one of y and z the
-// instructions of the roles, 2.4 us a chunk of 128 x 128 and 2.0 us of 64 x 64 on an SM (8 x 19 heads, N 1024, D 128:
-// 33 us; gradients of 2 x 16 heads, N 8192, D 128: 161 us).  There the tensor pipe is busy for 15 to 30 % of the time
-// and an SM's warps issue 1.3 to 1.7 instructions a cycle.
+// What bounds it: the chain of hand-overs from role to role, one block an SM: 2.3 to 2.4 us for a chunk and head of
+// 128 x 128 and 2.0 us of 64 x 64, with grouped queries (32 on 8 heads, N 65536, D 128: 252 us, 108 of them a block) as
+// with one head each.  The tensor pipe is busy for 15 to 30 % of the time, an SM's warps issue 1.3 to 1.7 instructions a
+// cycle, the memory gives 5.3 TB/s at most.  In copies of this kernel that leave out work (passes alone, us; gradients of
+// 2 x 16 heads, N 8192, D 128 | 4 x 16, N 4096, D 64 | 32/8, N 65536, D 128): as it is 125 | 43 | 252; without the
+// arithmetic of P 113 | 37 | 229, of the decayed X 121 | 41 | 244, of the decayed Y 123 | 43 | 238, of S 119 | 43 | 252;
+// without the output's stores 113 | 43 | 240; without all of these 90 | 31 | 180; without most MMAs as well 82 | 31 | 154.
 #include "la_decay.cuh"
 #include "la_tc_common.cuh"
 

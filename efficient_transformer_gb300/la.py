@@ -563,7 +563,12 @@ def decay_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torc
     ``initial_state`` (float32 [B, Hkv, D, Dv]) is S before the first token, ``final_state``
     receives S after the last; they may be the same tensor.  ``lengths`` (int32 [B]): tokens of
     each sequence; out rows past them are zeros and what the inputs hold there is not used.
-    Returns ``out`` [B, Hq, N, Dv]."""
+    Returns ``out`` [B, Hq, N, Dv].
+
+    float32 inputs are computed in float32.  bfloat16 ones run on the tensor cores where D and Dv are 64
+    or 128: sums and states in float32, the factors of the products (the state as q reads it among them)
+    rounded to bfloat16 once; ``out`` is then 3.1e-3 from exact (2-norm; its own rounding 1.7e-3),
+    ``final_state`` 4e-6 to 1e-5."""
     lib = load()
     B, Hq, Hkv, N, D, Dv = _check_qkv(q, k, v)
     _check_device(q, stream)

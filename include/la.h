@@ -293,8 +293,17 @@ la_status la_lowrank_bwd_t(const void *x, const void *U, const void *V, const vo
  * same formula.  scale: finite and not 0; for the gradient with a finite reciprocal too, and
  * grad_final_state / scale has to be within float32.
  *
+ * Arithmetic.  float32 inputs: float32 throughout.  bfloat16 inputs on the tensor cores
+ * (la_decay_kernel_path): float32 sums and states, but the factors of the products are rounded to
+ * bfloat16, once each: the decayed scores, q (k, grad_out) times its decay, the state as queries
+ * read it (initial_state and grad_final_state included), and the decayed k (q, v) that a
+ * state is summed from where the state itself is no output.  Outputs then are 3.1e-3 (2-norm)
+ * from the exact ones, where rounding them alone leaves 1.7e-3; states that go out, from two
+ * bfloat16 terms, 4e-6 to 1e-5.  For float32 arithmetic throughout give float32 inputs.
+ *
  * A NaN or infinity in a token's row reaches, besides the outputs that depend on it, at most
- * the other rows of the same 128-token chunk. */
+ * the other rows of the same 128-token chunk on the tensor cores (earlier ones among them: a weight of 0
+ * is multiplied there), none on the CUDA cores. */
 
 /* Bytes of workspace of la_decay_fwd (is_bwd = 0) or la_decay_bwd (is_bwd = 1, enough for the
  * forward too), with or without a state that goes out; 0 for arguments that they reject (and where
