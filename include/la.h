@@ -286,7 +286,8 @@ la_status la_lowrank_bwd_t(const void *x, const void *U, const void *V, const vo
  * pages have no counterpart of these entry points; layouts, grouped heads, dtypes, ownership,
  * streams and errors are la_fwd's: q, out [B, Hq, N, D | Dv], k, v [B, Hkv, N, D | Dv], D and Dv
  * in {32, 64, 128}, query head h reads key/value head h / n_rep; inputs may be strided
- * (la_strides, NULL: contiguous), outputs are contiguous.
+ * (la_strides, NULL: contiguous; 0 along a broadcast dimension), outputs are contiguous and overlap
+ * no input but for the states named below.
  *
  * log_decay [Hkv] is a float32 device vector, expected <= 0 (a non-finite -inf is gamma = 0:
  * each token sees itself alone); it gets no gradient.  Values above 0 grow the state by the
