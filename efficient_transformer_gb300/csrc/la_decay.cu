@@ -24,7 +24,6 @@ struct DecayPlan {
     la_path path;
     int seg_len, nseg;
     long long state_units;                      // sequences that the state kernel sums
-    bool sums_fin;                              // a state that goes out comes from the state kernel, not from the passes
     size_t state_bytes, part_bytes, ws_bytes;   // one array of segment states, one of their parts; all of them
 };
 
@@ -40,17 +39,16 @@ Parts sum_parts(long long units, int nsum, int chunks) {
     const int want = fit < 1 ? 1 : fit < chunks ? (int)fit : chunks;
     return parts_of(chunks, (chunks + want - 1) / want);
 }
-// The same where the sum over `heads` is an output: at most kDecayChain products in an accumulator, and where there
-// are more blocks than SMs the length whose waves end first, a block's start costing five products (10 x 16 heads, N 8192,
-// D 128, with the join: 222 us in whole sequences, 159 us in four parts each).
-Parts exact_parts(long long units, int nsum, int chunks, int heads, int Dv) {
-    const int chain = kDecayChain * decay_accumulators(Dv) / heads, most = chain < 1 ? 1 : chain < chunks ? chain : chunks;
+// The same where the sum over `heads` is an output: with more blocks than SMs the length whose waves end first, a
+// block's start (and, of more than one part, their join) costing five products.
+Parts exact_parts(long long units, int nsum, int chunks, int heads) {
     Parts best = sum_parts(units, nsum, chunks);
-    if (best.n > 1 && best.len <= most * kDecayTcChunk) return best;
+    if (nsum > 1 && best.n > 1) return best;   // (joined anyway)
     long long cost = -1;
-    for (int per = most; per >= 1 && per >= most / 16; --per) {
-        const Parts p = parts_of(chunks, per);
-        const long long c = (units * nsum * p.n + kPlanSms - 1) / kPlanSms * (5 + (long long)per * heads);
+    for (int n = 1; n <= 16 && n <= chunks; ++n) {
+        const Parts p = parts_of(chunks, (chunks + n - 1) / n);
+        const long long waves = (units * nsum * p.n + kPlanSms - 1) / kPlanSms;
+        const long long c = waves * (5 + (long long)(p.len / kDecayTcChunk) * heads) + (nsum == 1 && p.n > 1 ? 5 : 0);
         if (cost < 0 || c < cost) {
             cost = c;
             best = p;
@@ -154,14 +152,12 @@ DecayPlan make_plan(int B, int Hq, int Hkv, int N, int D, int Dv, la_dtype dt, b
     pl.nseg = (N + pl.seg_len - 1) / pl.seg_len;
     const int out_heads = bwd ? reps : 1;
     if (pl.nseg == 1) {
-        // one array is summed, where a state goes out
-        pl.sums_fin = pl.path == LA_PATH_TCGEN05 && (Dv == 128 || (long long)nchunks * out_heads > kDecayChain);
+        // a state that goes out, where its sum is in several parts
         pl.state_units = heads;
-        if (pl.sums_fin)
-            pl.ws_bytes = pl.part_bytes = (size_t)heads * exact_parts(heads, 1, nchunks, out_heads, Dv).n * D * Dv * 4;
+        const int n = pl.path == LA_PATH_TCGEN05 ? exact_parts(heads, 1, nchunks, out_heads).n : 1;
+        if (n > 1) pl.ws_bytes = pl.part_bytes = (size_t)heads * n * D * Dv * 4;
         return pl;
     }
-    pl.sums_fin = pl.path == LA_PATH_TCGEN05;
     pl.state_bytes = ((size_t)heads * pl.nseg * D * Dv * 4 + 255) / 256 * 256;
     if (pl.path == LA_PATH_SIMT) {
         pl.ws_bytes = pl.state_bytes * (bwd ? 2 : 1);
@@ -170,7 +166,7 @@ DecayPlan make_plan(int B, int Hq, int Hkv, int N, int D, int Dv, la_dtype dt, b
     // room for the parts of all segments (with a final state) and of all but the last
     pl.state_units = state_units;
     const int n0 = (pl.nseg - 1) * sum_parts(state_units, pl.nseg - 1, best_cps).n,
-              n1 = pl.nseg * exact_parts(state_units, pl.nseg, best_cps, out_heads, Dv).n;
+              n1 = pl.nseg * exact_parts(state_units, pl.nseg, best_cps, out_heads).n;
     pl.part_bytes = ((size_t)heads * (n0 > n1 ? n0 : n1) * D * Dv * 4 + 255) / 256 * 256;
     // forward: S; backward: S^T, A and A^T
     pl.ws_bytes = pl.state_bytes * (bwd ? 3 : 1) + pl.part_bytes * (bwd ? 2 : 1);
@@ -218,8 +214,8 @@ la_status run(bool bwd, const Given &a, int B, int Hq, int Hkv, int N, int D, in
         return LA_ERR_ARG;
     const DecayPlan pl = make_plan(B, Hq, Hkv, N, D, Dv, dt, bwd);
     const bool tc = pl.path == LA_PATH_TCGEN05, state_out = a.s_out || a.ds_out;
-    const bool sums = tc && (pl.nseg > 1 || (pl.sums_fin && state_out));   // the state kernel runs
-    if (tc ? sums : pl.ws_bytes > 0) {
+    const bool sums = tc && (pl.nseg > 1 || state_out);   // the state kernel runs
+    if (pl.ws_bytes > 0 && (pl.nseg > 1 || state_out)) {
         if (!ws || ws_bytes < pl.ws_bytes) return LA_ERR_WORKSPACE;
         if (!aligned(ws, 256)) return LA_ERR_ALIGN;
     }
@@ -243,14 +239,11 @@ la_status run(bool bwd, const Given &a, int B, int Hq, int Hkv, int N, int D, in
     sp.y[0] = a.k; sp.z[0] = a.v; sp.sy[0] = sk; sp.sz[0] = sv; sp.init[0] = a.s_in; sp.init_mul[0] = 1.f;
     sp.heads[0] = 1; sp.rev[0] = 0; sp.slots[0] = slots0; sp.exact[0] = a.s_out != nullptr;
     sp.n = 1;
-    // on the tensor cores a cut sequence's last state comes with the segments' sums, and so does one whose chain of
-    // products is long (kDecayChain); else with the pass itself
-    const bool main_fin = !pl.sums_fin;
     sp.fin[0] = a.s_out; sp.fin[1] = a.ds_out; sp.fin_mul[0] = 1.f; sp.fin_mul[1] = scale;
     sp.nsum = state_out ? pl.nseg : pl.nseg - 1;
     if (sums) {
         const int chunks = pl.seg_len / kDecayTcChunk;
-        const Parts parts = state_out ? exact_parts(pl.state_units, sp.nsum, chunks, bwd ? p.n_rep : 1, Dv)
+        const Parts parts = state_out ? exact_parts(pl.state_units, sp.nsum, chunks, bwd ? p.n_rep : 1)
                                       : sum_parts(pl.state_units, sp.nsum, chunks);
         sp.nsub = parts.n;
         sp.sub_len = parts.len;
@@ -261,7 +254,7 @@ la_status run(bool bwd, const Given &a, int B, int Hq, int Hkv, int N, int D, in
         sp.start[0] = slots0;
         DecayPass &f = p.pass[0];
         f.x = a.q; f.y = a.k; f.z = a.v; f.sx = sq; f.sy = sk; f.sz = sv; f.out = a.out;
-        f.slots = slots0; f.init = a.s_in; f.fin = main_fin ? a.s_out : nullptr; f.init_mul = f.fin_mul = 1.f;
+        f.slots = slots0; f.init = a.s_in; f.fin = tc ? nullptr : a.s_out; f.init_mul = f.fin_mul = 1.f;
         p.npass = 1;
     } else {
         // A = sum q g^T from the last token back
@@ -276,7 +269,7 @@ la_status run(bool bwd, const Given &a, int B, int Hq, int Hkv, int N, int D, in
         k.x = a.v; k.y = a.g; k.z = a.q; k.sx = sv; k.sy = sg; k.sz = sq; k.out = a.dk;
         k.slots = slots2; k.init = a.ds_in; k.tr = 1;
         v.x = a.k; v.y = a.q; v.z = a.g; v.sx = sk; v.sy = sq; v.sz = sg; v.out = a.dv;
-        v.slots = slots1; v.init = a.ds_in; v.fin = main_fin ? a.ds_out : nullptr;
+        v.slots = slots1; v.init = a.ds_in; v.fin = tc ? nullptr : a.ds_out;
         for (DecayPass *ps : {&k, &v}) {
             ps->many_yz = 1;
             ps->rev = 1;
@@ -297,11 +290,12 @@ la_status run(bool bwd, const Given &a, int B, int Hq, int Hkv, int N, int D, in
         if (sums && pl.nseg == 1) {
             // the sum of the array that goes out; after the pass, which reads the starting state that this may replace
             sp.start[0] = sp.start[1] = sp.start_tr[0] = sp.start_tr[1] = nullptr;
-            sp.part[0] = sp.part[1] = mem(0);
             sp.first = bwd;
             sp.n = 1;
+            sp.direct = sp.nsub == 1;
+            if (!sp.direct) sp.part[bwd] = mem(0);
             if (e == cudaSuccess) e = decay_tc_states(sp, s);
-            if (e == cudaSuccess) e = decay_tc_join(sp, s);
+            if (e == cudaSuccess && !sp.direct) e = decay_tc_join(sp, s);
         }
         return e == cudaSuccess ? LA_OK : cuda_fail(e);
     }

@@ -24,7 +24,7 @@ struct DecayPass {
                                 // [B Hkv][nseg] starting states of the segments, lane-blocked (decay_blocked) in the
                                 // pass's own orientation
     const float *init;          // nseg = 1: starting state [B Hkv][D][Dv] or null
-    float *fin;                 // state after the last token, or null
+    float *fin;                 // CUDA cores: state after the last token, or null
     int tr;                     // the pass's DX x DZ state is the transpose of the stored D x Dv one
     int many_yz;                // Hyz = n_rep Hkv heads of y and z for each head of x (summed into one
                                 // out); else Hx = n_rep Hkv heads of x for each head of y and z
@@ -65,6 +65,7 @@ struct DecayStateParams {
     int exact[2];               // a float32 state that the caller gets depends on these sums (tensor cores)
     float *fin[2];              // tensor cores: the state after the last segment, or null (its sum is taken
     float fin_mul[2];           // too then: nsum = nseg segments)
+    int direct;                 // tensor cores: one part in all, the state kernel writes fin itself
     int nsum;
     int first, n;               // state arrays of this launch: [first, first + n)
     int B, Hkv, N, D, Dv, seg_len, nseg;
@@ -99,11 +100,6 @@ cudaError_t decay_simt_passes(const DecayParams &p, int pass0, int npass, la_dty
 // Tensor-core kernels (la_decay_tc.cu): bfloat16, widths 64 and 128.  Segments are cut in token
 // order, multiples of kDecayTcChunk tokens; every pass of a call in one launch where the widths allow.
 constexpr int kDecayTcChunk = 128;
-// The MMA's sums are cut, not rounded, to float32 at each of their steps, so that a long chain of them drifts towards
-// zero: with two terms of y, 2.4e-7 of the sum a chunk and head.  Beside the 4e-6 that y's two terms leave, a
-// state that is an output has kDecayChain of them at most in an accumulator: 9e-6 in all, whatever the batch.
-constexpr int kDecayChain = 32;
-__host__ __device__ constexpr int decay_accumulators(int Dv) { return 512 / Dv; }   // of the state kernel
 cudaError_t decay_tc_states(const DecayStateParams &p, cudaStream_t s);
 cudaError_t decay_tc_join(const DecayStateParams &p, cudaStream_t s);
 cudaError_t decay_tc_passes(const DecayParams &p, cudaStream_t s);

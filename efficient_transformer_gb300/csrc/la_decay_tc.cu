@@ -1,22 +1,24 @@
 // la_decay_tc.cu -- decayed linear attention on the tensor cores (tcgen05 / TMEM / TMA), bfloat16.
 //
 // One block walks one segment of one key/value head in chunks of C = 128 tokens.  Per chunk (X, Y, Z:
-// see la_decay.cuh; W_ij = gamma^(i-j) for j <= i, else 0):
+// see la_decay.cuh; W_ij = gamma^(i-j) for j <= i, else 0; scale gamma^(i+1) = 2^(e_i) m_i with 1 <= |m_i| < 2):
 //   A  = X Y^T                                              [C x C]     scores
-//   P  = bf16(A o W)                                        (fp32 decay, one rounding)
-//   O  = P Z + bf16(gamma^(i+1) x_i) S_bf                   [C x DZ]
-//   S  = gamma^C S + (gamma^(C-1-j) y_j)^T Z                [DX x DZ]   fp32 in TMEM
-// Powers of gamma are only ever of whole distances >= 0, so no decay overflows.  The decayed Y^T is an
-// operand made from Y.  Where the state is an output (float32) it is split into two bf16 terms (hi + lo, 2^-17
-// relative) and both are multiplied; one rounding would leave 2^-9 there.  Where the state only reaches bf16
-// outputs it is rounded once, as P, S_bf and the decayed X are.
+//   P  = bf16(scale A_ij W_ij / m_i)                        (fp32 decay, one rounding)
+//   O  = P Z + (2^(e_i) x_i) (S_hi + S_lo)                  [C x DZ]    output row i: m_i O_i
+//   S  = gamma^C S + bf16(gamma^(C-1-j) y_j)^T Z            [DX x DZ]   fp32 in TMEM
+// Powers of gamma are only ever of whole distances >= 0, so no decay overflows.  Every term of an output is rounded
+// to bf16 once on its way, besides the output itself: in P, or as the decayed y.  The x of a row takes a power of two
+// only, which is exact (the rest of its decay waits for the float32 output, and P, rounded anyway, is made to fit), and S
+// is read as two bf16 terms (2^-17).  So outputs are within sqrt(2) of what rounding them alone leaves (2.4e-3 against
+// 1.7e-3 of the 2-norm); with x and S rounded once each they were at 3.1e-3 to 3.4e-3.  A state that goes out is not made
+// here but by the state kernel below, in three terms.
 //
 // Operands made by the CUDA cores are read by the MMA from TMEM where it has room: P and the decayed X take the place
 // of the scores (P over columns that its thread has read, the decayed X over the rest when P is done), Y^T has columns
 // of its own.  That halves the MMA's shared-memory reads, which at 128 x 128 x 16 from shared memory would
 // take all of its bandwidth, and leaves the shared memory to the TMA tiles.  The scores have two buffers, so that the
 // next item's scores and P run beside this one's O; where S and O are 128 columns wide that takes Y^T's place, and y is
-// decayed in its tile instead, in one term: there a state that is an output comes from the state kernel.
+// decayed in its tile instead.
 // Several heads of x share one chunk of y, z (grouped queries; S moves on after the last), or several heads
 // of y, z share one of x (their gradients; O and S sum over the heads).
 //
@@ -92,27 +94,29 @@ struct PassMaps {
     CUtensorMap m[3][4];   // per pass: x, y, z, out
 };
 
-// YSM: y is decayed in place in shared memory (else Y^T is made in TMEM, one or two terms).
+// YSM: y is decayed in place in shared memory (else Y^T is made in TMEM).
 template <int DX, int DZ>
 struct MainCfg {
     static constexpr bool YSM = DZ == 128;
     static constexpr int X_BYTES = C * DX * 2, Y_BYTES = C * DX * 2, Z_BYTES = C * DZ * 2, S_BYTES = DX * DZ * 2;
     static constexpr int O_BYTES = C * DZ * 2;
-    static constexpr int NX = DX == 64 ? 4 : 2;
+    // (an x tile is over when its scores are made and the row factors' X is in registers: one stage of them is enough
+    // beside 128-wide tiles of everything else)
+    static constexpr int NX = DX == 64 ? (DZ == 64 ? 4 : 3) : (DZ == 64 ? 2 : 1);
     static constexpr int NY = DX == 64 ? 3 : 2;
-    static constexpr int NZ = DZ == 64 ? 4 : DX == 64 ? 3 : 2;
+    static constexpr int NZ = DX == 64 ? (DZ == 64 ? 4 : 3) : (DZ == 64 ? 3 : 2);
     // output tiles: of their own; with YSM in the z tile that is used up or, where several heads share it, in place of
     // y's other stages (which such a block needs less: a y tile serves all of them)
     static constexpr int NO = YSM ? 0 : DX == 64 ? 2 : 1;
-    static constexpr int SMEM = NX * X_BYTES + NY * Y_BYTES + NZ * Z_BYTES + NO * O_BYTES + S_BYTES + 1024;
+    static constexpr int SMEM = NX * X_BYTES + NY * Y_BYTES + NZ * Z_BYTES + NO * O_BYTES + 2 * S_BYTES + 1024;
     static_assert(SMEM + 2048 <= kSmemLimit, "tiles, barriers and tables");
     static_assert(!YSM || (NY - 1) * Y_BYTES >= O_BYTES, "an output tile in y's other stages");
     // (S's MMA reads 128 columns from a y tile's start: with DX = 64 the next y stage or the first z tile)
     static_assert(DX == 128 || Z_BYTES >= C * 64 * 2, "128 columns from a y tile's start");
-    // TMEM: S, O, two buffers of scores, Y^T hi | lo
+    // TMEM: S, O, two buffers of scores, Y^T
     static constexpr int NSC = 2;
-    static constexpr int T_S = 0, T_O = DZ, T_A = 2 * DZ, T_YH = T_A + 128 * NSC, T_YL = T_YH + 64;
-    static_assert((YSM ? T_YH : T_YL + 64) <= 512, "TMEM columns");
+    static constexpr int T_S = 0, T_O = DZ, T_A = 2 * DZ, T_Y = T_A + 128 * NSC;
+    static_assert((YSM ? T_Y : T_Y + 64) <= 512, "TMEM columns");
 };
 
 // A block's part of the sequence: tokens [lo, hi).
@@ -158,6 +162,18 @@ __device__ __forceinline__ void fma2(float &x, float &y, float a, float b, float
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t u) { return *reinterpret_cast<__nv_bfloat162 *>(&u); }
 __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 h) { return *reinterpret_cast<uint32_t *>(&h); }
 
+// scale gamma^n of a row as 2^e and m (0 and 1 where it is nothing).
+struct RowFactor {
+    float p2, m;
+};
+__device__ __forceinline__ RowFactor row_factor(float f) {
+    const uint32_t b = __float_as_uint(f), e = b & 0x7f800000u;
+    RowFactor r;
+    r.p2 = __uint_as_float(e);
+    r.m = e ? __uint_as_float((b & 0x807fffffu) | 0x3f800000u) : 1.f;
+    return r;
+}
+
 // The decays w of a chunk's tokens, 16 groups of 8 of which a thread meets 2 in each group, as two bf16
 // terms.
 struct YtWeights {
@@ -173,12 +189,10 @@ struct YtWeights {
     }
 };
 
-// Decayed Y^T of one tile for the warp's 32 lanes d from d0: y w in bf16 into 64 columns at th and, with
-// `lo`, what that rounding left, into 64 at tl.  With w = wh + wl (bf16 each), hi = bf16(y wh), the remainder
-// y wh - hi is exact in bf16 (one fused multiply-add) and lo = bf16(remainder + y wl): three packed operations
-// a pair, 2^-17 relative in all.  (Alone, hi = bf16(y wh + bf16(y wl)).)  The tile's 8 x 8 blocks come
-// transposed out of shared memory in the layout of the store.
-__device__ __forceinline__ void yt_tile(const uint8_t *y, int d0, const YtWeights &w, bool lo, uint32_t th, uint32_t tl) {
+// Decayed Y^T of one tile for the warp's 32 lanes d from d0: y w in bf16 into 64 columns at th, with w = wh + wl (bf16
+// each) as bf16(y wh + bf16(y wl)).  The tile's 8 x 8 blocks come transposed out of shared memory in the layout of the
+// store.
+__device__ __forceinline__ void yt_tile(const uint8_t *y, int d0, const YtWeights &w, uint32_t th) {
     const int t = threadIdx.x % 32;
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {   // lanes d0 + 16 half ..
@@ -186,29 +200,32 @@ __device__ __forceinline__ void yt_tile(const uint8_t *y, int d0, const YtWeight
         const uint32_t lane = (uint32_t)(16 * half) << 16;
 #pragma unroll
         for (int jq = 0; jq < 4; ++jq) {     // tokens 32 jq ..
-            uint32_t v[8], h[8];
+            uint32_t v[8];
             ldmatrix_x4_trans(addr + jq * 32 * 128, v);
             ldmatrix_x4_trans(addr + (jq * 32 + 16) * 128, v + 4);
-            if (lo) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int g = jq * 4 + i / 2;   // group of 8 tokens
-                    const __nv_bfloat162 u = as_bf162(v[i]), wh = as_bf162(w.hi[g]), p = __hmul2(u, wh);
-                    h[i] = as_u32(p);
-                    v[i] = as_u32(__hfma2(u, as_bf162(w.lo[g]), __hfma2(u, wh, __hneg2(p))));
-                }
-                tmem_st_frag16(tl + lane + jq * 16, v);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int g = jq * 4 + i / 2;
-                    const __nv_bfloat162 u = as_bf162(v[i]);
-                    h[i] = as_u32(__hfma2(u, as_bf162(w.hi[g]), __hmul2(u, as_bf162(w.lo[g]))));
-                }
+            for (int i = 0; i < 8; ++i) {
+                const int g = jq * 4 + i / 2;   // group of 8 tokens
+                const __nv_bfloat162 u = as_bf162(v[i]);
+                v[i] = as_u32(__hfma2(u, as_bf162(w.hi[g]), __hmul2(u, as_bf162(w.lo[g]))));
             }
-            tmem_st_frag16(th + lane + jq * 16, h);
+            tmem_st_frag16(th + lane + jq * 16, v);
         }
     }
+}
+
+// 16 columns of row d of S as two bf16 terms, into two tiles of D rows.
+template <int D>
+__device__ __forceinline__ void store_state_terms(uint8_t *hi, uint8_t *lo, int d, const float *v, int c16) {
+    float r[16];
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+        const float2 h = unpack_bf16x2(pack_bf16x2(v[e], v[e + 1]));
+        r[e] = v[e] - h.x;
+        r[e + 1] = v[e + 1] - h.y;
+    }
+    store_state_row<D>(hi, d, v, c16);
+    store_state_row<D>(lo, d, r, c16);
 }
 
 // Zero rows [valid, C) of a C x W tile (what lies past a sequence's length must not meet an MMA or a weight of
@@ -239,7 +256,8 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
     uint8_t *ybuf = xbuf + NX * K::X_BYTES;
     uint8_t *zbuf = ybuf + NYS * K::Y_BYTES;
     uint8_t *sbf = zbuf + NZ * K::Z_BYTES;
-    uint8_t *obuf = YSM ? ybuf + K::Y_BYTES : sbf + K::S_BYTES;
+    uint8_t *slo = sbf + K::S_BYTES;
+    uint8_t *obuf = YSM ? ybuf + K::Y_BYTES : slo + K::S_BYTES;
 
     pdl_wait();
     const int warp = threadIdx.x / 32;
@@ -311,7 +329,11 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
     tc_fence_after();
     const uint32_t tm = tmem_base;
     const int items = nchunk * reps;
-    const bool exact = !YSM && ps.fin != nullptr;   // the state is an output
+    // scale gamma^n by which the state meets row i of chunk k
+    auto factor = [&](int k, int i) {
+        const int valid = min(C, part.hi - chunk0(k));
+        return row_factor(p.scale * pw[max((rev ? valid - i : i + 1) - (k == 0 ? off0 : 0), 0)]);
+    };
 
     if (warp == 0) {
         // ---------------- TMA producer
@@ -375,7 +397,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         // run in the order of their issue, so scores cannot overtake the P and X that they replace
         constexpr uint32_t idA = idesc_bf16(128, C, false, false);
         constexpr uint32_t idO = idesc_bf16(128, DZ, false, true);
-        const uint32_t tO = tm + K::T_O, sb = smem_u32(sbf);
+        const uint32_t tO = tm + K::T_O, sb = smem_u32(sbf), sl = smem_u32(slo);
         // of the next scores: x and y tile, buffer, item, chunk, head
         Ring sx, sy, sc;
         int si = 0, sk = 0, sr = 0;
@@ -436,7 +458,10 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                 if (first && !await(&s_conv, k & 1, &abort_flag)) break;
                 LA_TL(it, 5);
                 tc_fence_after();
-                if (elect_one()) mma_ts_mn<DX / 16>(tO, tA + 64, desc_mnmajor(sb, DX, 0, 0), idO, 1u);
+                if (elect_one()) {
+                    mma_ts_mn<DX / 16>(tO, tA + 64, desc_mnmajor(sl, DX, 0, 0), idO, 1u);
+                    mma_ts_mn<DX / 16>(tO, tA + 64, desc_mnmajor(sb, DX, 0, 0), idO, 1u);
+                }
                 __syncwarp();
             }
             if (elect_one()) {
@@ -480,11 +505,10 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             if (elect_one()) {
                 if constexpr (YSM) {
                     // (M = 128 rows d of which DX count: with 64 the others read what lies behind the tile)
-                    mma_ss_mn8(tS, desc_mnmajor(y, C, 0, 0), desc_mnmajor(z, C, 0, 0), idS);
+                    mma_ss_mn8(tS, desc_mnmajor(y, C, 0, 0), desc_mnmajor(z, C, 0, 0), idS, 1u);
                     mma_commit(&y_empty[ry.s]);
                 } else {
-                    mma_ts_mn<C / 16>(tS, tm + K::T_YH, desc_mnmajor(z, C, 0, 0), idS, 1u);
-                    if (exact) mma_ts_mn<C / 16>(tS, tm + K::T_YL, desc_mnmajor(z, C, 0, 0), idS, 1u);
+                    mma_ts_mn<C / 16>(tS, tm + K::T_Y, desc_mnmajor(z, C, 0, 0), idS, 1u);
                     mma_commit(&yt_done);
                 }
                 mma_commit(&z_empty[rz.s]);
@@ -508,7 +532,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         __syncwarp();
         warp_drain(&fin[1], 0);
     } else if (warp >= 4 && warp < 8) {
-        // ---------------- P = bf16(scale A o W), thread = row i, 32 columns at a time.  Away from the diagonal
+        // ---------------- P = bf16(scale A o W / m), thread = row i, 32 columns at a time.  Away from the diagonal
         // gamma^|i - j| = gamma^(distance to the near end of a block of 16) gamma^(distance in the block); on it the blocks
         // of 16 have the lower (reverse: upper) triangle of one pattern, or are such a full block, or nothing.  Both
         // patterns stay in registers, with `scale`
@@ -522,7 +546,8 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         }
         const bool low = lane < 16;
         Ring sc, rx, ry;
-        int r = 0, ot = 0;
+        int r = 0, ot = 0, k = 0;
+        float inv = 1.f;
 #pragma unroll 1
         for (int it = 0; it < items; ++it) {
             if (!await(&sc_full[sc.s], sc.p, &abort_flag)) break;
@@ -530,6 +555,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             if (i == 127) LA_TL(it, 7);
             const uint32_t ta = tm + K::T_A + sc.s * 128 + ((uint32_t)(wq * 32) << 16);
             const bool first = r == 0, last = ++r == reps;
+            if (first) inv = __fdividef(1.f, factor(k++, i).m);
             if (last || !many) {
                 mbar_arrive_w(&x_empty[rx.s]);
                 rx.next(NX);
@@ -553,8 +579,8 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                         const int j0 = cb * 32 + hb * 16;
                         const int near = rev ? j0 - i : i - j0 - 15;   // distance to the block's near end
                         const bool diag = cb == wq;
-                        const float full = !diag || (rev ? hb == 1 && low : hb == 0 && !low) ? pw[max(near, 0)] : 0.f;
-                        const float half = diag && low == (hb == 0) ? 1.f : 0.f;
+                        const float full = !diag || (rev ? hb == 1 && low : hb == 0 && !low) ? inv * pw[max(near, 0)] : 0.f;
+                        const float half = diag && low == (hb == 0) ? inv : 0.f;
 #pragma unroll
                         for (int e = 0; e < 16; e += 2) {
                             float a = g[e], b = g[e + 1];
@@ -581,7 +607,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             if (last) r = 0;
         }
     } else if (warp >= 8 && warp < 12) {
-        // ---------------- S: the operand S_bf of the state before the chunk, and its decay; thread = row d
+        // ---------------- S: the operands S_hi, S_lo of the state before the chunk, and its decay; thread = row d
         const int wq = warp % 4, d = wq * 32 + threadIdx.x % 32;
         const uint32_t ts = tm + K::T_S + ((uint32_t)(wq * 32) << 16);
         const bool have = wq * 32 < DX;
@@ -623,7 +649,6 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             }
         };
         // the powers of gamma that S takes before each chunk's Y^T Z; first the chunk that starts from memory
-        bool ok = true;
         const float g0 = nchunk > 0 ? pw[min(C, part.hi - chunk0(0)) - off0] : 1.f;
         const float g = pw[C], gl = pw[rev ? C : vlast];
         if (have) {
@@ -631,8 +656,8 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             for (int c32 = 0; c32 < DZ / 32; ++c32) {
                 float v[32];
                 start32(c32 * 32, v);
-                store_state_row<DX>(sbf, d, v, 2 * c32);
-                store_state_row<DX>(sbf, d, v + 16, 2 * c32 + 1);
+                store_state_terms<DX>(sbf, slo, d, v, 2 * c32);
+                store_state_terms<DX>(sbf, slo, d, v + 16, 2 * c32 + 1);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] *= g0;
                 tmem_st16(ts + c32 * 32, v);
@@ -643,15 +668,14 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
 #pragma unroll 1
         for (int k = 0; k < nchunk; ++k) {
             if (k > 0) {
-                ok = await(&s_full, (k - 1) & 1, &abort_flag);
-                if (!ok) break;
+                if (!await(&s_full, (k - 1) & 1, &abort_flag)) break;
                 tc_fence_after();
                 if (d == 0) LA_TL(k, 9);
                 const float gk = k == nchunk - 1 ? gl : g;
                 if (have) {
                     float va[16], vb[16];
                     auto part16 = [&](float *v, int c16) {
-                        store_state_row<DX>(sbf, d, v, c16);
+                        store_state_terms<DX>(sbf, slo, d, v, c16);
 #pragma unroll
                         for (int e = 0; e < 16; e += 2) mul2(v[e], v[e + 1], gk, gk);
                         tmem_st16(ts + c16 * 16, v);
@@ -674,49 +698,27 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             if (d == 0) LA_TL(k, 10);
             mbar_arrive_warp(&s_conv);
         }
-        if (!YSM && ok && ps.fin && u == p.nseg - 1) {
-            // what leaves a reverse pass decays once more; with no token at all it is what came in
-            const float mul = ps.fin_mul * (ps.first_off && n > 0 ? exp2f(l2 * ps.first_off) : 1.f);
-            if (nchunk > 0) {
-                ok = await(&s_full, (nchunk - 1) & 1, &abort_flag);
-                tc_fence_after();
-            }
-            float *f = ps.fin + (size_t)bg * E + d * sd;
-            if (ok && have)
-#pragma unroll 1
-                for (int c16 = 0; c16 < DZ / 16; ++c16) {
-                    float v[16];
-                    tmem_ld16(ts + c16 * 16, v);
-                    tmem_wait_regs<16>(v);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) f[(size_t)(c16 * 16 + e) * se] = v[e] * mul;
-                }
-        }
     } else if (warp >= 12 && warp < 16) {
         // ---------------- the decayed X, thread = row i: made in registers while P is under way, stored where the
-        // scores have been read.  scale x gamma^(i + 1) with the factor as two bf16 terms: one rounding
+        // scores have been read.  2^e x, exact
         const int wq = warp % 4, i = wq * 32 + threadIdx.x % 32;
         const int tiles = many ? nchunk : items, step = many ? reps : 1;   // output tiles; items of each
         Ring rx;
         int k = 0, r = 0;
 #pragma unroll 1
         for (int t = 0; t < tiles; ++t) {
-            const int valid = min(C, part.hi - chunk0(k));
             if (!await(&x_full[rx.s], rx.p, &abort_flag)) break;
             if (i == 0) LA_TL(t, 11);
             const uint8_t *x = xbuf + rx.s * K::X_BYTES;
-            const float g = p.scale * pw[max((rev ? valid - i : i + 1) - (k == 0 ? off0 : 0), 0)];
+            const float g = factor(k, i).p2;
             const __nv_bfloat162 gh = as_bf162(pack_bf16x2(g, g));
-            const float gr = g - unpack_bf16x2(as_u32(gh)).x;
-            const __nv_bfloat162 gl = as_bf162(pack_bf16x2(gr, gr));
             uint32_t w[DX / 2];
 #pragma unroll
             for (int c = 0; c < DX / 8; ++c) {
                 const uint4 v = *reinterpret_cast<const uint4 *>(x + swz_chunk(C, i, c));
                 const uint32_t a[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    w[4 * c + e] = as_u32(__hfma2(as_bf162(a[e]), gh, __hmul2(as_bf162(a[e]), gl)));
+                for (int e = 0; e < 4; ++e) w[4 * c + e] = as_u32(__hmul2(as_bf162(a[e]), gh));
             }
             mbar_arrive_w(&x_empty[rx.s]);   // the tile is free for the next load
             rx.next(NX);
@@ -746,6 +748,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         for (int t = 0; t < tiles; ++t) {
             const int c0 = chunk0(k), valid = min(C, part.hi - c0), zi = o_in_z ? (many ? (t + 1) * reps - 1 : t) % NZ : 0;
             uint8_t *o = o_in_z ? zbuf + zi * K::Z_BYTES : obuf + (NO > 1 ? t % NO : 0) * K::O_BYTES;
+            const float m = factor(k, i).m;
             if (!await(&o_full, t & 1, &abort_flag)) break;
             tc_fence_after();
             if (i == 0) LA_TL(t, 13);
@@ -764,7 +767,10 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                 }
                 uint32_t w[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+                for (int e = 0; e < 16; ++e) {
+                    mul2(v[2 * e], v[2 * e + 1], m, m);
+                    w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+                }
                 if (i >= valid) {   // past the length: zeros
 #pragma unroll
                     for (int e = 0; e < 16; ++e) w[e] = 0u;
@@ -848,7 +854,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                 if (t > 0 && !await(&yt_done, (t - 1) & 1, &abort_flag)) break;
                 tc_fence_after();
                 if (wq * 32 < DX) {
-                    yt_tile(y, wq * 32, w, exact, tm + K::T_YH + lane_off, tm + K::T_YL + lane_off);
+                    yt_tile(y, wq * 32, w, tm + K::T_Y + lane_off);
                     tmem_st_wait();
                 }
                 mbar_arrive_w(&y_empty[ry.s]);
@@ -882,12 +888,17 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
 }
 
 // ---------------------------------------------------------------------------------------
-// The sums over parts of segments (see DecayStateParams).  y is decayed to the part's end at once, so S in
-// TMEM only ever accumulates; in place in its tile, and where the state is exact with the rounding's remainder
-// in a tile of its own.  Warps: 0 TMA, 1 MMA, 4-11 y (two threads a token; 4-7 then write S).  Bound by memory where
-// the parts are long (8 heads, N 65536, 128 x 128: 57 us for 268 MB, 4.7 TB/s), else by its first chunk's latency (64
-// heads, N 4096, 64 x 64, parts of 8 chunks: 14 us).
-constexpr int kStateThreads = 384, kStateY = 256;
+// The sums over parts of segments (see DecayStateParams).  y is decayed to the part's end at once (y w, w <= 1).
+//   Sums that only bf16 outputs depend on: bf16(y w)^T Z, in place of y, all in one accumulator.
+//   A state that goes out: y w in float32 as three bf16 terms (2^-25), hi in place of y, mid and lo in tiles of
+// their own.  The MMA's sums are cut, not rounded, to float32 at every step, so that long chains of them drift (2e-7 a chunk and
+// head); each chunk and head has an accumulator of its own, smallest terms first, and eight warps add those up in
+// registers.  2 to 4e-7 of the state, whatever its length (in two terms and one accumulator 4e-6 to 7e-5).
+// Where a whole sequence is one part, these warps write the state itself (`direct`).
+// Warps: 0 TMA, 1 MMA, 4-11 y (two threads a token), 12-19 the sums.  Bound by memory where the parts are long (8
+// heads, N 65536, 128 x 128: TIME us for 268 MB), else by the first chunk's latency (64 heads, N 4096, 64 x 64, parts of 8
+// chunks: 14 us).
+constexpr int kStateThreads = 640, kStateY = 256, kStateSum = 256;
 
 struct StateMaps {
     CUtensorMap m[2][2];   // per array: y, z
@@ -896,14 +907,14 @@ struct StateMaps {
 template <int D, int DV>
 struct StateCfg {
     static constexpr int Y_BYTES = C * D * 2, STAGE = Y_BYTES + C * DV * 2;
-    // the MMA's M is 128 whatever D: what lies behind a y tile is its z tile; the remainder's tile, the last, has
-    // room for 128 columns of its own
-    static constexpr int LO_BYTES = C * 128 * 2;
-    static constexpr int FIT = (kSmemLimit - 1024 - 2048 - LO_BYTES) / STAGE, NS = FIT > 4 ? 4 : FIT;
-    static constexpr int SMEM = NS * STAGE + LO_BYTES + 1024;
+    // the MMA's M is 128 whatever D: what lies behind a y tile is its z tile, behind mid's tile lo's, and behind that one
+    // there is room for the rest of 128 columns
+    static constexpr int TERM_BYTES = Y_BYTES + C * 128 * 2;
+    static constexpr int FIT = (kSmemLimit - 1024 - 2048 - TERM_BYTES) / STAGE, NS = FIT > 4 ? 4 : FIT;
+    static constexpr int SMEM = NS * STAGE + TERM_BYTES + 1024;
     static_assert(D == 128 || STAGE - Y_BYTES >= C * 64 * 2, "128 columns from a y tile's start");
     static_assert(NS >= 2, "two stages");
-    static constexpr int NA = decay_accumulators(DV);
+    static constexpr int NA = 512 / DV;   // accumulators
 };
 
 template <int D, int DV>
@@ -912,10 +923,11 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
     using K = StateCfg<D, DV>;
     constexpr int NS = K::NS;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[NS], empty[NS], y_ready[NS], lo_free, zeroed, fin;
+    constexpr int NA = K::NA;
+    __shared__ uint64_t full[NS], empty[NS], y_ready[NS], acc_full[NA], acc_empty[NA], terms_free, zeroed, fin;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
-    uint8_t *stage = align1024(smem_raw), *lo_tile = stage + NS * K::STAGE;
+    uint8_t *stage = align1024(smem_raw), *mid_tile = stage + NS * K::STAGE, *lo_tile = mid_tile + K::Y_BYTES;
     pdl_wait();
     const int warp = threadIdx.x / 32;
     const int nparts = p.nsum * p.nsub, pidx = blockIdx.x % nparts, ah = blockIdx.x / nparts;
@@ -927,8 +939,6 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
     const float l2 = decay_log2(p.log_decay[h]);
     // chunks in the pass's order, the smallest powers first (small terms after large ones would be cut at their size)
     auto chunk0 = [&](int it) { return part.lo + C * (rev ? nchunk - 1 - it / heads : it / heads); };
-    float *dst = p.part[a] + ((size_t)bg * nparts + pidx) * D * DV;
-
     if (threadIdx.x == 0) {
         abort_flag = 0;
         for (int s = 0; s < NS; ++s) {
@@ -936,7 +946,11 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
             mbar_init(&empty[s], 1);
             mbar_init(&y_ready[s], kStateY);
         }
-        mbar_init(&lo_free, 1);
+        for (int s = 0; s < NA; ++s) {
+            mbar_init(&acc_full[s], 1);
+            mbar_init(&acc_empty[s], kStateSum);
+        }
+        mbar_init(&terms_free, 1);
         mbar_init(&zeroed, kStateY);
         mbar_init(&fin, 1);
         fence_barrier_init();
@@ -950,9 +964,6 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = tmem_base;
-    // a sum that is an output is made in several accumulators in turn, which meet at the end (kDecayChain)
-    const int na = exact ? K::NA : 1;
-
     if (warp == 0) {
         int issued = 0;
         for (int it = 0; it < items; ++it) {
@@ -972,72 +983,83 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
         for (int i = issued > NS ? issued - NS : 0; i < issued; ++i) warp_drain(&full[i % NS], (i / NS) & 1);
     } else if (warp == 1) {
         constexpr uint32_t id = idesc_bf16(128, DV, true, true);
-        // (M = 128 rows d of which D count: with 64 the others read what lies behind the tile; the accumulator
-        // starts at zero)
+        // (M = 128 rows d of which D count: with 64 the others read what lies behind the tile)
+        Ring st, ac;
         for (int it = 0; it < items; ++it) {
-            const int s = it % NS;
-            if (!await(&y_ready[s], (it / NS) & 1, &abort_flag)) break;
+            // (an accumulator's first use: the phase before the first counts as over)
+            if (exact && !await(&acc_empty[ac.s], ac.p ^ 1u, &abort_flag)) break;
+            if (!await(&y_ready[st.s], st.p, &abort_flag)) break;
             tc_fence_after();
-            const uint32_t y = smem_u32(stage + s * K::STAGE), z = y + K::Y_BYTES;
-            const uint32_t acc = tm + (exact ? it % K::NA : 0) * DV;
+            const uint32_t y = smem_u32(stage + st.s * K::STAGE), z = y + K::Y_BYTES, acc = tm + ac.s * DV;
             if (elect_one()) {
-                mma_ss_mn8(acc, desc_mnmajor(y, C, 0, 0), desc_mnmajor(z, C, 0, 0), id);
                 if (exact) {
-                    mma_ss_mn8(acc, desc_mnmajor(smem_u32(lo_tile), C, 0, 0), desc_mnmajor(z, C, 0, 0), id);
-                    mma_commit(&lo_free);
+                    mma_ss_mn8(acc, desc_mnmajor(smem_u32(lo_tile), C, 0, 0), desc_mnmajor(z, C, 0, 0), id, 0u);
+                    mma_ss_mn8(acc, desc_mnmajor(smem_u32(mid_tile), C, 0, 0), desc_mnmajor(z, C, 0, 0), id, 1u);
                 }
-                mma_commit(&empty[s]);
+                mma_ss_mn8(acc, desc_mnmajor(y, C, 0, 0), desc_mnmajor(z, C, 0, 0), id, exact || it > 0 ? 1u : 0u);
+                if (exact) mma_commit(&terms_free);
+                mma_commit(&empty[st.s]);
+                if (exact || it == items - 1) mma_commit(&acc_full[ac.s]);
             }
             __syncwarp();
+            st.next(NS);
+            if (exact) ac.next(NA);
         }
         if (elect_one()) mma_commit(&fin);
         __syncwarp();
         warp_drain(&fin, 0);
-    } else if (warp >= 4) {
-        const int i = threadIdx.x - 128, j = i % C, half = i / C, wq = warp % 4, d = wq * 32 + threadIdx.x % 32;
-        const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
-        if (warp < 8) {   // S = 0
-            const float z16[16] = {};
-            for (int c16 = 0; c16 < na * DV / 16; ++c16) tmem_st16(tm + lane_off + c16 * 16, z16);
-            tmem_st_wait();
-            tc_fence_before();
-        }
-        bool ok = true;
+    } else if (warp >= 4 && warp < 12) {
+        const int i = threadIdx.x - 128, j = i % C, half = i / C;
         for (int it = 0; it < items; ++it) {
             const int s = it % NS, c0 = chunk0(it), valid = min(C, part.hi - c0);
-            if (!(ok = await(&full[s], (it / NS) & 1, &abort_flag))) break;
+            if (!await(&full[s], (it / NS) & 1, &abort_flag)) break;
             uint8_t *y = stage + s * K::STAGE;
             if (p.lengths && valid < C) {
                 zero_rows<D>(y, valid, i, kStateY);
                 zero_rows<DV>(y + K::Y_BYTES, valid, i, kStateY);
                 mbar_arrive_warp(&zeroed);
-                if (!(ok = await(&zeroed, 0, &abort_flag))) break;
+                if (!await(&zeroed, 0, &abort_flag)) break;
             }
-            // what token j has ahead of it in the part, as two bf16 terms
+            // what token j has ahead of it in the part
             const float g = exp2f(l2 * max(rev ? c0 + j - part.lo : part.hi - 1 - c0 - j, 0));
-            const __nv_bfloat162 gh = as_bf162(pack_bf16x2(g, g));
-            const float gr = g - unpack_bf16x2(as_u32(gh)).x;
-            const __nv_bfloat162 gl = as_bf162(pack_bf16x2(gr, gr));
-            if (exact && it > 0 && !(ok = await(&lo_free, (it - 1) & 1, &abort_flag))) break;
+            if (exact) {
+                if (it > 0 && !await(&terms_free, (it - 1) & 1, &abort_flag)) break;
+#pragma unroll 2
+                for (int c = 0; c < D / 16; ++c) {
+                    const uint32_t at = swz_chunk(C, j, half * (D / 16) + c);
+                    const uint4 v = *reinterpret_cast<const uint4 *>(y + at);
+                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t h[4], m[4], l[4];
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-                const uint32_t at = swz_chunk(C, j, half * (D / 16) + c);
-                uint4 v = *reinterpret_cast<uint4 *>(y + at);
-                uint32_t x[4] = {v.x, v.y, v.z, v.w}, r[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const __nv_bfloat162 q = as_bf162(x[e]);
-                    if (exact) {
-                        // hi = bf16(y gh), the remainder y gh - hi exact in one multiply-add, lo = bf16(remainder + y gl)
-                        const __nv_bfloat162 hi = __hmul2(q, gh);
-                        r[e] = as_u32(__hfma2(q, gl, __hfma2(q, gh, __hneg2(hi))));
-                        x[e] = as_u32(hi);
-                    } else {
-                        x[e] = as_u32(__hfma2(q, gh, __hmul2(q, gl)));
+                    for (int e = 0; e < 4; ++e) {
+                        float2 f = unpack_bf16x2(x[e]);
+                        mul2(f.x, f.y, g, g);
+                        h[e] = pack_bf16x2(f.x, f.y);
+                        const float2 a = unpack_bf16x2(h[e]);
+                        f.x -= a.x;
+                        f.y -= a.y;
+                        m[e] = pack_bf16x2(f.x, f.y);
+                        const float2 b = unpack_bf16x2(m[e]);
+                        l[e] = pack_bf16x2(f.x - b.x, f.y - b.y);
                     }
+                    *reinterpret_cast<uint4 *>(y + at) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4 *>(mid_tile + at) = make_uint4(m[0], m[1], m[2], m[3]);
+                    *reinterpret_cast<uint4 *>(lo_tile + at) = make_uint4(l[0], l[1], l[2], l[3]);
                 }
-                *reinterpret_cast<uint4 *>(y + at) = make_uint4(x[0], x[1], x[2], x[3]);
-                if (exact) *reinterpret_cast<uint4 *>(lo_tile + at) = make_uint4(r[0], r[1], r[2], r[3]);
+            } else {
+                const __nv_bfloat162 gh = as_bf162(pack_bf16x2(g, g));
+                const float gr = g - unpack_bf16x2(as_u32(gh)).x;
+                const __nv_bfloat162 gl = as_bf162(pack_bf16x2(gr, gr));
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                    uint4 *q = reinterpret_cast<uint4 *>(y + swz_chunk(C, j, half * (D / 16) + c));
+                    uint4 v = *q;
+                    v.x = as_u32(__hfma2(as_bf162(v.x), gh, __hmul2(as_bf162(v.x), gl)));
+                    v.y = as_u32(__hfma2(as_bf162(v.y), gh, __hmul2(as_bf162(v.y), gl)));
+                    v.z = as_u32(__hfma2(as_bf162(v.z), gh, __hmul2(as_bf162(v.z), gl)));
+                    v.w = as_u32(__hfma2(as_bf162(v.w), gh, __hmul2(as_bf162(v.w), gl)));
+                    *q = v;
+                }
             }
             fence_proxy_async();
 #ifdef LA_TEST_HOOKS
@@ -1045,27 +1067,52 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
 #endif
                 mbar_arrive_warp(&y_ready[s]);
         }
-        if (warp < 8 && wq * 32 < D) {
-            if (ok && items > 0) ok = await(&fin, 0, &abort_flag);
+    } else if (warp >= 12) {
+        // thread = row d, half of the columns
+        constexpr int H = DV / 2;
+        const int wq = warp % 4, d = wq * 32 + threadIdx.x % 32, e0 = (warp - 12) / 4 * H;
+        const uint32_t ta = tm + ((uint32_t)(wq * 32) << 16) + e0;
+        const bool have = wq * 32 < D;
+        float S[H];
+#pragma unroll
+        for (int e = 0; e < H; ++e) S[e] = 0.f;
+        bool ok = true;
+        Ring ac;
+        for (int it = exact ? 0 : items - 1; it < items && it >= 0; ++it) {
+            if (!(ok = await(&acc_full[ac.s], ac.p, &abort_flag))) break;
             tc_fence_after();
-            if (ok)
-#pragma unroll 1
-                for (int c16 = 0; c16 < DV / 16; ++c16) {
+            if (have) {
+#pragma unroll
+                for (int c16 = 0; c16 < H / 16; ++c16) {
                     float v[16];
-                    tmem_ld16(tm + lane_off + c16 * 16, v);
+                    tmem_ld16(ta + ac.s * DV + c16 * 16, v);
                     tmem_wait_regs<16>(v);
-#pragma unroll 1
-                    for (int k = 1; k < na; ++k) {
-                        float x[16];
-                        tmem_ld16(tm + lane_off + k * DV + c16 * 16, x);
-                        tmem_wait_regs<16>(x);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] += x[e];
-                    }
-                    float4 *f = reinterpret_cast<float4 *>(dst + decay_blocked(D, d, c16 * 16));
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) f[e * D] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                    for (int e = 0; e < 16; ++e) S[c16 * 16 + e] += v[e];
                 }
+            }
+            tc_fence_before();
+            mbar_arrive_warp(&acc_empty[ac.s]);
+            ac.next(NA);
+        }
+        if (ok && have && p.direct) {
+            // the state after the last token (what leaves a reverse pass decays once more)
+            const int len = part.hi - part.lo, off = p.first_off[a];
+            const float g = p.init_mul[a] * exp2f(l2 * max(len - off, 0));
+            const float m = p.fin_mul[a] * (off && len > 0 ? exp2f(l2 * off) : 1.f);
+            const size_t at = ((size_t)bg * D + d) * DV + e0;
+#pragma unroll
+            for (int e = 0; e < H; e += 4) {
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (p.init[a]) x = *reinterpret_cast<const float4 *>(p.init[a] + at + e);
+                *reinterpret_cast<float4 *>(p.fin[a] + at + e) =
+                    make_float4(m * fmaf(g, x.x, S[e]), m * fmaf(g, x.y, S[e + 1]), m * fmaf(g, x.z, S[e + 2]),
+                                m * fmaf(g, x.w, S[e + 3]));
+            }
+        } else if (ok && have) {
+            float4 *f = reinterpret_cast<float4 *>(p.part[a] + ((size_t)bg * nparts + pidx) * D * DV + decay_blocked(D, d, e0));
+#pragma unroll
+            for (int e = 0; e < H / 4; ++e) f[e * D] = make_float4(S[4 * e], S[4 * e + 1], S[4 * e + 2], S[4 * e + 3]);
         }
     }
     tc_fence_before();
@@ -1076,7 +1123,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
 
 // ---------------------------------------------------------------------------------------
 // Starting states of the segments, and the last state where it is an output: T = the given state, then for each
-// segment T = gamma^tokens T + its sum, a thread carrying 4 x 4 elements; all states lane-blocked but the caller's.
+// segment (or part) T = gamma^tokens T + its sum, a thread carrying 4 x 4 elements; all states lane-blocked but the caller's.
 // A few microseconds of latency (4 to 9; eight parts loaded ahead instead of four do not shorten them).  Lane-blocked,
 // as a thread of the passes reads a whole row: from plain [D][Dv] states that took up to 50 us.
 constexpr int kJoinThreads = 64;

@@ -365,14 +365,16 @@ __device__ __forceinline__ void mma_ss_kk(uint32_t d_tmem, uint64_t a_desc, uint
 }
 #undef LA_SS_STEP
 
-// D += A B of two MN-major tiles (rows = K), 8 K steps.
-#define LA_MM_STEP(i)                                                            \
+// D (+)= A B of two MN-major tiles (rows = K), 8 K steps.
+#define LA_MM_STEP(i, pred)                                                      \
     "add.s64 da, %1, (" #i " * 128);\n\tadd.s64 db, %2, (" #i " * 128);\n\t"       \
-    "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, t;\n\t"
-__device__ __forceinline__ void mma_ss_mn8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
-    asm volatile("{\n\t.reg .pred t;\n\t.reg .b64 da, db;\n\tsetp.eq.u32 t, 0, 0;\n\t" LA_MM_STEP(0) LA_MM_STEP(1)
-                     LA_MM_STEP(2) LA_MM_STEP(3) LA_MM_STEP(4) LA_MM_STEP(5) LA_MM_STEP(6) LA_MM_STEP(7) "}" ::"r"(d_tmem),
-                 "l"(a_desc), "l"(b_desc), "r"(idesc)
+    "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, " pred ";\n\t"
+__device__ __forceinline__ void mma_ss_mn8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p, t;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t" LA_MM_STEP(
+                     0, "p") LA_MM_STEP(1, "t") LA_MM_STEP(2, "t") LA_MM_STEP(3, "t") LA_MM_STEP(4, "t") LA_MM_STEP(5, "t")
+                     LA_MM_STEP(6, "t") LA_MM_STEP(7, "t") "}" ::"r"(d_tmem),
+                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
                  : "memory");
 }
 #undef LA_MM_STEP
