@@ -22,7 +22,7 @@
 // Several heads of x share one chunk of y, z (grouped queries; S moves on after the last), or several heads
 // of y, z share one of x (their gradients; O and S sum over the heads).
 //
-// Warps: 0 TMA, 1 MMA of scores and O, 2 MMA of S, 4-7 P, 8-11 S -> S_bf and the decay of S, 12-15 the decayed X,
+// Warps: 0 TMA of x, 3 of y and z, 1 MMA of scores and O, 2 MMA of S, 4-7 P, 8-11 S -> S_bf and the decay of S, 12-15 the decayed X,
 // 16-19 the output rows, 20-23 the decayed y (and the zeros past a sequence's length).
 //
 // The reverse passes (gradients of k and v) take the same steps with j >= i and gamma^(j-i), chunks from the
@@ -100,15 +100,18 @@ struct MainCfg {
     static constexpr bool YSM = DZ == 128;
     static constexpr int X_BYTES = C * DX * 2, Y_BYTES = C * DX * 2, Z_BYTES = C * DZ * 2, S_BYTES = DX * DZ * 2;
     static constexpr int O_BYTES = C * DZ * 2;
-    // (an x tile is over when its scores are made and the row factors' X is in registers: one stage of them is enough
-    // beside 128-wide tiles of everything else)
-    static constexpr int NX = DX == 64 ? (DZ == 64 ? 4 : 3) : (DZ == 64 ? 2 : 1);
+    // At 128 x 128 there is room for five tiles beside S: with several heads of x to one y, z (those are loaded once a
+    // chunk) x has two stages, y one, z one and the output one; else x one (it is over when its scores are made and the row
+    // factors' X is in registers), y and z two.
+    static constexpr bool TIGHT = DX == 128 && DZ == 128;
+    static constexpr int NX = DX == 64 ? (DZ == 64 ? 4 : 3) : 2;
     static constexpr int NY = DX == 64 ? 3 : 2;
     static constexpr int NZ = DX == 64 ? (DZ == 64 ? 4 : 3) : (DZ == 64 ? 3 : 2);
     // output tiles: of their own; with YSM in the z tile that is used up or, where several heads share it, in place of
     // y's other stages (which such a block needs less: a y tile serves all of them)
     static constexpr int NO = YSM ? 0 : DX == 64 ? 2 : 1;
-    static constexpr int SMEM = NX * X_BYTES + NY * Y_BYTES + NZ * Z_BYTES + NO * O_BYTES + 2 * S_BYTES + 1024;
+    static constexpr int TILES = TIGHT ? 5 * X_BYTES : NX * X_BYTES + NY * Y_BYTES + NZ * Z_BYTES + NO * O_BYTES;
+    static constexpr int SMEM = TILES + 2 * S_BYTES + 1024;
     static_assert(SMEM + 2048 <= kSmemLimit, "tiles, barriers and tables");
     static_assert(!YSM || (NY - 1) * Y_BYTES >= O_BYTES, "an output tile in y's other stages");
     // (S's MMA reads 128 columns from a y tile's start: with DX = 64 the next y stage or the first z tile)
@@ -242,9 +245,9 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
                                                               int npass) {
     using K = MainCfg<DX, DZ>;
     constexpr bool YSM = K::YSM;
-    constexpr int NX = K::NX, NYS = K::NY, NZ = K::NZ, NSC = K::NSC, NO = K::NO;
+    constexpr int NXS = K::NX, NYS = K::NY, NZS = K::NZ, NSC = K::NSC, NO = K::NO;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t x_full[NX], x_empty[NX], y_full[NYS], y_empty[NYS], z_full[NZ], z_empty[NZ];
+    __shared__ uint64_t x_full[NXS], x_empty[NXS], y_full[NYS], y_empty[NYS], z_full[NZS], z_empty[NZS];
     // of one buffer of the scores: in, P made; by output tile: P of its first scores made, decayed X made
     __shared__ uint64_t sc_full[NSC], p_ready[NSC], p_first[2], xd_ready[2];
     __shared__ uint64_t y_scored[NYS], yt_ready[NYS];   // of a stage of y: its scores done, its decayed form made
@@ -253,20 +256,14 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
     uint8_t *xbuf = align1024(smem_raw);
-    uint8_t *ybuf = xbuf + NX * K::X_BYTES;
-    uint8_t *zbuf = ybuf + NYS * K::Y_BYTES;
-    uint8_t *sbf = zbuf + NZ * K::Z_BYTES;
-    uint8_t *slo = sbf + K::S_BYTES;
-    uint8_t *obuf = YSM ? ybuf + K::Y_BYTES : slo + K::S_BYTES;
-
     pdl_wait();
     const int warp = threadIdx.x / 32;
     const int pi = pass0 + blockIdx.x % npass, rest = blockIdx.x / npass;
     if (threadIdx.x == 0) {
         abort_flag = 0;
-        for (int s = 0; s < NX; ++s) {
+        for (int s = 0; s < NXS; ++s) {
             mbar_init(&x_full[s], 1);
-            mbar_init(&x_empty[s], 4 + 4);             // warps of P (the scores are over), of the decayed X
+            mbar_init(&x_empty[s], 1 + 4);             // its scores' MMA, warps of the decayed X
         }
         for (int s = 0; s < NYS; ++s) {
             mbar_init(&y_full[s], 1);
@@ -274,7 +271,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             mbar_init(&y_scored[s], 1);
             mbar_init(&yt_ready[s], 128);
         }
-        for (int s = 0; s < NZ; ++s) {
+        for (int s = 0; s < NZS; ++s) {
             mbar_init(&z_full[s], 1);
             mbar_init(&z_empty[s], YSM ? 2 + 4 : 2);   // both MMA warps (and the warps that store the output)
         }
@@ -308,8 +305,13 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
     const int n = decay_tokens(p.lengths, b, p.N), rev = ps.rev, many = ps.many_yz, reps = p.n_rep;
     // (the last segment in token order may be a short one: those blocks come last)
     const int u = rev ? p.nseg - 1 - rest / heads : rest / heads;
-    const int NY = YSM && !many && reps > 1 ? 1 : NYS;        // stages of y in use
-    const bool o_in_z = YSM && (many || reps == 1);           // output tiles are staged in z's
+    // stages in use; with YSM output tiles are staged in z's, or (shared y and z) in place of y's second
+    const bool shared = !many && reps > 1, o_in_z = YSM && !shared;
+    const int NX = K::TIGHT && !shared ? 1 : NXS, NY = YSM && shared ? 1 : NYS, NZ = K::TIGHT && shared ? 1 : NZS;
+    uint8_t *ybuf = xbuf + NX * K::X_BYTES;
+    uint8_t *zbuf = ybuf + NYS * K::Y_BYTES;
+    uint8_t *sbf = xbuf + K::TILES, *slo = sbf + K::S_BYTES;
+    uint8_t *obuf = YSM ? ybuf + K::Y_BYTES : zbuf + NZS * K::Z_BYTES;
     const Part part = part_of(n, p.N, u, p.nseg, p.seg_len, rev);
     const int nchunk = (part.hi - part.lo + C - 1) / C;
     const int off0 = u == 0 ? ps.first_off : 0;   // of the first chunk
@@ -336,59 +338,65 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
     };
 
     if (warp == 0) {
-        // ---------------- TMA producer
-        const CUtensorMap *mx = &maps.m[pi][0], *my = &maps.m[pi][1], *mz = &maps.m[pi][2];
-        Ring rx, ry, rz;
-        int nx = 0, ny = 0, nz = 0;   // issued
-        bool ok = true;
-        int k = 0, r = 0;
+        // ---------------- TMA loads of x
+        const CUtensorMap *mx = &maps.m[pi][0];
+        const int tiles = many ? nchunk : items;
+        Ring rx;
+        int n = 0, k = 0, r = 0;   // n issued
 #pragma unroll 1
-        for (int it = 0; it < items; ++it) {
-            const int c0 = chunk0(k), hq = h * reps + r, hyz = many ? hq : h;
-            if (r == 0 || !many) {
-                // (the first use of a stage: the phase before the first counts as over)
-                if (!(ok = await(&x_empty[rx.s], rx.p ^ 1u, &abort_flag))) break;
-                if (elect_one()) {
-                    uint8_t *x = xbuf + rx.s * K::X_BYTES;
-                    mbar_arrive_expect_tx(&x_full[rx.s], K::X_BYTES);
+        for (; n < tiles; ++n) {
+            // (the first use of a stage: the phase before the first counts as over)
+            if (!await(&x_empty[rx.s], rx.p ^ 1u, &abort_flag)) break;
+            if (elect_one()) {
+                uint8_t *x = xbuf + rx.s * K::X_BYTES;
+                mbar_arrive_expect_tx(&x_full[rx.s], K::X_BYTES);
 #pragma unroll
-                    for (int blk = 0; blk < DX / 64; ++blk)
-                        tma_load_4d(x + blk * C * 128, mx, &x_full[rx.s], blk * 64, c0, many ? h : hq, b);
-                }
-                __syncwarp();
-                rx.next(NX);
-                ++nx;
+                for (int blk = 0; blk < DX / 64; ++blk)
+                    tma_load_4d(x + blk * C * 128, mx, &x_full[rx.s], blk * 64, chunk0(k), many ? h : h * reps + r, b);
             }
-            if (r == 0 || many) {
-                if (!(ok = await(&y_empty[ry.s], ry.p ^ 1u, &abort_flag))) break;
-                if (elect_one()) {
-                    uint8_t *y = ybuf + ry.s * K::Y_BYTES;
-                    mbar_arrive_expect_tx(&y_full[ry.s], K::Y_BYTES);
-#pragma unroll
-                    for (int blk = 0; blk < DX / 64; ++blk)
-                        tma_load_4d(y + blk * C * 128, my, &y_full[ry.s], blk * 64, c0, hyz, b);
-                }
-                __syncwarp();
-                ry.next(NY);
-                ++ny;
-                if (!(ok = await(&z_empty[rz.s], rz.p ^ 1u, &abort_flag))) break;
-                if (elect_one()) {
-                    uint8_t *z = zbuf + rz.s * K::Z_BYTES;
-                    mbar_arrive_expect_tx(&z_full[rz.s], K::Z_BYTES);
-#pragma unroll
-                    for (int blk = 0; blk < DZ / 64; ++blk)
-                        tma_load_4d(z + blk * C * 128, mz, &z_full[rz.s], blk * 64, c0, hyz, b);
-                }
-                __syncwarp();
-                rz.next(NZ);
-                ++nz;
-            }
-            if (++r == reps) {
+            __syncwarp();
+            rx.next(NX);
+            if (many || ++r == reps) {
                 r = 0;
                 ++k;
             }
         }
-        for (int i = nx > NX ? nx - NX : 0; i < nx; ++i) warp_drain(&x_full[i % NX], (i / NX) & 1);
+        for (int i = n > NX ? n - NX : 0; i < n; ++i) warp_drain(&x_full[i % NX], (i / NX) & 1);
+    } else if (warp == 3) {
+        // ---------------- TMA loads of y and z
+        const CUtensorMap *my = &maps.m[pi][1], *mz = &maps.m[pi][2];
+        const int tiles = many ? items : nchunk;
+        Ring ry, rz;
+        int ny = 0, nz = 0, k = 0, r = 0;   // issued
+#pragma unroll 1
+        for (; ny < tiles; ++nz) {
+            const int c0 = chunk0(k), hyz = many ? h * reps + r : h;
+            if (!await(&y_empty[ry.s], ry.p ^ 1u, &abort_flag)) break;
+            if (elect_one()) {
+                uint8_t *y = ybuf + ry.s * K::Y_BYTES;
+                mbar_arrive_expect_tx(&y_full[ry.s], K::Y_BYTES);
+#pragma unroll
+                for (int blk = 0; blk < DX / 64; ++blk)
+                    tma_load_4d(y + blk * C * 128, my, &y_full[ry.s], blk * 64, c0, hyz, b);
+            }
+            __syncwarp();
+            ry.next(NY);
+            ++ny;
+            if (!await(&z_empty[rz.s], rz.p ^ 1u, &abort_flag)) break;
+            if (elect_one()) {
+                uint8_t *z = zbuf + rz.s * K::Z_BYTES;
+                mbar_arrive_expect_tx(&z_full[rz.s], K::Z_BYTES);
+#pragma unroll
+                for (int blk = 0; blk < DZ / 64; ++blk)
+                    tma_load_4d(z + blk * C * 128, mz, &z_full[rz.s], blk * 64, c0, hyz, b);
+            }
+            __syncwarp();
+            rz.next(NZ);
+            if (!many || ++r == reps) {
+                r = 0;
+                ++k;
+            }
+        }
         for (int i = ny > NY ? ny - NY : 0; i < ny; ++i) warp_drain(&y_full[i % NY], (i / NY) & 1);
         for (int i = nz > NZ ? nz - NZ : 0; i < nz; ++i) warp_drain(&z_full[i % NZ], (i / NZ) & 1);
     } else if (warp == 1) {
@@ -410,16 +418,18 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         uint32_t idle = 0;
 #pragma unroll 1
         while (it < items) {
-            if (si < items && si < it + NSC && is_over(&x_full[sx.s], sx.p) && is_over(&y_full[sy.s], sy.p)) {
-                const bool first = sr == 0, last = sr == reps - 1;
-                // a tile with rows past the sequence's length (its last): those are zeroed first
-                if (p.lengths && first && sk == nchunk - 1 && vlast < C && !await(&zeroed, 0, &abort_flag)) break;
+            // (a tile with rows past the sequence's length, its last: those are zeroed first)
+            const bool ragged = p.lengths && sk == nchunk - 1 && vlast < C;
+            if (si < items && si < it + NSC && is_over(&x_full[sx.s], sx.p) && is_over(&y_full[sy.s], sy.p) &&
+                (!ragged || is_over(&zeroed, 0))) {
+                const bool last = sr == reps - 1;
                 const uint32_t x = smem_u32(xbuf + sx.s * K::X_BYTES), y = smem_u32(ybuf + sy.s * K::Y_BYTES);
                 tc_fence_after();
                 LA_TL(si, 0);
                 if (elect_one()) {
                     mma_ss_kk<DX / 16>(tm + K::T_A + sc.s * 128, desc_kmajor(x, C, 0, 0), desc_kmajor(y, C, 0, 0), idA);
                     mma_commit(&sc_full[sc.s]);
+                    if (last || !many) mma_commit(&x_empty[sx.s]);
                     if (YSM && (last || many)) mma_commit(&y_scored[sy.s]);
                 }
                 __syncwarp();
@@ -446,27 +456,27 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             const bool first = r == 0, last = r == reps - 1;
             const bool opens = first || !many, ends = last || !many;   // an output tile
             LA_TL(it, 4);
-            if (!await(&z_full[iz.s], iz.p, &abort_flag)) break;
-            if (opens && !await(&o_free, op, &abort_flag)) break;   // (the first: the phase before it counts as over)
-            LA_TL(it, 2);
             const uint32_t z = smem_u32(zbuf + iz.s * K::Z_BYTES), tA = tm + K::T_A + ic.s * 128;
-            tc_fence_after();
-            if (elect_one()) mma_ts_mn<C / 16>(tO, tA, desc_mnmajor(z, C, 0, 0), idO, opens ? 0u : 1u);
-            __syncwarp();
             if (opens) {
+                // the state's part first: S moves on (in its own role) while P Z is under way
+                if (!await(&o_free, op, &abort_flag)) break;   // (the first: the phase before it counts as over)
                 if (!await(&xd_ready[it2.s], it2.p, &abort_flag)) break;
                 if (first && !await(&s_conv, k & 1, &abort_flag)) break;
                 LA_TL(it, 5);
                 tc_fence_after();
                 if (elect_one()) {
-                    mma_ts_mn<DX / 16>(tO, tA + 64, desc_mnmajor(sl, DX, 0, 0), idO, 1u);
+                    mma_ts_mn<DX / 16>(tO, tA + 64, desc_mnmajor(sl, DX, 0, 0), idO, 0u);
                     mma_ts_mn<DX / 16>(tO, tA + 64, desc_mnmajor(sb, DX, 0, 0), idO, 1u);
+                    if (many ? first : last) mma_commit(&s_full);   // the chunk's last reader of S_hi, S_lo
                 }
                 __syncwarp();
             }
+            if (!await(&z_full[iz.s], iz.p, &abort_flag)) break;
+            LA_TL(it, 2);
+            tc_fence_after();
             if (elect_one()) {
+                mma_ts_mn<C / 16>(tO, tA, desc_mnmajor(z, C, 0, 0), idO, 1u);
                 if (ends) mma_commit(&o_full);
-                if (many ? first : last) mma_commit(&s_full);   // the chunk's last reader of S_bf
                 if (last || many) mma_commit(&z_empty[iz.s]);
             }
             __syncwarp();
@@ -545,7 +555,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             tri[e] = ago >= 0 ? p.scale * pw[max(ago, 0)] : 0.f;
         }
         const bool low = lane < 16;
-        Ring sc, rx, ry;
+        Ring sc, ry;
         int r = 0, ot = 0, k = 0;
         float inv = 1.f;
 #pragma unroll 1
@@ -556,10 +566,6 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             const uint32_t ta = tm + K::T_A + sc.s * 128 + ((uint32_t)(wq * 32) << 16);
             const bool first = r == 0, last = ++r == reps;
             if (first) inv = __fdividef(1.f, factor(k++, i).m);
-            if (last || !many) {
-                mbar_arrive_w(&x_empty[rx.s]);
-                rx.next(NX);
-            }
             if (!YSM && (last || many)) {
                 mbar_arrive_w(&y_empty[ry.s]);
                 ry.next(NY);
@@ -995,9 +1001,9 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
                 if (exact) {
                     mma_ss_mn8(acc, desc_mnmajor(smem_u32(lo_tile), C, 0, 0), desc_mnmajor(z, C, 0, 0), id, 0u);
                     mma_ss_mn8(acc, desc_mnmajor(smem_u32(mid_tile), C, 0, 0), desc_mnmajor(z, C, 0, 0), id, 1u);
+                    mma_commit(&terms_free);
                 }
                 mma_ss_mn8(acc, desc_mnmajor(y, C, 0, 0), desc_mnmajor(z, C, 0, 0), id, exact || it > 0 ? 1u : 0u);
-                if (exact) mma_commit(&terms_free);
                 mma_commit(&empty[st.s]);
                 if (exact || it == items - 1) mma_commit(&acc_full[ac.s]);
             }
@@ -1023,28 +1029,34 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
             // what token j has ahead of it in the part
             const float g = exp2f(l2 * max(rev ? c0 + j - part.lo : part.hi - 1 - c0 - j, 0));
             if (exact) {
-                if (it > 0 && !await(&terms_free, (it - 1) & 1, &abort_flag)) break;
-#pragma unroll 2
+                // (the terms are found beside the MMAs of the item before)
+                uint32_t m[D / 16][4], l[D / 16][4];
+#pragma unroll
                 for (int c = 0; c < D / 16; ++c) {
-                    const uint32_t at = swz_chunk(C, j, half * (D / 16) + c);
-                    const uint4 v = *reinterpret_cast<const uint4 *>(y + at);
+                    uint4 *q = reinterpret_cast<uint4 *>(y + swz_chunk(C, j, half * (D / 16) + c));
+                    const uint4 v = *q;
                     const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t h[4], m[4], l[4];
+                    uint32_t h[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         float2 f = unpack_bf16x2(x[e]);
                         mul2(f.x, f.y, g, g);
                         h[e] = pack_bf16x2(f.x, f.y);
-                        const float2 a = unpack_bf16x2(h[e]);
-                        f.x -= a.x;
-                        f.y -= a.y;
-                        m[e] = pack_bf16x2(f.x, f.y);
-                        const float2 b = unpack_bf16x2(m[e]);
-                        l[e] = pack_bf16x2(f.x - b.x, f.y - b.y);
+                        const float2 hf = unpack_bf16x2(h[e]);
+                        f.x -= hf.x;
+                        f.y -= hf.y;
+                        m[c][e] = pack_bf16x2(f.x, f.y);
+                        const float2 mf = unpack_bf16x2(m[c][e]);
+                        l[c][e] = pack_bf16x2(f.x - mf.x, f.y - mf.y);
                     }
-                    *reinterpret_cast<uint4 *>(y + at) = make_uint4(h[0], h[1], h[2], h[3]);
-                    *reinterpret_cast<uint4 *>(mid_tile + at) = make_uint4(m[0], m[1], m[2], m[3]);
-                    *reinterpret_cast<uint4 *>(lo_tile + at) = make_uint4(l[0], l[1], l[2], l[3]);
+                    *q = make_uint4(h[0], h[1], h[2], h[3]);
+                }
+                if (it > 0 && !await(&terms_free, (it - 1) & 1, &abort_flag)) break;
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                    const uint32_t at = swz_chunk(C, j, half * (D / 16) + c);
+                    *reinterpret_cast<uint4 *>(mid_tile + at) = make_uint4(m[c][0], m[c][1], m[c][2], m[c][3]);
+                    *reinterpret_cast<uint4 *>(lo_tile + at) = make_uint4(l[c][0], l[c][1], l[c][2], l[c][3]);
                 }
             } else {
                 const __nv_bfloat162 gh = as_bf162(pack_bf16x2(g, g));
