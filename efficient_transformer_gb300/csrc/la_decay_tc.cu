@@ -331,7 +331,8 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
     tc_fence_after();
     const uint32_t tm = tmem_base;
     const int items = nchunk * reps;
-    // scale gamma^n by which the state meets row i of chunk k
+    // scale gamma^n by which the state meets row i of chunk k (the first chunk of a reverse pass may be the short one and
+    // has an offset; all others, and all of a forward pass, have the same)
     auto factor = [&](int k, int i) {
         const int valid = min(C, part.hi - chunk0(k));
         return row_factor(p.scale * pw[max((rev ? valid - i : i + 1) - (k == 0 ? off0 : 0), 0)]);
@@ -556,8 +557,8 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         }
         const bool low = lane < 16;
         Ring sc, ry;
-        int r = 0, ot = 0, k = 0;
-        float inv = 1.f;
+        int r = 0, ot = 0;
+        float inv = __fdividef(1.f, factor(0, i).m);
 #pragma unroll 1
         for (int it = 0; it < items; ++it) {
             if (!await(&sc_full[sc.s], sc.p, &abort_flag)) break;
@@ -565,7 +566,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             if (i == 127) LA_TL(it, 7);
             const uint32_t ta = tm + K::T_A + sc.s * 128 + ((uint32_t)(wq * 32) << 16);
             const bool first = r == 0, last = ++r == reps;
-            if (first) inv = __fdividef(1.f, factor(k++, i).m);
+            if (it == reps && rev) inv = __fdividef(1.f, factor(1, i).m);
             if (!YSM && (last || many)) {
                 mbar_arrive_w(&y_empty[ry.s]);
                 ry.next(NY);
@@ -709,6 +710,11 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         // scores have been read.  2^e x, exact
         const int wq = warp % 4, i = wq * 32 + threadIdx.x % 32;
         const int tiles = many ? nchunk : items, step = many ? reps : 1;   // output tiles; items of each
+        auto power = [&](int k) {
+            const float g = factor(k, i).p2;
+            return as_bf162(pack_bf16x2(g, g));
+        };
+        __nv_bfloat162 gh = power(0);
         Ring rx;
         int k = 0, r = 0;
 #pragma unroll 1
@@ -716,8 +722,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
             if (!await(&x_full[rx.s], rx.p, &abort_flag)) break;
             if (i == 0) LA_TL(t, 11);
             const uint8_t *x = xbuf + rx.s * K::X_BYTES;
-            const float g = factor(k, i).p2;
-            const __nv_bfloat162 gh = as_bf162(pack_bf16x2(g, g));
+            if (rev && k == 1) gh = power(1);
             uint32_t w[DX / 2];
 #pragma unroll
             for (int c = 0; c < DX / 8; ++c) {
@@ -749,12 +754,13 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
         const uint32_t to = tm + K::T_O + ((uint32_t)(wq * 32) << 16);
         const int tiles = many ? nchunk : items;
         const CUtensorMap *mo = &maps.m[pi][3];
+        float m = factor(0, i).m;
         int k = 0, r = 0;
 #pragma unroll 1
         for (int t = 0; t < tiles; ++t) {
             const int c0 = chunk0(k), valid = min(C, part.hi - c0), zi = o_in_z ? (many ? (t + 1) * reps - 1 : t) % NZ : 0;
             uint8_t *o = o_in_z ? zbuf + zi * K::Z_BYTES : obuf + (NO > 1 ? t % NO : 0) * K::O_BYTES;
-            const float m = factor(k, i).m;
+            if (rev && k == 1) m = factor(1, i).m;
             if (!await(&o_full, t & 1, &abort_flag)) break;
             tc_fence_after();
             if (i == 0) LA_TL(t, 13);
