@@ -39,16 +39,18 @@ Parts sum_parts(long long units, int nsum, int chunks) {
     const int want = fit < 1 ? 1 : fit < chunks ? (int)fit : chunks;
     return parts_of(chunks, (chunks + want - 1) / want);
 }
-// The same where the sum over `heads` is an output: with more blocks than SMs the length whose waves end first, a
-// block's start (and, of more than one part, their join) costing five products.
+// The same where the sum over `heads` is an output: a block takes its parts one after the other, so the count whose longest
+// block ends first: a part costs one product more, or two where it is joined (its state is written and read), and the
+// join five.
 Parts exact_parts(long long units, int nsum, int chunks, int heads) {
     Parts best = sum_parts(units, nsum, chunks);
     if (nsum > 1 && best.n > 1) return best;   // (joined anyway)
     long long cost = -1;
     for (int n = 1; n <= 16 && n <= chunks; ++n) {
         const Parts p = parts_of(chunks, (chunks + n - 1) / n);
-        const long long waves = (units * nsum * p.n + kPlanSms - 1) / kPlanSms;
-        const long long c = waves * (5 + (long long)(p.len / kDecayTcChunk) * heads) + (nsum == 1 && p.n > 1 ? 5 : 0);
+        const long long rounds = (units * nsum * p.n + kPlanSms - 1) / kPlanSms;
+        const bool joined = nsum > 1 || p.n > 1;
+        const long long c = rounds * ((joined ? 2 : 1) + (long long)(p.len / kDecayTcChunk) * heads) + (joined ? 5 : 0);
         if (cost < 0 || c < cost) {
             cost = c;
             best = p;

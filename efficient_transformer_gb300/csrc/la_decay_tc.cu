@@ -942,15 +942,37 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
     uint8_t *stage = align1024(smem_raw), *mid_tile = stage + NS * K::STAGE, *lo_tile = mid_tile + K::Y_BYTES;
     pdl_wait();
     const int warp = threadIdx.x / 32;
-    const int nparts = p.nsum * p.nsub, pidx = blockIdx.x % nparts, ah = blockIdx.x / nparts;
-    const int a = p.first + ah / (p.B * p.Hkv), bg = ah % (p.B * p.Hkv), b = bg / p.Hkv, h = bg % p.Hkv;
-    const int n = decay_tokens(p.lengths, b, p.N), rev = p.rev[a], heads = p.heads[a];
-    const bool exact = p.exact[a];
-    const Part part = sub_part_of(n, p.N, pidx / p.nsub, p.nseg, p.seg_len, pidx % p.nsub, p.nsub, p.sub_len, rev);
-    const int nchunk = (part.hi - part.lo + C - 1) / C, items = nchunk * heads;
-    const float l2 = decay_log2(p.log_decay[h]);
-    // chunks in the pass's order, the smallest powers first (small terms after large ones would be cut at their size)
-    auto chunk0 = [&](int it) { return part.lo + C * (rev ? nchunk - 1 - it / heads : it / heads); };
+    // the block's parts, one after the other (no wave of blocks starts anew); every role walks them
+    const int nparts = p.nsum * p.nsub, total = p.n * nparts * p.B * p.Hkv;
+    struct Task {
+        int a, bg, b, h, pidx, lo, hi, rev, heads, nchunk, items;
+        bool exact;
+        float l2;
+        // chunks in the pass's order, the smallest powers first (small terms after large ones would be cut at their size)
+        __device__ __forceinline__ int chunk0(int it) const {
+            return lo + C * (rev ? nchunk - 1 - it / heads : it / heads);
+        }
+    };
+    auto task = [&](int i) {
+        Task t;
+        t.pidx = i % nparts;
+        const int ah = i / nparts;
+        t.a = p.first + ah / (p.B * p.Hkv);
+        t.bg = ah % (p.B * p.Hkv);
+        t.b = t.bg / p.Hkv;
+        t.h = t.bg % p.Hkv;
+        t.rev = p.rev[t.a];
+        t.heads = p.heads[t.a];
+        t.exact = p.exact[t.a];
+        const Part part = sub_part_of(decay_tokens(p.lengths, t.b, p.N), p.N, t.pidx / p.nsub, p.nseg, p.seg_len,
+                                      t.pidx % p.nsub, p.nsub, p.sub_len, t.rev);
+        t.lo = part.lo;
+        t.hi = part.hi;
+        t.nchunk = (part.hi - part.lo + C - 1) / C;
+        t.items = t.nchunk * t.heads;
+        t.l2 = decay_log2(p.log_decay[t.h]);
+        return t;
+    };
     if (threadIdx.x == 0) {
         abort_flag = 0;
         for (int s = 0; s < NS; ++s) {
@@ -967,7 +989,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
         mbar_init(&fin, 1);
         fence_barrier_init();
     }
-    if (threadIdx.x >= 96 && threadIdx.x < 98) tma_prefetch_map(&maps.m[a][threadIdx.x - 96]);
+    if (threadIdx.x >= 96 && threadIdx.x < 98) tma_prefetch_map(&maps.m[p.first][threadIdx.x - 96]);
     if (warp == 1) {
         tmem_alloc(&tmem_base, 512);
         tmem_relinquish();
@@ -976,114 +998,133 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = tmem_base;
+    bool ok = true;
     if (warp == 0) {
+        Ring st;
         int issued = 0;
-        for (int it = 0; it < items; ++it) {
-            const int s = it % NS, c0 = chunk0(it), hh = h * heads + it % heads;
-            if (it >= NS && !await(&empty[s], (it / NS - 1) & 1, &abort_flag)) break;
-            uint8_t *y = stage + s * K::STAGE, *z = y + K::Y_BYTES;
-            if (elect_one()) {
-                mbar_arrive_expect_tx(&full[s], K::STAGE);
+        for (int i = blockIdx.x; ok && i < total; i += gridDim.x) {
+            const Task t = task(i);
+            for (int it = 0; it < t.items; ++it) {
+                const int c0 = t.chunk0(it), hh = t.h * t.heads + it % t.heads;
+                // (the first use of a stage: the phase before the first counts as over)
+                if (!(ok = await(&empty[st.s], st.p ^ 1u, &abort_flag))) break;
+                uint8_t *y = stage + st.s * K::STAGE, *z = y + K::Y_BYTES;
+                if (elect_one()) {
+                    const CUtensorMap *m = maps.m[t.a];
+                    mbar_arrive_expect_tx(&full[st.s], K::STAGE);
 #pragma unroll
-                for (int blk = 0; blk < D / 64; ++blk) tma_load_4d(y + blk * C * 128, &maps.m[a][0], &full[s], blk * 64, c0, hh, b);
+                    for (int blk = 0; blk < D / 64; ++blk) tma_load_4d(y + blk * C * 128, &m[0], &full[st.s], blk * 64, c0, hh, t.b);
 #pragma unroll
-                for (int blk = 0; blk < DV / 64; ++blk) tma_load_4d(z + blk * C * 128, &maps.m[a][1], &full[s], blk * 64, c0, hh, b);
+                    for (int blk = 0; blk < DV / 64; ++blk) tma_load_4d(z + blk * C * 128, &m[1], &full[st.s], blk * 64, c0, hh, t.b);
+                }
+                __syncwarp();
+                st.next(NS);
+                ++issued;
             }
-            __syncwarp();
-            issued = it + 1;
         }
         for (int i = issued > NS ? issued - NS : 0; i < issued; ++i) warp_drain(&full[i % NS], (i / NS) & 1);
     } else if (warp == 1) {
         constexpr uint32_t id = idesc_bf16(128, DV, true, true);
         // (M = 128 rows d of which D count: with 64 the others read what lies behind the tile)
         Ring st, ac;
-        for (int it = 0; it < items; ++it) {
-            // (an accumulator's first use: the phase before the first counts as over)
-            if (exact && !await(&acc_empty[ac.s], ac.p ^ 1u, &abort_flag)) break;
-            if (!await(&y_ready[st.s], st.p, &abort_flag)) break;
-            tc_fence_after();
-            const uint32_t y = smem_u32(stage + st.s * K::STAGE), z = y + K::Y_BYTES, acc = tm + ac.s * DV;
-            if (elect_one()) {
-                if (exact) {
-                    mma_ss_mn8(acc, desc_mnmajor(smem_u32(lo_tile), C, 0, 0), desc_mnmajor(z, C, 0, 0), id, 0u);
-                    mma_ss_mn8(acc, desc_mnmajor(smem_u32(mid_tile), C, 0, 0), desc_mnmajor(z, C, 0, 0), id, 1u);
-                    mma_commit(&terms_free);
+        for (int i = blockIdx.x; ok && i < total; i += gridDim.x) {
+            const Task t = task(i);
+            for (int it = 0; it < t.items; ++it) {
+                const bool opens = t.exact || it == 0, ends = t.exact || it == t.items - 1;   // an accumulator
+                if (opens && !(ok = await(&acc_empty[ac.s], ac.p ^ 1u, &abort_flag))) break;
+                if (!(ok = await(&y_ready[st.s], st.p, &abort_flag))) break;
+                tc_fence_after();
+                const uint32_t y = smem_u32(stage + st.s * K::STAGE), z = y + K::Y_BYTES, acc = tm + ac.s * DV;
+                if (elect_one()) {
+                    if (t.exact) {
+                        mma_ss_mn8(acc, desc_mnmajor(smem_u32(lo_tile), C, 0, 0), desc_mnmajor(z, C, 0, 0), id, 0u);
+                        mma_ss_mn8(acc, desc_mnmajor(smem_u32(mid_tile), C, 0, 0), desc_mnmajor(z, C, 0, 0), id, 1u);
+                        mma_commit(&terms_free);
+                    }
+                    mma_ss_mn8(acc, desc_mnmajor(y, C, 0, 0), desc_mnmajor(z, C, 0, 0), id, t.exact || it > 0 ? 1u : 0u);
+                    mma_commit(&empty[st.s]);
+                    if (ends) mma_commit(&acc_full[ac.s]);
                 }
-                mma_ss_mn8(acc, desc_mnmajor(y, C, 0, 0), desc_mnmajor(z, C, 0, 0), id, exact || it > 0 ? 1u : 0u);
-                mma_commit(&empty[st.s]);
-                if (exact || it == items - 1) mma_commit(&acc_full[ac.s]);
+                __syncwarp();
+                st.next(NS);
+                if (ends) ac.next(NA);
             }
-            __syncwarp();
-            st.next(NS);
-            if (exact) ac.next(NA);
         }
         if (elect_one()) mma_commit(&fin);
         __syncwarp();
         warp_drain(&fin, 0);
     } else if (warp >= 4 && warp < 12) {
-        const int i = threadIdx.x - 128, j = i % C, half = i / C;
-        for (int it = 0; it < items; ++it) {
-            const int s = it % NS, c0 = chunk0(it), valid = min(C, part.hi - c0);
-            if (!await(&full[s], (it / NS) & 1, &abort_flag)) break;
-            uint8_t *y = stage + s * K::STAGE;
-            if (p.lengths && valid < C) {
-                zero_rows<D>(y, valid, i, kStateY);
-                zero_rows<DV>(y + K::Y_BYTES, valid, i, kStateY);
-                mbar_arrive_warp(&zeroed);
-                if (!await(&zeroed, 0, &abort_flag)) break;
-            }
-            // what token j has ahead of it in the part
-            const float g = exp2f(l2 * max(rev ? c0 + j - part.lo : part.hi - 1 - c0 - j, 0));
-            if (exact) {
-                // (the terms are found beside the MMAs of the item before)
-                uint32_t m[D / 16][4], l[D / 16][4];
+        const int thr = threadIdx.x - 128, j = thr % C, half = thr / C;
+        Ring st;
+        uint32_t free_p = 1, zero_p = 0;   // (the first use of the terms' tiles: the phase before it counts as over)
+        for (int i = blockIdx.x; ok && i < total; i += gridDim.x) {
+            const Task t = task(i);
+            for (int it = 0; it < t.items; ++it) {
+                const int c0 = t.chunk0(it), valid = min(C, t.hi - c0);
+                if (!(ok = await(&full[st.s], st.p, &abort_flag))) break;
+                uint8_t *y = stage + st.s * K::STAGE;
+                if (p.lengths && valid < C) {
+                    zero_rows<D>(y, valid, thr, kStateY);
+                    zero_rows<DV>(y + K::Y_BYTES, valid, thr, kStateY);
+                    mbar_arrive_warp(&zeroed);
+                    if (!(ok = await(&zeroed, zero_p, &abort_flag))) break;
+                    zero_p ^= 1u;
+                }
+                // what token j has ahead of it in the part
+                const float g = exp2f(t.l2 * max(t.rev ? c0 + j - t.lo : t.hi - 1 - c0 - j, 0));
+                if (t.exact) {
+                    // (the terms are found beside the MMAs of the item before)
+                    uint32_t m[D / 16][4], l[D / 16][4];
 #pragma unroll
-                for (int c = 0; c < D / 16; ++c) {
-                    uint4 *q = reinterpret_cast<uint4 *>(y + swz_chunk(C, j, half * (D / 16) + c));
-                    const uint4 v = *q;
-                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t h[4];
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint4 *q = reinterpret_cast<uint4 *>(y + swz_chunk(C, j, half * (D / 16) + c));
+                        const uint4 v = *q;
+                        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                        uint32_t h[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float2 f = unpack_bf16x2(x[e]);
-                        mul2(f.x, f.y, g, g);
-                        h[e] = pack_bf16x2(f.x, f.y);
-                        const float2 hf = unpack_bf16x2(h[e]);
-                        f.x -= hf.x;
-                        f.y -= hf.y;
-                        m[c][e] = pack_bf16x2(f.x, f.y);
-                        const float2 mf = unpack_bf16x2(m[c][e]);
-                        l[c][e] = pack_bf16x2(f.x - mf.x, f.y - mf.y);
+                        for (int e = 0; e < 4; ++e) {
+                            float2 f = unpack_bf16x2(x[e]);
+                            mul2(f.x, f.y, g, g);
+                            h[e] = pack_bf16x2(f.x, f.y);
+                            const float2 hf = unpack_bf16x2(h[e]);
+                            f.x -= hf.x;
+                            f.y -= hf.y;
+                            m[c][e] = pack_bf16x2(f.x, f.y);
+                            const float2 mf = unpack_bf16x2(m[c][e]);
+                            l[c][e] = pack_bf16x2(f.x - mf.x, f.y - mf.y);
+                        }
+                        *q = make_uint4(h[0], h[1], h[2], h[3]);
                     }
-                    *q = make_uint4(h[0], h[1], h[2], h[3]);
-                }
-                if (it > 0 && !await(&terms_free, (it - 1) & 1, &abort_flag)) break;
+                    if (!(ok = await(&terms_free, free_p, &abort_flag))) break;
+                    free_p ^= 1u;
 #pragma unroll
-                for (int c = 0; c < D / 16; ++c) {
-                    const uint32_t at = swz_chunk(C, j, half * (D / 16) + c);
-                    *reinterpret_cast<uint4 *>(mid_tile + at) = make_uint4(m[c][0], m[c][1], m[c][2], m[c][3]);
-                    *reinterpret_cast<uint4 *>(lo_tile + at) = make_uint4(l[c][0], l[c][1], l[c][2], l[c][3]);
-                }
-            } else {
-                const __nv_bfloat162 gh = as_bf162(pack_bf16x2(g, g));
-                const float gr = g - unpack_bf16x2(as_u32(gh)).x;
-                const __nv_bfloat162 gl = as_bf162(pack_bf16x2(gr, gr));
+                    for (int c = 0; c < D / 16; ++c) {
+                        const uint32_t at = swz_chunk(C, j, half * (D / 16) + c);
+                        *reinterpret_cast<uint4 *>(mid_tile + at) = make_uint4(m[c][0], m[c][1], m[c][2], m[c][3]);
+                        *reinterpret_cast<uint4 *>(lo_tile + at) = make_uint4(l[c][0], l[c][1], l[c][2], l[c][3]);
+                    }
+                } else {
+                    const __nv_bfloat162 gh = as_bf162(pack_bf16x2(g, g));
+                    const float gr = g - unpack_bf16x2(as_u32(gh)).x;
+                    const __nv_bfloat162 gl = as_bf162(pack_bf16x2(gr, gr));
 #pragma unroll
-                for (int c = 0; c < D / 16; ++c) {
-                    uint4 *q = reinterpret_cast<uint4 *>(y + swz_chunk(C, j, half * (D / 16) + c));
-                    uint4 v = *q;
-                    v.x = as_u32(__hfma2(as_bf162(v.x), gh, __hmul2(as_bf162(v.x), gl)));
-                    v.y = as_u32(__hfma2(as_bf162(v.y), gh, __hmul2(as_bf162(v.y), gl)));
-                    v.z = as_u32(__hfma2(as_bf162(v.z), gh, __hmul2(as_bf162(v.z), gl)));
-                    v.w = as_u32(__hfma2(as_bf162(v.w), gh, __hmul2(as_bf162(v.w), gl)));
-                    *q = v;
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint4 *q = reinterpret_cast<uint4 *>(y + swz_chunk(C, j, half * (D / 16) + c));
+                        uint4 v = *q;
+                        v.x = as_u32(__hfma2(as_bf162(v.x), gh, __hmul2(as_bf162(v.x), gl)));
+                        v.y = as_u32(__hfma2(as_bf162(v.y), gh, __hmul2(as_bf162(v.y), gl)));
+                        v.z = as_u32(__hfma2(as_bf162(v.z), gh, __hmul2(as_bf162(v.z), gl)));
+                        v.w = as_u32(__hfma2(as_bf162(v.w), gh, __hmul2(as_bf162(v.w), gl)));
+                        *q = v;
+                    }
                 }
-            }
-            fence_proxy_async();
+                fence_proxy_async();
 #ifdef LA_TEST_HOOKS
-            if (!(g_la_test_skip_decay == 2 && blockIdx.x == 0 && it == 0 && warp == 4))
+                if (!(g_la_test_skip_decay == 2 && i == 0 && it == 0 && warp == 4))
 #endif
-                mbar_arrive_warp(&y_ready[s]);
+                    mbar_arrive_warp(&y_ready[st.s]);
+                st.next(NS);
+            }
         }
     } else if (warp >= 12) {
         // thread = row d, half of the columns
@@ -1091,46 +1132,50 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
         const int wq = warp % 4, d = wq * 32 + threadIdx.x % 32, e0 = (warp - 12) / 4 * H;
         const uint32_t ta = tm + ((uint32_t)(wq * 32) << 16) + e0;
         const bool have = wq * 32 < D;
-        float S[H];
-#pragma unroll
-        for (int e = 0; e < H; ++e) S[e] = 0.f;
-        bool ok = true;
         Ring ac;
-        for (int it = exact ? 0 : items - 1; it < items && it >= 0; ++it) {
-            if (!(ok = await(&acc_full[ac.s], ac.p, &abort_flag))) break;
-            tc_fence_after();
-            if (have) {
+        for (int i = blockIdx.x; i < total; i += gridDim.x) {
+            const Task t = task(i);
+            const int sums = t.exact ? t.items : min(t.items, 1);
+            float S[H];
 #pragma unroll
-                for (int c16 = 0; c16 < H / 16; ++c16) {
-                    float v[16];
-                    tmem_ld16(ta + ac.s * DV + c16 * 16, v);
-                    tmem_wait_regs<16>(v);
+            for (int e = 0; e < H; ++e) S[e] = 0.f;
+            for (int it = 0; it < sums; ++it) {
+                if (!(ok = await(&acc_full[ac.s], ac.p, &abort_flag))) break;
+                tc_fence_after();
+                if (have) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) S[c16 * 16 + e] += v[e];
+                    for (int c16 = 0; c16 < H / 16; ++c16) {
+                        float v[16];
+                        tmem_ld16(ta + ac.s * DV + c16 * 16, v);
+                        tmem_wait_regs<16>(v);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) S[c16 * 16 + e] += v[e];
+                    }
                 }
+                tc_fence_before();
+                mbar_arrive_warp(&acc_empty[ac.s]);
+                ac.next(NA);
             }
-            tc_fence_before();
-            mbar_arrive_warp(&acc_empty[ac.s]);
-            ac.next(NA);
-        }
-        if (ok && have && p.direct) {
-            // the state after the last token (what leaves a reverse pass decays once more)
-            const int len = part.hi - part.lo, off = p.first_off[a];
-            const float g = p.init_mul[a] * exp2f(l2 * max(len - off, 0));
-            const float m = p.fin_mul[a] * (off && len > 0 ? exp2f(l2 * off) : 1.f);
-            const size_t at = ((size_t)bg * D + d) * DV + e0;
+            if (!ok) break;
+            if (have && p.direct) {
+                // the state after the last token (what leaves a reverse pass decays once more)
+                const int len = t.hi - t.lo, off = p.first_off[t.a];
+                const float g = p.init_mul[t.a] * exp2f(t.l2 * max(len - off, 0));
+                const float m = p.fin_mul[t.a] * (off && len > 0 ? exp2f(t.l2 * off) : 1.f);
+                const size_t at = ((size_t)t.bg * D + d) * DV + e0;
 #pragma unroll
-            for (int e = 0; e < H; e += 4) {
-                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (p.init[a]) x = *reinterpret_cast<const float4 *>(p.init[a] + at + e);
-                *reinterpret_cast<float4 *>(p.fin[a] + at + e) =
-                    make_float4(m * fmaf(g, x.x, S[e]), m * fmaf(g, x.y, S[e + 1]), m * fmaf(g, x.z, S[e + 2]),
-                                m * fmaf(g, x.w, S[e + 3]));
+                for (int e = 0; e < H; e += 4) {
+                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (p.init[t.a]) x = *reinterpret_cast<const float4 *>(p.init[t.a] + at + e);
+                    *reinterpret_cast<float4 *>(p.fin[t.a] + at + e) =
+                        make_float4(m * fmaf(g, x.x, S[e]), m * fmaf(g, x.y, S[e + 1]), m * fmaf(g, x.z, S[e + 2]),
+                                    m * fmaf(g, x.w, S[e + 3]));
+                }
+            } else if (have) {
+                float4 *f = reinterpret_cast<float4 *>(p.part[t.a] + ((size_t)t.bg * nparts + t.pidx) * D * DV + decay_blocked(D, d, e0));
+#pragma unroll
+                for (int e = 0; e < H / 4; ++e) f[e * D] = make_float4(S[4 * e], S[4 * e + 1], S[4 * e + 2], S[4 * e + 3]);
             }
-        } else if (ok && have) {
-            float4 *f = reinterpret_cast<float4 *>(p.part[a] + ((size_t)bg * nparts + pidx) * D * DV + decay_blocked(D, d, e0));
-#pragma unroll
-            for (int e = 0; e < H / 4; ++e) f[e * D] = make_float4(S[4 * e], S[4 * e + 1], S[4 * e + 2], S[4 * e + 3]);
         }
     }
     tc_fence_before();
@@ -1180,6 +1225,14 @@ __global__ void __launch_bounds__(kJoinThreads) k_decay_join(const __grid_consta
             o[3] = make_float4(t[0].w, t[1].w, t[2].w, t[3].w);
         }
     };
+    // the last state where it is an output: each part straight to the end (the same rounding of gamma^tokens from part to
+    // part would add up: 1.3e-6 over 32 of them, 2e-7 so)
+    float4 f[4];
+    {
+        const float g = exp2f(l2 * max(n - p.first_off[a], 0));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = make_float4(g * t[i].x, g * t[i].y, g * t[i].z, g * t[i].w);
+    }
     store(0);
     int off = p.first_off[a];
     // kAhead parts' sums are on their way at a time: one after the other costs a memory latency each
@@ -1203,6 +1256,13 @@ __global__ void __launch_bounds__(kJoinThreads) k_decay_join(const __grid_consta
             for (int i = 0; i < 4; ++i)
                 t[i] = make_float4(fmaf(g, t[i].x, x[j][i].x), fmaf(g, t[i].y, x[j][i].y), fmaf(g, t[i].z, x[j][i].z),
                                    fmaf(g, t[i].w, x[j][i].w));
+            if (p.fin[a]) {
+                const float gf = exp2f(l2 * (p.rev[a] ? part.lo : n - part.hi));
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    f[i] = make_float4(fmaf(gf, x[j][i].x, f[i].x), fmaf(gf, x[j][i].y, f[i].y), fmaf(gf, x[j][i].z, f[i].z),
+                                       fmaf(gf, x[j][i].w, f[i].w));
+            }
             if (s == p.nsub - 1 && u + 1 < p.nseg) store(u + 1);
         }
     }
@@ -1212,7 +1272,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_decay_join(const __grid_consta
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             *reinterpret_cast<float4 *>(p.fin[a] + bg * E + (size_t)(d + i) * DV + e) =
-                make_float4(t[i].x * m, t[i].y * m, t[i].z * m, t[i].w * m);
+                make_float4(f[i].x * m, f[i].y * m, f[i].z * m, f[i].w * m);
     }
 }
 
@@ -1257,7 +1317,8 @@ cudaError_t states_d(const DecayStateParams &p, cudaStream_t s) {
     cudaError_t e = prepare(kern, StateCfg<D, DV>::SMEM);
     if (e != cudaSuccess) return e;
     TraceScope tr("decay_tc_state", s);
-    return launch_pdl(kern, dim3((unsigned)p.n * p.nsum * p.nsub * p.B * p.Hkv), dim3(kStateThreads), StateCfg<D, DV>::SMEM, s,
+    const long long total = (long long)p.n * p.nsum * p.nsub * p.B * p.Hkv;
+    return launch_pdl(kern, dim3(total < kPlanSms ? (unsigned)total : kPlanSms), dim3(kStateThreads), StateCfg<D, DV>::SMEM, s,
                       maps, p);
 }
 
