@@ -942,7 +942,8 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
     uint8_t *stage = align1024(smem_raw), *mid_tile = stage + NS * K::STAGE, *lo_tile = mid_tile + K::Y_BYTES;
     pdl_wait();
     const int warp = threadIdx.x / 32;
-    // the block's parts, one after the other (no wave of blocks starts anew); every role walks them
+    // the block's parts, one after the other (no wave of blocks starts anew); every role walks them.  The last in token
+    // order, which may be short, come last
     const int nparts = p.nsum * p.nsub, total = p.n * nparts * p.B * p.Hkv;
     struct Task {
         int a, bg, b, h, pidx, lo, hi, rev, heads, nchunk, items;
@@ -955,9 +956,9 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
     };
     auto task = [&](int i) {
         Task t;
-        t.pidx = i % nparts;
-        const int ah = i / nparts;
+        const int ah = i % (p.n * p.B * p.Hkv), q = i / (p.n * p.B * p.Hkv);
         t.a = p.first + ah / (p.B * p.Hkv);
+        t.pidx = p.rev[t.a] ? nparts - 1 - q : q;
         t.bg = ah % (p.B * p.Hkv);
         t.b = t.bg / p.Hkv;
         t.h = t.bg % p.Hkv;
