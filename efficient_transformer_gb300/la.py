@@ -204,14 +204,17 @@ def _stream_handle(stream) -> ctypes.c_void_p:
 
 
 def _check_device(like, stream):
-    """The library launches on the current device; the call's tensors, which lie on ``like``'s, and its stream must be of
-    that one."""
+    """The raw stream of a call.  The library launches on the current device; the call's tensors, which lie on ``like``'s,
+    and its stream must be of that one."""
     at, here = like.get_device(), torch.cuda.current_device()
     if at != here:
         raise ValueError(f"the tensors are on cuda:{at}, the current device is cuda:{here}: "
                          f"call under torch.cuda.device({at})")
     if stream is not None and stream.device.index != at:
         raise ValueError(f"the tensors are on cuda:{at}, the stream is one of {stream.device}")
+    if stream is not None:
+        return stream.cuda_stream
+    return torch.cuda.current_stream().cuda_stream if _raw is None else _raw(here)
 
 
 def workspace_size(B, Hq, Hkv, N, D, dtype: torch.dtype, is_causal: bool, has_weights: bool,
@@ -238,17 +241,16 @@ def _memory_on(stream):
     return _NO_SWITCH if stream is None else torch.cuda.stream(stream)
 
 
-def _keep(stream, made, given):
-    """Tensors that a call on ``stream`` shares with the current stream (``made`` by the call, or ``given`` to it): freed,
-    their memory is not reused before both streams are done with it."""
-    if stream is None:
-        return
+def _keep(stream, out, given):
+    """Tensors that a call on ``stream`` shares with the current stream (its outputs and what it was given): freed, their
+    memory is not reused before both streams are done with it."""
     here = torch.cuda.current_stream()
     if here == stream:
         return
-    for t in made:
+    for t in out:
         if t is not None:
             t.record_stream(here)
+            t.record_stream(stream)
     for t in given:
         if t is not None:
             t.record_stream(stream)
@@ -277,7 +279,6 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, is_causal: bool = Fal
     B, Hq, Hkv, N, D, Dv = _check_inputs(q, k, v, cos_weight, sin_weight)
     _check_device(q, stream)
     oshape = (B, Hq, N, Dv)
-    given = [q, k, v, cos_weight, sin_weight, out, workspace]
     if out is not None and (tuple(out.shape) != oshape or out.dtype != q.dtype or out.device != q.device
                             or not out.is_contiguous()):
         raise ValueError(f"out must be a contiguous {oshape} tensor of q's dtype on q's device")
@@ -286,7 +287,8 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, is_causal: bool = Fal
         out = torch.empty(oshape, dtype=q.dtype, device=q.device) if out is None else out
         ws = _workspace(lib.la_workspace_size_v(B, Hq, Hkv, N, D, Dv, dt, int(is_causal),
                                                 int(cos_weight is not None), 0), q.device, workspace)
-    _keep(stream, (out,), given)
+    if stream is not None:
+        _keep(stream, (out,), (q, k, v, cos_weight, sin_weight, workspace))
     nws = 0 if ws is None else ws.numel() * ws.element_size()
     strides = [_strides(t) for t in (q, k, v)]
     if Dv != D:
@@ -327,7 +329,6 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, grad_out: torch.Tenso
     _check_device(q, stream)
     if tuple(grad_out.shape) != (B, Hq, N, Dv):
         raise ValueError("grad_out must have the shape of out ([B, Hq, N, Dv])")
-    given = [q, k, v, grad_out, cos_weight, sin_weight, dq, dk, dv, workspace, fwd_workspace]
     with _memory_on(stream):
         dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
         dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
@@ -342,7 +343,8 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, grad_out: torch.Tenso
     nws = 0 if ws is None else ws.numel() * ws.element_size()
     if fwd_workspace is not None and fwd_workspace.device != q.device:
         raise ValueError("fwd_workspace must be on q's device")
-    _keep(stream, (dq, dk, dv), given)
+    if stream is not None:
+        _keep(stream, (dq, dk, dv), (q, k, v, grad_out, cos_weight, sin_weight, workspace, fwd_workspace))
     strides = [_strides(t) for t in (q, k, v, grad_out)]
     if Dv != D:
         if any(x is not None for x in strides):
@@ -402,14 +404,14 @@ def lowrank_fwd(x: torch.Tensor, U: torch.Tensor, V: torch.Tensor, bias: torch.T
     lib = load()
     M, K_in, r, K_out = _check_lowrank(x, U, V, bias)
     _check_device(x, stream)
-    given = [x, U, V, bias, out, t_out]
     if out is None:
         with _memory_on(stream):
             out = torch.empty(x.shape[:-1] + (K_out,), dtype=x.dtype, device=x.device)
     elif out.shape != x.shape[:-1] + (K_out,) or out.dtype != x.dtype or out.device != x.device \
             or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor [..., K_out] of x's dtype on x's device")
-    _keep(stream, (out,), given)
+    if stream is not None:
+        _keep(stream, (out, t_out), (x, U, V, bias))
     if t_out is None:
         st = lib.la_lowrank_fwd(_ptr(x), _ptr(U), _ptr(V), _ptr(bias), _ptr(out), M, K_in, r, K_out,
                                 _dtype_code(x), _stream_handle(stream))
@@ -443,7 +445,8 @@ def lowrank_bwd(x: torch.Tensor, U: torch.Tensor, V: torch.Tensor, grad_out: tor
         dx, dU, dV = torch.empty_like(x), torch.empty_like(U), torch.empty_like(V)
         db = torch.empty_like(bias) if bias is not None else None
         ws = _workspace(lib.la_lowrank_workspace_size(M, K_in, r, K_out, dt, 1), x.device, workspace)
-    _keep(stream, (dx, dU, dV, db), (x, U, V, grad_out, bias, workspace, t))
+    if stream is not None:
+        _keep(stream, (dx, dU, dV, db), (x, U, V, grad_out, bias, workspace, t))
     nws = 0 if ws is None else ws.numel() * ws.element_size()
     if t is None:
         st = lib.la_lowrank_bwd(_ptr(x), _ptr(U), _ptr(V), _ptr(grad_out), _ptr(dx), _ptr(dU), _ptr(dV), _ptr(db),
@@ -477,16 +480,8 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream(stream):
-    return _current_stream() if stream is None else stream.cuda_stream
-
-
 # torch's current stream as an integer, without a Stream object (2.8 of a call's 15 us) where torch has that
 _raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _current_stream():
-    return torch.cuda.current_stream().cuda_stream if _raw is None else _raw(torch.cuda.current_device())
 
 
 @functools.lru_cache(maxsize=256)
@@ -571,7 +566,7 @@ def decay_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torc
     ``final_state`` 4e-6 to 1e-5."""
     lib = load()
     B, Hq, Hkv, N, D, Dv = _check_qkv(q, k, v)
-    _check_device(q, stream)
+    raw = _check_device(q, stream)
     dt = _dtype_code(q)
     _check_vector("log_decay", log_decay, Hkv, torch.float32, q)
     if lengths is not None:
@@ -579,14 +574,14 @@ def decay_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torc
     for name, t in (("initial_state", initial_state), ("final_state", final_state)):
         if t is not None:
             _check_state(name, t, (B, Hkv, D, Dv), q)
-    given = (q, k, v, log_decay, initial_state, final_state, lengths, out, workspace)
     with _memory_on(stream):
         out = _output("out", out, (B, Hq, N, Dv), q)
         ws = _workspace(_decay_need(B, Hq, Hkv, N, D, Dv, dt, 0), q.device, workspace)
-    _keep(stream, (out,), given)
+    if stream is not None:
+        _keep(stream, (out,), (q, k, v, log_decay, initial_state, final_state, lengths, workspace))
     st = lib.la_decay_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), log_decay.data_ptr(),
                           _addr(initial_state), _addr(final_state), _addr(lengths), B, Hq, Hkv, N, D, Dv, dt, scale,
-                          _stride_arg(q), _stride_arg(k), _stride_arg(v), _addr(ws), _nbytes(ws), _raw_stream(stream))
+                          _stride_arg(q), _stride_arg(k), _stride_arg(v), _addr(ws), _nbytes(ws), raw)
     if st != LA_OK:
         _raise(lib, st, "la_decay_fwd")
     return out
@@ -603,7 +598,7 @@ def decay_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, grad_out: torch
     ``log_decay`` gets no gradient."""
     lib = load()
     B, Hq, Hkv, N, D, Dv = _check_qkv(q, k, v, grad_out)
-    _check_device(q, stream)
+    raw = _check_device(q, stream)
     if tuple(grad_out.shape) != (B, Hq, N, Dv):
         raise ValueError("grad_out must have the shape of out ([B, Hq, N, Dv])")
     dt = _dtype_code(q)
@@ -612,15 +607,15 @@ def decay_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, grad_out: torch
                     ("grad_initial_state", grad_initial_state)):
         if t is not None:
             _check_state(name, t, (B, Hkv, D, Dv), q)
-    given = (q, k, v, grad_out, log_decay, initial_state, grad_final_state, grad_initial_state, dq, dk, dv, workspace)
     with _memory_on(stream):
         dq, dk, dv = _output("dq", dq, q.shape, q), _output("dk", dk, k.shape, k), _output("dv", dv, v.shape, v)
         ws = _workspace(_decay_need(B, Hq, Hkv, N, D, Dv, dt, 1), q.device, workspace)
-    _keep(stream, (dq, dk, dv), given)
+    if stream is not None:
+        _keep(stream, (dq, dk, dv), (q, k, v, grad_out, log_decay, initial_state, grad_final_state, grad_initial_state, workspace))
     st = lib.la_decay_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), grad_out.data_ptr(), dq.data_ptr(), dk.data_ptr(),
                           dv.data_ptr(), log_decay.data_ptr(), _addr(initial_state), _addr(grad_final_state),
                           _addr(grad_initial_state), B, Hq, Hkv, N, D, Dv, dt, scale, _stride_arg(q), _stride_arg(k),
-                          _stride_arg(v), _stride_arg(grad_out), _addr(ws), _nbytes(ws), _raw_stream(stream))
+                          _stride_arg(v), _stride_arg(grad_out), _addr(ws), _nbytes(ws), raw)
     if st != LA_OK:
         _raise(lib, st, "la_decay_bwd")
     return dq, dk, dv
@@ -636,7 +631,7 @@ def decay_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, state: torch.T
     ``state``).  Returns ``out`` [B, Hq, 1, Dv]."""
     lib = load()
     B, Hq, Hkv, N, D, Dv = _check_qkv(q, k, v)
-    _check_device(q, stream)
+    raw = _check_device(q, stream)
     if N != 1:
         raise ValueError(f"decay_step takes one token per sequence (N = 1), got N = {N}")
     _check_vector("log_decay", log_decay, Hkv, torch.float32, q)
@@ -646,14 +641,14 @@ def decay_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, state: torch.T
     _check_state("state", state, (pool, Hkv, D, Dv), q)
     if state_out is not None:
         _check_state("state_out", state_out, (pool, Hkv, D, Dv), q)
-    given = (q, k, v, state, log_decay, slots, state_out, out)
     with _memory_on(stream):
         out = _output("out", out, (B, Hq, 1, Dv), q)
-    _keep(stream, (out,), given)
+    if stream is not None:
+        _keep(stream, (out,), (q, k, v, state, log_decay, slots, state_out))
     st = lib.la_decay_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), state.data_ptr(),
                            (state if state_out is None else state_out).data_ptr(), log_decay.data_ptr(), _addr(slots),
                            pool, B, Hq, Hkv, D, Dv, _dtype_code(q), scale, _stride_arg(q), _stride_arg(k),
-                           _stride_arg(v), _raw_stream(stream))
+                           _stride_arg(v), raw)
     if st != LA_OK:
         _raise(lib, st, "la_decay_step")
     return out
@@ -752,14 +747,14 @@ def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, *, q_weight: torch.Tensor
     turned.  Without positions: the norm alone; with ``normalize=False``: the rotation alone."""
     lib = load()
     B, Hq, Hkv, N, D = _check_qk(q, k)
-    _check_device(q, stream)
+    raw = _check_device(q, stream)
     a = _qk_args(q, q_weight, k_weight, eps, positions, inv_freq, sections, interleaved, normalize)
-    given = (q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out)
     with _memory_on(stream):
         q_out, k_out = _output("q_out", q_out, q.shape, q), _output("k_out", k_out, k.shape, k)
-    _keep(stream, (q_out, k_out), given)
+    if stream is not None:
+        _keep(stream, (q_out, k_out), (q, k, q_weight, k_weight, positions, inv_freq))
     st = lib.la_qk_norm_rope_fwd(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), B, Hq, Hkv, N, D,
-                                 _dtype_code(q), _stride_arg(q), _stride_arg(k), ctypes.byref(a), _raw_stream(stream))
+                                 _dtype_code(q), _stride_arg(q), _stride_arg(k), ctypes.byref(a), raw)
     if st != LA_OK:
         _raise(lib, st, "la_qk_norm_rope_fwd")
     return q_out, k_out
@@ -780,11 +775,10 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, grad_q: torch.Tensor, gra
     without that weight."""
     lib = load()
     B, Hq, Hkv, N, D = _check_qk(q, k, (("grad_q", grad_q), ("grad_k", grad_k)))
-    _check_device(q, stream)
+    raw = _check_device(q, stream)
     if grad_q.shape != q.shape or grad_k.shape != k.shape:
         raise ValueError("grad_q and grad_k must have the shapes of q and k")
     a = _qk_args(q, q_weight, k_weight, eps, positions, inv_freq, sections, interleaved, normalize)
-    given = (q, k, grad_q, grad_k, q_weight, k_weight, positions, inv_freq, dq, dk, workspace)
     dt, ws = _dtype_code(q), None
     with _memory_on(stream):
         dq, dk = _output("dq", dq, q.shape, q), _output("dk", dk, k.shape, k)
@@ -792,11 +786,12 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, grad_q: torch.Tensor, gra
         dkw = torch.empty_like(k_weight) if k_weight is not None else None
         if dqw is not None or dkw is not None:
             ws = _workspace(_qk_need(B, Hq, Hkv, N, D, dt), q.device, workspace)
-    _keep(stream, (dq, dk, dqw, dkw), given)
+    if stream is not None:
+        _keep(stream, (dq, dk, dqw, dkw), (q, k, grad_q, grad_k, q_weight, k_weight, positions, inv_freq, workspace))
     st = lib.la_qk_norm_rope_bwd(q.data_ptr(), k.data_ptr(), grad_q.data_ptr(), grad_k.data_ptr(), dq.data_ptr(),
                                  dk.data_ptr(), _addr(dqw), _addr(dkw), B, Hq, Hkv, N, D, dt, _stride_arg(q),
                                  _stride_arg(k), _stride_arg(grad_q), _stride_arg(grad_k), ctypes.byref(a), _addr(ws),
-                                 _nbytes(ws), _raw_stream(stream))
+                                 _nbytes(ws), raw)
     if st != LA_OK:
         _raise(lib, st, "la_qk_norm_rope_bwd")
     return dq, dk, dqw, dkw
