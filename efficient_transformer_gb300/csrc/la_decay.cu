@@ -62,8 +62,8 @@ Parts exact_parts(long long units, int nsum, int chunks, int heads) {
 // The segments of a sequence: the count whose schedule ends first.  A schedule is waves of blocks that run at once,
 // a block costing its start and its chunks (a chunk more where two blocks share an SM), and at least what the memory
 // traffic takes; more than one segment costs the kernels that sum and join them.  Times in microseconds, fitted to
-// GB300: on the tensor cores (one block an SM) 64 chunks of 128 x 128 take 157 us, 32 of 64 x 64 67 us, sums of 8
-// chunks 128 x 128 20 us; on the CUDA cores 64 chunks of 64 x 64 362 us with one block an SM and 610 us with two.
+// GB300: on the tensor cores (one block an SM) 27 chunks of four heads of 128 x 128 take 270 us, 32 of 64 x 64 78 us, sums
+// of 8 chunks 128 x 128 20 us; on the CUDA cores 64 chunks of 64 x 64 362 us with one block an SM and 610 us with two.
 struct Cost {
     int per_sm;                      // blocks an SM holds
     double start, chunk, pair;       // of a block: its start, a chunk, a chunk's factor beside another block

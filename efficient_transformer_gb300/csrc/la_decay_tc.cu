@@ -28,13 +28,14 @@
 // The reverse passes (gradients of k and v) take the same steps with j >= i and gamma^(j-i), chunks from the
 // last to the first.
 //
-// What bounds it: the chain of hand-overs from role to role, one block an SM: 2.3 to 2.4 us for a chunk and head of
-// 128 x 128 and 2.0 us of 64 x 64, with grouped queries (32 on 8 heads, N 65536, D 128: 252 us, 108 of them a block) as
-// with one head each.  The tensor pipe is busy for 15 to 30 % of the time, an SM's warps issue 1.3 to 1.7 instructions a
-// cycle, the memory gives 5.3 TB/s at most.  In copies of this kernel that leave out work (passes alone, us; gradients of
-// 2 x 16 heads, N 8192, D 128 | 4 x 16, N 4096, D 64 | 32/8, N 65536, D 128): as it is 125 | 43 | 252; without the
-// arithmetic of P 113 | 37 | 229, of the decayed X 121 | 41 | 244, of the decayed Y 123 | 43 | 238, of S 119 | 43 | 252;
-// without the output's stores 113 | 43 | 240; without all of these 90 | 31 | 180; without most MMAs as well 82 | 31 | 154.
+// What bounds it: the chain of hand-overs from role to role, one block an SM: 2.5 us for a chunk and head of 128 x 128
+// where y and z are shared (32 query on 8 heads, N 65536, D 128: 274 us, 108 of them a block), 3.1 us with one head each on
+// every SM (8 x 19 heads, N 8192: 218 us; there the memory gives 6.4 TB/s), 2.0 us of 64 x 64.  The tensor pipe is busy
+// for 16 to 39 % of the time, an SM's warps issue 1.1 to 1.8 instructions a cycle.  In copies of this kernel that leave out
+// work (passes alone, us; gradients of 2 x 16 heads, N 8192, D 128 | 4 x 16, N 4096, D 64 | 32/8, N 65536, D 128): as it is
+// 137 | 45 | 274; without the arithmetic of P 131 | 35 | 234, of the decayed X 133 | 43 | 252, of the decayed Y 137 | 45 |
+// 256, of S 131 | 45 | 270; without the output's stores 131 | 45 | 270; without all of these 104 | 33 | 211; without most
+// MMAs as well 90 | 31 | 160.  With x and S rounded to bf16 (and their MMA and tiles saved) it was 125 | 43 | 252.
 #include "la_decay.cuh"
 #include "la_tc_common.cuh"
 
@@ -160,6 +161,13 @@ __device__ __forceinline__ void fma2(float &x, float &y, float a, float b, float
     asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(c));
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(p) : "l"(q), "l"(r));
     asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
+}
+
+// The upper 8 bits of two floats' significands as bf16, taken off them: three of these are the whole 24.
+__device__ __forceinline__ uint32_t cut_bf16x2(float2 &f) {
+    const uint32_t x = __float_as_uint(f.x), y = __float_as_uint(f.y);
+    fma2(f.x, f.y, __uint_as_float(x & 0xffff0000u), __uint_as_float(y & 0xffff0000u), -1.f);
+    return __byte_perm(x, y, 0x7632);
 }
 
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t u) { return *reinterpret_cast<__nv_bfloat162 *>(&u); }
@@ -902,14 +910,15 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
 // ---------------------------------------------------------------------------------------
 // The sums over parts of segments (see DecayStateParams).  y is decayed to the part's end at once (y w, w <= 1).
 //   Sums that only bf16 outputs depend on: bf16(y w)^T Z, in place of y, all in one accumulator.
-//   A state that goes out: y w in float32 as three bf16 terms (2^-25), hi in place of y, mid and lo in tiles of
+//   A state that goes out: y w in float32 as three bf16 terms (all 24 bits), hi in place of y, mid and lo in tiles of
 // their own.  The MMA's sums are cut, not rounded, to float32 at every step, so that long chains of them drift (2e-7 a chunk and
 // head); each chunk and head has an accumulator of its own, smallest terms first, and eight warps add those up in
-// registers.  2 to 4e-7 of the state, whatever its length (in two terms and one accumulator 4e-6 to 7e-5).
+// registers.  1.3 to 3e-7 of the state, whatever its length (in two terms and one accumulator 4e-6 to 7e-5).
 // Where a whole sequence is one part, these warps write the state itself (`direct`).
-// Warps: 0 TMA, 1 MMA, 4-11 y (two threads a token), 12-19 the sums.  Bound by memory where the parts are long (8
-// heads, N 65536, 128 x 128: TIME us for 268 MB), else by the first chunk's latency (64 heads, N 4096, 64 x 64, parts of 8
-// chunks: 14 us).
+// Warps: 0 TMA, 1 MMA, 4-11 y (two threads a token), 12-19 the sums.  One term is bound by memory where the parts are long
+// (8 heads, N 65536, 128 x 128: 58 us for 268 MB), else by the first chunk's latency (64 heads, N 4096, 64 x 64, parts of
+// 8 chunks: 14 us).  Three terms take 69 us there, 73 us for 4 x 40 heads, N 4096, 128 x 64 (252 MB): the instructions that
+// split y (without them 50 us; rounded instead of cut terms 85) and the terms' way through shared memory.
 constexpr int kStateThreads = 640, kStateY = 256, kStateSum = 256;
 
 struct StateMaps {
@@ -1086,13 +1095,9 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_decay_tc_state(const __gri
                         for (int e = 0; e < 4; ++e) {
                             float2 f = unpack_bf16x2(x[e]);
                             mul2(f.x, f.y, g, g);
-                            h[e] = pack_bf16x2(f.x, f.y);
-                            const float2 hf = unpack_bf16x2(h[e]);
-                            f.x -= hf.x;
-                            f.y -= hf.y;
-                            m[c][e] = pack_bf16x2(f.x, f.y);
-                            const float2 mf = unpack_bf16x2(m[c][e]);
-                            l[c][e] = pack_bf16x2(f.x - mf.x, f.y - mf.y);
+                            h[e] = cut_bf16x2(f);
+                            m[c][e] = cut_bf16x2(f);
+                            l[c][e] = cut_bf16x2(f);
                         }
                         *q = make_uint4(h[0], h[1], h[2], h[3]);
                     }

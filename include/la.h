@@ -295,12 +295,11 @@ la_status la_lowrank_bwd_t(const void *x, const void *U, const void *V, const vo
  * grad_final_state / scale has to be within float32.
  *
  * Arithmetic.  float32 inputs: float32 throughout.  bfloat16 inputs on the tensor cores
- * (la_decay_kernel_path): float32 sums and states, but the factors of the products are rounded to
- * bfloat16, once each: the decayed scores, q (k, grad_out) times its decay, the state as queries
- * read it (initial_state and grad_final_state included), and the decayed k (q, v) that a
- * state is summed from where the state itself is no output.  Outputs then are 3.1e-3 (2-norm)
- * from the exact ones, where rounding them alone leaves 1.7e-3; states that go out, from two
- * bfloat16 terms, 4e-6 to 1e-5.  For float32 arithmetic throughout give float32 inputs.
+ * (la_decay_kernel_path): float32 sums and states; each term of an output is rounded to bfloat16 once on its way
+ * (as a decayed score, or as the decayed k (q, v) in the state that queries read) and the output once
+ * more: 2.3e-3 (2-norm) from the exact ones, where rounding the outputs alone leaves 1.7e-3.  The states that are given
+ * are read to 2^-17; those that go out are within 1e-6 (2-norm), 3e-7 as measured.  For float32
+ * arithmetic throughout give float32 inputs.
  *
  * A NaN or infinity in a token's row reaches, besides the outputs that depend on it, at most
  * the other rows of the same 128-token chunk on the tensor cores (earlier ones among them: a weight of 0

@@ -3,9 +3,9 @@ rows are off that a lost or misplaced carry cannot hide in: the relative 2-norm 
 import torch
 
 # Rounding to bfloat16 leaves 2^-8 of a value at worst and, uniformly spread over a step, 2^-8 / sqrt(3) and the mean of
-# a significand's inverse (0.72): 1.6e-3 of it in the mean square.  A row of random terms takes four independent such
-# roundings at most (scores, decayed x, state or decayed y, result): 3.3e-3 of its norm.  Three times that:
-LIMIT = 1e-2
+# a significand's inverse (0.72): 1.6e-3 of it in the mean square.  A row of random terms takes two independent such
+# roundings (a score or a decayed y of each term, the result): 2.3e-3 of its norm.  Three times that:
+LIMIT = 7e-3
 
 
 def forward(q, k, v, ld, scale=1.0, S0=None, n=None):

@@ -41,7 +41,7 @@ def test_rounded_results_pass(case):
     (q, k, v, go, ld, S0, dS1), want = case
     for x in (want[0], *want[2:5]):
         assert db.close(x.to(BF), x)
-    # scores, decayed x, state and result, each rounded once, chunk by chunk
+    # scores, decayed y and result, each rounded once, chunk by chunk
     g = torch.exp(ld.double())[:, None]
     S, rows, r = S0[0].clone(), [], SHAPE[1] // SHAPE[2]
     i = torch.arange(128).double()
@@ -50,8 +50,8 @@ def test_rounded_results_pass(case):
         kc, vc, qc = k[0, :, t:t + 128], v[0, :, t:t + 128], q[0, :, t:t + 128].view(SHAPE[2], r, 128, -1)
         w = (g[..., None] ** (i[:, None] - i[None]).clamp(min=0)).tril()
         P = bf(0.25 * torch.einsum("hrid,hjd->hrij", qc, kc) * w[:, None])
-        x = bf(0.25 * qc * (g ** (i + 1))[:, None, :, None])
-        rows.append(bf(torch.einsum("hrij,hje->hrie", P, vc) + torch.einsum("hrid,hde->hrie", x, bf(S))))
+        x = 0.25 * qc * (g ** (i + 1))[:, None, :, None]
+        rows.append(bf(torch.einsum("hrij,hje->hrie", P, vc) + torch.einsum("hrid,hde->hrie", x, S)))
         S = g[..., None] ** 128 * S + torch.einsum("hjd,hje->hde", bf(kc * (g ** (127 - i))[..., None]), vc)
     assert db.close(torch.cat(rows, 2).reshape(want[0].shape), want[0])
 

@@ -1,18 +1,16 @@
 """States that go out, whatever the batch: a state's accuracy does not follow from whether its sequence was cut.
 
-Bound (2-norm of a head's state, relative).  The two bfloat16 terms of each y leave 2^-17 of a product.  The matrix units cut
-their float32 sums at each step of 16 tokens, by half a step of the sum so far on average: 2^-24 of it at most in the mean.  A
-chunk of 128 tokens and one head is 8 steps for each of y's two terms, and an accumulator takes 32 such chunks and heads at
-most: 2^-17 + 32 16 2^-24.  One accumulator for whole sequences exceeded that: 7.4e-5 for the gradient of 8 x 128/16 heads, N 4096."""
+Bound (2-norm of a head's state, relative): as in test_gpu_decay_precision.  One accumulator for whole sequences and two
+bfloat16 terms exceeded it: 4e-6 for the terms, 7.4e-5 in all for the gradient of 8 x 128/16 heads, N 4096."""
 import pytest
 import torch
 
 from efficient_transformer_gb300 import build as la_build
 from efficient_transformer_gb300 import la
+from test_gpu_decay_precision import STATE as BOUND
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
-BOUND = 2.0 ** -17 + 32 * 16 * 2.0 ** -24
 
 
 @pytest.fixture(scope="module", autouse=True)
