@@ -13,7 +13,8 @@ bool width_ok(int D) { return D == 32 || D == 64 || D == 128; }
 la_status check(int B, int Hq, int Hkv, int N, int D, int Dv, int dtype, float scale) {
     if (B <= 0 || Hq <= 0 || Hkv <= 0 || N <= 0 || D <= 0 || Dv <= 0 || Hq % Hkv != 0) return LA_ERR_ARG;
     if (dtype != LA_F32 && dtype != LA_BF16) return LA_ERR_ARG;
-    if (!std::isfinite(scale) || scale == 0.f) return LA_ERR_ARG;
+    // (a subnormal one has no row factors of two and, as the gradients divide by it, no finite reciprocal)
+    if (!std::isnormal(scale)) return LA_ERR_ARG;
     // rows of a tensor are counted in 64 bits, heads and blocks in 31
     if ((unsigned long long)B * Hq >= (1u << 26) || (((unsigned long long)B * Hq * N) >> 50)) return LA_ERR_ARG;
     if (!width_ok(D) || !width_ok(Dv)) return LA_ERR_UNSUPPORTED;
@@ -201,8 +202,6 @@ la_status run(bool bwd, const Given &a, int B, int Hq, int Hkv, int N, int D, in
     la_status st = check(B, Hq, Hkv, N, D, Dv, dt, scale);
     if (st != LA_OK) return st;
     if (!a.q || !a.k || !a.v || !a.log_decay) return LA_ERR_ARG;
-    // (the reverse states are carried without `scale`: the incoming gradient is divided by it)
-    if (bwd && !std::isfinite(1.f / scale)) return LA_ERR_ARG;
     if (bwd ? (!a.g || !a.dq || !a.dk || !a.dv) : !a.out) return LA_ERR_ARG;
     // (the passes of the gradients read both states while one of them writes grad_initial_state)
     if (a.ds_out && (a.ds_out == a.s_in || a.ds_out == a.ds_in)) return LA_ERR_ARG;

@@ -22,8 +22,8 @@
 // Several heads of x share one chunk of y, z (grouped queries; S moves on after the last), or several heads
 // of y, z share one of x (their gradients; O and S sum over the heads).
 //
-// Warps: 0 TMA of x, 3 of y and z, 1 MMA of scores and O, 2 MMA of S, 4-7 P, 8-11 S -> S_bf and the decay of S, 12-15 the decayed X,
-// 16-19 the output rows, 20-23 the decayed y (and the zeros past a sequence's length).
+// Warps: 0 TMA of x, 3 of y and z, 1 MMA of scores and O, 2 MMA of S, 4-7 P, 8-11 S -> S_hi, S_lo and the decay of S,
+// 12-15 the decayed X, 16-19 the output rows, 20-23 the decayed y (and the zeros past a sequence's length).
 //
 // The reverse passes (gradients of k and v) take the same steps with j >= i and gamma^(j-i), chunks from the
 // last to the first.
@@ -911,9 +911,9 @@ __global__ void __launch_bounds__(kMainThreads, 1) k_decay_tc(const __grid_const
 // The sums over parts of segments (see DecayStateParams).  y is decayed to the part's end at once (y w, w <= 1).
 //   Sums that only bf16 outputs depend on: bf16(y w)^T Z, in place of y, all in one accumulator.
 //   A state that goes out: y w in float32 as three bf16 terms (all 24 bits), hi in place of y, mid and lo in tiles of
-// their own.  The MMA's sums are cut, not rounded, to float32 at every step, so that long chains of them drift (2e-7 a chunk and
-// head); each chunk and head has an accumulator of its own, smallest terms first, and eight warps add those up in
-// registers.  1.3 to 3e-7 of the state, whatever its length (in two terms and one accumulator 4e-6 to 7e-5).
+// their own.  The MMA's sums are cut, not rounded, to float32 at every step, so that long chains of them drift (2e-7 a
+// chunk and head); each chunk and head has an accumulator of its own, smallest terms first, and eight warps add those up
+// in registers.  1.3 to 3e-7 of the state, whatever its length (in two terms and one accumulator 4e-6 to 7e-5).
 // Where a whole sequence is one part, these warps write the state itself (`direct`).
 // Warps: 0 TMA, 1 MMA, 4-11 y (two threads a token), 12-19 the sums.  One term is bound by memory where the parts are long
 // (8 heads, N 65536, 128 x 128: 58 us for 268 MB), else by the first chunk's latency (64 heads, N 4096, 64 x 64, parts of

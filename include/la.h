@@ -291,8 +291,8 @@ la_status la_lowrank_bwd_t(const void *x, const void *U, const void *V, const vo
  *
  * log_decay [Hkv] is a float32 device vector, expected <= 0 (a non-finite -inf is gamma = 0:
  * each token sees itself alone); it gets no gradient.  Values above 0 grow the state by the
- * same formula.  scale: finite and not 0; for the gradient with a finite reciprocal too, and
- * grad_final_state / scale has to be within float32.
+ * same formula.  scale: a normal float32 (finite, not 0, not subnormal); grad_final_state / scale has
+ * to be within float32.
  *
  * Arithmetic.  float32 inputs: float32 throughout.  bfloat16 inputs on the tensor cores
  * (la_decay_kernel_path): float32 sums and states; each term of an output is rounded to bfloat16 once on its way
