@@ -1,0 +1,175 @@
+// la_ssm.cuh -- selective state space scan: launch parameters, work plan and the device functions that the scan, its
+// gradient and its single-token step share.
+//
+//   d = softplus(dt + dt_bias)           (or dt + dt_bias)
+//   h <- exp(d A) h + d x B,   y = C . h + skip x,   out = y z sigmoid(z)
+//
+// Every channel has S states of its own; B and C rows are shared by the channels of a group.
+#pragma once
+
+#include "la_internal.cuh"
+
+namespace la {
+
+constexpr int kSsmTile = 8;   // tokens between the states that the forward keeps for the gradient
+
+// Strides of a [B, N, E] input (h unused), or of a [B, N, G, S] one (h: along G).
+struct SsmParams {
+    const void *x, *dt, *B, *C, *z, *g;
+    Strides sx, sdt, sB, sC, sz, sg;
+    const float *A, *skip, *dt_bias, *init, *dfinal;
+    const int *lengths;
+    void *out;                       // scan; NULL: only the kept states (and the final one) are wanted
+    float *fin;                      // final state or NULL
+    float *kept;                     // states at every kSsmTile tokens [B][tiles][E][S] (written by the scan, read by the gradient)
+    void *dx, *ddt, *dz;
+    float *dinit;
+    int nB, N, E, S, G, Eg, softplus;
+    int seg_len, nseg;               // the launch's work split (a multiple of the kernels' tiles)
+    float *seg_state;                // [B][nseg][E][S] sums of the segments alone
+    float *seg_d;                    // [B][nseg][E] their sums of d
+    float *part_bc;                  // gradient: [G * blocks][B][N][2 S] dB and dC summed over a block's channels
+    float *part_A;                   // [B * nseg][E][S]
+    float *part_e;                   // [B * nseg][2][E]: skip's and dt_bias' gradients
+};
+
+// What reduces the gradient's parts.
+struct SsmReduceParams {
+    const float *part_bc, *part_A, *part_e;
+    const int *lengths;
+    void *dB, *dC;
+    float *dA, *dskip, *dbias;
+    int nB, N, E, S, G, blocks, parts;   // blocks of a group's channels; parts: B * nseg
+};
+
+struct SsmStepParams {
+    const void *x, *dt, *B, *C, *z;
+    Strides sx, sdt, sB, sC, sz;
+    const float *A, *skip, *dt_bias, *state;
+    float *state_out;
+    const int *slots;
+    void *out;
+    int pool, nB, E, S, G, Eg, softplus;
+};
+
+cudaError_t ssm_scan(const SsmParams &p, la_dtype dt, cudaStream_t s);             // p.nseg > 1: after ssm_segments
+cudaError_t ssm_segments(const SsmParams &p, la_dtype dt, bool reverse, cudaStream_t s);
+cudaError_t ssm_grad(const SsmParams &p, la_dtype dt, cudaStream_t s);
+cudaError_t ssm_reduce(const SsmReduceParams &p, la_dtype dt, cudaStream_t s);
+cudaError_t ssm_step(const SsmStepParams &p, la_dtype dt, cudaStream_t s);
+int ssm_scan_channels(int S);    // channels of a block of the scan
+int ssm_grad_channels(int S, la_dtype dt);    // ... and of the gradient
+
+#ifdef __CUDACC__
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x) {   // 2^x: 1.4e-7 relative, 32 a clock and SM on GB300
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two floats in one register pair: one instruction for two products or sums.
+struct F2 {
+    float x, y;
+};
+__device__ __forceinline__ F2 f2(float a) { return F2{a, a}; }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("{\n.reg .b64 a, b, c;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmov.b64 c, {%6, %7};\n"
+        "fma.rn.f32x2 a, a, b, c;\nmov.b64 {%0, %1}, a;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("{\n.reg .b64 a, b;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmul.rn.f32x2 a, a, b;\nmov.b64 {%0, %1}, a;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("{\n.reg .b64 a, b;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nadd.rn.f32x2 a, a, b;\nmov.b64 {%0, %1}, a;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ F2 ex22(F2 a) { return F2{ex2(a.x), ex2(a.y)}; }
+
+// log(1 + e) / e on [0, 1]: polynomial of least relative error (5e-9), 1.5e-7 in float32 arithmetic.  No cancellation for
+// small e, where log(1 + e) itself loses what 1 + e rounds away.
+__device__ __forceinline__ float log1p_over(float e) {
+    float a = -0.003243980696424842f;
+    a = fmaf(a, e, 0.019851261749863625f);
+    a = fmaf(a, e, -0.056959159672260284f);
+    a = fmaf(a, e, 0.10603617131710052f);
+    a = fmaf(a, e, -0.15305569767951965f);
+    a = fmaf(a, e, 0.19675931334495544f);
+    a = fmaf(a, e, -0.24954132735729218f);
+    a = fmaf(a, e, 0.3332996368408203f);
+    a = fmaf(a, e, -0.4999990165233612f);
+    return fmaf(a, e, 1.0f);
+}
+// softplus(v) = max(v, 0) + log(1 + exp(-|v|)); e = exp(-|v|) for its derivative.
+__device__ __forceinline__ float softplus(float v, float &e) {
+    e = ex2(-fabsf(v) * kLog2e);
+    return fmaf(e, log1p_over(e), fmaxf(v, 0.f));
+}
+__device__ __forceinline__ float sigmoid(float z) { return rcp(1.f + ex2(-z * kLog2e)); }
+
+// Sums of v[j] over the LPC lanes of a channel, each sum left with the lane that owns token j: lane r owns tokens
+// r OWN .. r OWN + OWN - 1 of the eight (OWN = 8 / LPC; with 16 lanes, lanes r and r + 8 both own token r).  Halves are
+// exchanged, so that 8 sums over 4 lanes take 6 shuffles instead of 16.
+template <int LPC>
+__device__ __forceinline__ void quad_sums(float (&v)[8], int lane) {
+    int n = 8;
+    if (LPC == 16) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 8);
+    }
+#pragma unroll
+    for (int m = (LPC == 16 ? 4 : LPC / 2); m >= 1; m >>= 1) {
+        n >>= 1;
+        const bool up = lane & m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) {
+                const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+                v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+            }
+    }
+}
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *dst, const void *src, bool there) {   // zeros where not there
+    const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
+    static_assert(BYTES == 16, "16 bytes a copy");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Eight elements (16 or 32 bytes) as float32 to shared memory.
+__device__ __forceinline__ void widen16(float *dst, const __nv_bfloat16 *src) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(src);
+    auto lo = [](unsigned w) { return __uint_as_float(w << 16); };
+    auto hi = [](unsigned w) { return __uint_as_float(w & 0xffff0000u); };
+    *reinterpret_cast<float4 *>(dst) = make_float4(lo(v.x), hi(v.x), lo(v.y), hi(v.y));
+    *reinterpret_cast<float4 *>(dst + 4) = make_float4(lo(v.z), hi(v.z), lo(v.w), hi(v.w));
+}
+__device__ __forceinline__ void widen16(float *dst, const float *src) {
+    *reinterpret_cast<float4 *>(dst) = *reinterpret_cast<const float4 *>(src);
+}
+
+#endif
+
+}  // namespace la

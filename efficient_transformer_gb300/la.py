@@ -53,6 +53,19 @@ class LaQkArgs(ctypes.Structure):
                 ("inv_freq", ctypes.c_void_p)]
 
 
+class LaSsmArgs(ctypes.Structure):
+    """la_ssm_args: inputs of la_ssm_*."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "dt", "B", "C", "z", "A", "skip", "dt_bias", "initial_state", "lengths")] + \
+        [(n + "_strides", ctypes.POINTER(LaStrides)) for n in ("x", "dt", "B", "C", "z")] + \
+        [(n, ctypes.c_int) for n in ("batch", "N", "E", "S", "G", "dtype", "softplus")]
+
+
+class LaSsmGrads(ctypes.Structure):
+    """la_ssm_grads: outputs of la_ssm_bwd."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dx", "ddt", "dB", "dC", "dz", "dA", "dskip", "ddt_bias",
+                                               "grad_initial_state")]
+
+
 class LinearAttentionError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -128,6 +141,25 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.la_qk_norm_rope_workspace_size.restype = sz
     lib.la_qk_norm_rope_bwd.argtypes = [vp] * 8 + [i] * 6 + [sp, sp, sp, sp, qp, vp, sz, vp]
     lib.la_qk_norm_rope_bwd.restype = i
+    lib.la_conv_fwd.argtypes = [vp] * 7 + [i] * 7 + [sp, vp]
+    lib.la_conv_fwd.restype = i
+    lib.la_conv_workspace_size.argtypes = [i] * 5
+    lib.la_conv_workspace_size.restype = sz
+    lib.la_conv_bwd.argtypes = [vp] * 11 + [i] * 7 + [sp, sp, vp, sz, vp]
+    lib.la_conv_bwd.restype = i
+    lib.la_conv_step.argtypes = [vp] * 7 + [i] * 7 + [sp, vp]
+    lib.la_conv_step.restype = i
+    ap, gp = ctypes.POINTER(LaSsmArgs), ctypes.POINTER(LaSsmGrads)
+    lib.la_ssm_workspace_size.argtypes = [i] * 7
+    lib.la_ssm_workspace_size.restype = sz
+    lib.la_ssm_states_size.argtypes = [i] * 4
+    lib.la_ssm_states_size.restype = sz
+    lib.la_ssm_fwd.argtypes = [ap, vp, vp, vp, sz, vp, sz, vp]
+    lib.la_ssm_fwd.restype = i
+    lib.la_ssm_bwd.argtypes = [ap, vp, sp, vp, vp, sz, gp, vp, sz, vp]
+    lib.la_ssm_bwd.restype = i
+    lib.la_ssm_step.argtypes = [ap, vp, vp, vp, vp, i, vp]
+    lib.la_ssm_step.restype = i
     lib.la_trace_start.argtypes = []
     lib.la_trace_start.restype = i
     lib.la_trace_stop.argtypes = []
@@ -142,8 +174,13 @@ def load(path: str | None = None) -> ctypes.CDLL:
     return lib
 
 
+_SIZES = {"la_conv": "W must be 2, 3 or 4, E a multiple of 8", "la_ssm": "S must be 8, 16, 32 or 64, E / G a multiple of 8"}
+
+
 def _raise(lib, status: int, call: str):
     what = lib.la_status_str(status).decode()
+    if status == LA_ERR_UNSUPPORTED and call.rsplit("_", 1)[0] in _SIZES:
+        what = "unsupported sizes: " + _SIZES[call.rsplit("_", 1)[0]]
     if status == LA_ERR_CUDA:
         what += ": " + lib.la_last_cuda_error().decode()
     raise LinearAttentionError(status, f"{call}: {what}")
@@ -794,6 +831,310 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, grad_q: torch.Tensor, gra
     if st != LA_OK:
         _raise(lib, st, "la_qk_norm_rope_bwd")
     return dq, dk, dqw, dkw
+
+
+# ---- short causal convolution and selective state space scan -----------------------------------
+
+def _check_tokens(name, t, shape, like):
+    """A tensor [B, N, ..] of x's type on x's device, its last dimension contiguous."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != like.get_device() or t.get_device() < 0:
+        raise ValueError(f"{name} must be a CUDA tensor on x's device")
+    if t.dtype is not like.dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, x has {like.dtype}")
+    if t.shape != shape or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be a tensor {tuple(shape)} whose last dimension is contiguous, got {tuple(t.shape)}")
+
+
+def _tokens_of(x):
+    """(B, N, E) of x, checked."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise ValueError("x must be a CUDA tensor [B, N, E]")
+    _check_tokens("x", x, x.shape, x)
+    return x.shape
+
+
+def _token_strides(t):
+    return None if t.is_contiguous() else _strides_of(t.stride(0), t.stride(2) if t.dim() == 4 else 0, t.stride(1))
+
+
+def _check_dense(name, t, shape, dtype, like):
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != like.get_device() \
+            or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on x's device")
+
+
+def _conv_args(x, weight, bias):
+    """(B, N, E, W, dtype code, weight's dtype code)"""
+    B, N, E = _tokens_of(x)
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2 or weight.shape[0] != E or not weight.is_contiguous() \
+            or weight.get_device() != x.get_device():
+        raise ValueError(f"weight must be a contiguous tensor [{E}, W] on x's device")
+    if weight.dtype is not torch.float32 and weight.dtype is not x.dtype:
+        raise TypeError("weight must be float32 or of x's dtype")
+    if bias is not None:
+        _check_dense("bias", bias, (E,), weight.dtype, x)
+    return B, N, E, weight.shape[1], _dtype_code(x), LA_F32 if weight.dtype is torch.float32 else LA_BF16
+
+
+def conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, *, silu: bool = True,
+             initial_state: torch.Tensor | None = None, final_state: torch.Tensor | None = None,
+             lengths: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Short causal convolution of every channel (``la_conv_fwd``): x [B, N, E], weight [E, W] (W 2 to 4, float32 or x's
+    dtype, bias [E] like it), out_t = silu(bias + sum_j weight[:, j] x_(t - W + 1 + j)), without the silu on request.
+
+    ``initial_state`` ([B, W - 1, E], x's dtype) holds the rows before the first token, ``final_state`` receives the last
+    W - 1; they may be the same tensor.  ``lengths`` (int32 [B]): tokens of each sequence; out rows past them are zeros and what
+    x holds there is not used.  Returns ``out`` [B, N, E]."""
+    lib = load()
+    B, N, E, W, dt, wdt = _conv_args(x, weight, bias)
+    raw = _check_device(x, stream)
+    if lengths is not None:
+        _check_dense("lengths", lengths, (B,), torch.int32, x)
+    for name, t in (("initial_state", initial_state), ("final_state", final_state)):
+        if t is not None:
+            _check_dense(name, t, (B, W - 1, E), x.dtype, x)
+    with _memory_on(stream):
+        out = _output("out", out, (B, N, E), x)
+    if stream is not None:
+        _keep(stream, (out,), (x, weight, bias, initial_state, final_state, lengths))
+    st = lib.la_conv_fwd(x.data_ptr(), weight.data_ptr(), _addr(bias), out.data_ptr(), _addr(initial_state),
+                         _addr(final_state), _addr(lengths), B, N, E, W, dt, wdt, silu, _token_strides(x), raw)
+    if st != LA_OK:
+        _raise(lib, st, "la_conv_fwd")
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def _conv_need(B, N, E, W, dt):
+    return int(load().la_conv_workspace_size(B, N, E, W, dt))
+
+
+def conv_workspace_size(B, N, E, W, dtype: torch.dtype) -> int:
+    """Bytes of workspace of ``conv_bwd``."""
+    return _conv_need(B, N, E, W, LA_F32 if dtype == torch.float32 else LA_BF16)
+
+
+def conv_bwd(x: torch.Tensor, weight: torch.Tensor, grad_out: torch.Tensor, bias: torch.Tensor | None = None, *,
+             silu: bool = True, initial_state: torch.Tensor | None = None, grad_final_state: torch.Tensor | None = None,
+             grad_initial_state: torch.Tensor | None = None, lengths: torch.Tensor | None = None,
+             dx: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Gradient of ``conv_fwd`` (``la_conv_bwd``): returns ``(dx, dweight, dbias)``, dbias None without a bias.
+    ``grad_final_state`` is the gradient of the final state (None: zeros); ``grad_initial_state``, when given, receives
+    the initial state's (both of x's dtype)."""
+    lib = load()
+    B, N, E, W, dt, wdt = _conv_args(x, weight, bias)
+    _check_tokens("grad_out", grad_out, x.shape, x)
+    raw = _check_device(x, stream)
+    if lengths is not None:
+        _check_dense("lengths", lengths, (B,), torch.int32, x)
+    for name, t in (("initial_state", initial_state), ("grad_final_state", grad_final_state),
+                    ("grad_initial_state", grad_initial_state)):
+        if t is not None:
+            _check_dense(name, t, (B, W - 1, E), x.dtype, x)
+    with _memory_on(stream):
+        dx = _output("dx", dx, (B, N, E), x)
+        dw = torch.empty_like(weight)
+        db = torch.empty_like(bias) if bias is not None else None
+        ws = _workspace(_conv_need(B, N, E, W, dt), x.device, workspace)
+    if stream is not None:
+        _keep(stream, (dx, dw, db), (x, weight, bias, grad_out, initial_state, grad_final_state, grad_initial_state, lengths,
+                                     workspace))
+    st = lib.la_conv_bwd(x.data_ptr(), weight.data_ptr(), _addr(bias), grad_out.data_ptr(), dx.data_ptr(), dw.data_ptr(),
+                         _addr(db), _addr(initial_state), _addr(grad_final_state), _addr(grad_initial_state), _addr(lengths),
+                         B, N, E, W, dt, wdt, silu, _token_strides(x), _token_strides(grad_out), _addr(ws), _nbytes(ws), raw)
+    if st != LA_OK:
+        _raise(lib, st, "la_conv_bwd")
+    return dx, dw, db
+
+
+def conv_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, *,
+              silu: bool = True, slots: torch.Tensor | None = None, state_out: torch.Tensor | None = None,
+              out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """One token of each sequence through the convolution (``la_conv_step``): x [B, 1, E] on a pool of states ``state``
+    ([pool, W - 1, E], x's dtype); slots, padding and ``state_out`` as in ``decay_step``.  Returns ``out`` [B, 1, E]."""
+    lib = load()
+    B, N, E, W, dt, wdt = _conv_args(x, weight, bias)
+    raw = _check_device(x, stream)
+    if N != 1:
+        raise ValueError(f"conv_step takes one token per sequence (N = 1), got N = {N}")
+    if slots is not None:
+        _check_dense("slots", slots, (B,), torch.int32, x)
+    pool = state.shape[0] if isinstance(state, torch.Tensor) and state.dim() == 3 else 0
+    _check_dense("state", state, (pool, W - 1, E), x.dtype, x)
+    if state_out is not None:
+        _check_dense("state_out", state_out, (pool, W - 1, E), x.dtype, x)
+    with _memory_on(stream):
+        out = _output("out", out, (B, 1, E), x)
+    if stream is not None:
+        _keep(stream, (out,), (x, state, weight, bias, slots, state_out))
+    st = lib.la_conv_step(x.data_ptr(), weight.data_ptr(), _addr(bias), out.data_ptr(), state.data_ptr(),
+                          (state if state_out is None else state_out).data_ptr(), _addr(slots), pool, B, E, W, dt, wdt, silu,
+                          _token_strides(x), raw)
+    if st != LA_OK:
+        _raise(lib, st, "la_conv_step")
+    return out
+
+
+def _ssm_args(x, dt, A, B, C, skip, z, dt_bias, softplus, initial_state=None, lengths=None):
+    """la_ssm_args of a call, checked."""
+    nB, N, E = _tokens_of(x)
+    _check_tokens("dt", dt, x.shape, x)
+    if not isinstance(B, torch.Tensor) or B.dim() != 4:
+        raise ValueError("B must be a CUDA tensor [B, N, G, S]")
+    G, S = B.shape[2:]
+    _check_tokens("B", B, (nB, N, G, S), x)
+    _check_tokens("C", C, (nB, N, G, S), x)
+    _check_dense("A", A, (E, S), torch.float32, x)
+    a = LaSsmArgs(x.data_ptr(), dt.data_ptr(), B.data_ptr(), C.data_ptr(), None, A.data_ptr())
+    a.x_strides, a.dt_strides, a.B_strides, a.C_strides = _token_strides(x), _token_strides(dt), _token_strides(B), _token_strides(C)
+    if z is not None:
+        _check_tokens("z", z, x.shape, x)
+        a.z, a.z_strides = z.data_ptr(), _token_strides(z)
+    if skip is not None:
+        _check_dense("skip", skip, (E,), torch.float32, x)
+        a.skip = skip.data_ptr()
+    if dt_bias is not None:
+        _check_dense("dt_bias", dt_bias, (E,), torch.float32, x)
+        a.dt_bias = dt_bias.data_ptr()
+    if initial_state is not None:
+        _check_dense("initial_state", initial_state, (nB, E, S), torch.float32, x)
+        a.initial_state = initial_state.data_ptr()
+    if lengths is not None:
+        _check_dense("lengths", lengths, (nB,), torch.int32, x)
+        a.lengths = lengths.data_ptr()
+    a.batch, a.N, a.E, a.S, a.G, a.dtype, a.softplus = nB, N, E, S, G, _dtype_code(x), softplus
+    return a, nB, N, E, S, G
+
+
+@functools.lru_cache(maxsize=256)
+def _ssm_need(B, N, E, S, G, dt, is_bwd):
+    return int(load().la_ssm_workspace_size(B, N, E, S, G, dt, is_bwd))
+
+
+def ssm_workspace_size(B, N, E, S, G, dtype: torch.dtype, is_bwd: bool) -> int:
+    """Bytes of workspace of ``ssm_fwd``, or of ``ssm_bwd`` (enough for both)."""
+    return _ssm_need(B, N, E, S, G, LA_F32 if dtype == torch.float32 else LA_BF16, int(is_bwd))
+
+
+@functools.lru_cache(maxsize=256)
+def ssm_states_size(B, N, E, S) -> int:
+    """Bytes of the states that ``ssm_fwd(..., states=)`` keeps for ``ssm_bwd``."""
+    return int(load().la_ssm_states_size(B, N, E, S))
+
+
+def _check_states(states, need, like):
+    if not isinstance(states, torch.Tensor) or states.get_device() != like.get_device() or not states.is_contiguous() \
+            or _nbytes(states) < need:
+        raise ValueError(f"states must be a contiguous CUDA tensor of at least {need} bytes on x's device")
+
+
+def ssm_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, *,
+            skip: torch.Tensor | None = None, z: torch.Tensor | None = None, dt_bias: torch.Tensor | None = None,
+            softplus: bool = True, initial_state: torch.Tensor | None = None, final_state: torch.Tensor | None = None,
+            lengths: torch.Tensor | None = None, states: torch.Tensor | None = None, out: torch.Tensor | None = None,
+            workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Selective state space scan, for prompts and training (``la_ssm_fwd``): d_t = softplus(dt_t + dt_bias),
+    h_t = exp(d_t A) h_(t-1) + d_t x_t B_t, out_t = (C_t . h_t + skip x_t) silu(z_t).
+
+    x, dt, z [B, N, E] (z None: no gate); B, C [B, N, G, S], shared by the E / G channels of a group; A [E, S], skip and
+    dt_bias [E] float32.  ``softplus=False``: d_t = dt_t + dt_bias.  ``initial_state`` (float32 [B, E, S]) is h before the first
+    token, ``final_state`` receives h after the last; they may be the same tensor.  ``lengths`` (int32 [B]): tokens of each
+    sequence; out rows past them are zeros and what the inputs hold there is not used.  ``states`` (at least
+    ``ssm_states_size`` bytes) keeps what ``ssm_bwd`` needs.  Returns ``out`` [B, N, E].  Float32 arithmetic."""
+    lib = load()
+    a, nB, N, E, S, G = _ssm_args(x, dt, A, B, C, skip, z, dt_bias, softplus, initial_state, lengths)
+    raw = _check_device(x, stream)
+    if final_state is not None:
+        _check_dense("final_state", final_state, (nB, E, S), torch.float32, x)
+    if states is not None:
+        _check_states(states, ssm_states_size(nB, N, E, S), x)
+    with _memory_on(stream):
+        out = _output("out", out, (nB, N, E), x)
+        ws = _workspace(_ssm_need(nB, N, E, S, G, a.dtype, 0), x.device, workspace)
+    if stream is not None:
+        _keep(stream, (out,), (x, dt, A, B, C, skip, z, dt_bias, initial_state, final_state, lengths, states, workspace))
+    st = lib.la_ssm_fwd(ctypes.byref(a), out.data_ptr(), _addr(final_state), _addr(states), _nbytes(states), _addr(ws),
+                        _nbytes(ws), raw)
+    if st != LA_OK:
+        _raise(lib, st, "la_ssm_fwd")
+    return out
+
+
+def ssm_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, grad_out: torch.Tensor,
+            *, skip: torch.Tensor | None = None, z: torch.Tensor | None = None, dt_bias: torch.Tensor | None = None,
+            softplus: bool = True, initial_state: torch.Tensor | None = None,
+            grad_final_state: torch.Tensor | None = None, grad_initial_state: torch.Tensor | None = None,
+            lengths: torch.Tensor | None = None, states: torch.Tensor | None = None,
+            workspace: torch.Tensor | None = None, stream=None):
+    """Gradient of ``ssm_fwd`` (``la_ssm_bwd``): returns ``(dx, ddt, dA, dB, dC, dskip, dz, ddt_bias)``; dskip, dz and
+    ddt_bias None without their inputs.  ``states``: those that ``ssm_fwd`` kept for these inputs (None: they are found
+    again first, one more pass).  ``grad_final_state`` is the gradient of the final state (None: zeros);
+    ``grad_initial_state``, when given, receives the initial state's."""
+    lib = load()
+    a, nB, N, E, S, G = _ssm_args(x, dt, A, B, C, skip, z, dt_bias, softplus, initial_state, lengths)
+    _check_tokens("grad_out", grad_out, x.shape, x)
+    raw = _check_device(x, stream)
+    for name, t in (("grad_final_state", grad_final_state), ("grad_initial_state", grad_initial_state)):
+        if t is not None:
+            _check_dense(name, t, (nB, E, S), torch.float32, x)
+    need = ssm_states_size(nB, N, E, S)
+    given = states
+    if states is not None:
+        _check_states(states, need, x)
+    f4 = torch.float32
+    with _memory_on(stream):
+        dx, ddt = _output("dx", None, (nB, N, E), x), _output("ddt", None, (nB, N, E), x)
+        dz = _output("dz", None, (nB, N, E), x) if z is not None else None
+        dB, dC = (torch.empty((nB, N, G, S), dtype=x.dtype, device=x.device) for _ in range(2))
+        dA = torch.empty((E, S), dtype=f4, device=x.device)
+        dskip = torch.empty((E,), dtype=f4, device=x.device) if skip is not None else None
+        dbias = torch.empty((E,), dtype=f4, device=x.device) if dt_bias is not None else None
+        ws = _workspace(_ssm_need(nB, N, E, S, G, a.dtype, 1), x.device, workspace)
+        if states is None:
+            states = torch.empty((need,), dtype=torch.uint8, device=x.device)
+    if stream is not None:
+        _keep(stream, (dx, ddt, dA, dB, dC, dskip, dz, dbias),
+              (x, dt, A, B, C, grad_out, skip, z, dt_bias, initial_state, grad_final_state, grad_initial_state, lengths, given,
+               workspace))
+    if given is None:
+        st = lib.la_ssm_fwd(ctypes.byref(a), None, None, states.data_ptr(), need, _addr(ws), _nbytes(ws), raw)
+        if st != LA_OK:
+            _raise(lib, st, "la_ssm_fwd")
+    g = LaSsmGrads(dx.data_ptr(), ddt.data_ptr(), dB.data_ptr(), dC.data_ptr(), _addr(dz), dA.data_ptr(), _addr(dskip),
+                   _addr(dbias), _addr(grad_initial_state))
+    st = lib.la_ssm_bwd(ctypes.byref(a), grad_out.data_ptr(), _token_strides(grad_out), _addr(grad_final_state),
+                        states.data_ptr(), _nbytes(states), ctypes.byref(g), _addr(ws), _nbytes(ws), raw)
+    if st != LA_OK:
+        _raise(lib, st, "la_ssm_bwd")
+    return dx, ddt, dA, dB, dC, dskip, dz, dbias
+
+
+def ssm_step(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, state: torch.Tensor, *,
+             skip: torch.Tensor | None = None, z: torch.Tensor | None = None, dt_bias: torch.Tensor | None = None,
+             softplus: bool = True, slots: torch.Tensor | None = None, state_out: torch.Tensor | None = None,
+             out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """One token of each sequence through the scan (``la_ssm_step``): x, dt, z [B, 1, E], B, C [B, 1, G, S] on a pool of
+    states ``state`` (float32 [pool, E, S]); slots, padding and ``state_out`` as in ``decay_step``.  Returns ``out`` [B, 1, E]."""
+    lib = load()
+    a, nB, N, E, S, G = _ssm_args(x, dt, A, B, C, skip, z, dt_bias, softplus)
+    raw = _check_device(x, stream)
+    if N != 1:
+        raise ValueError(f"ssm_step takes one token per sequence (N = 1), got N = {N}")
+    if slots is not None:
+        _check_dense("slots", slots, (nB,), torch.int32, x)
+    pool = state.shape[0] if isinstance(state, torch.Tensor) and state.dim() == 3 else 0
+    _check_dense("state", state, (pool, E, S), torch.float32, x)
+    if state_out is not None:
+        _check_dense("state_out", state_out, (pool, E, S), torch.float32, x)
+    with _memory_on(stream):
+        out = _output("out", out, (nB, 1, E), x)
+    if stream is not None:
+        _keep(stream, (out,), (x, dt, A, B, C, state, skip, z, dt_bias, slots, state_out))
+    st = lib.la_ssm_step(ctypes.byref(a), out.data_ptr(), state.data_ptr(), (state if state_out is None else state_out).data_ptr(),
+                         _addr(slots), pool, raw)
+    if st != LA_OK:
+        _raise(lib, st, "la_ssm_step")
+    return out
 
 
 def get_status(stream=None) -> None:

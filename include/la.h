@@ -395,6 +395,103 @@ la_status la_qk_norm_rope_bwd(const void *q, const void *k, const void *grad_q, 
                               const la_strides *gk_strides, const la_qk_args *args, void *workspace, size_t ws_bytes,
                               void *stream);
 
+/* ---- short causal convolution ---------------------------------------------------------------
+ *
+ * Each channel e of x [B, N, E] alone, with W taps (2 to 4):
+ *
+ *   v_t = bias + sum_j weight[e][j] x_(t - W + 1 + j),    out_t = v_t sigmoid(v_t)   (silu = 0: v_t)
+ *
+ * Rows before the first token are the initial state's, [B, W - 1, E] of x's type, the oldest first (NULL:
+ * zeros); the final state is the last W - 1 rows, of the initial state where there are fewer, and may be the
+ * same buffer.  weight [E, W], bias [E] (NULL: none): float32, or x's type (weight_dtype).  E a multiple of 8.
+ * lengths: NULL, or B device int32: sequence b has min(max(lengths[b], 0), N) tokens; rows past them are not
+ * used, whatever they hold, and their out rows are zeros.  x may be strided (la_strides, h not used: NULL
+ * contiguous; 16-byte rows, i.e. multiples of 8 bfloat16 or 4 float32 elements, else LA_ERR_ALIGN; 0 along a broadcast
+ * dimension).  Outputs are contiguous and overlap no input but for the states named.  Float32 arithmetic, one
+ * rounding of an output.  The pages have no counterpart of these entry points; ownership, streams and errors
+ * are la_fwd's (LA_ERR_UNSUPPORTED: W or E); every pointer is 16-byte aligned, lengths and slots 4. */
+la_status la_conv_fwd(const void *x, const void *weight, const void *bias, void *out, const void *initial_state,
+                      void *final_state, const int *lengths, int B, int N, int E, int W, la_dtype dtype,
+                      la_dtype weight_dtype, int silu, const la_strides *x_strides, void *stream);
+
+/* Bytes of workspace of la_conv_bwd; 0 for arguments that it rejects.  Host-only. */
+size_t la_conv_workspace_size(int B, int N, int E, int W, la_dtype dtype);
+
+/* Exact gradient: dx [B, N, E] (rows past a length: zeros), dweight [E, W] and, where not NULL, dbias [E] (which needs a
+ * bias), of the weight's type, and, where not NULL, grad_initial_state [B, W - 1, E] of x's type, which may be none of
+ * the inputs (LA_ERR_ARG).  grad_final_state: the gradient of the final state, or NULL (zeros).  Sums over tokens are
+ * taken in float32 in a fixed order. */
+la_status la_conv_bwd(const void *x, const void *weight, const void *bias, const void *grad_out, void *dx, void *dweight,
+                      void *dbias, const void *initial_state, const void *grad_final_state, void *grad_initial_state,
+                      const int *lengths, int B, int N, int E, int W, la_dtype dtype, la_dtype weight_dtype, int silu,
+                      const la_strides *x_strides, const la_strides *g_strides, void *workspace, size_t ws_bytes,
+                      void *stream);
+
+/* One token per sequence, x and out [B, 1, E], on a pool of states [pool, W - 1, E] of x's type: sequence b owns slot
+ * slots[b] (device int32; NULL: slot b), whose rows move up by one into state_out at the same slot (which may be
+ * `state`: in place; slots that no sequence names are not touched).  A slot outside [0, pool) is a padding row: out
+ * zeros, no state touched.  Two sequences of one call must not name the same slot. */
+la_status la_conv_step(const void *x, const void *weight, const void *bias, void *out, const void *state, void *state_out,
+                       const int *slots, int pool, int B, int E, int W, la_dtype dtype, la_dtype weight_dtype, int silu,
+                       const la_strides *x_strides, void *stream);
+
+/* ---- selective state space scan ---------------------------------------------------------------
+ *
+ * Every channel e of x [B, N, E] has S states (8, 16, 32 or 64) that decay by a factor of their own with every token:
+ *
+ *   d_t = softplus(dt_t + dt_bias)            (softplus = 0: dt_t + dt_bias)
+ *   h_t = exp(d_t A) h_(t-1) + d_t x_t B_t,   out_t = (C_t . h_t + skip x_t) z_t sigmoid(z_t)
+ *
+ * x, dt, z, out [B, N, E] (z NULL: no gate); B, C [B, N, G, S], read by the E / G channels of a group in turn (E / G a
+ * multiple of 8); A [E, S], skip [E], dt_bias [E] float32 (skip, dt_bias NULL: zeros).  A is finite, expected < 0;
+ * other values grow the states by the same formula.  Inputs may be strided (la_strides; h is the step of B's and C's groups, not
+ * used by the others; every stride a multiple of 16 bytes, else LA_ERR_ALIGN); outputs are contiguous and overlap no
+ * input but for the states named.  States are float32 [B, E, S]: initial_state (NULL: zeros) comes in, the final one,
+ * after each sequence's last token, goes out and may be the same buffer.  lengths: as la_conv_fwd's.
+ *
+ * Arithmetic is float32 for both types, one rounding of an output; states and sums err by a few 2^-23 of their
+ * terms for each token that they remember.  A NaN or infinity in a token reaches what depends on it alone.  The pages have
+ * no counterpart of these entry points; ownership, streams and errors are la_fwd's (LA_ERR_UNSUPPORTED: S or E / G);
+ * every pointer is 16-byte aligned but skip, dt_bias, lengths and slots (4 bytes). */
+typedef struct {
+    const void *x, *dt, *B, *C, *z;
+    const float *A, *skip, *dt_bias, *initial_state;
+    const int *lengths;
+    const la_strides *x_strides, *dt_strides, *B_strides, *C_strides, *z_strides;   /* host; NULL: contiguous */
+    int batch, N, E, S, G;
+    la_dtype dtype;
+    int softplus;
+} la_ssm_args;
+
+/* Bytes of workspace of la_ssm_fwd (is_bwd = 0) or la_ssm_bwd (is_bwd = 1, enough for the forward too), and bytes of
+ * the states that a training forward keeps for its gradient (every eighth token's, float32); 0 for arguments that
+ * they reject (and where none is needed).  Host-only. */
+size_t la_ssm_workspace_size(int batch, int N, int E, int S, int G, la_dtype dtype, int is_bwd);
+size_t la_ssm_states_size(int batch, int N, int E, int S);
+
+/* Prompts and training.  out may be NULL where `states` is given: only these (and the final state) are computed.
+ * states: NULL, or states_bytes >= la_ssm_states_size (else LA_ERR_WORKSPACE), for la_ssm_bwd. */
+la_status la_ssm_fwd(const la_ssm_args *args, void *out, float *final_state, void *states, size_t states_bytes,
+                     void *workspace, size_t ws_bytes, void *stream);
+
+/* Exact gradient for grad_out [B, N, E] (strided like x) and grad_final_state [B, E, S] (NULL: zeros).  `states` are those
+ * that la_ssm_fwd left for the same args.  All of dx, ddt, dz [B, N, E] (dz with z only; rows past a length: zeros), dB, dC
+ * [B, N, G, S] and dA [E, S] are written; dskip, ddt_bias [E] and grad_initial_state [B, E, S] where not NULL (the first two need
+ * skip and dt_bias).  dA, dskip, ddt_bias and grad_initial_state are float32, the last may be none of the inputs
+ * (LA_ERR_ARG).  All sums are taken in float32 in a fixed order. */
+typedef struct {
+    void *dx, *ddt, *dB, *dC, *dz;
+    float *dA, *dskip, *ddt_bias, *grad_initial_state;
+} la_ssm_grads;
+la_status la_ssm_bwd(const la_ssm_args *args, const void *grad_out, const la_strides *g_strides,
+                     const float *grad_final_state, const void *states, size_t states_bytes, const la_ssm_grads *grads,
+                     void *workspace, size_t ws_bytes, void *stream);
+
+/* One token per sequence (args->N = 1; initial_state and lengths NULL) on a pool of states [pool, E, S]; slots, state_out
+ * and padding as in la_conv_step. */
+la_status la_ssm_step(const la_ssm_args *args, void *out, const float *state, float *state_out, const int *slots, int pool,
+                      void *stream);
+
 /* Forward for callers that cannot allocate device memory.
  *
  * Some callers have no way to obtain scratch memory on the GPU: a plugin host that hands
