@@ -28,11 +28,11 @@ void cut(int N, long long blocks, long long slots, int least, int *seg_len, int 
     *nseg = (N + *seg_len - 1) / *seg_len;
 }
 
-SsmPlan make_plan(int nB, int N, int E, int S, int G, la_dtype dt, bool bwd) {
+SsmPlan make_plan(int nB, int N, int E, int S, int G, bool bwd) {
     SsmPlan pl{};
-    const int Eg = E / G, ch = bwd ? ssm_grad_channels(S, dt) : ssm_scan_channels(S);
+    const int Eg = E / G, ch = bwd ? ssm_grad_channels(S) : ssm_scan_channels(S);
     pl.blocks = (Eg + ch - 1) / ch;
-    cut(N, (long long)nB * G * pl.blocks, (bwd ? 3 : 6) * kPlanSms, 128, &pl.seg_len, &pl.nseg);
+    cut(N, (long long)nB * G * pl.blocks, (bwd ? 3 : 7) * kPlanSms, 128, &pl.seg_len, &pl.nseg);
     pl.parts = nB * pl.nseg;
     size_t at = 0;
     auto take = [&](size_t floats) {
@@ -119,9 +119,9 @@ extern "C" {
 
 size_t la_ssm_workspace_size(int batch, int N, int E, int S, int G, la_dtype dtype, int is_bwd) {
     if (check(batch, N, E, S, G, dtype) != LA_OK) return 0;
-    const size_t fwd = make_plan(batch, N, E, S, G, dtype, false).bytes;
+    const size_t fwd = make_plan(batch, N, E, S, G, false).bytes;
     if (!is_bwd) return fwd;
-    const size_t bwd = make_plan(batch, N, E, S, G, dtype, true).bytes;
+    const size_t bwd = make_plan(batch, N, E, S, G, true).bytes;
     return fwd > bwd ? fwd : bwd;
 }
 
@@ -139,7 +139,7 @@ la_status la_ssm_fwd(const la_ssm_args *a, void *out, float *final_state, void *
     for (const void *p : {(const void *)out, (const void *)final_state, (const void *)states})
         if (p && !aligned(p, 16)) return LA_ERR_ALIGN;
     if (states && states_bytes < states_bytes_of(a->batch, a->N, a->E, a->S)) return LA_ERR_WORKSPACE;
-    const SsmPlan pl = make_plan(a->batch, a->N, a->E, a->S, a->G, a->dtype, false);
+    const SsmPlan pl = make_plan(a->batch, a->N, a->E, a->S, a->G, false);
     if (pl.bytes > 0) {
         if (!workspace || ws_bytes < pl.bytes) return LA_ERR_WORKSPACE;
         if (!aligned(workspace, 256)) return LA_ERR_ALIGN;
@@ -173,7 +173,7 @@ la_status la_ssm_bwd(const la_ssm_args *a, const void *grad_out, const la_stride
     e = strides_of(g_strides, a->batch, a->N, 0, a->E, a->dtype, &sg);
     if (e != LA_OK) return e;
     if (states_bytes < states_bytes_of(a->batch, a->N, a->E, a->S)) return LA_ERR_WORKSPACE;
-    const SsmPlan pl = make_plan(a->batch, a->N, a->E, a->S, a->G, a->dtype, true);
+    const SsmPlan pl = make_plan(a->batch, a->N, a->E, a->S, a->G, true);
     if (!workspace || ws_bytes < pl.bytes) return LA_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return LA_ERR_ALIGN;
     SsmParams p = params_of(a, st, pl, workspace);

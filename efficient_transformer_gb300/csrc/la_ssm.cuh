@@ -21,7 +21,7 @@ struct SsmParams {
     const int *lengths;
     void *out;                       // scan; NULL: only the kept states (and the final one) are wanted
     float *fin;                      // final state or NULL
-    float *kept;                     // states at every kSsmTile tokens [B][tiles][E][S] (written by the scan, read by the gradient)
+    float *kept;                     // states at every kSsmTile tokens [B][tiles][S / 4][E][4] (written by the scan, read by the gradient)
     void *dx, *ddt, *dz;
     float *dinit;
     int nB, N, E, S, G, Eg, softplus;
@@ -58,7 +58,7 @@ cudaError_t ssm_grad(const SsmParams &p, la_dtype dt, cudaStream_t s);
 cudaError_t ssm_reduce(const SsmReduceParams &p, la_dtype dt, cudaStream_t s);
 cudaError_t ssm_step(const SsmStepParams &p, la_dtype dt, cudaStream_t s);
 int ssm_scan_channels(int S);    // channels of a block of the scan
-int ssm_grad_channels(int S, la_dtype dt);    // ... and of the gradient
+int ssm_grad_channels(int S);    // ... and of the gradient
 
 #ifdef __CUDACC__
 
@@ -118,40 +118,62 @@ __device__ __forceinline__ float log1p_over(float e) {
     a = fmaf(a, e, -0.4999990165233612f);
     return fmaf(a, e, 1.0f);
 }
+__device__ __forceinline__ F2 log1p_over(F2 e) {
+    F2 a = f2(-0.003243980696424842f);
+    a = fma2(a, e, f2(0.019851261749863625f));
+    a = fma2(a, e, f2(-0.056959159672260284f));
+    a = fma2(a, e, f2(0.10603617131710052f));
+    a = fma2(a, e, f2(-0.15305569767951965f));
+    a = fma2(a, e, f2(0.19675931334495544f));
+    a = fma2(a, e, f2(-0.24954132735729218f));
+    a = fma2(a, e, f2(0.3332996368408203f));
+    a = fma2(a, e, f2(-0.4999990165233612f));
+    return fma2(a, e, f2(1.0f));
+}
 // softplus(v) = max(v, 0) + log(1 + exp(-|v|)); e = exp(-|v|) for its derivative.
 __device__ __forceinline__ float softplus(float v, float &e) {
     e = ex2(-fabsf(v) * kLog2e);
     return fmaf(e, log1p_over(e), fmaxf(v, 0.f));
 }
+__device__ __forceinline__ F2 softplus(F2 v, F2 &e) {
+    e = F2{ex2(-fabsf(v.x) * kLog2e), ex2(-fabsf(v.y) * kLog2e)};
+    return fma2(e, log1p_over(e), F2{fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)});
+}
 __device__ __forceinline__ float sigmoid(float z) { return rcp(1.f + ex2(-z * kLog2e)); }
+__device__ __forceinline__ F2 sigmoid(F2 z) {
+    const F2 e = mul2(z, f2(-kLog2e)), s = add2(F2{ex2(e.x), ex2(e.y)}, f2(1.f));
+    return F2{rcp(s.x), rcp(s.y)};
+}
 
-// Sums of v[j] over the LPC lanes of a channel, each sum left with the lane that owns token j: lane r owns tokens
-// r OWN .. r OWN + OWN - 1 of the eight (OWN = 8 / LPC; with 16 lanes, lanes r and r + 8 both own token r).  Halves are
+// A warp's lanes: channel lane % CPW, part r = lane / CPW of its states (CPW = 32 / LPC): lanes of the same part are neighbours,
+// which makes their common loads of B and C 2 cycles of shared memory each instead of 4.
+//
+// Sums of v[j] over the LPC lanes of a channel, each sum left with the lane that owns token j: lane part r owns tokens
+// r OWN .. r OWN + OWN - 1 of the eight (OWN = 8 / LPC; with 16 parts, r and r + 8 both own token r).  Halves are
 // exchanged, so that 8 sums over 4 lanes take 6 shuffles instead of 16.
 template <int LPC>
-__device__ __forceinline__ void quad_sums(float (&v)[8], int lane) {
+__device__ __forceinline__ void part_sums(float (&v)[8], int lane) {
+    constexpr int CPW = 32 / LPC;
     int n = 8;
     if (LPC == 16) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 8);
+        for (int i = 0; i < 8; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 8 * CPW);
     }
 #pragma unroll
     for (int m = (LPC == 16 ? 4 : LPC / 2); m >= 1; m >>= 1) {
         n >>= 1;
-        const bool up = lane & m;
+        const bool up = lane & (m * CPW);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (i < n) {
                 const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
-                v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+                v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m * CPW);
             }
     }
 }
 
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void *dst, const void *src, bool there) {   // zeros where not there
+__device__ __forceinline__ void copy_async(void *dst, const void *src, bool there) {   // 16 bytes, zeros where not there
     const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
-    static_assert(BYTES == 16, "16 bytes a copy");
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }

@@ -17,37 +17,53 @@
 namespace la {
 namespace {
 
-constexpr int kAhead = 2, kStages = kAhead + 2;
+constexpr int kRing = 4;   // units (8 tokens of a warp's channels) in flight: one worked on, one leaving, two coming
 
 constexpr int warps_of(int S) { return S == 64 ? 8 : 4; }
-// (128 channels a block; 64 states of float32 rows: 64, what shared memory holds)
-constexpr int groups_of(int S, int bytes) { return S == 8 ? 2 : S == 16 || (S == 64 && bytes == 4) ? 4 : 8; }
+constexpr int groups_of(int S) { return S == 8 ? 2 : S == 16 ? 4 : 8; }   // channel groups of a warp (128 channels a block)
 
 template <typename T, int S>
 struct Shape {
     static constexpr int LPC = S / 4, CPW = 32 / LPC, NW = warps_of(S), THREADS = NW * 32, OWN = LPC < 8 ? 8 / LPC : 1;
-    static constexpr int CHK = NW * CPW, K = groups_of(S, (int)sizeof(T)), CH = CHK * K;
-    static constexpr int V = 16 / (int)sizeof(T);
-    static constexpr int ROW = CHK * (int)sizeof(T) + 16, XBYTES = K * 8 * ROW, BBYTES = 8 * S * (int)sizeof(T);
-    static constexpr int STAGE = 4 * XBYTES + 2 * BBYTES;                  // x, dt, z, g [K][8][CHK]; B, C [8][S]
+    static constexpr int CHK = NW * CPW, K = groups_of(S), CH = CHK * K;
+    // a warp's rows of 8 tokens come and go by copies of CB bytes
+    static constexpr int ROW = CPW * (int)sizeof(T), CB = ROW < 16 ? ROW : 16, PER = ROW / CB;
+    static constexpr int XBYTES = 8 * ROW, UNIT = 4 * XBYTES;              // x, dt, z, g
+    static constexpr int IN = (4 * 8 * PER + 31) / 32, OUT = (3 * 8 * PER + 31) / 32;   // copies of a lane
+    static constexpr int V = 16 / (int)sizeof(T), BV = S / V, NB = 8 * BV;
     static constexpr int WIDE = 8 * 2 * S;                                 // floats: B and C of a tile; a warp's dB and dC
-    static constexpr int KEEP = K * THREADS;                               // float4 each: P, dA; float2: dskip, ddt_bias
-    static constexpr int OFF_WIDE = kStages * STAGE, OFF_P = OFF_WIDE + 2 * WIDE * 4, OFF_A = OFF_P + KEEP * 16,
-                         OFF_E = OFF_A + KEEP * 16, OFF_RED = OFF_E + KEEP * 8, SMEM = OFF_RED + 2 * NW * WIDE * 4;
-    static_assert(SMEM <= 227 * 1024, "shared memory of a block");
+    static constexpr int KEEP = K * THREADS;                               // P, dA, A; sums for skip and dt_bias, bias and skip
+    static constexpr int OFF_WIDE = NW * kRing * UNIT, OFF_P = OFF_WIDE + 2 * WIDE * 4, OFF_DA = OFF_P + KEEP * 16,
+                         OFF_A = OFF_DA + KEEP * 16, OFF_E = OFF_A + KEEP * 16, OFF_RED = OFF_E + KEEP * 16,
+                         SMEM = OFF_RED + 2 * NW * WIDE * 4;
+    static_assert(SMEM <= 227 * 1024 && 2 * NB <= THREADS, "a block's shared memory and its copies of B and C");
 };
+
+template <int BYTES>
+__device__ __forceinline__ void copy_in(void *dst, const void *src, bool there) {
+    const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
+    if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(there ? 16 : 0) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(BYTES), "r"(there ? BYTES : 0) : "memory");
+}
+template <int BYTES>
+__device__ __forceinline__ void copy_out(void *dst, const void *src) {
+    if (BYTES == 16) *static_cast<uint4 *>(dst) = *static_cast<const uint4 *>(src);
+    else if (BYTES == 8) *static_cast<uint2 *>(dst) = *static_cast<const uint2 *>(src);
+    else *static_cast<unsigned *>(dst) = *static_cast<const unsigned *>(src);
+}
 
 template <typename T, int S>
 __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 3) k_ssm_grad(SsmParams p) {
     using H = Shape<T, S>;
-    constexpr int LPC = H::LPC, OWN = H::OWN, V = H::V, CHK = H::CHK, TH = H::THREADS;
+    constexpr int LPC = H::LPC, CPW = H::CPW, OWN = H::OWN, OP = OWN > 1 ? OWN / 2 : 1, CHK = H::CHK, TH = H::THREADS, CB = H::CB;
     extern __shared__ __align__(16) unsigned char smem[];
     float *wide = reinterpret_cast<float *>(smem + H::OFF_WIDE);
-    float4 *keep_P = reinterpret_cast<float4 *>(smem + H::OFF_P), *keep_A = reinterpret_cast<float4 *>(smem + H::OFF_A);
-    float2 *keep_e = reinterpret_cast<float2 *>(smem + H::OFF_E);
+    float4 *keep_P = reinterpret_cast<float4 *>(smem + H::OFF_P), *keep_dA = reinterpret_cast<float4 *>(smem + H::OFF_DA),
+           *keep_A = reinterpret_cast<float4 *>(smem + H::OFF_A), *keep_e = reinterpret_cast<float4 *>(smem + H::OFF_E);
     float *red = reinterpret_cast<float *>(smem + H::OFF_RED);
     pdl_wait();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane % LPC, mine = warp * H::CPW + lane / LPC;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane / CPW, chan = lane % CPW;
+    unsigned char *ring = smem + warp * kRing * H::UNIT;
     const int blocks = (p.Eg + H::CH - 1) / H::CH;
     unsigned idx = blockIdx.x;
     const int cb = idx % blocks;
@@ -56,99 +72,95 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 3) k_ssm_g
     idx /= p.G;
     const int seg = idx % p.nseg, b = idx / p.nseg;
     const int c0 = cb * H::CH, left = min(H::CH, p.Eg - c0), nk = (left + CHK - 1) / CHK;
-    const int e0 = grp * p.Eg + c0;
+    const int e0 = grp * p.Eg + c0, w0 = warp * CPW;                         // the warp's first channel of each group
     const int t0 = seg * p.seg_len, t1 = min(t0 + p.seg_len, p.N);
     const int len = p.lengths ? min(max(p.lengths[b], 0), p.N) : p.N;
-    const int te = min(t1, len), nt = te > t0 ? (te - t0 + 7) / 8 : 0;
+    const int te = min(t1, len), nt = te > t0 ? (te - t0 + 7) / 8 : 0, units = nt * nk;
     const bool gated = p.z != nullptr;
 
-    auto row = [&](const void *base, const Strides &st) {
-        return static_cast<const T *>(base) + b * st.b + (long long)t0 * st.n + e0;
-    };
-    const T *src[4] = {row(p.x, p.sx), row(p.dt, p.sdt), row(p.z, p.sz), row(p.g, p.sg)};
-    const long long step[4] = {p.sx.n, p.sdt.n, p.sz.n, p.sg.n};
-    const T *mat[2] = {static_cast<const T *>(p.B) + b * p.sB.b + (long long)t0 * p.sB.n + grp * p.sB.h,
-                       static_cast<const T *>(p.C) + b * p.sC.b + (long long)t0 * p.sC.n + grp * p.sC.h};
-    const long long mstep[2] = {p.sB.n, p.sC.n};
-
-    // tiles go from the last to the first: the i-th is tile nt - 1 - i
-    auto load = [&](int i) {
-        if (i < nt) {
-            unsigned char *st = smem + (i % kStages) * H::STAGE;
-            const int first = (nt - 1 - i) * 8;
-            constexpr int XV = CHK / V, PER = H::K * 8 * XV;
+    // A lane's copies: one place of every unit (row, tensor, piece of the row).  Tiles go from the last to the first, and in
+    // each the groups in turn; unit u is group u % nk of tile nt - 1 - u / nk.
+    const T *from[H::IN];
+    long long back[H::IN];
+    int in_row[H::IN];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (k == 2 && !gated) continue;
-                for (int v = tid; v < PER; v += TH) {
-                    const int t = v / XV % 8, kk = v / (8 * XV), c = kk * CHK + v % XV * V;
-                    const bool in = t0 + first + t < te && c < left;
-                    copy_async<16>(st + k * H::XBYTES + (kk * 8 + t) * H::ROW + v % XV * 16,
-                                   in ? src[k] + (long long)(first + t) * step[k] + c : src[k], in);
-                }
+    for (int q = 0; q < H::IN; ++q) {
+        const int v = lane + q * 32, m = v / (8 * H::PER), c = v % H::PER * (CB / (int)sizeof(T));
+        in_row[q] = v / H::PER % 8;
+        const void *base = m == 0 ? p.x : m == 1 ? p.dt : m == 2 ? p.z : p.g;
+        const Strides st = m == 0 ? p.sx : m == 1 ? p.sdt : m == 2 ? p.sz : p.sg;
+        back[q] = 8 * st.n;
+        from[q] = static_cast<const T *>(base ? base : p.x) + b * st.b + (t0 + (nt - 1) * 8 + (long long)in_row[q]) * st.n + e0 + w0 + c;
+        if (m > 3 || !base) in_row[q] = 1 << 30;
+    }
+    int load_k = 0, load_tile = nt - 1;
+    auto load = [&](int u) {
+        if (u < units) {
+            unsigned char *to = ring + (u % kRing) * H::UNIT + lane * CB;
+#pragma unroll
+            for (int q = 0; q < H::IN; ++q) {
+                const int c = load_k * CHK;
+                const bool in = t0 + load_tile * 8 + in_row[q] < te && c + w0 + (lane + q * 32) % H::PER * (CB / (int)sizeof(T)) < left;
+                if (4 * 8 * H::PER % 32 == 0 || lane + q * 32 < 4 * 8 * H::PER)
+                    copy_in<CB>(to + q * 32 * CB, in ? from[q] + c : static_cast<const T *>(p.x), in);
+                if (load_k + 1 == nk) from[q] -= back[q];
             }
-            constexpr int BV = S / V, BPER = 8 * BV;
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                for (int v = tid; v < BPER; v += TH) {
-                    const int t = v / BV, c = v % BV * V;
-                    const bool in = t0 + first + t < te;
-                    copy_async<16>(st + 4 * H::XBYTES + k * H::BBYTES + v * 16,
-                                   in ? mat[k] + (long long)(first + t) * mstep[k] + c : mat[k], in);
-                }
+            if (++load_k == nk) load_k = 0, --load_tile;
         }
         copy_commit();
     };
-    auto widen = [&](int i) {
-        if (i >= nt) return;
-        const unsigned char *st = smem + (i % kStages) * H::STAGE + 4 * H::XBYTES;
-        float *to = wide + (i & 1) * H::WIDE;
-        constexpr int BV = S / V, BPER = 8 * BV;
+    // the rows of dx, ddt and dz that a unit leaves in the places of x, dt and z
+    auto leave = [&](int u, int tile, int k) {
+        const unsigned char *at = ring + (u % kRing) * H::UNIT + lane * CB;
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            for (int v = tid; v < BPER; v += TH)
-                widen16(to + v / BV * (2 * S) + k * S + v % BV * V, reinterpret_cast<const T *>(st + k * H::BBYTES + v * 16));
-    };
-    // what a tile leaves behind: rows of dx, ddt and dz (in the places of x, dt and z), and its part of dB and dC
-    auto leave = [&](int i) {
-        if (i < 0) return;
-        const unsigned char *st = smem + (i % kStages) * H::STAGE;
-        const int first = t0 + (nt - 1 - i) * 8;
-        constexpr int XV = CHK / V, PER = H::K * 8 * XV;
-        T *const to[3] = {static_cast<T *>(p.dx), static_cast<T *>(p.ddt), static_cast<T *>(p.dz)};
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            if (k == 2 && !gated) continue;
-            T *out = to[k] + ((long long)b * p.N + first) * p.E + e0;
-            for (int v = tid; v < PER; v += TH) {
-                const int t = v / XV % 8, kk = v / (8 * XV), c = kk * CHK + v % XV * V;
-                if (first + t < te && c < left)
-                    *reinterpret_cast<uint4 *>(out + (long long)t * p.E + c) =
-                        *reinterpret_cast<const uint4 *>(st + k * H::XBYTES + (kk * 8 + t) * H::ROW + v % XV * 16);
-            }
+        for (int q = 0; q < H::OUT; ++q) {
+            const int v = lane + q * 32, m = v / (8 * H::PER), c = k * CHK + w0 + v % H::PER * (CB / (int)sizeof(T));
+            const int t = t0 + tile * 8 + v / H::PER % 8;
+            T *to = static_cast<T *>(m == 0 ? p.dx : m == 1 ? p.ddt : p.dz);
+            if (m < 3 && (m < 2 || gated) && t < te && c < left)
+                copy_out<CB>(to + ((long long)b * p.N + t) * p.E + e0 + c, at + q * 32 * CB);
         }
-        const float *from = red + (i & 1) * H::NW * H::WIDE;
+    };
+    // B and C of a tile: a copy a thread, through registers a tile ahead
+    const int bv = tid % H::NB;
+    const bool bthere = tid < 2 * H::NB;
+    const T *bfrom = static_cast<const T *>(tid < H::NB ? p.B : p.C);
+    const long long bstep = tid < H::NB ? p.sB.n : p.sC.n;
+    bfrom += b * (tid < H::NB ? p.sB.b : p.sC.b) + grp * (tid < H::NB ? p.sB.h : p.sC.h) + bv % H::BV * H::V;
+    alignas(16) T raw[H::V];
+    auto ask = [&](int i) {   // rows past the length: zeros
+        const int t = t0 + (nt - 1 - i) * 8 + bv / H::BV;
+        *reinterpret_cast<uint4 *>(raw) = bthere && i < nt && t < te ? *reinterpret_cast<const uint4 *>(bfrom + t * bstep) : make_uint4(0, 0, 0, 0);
+    };
+    auto widen = [&](int i) {
+        if (bthere) widen16(wide + (i & 1) * H::WIDE + bv / H::BV * (2 * S) + tid / H::NB * S + bv % H::BV * H::V, raw);
+    };
+    // a tile's part of dB and dC
+    auto leave_bc = [&](int i) {
+        if (i < 0) return;
+        const int first = t0 + (nt - 1 - i) * 8;
+        const float *a = red + (i & 1) * H::NW * H::WIDE;
         float *part = p.part_bc + (((size_t)(grp * blocks + cb) * p.nB + b) * p.N + first) * (2 * S);
         for (int v = tid; v < H::WIDE; v += TH) {
             float sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < H::NW; ++w) sum += from[w * H::WIDE + v];
+            for (int w = 0; w < H::NW; ++w) sum += a[w * H::WIDE + v];
             if (first + v / (2 * S) < te) part[v] = sum;
         }
     };
 
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) load(i);
-
+    load(0);
+    load(1);
+    ask(0);
     // P of the segment's end: the final state's gradient through the later segments
 #pragma unroll 1
     for (int k = 0; k < nk; ++k) {
-        const int c = k * CHK + mine;
+        const int c = k * CHK + w0 + chan;
         const bool there = c < left;
         const size_t e = e0 + (there ? c : 0);
         const float4 A = *reinterpret_cast<const float4 *>(p.A + e * S + 4 * r);
         float4 P = p.dfinal && there ? *reinterpret_cast<const float4 *>(p.dfinal + ((size_t)b * p.E + e) * S + 4 * r)
-                            : make_float4(0.f, 0.f, 0.f, 0.f);
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
         for (int j = p.nseg - 1; j > seg; --j) {
             const size_t w = ((size_t)b * p.nseg + j) * p.E + e;
             const float d = p.seg_d[w] * kLog2e;
@@ -157,28 +169,26 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 3) k_ssm_g
                             fmaf(ex2(d * A.w), P.w, R.w));
         }
         keep_P[k * TH + tid] = P;
-        keep_A[k * TH + tid] = make_float4(0.f, 0.f, 0.f, 0.f);
-        keep_e[k * TH + tid] = make_float2(0.f, 0.f);
+        keep_dA[k * TH + tid] = make_float4(0.f, 0.f, 0.f, 0.f);
+        keep_A[k * TH + tid] = make_float4(A.x * kLog2e, A.y * kLog2e, A.z * kLog2e, A.w * kLog2e);
+        keep_e[k * TH + tid] = make_float4(0.f, 0.f, p.dt_bias ? p.dt_bias[e] : 0.f, p.skip ? p.skip[e] : 0.f);
     }
-
-    copy_wait<kAhead - 1>();
-    __syncthreads();
     widen(0);
+    ask(1);
     const size_t kept0 = (size_t)b * ((p.N + kSsmTile - 1) / kSsmTile);
     auto kept = [&](int i, int k) {
-        const int c = k * CHK + mine;
-        const size_t w = (kept0 + t0 / 8 + nt - 1 - i) * p.E + e0 + c;
-        return c < left ? *reinterpret_cast<const float4 *>(p.kept + w * S + 4 * r) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const int c = k * CHK + w0 + chan;
+        const size_t w = ((kept0 + t0 / 8 + nt - 1 - i) * LPC + r) * p.E + e0 + c;
+        return c < left ? *reinterpret_cast<const float4 *>(p.kept + w * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
     };
     float4 h_next = make_float4(0.f, 0.f, 0.f, 0.f);
     if (nt > 0) h_next = kept(0, 0);
+    int u = 0;
     for (int i = 0; i < nt; ++i) {
-        copy_wait<kAhead - 2>();
-        __syncthreads();
-        leave(i - 1);
-        load(i + kAhead);
+        __syncthreads();   // the tile's B and C are whole, and the warps' dB and dC of the one before
+        leave_bc(i - 1);
         widen(i + 1);
-        unsigned char *st = smem + (i % kStages) * H::STAGE;
+        ask(i + 2);
         const float *bc = wide + (i & 1) * H::WIDE + 4 * r;
         const int first = t0 + (nt - 1 - i) * 8;
         F2 accB[8][2], accC[8][2];
@@ -187,116 +197,133 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 3) k_ssm_g
 #pragma unroll
             for (int m = 0; m < 2; ++m) accB[j][m] = accC[j][m] = f2(0.f);
 #pragma unroll 1
-        for (int k = 0; k < nk; ++k) {
-            const int c = k * CHK + mine;
-            const bool there = c < left;
-            const int e = e0 + (there ? c : 0);
+        for (int k = 0; k < nk; ++k, ++u) {
+            copy_wait<1>();
+            __syncwarp();   // the unit's rows have come; the last one's outputs are whole
+            if (u > 0) leave(u - 1, k > 0 ? nt - 1 - i : nt - i, k > 0 ? k - 1 : nk - 1);
+            load(u + 2);
+            unsigned char *st = ring + (u % kRing) * H::UNIT;
             const float4 h4 = h_next;
-            if (k + 1 < nk) h_next = kept(i, k + 1);
-            else if (i + 1 < nt) h_next = kept(i + 1, 0);
-            const float4 A4 = *reinterpret_cast<const float4 *>(p.A + (size_t)e * S + 4 * r);
-            const F2 A[2] = {F2{A4.x * kLog2e, A4.y * kLog2e}, F2{A4.z * kLog2e, A4.w * kLog2e}};
-            const float bias = p.dt_bias ? p.dt_bias[e] : 0.f, skip = p.skip ? p.skip[e] : 0.f;
-            // the lane's own tokens
-            float x[OWN], d[OWN], u[OWN], dy[OWN], slope[OWN], gz[OWN];
-            unsigned char *at0 = st + (k * 8 + (LPC == 16 ? r % 8 : r * OWN)) * H::ROW + mine * (int)sizeof(T);
-            const int own0 = first + (LPC == 16 ? r % 8 : r * OWN);
+            if (u + 1 < units) h_next = k + 1 < nk ? kept(i, k + 1) : kept(i + 1, 0);
+            float4 es = keep_e[k * TH + tid];
+            const float bias = es.z, skip = es.w;
+            // the lane's own tokens, in pairs (of one: it and itself)
+            F2 x[OP], d[OP], u2[OP], dy[OP], slope[OP], gz[OP];
+            const int own = LPC == 16 ? r % 8 : r * OWN;
+            unsigned char *at0 = st + own * H::ROW + chan * (int)sizeof(T);
 #pragma unroll
-            for (int o = 0; o < OWN; ++o) {
-                const unsigned char *at = at0 + o * H::ROW;
-                auto get = [&](int m) { return to_f32(*reinterpret_cast<const T *>(at + m * H::XBYTES)); };
+            for (int o = 0; o < OP; ++o) {
+                const unsigned char *at = at0 + 2 * o * H::ROW;
+                auto get = [&](int m) {
+                    const unsigned char *q = at + m * H::XBYTES;
+                    return F2{to_f32(*reinterpret_cast<const T *>(q)), to_f32(*reinterpret_cast<const T *>(q + (OWN > 1 ? H::ROW : 0)))};
+                };
                 x[o] = get(0);
-                const float v = get(1) + bias, g = get(3);
-                float sp = v;
-                slope[o] = 1.f;
+                const F2 v = add2(get(1), f2(bias)), g = get(3);
+                d[o] = v;
+                slope[o] = f2(1.f);
                 if (p.softplus) {
-                    float ev;
-                    sp = softplus(v, ev);
-                    const float s1 = rcp(1.f + ev);
-                    slope[o] = v >= 0.f ? s1 : ev * s1;
+                    F2 ev;
+                    d[o] = softplus(v, ev);
+                    const F2 s1 = add2(ev, f2(1.f)), q = F2{rcp(s1.x), rcp(s1.y)};
+                    slope[o] = mul2(q, F2{v.x >= 0.f ? 1.f : ev.x, v.y >= 0.f ? 1.f : ev.y});
                 }
-                const bool in = own0 + o < te;
-                d[o] = in ? sp : 0.f;
-                u[o] = d[o] * x[o];
+                if (first + 8 > te) {   // past the length: h stays as it is
+                    const int t = first + own + 2 * o;
+                    d[o] = F2{t < te ? d[o].x : 0.f, t + 1 < te ? d[o].y : 0.f};
+                    slope[o] = F2{t < te ? slope[o].x : 0.f, t + 1 < te ? slope[o].y : 0.f};
+                }
+                u2[o] = mul2(d[o], x[o]);
                 dy[o] = g;
-                gz[o] = 0.f;
+                gz[o] = f2(0.f);
                 if (gated) {
-                    const float z = get(2), sz = sigmoid(z);
-                    dy[o] = g * (z * sz);
-                    gz[o] = g * sz * fmaf(z, 1.f - sz, 1.f);
+                    const F2 z = get(2), sz = sigmoid(z), zs = mul2(z, sz);
+                    dy[o] = mul2(g, zs);
+                    // (z sigmoid(z))' = s (1 + z (1 - s)) = s + z s (1 - s)
+                    gz[o] = mul2(g, fma2(zs, F2{1.f - sz.x, 1.f - sz.y}, sz));
                 }
             }
-            auto all = [&](const float (&v)[OWN], int j) {   // token j's value, from the lane that owns it
-                return __shfl_sync(0xffffffffu, v[j % OWN], j / OWN, LPC);
+            auto all = [&](const F2 (&v)[OP], int j) {   // token j's value, from the lane that owns it
+                const int o = j % OWN;
+                return f2(__shfl_sync(0xffffffffu, o % 2 ? v[o / 2].y : v[o / 2].x, j / OWN * CPW + chan));
             };
-            // forward: h after each token, a beside it
-            F2 a[8][2], hs[8][2];
+            const float4 A4 = keep_A[k * TH + tid];
+            const F2 A[2] = {F2{A4.x, A4.y}, F2{A4.z, A4.w}};
+            // forward: h after each token
+            F2 hs[8][2];
             {
                 F2 h[2] = {F2{h4.x, h4.y}, F2{h4.z, h4.w}};
                 float y[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const F2 dj = f2(all(d, j)), uj = f2(all(u, j)), gj = f2(all(dy, j));
+                    const F2 dj = all(d, j), uj = all(u2, j), gj = all(dy, j);
                     const float4 B4 = *reinterpret_cast<const float4 *>(bc + j * 2 * S), C4 = *reinterpret_cast<const float4 *>(bc + j * 2 * S + S);
                     const F2 Bj[2] = {F2{B4.x, B4.y}, F2{B4.z, B4.w}}, Cj[2] = {F2{C4.x, C4.y}, F2{C4.z, C4.w}};
-                    F2 acc = f2(0.f);
+                    F2 acc;
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
-                        a[j][m] = ex22(mul2(dj, A[m]));
-                        h[m] = fma2(a[j][m], h[m], mul2(uj, Bj[m]));
+                        h[m] = fma2(ex22(mul2(dj, A[m])), h[m], mul2(uj, Bj[m]));
                         hs[j][m] = h[m];
                         accC[j][m] = fma2(gj, h[m], accC[j][m]);
-                        acc = fma2(Cj[m], h[m], acc);
+                        acc = m == 0 ? mul2(Cj[m], h[m]) : fma2(Cj[m], h[m], acc);
                     }
                     y[j] = acc.x + acc.y;
                 }
                 if (gated) {
-                    quad_sums<LPC>(y, lane);
+                    part_sums<LPC>(y, lane);
 #pragma unroll
-                    for (int o = 0; o < OWN; ++o)
-                        if (LPC < 16 || r < 8)
-                            *reinterpret_cast<T *>(at0 + o * H::ROW + 2 * H::XBYTES) = from_f32<T>(gz[o] * fmaf(skip, x[o], y[o]));
+                    for (int o = 0; o < OP; ++o) {
+                        const F2 dz = mul2(gz[o], fma2(f2(skip), x[o], F2{y[2 * o], OWN > 1 ? y[2 * o + 1] : y[2 * o]}));
+                        T *to = reinterpret_cast<T *>(at0 + 2 * o * H::ROW + 2 * H::XBYTES);
+                        if (LPC < 16 || r < 8) *to = from_f32<T>(dz.x);
+                        if (OWN > 1) *reinterpret_cast<T *>(reinterpret_cast<unsigned char *>(to) + H::ROW) = from_f32<T>(dz.y);
+                    }
                 }
             }
-            // and back
+            // and back; a is found again (keeping the eight tokens' would take 32 registers more, and spills)
             float du[8], dq[8];
-            const float4 P4 = keep_P[k * TH + tid], dA4 = keep_A[k * TH + tid];
+            const float4 P4 = keep_P[k * TH + tid], dA4 = keep_dA[k * TH + tid];
             F2 P[2] = {F2{P4.x, P4.y}, F2{P4.z, P4.w}}, dA[2] = {F2{dA4.x, dA4.y}, F2{dA4.z, dA4.w}};
 #pragma unroll
             for (int j = 7; j >= 0; --j) {
-                const F2 dj = f2(all(d, j)), uj = f2(all(u, j)), gj = f2(all(dy, j));
+                const F2 dj = all(d, j), uj = all(u2, j), gj = all(dy, j);
                 const float4 B4 = *reinterpret_cast<const float4 *>(bc + j * 2 * S), C4 = *reinterpret_cast<const float4 *>(bc + j * 2 * S + S);
                 const F2 Bj[2] = {F2{B4.x, B4.y}, F2{B4.z, B4.w}}, Cj[2] = {F2{C4.x, C4.y}, F2{C4.z, C4.w}};
-                F2 sb = f2(0.f), sq = f2(0.f);
+                F2 sb, sq;
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
                     const F2 before = j > 0 ? hs[j > 0 ? j - 1 : 0][m] : m == 0 ? F2{h4.x, h4.y} : F2{h4.z, h4.w};
                     const F2 G = fma2(Cj[m], gj, P[m]);
-                    sb = fma2(G, Bj[m], sb);
+                    sb = m == 0 ? mul2(G, Bj[m]) : fma2(G, Bj[m], sb);
                     accB[j][m] = fma2(G, uj, accB[j][m]);
-                    P[m] = mul2(a[j][m], G);
+                    P[m] = mul2(ex22(mul2(dj, A[m])), G);
                     const F2 q = mul2(P[m], before);
-                    sq = fma2(q, A[m], sq);
+                    sq = m == 0 ? mul2(q, A[m]) : fma2(q, A[m], sq);
                     dA[m] = fma2(q, dj, dA[m]);
                 }
                 du[j] = sb.x + sb.y;
                 dq[j] = sq.x + sq.y;
             }
             keep_P[k * TH + tid] = make_float4(P[0].x, P[0].y, P[1].x, P[1].y);
-            keep_A[k * TH + tid] = make_float4(dA[0].x, dA[0].y, dA[1].x, dA[1].y);
-            quad_sums<LPC>(du, lane);
-            quad_sums<LPC>(dq, lane);
-            float2 es = keep_e[k * TH + tid];
+            keep_dA[k * TH + tid] = make_float4(dA[0].x, dA[0].y, dA[1].x, dA[1].y);
+            part_sums<LPC>(du, lane);
+            part_sums<LPC>(dq, lane);
 #pragma unroll
-            for (int o = 0; o < OWN; ++o) {
-                const float dx = fmaf(d[o], du[o], skip * dy[o]);
-                // (past the length: d, x and dy are zeros, the sums over states are not)
-                const float ddt = own0 + o < te ? fmaf(x[o], du[o], kLn2 * dq[o]) * slope[o] : 0.f;
-                es.x = fmaf(dy[o], x[o], es.x);
-                es.y += ddt;
+            for (int o = 0; o < OP; ++o) {
+                const F2 s1 = F2{du[2 * o], OWN > 1 ? du[2 * o + 1] : du[2 * o]}, s2 = F2{dq[2 * o], OWN > 1 ? dq[2 * o + 1] : dq[2 * o]};
+                const F2 dx = fma2(d[o], s1, mul2(f2(skip), dy[o]));
+                // (past the length: d, x, dy and the slope are zeros, the sums over states are not)
+                const F2 ddt = mul2(fma2(x[o], s1, mul2(f2(kLn2), s2)), slope[o]), ey = mul2(dy[o], x[o]);
+                es.x += OWN > 1 ? ey.x + ey.y : ey.x;
+                es.y += OWN > 1 ? ddt.x + ddt.y : ddt.x;
+                unsigned char *at = at0 + 2 * o * H::ROW;
                 if (LPC < 16 || r < 8) {
-                    *reinterpret_cast<T *>(at0 + o * H::ROW) = from_f32<T>(dx);
-                    *reinterpret_cast<T *>(at0 + o * H::ROW + H::XBYTES) = from_f32<T>(ddt);
+                    *reinterpret_cast<T *>(at) = from_f32<T>(dx.x);
+                    *reinterpret_cast<T *>(at + H::XBYTES) = from_f32<T>(ddt.x);
+                }
+                if (OWN > 1) {
+                    *reinterpret_cast<T *>(at + H::ROW) = from_f32<T>(dx.y);
+                    *reinterpret_cast<T *>(at + H::ROW + H::XBYTES) = from_f32<T>(ddt.y);
                 }
             }
             keep_e[k * TH + tid] = es;
@@ -315,7 +342,7 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 3) k_ssm_g
             }
         int base = 0, n = 64;
 #pragma unroll
-        for (int m = 16; m >= LPC; m >>= 1) {
+        for (int m = CPW / 2; m >= 1; m >>= 1) {
             n >>= 1;
             const bool up = lane & m;
             base += up ? n : 0;
@@ -326,46 +353,45 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 3) k_ssm_g
                     v[q] = hold + __shfl_xor_sync(0xffffffffu, send, m);
                 }
         }
-        constexpr int LEFT = 64 / H::CPW;   // values a lane is left with
+        constexpr int LEFT = 64 / CPW;   // values a lane is left with
         float *to = red + ((i & 1) * H::NW + warp) * H::WIDE + 4 * r;
 #pragma unroll
         for (int q = 0; q < LEFT; q += 4) {
-            if (LEFT >= 4) {
-                const int w = base + q;
-                *reinterpret_cast<float4 *>(to + (w / 8) * 2 * S + (w % 8 / 4) * S) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
-            }
+            const int w = base + q;
+            *reinterpret_cast<float4 *>(to + (w / 8) * 2 * S + (w % 8 / 4) * S) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
         }
     }
     __syncthreads();
-    leave(nt - 1);
+    leave_bc(nt - 1);
+    if (units > 0) leave(units - 1, 0, nk - 1);
     // rows past the length
     {
-        constexpr int XV = H::CH / V;
+        constexpr int XV = H::CH / H::V;
         const int z0 = max(te, t0);
-        T *const to[3] = {static_cast<T *>(p.dx), static_cast<T *>(p.ddt), static_cast<T *>(p.dz)};
+        T *const rows[3] = {static_cast<T *>(p.dx), static_cast<T *>(p.ddt), static_cast<T *>(p.dz)};
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            if (k == 2 && !gated) continue;
-            T *out = to[k] + (long long)b * p.N * p.E + e0;
+        for (int m = 0; m < 3; ++m) {
+            if (m == 2 && !gated) continue;
+            T *out = rows[m] + (long long)b * p.N * p.E + e0;
             for (long long v = tid; v < (long long)(t1 - z0) * XV; v += TH) {
-                const int c = (int)(v % XV) * V;
+                const int c = (int)(v % XV) * H::V;
                 if (c < left) *reinterpret_cast<uint4 *>(out + (z0 + v / XV) * p.E + c) = make_uint4(0, 0, 0, 0);
             }
         }
     }
 #pragma unroll 1
     for (int k = 0; k < nk; ++k) {
-        const int c = k * CHK + mine;
+        const int c = k * CHK + w0 + chan;
         const bool there = c < left;
         const size_t e = e0 + (there ? c : 0), w = (size_t)b * p.nseg + seg;
-        float2 es = keep_e[k * TH + tid];
+        float4 es = keep_e[k * TH + tid];
 #pragma unroll
         for (int m = 1; m < (LPC == 16 ? 8 : LPC); m <<= 1) {
-            es.x += __shfl_xor_sync(0xffffffffu, es.x, m);
-            es.y += __shfl_xor_sync(0xffffffffu, es.y, m);
+            es.x += __shfl_xor_sync(0xffffffffu, es.x, m * CPW);
+            es.y += __shfl_xor_sync(0xffffffffu, es.y, m * CPW);
         }
         if (!there) continue;
-        *reinterpret_cast<float4 *>(p.part_A + (w * p.E + e) * S + 4 * r) = keep_A[k * TH + tid];
+        *reinterpret_cast<float4 *>(p.part_A + (w * p.E + e) * S + 4 * r) = keep_dA[k * TH + tid];
         if (r == 0) {
             p.part_e[(w * 2) * p.E + e] = es.x;
             p.part_e[(w * 2 + 1) * p.E + e] = es.y;
@@ -434,7 +460,7 @@ cudaError_t launch(const SsmParams &p, cudaStream_t s) {
 
 }  // namespace
 
-int ssm_grad_channels(int S, la_dtype dt) { return warps_of(S) * (32 / (S / 4)) * groups_of(S, dt == LA_BF16 ? 2 : 4); }
+int ssm_grad_channels(int S) { return warps_of(S) * (32 / (S / 4)) * groups_of(S); }
 
 cudaError_t ssm_grad(const SsmParams &p, la_dtype dt, cudaStream_t s) {
     if (dt == LA_BF16) {

@@ -4,7 +4,7 @@
 // The decay differs by channel, state and token, so there is no product for the tensor cores: a state costs 4 float
 // operations and one ex2 a token.  A warp holds 32 / LPC channels, the LPC lanes of a channel SPT states each, in registers.
 // A lane finds d, d x and the gate of OWN = 8 / LPC of every eight tokens (its "own"); they go to the channel's
-// lanes by shuffles, and the lanes' sums of C h come back to the owner by exchanged halves (quad_sums), so nothing of it
+// lanes by shuffles, and the lanes' sums of C h come back to the owner by exchanged halves (part_sums), so nothing of it
 // passes through shared memory.  Rows of x, dt, z, B and C come by asynchronous copies a few tiles ahead; B and C, which all
 // warps of a block read, are widened to float32 once a block.  Outputs replace the x that their lane alone has
 // read and leave as whole rows.
@@ -15,7 +15,7 @@ namespace {
 
 enum Mode { kScan = 0, kSums = 1, kReverse = 2 };
 
-constexpr int kWarps = 4, kThreads = kWarps * 32, kRows = 16, kAhead = 3, kStages = kAhead + 2;
+constexpr int kWarps = 4, kThreads = kWarps * 32, kRows = 16, kAhead = 2, kStages = kAhead + 2;
 
 constexpr int spt_of(int S) { return S <= 16 ? 4 : 8; }
 
@@ -28,6 +28,8 @@ struct Shape {
     static constexpr int ROW = CH * (int)sizeof(T) + 16, BROW = S * (int)sizeof(T);
     static constexpr int XBYTES = kRows * ROW, BBYTES = kRows * BROW;
     static constexpr int STAGE = TENSORS * XBYTES + MATS * BBYTES;
+    static constexpr int XV = CH / V, NX = kRows * XV, BV = S / V, NB = kRows * BV;   // copies of a row, of a tile
+    static constexpr int COPIES = (TENSORS * NX + MATS * NB + kThreads - 1) / kThreads;
     static constexpr int WIDE = kRows * MATS * S;                            // floats of a tile's B and C
     static constexpr int SMEM = kStages * STAGE + 2 * WIDE * 4;
 };
@@ -35,12 +37,12 @@ struct Shape {
 template <typename T, int S, int MODE>
 __global__ void __launch_bounds__(kThreads) k_ssm_scan(SsmParams p) {
     using H = Shape<T, S, MODE>;
-    constexpr int SPT = H::SPT, LPC = H::LPC, CH = H::CH, OWN = H::OWN, V = H::V, TENSORS = H::TENSORS, MATS = H::MATS;
-    constexpr int PAIRS = SPT / 2;
+    constexpr int SPT = H::SPT, LPC = H::LPC, CPW = H::CPW, CH = H::CH, OWN = H::OWN, V = H::V, TENSORS = H::TENSORS, MATS = H::MATS;
+    constexpr int PAIRS = SPT / 2, OP = OWN > 1 ? OWN / 2 : 1;               // pairs of own tokens (of one: it and itself)
     extern __shared__ __align__(16) unsigned char smem[];
     float *wide = reinterpret_cast<float *>(smem + kStages * H::STAGE);
     pdl_wait();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane % LPC;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane / CPW, chan = lane % CPW;
     const int tiles = (p.Eg + CH - 1) / CH;
     unsigned idx = blockIdx.x;
     const int ct = idx % tiles;
@@ -50,73 +52,93 @@ __global__ void __launch_bounds__(kThreads) k_ssm_scan(SsmParams p) {
     const int nsegs = MODE == kScan ? p.nseg : p.nseg - 1;                   // segments of this launch
     const int seg = idx % nsegs + (MODE == kReverse), b = idx / nsegs;
     const int c0 = ct * CH, left = min(CH, p.Eg - c0);                       // the block's channels of its group
-    const int mine = warp * H::CPW + lane / LPC;
+    const int mine = warp * CPW + chan;
     const bool there = mine < left;
     const int e = grp * p.Eg + c0 + (there ? mine : 0);
     const int t0 = seg * p.seg_len, t1 = min(t0 + p.seg_len, p.N);
     const int len = p.lengths ? min(max(p.lengths[b], 0), p.N) : p.N;
-    const int te = min(t1, len), nt = te > t0 ? (te - t0 + kRows - 1) / kRows : 0;
-
-    auto row = [&](const void *base, const Strides &st) {
-        return static_cast<const T *>(base) + b * st.b + (long long)t0 * st.n + grp * p.Eg + c0;
-    };
-    const T *src[3] = {row(MODE == kReverse ? p.g : p.x, MODE == kReverse ? p.sg : p.sx), row(p.dt, p.sdt), row(p.z, p.sz)};
-    const long long step[3] = {MODE == kReverse ? p.sg.n : p.sx.n, p.sdt.n, p.sz.n};
-    const T *mat[2];
-    long long mstep[2];
-    {
-        const T *mB = static_cast<const T *>(p.B) + b * p.sB.b + (long long)t0 * p.sB.n + grp * p.sB.h;
-        const T *mC = static_cast<const T *>(p.C) + b * p.sC.b + (long long)t0 * p.sC.n + grp * p.sC.h;
-        mat[0] = MODE == kReverse ? mC : mB;
-        mstep[0] = MODE == kReverse ? p.sC.n : p.sB.n;
-        mat[1] = mC;
-        mstep[1] = p.sC.n;
-    }
+    const int te = min(t1, len), n = max(te - t0, 0), nt = (n + kRows - 1) / kRows;
     const bool gated = p.z != nullptr;
 
-    // tile `i` of the order of work (in reverse: the last first) to its stage; rows past te and channels past the group: zeros
-    auto place = [&](int i) { return MODE == kReverse ? nt - 1 - i : i; };
-    auto load = [&](int i) {
+    // A thread's copies: the same place of every tile, a tile's step apart.  Tiles in the order of work (in reverse: the last
+    // first); rows past te and channels past the group's: zeros.
+    const T *from[H::COPIES];
+    long long step[H::COPIES];
+    int row[H::COPIES];
+    unsigned to[H::COPIES];
+#pragma unroll
+    for (int k = 0; k < H::COPIES; ++k) {
+        const int v = tid + k * kThreads;
+        const void *base = p.x;
+        Strides st = p.sx;
+        int c;
+        if (v < TENSORS * H::NX) {
+            const int w = v % H::NX, m = v / H::NX;
+            if (MODE == kReverse && m == 0) base = p.g, st = p.sg;
+            if (m == 1) base = p.dt, st = p.sdt;
+            if (m == 2) base = p.z, st = p.sz;
+            row[k] = w / H::XV;
+            c = w % H::XV * V;
+            to[k] = m * H::XBYTES + row[k] * H::ROW + c * (int)sizeof(T);
+            if (c >= left || !base) row[k] = 1 << 30;
+            c += grp * p.Eg + c0;
+        } else {
+            const int u = v - TENSORS * H::NX, m = u / H::NB;
+            const bool C = MODE == kReverse || m == 1;
+            base = C ? p.C : p.B;
+            st = C ? p.sC : p.sB;
+            row[k] = u % H::NB / H::BV;
+            c = u % H::BV * V;
+            to[k] = TENSORS * H::XBYTES + u * 16;
+            if (m >= MATS) row[k] = 1 << 30;
+            base = static_cast<const T *>(base) + grp * st.h;
+        }
+        const long long first = t0 + (MODE == kReverse ? (nt - 1) * kRows : 0);
+        from[k] = row[k] < kRows ? static_cast<const T *>(base) + b * st.b + (first + row[k]) * st.n + c : nullptr;
+        step[k] = (MODE == kReverse ? -kRows : kRows) * st.n;
+    }
+    const T *const anchor = static_cast<const T *>(p.dt);
+    auto load = [&](int i, int stage) {
         if (i < nt) {
-            unsigned char *st = smem + (i % kStages) * H::STAGE;
-            const int first = place(i) * kRows;
-            constexpr int XV = CH / V, PER = kRows * XV;
+            const int first = (MODE == kReverse ? nt - 1 - i : i) * kRows;
 #pragma unroll
-            for (int k = 0; k < TENSORS; ++k) {
-                if (k == 2 && !gated) break;
-                for (int v = tid; v < PER; v += kThreads) {
-                    const int t = v / XV, c = v % XV * V;
-                    const bool in = t0 + first + t < te && c < left;
-                    copy_async<16>(st + k * H::XBYTES + t * H::ROW + c * (int)sizeof(T),
-                                   in ? src[k] + (long long)(first + t) * step[k] + c : src[k], in);
-                }
+            for (int k = 0; k < H::COPIES; ++k) {
+                const bool in = first + row[k] < n;
+                if ((k + 1) * kThreads <= TENSORS * H::NX + MATS * H::NB || tid + k * kThreads < TENSORS * H::NX + MATS * H::NB)
+                    copy_async(smem + stage * H::STAGE + to[k], in ? from[k] : anchor, in);
+                from[k] += step[k];
             }
-            constexpr int BV = S / V, BPER = kRows * BV;
-#pragma unroll
-            for (int k = 0; k < MATS; ++k)
-                for (int v = tid; v < BPER; v += kThreads) {
-                    const int t = v / BV, c = v % BV * V;
-                    const bool in = t0 + first + t < te;
-                    copy_async<16>(st + TENSORS * H::XBYTES + k * H::BBYTES + v * 16,
-                                   in ? mat[k] + (long long)(first + t) * mstep[k] + c : mat[k], in);
-                }
         }
         copy_commit();
     };
     // B and C of a tile as float32, [row][B states, C states]
-    auto widen = [&](int i) {
+    auto widen = [&](int i, int stage) {
         if (i >= nt) return;
-        const unsigned char *st = smem + (i % kStages) * H::STAGE + TENSORS * H::XBYTES;
-        float *to = wide + (i & 1) * H::WIDE;
-        constexpr int BV = S / V, BPER = kRows * BV;
+        const unsigned char *st = smem + stage * H::STAGE + TENSORS * H::XBYTES;
+        float *w = wide + (i & 1) * H::WIDE;
 #pragma unroll
-        for (int k = 0; k < MATS; ++k)
-            for (int v = tid; v < BPER; v += kThreads)
-                widen16(to + v / BV * (MATS * S) + k * S + v % BV * V, reinterpret_cast<const T *>(st + k * H::BBYTES + v * 16));
+        for (int k = 0; k < (MATS * H::NB + kThreads - 1) / kThreads; ++k) {
+            const int v = tid + k * kThreads;
+            if (MATS * H::NB % kThreads == 0 || v < MATS * H::NB)
+                widen16(w + v % H::NB / H::BV * (MATS * S) + v / H::NB * S + v % H::BV * V, reinterpret_cast<const T *>(st + v * 16));
+        }
+    };
+    // the outputs of a tile, in the places of its x
+    T *out = MODE == kScan && p.out ? static_cast<T *>(p.out) + ((long long)b * p.N + t0) * p.E + grp * p.Eg + c0 : nullptr;
+    auto leave = [&](int i, int stage) {
+        if (MODE != kScan || !out || i < 0) return;
+        const unsigned char *st = smem + stage * H::STAGE;
+#pragma unroll
+        for (int k = 0; k < (H::NX + kThreads - 1) / kThreads; ++k) {
+            const int v = tid + k * kThreads, t = v / H::XV, c = v % H::XV * V;
+            if ((H::NX % kThreads == 0 || v < H::NX) && i * kRows + t < n && c < left)
+                *reinterpret_cast<uint4 *>(out + (long long)(i * kRows + t) * p.E + c) =
+                    *reinterpret_cast<const uint4 *>(st + t * H::ROW + c * (int)sizeof(T));
+        }
     };
 
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) load(i);
+    for (int i = 0; i < kAhead; ++i) load(i, i);
 
     F2 A[PAIRS], h[PAIRS];
     const float bias = p.dt_bias ? p.dt_bias[e] : 0.f, skip = MODE == kScan && p.skip ? p.skip[e] : 0.f;
@@ -129,14 +151,14 @@ __global__ void __launch_bounds__(kThreads) k_ssm_scan(SsmParams p) {
         }
     }
     auto states = [&](const float *base, size_t block) { return base + (block * p.E + e) * S + r * SPT; };
-    auto take = [&](const float *from) {
+    auto take = [&](const float *a) {
 #pragma unroll
-        for (int i = 0; i < PAIRS; ++i) h[i] = *reinterpret_cast<const F2 *>(from + 2 * i);
+        for (int i = 0; i < PAIRS; ++i) h[i] = *reinterpret_cast<const F2 *>(a + 2 * i);
     };
-    auto put = [&](float *to) {
+    auto put = [&](float *a) {
 #pragma unroll
         for (int i = 0; i < SPT / 4; ++i)
-            *reinterpret_cast<float4 *>(to + 4 * i) = make_float4(h[2 * i].x, h[2 * i].y, h[2 * i + 1].x, h[2 * i + 1].y);
+            *reinterpret_cast<float4 *>(a + 4 * i) = make_float4(h[2 * i].x, h[2 * i].y, h[2 * i + 1].x, h[2 * i + 1].y);
     };
     // The start.  Segment 0's sum holds the initial state, so that only it is read besides the first segment itself, which
     // takes its copy in the last slot: the final state may replace the initial one at any time.
@@ -148,84 +170,96 @@ __global__ void __launch_bounds__(kThreads) k_ssm_scan(SsmParams p) {
             take(states(p.seg_state, w0));
             for (int j = 1; j < seg; ++j) {
                 const float d = p.seg_d[(w0 + j) * p.E + e];
-                const float *from = states(p.seg_state, w0 + j);
+                const float *a = states(p.seg_state, w0 + j);
 #pragma unroll
                 for (int i = 0; i < PAIRS; ++i)
-                    h[i] = fma2(ex22(mul2(f2(d), A[i])), h[i], *reinterpret_cast<const F2 *>(from + 2 * i));
+                    h[i] = fma2(ex22(mul2(f2(d), A[i])), h[i], *reinterpret_cast<const F2 *>(a + 2 * i));
             }
         }
     } else if (MODE != kReverse && seg == 0 && p.init) {
         take(states(p.init, b));
         if (MODE == kSums && there) put(const_cast<float *>(states(p.seg_state, (size_t)b * p.nseg + p.nseg - 1)));
     }
+    // (states kept for the gradient: [tile][S / 4][E][4])
+    float *kept = MODE == kScan && p.kept && there
+                      ? p.kept + (((size_t)b * ((p.N + kSsmTile - 1) / kSsmTile) + t0 / kSsmTile) * S / 4 * p.E + e) * 4 +
+                            (size_t)r * (SPT / 4) * p.E * 4
+                      : nullptr;
     float dsum = 0.f;
 
     // Every tile: the copies of the next one have come, whole (barrier); the last one's outputs leave; another is asked
     // for, into the stage that was emptied before the barrier; the next one's B and C are widened; this one is worked on.
-    auto leave = [&](int i) {
-        if (MODE != kScan || !p.out || i < 0) return;
-        const unsigned char *st = smem + (i % kStages) * H::STAGE;
-        constexpr int XV = CH / V, PER = kRows * XV;
-        T *out = static_cast<T *>(p.out) + ((long long)b * p.N + t0 + (long long)i * kRows) * p.E + grp * p.Eg + c0;
-        for (int v = tid; v < PER; v += kThreads) {
-            const int t = v / XV, c = v % XV * V;
-            if (t0 + i * kRows + t < te && c < left)
-                *reinterpret_cast<uint4 *>(out + (long long)t * p.E + c) = *reinterpret_cast<const uint4 *>(st + t * H::ROW + c * (int)sizeof(T));
-        }
-    };
     copy_wait<kAhead - 1>();
     __syncthreads();
-    widen(0);
+    widen(0, 0);
+    int stage = 0;
+    auto after = [](int s, int k) { return s + k >= kStages ? s + k - kStages : s + k; };
     for (int i = 0; i < nt; ++i) {
         copy_wait<kAhead - 2>();
         __syncthreads();
-        leave(i - 1);
-        load(i + kAhead);
-        widen(i + 1);
-        unsigned char *st = smem + (i % kStages) * H::STAGE;
+        leave(i - 1, after(stage, kStages - 1));
+        load(i + kAhead, after(stage, kAhead));
+        widen(i + 1, after(stage, 1));
+        unsigned char *own = smem + stage * H::STAGE + r * OWN * H::ROW + mine * (int)sizeof(T);
         const float *bc = wide + (i & 1) * H::WIDE + r * SPT;
-        const int first = place(i) * kRows;
+        const int first = (MODE == kReverse ? nt - 1 - i : i) * kRows;
+        stage = after(stage, 1);
 #pragma unroll 1
         for (int q = 0; q < kRows / 8; ++q) {
             const int c8 = MODE == kReverse ? kRows - 8 - q * 8 : q * 8;     // the eight tokens' place in the tile
-            if (MODE == kScan && p.kept && there && t0 + first + c8 < te)
-                put(const_cast<float *>(states(p.kept, (size_t)b * ((p.N + kSsmTile - 1) / kSsmTile) + (t0 + first + c8) / kSsmTile)));
-            float d[OWN], u[OWN], x[OWN];
+            if (MODE != kReverse && first + c8 >= n) break;
+            if (MODE == kScan && kept) {
 #pragma unroll
-            for (int o = 0; o < OWN; ++o) {
-                const int t = c8 + r * OWN + o;
-                const unsigned char *at = st + t * H::ROW + mine * (int)sizeof(T);
-                x[o] = to_f32(*reinterpret_cast<const T *>(at));
-                const float v = to_f32(*reinterpret_cast<const T *>(at + H::XBYTES)) + bias;
-                float ev;
-                const float sp = p.softplus ? softplus(v, ev) : v;
-                d[o] = t0 + first + t < te ? sp : 0.f;                       // past the length: h stays as it is
-                if (MODE == kReverse) {
-                    float gz = 1.f;
-                    if (gated) {
-                        const float z = to_f32(*reinterpret_cast<const T *>(at + 2 * H::XBYTES));
-                        gz = z * sigmoid(z);
-                    }
-                    u[o] = x[o] * gz;                                        // the gradient of y
-                } else {
-                    u[o] = d[o] * x[o];
-                }
-                if (MODE != kScan) dsum += d[o];
+                for (int k = 0; k < SPT / 4; ++k)
+                    *reinterpret_cast<float4 *>(kept + (size_t)k * p.E * 4) = make_float4(h[2 * k].x, h[2 * k].y, h[2 * k + 1].x, h[2 * k + 1].y);
+                kept += (size_t)S * p.E;
             }
+            unsigned char *at = own + c8 * H::ROW;
+            auto pair = [&](int m, int o) {                                  // own tokens 2 o and 2 o + 1 of tensor m
+                const unsigned char *a = at + m * H::XBYTES + 2 * o * H::ROW;
+                return F2{to_f32(*reinterpret_cast<const T *>(a)), to_f32(*reinterpret_cast<const T *>(a + (OWN > 1 ? H::ROW : 0)))};
+            };
+            F2 d[OP], u[OP], x[OP];
+#pragma unroll
+            for (int o = 0; o < OP; ++o) {
+                x[o] = pair(0, o);
+                d[o] = add2(pair(1, o), f2(bias));
+                if (p.softplus) {
+                    F2 ev;
+                    d[o] = softplus(d[o], ev);
+                }
+                if (first + c8 + 8 > n) {                                    // past the length: h stays as it is
+                    const int t = first + c8 + r * OWN + 2 * o;
+                    d[o] = F2{t < n ? d[o].x : 0.f, t + 1 < n ? d[o].y : 0.f};
+                }
+                if (MODE == kReverse) {                                      // the gradient of y
+                    u[o] = x[o];
+                    if (gated) {
+                        const F2 z = pair(2, o);
+                        u[o] = mul2(u[o], mul2(z, sigmoid(z)));
+                    }
+                } else {
+                    u[o] = mul2(d[o], x[o]);
+                }
+                if (MODE != kScan) dsum += OWN > 1 ? d[o].x + d[o].y : d[o].x;
+            }
+            auto all = [&](const F2 (&v)[OP], int j) {                       // token j's value, from the lane that owns it
+                const int o = j % OWN;
+                return f2(__shfl_sync(0xffffffffu, o % 2 ? v[o / 2].y : v[o / 2].x, j / OWN * CPW + chan));
+            };
             float y[8];
 #pragma unroll
             for (int jj = 0; jj < 8; ++jj) {
                 const int j = MODE == kReverse ? 7 - jj : jj;
-                const F2 dj = f2(__shfl_sync(0xffffffffu, d[j % OWN], j / OWN, LPC));
-                const F2 uj = f2(__shfl_sync(0xffffffffu, u[j % OWN], j / OWN, LPC));
-                const float *at = bc + (c8 + j) * (MATS * S);
-                F2 acc = f2(0.f);
+                const F2 dj = all(d, j), uj = all(u, j);
+                const float *m4 = bc + (c8 + j) * (MATS * S);
+                F2 acc;
 #pragma unroll
                 for (int i4 = 0; i4 < SPT / 4; ++i4) {
-                    const float4 m = *reinterpret_cast<const float4 *>(at + 4 * i4);
+                    const float4 m = *reinterpret_cast<const float4 *>(m4 + 4 * i4);
                     const F2 m2[2] = {F2{m.x, m.y}, F2{m.z, m.w}};
                     float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (MODE == kScan) c = *reinterpret_cast<const float4 *>(at + S + 4 * i4);
+                    if (MODE == kScan) c = *reinterpret_cast<const float4 *>(m4 + S + 4 * i4);
                     const F2 cc[2] = {F2{c.x, c.y}, F2{c.z, c.w}};
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
@@ -235,23 +269,23 @@ __global__ void __launch_bounds__(kThreads) k_ssm_scan(SsmParams p) {
                             hk = mul2(a, fma2(uj, m2[k], hk));
                         } else {
                             hk = fma2(a, hk, mul2(uj, m2[k]));
-                            if (MODE == kScan) acc = fma2(cc[k], hk, acc);
+                            if (MODE == kScan) acc = i4 + k == 0 ? mul2(cc[k], hk) : fma2(cc[k], hk, acc);
                         }
                     }
                 }
-                y[j] = acc.x + acc.y;
+                if (MODE == kScan) y[j] = acc.x + acc.y;
             }
-            if (MODE == kScan) {
-                quad_sums<LPC>(y, lane);
+            if (MODE == kScan && out) {
+                part_sums<LPC>(y, lane);
 #pragma unroll
-                for (int o = 0; o < OWN; ++o) {
-                    unsigned char *at = st + (c8 + r * OWN + o) * H::ROW + mine * (int)sizeof(T);
-                    float w = fmaf(skip, x[o], y[o]);
+                for (int o = 0; o < OP; ++o) {
+                    F2 w = fma2(f2(skip), x[o], F2{y[2 * o], OWN > 1 ? y[2 * o + 1] : y[2 * o]});
                     if (gated) {
-                        const float z = to_f32(*reinterpret_cast<const T *>(at + 2 * H::XBYTES));
-                        w *= z * sigmoid(z);
+                        const F2 z = pair(2, o);
+                        w = mul2(w, mul2(z, sigmoid(z)));
                     }
-                    *reinterpret_cast<T *>(at) = from_f32<T>(w);
+                    *reinterpret_cast<T *>(at + 2 * o * H::ROW) = from_f32<T>(w.x);
+                    if (OWN > 1) *reinterpret_cast<T *>(at + (2 * o + 1) * H::ROW) = from_f32<T>(w.y);
                 }
             }
         }
@@ -259,7 +293,7 @@ __global__ void __launch_bounds__(kThreads) k_ssm_scan(SsmParams p) {
     if (MODE != kScan) {
         // the segment alone: its last state (in reverse: the gradient of the state before it) and its sum of d
 #pragma unroll
-        for (int m = 1; m < LPC; m <<= 1) dsum += __shfl_xor_sync(0xffffffffu, dsum, m);
+        for (int m = CPW; m < 32; m <<= 1) dsum += __shfl_xor_sync(0xffffffffu, dsum, m);
         if (there) {
             const size_t w = (size_t)b * p.nseg + seg;
             put(const_cast<float *>(states(p.seg_state, w)));
@@ -268,16 +302,13 @@ __global__ void __launch_bounds__(kThreads) k_ssm_scan(SsmParams p) {
         return;
     }
     if (p.fin && seg == p.nseg - 1 && there) put(const_cast<float *>(states(p.fin, b)));
-    if (!p.out) return;
+    if (!out) return;
     __syncthreads();
-    leave(nt - 1);
+    leave(nt - 1, after(stage, kStages - 1));
     // rows past the length
-    T *out = static_cast<T *>(p.out) + (long long)b * p.N * p.E + grp * p.Eg + c0;
-    constexpr int XV = CH / V;
-    const int z0 = max(te, t0);
-    for (long long v = tid; v < (long long)(t1 - z0) * XV; v += kThreads) {
-        const int c = (int)(v % XV) * V;
-        if (c < left) *reinterpret_cast<uint4 *>(out + (z0 + v / XV) * p.E + c) = make_uint4(0, 0, 0, 0);
+    for (long long v = (long long)n * H::XV + tid; v < (long long)(t1 - t0) * H::XV; v += kThreads) {
+        const int c = (int)(v % H::XV) * V;
+        if (c < left) *reinterpret_cast<uint4 *>(out + (v / H::XV) * p.E + c) = make_uint4(0, 0, 0, 0);
     }
 }
 
