@@ -18,21 +18,36 @@ struct SsmPlan {
     int blocks, parts;
 };
 
-// Segments of `unit`-token tiles so that `blocks` sequences of blocks fill `slots` places, none shorter than `least` tokens.
-void cut(int N, long long blocks, long long slots, int least, int *seg_len, int *nseg) {
-    long long want = blocks >= slots / 2 ? 1 : slots / blocks;
-    const long long most = (N + least - 1) / least;
-    if (want > most) want = most;
-    if (want > 64) want = 64;
-    *seg_len = (int)(((N + want - 1) / want + kUnit - 1) / kUnit * kUnit);
-    *nseg = (N + *seg_len - 1) / *seg_len;
+// The segments of a sequence: the count whose kernels end first, in microseconds fitted to GB300.  The scan's blocks of a
+// segment each (1024 states) share the SMs evenly, 42 ns a token and block; less than about 1.75 blocks leave an SM
+// waiting.  The gradient's (8 to 16 times as much work) run in waves of two blocks an SM, 1.2 us a token.  More than one
+// segment costs the sums of all but one, 29 ns a token and block, and a launch.
+void cut(int N, bool bwd, long long blocks, long long sum_blocks, int slots, int *seg_len, int *nseg) {
+    double best = -1.0;
+    const int most = N < 64 * 64 ? (N + 63) / 64 : 64;
+    auto per_sm = [&](long long b) {
+        const double k = (double)((b + kPlanSms - 1) / kPlanSms);
+        return k > 1.75 ? k : 1.75;
+    };
+    for (int want = 1; want <= most; ++want) {
+        const int len = ((N + want - 1) / want + kUnit - 1) / kUnit * kUnit, n = (N + len - 1) / len;
+        double cost = bwd ? (double)((blocks * n + slots - 1) / slots) * (10.0 + 1.2 * len) : 0.042 * len * per_sm(blocks * n);
+        if (n > 1) cost += 0.029 * len * per_sm(sum_blocks * (n - 1)) + 4.5 + 0.25 * n;
+        if (best < 0 || cost < best) {
+            best = cost;
+            *seg_len = len;
+            *nseg = n;
+        }
+    }
 }
 
 SsmPlan make_plan(int nB, int N, int E, int S, int G, bool bwd) {
     SsmPlan pl{};
-    const int Eg = E / G, ch = bwd ? ssm_grad_channels(S) : ssm_scan_channels(S);
-    pl.blocks = (Eg + ch - 1) / ch;
-    cut(N, (long long)nB * G * pl.blocks, (bwd ? 3 : 7) * kPlanSms, 128, &pl.seg_len, &pl.nseg);
+    const int Eg = E / G;
+    auto blocks = [&](int ch) { return (Eg + ch - 1) / ch; };
+    const long long heads = (long long)nB * G, scan = heads * blocks(ssm_scan_channels(S));
+    pl.blocks = blocks(bwd ? ssm_grad_channels(S) : ssm_scan_channels(S));
+    cut(N, bwd, heads * pl.blocks, scan, (S == 64 ? 1 : 2) * kPlanSms, &pl.seg_len, &pl.nseg);
     pl.parts = nB * pl.nseg;
     size_t at = 0;
     auto take = [&](size_t floats) {

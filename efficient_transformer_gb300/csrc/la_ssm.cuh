@@ -148,23 +148,23 @@ __device__ __forceinline__ F2 sigmoid(F2 z) {
 // A warp's lanes: channel lane % CPW, part r = lane / CPW of its states (CPW = 32 / LPC): lanes of the same part are neighbours,
 // which makes their common loads of B and C 2 cycles of shared memory each instead of 4.
 //
-// Sums of v[j] over the LPC lanes of a channel, each sum left with the lane that owns token j: lane part r owns tokens
-// r OWN .. r OWN + OWN - 1 of the eight (OWN = 8 / LPC; with 16 parts, r and r + 8 both own token r).  Halves are
-// exchanged, so that 8 sums over 4 lanes take 6 shuffles instead of 16.
-template <int LPC>
-__device__ __forceinline__ void part_sums(float (&v)[8], int lane) {
+// Sums of v[j], of NT tokens each, over the LPC lanes of a channel, each sum left with the lane that owns token j: lane
+// part r owns tokens r OWN .. r OWN + OWN - 1 (OWN = NT / LPC; with more lanes than tokens, parts r and r + NT own token r).
+// Halves are exchanged, so that 8 sums over 4 lanes take 6 shuffles instead of 16.
+template <int LPC, int NT>
+__device__ __forceinline__ void part_sums(float (&v)[NT], int lane) {
     constexpr int CPW = 32 / LPC;
-    int n = 8;
-    if (LPC == 16) {
+    int n = NT;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 8 * CPW);
-    }
+    for (int m = LPC / 2; m >= NT && m >= 1; m >>= 1)
 #pragma unroll
-    for (int m = (LPC == 16 ? 4 : LPC / 2); m >= 1; m >>= 1) {
+        for (int i = 0; i < NT; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], m * CPW);
+#pragma unroll
+    for (int m = (LPC < NT ? LPC : NT) / 2; m >= 1; m >>= 1) {
         n >>= 1;
         const bool up = lane & (m * CPW);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < NT / 2; ++i)
             if (i < n) {
                 const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
                 v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m * CPW);

@@ -6,21 +6,26 @@
 //   dB_t = sum_e G u,  dC_t = sum_e dy h,  du = sum_s G B,  dA = sum_t q d,  dd = sum_s q A + x du
 //   dx = d du + skip dy,  ddt = dd sigmoid(v),  dz = grad_out y (z sigmoid(z))',  dskip = sum dy x
 //
-// 12 float operations and one ex2 a state and token: h is found again from the state that the scan kept for every
-// eight tokens, in registers, with a beside it; then the eight tokens are walked back.  Layout as in the scan: the LPC lanes of
-// a channel hold 4 states each, a lane prepares its own tokens, sums over states come by exchanged halves.  The sums over
-// channels (dB, dC) would cost more than all the rest if each token's were exchanged, so a warp takes K channel groups
-// one after the other for the same eight tokens and adds up in 64 registers; only then are its lanes' sums exchanged, the warps'
-// added in shared memory, and the block's written as one part.  P and dA wait in shared memory meanwhile.
+// 12 float operations and an ex2 a state and token.  h is found again from the state that the scan kept for every eight
+// tokens, in registers, with a beside it; then the eight tokens are walked back.  Layout as in the scan, but 4 states a
+// lane (h and a of eight tokens are 64 registers): a lane prepares its own tokens, those of the next unit while it works on
+// this one; sums over states come by exchanged halves.
+//
+// The sums over channels (dB, dC) would cost more than all the rest if each token's were exchanged.  So a warp takes K
+// channel groups one after the other for the same eight tokens and adds up in 64 registers; only then do its lanes exchange
+// halves, the warps' sums meet in shared memory, and the block's are written as one part.  P, dA and A of the groups
+// wait in shared memory meanwhile.  A unit is a warp's channels of one group and eight tokens; its rows come and go by the
+// warp's own copies, so that there is a barrier only for each eight tokens.
 #include "la_ssm.cuh"
 
 namespace la {
 namespace {
 
-constexpr int kRing = 4;   // units (8 tokens of a warp's channels) in flight: one worked on, one leaving, two coming
+constexpr int kRing = 8;      // units of a warp in shared memory (a power of 2): one leaves, one is worked on, one is prepared,
+constexpr int kAhead = 3;     // and copies run this many units ahead
 
 constexpr int warps_of(int S) { return S == 64 ? 8 : 4; }
-constexpr int groups_of(int S) { return S == 8 ? 2 : S == 16 ? 4 : 8; }   // channel groups of a warp (128 channels a block)
+constexpr int groups_of(int S) { return S == 8 ? 4 : 8; }   // channel groups of a warp
 
 template <typename T, int S>
 struct Shape {
@@ -53,17 +58,18 @@ __device__ __forceinline__ void copy_out(void *dst, const void *src) {
 }
 
 template <typename T, int S>
-__global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 3) k_ssm_grad(SsmParams p) {
+__global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_grad(SsmParams p) {
     using H = Shape<T, S>;
     constexpr int LPC = H::LPC, CPW = H::CPW, OWN = H::OWN, OP = OWN > 1 ? OWN / 2 : 1, CHK = H::CHK, TH = H::THREADS, CB = H::CB;
+    constexpr int EC = CB / (int)sizeof(T);                                  // channels of a copy
     extern __shared__ __align__(16) unsigned char smem[];
     float *wide = reinterpret_cast<float *>(smem + H::OFF_WIDE);
-    float4 *keep_P = reinterpret_cast<float4 *>(smem + H::OFF_P), *keep_dA = reinterpret_cast<float4 *>(smem + H::OFF_DA),
-           *keep_A = reinterpret_cast<float4 *>(smem + H::OFF_A), *keep_e = reinterpret_cast<float4 *>(smem + H::OFF_E);
     float *red = reinterpret_cast<float *>(smem + H::OFF_RED);
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane / CPW, chan = lane % CPW;
-    unsigned char *ring = smem + warp * kRing * H::UNIT;
+    unsigned char *const ring = smem + warp * kRing * H::UNIT;
+    float4 *const keep_P = reinterpret_cast<float4 *>(smem + H::OFF_P) + tid, *const keep_dA = reinterpret_cast<float4 *>(smem + H::OFF_DA) + tid,
+                  *const keep_A = reinterpret_cast<float4 *>(smem + H::OFF_A) + tid, *const keep_e = reinterpret_cast<float4 *>(smem + H::OFF_E) + tid;
     const int blocks = (p.Eg + H::CH - 1) / H::CH;
     unsigned idx = blockIdx.x;
     const int cb = idx % blocks;
@@ -75,218 +81,255 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 3) k_ssm_g
     const int e0 = grp * p.Eg + c0, w0 = warp * CPW;                         // the warp's first channel of each group
     const int t0 = seg * p.seg_len, t1 = min(t0 + p.seg_len, p.N);
     const int len = p.lengths ? min(max(p.lengths[b], 0), p.N) : p.N;
-    const int te = min(t1, len), nt = te > t0 ? (te - t0 + 7) / 8 : 0, units = nt * nk;
-    const bool gated = p.z != nullptr;
+    const int te = min(t1, len), n = max(te - t0, 0), nt = (n + 7) / 8, units = nt * nk;
+    const bool gated = p.z != nullptr, sp = p.softplus;
 
-    // A lane's copies: one place of every unit (row, tensor, piece of the row).  Tiles go from the last to the first, and in
-    // each the groups in turn; unit u is group u % nk of tile nt - 1 - u / nk.
+    // A lane's copies: one place of every unit (tensor, row, piece of the row).  Unit u is group u % nk of tile nt - 1 - u / nk;
+    // pointers move on by a group, and after the last group to the first of the tile before.  A copy is there for the
+    // groups below `in_k`, in the last tile only where its row is within the length.
     const T *from[H::IN];
-    long long back[H::IN];
-    int in_row[H::IN];
+    long long wrap[H::IN];
+    int in_k[H::IN];
+    T *to[H::OUT];
+    int out_k[H::OUT];
+    const int last_rows = n - (nt - 1) * 8;                                  // tokens of the last tile
+    auto groups = [&](int c) { return c < left ? (left - c - 1) / CHK + 1 : 0; };   // groups whose channel w0 + c is there
 #pragma unroll
     for (int q = 0; q < H::IN; ++q) {
-        const int v = lane + q * 32, m = v / (8 * H::PER), c = v % H::PER * (CB / (int)sizeof(T));
-        in_row[q] = v / H::PER % 8;
+        const int v = lane + q * 32, m = v / (8 * H::PER), row = v / H::PER % 8, c = w0 + v % H::PER * EC;
         const void *base = m == 0 ? p.x : m == 1 ? p.dt : m == 2 ? p.z : p.g;
         const Strides st = m == 0 ? p.sx : m == 1 ? p.sdt : m == 2 ? p.sz : p.sg;
-        back[q] = 8 * st.n;
-        from[q] = static_cast<const T *>(base ? base : p.x) + b * st.b + (t0 + (nt - 1) * 8 + (long long)in_row[q]) * st.n + e0 + w0 + c;
-        if (m > 3 || !base) in_row[q] = 1 << 30;
+        wrap[q] = -8 * st.n - (long long)(nk - 1) * CHK;
+        from[q] = static_cast<const T *>(base ? base : p.x) + b * st.b + (t0 + (nt - 1) * 8 + (long long)row) * st.n + e0 + c;
+        in_k[q] = m > 3 || !base ? 0 : groups(c) + (row < last_rows ? 0 : 256);   // 256: not in the last tile
     }
-    int load_k = 0, load_tile = nt - 1;
-    auto load = [&](int u) {
-        if (u < units) {
-            unsigned char *to = ring + (u % kRing) * H::UNIT + lane * CB;
+#pragma unroll
+    for (int q = 0; q < H::OUT; ++q) {
+        const int v = lane + q * 32, m = v / (8 * H::PER), row = v / H::PER % 8, c = w0 + v % H::PER * EC;
+        void *base = m == 0 ? p.dx : m == 1 ? p.ddt : p.dz;
+        to[q] = static_cast<T *>(base ? base : p.dx) + ((long long)b * p.N + t0 + (nt - 1) * 8 + row) * p.E + e0 + c;
+        out_k[q] = m > 2 || !base ? 0 : groups(c) + (row < last_rows ? 0 : 256);
+    }
+    int load_k = 0, load_u = 0, load_at = 0;
+    auto load = [&]() {
+        if (load_u < units) {
+            const bool wraps = load_k + 1 == nk;
 #pragma unroll
             for (int q = 0; q < H::IN; ++q) {
-                const int c = load_k * CHK;
-                const bool in = t0 + load_tile * 8 + in_row[q] < te && c + w0 + (lane + q * 32) % H::PER * (CB / (int)sizeof(T)) < left;
+                const bool in = load_k < (in_k[q] & 255) && (in_k[q] < 256 || load_u >= nk);
                 if (4 * 8 * H::PER % 32 == 0 || lane + q * 32 < 4 * 8 * H::PER)
-                    copy_in<CB>(to + q * 32 * CB, in ? from[q] + c : static_cast<const T *>(p.x), in);
-                if (load_k + 1 == nk) from[q] -= back[q];
+                    copy_in<CB>(ring + load_at + (lane + q * 32) * CB, in ? from[q] : static_cast<const T *>(p.x), in);
+                from[q] += wraps ? wrap[q] : CHK;
             }
-            if (++load_k == nk) load_k = 0, --load_tile;
+            load_k = wraps ? 0 : load_k + 1;
+            ++load_u;
+            load_at = (load_at + H::UNIT) % (kRing * H::UNIT);
         }
         copy_commit();
     };
     // the rows of dx, ddt and dz that a unit leaves in the places of x, dt and z
-    auto leave = [&](int u, int tile, int k) {
-        const unsigned char *at = ring + (u % kRing) * H::UNIT + lane * CB;
+    int leave_k = 0, leave_u = 0, leave_at = 0;
+    const long long out_wrap = -8ll * p.E - (long long)(nk - 1) * CHK;
+    auto leave = [&]() {
+        const bool wraps = leave_k + 1 == nk;
 #pragma unroll
         for (int q = 0; q < H::OUT; ++q) {
-            const int v = lane + q * 32, m = v / (8 * H::PER), c = k * CHK + w0 + v % H::PER * (CB / (int)sizeof(T));
-            const int t = t0 + tile * 8 + v / H::PER % 8;
-            T *to = static_cast<T *>(m == 0 ? p.dx : m == 1 ? p.ddt : p.dz);
-            if (m < 3 && (m < 2 || gated) && t < te && c < left)
-                copy_out<CB>(to + ((long long)b * p.N + t) * p.E + e0 + c, at + q * 32 * CB);
+            if (leave_k < (out_k[q] & 255) && (out_k[q] < 256 || leave_u >= nk))
+                copy_out<CB>(to[q], ring + leave_at + (lane + q * 32) * CB);
+            to[q] += wraps ? out_wrap : CHK;
         }
+        leave_k = wraps ? 0 : leave_k + 1;
+        ++leave_u;
+        leave_at = (leave_at + H::UNIT) % (kRing * H::UNIT);
     };
     // B and C of a tile: a copy a thread, through registers a tile ahead
     const int bv = tid % H::NB;
     const bool bthere = tid < 2 * H::NB;
     const T *bfrom = static_cast<const T *>(tid < H::NB ? p.B : p.C);
     const long long bstep = tid < H::NB ? p.sB.n : p.sC.n;
-    bfrom += b * (tid < H::NB ? p.sB.b : p.sC.b) + grp * (tid < H::NB ? p.sB.h : p.sC.h) + bv % H::BV * H::V;
+    bfrom += b * (tid < H::NB ? p.sB.b : p.sC.b) + grp * (tid < H::NB ? p.sB.h : p.sC.h) + bv % H::BV * H::V +
+             (t0 + (nt - 1) * 8 + bv / H::BV) * bstep;
     alignas(16) T raw[H::V];
     auto ask = [&](int i) {   // rows past the length: zeros
-        const int t = t0 + (nt - 1 - i) * 8 + bv / H::BV;
-        *reinterpret_cast<uint4 *>(raw) = bthere && i < nt && t < te ? *reinterpret_cast<const uint4 *>(bfrom + t * bstep) : make_uint4(0, 0, 0, 0);
+        const bool in = bthere && i < nt && (i > 0 || bv / H::BV < last_rows);
+        *reinterpret_cast<uint4 *>(raw) = in ? *reinterpret_cast<const uint4 *>(bfrom) : make_uint4(0, 0, 0, 0);
+        bfrom -= 8 * bstep;
     };
+    float *const wide_to = wide + bv / H::BV * (2 * S) + tid / H::NB * S + bv % H::BV * H::V;
     auto widen = [&](int i) {
-        if (bthere) widen16(wide + (i & 1) * H::WIDE + bv / H::BV * (2 * S) + tid / H::NB * S + bv % H::BV * H::V, raw);
+        if (bthere) widen16(wide_to + (i & 1) * H::WIDE, raw);
     };
     // a tile's part of dB and dC
+    float *part = p.part_bc + (((size_t)(grp * blocks + cb) * p.nB + b) * p.N + t0 + (long long)(nt - 1) * 8) * (2 * S) + tid;
     auto leave_bc = [&](int i) {
-        if (i < 0) return;
-        const int first = t0 + (nt - 1 - i) * 8;
-        const float *a = red + (i & 1) * H::NW * H::WIDE;
-        float *part = p.part_bc + (((size_t)(grp * blocks + cb) * p.nB + b) * p.N + first) * (2 * S);
-        for (int v = tid; v < H::WIDE; v += TH) {
-            float sum = 0.f;
+        const float *a = red + (i & 1) * H::NW * H::WIDE + tid;
 #pragma unroll
-            for (int w = 0; w < H::NW; ++w) sum += a[w * H::WIDE + v];
-            if (first + v / (2 * S) < te) part[v] = sum;
+        for (int v = 0; v < H::WIDE; v += TH) {
+            float sum = a[v];
+#pragma unroll
+            for (int w = 1; w < H::NW; ++w) sum += a[w * H::WIDE + v];
+            if (i > 0 || (v + tid) / (2 * S) < last_rows) part[v] = sum;
         }
+        part -= 8 * 2 * S;
     };
 
-    load(0);
-    load(1);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load();
     ask(0);
-    // P of the segment's end: the final state's gradient through the later segments
-#pragma unroll 1
-    for (int k = 0; k < nk; ++k) {
-        const int c = k * CHK + w0 + chan;
-        const bool there = c < left;
-        const size_t e = e0 + (there ? c : 0);
-        const float4 A = *reinterpret_cast<const float4 *>(p.A + e * S + 4 * r);
-        float4 P = p.dfinal && there ? *reinterpret_cast<const float4 *>(p.dfinal + ((size_t)b * p.E + e) * S + 4 * r)
-                                     : make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int j = p.nseg - 1; j > seg; --j) {
-            const size_t w = ((size_t)b * p.nseg + j) * p.E + e;
-            const float d = p.seg_d[w] * kLog2e;
-            const float4 R = there ? *reinterpret_cast<const float4 *>(p.seg_state + w * S + 4 * r) : P;
-            P = make_float4(fmaf(ex2(d * A.x), P.x, R.x), fmaf(ex2(d * A.y), P.y, R.y), fmaf(ex2(d * A.z), P.z, R.z),
-                            fmaf(ex2(d * A.w), P.w, R.w));
+    // P of the segment's end: the final state's gradient through the later segments, all groups side by side (their loads
+    // are what this takes)
+    {
+        float4 A[H::K], P[H::K];
+        size_t e[H::K];
+        bool there[H::K];
+#pragma unroll
+        for (int k = 0; k < H::K; ++k) {
+            const int c = k * CHK + w0 + chan;
+            there[k] = c < left;
+            e[k] = e0 + (there[k] ? c : 0);
+            A[k] = *reinterpret_cast<const float4 *>(p.A + e[k] * S + 4 * r);
+            P[k] = p.dfinal && there[k] ? *reinterpret_cast<const float4 *>(p.dfinal + ((size_t)b * p.E + e[k]) * S + 4 * r)
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        keep_P[k * TH + tid] = P;
-        keep_dA[k * TH + tid] = make_float4(0.f, 0.f, 0.f, 0.f);
-        keep_A[k * TH + tid] = make_float4(A.x * kLog2e, A.y * kLog2e, A.z * kLog2e, A.w * kLog2e);
-        keep_e[k * TH + tid] = make_float4(0.f, 0.f, p.dt_bias ? p.dt_bias[e] : 0.f, p.skip ? p.skip[e] : 0.f);
+        for (int j = p.nseg - 1; j > seg; --j) {
+            const size_t w = ((size_t)b * p.nseg + j) * p.E;
+#pragma unroll
+            for (int k = 0; k < H::K; ++k) {
+                const float d = there[k] ? p.seg_d[w + e[k]] * kLog2e : 0.f;
+                const float4 R = there[k] ? *reinterpret_cast<const float4 *>(p.seg_state + (w + e[k]) * S + 4 * r) : make_float4(0.f, 0.f, 0.f, 0.f);
+                P[k] = make_float4(fmaf(ex2(d * A[k].x), P[k].x, R.x), fmaf(ex2(d * A[k].y), P[k].y, R.y),
+                                   fmaf(ex2(d * A[k].z), P[k].z, R.z), fmaf(ex2(d * A[k].w), P[k].w, R.w));
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < H::K; ++k) {
+            keep_P[k * TH] = P[k];
+            keep_dA[k * TH] = make_float4(0.f, 0.f, 0.f, 0.f);
+            keep_A[k * TH] = make_float4(A[k].x * kLog2e, A[k].y * kLog2e, A[k].z * kLog2e, A[k].w * kLog2e);
+            keep_e[k * TH] = make_float4(0.f, 0.f, p.dt_bias ? p.dt_bias[e[k]] : 0.f, p.skip ? p.skip[e[k]] : 0.f);
+        }
     }
     widen(0);
     ask(1);
-    const size_t kept0 = (size_t)b * ((p.N + kSsmTile - 1) / kSsmTile);
-    auto kept = [&](int i, int k) {
-        const int c = k * CHK + w0 + chan;
-        const size_t w = ((kept0 + t0 / 8 + nt - 1 - i) * LPC + r) * p.E + e0 + c;
-        return c < left ? *reinterpret_cast<const float4 *>(p.kept + w * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+    // h at the start of a unit's tokens, read a unit ahead
+    const float4 *kept = reinterpret_cast<const float4 *>(p.kept) +
+                         (((size_t)b * ((p.N + kSsmTile - 1) / kSsmTile) + t0 / 8 + nt - 1) * LPC + r) * p.E + e0 + w0 + chan;
+    const long long kept_wrap = -(long long)LPC * p.E - (long long)(nk - 1) * CHK;
+    const int kept_k = groups(w0 + chan);
+    int next_k = 0;
+    auto take = [&]() {
+        const float4 h = next_k < kept_k ? *kept : make_float4(0.f, 0.f, 0.f, 0.f);
+        const bool wraps = next_k + 1 == nk;
+        kept += wraps ? kept_wrap : CHK;
+        next_k = wraps ? 0 : next_k + 1;
+        return h;
     };
-    float4 h_next = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (nt > 0) h_next = kept(0, 0);
-    int u = 0;
+
+    // The lane's own tokens of a unit, in pairs (of one: it and itself).
+    struct Own {
+        F2 x[OP], d[OP], u[OP], dy[OP], slope[OP], gz[OP];
+        float skip;
+    };
+    const int own = LPC == 16 ? r % 8 : r * OWN;
+    const unsigned own_at = own * H::ROW + chan * (int)sizeof(T);
+    auto prepare = [&](const unsigned char *st, int k, int t, Own &w) {      // t: of the first own token, from t0 on
+        const float4 es = keep_e[k * TH];
+        w.skip = es.w;
+#pragma unroll
+        for (int o = 0; o < OP; ++o) {
+            const unsigned char *at = st + own_at + 2 * o * H::ROW;
+            auto get = [&](int m) {
+                const unsigned char *q = at + m * H::XBYTES;
+                return F2{to_f32(*reinterpret_cast<const T *>(q)), to_f32(*reinterpret_cast<const T *>(q + (OWN > 1 ? H::ROW : 0)))};
+            };
+            w.x[o] = get(0);
+            const F2 v = add2(get(1), f2(es.z)), g = get(3);
+            F2 ev;
+            const F2 plus = softplus(v, ev), s1 = add2(ev, f2(1.f)), q = F2{rcp(s1.x), rcp(s1.y)};
+            const F2 sl = mul2(q, F2{v.x >= 0.f ? 1.f : ev.x, v.y >= 0.f ? 1.f : ev.y});
+            // (past the length: h stays as it is)
+            const bool in0 = t + 2 * o < n, in1 = t + 2 * o + 1 < n;
+            w.d[o] = F2{in0 ? (sp ? plus.x : v.x) : 0.f, in1 ? (sp ? plus.y : v.y) : 0.f};
+            w.slope[o] = F2{in0 ? (sp ? sl.x : 1.f) : 0.f, in1 ? (sp ? sl.y : 1.f) : 0.f};
+            w.u[o] = mul2(w.d[o], w.x[o]);
+            // (z sigmoid(z))' = s (1 + z (1 - s)) = s + z s (1 - s)
+            const F2 z = get(2), sz = sigmoid(z), zs = mul2(z, sz);
+            w.dy[o] = mul2(g, F2{gated ? zs.x : 1.f, gated ? zs.y : 1.f});
+            w.gz[o] = mul2(g, fma2(zs, F2{1.f - sz.x, 1.f - sz.y}, sz));
+        }
+    };
+    auto all = [&](const F2 (&v)[OP], int j) {   // token j's value, from the lane that owns it
+        const int o = j % OWN;
+        return f2(__shfl_sync(0xffffffffu, o % 2 ? v[o / 2].y : v[o / 2].x, j / OWN * CPW + chan));
+    };
+    Own now;
+    float4 h_next = nt > 0 ? take() : make_float4(0.f, 0.f, 0.f, 0.f);
+    copy_wait<kAhead - 1>();
+    __syncwarp();
+    prepare(ring, 0, (nt - 1) * 8 + own, now);
+    int at = 0;
     for (int i = 0; i < nt; ++i) {
         __syncthreads();   // the tile's B and C are whole, and the warps' dB and dC of the one before
-        leave_bc(i - 1);
+        if (i > 0) leave_bc(i - 1);
         widen(i + 1);
         ask(i + 2);
         const float *bc = wide + (i & 1) * H::WIDE + 4 * r;
-        const int first = t0 + (nt - 1 - i) * 8;
+        const int first = (nt - 1 - i) * 8;
         F2 accB[8][2], accC[8][2];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
             for (int m = 0; m < 2; ++m) accB[j][m] = accC[j][m] = f2(0.f);
 #pragma unroll 1
-        for (int k = 0; k < nk; ++k, ++u) {
-            copy_wait<1>();
-            __syncwarp();   // the unit's rows have come; the last one's outputs are whole
-            if (u > 0) leave(u - 1, k > 0 ? nt - 1 - i : nt - i, k > 0 ? k - 1 : nk - 1);
-            load(u + 2);
-            unsigned char *st = ring + (u % kRing) * H::UNIT;
+        for (int k = 0; k < nk; ++k) {
+            copy_wait<kAhead - 2>();
+            __syncwarp();   // the next unit's rows have come; the last one's outputs are whole
+            if (i + k > 0) leave();
+            load();
+            unsigned char *const st = ring + at + own_at;
+            at = (at + H::UNIT) % (kRing * H::UNIT);
             const float4 h4 = h_next;
-            if (u + 1 < units) h_next = k + 1 < nk ? kept(i, k + 1) : kept(i + 1, 0);
-            float4 es = keep_e[k * TH + tid];
-            const float bias = es.z, skip = es.w;
-            // the lane's own tokens, in pairs (of one: it and itself)
-            F2 x[OP], d[OP], u2[OP], dy[OP], slope[OP], gz[OP];
-            const int own = LPC == 16 ? r % 8 : r * OWN;
-            unsigned char *at0 = st + own * H::ROW + chan * (int)sizeof(T);
-#pragma unroll
-            for (int o = 0; o < OP; ++o) {
-                const unsigned char *at = at0 + 2 * o * H::ROW;
-                auto get = [&](int m) {
-                    const unsigned char *q = at + m * H::XBYTES;
-                    return F2{to_f32(*reinterpret_cast<const T *>(q)), to_f32(*reinterpret_cast<const T *>(q + (OWN > 1 ? H::ROW : 0)))};
-                };
-                x[o] = get(0);
-                const F2 v = add2(get(1), f2(bias)), g = get(3);
-                d[o] = v;
-                slope[o] = f2(1.f);
-                if (p.softplus) {
-                    F2 ev;
-                    d[o] = softplus(v, ev);
-                    const F2 s1 = add2(ev, f2(1.f)), q = F2{rcp(s1.x), rcp(s1.y)};
-                    slope[o] = mul2(q, F2{v.x >= 0.f ? 1.f : ev.x, v.y >= 0.f ? 1.f : ev.y});
-                }
-                if (first + 8 > te) {   // past the length: h stays as it is
-                    const int t = first + own + 2 * o;
-                    d[o] = F2{t < te ? d[o].x : 0.f, t + 1 < te ? d[o].y : 0.f};
-                    slope[o] = F2{t < te ? slope[o].x : 0.f, t + 1 < te ? slope[o].y : 0.f};
-                }
-                u2[o] = mul2(d[o], x[o]);
-                dy[o] = g;
-                gz[o] = f2(0.f);
-                if (gated) {
-                    const F2 z = get(2), sz = sigmoid(z), zs = mul2(z, sz);
-                    dy[o] = mul2(g, zs);
-                    // (z sigmoid(z))' = s (1 + z (1 - s)) = s + z s (1 - s)
-                    gz[o] = mul2(g, fma2(zs, F2{1.f - sz.x, 1.f - sz.y}, sz));
-                }
-            }
-            auto all = [&](const F2 (&v)[OP], int j) {   // token j's value, from the lane that owns it
-                const int o = j % OWN;
-                return f2(__shfl_sync(0xffffffffu, o % 2 ? v[o / 2].y : v[o / 2].x, j / OWN * CPW + chan));
-            };
-            const float4 A4 = keep_A[k * TH + tid];
+            if (i + 1 < nt || k + 1 < nk) h_next = take();
+            const float4 A4 = keep_A[k * TH], P4 = keep_P[k * TH], dA4 = keep_dA[k * TH];
             const F2 A[2] = {F2{A4.x, A4.y}, F2{A4.z, A4.w}};
-            // forward: h after each token
-            F2 hs[8][2];
+            Own then;
+            prepare(ring + at, k + 1 < nk ? k + 1 : 0, first - (k + 1 < nk ? 0 : 8) + own, then);
+            // forward: h after each token, a beside it
+            F2 hs[8][2], a[8][2];
             {
                 F2 h[2] = {F2{h4.x, h4.y}, F2{h4.z, h4.w}};
                 float y[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const F2 dj = all(d, j), uj = all(u2, j), gj = all(dy, j);
+                    const F2 dj = all(now.d, j), uj = all(now.u, j), gj = all(now.dy, j);
                     const float4 B4 = *reinterpret_cast<const float4 *>(bc + j * 2 * S), C4 = *reinterpret_cast<const float4 *>(bc + j * 2 * S + S);
                     const F2 Bj[2] = {F2{B4.x, B4.y}, F2{B4.z, B4.w}}, Cj[2] = {F2{C4.x, C4.y}, F2{C4.z, C4.w}};
                     F2 acc;
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
-                        h[m] = fma2(ex22(mul2(dj, A[m])), h[m], mul2(uj, Bj[m]));
+                        a[j][m] = ex22(mul2(dj, A[m]));
+                        h[m] = fma2(a[j][m], h[m], mul2(uj, Bj[m]));
                         hs[j][m] = h[m];
                         accC[j][m] = fma2(gj, h[m], accC[j][m]);
                         acc = m == 0 ? mul2(Cj[m], h[m]) : fma2(Cj[m], h[m], acc);
                     }
                     y[j] = acc.x + acc.y;
                 }
-                if (gated) {
-                    part_sums<LPC>(y, lane);
+                part_sums<LPC, 8>(y, lane);
 #pragma unroll
-                    for (int o = 0; o < OP; ++o) {
-                        const F2 dz = mul2(gz[o], fma2(f2(skip), x[o], F2{y[2 * o], OWN > 1 ? y[2 * o + 1] : y[2 * o]}));
-                        T *to = reinterpret_cast<T *>(at0 + 2 * o * H::ROW + 2 * H::XBYTES);
-                        if (LPC < 16 || r < 8) *to = from_f32<T>(dz.x);
-                        if (OWN > 1) *reinterpret_cast<T *>(reinterpret_cast<unsigned char *>(to) + H::ROW) = from_f32<T>(dz.y);
-                    }
+                for (int o = 0; o < OP; ++o) {   // (without a gate: into the place of z, which nothing reads)
+                    const F2 dz = mul2(now.gz[o], fma2(f2(now.skip), now.x[o], F2{y[2 * o], OWN > 1 ? y[2 * o + 1] : y[2 * o]}));
+                    unsigned char *q = st + 2 * o * H::ROW + 2 * H::XBYTES;
+                    if (LPC < 16 || r < 8) *reinterpret_cast<T *>(q) = from_f32<T>(dz.x);
+                    if (OWN > 1) *reinterpret_cast<T *>(q + H::ROW) = from_f32<T>(dz.y);
                 }
             }
-            // and back; a is found again (keeping the eight tokens' would take 32 registers more, and spills)
+            // and back
             float du[8], dq[8];
-            const float4 P4 = keep_P[k * TH + tid], dA4 = keep_dA[k * TH + tid];
             F2 P[2] = {F2{P4.x, P4.y}, F2{P4.z, P4.w}}, dA[2] = {F2{dA4.x, dA4.y}, F2{dA4.z, dA4.w}};
 #pragma unroll
             for (int j = 7; j >= 0; --j) {
-                const F2 dj = all(d, j), uj = all(u2, j), gj = all(dy, j);
+                const F2 dj = all(now.d, j), uj = all(now.u, j), gj = all(now.dy, j);
                 const float4 B4 = *reinterpret_cast<const float4 *>(bc + j * 2 * S), C4 = *reinterpret_cast<const float4 *>(bc + j * 2 * S + S);
                 const F2 Bj[2] = {F2{B4.x, B4.y}, F2{B4.z, B4.w}}, Cj[2] = {F2{C4.x, C4.y}, F2{C4.z, C4.w}};
                 F2 sb, sq;
@@ -296,7 +339,7 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 3) k_ssm_g
                     const F2 G = fma2(Cj[m], gj, P[m]);
                     sb = m == 0 ? mul2(G, Bj[m]) : fma2(G, Bj[m], sb);
                     accB[j][m] = fma2(G, uj, accB[j][m]);
-                    P[m] = mul2(ex22(mul2(dj, A[m])), G);
+                    P[m] = mul2(a[j][m], G);
                     const F2 q = mul2(P[m], before);
                     sq = m == 0 ? mul2(q, A[m]) : fma2(q, A[m], sq);
                     dA[m] = fma2(q, dj, dA[m]);
@@ -304,29 +347,31 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 3) k_ssm_g
                 du[j] = sb.x + sb.y;
                 dq[j] = sq.x + sq.y;
             }
-            keep_P[k * TH + tid] = make_float4(P[0].x, P[0].y, P[1].x, P[1].y);
-            keep_dA[k * TH + tid] = make_float4(dA[0].x, dA[0].y, dA[1].x, dA[1].y);
-            part_sums<LPC>(du, lane);
-            part_sums<LPC>(dq, lane);
+            keep_P[k * TH] = make_float4(P[0].x, P[0].y, P[1].x, P[1].y);
+            keep_dA[k * TH] = make_float4(dA[0].x, dA[0].y, dA[1].x, dA[1].y);
+            part_sums<LPC, 8>(du, lane);
+            part_sums<LPC, 8>(dq, lane);
+            float2 es = *reinterpret_cast<const float2 *>(&keep_e[k * TH]);
 #pragma unroll
             for (int o = 0; o < OP; ++o) {
                 const F2 s1 = F2{du[2 * o], OWN > 1 ? du[2 * o + 1] : du[2 * o]}, s2 = F2{dq[2 * o], OWN > 1 ? dq[2 * o + 1] : dq[2 * o]};
-                const F2 dx = fma2(d[o], s1, mul2(f2(skip), dy[o]));
+                const F2 dx = fma2(now.d[o], s1, mul2(f2(now.skip), now.dy[o]));
                 // (past the length: d, x, dy and the slope are zeros, the sums over states are not)
-                const F2 ddt = mul2(fma2(x[o], s1, mul2(f2(kLn2), s2)), slope[o]), ey = mul2(dy[o], x[o]);
+                const F2 ddt = mul2(fma2(now.x[o], s1, mul2(f2(kLn2), s2)), now.slope[o]), ey = mul2(now.dy[o], now.x[o]);
                 es.x += OWN > 1 ? ey.x + ey.y : ey.x;
                 es.y += OWN > 1 ? ddt.x + ddt.y : ddt.x;
-                unsigned char *at = at0 + 2 * o * H::ROW;
+                unsigned char *q = st + 2 * o * H::ROW;
                 if (LPC < 16 || r < 8) {
-                    *reinterpret_cast<T *>(at) = from_f32<T>(dx.x);
-                    *reinterpret_cast<T *>(at + H::XBYTES) = from_f32<T>(ddt.x);
+                    *reinterpret_cast<T *>(q) = from_f32<T>(dx.x);
+                    *reinterpret_cast<T *>(q + H::XBYTES) = from_f32<T>(ddt.x);
                 }
                 if (OWN > 1) {
-                    *reinterpret_cast<T *>(at + H::ROW) = from_f32<T>(dx.y);
-                    *reinterpret_cast<T *>(at + H::ROW + H::XBYTES) = from_f32<T>(ddt.y);
+                    *reinterpret_cast<T *>(q + H::ROW) = from_f32<T>(dx.y);
+                    *reinterpret_cast<T *>(q + H::ROW + H::XBYTES) = from_f32<T>(ddt.y);
                 }
             }
-            keep_e[k * TH + tid] = es;
+            *reinterpret_cast<float2 *>(&keep_e[k * TH]) = es;
+            now = then;
         }
         // dB and dC of the tile over the warp's channels: lanes of the same states exchange halves of the 64 sums (value
         // j * 8 + n: token j; n < 4: dB, else dC, of the lane's 4 states), until each is with one lane
@@ -340,42 +385,43 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 3) k_ssm_g
                 v[j * 8 + 4 + 2 * m] = accC[j][m].x;
                 v[j * 8 + 4 + 2 * m + 1] = accC[j][m].y;
             }
-        int base = 0, n = 64;
+        int base = 0, half = 64;
 #pragma unroll
         for (int m = CPW / 2; m >= 1; m >>= 1) {
-            n >>= 1;
+            half >>= 1;
             const bool up = lane & m;
-            base += up ? n : 0;
+            base += up ? half : 0;
 #pragma unroll
             for (int q = 0; q < 32; ++q)
-                if (q < n) {
-                    const float send = up ? v[q] : v[q + n], hold = up ? v[q + n] : v[q];
+                if (q < half) {
+                    const float send = up ? v[q] : v[q + half], hold = up ? v[q + half] : v[q];
                     v[q] = hold + __shfl_xor_sync(0xffffffffu, send, m);
                 }
         }
         constexpr int LEFT = 64 / CPW;   // values a lane is left with
-        float *to = red + ((i & 1) * H::NW + warp) * H::WIDE + 4 * r;
+        float *sums = red + ((i & 1) * H::NW + warp) * H::WIDE + 4 * r;
 #pragma unroll
         for (int q = 0; q < LEFT; q += 4) {
             const int w = base + q;
-            *reinterpret_cast<float4 *>(to + (w / 8) * 2 * S + (w % 8 / 4) * S) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+            *reinterpret_cast<float4 *>(sums + (w / 8) * 2 * S + (w % 8 / 4) * S) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
         }
     }
     __syncthreads();
-    leave_bc(nt - 1);
-    if (units > 0) leave(units - 1, 0, nk - 1);
+    if (nt > 0) {
+        leave_bc(nt - 1);
+        leave();
+    }
     // rows past the length
     {
         constexpr int XV = H::CH / H::V;
-        const int z0 = max(te, t0);
-        T *const rows[3] = {static_cast<T *>(p.dx), static_cast<T *>(p.ddt), static_cast<T *>(p.dz)};
+        T *const out3[3] = {static_cast<T *>(p.dx), static_cast<T *>(p.ddt), static_cast<T *>(p.dz)};
 #pragma unroll
         for (int m = 0; m < 3; ++m) {
             if (m == 2 && !gated) continue;
-            T *out = rows[m] + (long long)b * p.N * p.E + e0;
-            for (long long v = tid; v < (long long)(t1 - z0) * XV; v += TH) {
+            T *out = out3[m] + ((long long)b * p.N + t0) * p.E + e0;
+            for (long long v = (long long)n * XV + tid; v < (long long)(t1 - t0) * XV; v += TH) {
                 const int c = (int)(v % XV) * H::V;
-                if (c < left) *reinterpret_cast<uint4 *>(out + (z0 + v / XV) * p.E + c) = make_uint4(0, 0, 0, 0);
+                if (c < left) *reinterpret_cast<uint4 *>(out + (v / XV) * p.E + c) = make_uint4(0, 0, 0, 0);
             }
         }
     }
@@ -384,19 +430,19 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 3) k_ssm_g
         const int c = k * CHK + w0 + chan;
         const bool there = c < left;
         const size_t e = e0 + (there ? c : 0), w = (size_t)b * p.nseg + seg;
-        float4 es = keep_e[k * TH + tid];
+        float4 es = keep_e[k * TH];
 #pragma unroll
         for (int m = 1; m < (LPC == 16 ? 8 : LPC); m <<= 1) {
             es.x += __shfl_xor_sync(0xffffffffu, es.x, m * CPW);
             es.y += __shfl_xor_sync(0xffffffffu, es.y, m * CPW);
         }
         if (!there) continue;
-        *reinterpret_cast<float4 *>(p.part_A + (w * p.E + e) * S + 4 * r) = keep_dA[k * TH + tid];
+        *reinterpret_cast<float4 *>(p.part_A + (w * p.E + e) * S + 4 * r) = keep_dA[k * TH];
         if (r == 0) {
             p.part_e[(w * 2) * p.E + e] = es.x;
             p.part_e[(w * 2 + 1) * p.E + e] = es.y;
         }
-        if (p.dinit && seg == 0) *reinterpret_cast<float4 *>(p.dinit + ((size_t)b * p.E + e) * S + 4 * r) = keep_P[k * TH + tid];
+        if (p.dinit && seg == 0) *reinterpret_cast<float4 *>(p.dinit + ((size_t)b * p.E + e) * S + 4 * r) = keep_P[k * TH];
     }
 }
 

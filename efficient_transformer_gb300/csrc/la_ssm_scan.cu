@@ -15,9 +15,12 @@ namespace {
 
 enum Mode { kScan = 0, kSums = 1, kReverse = 2 };
 
-constexpr int kWarps = 4, kThreads = kWarps * 32, kRows = 16, kAhead = 2, kStages = kAhead + 2;
+constexpr int kWarps = 4, kThreads = kWarps * 32, kRows = 16, kAhead = 2, kStages = kAhead + 3;
 
-constexpr int spt_of(int S) { return S <= 16 ? 4 : 8; }
+// States of a lane: 8, or 16 where a channel would be spread over more than four lanes.  (4 a lane make twice the warps, but
+// share a channel's preparation, shuffles and sums among fewer states: a third more instructions, 4 x 4096 x 4096 x 16 420 us
+// against 352.)
+constexpr int spt_of(int S) { return S <= 32 ? 8 : 16; }
 
 template <typename T, int S, int MODE>
 struct Shape {
@@ -35,7 +38,7 @@ struct Shape {
 };
 
 template <typename T, int S, int MODE>
-__global__ void __launch_bounds__(kThreads) k_ssm_scan(SsmParams p) {
+__global__ void __launch_bounds__(kThreads, 3) k_ssm_scan(SsmParams p) {
     using H = Shape<T, S, MODE>;
     constexpr int SPT = H::SPT, LPC = H::LPC, CPW = H::CPW, CH = H::CH, OWN = H::OWN, V = H::V, TENSORS = H::TENSORS, MATS = H::MATS;
     constexpr int PAIRS = SPT / 2, OP = OWN > 1 ? OWN / 2 : 1;               // pairs of own tokens (of one: it and itself)
@@ -168,6 +171,7 @@ __global__ void __launch_bounds__(kThreads) k_ssm_scan(SsmParams p) {
             if (p.init) take(states(p.seg_state, w0 + p.nseg - 1));
         } else {
             take(states(p.seg_state, w0));
+#pragma unroll 4
             for (int j = 1; j < seg; ++j) {
                 const float d = p.seg_d[(w0 + j) * p.E + e];
                 const float *a = states(p.seg_state, w0 + j);
@@ -187,113 +191,144 @@ __global__ void __launch_bounds__(kThreads) k_ssm_scan(SsmParams p) {
                       : nullptr;
     float dsum = 0.f;
 
-    // Every tile: the copies of the next one have come, whole (barrier); the last one's outputs leave; another is asked
-    // for, into the stage that was emptied before the barrier; the next one's B and C are widened; this one is worked on.
+    // Eight tokens at a time, in three parts that overlap: the next ones' steps are prepared and the last ones' sums and gates
+    // are finished while these run through the states.  No branches between them (what a call does not have is selected
+    // away), so that the compiler may interleave all three: a warp alone on its scheduler would wait for most of them.
+    struct Own {
+        F2 d[OP], u[OP], x[OP];
+    };
+    unsigned char *const mine0 = smem + r * OWN * H::ROW + mine * (int)sizeof(T);
+    auto pair = [&](const unsigned char *at, int m, int o) {                 // own tokens 2 o and 2 o + 1 of tensor m
+        const unsigned char *a = at + m * H::XBYTES + 2 * o * H::ROW;
+        return F2{to_f32(*reinterpret_cast<const T *>(a)), to_f32(*reinterpret_cast<const T *>(a + (OWN > 1 ? H::ROW : 0)))};
+    };
+    const bool sp = p.softplus;
+    auto gate = [&](const unsigned char *at, int o) {
+        const F2 z = pair(at, 2, o), g = mul2(z, sigmoid(z));
+        return F2{gated ? g.x : 1.f, gated ? g.y : 1.f};
+    };
+    auto prepare = [&](const unsigned char *at, int t, Own &w) {             // t: of the lane's first own token, from t0 on
+#pragma unroll
+        for (int o = 0; o < OP; ++o) {
+            w.x[o] = pair(at, 0, o);
+            const F2 v = add2(pair(at, 1, o), f2(bias));
+            F2 ev;
+            const F2 s = softplus(v, ev);
+            // (past the length: h stays as it is)
+            w.d[o] = F2{t + 2 * o < n ? (sp ? s.x : v.x) : 0.f, t + 2 * o + 1 < n ? (sp ? s.y : v.y) : 0.f};
+            w.u[o] = MODE == kReverse ? mul2(w.x[o], gate(at, o)) : mul2(w.d[o], w.x[o]);   // (in reverse: the gradient of y)
+        }
+    };
+    auto run = [&](const Own &w, const float *bc, float (&y)[8]) {           // bc: the tokens' B and C
+        auto all = [&](const F2 (&v)[OP], int j) {                           // token j's value, from the lane that owns it
+            const int o = j % OWN;
+            return f2(__shfl_sync(0xffffffffu, o % 2 ? v[o / 2].y : v[o / 2].x, j / OWN * CPW + chan));
+        };
+#pragma unroll
+        for (int jj = 0; jj < 8; ++jj) {
+            const int j = MODE == kReverse ? 7 - jj : jj;
+            const F2 dj = all(w.d, j), uj = all(w.u, j);
+            const float *m4 = bc + j * (MATS * S);
+            F2 acc;
+#pragma unroll
+            for (int i4 = 0; i4 < SPT / 4; ++i4) {
+                const float4 m = *reinterpret_cast<const float4 *>(m4 + 4 * i4);
+                const F2 m2[2] = {F2{m.x, m.y}, F2{m.z, m.w}};
+                float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (MODE == kScan) c = *reinterpret_cast<const float4 *>(m4 + S + 4 * i4);
+                const F2 cc[2] = {F2{c.x, c.y}, F2{c.z, c.w}};
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    F2 &hk = h[2 * i4 + k];
+                    const F2 a = ex22(mul2(dj, A[2 * i4 + k]));
+                    if (MODE == kReverse) {
+                        hk = mul2(a, fma2(uj, m2[k], hk));
+                    } else {
+                        hk = fma2(a, hk, mul2(uj, m2[k]));
+                        if (MODE == kScan) acc = i4 + k == 0 ? mul2(cc[k], hk) : fma2(cc[k], hk, acc);
+                    }
+                }
+            }
+            if (MODE == kScan) y[j] = acc.x + acc.y;
+        }
+    };
+    auto finish = [&](unsigned char *at, const Own &w, float (&y)[8]) {
+        if (MODE != kScan) return;
+        part_sums<LPC, 8>(y, lane);
+#pragma unroll
+        for (int o = 0; o < OP; ++o) {
+            F2 v = fma2(f2(skip), w.x[o], F2{y[2 * o], OWN > 1 ? y[2 * o + 1] : y[2 * o]});
+            v = mul2(v, gate(at, o));
+            *reinterpret_cast<T *>(at + 2 * o * H::ROW) = from_f32<T>(v.x);
+            if (OWN > 1) *reinterpret_cast<T *>(at + (2 * o + 1) * H::ROW) = from_f32<T>(v.y);
+        }
+    };
+    auto keep = [&](bool in) {
+        if (MODE != kScan) return;
+        if (kept && in) {
+#pragma unroll
+            for (int k = 0; k < SPT / 4; ++k)
+                *reinterpret_cast<float4 *>(kept + (size_t)k * p.E * 4) = make_float4(h[2 * k].x, h[2 * k].y, h[2 * k + 1].x, h[2 * k + 1].y);
+            kept += (size_t)S * p.E;
+        }
+    };
+
+    // Every tile: the copies of the next one have come, whole (barrier); the outputs of the one before the last leave; another
+    // is asked for, into the stage that was emptied before the barrier; the next one's B and C are widened; this one is run.
+    constexpr int C0 = MODE == kReverse ? 8 : 0, C1 = 8 - C0;                // the places of its first and second eight tokens
+    static_assert(kRows == 16, "two times eight tokens a tile");
     copy_wait<kAhead - 1>();
     __syncthreads();
     widen(0, 0);
     int stage = 0;
     auto after = [](int s, int k) { return s + k >= kStages ? s + k - kStages : s + k; };
+    Own own[2];
+    float y[2][8];
+    prepare(mine0 + C0 * H::ROW, (MODE == kReverse ? (nt - 1) * kRows : 0) + C0 + r * OWN, own[0]);
+    own[1] = own[0];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[1][j] = 0.f;
+    // (a sum of d counts what is run, not what is prepared)
+    auto count = [&](const Own &w) {
+        if (MODE == kScan) return;
+#pragma unroll
+        for (int o = 0; o < OP; ++o) dsum += OWN > 1 ? w.d[o].x + w.d[o].y : w.d[o].x;
+    };
     for (int i = 0; i < nt; ++i) {
         copy_wait<kAhead - 2>();
         __syncthreads();
-        leave(i - 1, after(stage, kStages - 1));
+        leave(i - 2, after(stage, kStages - 2));
         load(i + kAhead, after(stage, kAhead));
         widen(i + 1, after(stage, 1));
-        unsigned char *own = smem + stage * H::STAGE + r * OWN * H::ROW + mine * (int)sizeof(T);
+        unsigned char *const at = mine0 + stage * H::STAGE, *const next = mine0 + after(stage, 1) * H::STAGE,
+                      *const last = mine0 + after(stage, kStages - 1) * H::STAGE;
         const float *bc = wide + (i & 1) * H::WIDE + r * SPT;
-        const int first = (MODE == kReverse ? nt - 1 - i : i) * kRows;
+        const int first = (MODE == kReverse ? nt - 1 - i : i) * kRows, then = first + (MODE == kReverse ? -kRows : kRows);
         stage = after(stage, 1);
-#pragma unroll 1
-        for (int q = 0; q < kRows / 8; ++q) {
-            const int c8 = MODE == kReverse ? kRows - 8 - q * 8 : q * 8;     // the eight tokens' place in the tile
-            if (MODE != kReverse && first + c8 >= n) break;
-            if (MODE == kScan && kept) {
-#pragma unroll
-                for (int k = 0; k < SPT / 4; ++k)
-                    *reinterpret_cast<float4 *>(kept + (size_t)k * p.E * 4) = make_float4(h[2 * k].x, h[2 * k].y, h[2 * k + 1].x, h[2 * k + 1].y);
-                kept += (size_t)S * p.E;
-            }
-            unsigned char *at = own + c8 * H::ROW;
-            auto pair = [&](int m, int o) {                                  // own tokens 2 o and 2 o + 1 of tensor m
-                const unsigned char *a = at + m * H::XBYTES + 2 * o * H::ROW;
-                return F2{to_f32(*reinterpret_cast<const T *>(a)), to_f32(*reinterpret_cast<const T *>(a + (OWN > 1 ? H::ROW : 0)))};
-            };
-            F2 d[OP], u[OP], x[OP];
-#pragma unroll
-            for (int o = 0; o < OP; ++o) {
-                x[o] = pair(0, o);
-                d[o] = add2(pair(1, o), f2(bias));
-                if (p.softplus) {
-                    F2 ev;
-                    d[o] = softplus(d[o], ev);
-                }
-                if (first + c8 + 8 > n) {                                    // past the length: h stays as it is
-                    const int t = first + c8 + r * OWN + 2 * o;
-                    d[o] = F2{t < n ? d[o].x : 0.f, t + 1 < n ? d[o].y : 0.f};
-                }
-                if (MODE == kReverse) {                                      // the gradient of y
-                    u[o] = x[o];
-                    if (gated) {
-                        const F2 z = pair(2, o);
-                        u[o] = mul2(u[o], mul2(z, sigmoid(z)));
-                    }
-                } else {
-                    u[o] = mul2(d[o], x[o]);
-                }
-                if (MODE != kScan) dsum += OWN > 1 ? d[o].x + d[o].y : d[o].x;
-            }
-            auto all = [&](const F2 (&v)[OP], int j) {                       // token j's value, from the lane that owns it
-                const int o = j % OWN;
-                return f2(__shfl_sync(0xffffffffu, o % 2 ? v[o / 2].y : v[o / 2].x, j / OWN * CPW + chan));
-            };
-            float y[8];
-#pragma unroll
-            for (int jj = 0; jj < 8; ++jj) {
-                const int j = MODE == kReverse ? 7 - jj : jj;
-                const F2 dj = all(d, j), uj = all(u, j);
-                const float *m4 = bc + (c8 + j) * (MATS * S);
-                F2 acc;
-#pragma unroll
-                for (int i4 = 0; i4 < SPT / 4; ++i4) {
-                    const float4 m = *reinterpret_cast<const float4 *>(m4 + 4 * i4);
-                    const F2 m2[2] = {F2{m.x, m.y}, F2{m.z, m.w}};
-                    float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (MODE == kScan) c = *reinterpret_cast<const float4 *>(m4 + S + 4 * i4);
-                    const F2 cc[2] = {F2{c.x, c.y}, F2{c.z, c.w}};
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        F2 &hk = h[2 * i4 + k];
-                        const F2 a = ex22(mul2(dj, A[2 * i4 + k]));
-                        if (MODE == kReverse) {
-                            hk = mul2(a, fma2(uj, m2[k], hk));
-                        } else {
-                            hk = fma2(a, hk, mul2(uj, m2[k]));
-                            if (MODE == kScan) acc = i4 + k == 0 ? mul2(cc[k], hk) : fma2(cc[k], hk, acc);
-                        }
-                    }
-                }
-                if (MODE == kScan) y[j] = acc.x + acc.y;
-            }
-            if (MODE == kScan && out) {
-                part_sums<LPC>(y, lane);
-#pragma unroll
-                for (int o = 0; o < OP; ++o) {
-                    F2 w = fma2(f2(skip), x[o], F2{y[2 * o], OWN > 1 ? y[2 * o + 1] : y[2 * o]});
-                    if (gated) {
-                        const F2 z = pair(2, o);
-                        w = mul2(w, mul2(z, sigmoid(z)));
-                    }
-                    *reinterpret_cast<T *>(at + 2 * o * H::ROW) = from_f32<T>(w.x);
-                    if (OWN > 1) *reinterpret_cast<T *>(at + (2 * o + 1) * H::ROW) = from_f32<T>(w.y);
-                }
-            }
+        keep(first < n);
+        count(own[0]);
+        {
+            Own w;
+            prepare(at + C1 * H::ROW, first + C1 + r * OWN, w);
+            run(own[0], bc + C0 * (MATS * S), y[0]);
+            finish(last + C1 * H::ROW, own[1], y[1]);   // (before the first tile: into a stage that nothing reads)
+            own[1] = w;
+        }
+        keep(first + 8 < n);
+        count(own[1]);
+        {
+            Own w;
+            prepare(next + C0 * H::ROW, then + C0 + r * OWN, w);
+            run(own[1], bc + C1 * (MATS * S), y[1]);
+            finish(at + C0 * H::ROW, own[0], y[0]);
+            own[0] = w;
         }
     }
+    finish(mine0 + after(stage, kStages - 1) * H::STAGE + C1 * H::ROW, own[1], y[1]);
     if (MODE != kScan) {
         // the segment alone: its last state (in reverse: the gradient of the state before it) and its sum of d
 #pragma unroll
-        for (int m = CPW; m < 32; m <<= 1) dsum += __shfl_xor_sync(0xffffffffu, dsum, m);
+        for (int m = CPW; LPC > 1 && m < 32; m <<= 1) dsum += __shfl_xor_sync(0xffffffffu, dsum, m);
         if (there) {
             const size_t w = (size_t)b * p.nseg + seg;
             put(const_cast<float *>(states(p.seg_state, w)));
@@ -304,6 +339,7 @@ __global__ void __launch_bounds__(kThreads) k_ssm_scan(SsmParams p) {
     if (p.fin && seg == p.nseg - 1 && there) put(const_cast<float *>(states(p.fin, b)));
     if (!out) return;
     __syncthreads();
+    leave(nt - 2, after(stage, kStages - 2));
     leave(nt - 1, after(stage, kStages - 1));
     // rows past the length
     for (long long v = (long long)n * H::XV + tid; v < (long long)(t1 - t0) * H::XV; v += kThreads) {
@@ -325,28 +361,25 @@ cudaError_t launch(const SsmParams &p, cudaStream_t s) {
     return launch_pdl(kern, dim3((unsigned)blocks), dim3(kThreads), H::SMEM, s, p);
 }
 
+template <typename T, int MODE>
+cudaError_t by_states(const SsmParams &p, cudaStream_t s) {
+    return p.S == 8 ? launch<T, 8, MODE>(p, s) : p.S == 16 ? launch<T, 16, MODE>(p, s)
+                                            : p.S == 32 ? launch<T, 32, MODE>(p, s) : launch<T, 64, MODE>(p, s);
+}
+
 template <int MODE>
-cudaError_t by_shape(const SsmParams &p, la_dtype dt, cudaStream_t s) {
-    if (dt == LA_BF16) {
-        if (p.S == 8) return launch<__nv_bfloat16, 8, MODE>(p, s);
-        if (p.S == 16) return launch<__nv_bfloat16, 16, MODE>(p, s);
-        if (p.S == 32) return launch<__nv_bfloat16, 32, MODE>(p, s);
-        return launch<__nv_bfloat16, 64, MODE>(p, s);
-    }
-    if (p.S == 8) return launch<float, 8, MODE>(p, s);
-    if (p.S == 16) return launch<float, 16, MODE>(p, s);
-    if (p.S == 32) return launch<float, 32, MODE>(p, s);
-    return launch<float, 64, MODE>(p, s);
+cudaError_t by_type(const SsmParams &p, la_dtype dt, cudaStream_t s) {
+    return dt == LA_BF16 ? by_states<__nv_bfloat16, MODE>(p, s) : by_states<float, MODE>(p, s);
 }
 
 }  // namespace
 
 int ssm_scan_channels(int S) { return kWarps * 32 / (S / spt_of(S)); }
 
-cudaError_t ssm_scan(const SsmParams &p, la_dtype dt, cudaStream_t s) { return by_shape<kScan>(p, dt, s); }
+cudaError_t ssm_scan(const SsmParams &p, la_dtype dt, cudaStream_t s) { return by_type<kScan>(p, dt, s); }
 
 cudaError_t ssm_segments(const SsmParams &p, la_dtype dt, bool reverse, cudaStream_t s) {
-    return reverse ? by_shape<kReverse>(p, dt, s) : by_shape<kSums>(p, dt, s);
+    return reverse ? by_type<kReverse>(p, dt, s) : by_type<kSums>(p, dt, s);
 }
 
 }  // namespace la
