@@ -8,6 +8,7 @@
 // token) and walks a run of tokens with the last W rows in registers, two channels an instruction; the next tokens' loads
 // are issued before the present ones are worked on.
 #include <initializer_list>
+#include <type_traits>
 
 #include "la_ssm.cuh"
 
@@ -172,21 +173,26 @@ __global__ void __launch_bounds__(256, 2) k_conv(ConvParams p) {
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) in[q] = next[q];
         if (t + kBatch < te) ask<T>(next, at, row.step, t + 2 * kBatch <= te, [&](int q) { return row(t + kBatch + q); });
+        auto each = [&](auto whole) {   // (whole: all of these tokens are within the length and the run)
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-            F2 v[2];
+            for (int q = 0; q < kBatch; ++q) {
+                F2 v[2];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+                for (int c = 0; c < 2; ++c) {
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j) win[j][c] = win[j + 1][c];
-                win[W - 1][c] = pair(in[q], c);
-                v[c] = k.bias[c];
+                    for (int j = 0; j < W - 1; ++j) win[j][c] = win[j + 1][c];
+                    win[W - 1][c] = pair(in[q], c);
+                    v[c] = k.bias[c];
 #pragma unroll
-                for (int j = 0; j < W; ++j) v[c] = fma2(k.w[j][c], win[j][c], v[c]);
-                if (p.silu) v[c] = mul2(v[c], sigmoid(v[c]));
+                    for (int j = 0; j < W; ++j) v[c] = fma2(k.w[j][c], win[j][c], v[c]);
+                    if (p.silu) v[c] = mul2(v[c], sigmoid(v[c]));
+                }
+                if (whole.value) put_row<T>(out, (long long)q * p.E, row_of<T>(v[0], v[1]));
+                else if (t + q < t1) put_row<T>(out, (long long)q * p.E, t + q < len ? row_of<T>(v[0], v[1]) : no_row<T>());
             }
-            if (t + q < t1) put_row<T>(out, (long long)q * p.E, t + q < len ? row_of<T>(v[0], v[1]) : no_row<T>());
-        }
+        };
+        if (t + kBatch <= te) each(std::true_type{});
+        else each(std::false_type{});
         out += (long long)kBatch * p.E;
     }
 }
@@ -241,51 +247,59 @@ __global__ void __launch_bounds__(256, 2) k_conv_grad(ConvParams p) {
                 ask<T>(next, xat, row.step, t + 2 * Q <= tw, [&](int q) { return row(t + Q + q); });
                 ask<T>(gnext, gat, p.sg.n, t + 2 * Q <= tw, [&](int q) { return grad(t + Q + q); });
             }
+            auto each = [&](auto whole) {   // (whole: all of these tokens are within the length and the run, their rows too)
 #pragma unroll
-            for (int q = 0; q < Q; ++q) {
-                const int at = t + q - (W - 1);   // the row whose gradient is whole now
-                F2 d[2];
+                for (int q = 0; q < Q; ++q) {
+                    const int at = t + q - (W - 1);   // the row whose gradient is whole now
+                    F2 d[2];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
+                    for (int c = 0; c < 2; ++c) {
 #pragma unroll
-                    for (int j = 0; j < W - 1; ++j) {
-                        win[j][c] = win[j + 1][c];
-                        gw[j][c] = gw[j + 1][c];
+                        for (int j = 0; j < W - 1; ++j) {
+                            win[j][c] = win[j + 1][c];
+                            gw[j][c] = gw[j + 1][c];
+                        }
+                        win[W - 1][c] = pair(in[q], c);
+                        F2 g = pair(gin[q], c);
+                        if (p.silu) {
+                            F2 v = k.bias[c];
+#pragma unroll
+                            for (int j = 0; j < W; ++j) v = fma2(k.w[j][c], win[j][c], v);
+                            // (v sigmoid(v))' = s + v s (1 - s)
+                            const F2 s = sigmoid(v), vs = mul2(v, s);
+                            g = mul2(g, add2(s, fma2(F2{-vs.x, -vs.y}, s, vs)));
+                            if (!whole.value && t + q >= len) g = f2(0.f);
+                        }
+                        gw[W - 1][c] = g;
+                        if (whole.value || t + q < t1) {
+                            db[c] = add2(db[c], g);
+#pragma unroll
+                            for (int j = 0; j < W; ++j) dw[j][c] = fma2(g, win[j][c], dw[j][c]);
+                        }
+                        d[c] = mul2(k.w[0][c], gw[W - 1][c]);
+#pragma unroll
+                        for (int j = 1; j < W; ++j) d[c] = fma2(k.w[j][c], gw[W - 1 - j][c], d[c]);
                     }
-                    win[W - 1][c] = pair(in[q], c);
-                    F2 g = pair(gin[q], c);
-                    if (p.silu) {
-                        F2 v = k.bias[c];
-#pragma unroll
-                        for (int j = 0; j < W; ++j) v = fma2(k.w[j][c], win[j][c], v);
-                        // (v sigmoid(v))' = s + v s (1 - s)
-                        const F2 s = sigmoid(v);
-                        g = mul2(g, fma2(mul2(v, s), F2{1.f - s.x, 1.f - s.y}, s));
-                        if (t + q >= len) g = f2(0.f);
+                    if (whole.value) {
+                        put_row<T>(dx, (long long)at * p.E, row_of<T>(d[0], d[1]));
+                        continue;
                     }
-                    gw[W - 1][c] = g;
-                    if (t + q < t1) {
-                        db[c] = add2(db[c], g);
-#pragma unroll
-                        for (int j = 0; j < W; ++j) dw[j][c] = fma2(g, win[j][c], dw[j][c]);
+                    // (a thread's first W - 1 rows are whole in the run before, but for those in front of the first token)
+                    const bool front = at < 0;
+                    if (at >= t1 || (front ? run != 0 || !p.dinit : at < t0)) continue;
+                    const int f = at + (W - 1) - len;   // the row's place in the final state
+                    if (p.dfinal && f >= 0 && f < W - 1) {
+                        const Row<T> add = get_row<T>(p.dfinal, row.s0 + (long long)f * p.E);
+                        d[0] = add2(d[0], pair(add, 0));
+                        d[1] = add2(d[1], pair(add, 1));
                     }
-                    d[c] = mul2(k.w[0][c], gw[W - 1][c]);
-#pragma unroll
-                    for (int j = 1; j < W; ++j) d[c] = fma2(k.w[j][c], gw[W - 1 - j][c], d[c]);
+                    const Row<T> o = at < len ? row_of<T>(d[0], d[1]) : no_row<T>();
+                    if (front) put_row<T>(p.dinit, row.s0 + (long long)(at + W - 1) * p.E, o);
+                    else put_row<T>(dx, (long long)at * p.E, o);
                 }
-                // (a thread's first W - 1 rows are whole in the run before, but for those in front of the first token)
-                const bool front = at < 0;
-                if (at >= t1 || (front ? run != 0 || !p.dinit : at < t0)) continue;
-                const int f = at + (W - 1) - len;   // the row's place in the final state
-                if (p.dfinal && f >= 0 && f < W - 1) {
-                    const Row<T> add = get_row<T>(p.dfinal, row.s0 + (long long)f * p.E);
-                    d[0] = add2(d[0], pair(add, 0));
-                    d[1] = add2(d[1], pair(add, 1));
-                }
-                const Row<T> o = at < len ? row_of<T>(d[0], d[1]) : no_row<T>();
-                if (front) put_row<T>(p.dinit, row.s0 + (long long)(at + W - 1) * p.E, o);
-                else put_row<T>(dx, (long long)at * p.E, o);
-            }
+            };
+            if (t >= t0 + W - 1 && t + Q <= min(t1, len)) each(std::true_type{});
+            else each(std::false_type{});
         }
     }
 #pragma unroll

@@ -290,9 +290,10 @@ __global__ void __launch_bounds__(kThreads, 3) k_ssm_scan(SsmParams p) {
     for (int j = 0; j < 8; ++j) y[1][j] = 0.f;
     // (a sum of d counts what is run, not what is prepared)
     auto count = [&](const Own &w) {
-        if (MODE == kScan) return;
+        if constexpr (MODE != kScan) {
 #pragma unroll
-        for (int o = 0; o < OP; ++o) dsum += OWN > 1 ? w.d[o].x + w.d[o].y : w.d[o].x;
+            for (int o = 0; o < OP; ++o) dsum += OWN > 1 ? w.d[o].x + w.d[o].y : w.d[o].x;
+        }
     };
     for (int i = 0; i < nt; ++i) {
         copy_wait<kAhead - 2>();

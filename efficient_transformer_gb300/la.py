@@ -577,7 +577,7 @@ def _output(name, t, shape, like):
     if t is None:   # (empty_like is the quicker of the two by 1 to 2 us)
         return torch.empty_like(like) if like.shape == shape and like.is_contiguous() else like.new_empty(shape)
     if tuple(t.shape) != tuple(shape) or t.dtype != like.dtype or t.device != like.device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor of q's dtype on q's device")
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor of the inputs' dtype on their device")
     return t
 
 
@@ -854,7 +854,10 @@ def _tokens_of(x):
 
 
 def _token_strides(t):
-    return None if t.is_contiguous() else _strides_of(t.stride(0), t.stride(2) if t.dim() == 4 else 0, t.stride(1))
+    if t.is_contiguous():
+        return None
+    st = t.stride()
+    return _strides_of(st[0], st[2] if len(st) == 4 else 0, st[1])
 
 
 def _check_dense(name, t, shape, dtype, like):
@@ -863,8 +866,28 @@ def _check_dense(name, t, shape, dtype, like):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on x's device")
 
 
+_F32 = torch.float32
+
+
+def _tokens_ok(t, shape, dtype, device):
+    return t.dtype is dtype and t.get_device() == device and t.shape == shape and (t.is_contiguous() or t.stride(-1) == 1)
+
+
+def _dense_ok(t, shape, dtype, device):
+    return t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous()
+
+
 def _conv_args(x, weight, bias):
     """(B, N, E, W, dtype code, weight's dtype code)"""
+    try:   # (all at once; what is wrong is found out below)
+        dev, ty, wty = x.get_device(), x.dtype, weight.dtype
+        B, N, E = shape = x.shape
+        Ew, W = weight.shape
+        if dev >= 0 and Ew == E and (wty is ty or wty is _F32) and _tokens_ok(x, shape, ty, dev) and \
+                _dense_ok(weight, weight.shape, wty, dev) and (bias is None or _dense_ok(bias, (E,), wty, dev)):
+            return B, N, E, W, _dtype_code(x), LA_F32 if wty is _F32 else LA_BF16
+    except (AttributeError, ValueError):
+        pass
     B, N, E = _tokens_of(x)
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2 or weight.shape[0] != E or not weight.is_contiguous() \
             or weight.get_device() != x.get_device():
@@ -975,8 +998,8 @@ def conv_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tensor, bias: 
     return out
 
 
-def _ssm_args(x, dt, A, B, C, skip, z, dt_bias, softplus, initial_state=None, lengths=None):
-    """la_ssm_args of a call, checked."""
+def _check_ssm(x, dt, A, B, C, skip, z, dt_bias, initial_state, lengths):
+    """Raises for what is wrong with the inputs of a scan."""
     nB, N, E = _tokens_of(x)
     _check_tokens("dt", dt, x.shape, x)
     if not isinstance(B, torch.Tensor) or B.dim() != 4:
@@ -985,25 +1008,34 @@ def _ssm_args(x, dt, A, B, C, skip, z, dt_bias, softplus, initial_state=None, le
     _check_tokens("B", B, (nB, N, G, S), x)
     _check_tokens("C", C, (nB, N, G, S), x)
     _check_dense("A", A, (E, S), torch.float32, x)
-    a = LaSsmArgs(x.data_ptr(), dt.data_ptr(), B.data_ptr(), C.data_ptr(), None, A.data_ptr())
-    a.x_strides, a.dt_strides, a.B_strides, a.C_strides = _token_strides(x), _token_strides(dt), _token_strides(B), _token_strides(C)
     if z is not None:
         _check_tokens("z", z, x.shape, x)
-        a.z, a.z_strides = z.data_ptr(), _token_strides(z)
-    if skip is not None:
-        _check_dense("skip", skip, (E,), torch.float32, x)
-        a.skip = skip.data_ptr()
-    if dt_bias is not None:
-        _check_dense("dt_bias", dt_bias, (E,), torch.float32, x)
-        a.dt_bias = dt_bias.data_ptr()
-    if initial_state is not None:
-        _check_dense("initial_state", initial_state, (nB, E, S), torch.float32, x)
-        a.initial_state = initial_state.data_ptr()
-    if lengths is not None:
-        _check_dense("lengths", lengths, (nB,), torch.int32, x)
-        a.lengths = lengths.data_ptr()
-    a.batch, a.N, a.E, a.S, a.G, a.dtype, a.softplus = nB, N, E, S, G, _dtype_code(x), softplus
-    return a, nB, N, E, S, G
+    for name, t, shape, dtype in (("skip", skip, (E,), _F32), ("dt_bias", dt_bias, (E,), _F32),
+                                  ("initial_state", initial_state, (nB, E, S), _F32), ("lengths", lengths, (nB,), torch.int32)):
+        if t is not None:
+            _check_dense(name, t, shape, dtype, x)
+
+
+def _ssm_args(x, dt, A, B, C, skip, z, dt_bias, softplus, initial_state=None, lengths=None):
+    """(la_ssm_args of a call, batch, N, E, S, G), checked."""
+    try:   # (all at once; what is wrong is found out by _check_ssm)
+        dev, ty = x.get_device(), x.dtype
+        nB, N, E = shape = x.shape
+        _, _, G, S = rows = B.shape
+        if dev >= 0 and rows[0] == nB and rows[1] == N and _tokens_ok(x, shape, ty, dev) and _tokens_ok(dt, shape, ty, dev) and \
+                _tokens_ok(B, rows, ty, dev) and _tokens_ok(C, rows, ty, dev) and _dense_ok(A, (E, S), _F32, dev) and \
+                (z is None or _tokens_ok(z, shape, ty, dev)) and (skip is None or _dense_ok(skip, (E,), _F32, dev)) and \
+                (dt_bias is None or _dense_ok(dt_bias, (E,), _F32, dev)) and \
+                (initial_state is None or _dense_ok(initial_state, (nB, E, S), _F32, dev)) and \
+                (lengths is None or _dense_ok(lengths, (nB,), torch.int32, dev)):
+            return LaSsmArgs(x.data_ptr(), dt.data_ptr(), B.data_ptr(), C.data_ptr(), _addr(z), A.data_ptr(), _addr(skip),
+                             _addr(dt_bias), _addr(initial_state), _addr(lengths), _token_strides(x), _token_strides(dt),
+                             _token_strides(B), _token_strides(C), None if z is None else _token_strides(z), nB, N, E, S, G,
+                             _dtype_code(x), softplus), nB, N, E, S, G
+    except (AttributeError, ValueError):
+        pass
+    _check_ssm(x, dt, A, B, C, skip, z, dt_bias, initial_state, lengths)
+    raise ValueError("la_ssm: inputs do not fit together")
 
 
 @functools.lru_cache(maxsize=256)
@@ -1081,14 +1113,13 @@ def ssm_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
     given = states
     if states is not None:
         _check_states(states, need, x)
-    f4 = torch.float32
-    with _memory_on(stream):
+    with _memory_on(stream):   # (empty_like is the quickest)
         dx, ddt = _output("dx", None, (nB, N, E), x), _output("ddt", None, (nB, N, E), x)
         dz = _output("dz", None, (nB, N, E), x) if z is not None else None
-        dB, dC = (torch.empty((nB, N, G, S), dtype=x.dtype, device=x.device) for _ in range(2))
-        dA = torch.empty((E, S), dtype=f4, device=x.device)
-        dskip = torch.empty((E,), dtype=f4, device=x.device) if skip is not None else None
-        dbias = torch.empty((E,), dtype=f4, device=x.device) if dt_bias is not None else None
+        dB, dC = _output("dB", None, (nB, N, G, S), B), _output("dC", None, (nB, N, G, S), C)
+        dA = torch.empty_like(A)
+        dskip = torch.empty_like(skip) if skip is not None else None
+        dbias = torch.empty_like(dt_bias) if dt_bias is not None else None
         ws = _workspace(_ssm_need(nB, N, E, S, G, a.dtype, 1), x.device, workspace)
         if states is None:
             states = torch.empty((need,), dtype=torch.uint8, device=x.device)
