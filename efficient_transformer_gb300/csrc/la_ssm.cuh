@@ -102,7 +102,15 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
-__device__ __forceinline__ F2 ex22(F2 a) { return F2{ex2(a.x), ex2(a.y)}; }
+// Decays 2^(d A) (A times log2(e)).  The instruction errs towards zero, by 6e-9 on average for the small exponents of long
+// memories, and a decay's error adds up over all that a state remembers: the exponent is raised by that (2^kTilt itself is 1, so
+// that a step of 0 changes nothing).
+constexpr float kTilt = 1e-8f;
+__device__ __forceinline__ F2 decay2(F2 d, F2 A) {
+    const F2 x = fma2(d, A, f2(kTilt));
+    return F2{ex2(x.x), ex2(x.y)};
+}
+__device__ __forceinline__ float decay(float d, float A) { return ex2(fmaf(d, A, kTilt)); }
 
 // log(1 + e) / e on [0, 1]: polynomial of least relative error (5e-9), 1.5e-7 in float32 arithmetic.  No cancellation for
 // small e, where log(1 + e) itself loses what 1 + e rounds away.

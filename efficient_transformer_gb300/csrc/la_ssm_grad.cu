@@ -197,8 +197,8 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_g
             for (int k = 0; k < H::K; ++k) {
                 const float d = there[k] ? p.seg_d[w + e[k]] * kLog2e : 0.f;
                 const float4 R = there[k] ? *reinterpret_cast<const float4 *>(p.seg_state + (w + e[k]) * S + 4 * r) : make_float4(0.f, 0.f, 0.f, 0.f);
-                P[k] = make_float4(fmaf(ex2(d * A[k].x), P[k].x, R.x), fmaf(ex2(d * A[k].y), P[k].y, R.y),
-                                   fmaf(ex2(d * A[k].z), P[k].z, R.z), fmaf(ex2(d * A[k].w), P[k].w, R.w));
+                P[k] = make_float4(fmaf(decay(d, A[k].x), P[k].x, R.x), fmaf(decay(d, A[k].y), P[k].y, R.y),
+                                   fmaf(decay(d, A[k].z), P[k].z, R.z), fmaf(decay(d, A[k].w), P[k].w, R.w));
             }
         }
 #pragma unroll
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_g
                     F2 acc;
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
-                        a[j][m] = ex22(mul2(dj, A[m]));
+                        a[j][m] = decay2(dj, A[m]);
                         h[m] = fma2(a[j][m], h[m], mul2(uj, Bj[m]));
                         hs[j][m] = h[m];
                         accC[j][m] = fma2(gj, h[m], accC[j][m]);
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_g
             }
             // and back
             float du[8], dq[8];
-            F2 P[2] = {F2{P4.x, P4.y}, F2{P4.z, P4.w}}, dA[2] = {F2{dA4.x, dA4.y}, F2{dA4.z, dA4.w}};
+            F2 P[2] = {F2{P4.x, P4.y}, F2{P4.z, P4.w}}, dA[2];   // (dA of the eight tokens first: short sums)
 #pragma unroll
             for (int j = 7; j >= 0; --j) {
                 const F2 dj = all(now.d, j), uj = all(now.u, j), gj = all(now.dy, j);
@@ -342,13 +342,13 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_g
                     P[m] = mul2(a[j][m], G);
                     const F2 q = mul2(P[m], before);
                     sq = m == 0 ? mul2(q, A[m]) : fma2(q, A[m], sq);
-                    dA[m] = fma2(q, dj, dA[m]);
+                    dA[m] = j == 7 ? mul2(q, dj) : fma2(q, dj, dA[m]);
                 }
                 du[j] = sb.x + sb.y;
                 dq[j] = sq.x + sq.y;
             }
             keep_P[k * TH] = make_float4(P[0].x, P[0].y, P[1].x, P[1].y);
-            keep_dA[k * TH] = make_float4(dA[0].x, dA[0].y, dA[1].x, dA[1].y);
+            keep_dA[k * TH] = make_float4(dA4.x + dA[0].x, dA4.y + dA[0].y, dA4.z + dA[1].x, dA4.w + dA[1].y);
             part_sums<LPC, 8>(du, lane);
             part_sums<LPC, 8>(dq, lane);
             float2 es = *reinterpret_cast<const float2 *>(&keep_e[k * TH]);
@@ -461,6 +461,7 @@ __global__ void __launch_bounds__(256) k_ssm_reduce(SsmReduceParams p, unsigned 
         const int b = (int)(bt / p.N), t = (int)(bt % p.N);
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         if (t < (p.lengths ? min(max(p.lengths[b], 0), p.N) : p.N))
+#pragma unroll 8
             for (int c = 0; c < p.blocks; ++c) {
                 const float4 v = *reinterpret_cast<const float4 *>(
                     p.part_bc + ((size_t)(g * p.blocks + c) * p.nB * p.N + bt) * (2 * p.S) + 4 * w);
@@ -477,6 +478,7 @@ __global__ void __launch_bounds__(256) k_ssm_reduce(SsmReduceParams p, unsigned 
         const size_t i = (size_t)(blockIdx.x - bc_blocks) * 256 + threadIdx.x, n = (size_t)p.E * p.S / 4;
         if (i >= n) return;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
         for (int w = 0; w < p.parts; ++w) {
             const float4 v = reinterpret_cast<const float4 *>(p.part_A)[w * n + i];
             s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
@@ -489,6 +491,7 @@ __global__ void __launch_bounds__(256) k_ssm_reduce(SsmReduceParams p, unsigned 
     float *to = i < p.E ? p.dskip : p.dbias;
     if (!to) return;
     float s = 0.f;
+#pragma unroll 8
     for (int w = 0; w < p.parts; ++w) s += p.part_e[(size_t)w * 2 * p.E + i];
     to[i % p.E] = s;
 }

@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_ssm_scan(SsmParams p) {
                 const float *a = states(p.seg_state, w0 + j);
 #pragma unroll
                 for (int i = 0; i < PAIRS; ++i)
-                    h[i] = fma2(ex22(mul2(f2(d), A[i])), h[i], *reinterpret_cast<const F2 *>(a + 2 * i));
+                    h[i] = fma2(decay2(f2(d), A[i]), h[i], *reinterpret_cast<const F2 *>(a + 2 * i));
             }
         }
     } else if (MODE != kReverse && seg == 0 && p.init) {
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_ssm_scan(SsmParams p) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     F2 &hk = h[2 * i4 + k];
-                    const F2 a = ex22(mul2(dj, A[2 * i4 + k]));
+                    const F2 a = decay2(dj, A[2 * i4 + k]);
                     if (MODE == kReverse) {
                         hk = mul2(a, fma2(uj, m2[k], hk));
                     } else {

@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kThreads) k_ssm_step(SsmStepParams p) {
         F2 n[4], acc;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-            n[m] = fma2(ex22(mul2(d2, A.pair(m))), h[i].pair(m), mul2(u, B[i].pair(m)));
+            n[m] = fma2(decay2(d2, A.pair(m)), h[i].pair(m), mul2(u, B[i].pair(m)));
             acc = m == 0 ? mul2(n[m], C[i].pair(m)) : fma2(n[m], C[i].pair(m), acc);
         }
         float y = acc.x + acc.y;
