@@ -16,6 +16,10 @@
 // halves, the warps' sums meet in shared memory, and the block's are written as one part.  P, dA and A of the groups
 // wait in shared memory meanwhile.  A unit is a warp's channels of one group and eight tokens; its rows come and go by the
 // warp's own copies, so that there is a barrier only for each eight tokens.
+//
+// 4 x 4096 x 4096 x 16, bfloat16: 1072 us (float operations alone: 330); 244 registers, two blocks an SM, issue slots 51 %,
+// shared memory 63 %.  168 registers and three blocks repeat shuffles and ex2 or spill: 1228; 8 states a lane with four
+// tokens at a time find h again twice as often: 1404.
 #include "la_ssm.cuh"
 
 namespace la {

@@ -5,9 +5,13 @@
 // operations and one ex2 a token.  A warp holds 32 / LPC channels, the LPC lanes of a channel SPT states each, in registers.
 // A lane finds d, d x and the gate of OWN = 8 / LPC of every eight tokens (its "own"); they go to the channel's
 // lanes by shuffles, and the lanes' sums of C h come back to the owner by exchanged halves (part_sums), so nothing of it
-// passes through shared memory.  Rows of x, dt, z, B and C come by asynchronous copies a few tiles ahead; B and C, which all
+// passes through shared memory.  Rows of x, dt, z, B and C come by asynchronous copies two tiles ahead; B and C, which all
 // warps of a block read, are widened to float32 once a block.  Outputs replace the x that their lane alone has
 // read and leave as whole rows.
+//
+// 65536 x 2048 x 16, bfloat16: 591 us for the scan, 387 for the sums of 13 of its 14 segments; 16 x 2048 x 4096 x 16 in one
+// segment 590.  All pipes are near each other: of the scan's time issue slots 60 %, shared memory 66 %, float operations
+// 49 %, ex2 42 %; the bytes alone would take a quarter (1.9 TB/s).
 #include "la_ssm.cuh"
 
 namespace la {

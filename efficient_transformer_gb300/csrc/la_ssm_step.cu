@@ -4,9 +4,9 @@
 //
 // Bound by memory: a state is read and written once for 4 operations and an ex2.  A thread holds 8 states of one channel for
 // each of U sequences (A, skip and the bias once for all; with 4 states a lane the preparation, which a channel's lanes all
-// do, was most of the instructions: 192 sequences of 4096 x 16 26 us), all its loads are issued before the first is used,
-// and the S / 8 lanes of the channel add up C h.  U = 2 where that leaves four blocks an SM (fewer reads of A, more bytes in
-// flight), else 1 (more threads).
+// do, was most of the instructions), all its loads are issued before the first is used, and the S / 8 lanes of the channel
+// add up C h.  U = 2 where that leaves four blocks an SM (fewer reads of A, more bytes in flight), else 1 (more threads).
+// 192 sequences of 4096 x 16, bfloat16: 22.5 us a call, 4.8 TB/s.
 #include "la_ssm.cuh"
 
 namespace la {
