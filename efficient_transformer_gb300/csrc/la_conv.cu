@@ -380,7 +380,7 @@ bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % 
 // Sizes and types; the weight's type is float32 or the inputs'.
 la_status check(int B, int N, int E, int W, la_dtype dt, la_dtype wt) {
     if (B <= 0 || N <= 0 || E <= 0 || (dt != LA_F32 && dt != LA_BF16) || (wt != LA_F32 && wt != dt)) return LA_ERR_ARG;
-    if (N > (1 << 30) || (long long)B * N > (1ll << 40)) return LA_ERR_ARG;
+    if (N > (1 << 30) || (long long)B * N > (1ll << 40) || (long long)B * E > (1ll << 39)) return LA_ERR_ARG;
     if (W < 2 || W > 4 || E % 8) return LA_ERR_UNSUPPORTED;
     return LA_OK;
 }

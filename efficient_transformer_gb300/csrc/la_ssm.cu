@@ -75,6 +75,7 @@ la_status check(int nB, int N, int E, int S, int G, la_dtype dt) {
     if (N > (1 << 30) || (long long)nB * N > (1ll << 36) || E > (1 << 24) || (long long)nB * E > (1ll << 30)) return LA_ERR_ARG;
     if ((long long)nB * N / 256 * ((long long)G * S / 2) >= (1ll << 31) - (1 << 24)) return LA_ERR_ARG;
     if ((long long)nB * (E / 8) * 64 >= (1ll << 31)) return LA_ERR_ARG;
+    if ((double)nB * N * E * S > (double)(1ll << 56)) return LA_ERR_ARG;   // (bytes of states and parts)
     return LA_OK;
 }
 

@@ -182,6 +182,16 @@ def test_sizes(lib):
         assert b >= f >= 0 and b >= 4 * (2 * B * N * G * S + B * E * (S + 2))
 
 
+def test_sizes_past_the_offsets(lib):
+    """Bytes of states that 64 bits do not hold, and grids past 31 bits, are refused, not cut off."""
+    dt = la.LA_BF16
+    assert lib.la_ssm_states_size(1, 1 << 30, 1 << 24, 64) == 0
+    assert lib.la_ssm_workspace_size(1, 1 << 30, 1 << 24, 64, 1, dt, 1) == 0
+    assert lib.la_ssm_states_size(1, 1 << 20, 1 << 13, 16) == (1 << 17) * (1 << 13) * 64
+    big = (1 << 31) - 8
+    assert lib.la_conv_step(FAKE, FAKE, None, FAKE, FAKE, FAKE, None, big, big, big, 4, dt, dt, 1, None, None) == la.LA_ERR_ARG
+
+
 # ---- binding --------------------------------------------------------------------------------------
 
 def tensors(**over):
