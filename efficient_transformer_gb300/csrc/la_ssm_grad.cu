@@ -7,9 +7,9 @@
 //   dx = d du + skip dy,  ddt = dd sigmoid(v),  dz = grad_out y (z sigmoid(z))',  dskip = sum dy x
 //
 // 12 float operations and an ex2 a state and token.  h is found again from the state that the scan kept for every eight
-// tokens, in registers, with a beside it; then the eight tokens are walked back.  Layout as in the scan, but 4 states a
-// lane (h and a of eight tokens are 64 registers): a lane prepares its own tokens, those of the next unit while it works on
-// this one; sums over states come by exchanged halves.
+// tokens, in registers; then the eight tokens are walked back.  Layout as in the scan, but 4 states a lane (h of eight tokens and
+// the sums below are 96 registers): a lane prepares its own tokens, those of the next unit while it works on this one; sums over
+// states come by exchanged halves.
 //
 // The sums over channels (dB, dC) would cost more than all the rest if each token's were exchanged.  So a warp takes K
 // channel groups one after the other for the same eight tokens and adds up in 64 registers; only then do its lanes exchange
@@ -17,9 +17,9 @@
 // wait in shared memory meanwhile.  A unit is a warp's channels of one group and eight tokens; its rows come and go by the
 // warp's own copies, so that there is a barrier only for each eight tokens.
 //
-// 4 x 4096 x 4096 x 16, bfloat16: 1072 us (float operations alone: 330); 244 registers, two blocks an SM, issue slots 51 %,
-// shared memory 63 %.  168 registers and three blocks repeat shuffles and ex2 or spill: 1228; 8 states a lane with four
-// tokens at a time find h again twice as often: 1404.
+// 4 x 4096 x 4096 x 16, bfloat16: 1056 us (float operations alone: 330); 245 registers, two blocks an SM, issue slots 51 %,
+// shared memory 63 %.  168 registers and three blocks spill; 8 states a lane with four tokens at a time find h again twice
+// as often: 1404.
 #include "la_ssm.cuh"
 
 namespace la {
@@ -45,7 +45,7 @@ struct Shape {
     static constexpr int OFF_WIDE = NW * kRing * UNIT, OFF_P = OFF_WIDE + 2 * WIDE * 4, OFF_DA = OFF_P + KEEP * 16,
                          OFF_A = OFF_DA + KEEP * 16, OFF_E = OFF_A + KEEP * 16, OFF_RED = OFF_E + KEEP * 16,
                          SMEM = OFF_RED + 2 * NW * WIDE * 4;
-    static_assert(SMEM <= 227 * 1024 && 2 * NB <= THREADS, "a block's shared memory and its copies of B and C");
+    static_assert(SMEM <= 227 * 1024 && 2 * NB <= THREADS && WIDE % THREADS == 0, "a block's shared memory and its copies of B and C");
 };
 
 template <int BYTES>
@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_g
             P[k] = p.dfinal && there[k] ? *reinterpret_cast<const float4 *>(p.dfinal + ((size_t)b * p.E + e[k]) * S + 4 * r)
                                         : make_float4(0.f, 0.f, 0.f, 0.f);
         }
+#pragma unroll 2
         for (int j = p.nseg - 1; j > seg; --j) {
             const size_t w = ((size_t)b * p.nseg + j) * p.E;
 #pragma unroll
@@ -298,8 +299,8 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_g
             const F2 A[2] = {F2{A4.x, A4.y}, F2{A4.z, A4.w}};
             Own then;
             prepare(ring + at, k + 1 < nk ? k + 1 : 0, first - (k + 1 < nk ? 0 : 8) + own, then);
-            // forward: h after each token, a beside it
-            F2 hs[8][2], a[8][2];
+            // forward: h after each token
+            F2 hs[8][2];
             {
                 F2 h[2] = {F2{h4.x, h4.y}, F2{h4.z, h4.w}};
                 float y[8];
@@ -311,8 +312,7 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_g
                     F2 acc;
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
-                        a[j][m] = decay2(dj, A[m]);
-                        h[m] = fma2(a[j][m], h[m], mul2(uj, Bj[m]));
+                        h[m] = fma2(decay2(dj, A[m]), h[m], mul2(uj, Bj[m]));
                         hs[j][m] = h[m];
                         accC[j][m] = fma2(gj, h[m], accC[j][m]);
                         acc = m == 0 ? mul2(Cj[m], h[m]) : fma2(Cj[m], h[m], acc);
@@ -329,6 +329,11 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_g
                 }
             }
             // and back
+            // (new values to the compiler, which else keeps all tokens' shuffled d, d x, dy and decays from above in 56
+            // registers more: finding them again is 1 % quicker)
+#pragma unroll
+            for (int o = 0; o < OP; ++o)
+                asm volatile("" : "+f"(now.d[o].x), "+f"(now.d[o].y), "+f"(now.u[o].x), "+f"(now.u[o].y), "+f"(now.dy[o].x), "+f"(now.dy[o].y));
             float du[8], dq[8];
             F2 P[2] = {F2{P4.x, P4.y}, F2{P4.z, P4.w}}, dA[2];   // (dA of the eight tokens first: short sums)
 #pragma unroll
@@ -343,7 +348,7 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_g
                     const F2 G = fma2(Cj[m], gj, P[m]);
                     sb = m == 0 ? mul2(G, Bj[m]) : fma2(G, Bj[m], sb);
                     accB[j][m] = fma2(G, uj, accB[j][m]);
-                    P[m] = mul2(a[j][m], G);
+                    P[m] = mul2(decay2(dj, A[m]), G);
                     const F2 q = mul2(P[m], before);
                     sq = m == 0 ? mul2(q, A[m]) : fma2(q, A[m], sq);
                     dA[m] = j == 7 ? mul2(q, dj) : fma2(q, dj, dA[m]);
