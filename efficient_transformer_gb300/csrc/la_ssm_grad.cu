@@ -6,7 +6,7 @@
 //   dB_t = sum_e G u,  dC_t = sum_e dy h,  du = sum_s G B,  dA = sum_t q d,  dd = sum_s q A + x du
 //   dx = d du + skip dy,  ddt = dd sigmoid(v),  dz = grad_out y (z sigmoid(z))',  dskip = sum dy x
 //
-// 12 float operations and an ex2 a state and token.  h is found again from the state that the scan kept for every eight
+// 12 float operations and two ex2 a state and token.  h is found again from the state that the scan kept for every eight
 // tokens, in registers; then the eight tokens are walked back.  Layout as in the scan, but 4 states a lane (h of eight tokens and
 // the sums below are 96 registers): a lane prepares its own tokens, those of the next unit while it works on this one; sums over
 // states come by exchanged halves.
