@@ -1106,17 +1106,19 @@ def ssm_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
     a, nB, N, E, S, G = _ssm_args(x, dt, A, B, C, skip, z, dt_bias, softplus, initial_state, lengths)
     _check_tokens("grad_out", grad_out, x.shape, x)
     raw = _check_device(x, stream)
-    for name, t in (("grad_final_state", grad_final_state), ("grad_initial_state", grad_initial_state)):
-        if t is not None:
-            _check_dense(name, t, (nB, E, S), torch.float32, x)
-    need = ssm_states_size(nB, N, E, S)
-    given = states
+    if grad_final_state is not None:
+        _check_dense("grad_final_state", grad_final_state, (nB, E, S), _F32, x)
+    if grad_initial_state is not None:
+        _check_dense("grad_initial_state", grad_initial_state, (nB, E, S), _F32, x)
+    need, given = ssm_states_size(nB, N, E, S), states
     if states is not None:
         _check_states(states, need, x)
     with _memory_on(stream):   # (empty_like is the quickest)
-        dx, ddt = _output("dx", None, (nB, N, E), x), _output("ddt", None, (nB, N, E), x)
-        dz = _output("dz", None, (nB, N, E), x) if z is not None else None
-        dB, dC = _output("dB", None, (nB, N, G, S), B), _output("dC", None, (nB, N, G, S), C)
+        dx = torch.empty_like(x) if x.is_contiguous() else x.new_empty((nB, N, E))
+        ddt = torch.empty_like(dx)
+        dz = torch.empty_like(dx) if z is not None else None
+        dB = torch.empty_like(B) if B.is_contiguous() else B.new_empty((nB, N, G, S))
+        dC = torch.empty_like(dB)
         dA = torch.empty_like(A)
         dskip = torch.empty_like(skip) if skip is not None else None
         dbias = torch.empty_like(dt_bias) if dt_bias is not None else None
