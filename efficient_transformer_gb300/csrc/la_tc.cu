@@ -298,6 +298,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_tc_fwd(const __grid_constant
     constexpr int C = K::C, NS = K::NS;
     constexpr int OFF_K = K::Q_BYTES, OFF_V = OFF_K + K::K_BYTES;
     constexpr int NO = K::O2 ? 2 : 1;   // O buffers
+    // causal, one O buffer (D = 128 with C = 64): the warps that write the backward's den read it from O too, so the next
+    // chunk's products wait for them as well as for the epilogue
+    constexpr bool kDenFrees = CAUSAL && NO == 1;
     extern __shared__ uint8_t smem_raw[];
     pdl_wait();
     LA_SPAN(1, 0);
@@ -352,7 +355,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_tc_fwd(const __grid_constant
         }
         for (int o = 0; o < 2; ++o) {
             mbar_init(&bar_ofull[o], 1);
-            mbar_init(&bar_ofree[o], 128);
+            mbar_init(&bar_ofree[o], kDenFrees ? 256 : 128);
         }
         mbar_init(&bar_afull, 1);
         mbar_init(&bar_pready, 128);
@@ -588,13 +591,18 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_tc_fwd(const __grid_constant
                 mbar_arrive_warp(&bar_pready);
             };
             // the backward's den of chunk k: phi(q) . z (columns D, D + 1 of chunk k's O buffer,
-            // read once its products are done and before this warpgroup's next state conversion
-            // lets chunk k + 2 reuse the buffer) plus this thread's fp32 row sum of mask(A)
+            // read once its products are done) plus this thread's fp32 row sum of mask(A).  With two
+            // buffers this warpgroup's next state conversion, after it, is what lets chunk k + 2
+            // reuse this one; with one, chunk k + 1's conversion has gone before: bar_ofree
             auto write_den = [&](int k, float rsum) {
                 float dz[2] = {0.f, 0.f};
                 if (ok) {
                     tmem_ld2((k % NO ? tO1 : tO0) + lane_off + D, dz);
                     tmem_wait_regs<2>(dz);
+                }
+                if constexpr (kDenFrees) {
+                    tc_fence_before();
+                    mbar_arrive_warp(&bar_ofree[0]);
                 }
                 const int t = t0 + k * C + ti;
                 if (ok && p.den && t < t1 && i / C < gr) {
