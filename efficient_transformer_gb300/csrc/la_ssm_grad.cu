@@ -6,10 +6,10 @@
 //   dB_t = sum_e G u,  dC_t = sum_e dy h,  du = sum_s G B,  dA = sum_t q d,  dd = sum_s q A + x du
 //   dx = d du + skip dy,  ddt = dd sigmoid(v),  dz = grad_out y (z sigmoid(z))',  dskip = sum dy x
 //
-// 12 float operations and two ex2 a state and token.  h is found again from the state that the scan kept for every eight
-// tokens, in registers; then the eight tokens are walked back.  Layout as in the scan, but 4 states a lane (h of eight tokens and
-// the sums below are 96 registers): a lane prepares its own tokens, those of the next unit while it works on this one; sums over
-// states come by exchanged halves.
+// 12 float operations and an ex2 a state and token.  h is found again from the state that the scan kept for every eight
+// tokens; then the eight tokens are walked back, h and the decays still in registers.  Layout as in the scan, but 4 states a
+// lane (h and decays of eight tokens and the sums below are 128 registers): a lane prepares its own tokens, those of the next
+// unit while it works on this one; sums over states come by exchanged halves.
 //
 // The sums over channels (dB, dC) would cost more than all the rest if each token's were exchanged.  So a warp takes K
 // channel groups one after the other for the same eight tokens and adds up in 64 registers; only then do its lanes exchange
@@ -17,9 +17,11 @@
 // wait in shared memory meanwhile.  A unit is a warp's channels of one group and eight tokens; its rows come and go by the
 // warp's own copies, so that there is a barrier only for each eight tokens.
 //
-// 4 x 4096 x 4096 x 16, bfloat16: 1056 us (float operations alone: 330); 245 registers, two blocks an SM, issue slots 51 %,
-// shared memory 63 %.  168 registers and three blocks spill; 8 states a lane with four tokens at a time find h again twice
-// as often: 1404.
+// 4 x 4096 x 4096 x 16, bfloat16: 1048 us (float operations alone: 330); 246 registers, two blocks an SM, issue slots 53 %,
+// shared memory 68 %.  168 registers and three blocks spill; 8 states a lane with four tokens at a time find h again twice
+// as often: 1404.  Neither 5 % fewer instructions (packed sums, simpler counters) nor 3 % less shared memory change the time:
+// eight warps an SM do not hide the chains through h, P and the shuffles.  The tokens' d, d x and dy handed out through shared
+// memory instead of shuffles: 1098, and 1118 with the decays found again to free their registers (three blocks: 1494).
 #include "la_ssm.cuh"
 
 namespace la {
@@ -73,7 +75,8 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_g
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane / CPW, chan = lane % CPW;
     unsigned char *const ring = smem + warp * kRing * H::UNIT;
     float4 *const keep_P = reinterpret_cast<float4 *>(smem + H::OFF_P) + tid, *const keep_dA = reinterpret_cast<float4 *>(smem + H::OFF_DA) + tid,
-                  *const keep_A = reinterpret_cast<float4 *>(smem + H::OFF_A) + tid, *const keep_e = reinterpret_cast<float4 *>(smem + H::OFF_E) + tid;
+                  *const keep_A = reinterpret_cast<float4 *>(smem + H::OFF_A) + tid;
+    float2 *const keep_c = reinterpret_cast<float2 *>(smem + H::OFF_E) + tid, *const keep_s = keep_c + H::KEEP;   // bias, skip; sums
     const int blocks = (p.Eg + H::CH - 1) / H::CH;
     unsigned idx = blockIdx.x;
     const int cb = idx % blocks;
@@ -195,7 +198,7 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_g
             P[k] = p.dfinal && there[k] ? *reinterpret_cast<const float4 *>(p.dfinal + ((size_t)b * p.E + e[k]) * S + 4 * r)
                                         : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-#pragma unroll 2
+#pragma unroll 3
         for (int j = p.nseg - 1; j > seg; --j) {
             const size_t w = ((size_t)b * p.nseg + j) * p.E;
 #pragma unroll
@@ -211,7 +214,8 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_g
             keep_P[k * TH] = P[k];
             keep_dA[k * TH] = make_float4(0.f, 0.f, 0.f, 0.f);
             keep_A[k * TH] = make_float4(A[k].x * kLog2e, A[k].y * kLog2e, A[k].z * kLog2e, A[k].w * kLog2e);
-            keep_e[k * TH] = make_float4(0.f, 0.f, p.dt_bias ? p.dt_bias[e[k]] : 0.f, p.skip ? p.skip[e[k]] : 0.f);
+            keep_c[k * TH] = make_float2(p.dt_bias ? p.dt_bias[e[k]] : 0.f, p.skip ? p.skip[e[k]] : 0.f);
+            keep_s[k * TH] = make_float2(0.f, 0.f);
         }
     }
     widen(0);
@@ -238,8 +242,8 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_g
     const int own = LPC == 16 ? r % 8 : r * OWN;
     const unsigned own_at = own * H::ROW + chan * (int)sizeof(T);
     auto prepare = [&](const unsigned char *st, int k, int t, Own &w) {      // t: of the first own token, from t0 on
-        const float4 es = keep_e[k * TH];
-        w.skip = es.w;
+        const float2 es = keep_c[k * TH];
+        w.skip = es.y;
 #pragma unroll
         for (int o = 0; o < OP; ++o) {
             const unsigned char *at = st + own_at + 2 * o * H::ROW;
@@ -248,7 +252,7 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_g
                 return F2{to_f32(*reinterpret_cast<const T *>(q)), to_f32(*reinterpret_cast<const T *>(q + (OWN > 1 ? H::ROW : 0)))};
             };
             w.x[o] = get(0);
-            const F2 v = add2(get(1), f2(es.z)), g = get(3);
+            const F2 v = add2(get(1), f2(es.x)), g = get(3);
             F2 ev;
             const F2 plus = softplus(v, ev), s1 = add2(ev, f2(1.f)), q = F2{rcp(s1.x), rcp(s1.y)};
             const F2 sl = mul2(q, F2{v.x >= 0.f ? 1.f : ev.x, v.y >= 0.f ? 1.f : ev.y});
@@ -329,11 +333,6 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_g
                 }
             }
             // and back
-            // (new values to the compiler, which else keeps all tokens' shuffled d, d x, dy and decays from above in 56
-            // registers more: finding them again is 1 % quicker)
-#pragma unroll
-            for (int o = 0; o < OP; ++o)
-                asm volatile("" : "+f"(now.d[o].x), "+f"(now.d[o].y), "+f"(now.u[o].x), "+f"(now.u[o].y), "+f"(now.dy[o].x), "+f"(now.dy[o].y));
             float du[8], dq[8];
             F2 P[2] = {F2{P4.x, P4.y}, F2{P4.z, P4.w}}, dA[2];   // (dA of the eight tokens first: short sums)
 #pragma unroll
@@ -360,7 +359,7 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_g
             keep_dA[k * TH] = make_float4(dA4.x + dA[0].x, dA4.y + dA[0].y, dA4.z + dA[1].x, dA4.w + dA[1].y);
             part_sums<LPC, 8>(du, lane);
             part_sums<LPC, 8>(dq, lane);
-            float2 es = *reinterpret_cast<const float2 *>(&keep_e[k * TH]);
+            float2 es = keep_s[k * TH];
 #pragma unroll
             for (int o = 0; o < OP; ++o) {
                 const F2 s1 = F2{du[2 * o], OWN > 1 ? du[2 * o + 1] : du[2 * o]}, s2 = F2{dq[2 * o], OWN > 1 ? dq[2 * o + 1] : dq[2 * o]};
@@ -379,7 +378,7 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_g
                     *reinterpret_cast<T *>(q + H::ROW + H::XBYTES) = from_f32<T>(ddt.y);
                 }
             }
-            *reinterpret_cast<float2 *>(&keep_e[k * TH]) = es;
+            keep_s[k * TH] = es;
             now = then;
         }
         // dB and dC of the tile over the warp's channels: lanes of the same states exchange halves of the 64 sums (value
@@ -439,7 +438,7 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_g
         const int c = k * CHK + w0 + chan;
         const bool there = c < left;
         const size_t e = e0 + (there ? c : 0), w = (size_t)b * p.nseg + seg;
-        float4 es = keep_e[k * TH];
+        float2 es = keep_s[k * TH];
 #pragma unroll
         for (int m = 1; m < (LPC == 16 ? 8 : LPC); m <<= 1) {
             es.x += __shfl_xor_sync(0xffffffffu, es.x, m * CPW);
