@@ -213,11 +213,12 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_g
         for (int k = 0; k < H::K; ++k) {
             keep_P[k * TH] = P[k];
             keep_dA[k * TH] = make_float4(0.f, 0.f, 0.f, 0.f);
-            // A place without a channel has no steps: with the bias and A of another, a step that no token takes could be a decay
-            // without a value, and infinity times 0 in its sums would reach dB and dC through the other lanes.  A of 0: decays of 1.
+            // A place without a channel has the bias of another and a dt of 0, a step that no token takes: with that one's A its
+            // decay could have no value, and infinity times 0 in its sums would reach dB and dC through the other lanes.  With an A
+            // of 0 every decay is 1.
             keep_A[k * TH] = there[k] ? make_float4(A[k].x * kLog2e, A[k].y * kLog2e, A[k].z * kLog2e, A[k].w * kLog2e)
                                       : make_float4(0.f, 0.f, 0.f, 0.f);
-            keep_c[k * TH] = make_float2(p.dt_bias && there[k] ? p.dt_bias[e[k]] : 0.f, p.skip && there[k] ? p.skip[e[k]] : 0.f);
+            keep_c[k * TH] = make_float2(p.dt_bias ? p.dt_bias[e[k]] : 0.f, p.skip ? p.skip[e[k]] : 0.f);
             keep_s[k * TH] = make_float2(0.f, 0.f);
         }
     }
