@@ -111,7 +111,15 @@ __device__ __forceinline__ F2 decay2(F2 d, F2 A) {
     const F2 x = fma2(d, A, f2(kTilt));
     return F2{ex2(x.x), ex2(x.y)};
 }
-__device__ __forceinline__ float decay(float d, float A) { return ex2(fmaf(d, A, kTilt)); }
+// 2^(d A) h + sum for a whole segment, whose steps add up to d.  Its factor alone may be past 2^128 (A > 0) where the result is
+// not, so its root is applied twice.  The root is at most 2^127.9, for a state of 0 has to stay 0; twice that takes any
+// normal state past 2^128.  (min.NaN: a NaN in d stays one.)
+__device__ __forceinline__ float join(float d, float A, float h, float sum) {
+    float x = 0.5f * fmaf(d, A, kTilt);
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(x), "f"(127.9f));
+    const float root = ex2(x);
+    return fmaf(root, root * h, sum);
+}
 
 // log(1 + e) / e on [0, 1]: polynomial of least relative error (5e-9), 1.5e-7 in float32 arithmetic.  No cancellation for
 // small e, where log(1 + e) itself loses what 1 + e rounds away.

@@ -205,8 +205,8 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_g
             for (int k = 0; k < H::K; ++k) {
                 const float d = there[k] ? p.seg_d[w + e[k]] * kLog2e : 0.f;
                 const float4 R = there[k] ? *reinterpret_cast<const float4 *>(p.seg_state + (w + e[k]) * S + 4 * r) : make_float4(0.f, 0.f, 0.f, 0.f);
-                P[k] = make_float4(fmaf(decay(d, A[k].x), P[k].x, R.x), fmaf(decay(d, A[k].y), P[k].y, R.y),
-                                   fmaf(decay(d, A[k].z), P[k].z, R.z), fmaf(decay(d, A[k].w), P[k].w, R.w));
+                P[k] = make_float4(join(d, A[k].x, P[k].x, R.x), join(d, A[k].y, P[k].y, R.y), join(d, A[k].z, P[k].z, R.z),
+                                   join(d, A[k].w, P[k].w, R.w));
             }
         }
 #pragma unroll

@@ -180,8 +180,10 @@ __global__ void __launch_bounds__(kThreads, 3) k_ssm_scan(SsmParams p) {
                 const float d = p.seg_d[(w0 + j) * p.E + e];
                 const float *a = states(p.seg_state, w0 + j);
 #pragma unroll
-                for (int i = 0; i < PAIRS; ++i)
-                    h[i] = fma2(decay2(f2(d), A[i]), h[i], *reinterpret_cast<const F2 *>(a + 2 * i));
+                for (int i = 0; i < PAIRS; ++i) {
+                    const F2 sum = *reinterpret_cast<const F2 *>(a + 2 * i);
+                    h[i] = F2{join(d, A[i].x, h[i].x, sum.x), join(d, A[i].y, h[i].y, sum.y)};
+                }
             }
         }
     } else if (MODE != kReverse && seg == 0 && p.init) {

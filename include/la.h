@@ -444,7 +444,7 @@ la_status la_conv_step(const void *x, const void *weight, const void *bias, void
  *
  * x, dt, z, out [B, N, E] (z NULL: no gate); B, C [B, N, G, S], read by the E / G channels of a group in turn (E / G a
  * multiple of 8); A [E, S], skip [E], dt_bias [E] float32 (skip, dt_bias NULL: zeros).  A is finite, expected < 0;
- * other values grow the states by the same formula.  Inputs may be strided (la_strides; h is the step of B's and C's groups, not
+ * other values grow the states by the same formula (one token's exp(d A) is to be below 2^128).  Inputs may be strided (la_strides; h is the step of B's and C's groups, not
  * used by the others; every stride a multiple of 16 bytes, else LA_ERR_ALIGN); outputs are contiguous and overlap no
  * input but for the states named.  States are float32 [B, E, S]: initial_state (NULL: zeros) comes in, the final one,
  * after each sequence's last token, goes out and may be the same buffer.  lengths: as la_conv_fwd's.

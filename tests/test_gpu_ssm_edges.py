@@ -39,3 +39,48 @@ def test_growing_states_of_few_channels(S):
     a["A"] = torch.full((24, S), 3.0, device="cuda")
     a["dt"], a["dt_bias"] = a["dt"] * 0.5 - 32, torch.full((24,), 30.0, device="cuda")
     compare(run_scan(a), want_scan(a), F)
+
+
+# ---- growing states of a sequence that is cut into segments -------------------------------------------
+
+@pytest.mark.parametrize("S", [8, 16, 64])
+def test_zero_states_stay_zero_where_decays_have_no_value(S):
+    """A = 1, steps near 2: a segment's whole decay is past 2^128.  x is zero but for the last tokens, grad_out but for the first
+    ones, so that all values are finite: the states, and the gradients through them, are zeros where the segments meet."""
+    N = 700
+    a = inputs(1, N, 16, S, 1, dtype=F, seed=70 + S, strided=False)
+    a["A"] = torch.ones(16, S, device="cuda")
+    a["dt"], a["dt_bias"] = 1.8 + 0.4 * a["dt"].sigmoid(), torch.zeros(16, device="cuda")
+    a["x"][:, :-8], a["grad_out"][:, 8:] = 0, 0
+    del a["initial_state"], a["grad_final_state"]
+    compare(run_scan(a, softplus=False), want_scan(a, softplus=False), F)
+
+
+@pytest.mark.parametrize("S", [8, 16, 64])
+def test_small_states_grow_past_a_decay_without_a_value(S):
+    """An initial state of 1e-37 and a gradient of the final one of 1e-37 grow by exp(150) within one segment: more than any
+    decay that float32 holds, and neither leaves its range."""
+    N = 700
+    a = inputs(1, N, 16, S, 1, dtype=F, seed=74 + S, strided=False)
+    a["A"] = torch.ones(16, S, device="cuda")
+    a["dt"], a["dt_bias"] = 1e-3 * a["dt"].sigmoid(), torch.zeros(16, device="cuda")
+    a["dt"][:, 320:350] += 5
+    a["x"].zero_()
+    a["grad_out"].zero_()
+    for k in ("initial_state", "grad_final_state"):
+        a[k] = (1 + a[k].sigmoid()) * 1e-37
+    compare(run_scan(a, softplus=False), want_scan(a, softplus=False), F)
+
+
+@pytest.mark.parametrize("where", [70, 350, 699])
+def test_an_infinite_step_cuts_the_gradient(where):
+    """A step of infinity is a decay of 0: the gradients of the tokens before it are those of a sequence that ends there."""
+    a = inputs(1, 700, 16, 16, 1, dtype=F, seed=78, strided=False)
+    del a["grad_final_state"]
+    short = dict(a, lengths=torch.tensor([where], dtype=torch.int32, device="cuda"))
+    want = run_scan(short)
+    a["dt"][:, where] = float("inf")
+    got = run_scan(a)
+    for k in ("out", "dx", "ddt", "dz", "dB", "dC"):
+        assert bool(got[k][:, :where].isfinite().all()) and torch.equal(got[k][:, :where], want[k][:, :where]), k
+    assert torch.equal(got["grad_initial_state"], want["grad_initial_state"])
