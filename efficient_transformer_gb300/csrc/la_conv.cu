@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(256, 2) k_conv_grad(ConvParams p) {
                             if (!whole.value && t + q >= len) g = f2(0.f);
                         }
                         gw[W - 1][c] = g;
-                        if (whole.value || t + q < t1) {
+                        if (whole.value || (t + q < t1 && t + q < len)) {   // (past the length g' = 0, but the window need not be finite)
                             db[c] = add2(db[c], g);
 #pragma unroll
                             for (int j = 0; j < W; ++j) dw[j][c] = fma2(g, win[j][c], dw[j][c]);

@@ -84,3 +84,19 @@ def test_an_infinite_step_cuts_the_gradient(where):
     for k in ("out", "dx", "ddt", "dz", "dB", "dC"):
         assert bool(got[k][:, :where].isfinite().all()) and torch.equal(got[k][:, :where], want[k][:, :where]), k
     assert torch.equal(got["grad_initial_state"], want["grad_initial_state"])
+
+
+# ---- rows behind a length in the convolution ----------------------------------------------------------
+
+@pytest.mark.parametrize("W", [2, 3, 4])
+def test_infinite_last_row_of_a_padded_sequence(W):
+    """Without silu: x of the last token meets the newest tap alone; the rows behind the length add nothing to the others."""
+    g = torch.Generator().manual_seed(90 + W)
+    r = lambda *s: torch.randn(*s, generator=g).cuda()  # noqa: E731
+    x, w, go = r(2, 40, 16), r(16, W), r(2, 40, 16)
+    n = torch.tensor([17, 40], dtype=torch.int32, device="cuda")
+    x[0, 16] = 0
+    _, want, _ = la.conv_bwd(x, w, go, silu=False, lengths=n)
+    x[0, 16] = float("inf")
+    dx, got, _ = la.conv_bwd(x, w, go, silu=False, lengths=n)
+    assert torch.equal(got[:, :-1], want[:, :-1]) and bool(got[:, -1].isinf().all()) and bool(dx.isfinite().all())
