@@ -8,6 +8,7 @@
 // token) and walks a run of tokens with the last W rows in registers, two channels an instruction; the next tokens' loads
 // are issued before the present ones are worked on.  65536 x 2048 bfloat16: 86 us, 6.2 TB/s; the gradient of 4 x 4096 x 4096 85 us,
 // 4.7 TB/s (128 registers, 16 warps an SM).
+#include <climits>
 #include <initializer_list>
 #include <type_traits>
 
@@ -380,6 +381,7 @@ bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % 
 // Sizes and types; the weight's type is float32 or the inputs'.
 la_status check(int B, int N, int E, int W, la_dtype dt, la_dtype wt) {
     if (B <= 0 || N <= 0 || E <= 0 || (dt != LA_F32 && dt != LA_BF16) || (wt != LA_F32 && wt != dt)) return LA_ERR_ARG;
+    if (E > INT_MAX - 127) return LA_ERR_ARG;   // (the end of the last tile of 128 channels)
     if (N > (1 << 30) || (long long)B * N > (1ll << 40) || (long long)B * E > (1ll << 39)) return LA_ERR_ARG;
     if (W < 2 || W > 4 || E % 8) return LA_ERR_UNSUPPORTED;
     return LA_OK;

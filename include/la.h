@@ -403,7 +403,8 @@ la_status la_qk_norm_rope_bwd(const void *q, const void *k, const void *grad_q, 
  *
  * Rows before the first token are the initial state's, [B, W - 1, E] of x's type, the oldest first (NULL:
  * zeros); the final state is the last W - 1 rows, of the initial state where there are fewer, and may be the
- * same buffer.  weight [E, W], bias [E] (NULL: none): float32, or x's type (weight_dtype).  E a multiple of 8.
+ * same buffer.  weight [E, W], bias [E] (NULL: none): float32, or x's type (weight_dtype).  E a multiple of 8, at most
+ * 2^31 - 128.
  * lengths: NULL, or B device int32: sequence b has min(max(lengths[b], 0), N) tokens; rows past them are not
  * used, whatever they hold, and their out rows are zeros.  x may be strided (la_strides, h not used: NULL
  * contiguous; 16-byte rows, i.e. multiples of 8 bfloat16 or 4 float32 elements, else LA_ERR_ALIGN; 0 along a broadcast
