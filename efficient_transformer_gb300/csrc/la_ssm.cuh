@@ -102,13 +102,17 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
-// Decays 2^(d A) (A times log2(e)).  The instruction errs towards zero, by 6e-9 (exponents of 1e-3) to 3e-8 (0.1) on average, and
-// a decay's error adds up over all that a state remembers: the exponent is raised by 2.4e-8 (2^kTilt itself is 1, so that a
-// step of 0 changes nothing).  Of 1e-8 to 2.8e-8 this leaves the least: prompts of 54 tokens 4.5e-7 of the final state
-// (1e-8: 8.0e-7), of 4096 2.0e-7 (3.2e-7), of 16384 2.7e-7 (3.5e-7).
-constexpr float kTilt = 2.4e-8f;
-__device__ __forceinline__ F2 decay2(F2 d, F2 A) {
-    const F2 x = fma2(d, A, f2(kTilt));
+// Decays 2^(d A) (A times log2(e)).  The instruction errs towards zero on average, and a decay's error adds up over all that a
+// state remembers, so the exponent is raised first (an fma in place of the product).  What is on average right differs by the
+// exponent: it errs by -5e-9 to -8e-9 for |x| in 1e-5 .. 2^-8, by -1.7e-8 to -2.5e-8 in 2^-8 .. 1.  A lane of the scan takes the
+// one or the other for eight tokens, by what its slowest state, which remembers the most, meets at the first of them (so that no
+// token has a part in the rows before it).  That leaves 2e-9 below 2^-8 and 6e-9 above it, and up to 2e-8, still less than
+// without, for the faster states of a lane whose slowest one is below.  65536 x 2048 x 16: 979 us with one constant, 993 so.
+// (2^tilt is 1 for either: a step of 0 changes nothing.)
+constexpr float kTiltSlow = 9e-9f, kTilt = 2.8e-8f;
+__device__ __forceinline__ F2 tilt_of(float x) { return f2(fabsf(x) < 0x1p-8f ? kTiltSlow : kTilt); }
+__device__ __forceinline__ F2 decay2(F2 d, F2 A, F2 tilt) {
+    const F2 x = fma2(d, A, tilt);
     return F2{ex2(x.x), ex2(x.y)};
 }
 // 2^(d A) h + sum for a whole segment, whose steps add up to d.  Its factor alone may be past 2^128 (A > 0) where the result is

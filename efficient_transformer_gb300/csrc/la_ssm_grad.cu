@@ -305,6 +305,7 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_g
             if (i + 1 < nt || k + 1 < nk) h_next = take();
             const float4 A4 = keep_A[k * TH], P4 = keep_P[k * TH], dA4 = keep_dA[k * TH];
             const F2 A[2] = {F2{A4.x, A4.y}, F2{A4.z, A4.w}};
+            const F2 d0 = all(now.d, 0), tilt = tilt_of(d0.x * fminf(fminf(fabsf(A4.x), fabsf(A4.y)), fminf(fabsf(A4.z), fabsf(A4.w))));
             Own then;
             prepare(ring + at, k + 1 < nk ? k + 1 : 0, first - (k + 1 < nk ? 0 : 8) + own, then);
             // forward: h after each token
@@ -314,13 +315,13 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_g
                 float y[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const F2 dj = all(now.d, j), uj = all(now.u, j), gj = all(now.dy, j);
+                    const F2 dj = j == 0 ? d0 : all(now.d, j), uj = all(now.u, j), gj = all(now.dy, j);
                     const float4 B4 = *reinterpret_cast<const float4 *>(bc + j * 2 * S), C4 = *reinterpret_cast<const float4 *>(bc + j * 2 * S + S);
                     const F2 Bj[2] = {F2{B4.x, B4.y}, F2{B4.z, B4.w}}, Cj[2] = {F2{C4.x, C4.y}, F2{C4.z, C4.w}};
                     F2 acc;
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
-                        h[m] = fma2(decay2(dj, A[m]), h[m], mul2(uj, Bj[m]));
+                        h[m] = fma2(decay2(dj, A[m], tilt), h[m], mul2(uj, Bj[m]));
                         hs[j][m] = h[m];
                         accC[j][m] = fma2(gj, h[m], accC[j][m]);
                         acc = m == 0 ? mul2(Cj[m], h[m]) : fma2(Cj[m], h[m], acc);
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_g
                     const F2 G = fma2(Cj[m], gj, P[m]);
                     sb = m == 0 ? mul2(G, Bj[m]) : fma2(G, Bj[m], sb);
                     accB[j][m] = fma2(G, uj, accB[j][m]);
-                    P[m] = mul2(decay2(dj, A[m]), G);
+                    P[m] = mul2(decay2(dj, A[m], tilt), G);
                     const F2 q = mul2(P[m], before);
                     sq = m == 0 ? mul2(q, A[m]) : fma2(q, A[m], sq);
                     dA[m] = j == 7 ? mul2(q, dj) : fma2(q, dj, dA[m]);

@@ -41,8 +41,9 @@ struct Shape {
     static constexpr int SMEM = kStages * STAGE + 2 * WIDE * 4;
 };
 
+// (four blocks an SM where the sums fit 128 registers without spills)
 template <typename T, int S, int MODE>
-__global__ void __launch_bounds__(kThreads, 3) k_ssm_scan(SsmParams p) {
+__global__ void __launch_bounds__(kThreads, MODE != kScan && (S == 16 || S == 32) ? 4 : 3) k_ssm_scan(SsmParams p) {
     using H = Shape<T, S, MODE>;
     constexpr int SPT = H::SPT, LPC = H::LPC, CPW = H::CPW, CH = H::CH, OWN = H::OWN, V = H::V, TENSORS = H::TENSORS, MATS = H::MATS;
     constexpr int PAIRS = SPT / 2, OP = OWN > 1 ? OWN / 2 : 1;               // pairs of own tokens (of one: it and itself)
@@ -148,6 +149,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_ssm_scan(SsmParams p) {
     for (int i = 0; i < kAhead; ++i) load(i, i);
 
     F2 A[PAIRS], h[PAIRS];
+    float slow;                                                              // the least |A|
     const float bias = p.dt_bias ? p.dt_bias[e] : 0.f, skip = MODE == kScan && p.skip ? p.skip[e] : 0.f;
     {
         const float *a = p.A + (size_t)e * S + r * SPT;
@@ -155,6 +157,8 @@ __global__ void __launch_bounds__(kThreads, 3) k_ssm_scan(SsmParams p) {
         for (int i = 0; i < PAIRS; ++i) {
             A[i] = F2{a[2 * i] * kLog2e, a[2 * i + 1] * kLog2e};
             h[i] = f2(0.f);
+            const float least = fminf(fabsf(A[i].x), fabsf(A[i].y));
+            slow = i == 0 ? least : fminf(slow, least);
         }
     }
     auto states = [&](const float *base, size_t block) { return base + (block * p.E + e) * S + r * SPT; };
@@ -230,10 +234,11 @@ __global__ void __launch_bounds__(kThreads, 3) k_ssm_scan(SsmParams p) {
             const int o = j % OWN;
             return f2(__shfl_sync(0xffffffffu, o % 2 ? v[o / 2].y : v[o / 2].x, j / OWN * CPW + chan));
         };
+        const F2 d0 = all(w.d, 0), tilt = tilt_of(d0.x * slow);
 #pragma unroll
         for (int jj = 0; jj < 8; ++jj) {
             const int j = MODE == kReverse ? 7 - jj : jj;
-            const F2 dj = all(w.d, j), uj = all(w.u, j);
+            const F2 dj = j == 0 ? d0 : all(w.d, j), uj = all(w.u, j);
             const float *m4 = bc + j * (MATS * S);
             F2 acc;
 #pragma unroll
@@ -246,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_ssm_scan(SsmParams p) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     F2 &hk = h[2 * i4 + k];
-                    const F2 a = decay2(dj, A[2 * i4 + k]);
+                    const F2 a = decay2(dj, A[2 * i4 + k], tilt);
                     if (MODE == kReverse) {
                         hk = mul2(a, fma2(uj, m2[k], hk));
                     } else {

@@ -6,7 +6,8 @@
 // each of U sequences (A, skip and the bias once for all; with 4 states a lane the preparation, which a channel's lanes all
 // do, was most of the instructions), all its loads are issued before the first is used, and the S / 8 lanes of the channel
 // add up C h.  U = 2 where that leaves four blocks an SM (fewer reads of A, more bytes in flight), else 1 (more threads).
-// 192 sequences of 4096 x 16, bfloat16: 22.5 us a call, 4.8 TB/s.
+// 192 sequences of 4096 x 16, bfloat16: 22.5 us a call, 4.8 TB/s.  All decays have the slow states' correction (la_ssm.cuh): to
+// choose it by the step, as the scan does, took 6 % more.
 #include "la_ssm.cuh"
 
 namespace la {
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) k_ssm_step(SsmStepParams p) {
         F2 n[4], acc;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-            n[m] = fma2(decay2(d2, A.pair(m)), h[i].pair(m), mul2(u, B[i].pair(m)));
+            n[m] = fma2(decay2(d2, A.pair(m), f2(kTiltSlow)), h[i].pair(m), mul2(u, B[i].pair(m)));
             acc = m == 0 ? mul2(n[m], C[i].pair(m)) : fma2(n[m], C[i].pair(m), acc);
         }
         float y = acc.x + acc.y;
