@@ -100,3 +100,46 @@ def test_infinite_last_row_of_a_padded_sequence(W):
     x[0, 16] = float("inf")
     dx, got, _ = la.conv_bwd(x, w, go, silu=False, lengths=n)
     assert torch.equal(got[:, :-1], want[:, :-1]) and bool(got[:, -1].isinf().all()) and bool(dx.isfinite().all())
+
+
+# ---- sums over several blocks of a group's channels ---------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(1, 24, 528, 16, 1), (1, 18, 544, 16, 2), (2, 12, 272, 32, 2), (1, 20, 136, 64, 1), (1, 10, 544, 8, 2),
+                                   (2, 9, 256, 64, 1), (1, 300, 288, 16, 1)], ids=lambda s: "x".join(map(str, s)))
+def test_several_blocks_of_a_group(shape, dtype):
+    a = inputs(*shape, dtype=dtype, seed=sum(shape) + 1)
+    compare(run_scan(a), want_scan(a), dtype)
+
+
+# ---- NaN and infinities --------------------------------------------------------------------------------
+
+# tokens before (e), at (a) and after (l) the NaN that it reaches: the states after it through d x B, the gradients of the
+# states before it through the gate, C and the decays
+REACH = {
+    "x": dict(dx="", ddt="al", dz="al", dB="a", dC="al"),
+    "dt": dict(dx="ea", ddt="eal", dz="al", dB="ea", dC="al"),
+    "B": dict(dx="a", ddt="al", dz="al", dB="", dC="al"),
+    "C": dict(dx="ea", ddt="ea", dz="a", dB="ea", dC=""),
+    "z": dict(dx="ea", ddt="ea", dz="a", dB="ea", dC="a"),
+    "grad_out": dict(dx="ea", ddt="ea", dz="a", dB="ea", dC="a"),
+}
+
+
+@pytest.mark.parametrize("N,where", [(40, 3), (40, 20), (700, 350)])
+@pytest.mark.parametrize("name", list(REACH))
+def test_nan_of_a_token_in_the_gradient(name, N, where):
+    """A NaN in one token reaches what depends on it by the formula, and nothing else changes by a bit."""
+    a = inputs(2, N, 72, 16, 1, dtype=F, seed=80, strided=False)
+    want = run_scan(a)
+    a[name][1, where, ..., 5] = float("nan")
+    got = run_scan(a)
+    at = dict(e=slice(0, where), a=slice(where, where + 1), l=slice(where + 1, None))
+    for k, tokens in REACH[name].items():
+        # channel 5 (of x, dt, z, grad_out) or all (of B and C, in state 5 alone); sums over channels
+        where_k = slice(None) if (k in ("dB", "dC")) != (name in ("B", "C")) else slice(5, 6)
+        hit = torch.zeros_like(want[k], dtype=torch.bool)
+        for t in tokens:
+            hit[1, at[t], ..., where_k] = True
+        assert torch.equal(torch.isnan(got[k]), hit), k
+        assert torch.equal(got[k][~hit], want[k][~hit]), k
