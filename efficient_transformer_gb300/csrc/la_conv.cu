@@ -7,7 +7,8 @@
 // Bound by memory: each row is read once but for the W - 1 rows at a run's edge.  A thread owns four channels (one load a
 // token) and walks a run of tokens with the last W rows in registers, two channels an instruction; the next tokens' loads
 // are issued before the present ones are worked on.  65536 x 2048 bfloat16: 86 us, 6.2 TB/s; the gradient of 4 x 4096 x 4096 85 us,
-// 4.7 TB/s (128 registers, 16 warps an SM).
+// 4.7 TB/s (128 registers, 16 warps an SM).  float32: 167 us, 6.4 TB/s, and 211 us, 3.8 TB/s (the bound of 128 registers, chosen for
+// bfloat16, spills 388 bytes there).
 #include <climits>
 #include <initializer_list>
 #include <type_traits>

@@ -18,10 +18,12 @@ struct SsmPlan {
     int blocks, parts;
 };
 
-// The segments of a sequence: the count whose kernels end first, in microseconds fitted to GB300.  The scan's blocks of a
-// segment each (1024 states) share the SMs evenly, 42 ns a token and block; less than about 1.75 blocks leave an SM
-// waiting.  The gradient's (8 to 16 times as much work) run in waves of two blocks an SM, 1.2 us a token.  More than one
-// segment costs the sums of all but one, 29 ns a token and block, and a launch.
+// The segments of a sequence: the count whose kernels end first, in microseconds fitted to GB300 with 16 states a channel in
+// bfloat16.  The scan's blocks of a segment each (1024 states) share the SMs evenly, 42 ns a token and block; less than about 1.75
+// blocks leave an SM waiting.  The gradient's (8 to 16 times as much work) run in waves of two blocks an SM, 1.2 us a token.  More
+// than one segment costs the sums of all but one, 29 ns a token and block, and a launch.  Other state counts (2048 states a block of the
+// scan for 64; 2048 to 8192 of the gradient) and float32 are planned with the same figures, and sequences with lengths as if all
+// were full.
 void cut(int N, bool bwd, long long blocks, long long sum_blocks, int slots, int *seg_len, int *nseg) {
     double best = -1.0;
     const int most = N < 64 * 64 ? (N + 63) / 64 : 64;

@@ -17,8 +17,8 @@
 // wait in shared memory meanwhile.  A unit is a warp's channels of one group and eight tokens; its rows come and go by the
 // warp's own copies, so that there is a barrier only for each eight tokens.
 //
-// 4 x 4096 x 4096 x 16, bfloat16: 1048 us (float operations alone: 330); 246 registers, two blocks an SM, issue slots 53 %,
-// shared memory 68 %.  168 registers and three blocks spill; 8 states a lane with four tokens at a time find h again twice
+// 4 x 4096 x 4096 x 16, bfloat16: 1054 us (float operations alone: 320); 246 registers, two blocks an SM, issue slots 54 %,
+// shared memory 66 %.  64 states: one block an SM, 28 (float32: 32) bytes spilled.  168 registers and three blocks spill; 8 states a lane with four tokens at a time find h again twice
 // as often: 1404.  Neither 5 % fewer instructions (packed sums, simpler counters) nor 3 % less shared memory change the time:
 // eight warps an SM do not hide the chains through h, P and the shuffles.  The tokens' d, d x and dy handed out through shared
 // memory instead of shuffles: 1098, and 1118 with the decays found again to free their registers (three blocks: 1494).
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(Shape<T, S>::THREADS, S == 64 ? 1 : 2) k_ssm_g
                     if (OWN > 1) *reinterpret_cast<T *>(q + H::ROW) = from_f32<T>(dz.y);
                 }
             }
-            // and back
+            // and back (the decays are written as found again; the compiler keeps those of the way there: one ex2 a state runs)
             float du[8], dq[8];
             F2 P[2] = {F2{P4.x, P4.y}, F2{P4.z, P4.w}}, dA[2];   // (dA of the eight tokens first: short sums)
 #pragma unroll

@@ -9,9 +9,9 @@
 // warps of a block read, are widened to float32 once a block.  Outputs replace the x that their lane alone has
 // read and leave as whole rows.
 //
-// 65536 x 2048 x 16, bfloat16: 591 us for the scan, 387 for the sums of 13 of its 14 segments; 16 x 2048 x 4096 x 16 in one
-// segment 590.  All pipes are near each other: of the scan's time issue slots 60 %, shared memory 66 %, float operations
-// 49 %, ex2 42 %; the bytes alone would take a quarter (1.9 TB/s).
+// 65536 x 2048 x 16, bfloat16: 598 us for the scan, 392 for the sums of 18 of its 19 segments; 16 x 2048 x 4096 x 16 in one
+// segment 598.  All pipes are near each other: of the scan's time issue slots 61 %, shared memory 66 %, float operations
+// 49 %, ex2 42 %; the bytes alone would take a quarter (1.9 TB/s).  float32: 667 and 402.
 #include "la_ssm.cuh"
 
 namespace la {

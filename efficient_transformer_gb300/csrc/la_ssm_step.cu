@@ -6,7 +6,7 @@
 // each of U sequences (A, skip and the bias once for all; with 4 states a lane the preparation, which a channel's lanes all
 // do, was most of the instructions), all its loads are issued before the first is used, and the S / 8 lanes of the channel
 // add up C h.  U = 2 where that leaves four blocks an SM (fewer reads of A, more bytes in flight), else 1 (more threads).
-// 192 sequences of 4096 x 16, bfloat16: 22.5 us a call, 4.8 TB/s.  All decays have the slow states' correction (la_ssm.cuh): to
+// 192 sequences of 4096 x 16, bfloat16: 22.3 us a call, 4.8 TB/s.  All decays have the slow states' correction (la_ssm.cuh): to
 // choose it by the step, as the scan does, took 6 % more.
 #include "la_ssm.cuh"
 

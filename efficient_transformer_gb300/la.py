@@ -1100,7 +1100,7 @@ def ssm_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
             workspace: torch.Tensor | None = None, stream=None):
     """Gradient of ``ssm_fwd`` (``la_ssm_bwd``): returns ``(dx, ddt, dA, dB, dC, dskip, dz, ddt_bias)``; dskip, dz and
     ddt_bias None without their inputs.  ``states``: those that ``ssm_fwd`` kept for these inputs (None: they are found
-    again first, one more pass).  ``grad_final_state`` is the gradient of the final state (None: zeros);
+    again first, one more pass, from what ``initial_state`` holds now: not after a forward that replaced it).  ``grad_final_state`` is the gradient of the final state (None: zeros);
     ``grad_initial_state``, when given, receives the initial state's."""
     lib = load()
     a, nB, N, E, S, G = _ssm_args(x, dt, A, B, C, skip, z, dt_bias, softplus, initial_state, lengths)
