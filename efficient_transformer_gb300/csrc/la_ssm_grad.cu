@@ -18,10 +18,11 @@
 // warp's own copies, so that there is a barrier only for each eight tokens.
 //
 // 4 x 4096 x 4096 x 16, bfloat16: 1054 us (float operations alone: 320); 246 registers, two blocks an SM, issue slots 54 %,
-// shared memory 66 %.  64 states: one block an SM, 28 (float32: 32) bytes spilled.  168 registers and three blocks spill; 8 states a lane with four tokens at a time find h again twice
-// as often: 1404.  Neither 5 % fewer instructions (packed sums, simpler counters) nor 3 % less shared memory change the time:
-// eight warps an SM do not hide the chains through h, P and the shuffles.  The tokens' d, d x and dy handed out through shared
-// memory instead of shuffles: 1098, and 1118 with the decays found again to free their registers (three blocks: 1494).
+// shared memory 66 %.  64 states: one block an SM, 28 (float32: 32) bytes spilled.  168 registers and three blocks spill; 8
+// states a lane with four tokens at a time find h again twice as often: 1404.  Neither 5 % fewer instructions (packed sums,
+// simpler counters) nor 3 % less shared memory change the time: eight warps an SM do not hide the chains through h, P and the
+// shuffles.  The tokens' d, d x and dy handed out through shared memory instead of shuffles: 1098, and 1118 with the decays
+// found again to free their registers (three blocks: 1494).
 #include "la_ssm.cuh"
 
 namespace la {
